@@ -138,7 +138,7 @@ const char *ffd_status_string(ffd_status status);
 int32_t ffd_last_cuda_error(void);
 
 /* Library version, major * 10000 + minor * 100 + patch (3.00: ffd_decode_params gained
- * wait_limit_us and schedule). */
+ * wait_limit_us and schedule; 3.10: the 4-bit cache). */
 int32_t ffd_version(void);
 
 /*
@@ -398,6 +398,147 @@ ffd_status ffd_decode_attention_static(const ffd_decode_params *params, const vo
                                        const int32_t *block_table, float *out,
                                        uint8_t *keep_mask, float *m_tilde, int32_t *error_word,
                                        void *stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * The 4-bit cache: keys AND values of a paged cache held in 4 bits, written token by token, read
+ * back, and attended to by one or more query tokens per sequence. It stands beside the thumbnail /
+ * residual cache above: 160 bytes a token and KV head instead of 440 (or 512 of bf16 K and V), for
+ * callers that trade the near-fp16 keys for capacity. The pages name low-bit KV caches as the
+ * systems FFD is compared with (Main results); the format is this library's own.
+ *
+ * Format, per token, KV head and tensor (K or V), and group g of 32 channels (x: the group's
+ * bf16 or fp16 inputs):
+ *   scale = f16((max x - min x) / 15)             fp32 difference and quotient, each rounded once
+ *   off   = f16(min x - 16 scale)                 fp32 fused multiply-add
+ *   c     = clamp(round((x - off) / scale), 16, 31) - 16, half to even; 0 where scale is 0
+ *           (decided at the boundaries b_k = fma(k + 1/2, scale, off) in fp32, k = 16 .. 30)
+ *   the value held = f16(fma(c + 16, scale, off)) rounded once.
+ * |value - x| <= scale / 2, plus the roundings of off and of the value (2^-11 of each). The 16 is
+ * there because a 4-bit code in the top mantissa bits of an f16 of exponent 4 reads as 16 + c: a
+ * pair of values is one logical operation and one fused multiply-add.
+ *
+ *   k4, v4   u8 [P][Hkv][FFD_KV4_RECORD_BYTES]  one record per (page, KV head), 16-byte aligned:
+ *     bytes [0, 4096)     codes: token r has 64 bytes, 16 words of 8 channels; channel
+ *                         8 J + 2 i + e (i < 4, e < 2) is nibble i + 4 e of word J. Tokens 2L and
+ *                         2L + 1 share the 128-byte line L; 32-byte sector s of the line
+ *                         (s = 2 (r % 2) + J / 8) is stored at sector s ^ (L % 4)
+ *     bytes [4096, 5120)  f16 pairs (scale, off) of token r, group g at 4096 + 16 r + 4 g
+ * --------------------------------------------------------------------------------------------- */
+#define FFD_KV4_RECORD_BYTES 5120
+
+/* Element types of the 4-bit cache's inputs, queries and outputs. */
+#define FFD_DTYPE_BF16 0
+#define FFD_DTYPE_F16 1
+
+/*
+ * ffd_kv4_write -- quantise new K and V rows into the 4-bit cache: a decode step's one token per
+ * sequence, drafted tokens, or whole prompts, in one launch.
+ *   cache         shape of the cache (head_dim 128, page_size 64)
+ *   dtype         FFD_DTYPE_BF16 or FFD_DTYPE_F16, of k_new and v_new
+ *   batch         B >= 1 sequences
+ *   max_blocks_per_seq  row stride of block_table (>= 1)
+ *   total_tokens  T >= 0 rows of k_new and v_new
+ *   k_new, v_new  device [T][Hkv][128], rows k_stride / v_stride elements apart (>= Hkv * 128 and a
+ *                 multiple of 8, so that they may lie inside a fused projection), 16-byte aligned
+ *   cu_tokens     device int32 [B+1], non-decreasing: sequence b has rows cu[b] .. cu[b+1]-1. Rows
+ *                 before cu[0] and from cu[B] on belong to nobody and are not read. NULL: T is a
+ *                 multiple of B and every sequence has T / B rows.
+ *   positions     device int32 [B]: token index of the sequence's first row; a negative entry
+ *                 writes nothing for that sequence
+ *   block_table   device int32 [B][max_blocks_per_seq]
+ *   k4, v4        device records (layout above): the tokens' codes and parameters are rewritten,
+ *                 nothing else
+ *   error_word    device int32, or NULL: FFD_ERRBIT_BOUNDS for a token index >=
+ *                 64 * max_blocks_per_seq or a page outside [0, P) (that token is skipped),
+ *                 FFD_ERRBIT_RANGE for an input with |x| > 16384 or NaN (its group is written; what
+ *                 it then holds is unspecified)
+ * Two rows that name the same (page, token) race; the caller's block table must not do that.
+ * Returns FFD_OK, FFD_ERR_INVALID_ARG, FFD_ERR_UNSUPPORTED or FFD_ERR_CUDA.
+ */
+ffd_status ffd_kv4_write(const ffd_cache_desc *cache, int32_t dtype, int32_t batch,
+                         int32_t max_blocks_per_seq, int32_t total_tokens, const void *k_new,
+                         int64_t k_stride, const void *v_new, int64_t v_stride,
+                         const int32_t *cu_tokens, const int32_t *positions,
+                         const int32_t *block_table, uint8_t *k4, uint8_t *v4,
+                         int32_t *error_word, void *stream);
+
+/*
+ * ffd_kv4_read -- the values that the 4-bit cache holds for a run of tokens of each sequence, as
+ * plain rows. cu_tokens, positions, block_table, the strides and the errors are as for
+ * ffd_kv4_write; rows of k_out / v_out that belong to nobody, and those of a sequence with a
+ * negative position, are left as they were.
+ *   k_out, v_out  device [T][Hkv][128] of dtype, or NULL for the tensor that is not wanted (not
+ *                 both); the f16 value held, rounded once more for FFD_DTYPE_BF16
+ *   error_word    device int32, or NULL: FFD_ERRBIT_BOUNDS for a token index >=
+ *                 64 * max_blocks_per_seq or a page outside [0, P): the token's rows become 0
+ */
+ffd_status ffd_kv4_read(const ffd_cache_desc *cache, int32_t dtype, int32_t batch,
+                        int32_t max_blocks_per_seq, int32_t total_tokens, const int32_t *cu_tokens,
+                        const int32_t *positions, const int32_t *block_table, const uint8_t *k4,
+                        const uint8_t *v4, void *k_out, int64_t k_stride, void *v_out,
+                        int64_t v_stride, int32_t *error_word, void *stream);
+
+/* One attention call over the 4-bit cache. */
+typedef struct {
+    int32_t batch;              /* B >= 1 sequences */
+    int32_t num_q_heads;        /* Hq, a multiple of num_kv_heads */
+    int32_t num_kv_heads;       /* Hkv; G = Hq / Hkv in 1..8 */
+    int32_t head_dim;           /* must be 128 */
+    int32_t page_size;          /* must be 64 */
+    int32_t num_pages;          /* P, bound for block_table entries */
+    int32_t max_blocks_per_seq; /* row stride of block_table; seq_lens[b] <= 64 * this */
+    int32_t dtype;              /* FFD_DTYPE_BF16 or FFD_DTYPE_F16, of q and out */
+    int32_t max_q_len;          /* >= 1, the most query tokens of one sequence */
+    int32_t total_q;            /* >= 1, rows of q, out and lse */
+    int32_t window;             /* 0: every earlier token is visible; w > 0: the last w are (the
+                                   query's own token included) */
+    int32_t num_splits;         /* 0: library's choice; else the number of KV partitions, as for
+                                   ffd_decode_attention (at most one CTA per SM) */
+    int64_t q_stride;           /* elements between the rows of q: >= Hq * 128, a multiple of 8; 0
+                                   means Hq * 128 */
+    float sm_scale;             /* score scale, finite and > 0; normally 1/sqrt(head_dim) */
+    int32_t wait_limit_us;      /* as in ffd_decode_params */
+} ffd_kv4_params;
+
+/* Bytes of device workspace that ffd_kv4_attention needs for these parameters on the current
+ * device (0 for parameters that it would reject). */
+size_t ffd_kv4_workspace_size(const ffd_kv4_params *params);
+
+/*
+ * ffd_kv4_attention -- softmax attention of the newest tokens of each sequence over its 4-bit
+ * cache: one token (decoding), a few (drafted tokens verified together) or many (a chunk of a
+ * prompt, whose K and V were written first). Sequence b has n = seq_lens[b] cached tokens, of which
+ * its nq query tokens are the last: query i sits at p = n - nq + i and sees the tokens j with
+ * 0 <= j <= p, j > p - window when window > 0, and keep_in of j's block nonzero when it is given:
+ *   s_j = sm_scale q . K_j,  lse = log sum_j e^(s_j),  out = sum_j e^(s_j - lse) V_j
+ * over the values that the cache holds. A row that sees no token (n < nq, a mask that leaves
+ * nothing) gets out = 0 and lse = -inf. A query with an infinity or a NaN in it leaves its own
+ * (row, head) unspecified and no other.
+ *   q           device [total_q][Hq][128] of dtype, rows params->q_stride elements apart, 16-byte
+ *               aligned
+ *   k4, v4      device records of the cache, 16-byte aligned. Tokens at or past n are never used:
+ *               their bytes may be anything.
+ *   seq_lens    device int32 [B], 0 <= seq_lens[b] <= 64 * max_blocks_per_seq
+ *   cu_q        device int32 [B+1]: sequence b's query tokens are rows cu_q[b] .. cu_q[b+1]-1, at
+ *               most max_q_len of them (none is fine). NULL: every sequence has max_q_len, and
+ *               total_q = B * max_q_len. Rows that belong to nobody are left as they were.
+ *   block_table device int32 [B][max_blocks_per_seq]; entries of blocks that no query of the
+ *               sequence sees (past n, behind the window, dropped by keep_in) are not read
+ *   keep_in     device u8 [B][Hkv][max_blocks_per_seq] or NULL: nonzero = the block may be seen
+ *               (for instance ffd_select_blocks's mask, or a decode step's keep_mask)
+ *   out         device [total_q][Hq][128] of dtype, 16-byte aligned
+ *   lse         device fp32 [total_q][Hq] or NULL
+ *   workspace   device, >= ffd_kv4_workspace_size(params) bytes, 256-byte aligned; its first 4
+ *               bytes are the device error word. Zero-fill it once before first use; each call
+ *               leaves it ready for the next one. Calls that share a workspace must be ordered.
+ * Errors: host-side statuses; FFD_ERRBIT_BOUNDS for a block-table entry outside [0, P) (the block
+ * is treated as dropped), a sequence length out of range (clamped), or a cu_q entry out of range
+ * (that sequence's rows are left as they were).
+ */
+ffd_status ffd_kv4_attention(const ffd_kv4_params *params, const void *q, const uint8_t *k4,
+                             const uint8_t *v4, const int32_t *seq_lens, const int32_t *cu_q,
+                             const int32_t *block_table, const uint8_t *keep_in, void *out,
+                             float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * ffd_set_profile_events -- optional instrumentation. While both events are non-NULL, every

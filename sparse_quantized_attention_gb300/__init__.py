@@ -12,7 +12,9 @@ from .ffd import (CacheDesc, DecodeParams, FFDError, QuantizedCache, alloc_quant
                   ffd_select_workspace_size, ffd_select_blocks, ffd_decode_attention_masked,
                   ffd_art_workspace_size, alloc_art_workspace, ffd_art_attention,
                   ffd_suggest_schedule, ffd_last_cuda_error, SCHEDULE_FUSED,
-                  SCHEDULE_SCAN_REFINE)
+                  SCHEDULE_SCAN_REFINE, Kv4Cache, Kv4Params, alloc_kv4_cache, alloc_kv4_workspace,
+                  ffd_kv4_attention, ffd_kv4_read, ffd_kv4_workspace_size, ffd_kv4_write,
+                  make_kv4_params)
 
 __all__ = ["CacheDesc", "DecodeParams", "FFDError", "QuantizedCache", "alloc_quantized_cache",
            "alloc_workspace", "ffd_append_kv", "ffd_decode_attention", "ffd_decode_attention_static",
@@ -23,4 +25,6 @@ __all__ = ["CacheDesc", "DecodeParams", "FFDError", "QuantizedCache", "alloc_qua
            "alloc_select_workspace", "ffd_select_workspace_size", "ffd_select_blocks",
            "ffd_decode_attention_masked", "ffd_art_workspace_size", "alloc_art_workspace",
            "ffd_art_attention", "ffd_suggest_schedule", "ffd_last_cuda_error", "SCHEDULE_FUSED",
-           "SCHEDULE_SCAN_REFINE"]
+           "SCHEDULE_SCAN_REFINE", "Kv4Cache", "Kv4Params", "alloc_kv4_cache",
+           "alloc_kv4_workspace", "ffd_kv4_attention", "ffd_kv4_read", "ffd_kv4_workspace_size",
+           "ffd_kv4_write", "make_kv4_params"]

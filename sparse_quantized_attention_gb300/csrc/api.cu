@@ -32,14 +32,16 @@ cudaError_t launch_art(const DecodeArgs &a, float tau, float phi, int patience, 
 using namespace ffd;
 
 namespace {
-
 thread_local int g_last_cuda = 0;  // the cudaError_t behind this thread's latest FFD_ERR_CUDA
+}
 
-ffd_status cuda_status(cudaError_t e) {
+ffd_status ffd::cuda_status(cudaError_t e) {
     if (e == cudaSuccess) return FFD_OK;
     g_last_cuda = static_cast<int>(e);
     return FFD_ERR_CUDA;
 }
+
+namespace {
 
 constexpr size_t kAlign = 256;
 
@@ -57,7 +59,9 @@ uint64_t wait_bound_ns(const ffd_decode_params *p) {
     return p->wait_limit_us > 0 ? (uint64_t)p->wait_limit_us * 1000ull : kWaitTimeoutNs;
 }
 
-int current_sm_count() {
+}  // namespace
+
+int ffd::current_sm_count() {
     static int cache[128];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -69,6 +73,8 @@ int current_sm_count() {
     if (dev >= 0 && dev < 128) cache[dev] = v;
     return v;
 }
+
+namespace {
 
 ffd_status check_params(const ffd_decode_params *p) {
     if (!p) return FFD_ERR_INVALID_ARG;
@@ -247,7 +253,7 @@ const char *ffd_status_string(ffd_status s) {
     return "FFD_ERR_UNKNOWN";
 }
 
-int32_t ffd_version(void) { return 300; }
+int32_t ffd_version(void) { return 310; }
 
 ffd_status ffd_quantize_keys(const ffd_cache_desc *cache, const void *k_bf16, uint8_t *thumb,
                              uint8_t *resid, const int32_t *page_ids, int32_t num_page_ids,

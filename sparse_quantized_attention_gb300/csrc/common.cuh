@@ -111,6 +111,11 @@ inline cudaError_t raise_smem_limit(Kernel *kernel, int bytes, int (&done)[kMaxD
     return e;
 }
 
+// Host (api.cu): the status of a CUDA call (its error is kept for ffd_last_cuda_error), and the SM
+// count of the current device (-1 if it cannot be asked; asked once per device).
+ffd_status cuda_status(cudaError_t e);
+int current_sm_count();
+
 __device__ __forceinline__ void raise_error(int *word, int bit) {
     if (word) atomicOr(word, bit);
 }

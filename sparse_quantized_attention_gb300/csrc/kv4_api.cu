@@ -1,0 +1,171 @@
+// kv4_api.cu -- the 4-bit cache's C entries (declared in include/ffd.h): argument checks, workspace
+// planning and launches.
+#include <math.h>
+
+#include "kv4.cuh"
+#include "ptx.cuh"
+
+namespace ffd {
+namespace kv4 {
+cudaError_t launch_write(const RowsArgs &a, int dtype, const void *k, const void *v, uint8_t *k4,
+                         uint8_t *v4, cudaStream_t stream);
+cudaError_t launch_read(const RowsArgs &a, int dtype, const uint8_t *k4, const uint8_t *v4, void *k,
+                        void *v, cudaStream_t stream);
+cudaError_t launch_attention(const AttnArgs &a, int dtype, cudaStream_t stream);
+}  // namespace kv4
+}  // namespace ffd
+
+using namespace ffd;
+using namespace ffd::kv4;
+
+namespace {
+
+constexpr size_t kAlign = 256;
+
+bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+// The checks that a write and a read share.
+ffd_status check_rows(const ffd_cache_desc *cache, int32_t dtype, int32_t batch, int32_t max_blocks,
+                      int32_t total, const void *k, int64_t k_stride, const void *v,
+                      int64_t v_stride, const int32_t *cu, const int32_t *positions,
+                      const int32_t *block_table, const uint8_t *k4, const uint8_t *v4) {
+    if (!cache || !positions || !block_table) return FFD_ERR_INVALID_ARG;
+    if (cache->num_pages < 1 || cache->num_kv_heads < 1 || batch < 1 || max_blocks < 1 || total < 0)
+        return FFD_ERR_INVALID_ARG;
+    if (cache->head_dim != kD || cache->page_size != kPage) return FFD_ERR_UNSUPPORTED;
+    if (dtype != FFD_DTYPE_BF16 && dtype != FFD_DTYPE_F16) return FFD_ERR_INVALID_ARG;
+    if (!cu && total % batch != 0) return FFD_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)cache->num_kv_heads * kD;
+    if (k && (k_stride < row || k_stride % 8 != 0 || !k4)) return FFD_ERR_INVALID_ARG;
+    if (v && (v_stride < row || v_stride % 8 != 0 || !v4)) return FFD_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k4, 16) || !aligned(v4, 16) ||
+        !aligned(cu, 4) || !aligned(positions, 4) || !aligned(block_table, 4))
+        return FFD_ERR_INVALID_ARG;
+    if ((int64_t)max_blocks * kPage > INT32_MAX) return FFD_ERR_UNSUPPORTED;
+    // the launch's blocks of 256 threads, 16 threads a (row, KV head) at most
+    if ((int64_t)total * cache->num_kv_heads > (int64_t)INT32_MAX * 16) return FFD_ERR_UNSUPPORTED;
+    return FFD_OK;
+}
+
+RowsArgs rows_args(const ffd_cache_desc *cache, int32_t batch, int32_t max_blocks, int32_t total,
+                   int64_t k_stride, int64_t v_stride, const int32_t *cu, const int32_t *positions,
+                   const int32_t *block_table, int32_t *error_word) {
+    RowsArgs a{};
+    a.B = batch;
+    a.Hkv = cache->num_kv_heads;
+    a.P = cache->num_pages;
+    a.max_blocks = max_blocks;
+    a.T = total;
+    a.per = cu ? 0 : total / batch;
+    a.cu = cu;
+    a.positions = positions;
+    a.block_table = block_table;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.err = error_word;
+    return a;
+}
+
+ffd_status check_params(const ffd_kv4_params *p) {
+    if (!p) return FFD_ERR_INVALID_ARG;
+    if (p->batch < 1 || p->num_q_heads < 1 || p->num_kv_heads < 1 || p->num_pages < 1 ||
+        p->max_blocks_per_seq < 1 || p->max_q_len < 1 || p->total_q < 1 || p->window < 0 ||
+        p->num_splits < 0 || p->wait_limit_us < 0)
+        return FFD_ERR_INVALID_ARG;
+    if (p->dtype != FFD_DTYPE_BF16 && p->dtype != FFD_DTYPE_F16) return FFD_ERR_INVALID_ARG;
+    if (p->num_q_heads % p->num_kv_heads != 0) return FFD_ERR_INVALID_ARG;
+    if (!isfinite(p->sm_scale) || !(p->sm_scale > 0.0f)) return FFD_ERR_INVALID_ARG;
+    if (p->q_stride != 0 && (p->q_stride < (int64_t)p->num_q_heads * kD || p->q_stride % 8 != 0))
+        return FFD_ERR_INVALID_ARG;
+    if (p->head_dim != kD || p->page_size != kPage) return FFD_ERR_UNSUPPORTED;
+    if (p->num_q_heads / p->num_kv_heads > kMaxG) return FFD_ERR_UNSUPPORTED;
+    if ((int64_t)p->batch * p->num_kv_heads > 65535) return FFD_ERR_UNSUPPORTED;
+    if ((int64_t)p->max_blocks_per_seq * kPage > INT32_MAX) return FFD_ERR_UNSUPPORTED;
+    return FFD_OK;
+}
+
+size_t workspace_bytes_of(const ffd_kv4_params *) { return kAlign; }
+
+}  // namespace
+
+extern "C" {
+
+ffd_status ffd_kv4_write(const ffd_cache_desc *cache, int32_t dtype, int32_t batch,
+                         int32_t max_blocks_per_seq, int32_t total_tokens, const void *k_new,
+                         int64_t k_stride, const void *v_new, int64_t v_stride,
+                         const int32_t *cu_tokens, const int32_t *positions,
+                         const int32_t *block_table, uint8_t *k4, uint8_t *v4,
+                         int32_t *error_word, void *stream) {
+    if (!k_new || !v_new) return FFD_ERR_INVALID_ARG;
+    const ffd_status st =
+        check_rows(cache, dtype, batch, max_blocks_per_seq, total_tokens, k_new, k_stride, v_new,
+                   v_stride, cu_tokens, positions, block_table, k4, v4);
+    if (st != FFD_OK) return st;
+    const RowsArgs a = rows_args(cache, batch, max_blocks_per_seq, total_tokens, k_stride, v_stride,
+                                 cu_tokens, positions, block_table, error_word);
+    return cuda_status(
+        launch_write(a, dtype, k_new, v_new, k4, v4, static_cast<cudaStream_t>(stream)));
+}
+
+ffd_status ffd_kv4_read(const ffd_cache_desc *cache, int32_t dtype, int32_t batch,
+                        int32_t max_blocks_per_seq, int32_t total_tokens, const int32_t *cu_tokens,
+                        const int32_t *positions, const int32_t *block_table, const uint8_t *k4,
+                        const uint8_t *v4, void *k_out, int64_t k_stride, void *v_out,
+                        int64_t v_stride, int32_t *error_word, void *stream) {
+    if (!k_out && !v_out) return FFD_ERR_INVALID_ARG;
+    const ffd_status st =
+        check_rows(cache, dtype, batch, max_blocks_per_seq, total_tokens, k_out, k_stride, v_out,
+                   v_stride, cu_tokens, positions, block_table, k4, v4);
+    if (st != FFD_OK) return st;
+    const RowsArgs a = rows_args(cache, batch, max_blocks_per_seq, total_tokens, k_stride, v_stride,
+                                 cu_tokens, positions, block_table, error_word);
+    return cuda_status(
+        launch_read(a, dtype, k4, v4, k_out, v_out, static_cast<cudaStream_t>(stream)));
+}
+
+size_t ffd_kv4_workspace_size(const ffd_kv4_params *params) {
+    return check_params(params) == FFD_OK ? workspace_bytes_of(params) : 0;
+}
+
+ffd_status ffd_kv4_attention(const ffd_kv4_params *params, const void *q, const uint8_t *k4,
+                             const uint8_t *v4, const int32_t *seq_lens, const int32_t *cu_q,
+                             const int32_t *block_table, const uint8_t *keep_in, void *out,
+                             float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!q || !k4 || !v4 || !seq_lens || !block_table || !out || !workspace)
+        return FFD_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k4, 16) || !aligned(v4, 16) || !aligned(out, 16) ||
+        !aligned(seq_lens, 4) || !aligned(cu_q, 4) || !aligned(block_table, 4) || !aligned(lse, 4) ||
+        !aligned(workspace, kAlign))
+        return FFD_ERR_INVALID_ARG;
+    const ffd_status st = check_params(params);
+    if (st != FFD_OK) return st;
+    const ffd_kv4_params &p = *params;
+    if (!cu_q && p.total_q != (int64_t)p.batch * p.max_q_len) return FFD_ERR_INVALID_ARG;
+    if (workspace_bytes < workspace_bytes_of(params)) return FFD_ERR_WORKSPACE;
+    AttnArgs a{};
+    a.B = p.batch;
+    a.Hq = p.num_q_heads;
+    a.Hkv = p.num_kv_heads;
+    a.G = p.num_q_heads / p.num_kv_heads;
+    a.P = p.num_pages;
+    a.max_blocks = p.max_blocks_per_seq;
+    a.max_q = p.max_q_len;
+    a.total_q = p.total_q;
+    a.window = p.window;
+    a.q_stride = p.q_stride ? p.q_stride : (int64_t)p.num_q_heads * kD;
+    a.sm_scale = p.sm_scale;
+    a.q = q;
+    a.k4 = k4;
+    a.v4 = v4;
+    a.keep_in = keep_in;
+    a.seq_lens = seq_lens;
+    a.cu_q = cu_q;
+    a.block_table = block_table;
+    a.out = out;
+    a.lse = lse;
+    a.err = static_cast<int *>(workspace);
+    a.wait_ns = p.wait_limit_us > 0 ? (uint64_t)p.wait_limit_us * 1000ull : kWaitTimeoutNs;
+    return cuda_status(launch_attention(a, p.dtype, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -53,6 +53,17 @@ class DecodeParams(ctypes.Structure):
                 ("wait_limit_us", ctypes.c_int32), ("schedule", ctypes.c_int32)]
 
 
+class Kv4Params(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("max_blocks_per_seq", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("max_q_len", ctypes.c_int32), ("total_q", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("num_splits", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64), ("sm_scale", ctypes.c_float),
+                ("wait_limit_us", ctypes.c_int32)]
+
+
 def make_params(batch, num_q_heads, num_kv_heads, num_pages, max_blocks_per_seq, *, sink=64,
                 local=1024, delta=5.0, sm_scale=None, num_splits=0,
                 wait_limit_us=0, schedule=0) -> DecodeParams:
@@ -119,6 +130,18 @@ def lib() -> ctypes.CDLL:
                                             ctypes.c_float, ctypes.c_int32] + [P] * 10 + \
                 [ctypes.c_size_t, P]
             L.ffd_art_attention.restype = st
+            i32, i64 = ctypes.c_int32, ctypes.c_int64
+            L.ffd_kv4_write.argtypes = [ctypes.POINTER(CacheDesc), i32, i32, i32, i32, P, i64, P,
+                                        i64] + [P] * 7
+            L.ffd_kv4_write.restype = st
+            L.ffd_kv4_read.argtypes = [ctypes.POINTER(CacheDesc), i32, i32, i32, i32] + [P] * 6 + \
+                [i64, P, i64, P, P]
+            L.ffd_kv4_read.restype = st
+            L.ffd_kv4_workspace_size.argtypes = [ctypes.POINTER(Kv4Params)]
+            L.ffd_kv4_workspace_size.restype = ctypes.c_size_t
+            L.ffd_kv4_attention.argtypes = [ctypes.POINTER(Kv4Params)] + [P] * 10 + \
+                [ctypes.c_size_t, P]
+            L.ffd_kv4_attention.restype = st
             L.ffd_set_profile_events.argtypes = [P, P]
             L.ffd_set_profile_events.restype = st
             L.ffd_get_error.argtypes = [P, P]
@@ -309,6 +332,168 @@ def ffd_dense_decode(params: DecodeParams, q, k, v, seq_lens, block_table, out, 
         ctypes.byref(params), _ptr(q), _ptr(k), _ptr(v), _ptr(seq_lens), _ptr(block_table),
         _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
         _stream(stream)), "ffd_dense_decode")
+
+# ---- the 4-bit cache ----------------------------------------------------------------------------
+KV4_RECORD_BYTES = 5120
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1}  # FFD_DTYPE_BF16, FFD_DTYPE_F16
+
+
+class Kv4Cache(NamedTuple):
+    """Keys and values in 4 bits, one record per (page, KV head) each (layout in include/ffd.h):
+    k4, v4 u8 [P, Hkv, 5120]."""
+    k4: torch.Tensor
+    v4: torch.Tensor
+
+
+def alloc_kv4_cache(num_pages: int, num_kv_heads: int, device="cuda") -> Kv4Cache:
+    shp = (num_pages, num_kv_heads, KV4_RECORD_BYTES)
+    return Kv4Cache(torch.empty(shp, dtype=torch.uint8, device=device),
+                    torch.empty(shp, dtype=torch.uint8, device=device))
+
+
+def _need(ok: bool, where: str):
+    if not ok:
+        raise FFDError(1, where)
+
+
+def _on_one_gpu(where: str, *tensors) -> int:
+    """Index of the device that holds every given tensor (None ones aside)."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.get_device() != dev):
+            raise FFDError(1, f"{where}: tensors on different devices, or not on a GPU")
+    return dev
+
+
+def _rows_ok(x, num_kv_heads) -> bool:
+    """Rows [T, Hkv, 128] of bf16 or fp16 that lie whole, any distance apart."""
+    return (x.dim() == 3 and x.dtype in _DTYPES and x.shape[1] == num_kv_heads
+            and x.shape[2] == HEAD_DIM and (x.shape[0] == 0 or (
+                x.stride(2) == 1 and (x.shape[1] == 1 or x.stride(1) == HEAD_DIM))))
+
+
+def _row_stride(x) -> int:
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * HEAD_DIM
+
+
+def _ints_ok(x, n) -> bool:
+    return x is None or (x.dtype == torch.int32 and x.dim() == 1 and x.shape[0] == n
+                         and x.is_contiguous())
+
+
+def _table_ok(x) -> bool:
+    return x.dtype == torch.int32 and x.dim() == 2 and x.is_contiguous()
+
+
+def _kv4_ok(cache) -> bool:
+    a, b = cache.k4, cache.v4
+    return (a.dtype == b.dtype == torch.uint8 and a.dim() == 3 and a.shape == b.shape
+            and a.shape[2] == KV4_RECORD_BYTES and a.is_contiguous() and b.is_contiguous())
+
+
+def _launch(dev: int, stream, call):
+    """call(stream pointer) on the tensors' device, on its current stream by default."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    raw = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if torch.cuda.current_device() == dev:
+        return call(raw)
+    with torch.cuda.device(dev):
+        return call(raw)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def ffd_kv4_write(k_new, v_new, positions, block_table, cache: Kv4Cache, *, cu_tokens=None,
+                  error_word=None, stream=None) -> None:
+    """Quantise rows k_new, v_new [T, Hkv, 128] (bf16 or fp16; rows may lie inside wider ones) into
+    the 4-bit cache. Sequence b's rows are cu_tokens[b] .. cu_tokens[b+1]-1 (T / B each when None)
+    and go to tokens positions[b], positions[b]+1, ... (negative: nothing for that sequence)."""
+    where = "ffd_kv4_write"
+    dev = _on_one_gpu(where, k_new, v_new, positions, block_table, *cache, cu_tokens, error_word)
+    _need(_kv4_ok(cache) and _table_ok(block_table), where)
+    (P, Hkv, _), B = cache.k4.shape, block_table.shape[0]
+    _need(_rows_ok(k_new, Hkv) and _rows_ok(v_new, Hkv) and k_new.dtype == v_new.dtype
+          and k_new.shape[0] == v_new.shape[0] and positions is not None
+          and _ints_ok(positions, B) and _ints_ok(cu_tokens, B + 1), where)
+    desc = CacheDesc(P, Hkv, HEAD_DIM, PAGE)
+    _check(_launch(dev, stream, lambda s: lib().ffd_kv4_write(
+        ctypes.byref(desc), _DTYPES[k_new.dtype], B, block_table.shape[1], k_new.shape[0],
+        _addr(k_new), _row_stride(k_new), _addr(v_new), _row_stride(v_new), _addr(cu_tokens),
+        _addr(positions), _addr(block_table), _addr(cache.k4), _addr(cache.v4),
+        _addr(error_word), s)), where)
+
+
+def ffd_kv4_read(cache: Kv4Cache, positions, block_table, k_out, v_out, *, cu_tokens=None,
+                 error_word=None, stream=None) -> None:
+    """The values the 4-bit cache holds, as rows k_out, v_out [T, Hkv, 128] (bf16 or fp16; either
+    may be None). Rows and tokens are matched as in ffd_kv4_write."""
+    where = "ffd_kv4_read"
+    dev = _on_one_gpu(where, cache.k4, cache.v4, positions, block_table, k_out, v_out, cu_tokens,
+                      error_word)
+    _need(_kv4_ok(cache) and _table_ok(block_table), where)
+    (P, Hkv, _), B = cache.k4.shape, block_table.shape[0]
+    rows = [x for x in (k_out, v_out) if x is not None]
+    _need(len(rows) > 0 and all(_rows_ok(x, Hkv) and x.dtype == rows[0].dtype
+                                and x.shape[0] == rows[0].shape[0] for x in rows)
+          and _ints_ok(positions, B) and _ints_ok(cu_tokens, B + 1), where)
+    desc = CacheDesc(P, Hkv, HEAD_DIM, PAGE)
+    ks, vs = (0 if x is None else _row_stride(x) for x in (k_out, v_out))
+    _check(_launch(dev, stream, lambda s: lib().ffd_kv4_read(
+        ctypes.byref(desc), _DTYPES[rows[0].dtype], B, block_table.shape[1], rows[0].shape[0],
+        _addr(cu_tokens), _addr(positions), _addr(block_table), _addr(cache.k4), _addr(cache.v4),
+        _addr(k_out), ks, _addr(v_out), vs, _addr(error_word), s)), where)
+
+
+def make_kv4_params(batch, num_q_heads, num_kv_heads, num_pages, max_blocks_per_seq, *,
+                    max_q_len=1, total_q=None, dtype=torch.bfloat16, window=0, sm_scale=None,
+                    num_splits=0, q_stride=0, wait_limit_us=0) -> Kv4Params:
+    """total_q None: every sequence has max_q_len query tokens."""
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(HEAD_DIM)
+    if total_q is None:
+        total_q = batch * max_q_len
+    return Kv4Params(batch, num_q_heads, num_kv_heads, HEAD_DIM, PAGE, num_pages,
+                     max_blocks_per_seq, _DTYPES[dtype], max_q_len, total_q, window, num_splits,
+                     q_stride, sm_scale, wait_limit_us)
+
+
+def ffd_kv4_workspace_size(params: Kv4Params) -> int:
+    return int(lib().ffd_kv4_workspace_size(ctypes.byref(params)))
+
+
+def alloc_kv4_workspace(params: Kv4Params, device="cuda") -> torch.Tensor:
+    n = ffd_kv4_workspace_size(params)
+    if n == 0:
+        raise FFDError(1, "4-bit attention workspace size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def ffd_kv4_attention(params: Kv4Params, q, cache: Kv4Cache, seq_lens, block_table, out, workspace,
+                      *, cu_q=None, keep_in=None, lse=None, stream=None) -> None:
+    """Attention of each sequence's newest tokens over its 4-bit cache: q [total_q, Hq, 128], rows
+    params.q_stride elements apart, out [total_q, Hq, 128], lse fp32 [total_q, Hq] or None."""
+    where = "ffd_kv4_attention"
+    dev = _on_one_gpu(where, q, *cache, seq_lens, block_table, out, workspace, cu_q, keep_in, lse)
+    B, Hq, Hkv, T = params.batch, params.num_q_heads, params.num_kv_heads, params.total_q
+    _need(_kv4_ok(cache) and cache.k4.shape[0] == params.num_pages and cache.k4.shape[1] == Hkv
+          and _table_ok(block_table) and block_table.shape == (B, params.max_blocks_per_seq)
+          and _rows_ok(q, Hq) and _rows_ok(out, Hq) and q.shape[0] == T and out.is_contiguous()
+          and out.shape[0] == T and q.dtype == out.dtype and _DTYPES[q.dtype] == params.dtype
+          and (T <= 1 or q.stride(0) == (params.q_stride or Hq * HEAD_DIM))
+          and _ints_ok(seq_lens, B) and _ints_ok(cu_q, B + 1)
+          and (keep_in is None or (
+              keep_in.dtype == torch.uint8 and keep_in.is_contiguous()
+              and keep_in.shape == (B, Hkv, params.max_blocks_per_seq)))
+          and (lse is None or (lse.dtype == torch.float32 and lse.is_contiguous()
+                               and lse.shape == (T, Hq)))
+          and workspace.is_contiguous(), where)
+    _check(_launch(dev, stream, lambda s: lib().ffd_kv4_attention(
+        ctypes.byref(params), _addr(q), _addr(cache.k4), _addr(cache.v4), _addr(seq_lens),
+        _addr(cu_q), _addr(block_table), _addr(keep_in), _addr(out), _addr(lse), _addr(workspace),
+        workspace.numel() * workspace.element_size(), s)), where)
 
 
 def ffd_get_error(error_word, *, stream=None) -> int:

@@ -1,0 +1,165 @@
+"""Refusals of the 4-bit cache's entries (no GPU needed): bad arguments come back as a status, or as
+an FFDError from the binding, before anything is enqueued."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import sparse_quantized_attention_gb300 as ffd
+from sparse_quantized_attention_gb300 import _build
+
+FAKE = 0x10000  # never dereferenced: every call here fails validation first
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return ffd.lib()
+
+
+def test_exports_and_version(lib):
+    raw = ctypes.CDLL(_build.LIB)
+    for name in ("ffd_kv4_write", "ffd_kv4_read", "ffd_kv4_workspace_size", "ffd_kv4_attention"):
+        assert hasattr(raw, name)
+    assert ffd.ffd_version() == 310
+
+
+def rows_call(lib, read, desc=(4, 2, 128, 64), dtype=0, batch=2, mb=3, total=6, ks=256, vs=256,
+              **kw):
+    a = dict(k=FAKE, v=FAKE, cu=FAKE, pos=FAKE, bt=FAKE, k4=FAKE, v4=FAKE)
+    a.update(kw)
+    d = ctypes.byref(ffd.CacheDesc(*desc)) if desc else None
+    if read:
+        return lib.ffd_kv4_read(d, dtype, batch, mb, total, a["cu"], a["pos"], a["bt"], a["k4"],
+                                a["v4"], a["k"], ks, a["v"], vs, None, None)
+    return lib.ffd_kv4_write(d, dtype, batch, mb, total, a["k"], ks, a["v"], vs, a["cu"], a["pos"],
+                             a["bt"], a["k4"], a["v4"], None, None)
+
+
+@pytest.mark.parametrize("read", [False, True], ids=["write", "read"])
+@pytest.mark.parametrize("kw,status", [
+    (dict(desc=None), 1),
+    (dict(desc=(0, 2, 128, 64)), 1),
+    (dict(desc=(4, 0, 128, 64)), 1),
+    (dict(desc=(4, 2, 64, 64)), 2),
+    (dict(desc=(4, 2, 128, 32)), 2),
+    (dict(dtype=2), 1),
+    (dict(dtype=-1), 1),
+    (dict(batch=0), 1),
+    (dict(mb=0), 1),
+    (dict(mb=1 << 26), 2),
+    (dict(total=-1), 1),
+    (dict(cu=None, total=5), 1),       # rows not shared out evenly
+    (dict(ks=255), 1),
+    (dict(ks=260), 1),
+    (dict(vs=128), 1),
+    (dict(k=FAKE + 8), 1),
+    (dict(v=FAKE + 2), 1),
+    (dict(k4=FAKE + 8), 1),
+    (dict(v4=None), 1),
+    (dict(cu=FAKE + 2), 1),
+    (dict(pos=None), 1),
+    (dict(bt=None), 1),
+    (dict(k=None, v=None), 1),
+    (dict(desc=(4, 1 << 20, 128, 64), ks=1 << 27, vs=1 << 27, total=1 << 30), 2),
+])
+def test_rows_refusals(lib, read, kw, status):
+    assert rows_call(lib, read, **kw) == status
+
+
+def test_write_wants_both_tensors(lib):
+    assert rows_call(lib, False, k=None) == 1
+    assert rows_call(lib, False, v=None) == 1
+
+
+def test_no_rows_is_no_work(lib):
+    assert rows_call(lib, False, total=0) == 0
+    assert rows_call(lib, True, total=0) == 0
+
+
+def params(**kw):
+    base = dict(batch=2, num_q_heads=8, num_kv_heads=2, num_pages=10, max_blocks_per_seq=5,
+                max_q_len=3, total_q=6, num_splits=2)
+    base.update(kw)
+    return ffd.make_kv4_params(base.pop("batch"), base.pop("num_q_heads"),
+                               base.pop("num_kv_heads"), base.pop("num_pages"),
+                               base.pop("max_blocks_per_seq"), **base)
+
+
+def attend(lib, p, ws_bytes=1 << 40, **kw):
+    a = dict(q=FAKE, k4=FAKE, v4=FAKE, sl=FAKE, cu=FAKE, bt=FAKE, keep=None, out=FAKE, lse=None,
+             ws=FAKE)
+    a.update(kw)
+    return lib.ffd_kv4_attention(ctypes.byref(p) if p else None, *[a[k] for k in (
+        "q", "k4", "v4", "sl", "cu", "bt", "keep", "out", "lse", "ws")], ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(batch=0), 1),
+    (dict(num_q_heads=7), 1),
+    (dict(num_q_heads=18), 2),          # G = 9
+    (dict(num_pages=0), 1),
+    (dict(max_blocks_per_seq=0), 1),
+    (dict(max_blocks_per_seq=1 << 26), 2),
+    (dict(max_q_len=0), 1),
+    (dict(total_q=0), 1),
+    (dict(window=-1), 1),
+    (dict(num_splits=-1), 1),
+    (dict(wait_limit_us=-1), 1),
+    (dict(sm_scale=0.0), 1),
+    (dict(sm_scale=-1.0), 1),
+    (dict(sm_scale=math.nan), 1),
+    (dict(sm_scale=math.inf), 1),
+    (dict(q_stride=8), 1),
+    (dict(q_stride=1028), 1),
+    (dict(batch=40000), 2),
+])
+def test_attention_refuses_params(lib, kw, status):
+    p = params(**kw)
+    assert attend(lib, p) == status
+    assert ffd.ffd_kv4_workspace_size(p) == 0
+
+
+def test_attention_refuses_shapes_and_pointers(lib):
+    p = params()
+    need = ffd.ffd_kv4_workspace_size(p)
+    assert need > 0 and need % 256 == 0
+    for field, value, status in (("head_dim", 64, 2), ("page_size", 16, 2), ("dtype", 3, 1)):
+        bad = params()
+        setattr(bad, field, value)
+        assert attend(lib, bad) == status
+    assert attend(lib, None) == 1
+    for key in ("q", "k4", "v4", "sl", "bt", "out", "ws"):
+        assert attend(lib, p, **{key: None}) == 1, key
+    for key, off in (("q", 8), ("k4", 4), ("v4", 8), ("out", 2), ("ws", 16), ("cu", 2), ("sl", 1),
+                     ("lse", 2)):
+        assert attend(lib, p, **{key: FAKE + off}) == 1, key
+    assert attend(lib, p, ws_bytes=need - 1) == 3
+    # without offsets every sequence has max_q_len rows
+    assert attend(lib, params(total_q=5), cu=None) == 1
+
+
+def test_binding_refuses_tensors(lib):
+    """CPU tensors and wrong shapes or types never reach a kernel."""
+    bt = torch.zeros((2, 3), dtype=torch.int32)
+    pos = torch.zeros(2, dtype=torch.int32)
+    x = torch.zeros((2, 2, 128), dtype=torch.bfloat16)
+    cache = ffd.alloc_kv4_cache(4, 2, device="cpu")
+    with pytest.raises(ffd.FFDError):
+        ffd.ffd_kv4_write(x, x, pos, bt, cache)
+    with pytest.raises(ffd.FFDError):
+        ffd.ffd_kv4_read(cache, pos, bt, x, None)
+    p = params(max_q_len=1, total_q=2)
+    q = torch.zeros((2, 8, 128), dtype=torch.bfloat16)
+    with pytest.raises(ffd.FFDError):
+        ffd.ffd_kv4_attention(p, q, cache, pos, bt, q.clone(), torch.zeros(1 << 20))
+    ok = ffd.ffd
+    assert ok._rows_ok(x, 2) and not ok._rows_ok(x, 1) and not ok._rows_ok(x.float(), 2)
+    assert not ok._rows_ok(x.transpose(1, 2), 128)
+    wide = torch.zeros((2, 600), dtype=torch.bfloat16)
+    assert ok._rows_ok(wide[:, 8:264].unflatten(1, (2, 128)), 2)
+    assert not ok._rows_ok(wide[:, :512:2].unflatten(1, (2, 128)), 2)
+    assert not ok._ints_ok(pos.long(), 2) and not ok._ints_ok(pos, 3)
+    assert not ok._table_ok(bt[:, :2])
+    assert not ok._kv4_ok(ffd.Kv4Cache(cache.k4, cache.v4[:2]))
