@@ -129,10 +129,15 @@ struct AttnArgs {
     const int32_t *seq_lens, *cu_q, *block_table;
     void *out;
     float *lse;
-    int *err;
-    float *ws_part;
-    int *ws_cnt;
+    int *err;  // the workspace: error word first
     uint64_t wait_ns;
+};
+
+// Launch shape and workspace of an attention call (byte offsets behind the error word).
+struct Plan {
+    int cols;  // query columns of the decode kernel (8 or 16), 0: rows go one by one
+    int ctas;
+    size_t tickets, records, parked, total;
 };
 
 }  // namespace kv4

@@ -11,7 +11,10 @@ cudaError_t launch_write(const RowsArgs &a, int dtype, const void *k, const void
                          uint8_t *v4, cudaStream_t stream);
 cudaError_t launch_read(const RowsArgs &a, int dtype, const uint8_t *k4, const uint8_t *v4, void *k,
                         void *v, cudaStream_t stream);
-cudaError_t launch_attention(const AttnArgs &a, int dtype, cudaStream_t stream);
+cudaError_t launch_rows(const AttnArgs &a, int dtype, cudaStream_t stream);
+cudaError_t launch_decode(const AttnArgs &a, const Plan &pl, int dtype, cudaStream_t stream);
+size_t decode_record_bytes(int cols);
+int decode_warps();
 }  // namespace kv4
 }  // namespace ffd
 
@@ -21,6 +24,7 @@ using namespace ffd::kv4;
 namespace {
 
 constexpr size_t kAlign = 256;
+constexpr size_t kMaxUnits = 65535;  // (sequence, KV head) pairs of an attention call
 
 bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
@@ -79,12 +83,47 @@ ffd_status check_params(const ffd_kv4_params *p) {
         return FFD_ERR_INVALID_ARG;
     if (p->head_dim != kD || p->page_size != kPage) return FFD_ERR_UNSUPPORTED;
     if (p->num_q_heads / p->num_kv_heads > kMaxG) return FFD_ERR_UNSUPPORTED;
-    if ((int64_t)p->batch * p->num_kv_heads > 65535) return FFD_ERR_UNSUPPORTED;
+    if ((int64_t)p->batch * p->num_kv_heads > (int64_t)kMaxUnits) return FFD_ERR_UNSUPPORTED;
     if ((int64_t)p->max_blocks_per_seq * kPage > INT32_MAX) return FFD_ERR_UNSUPPORTED;
+    // a page of a unit is named by an int32
+    if ((int64_t)p->batch * p->num_kv_heads * p->max_blocks_per_seq > INT32_MAX)
+        return FFD_ERR_UNSUPPORTED;
     return FFD_OK;
 }
 
-size_t workspace_bytes_of(const ffd_kv4_params *) { return kAlign; }
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+// At least this many pages (upper bound from the table's width) for each CTA of the decode kernel.
+constexpr int64_t kMinPagesPerCta = 8;
+
+// Workspace: [error word | merge tickets per unit | two records per CTA | a parked state per warp].
+// The tickets, the only part that has to start at zero, have the same place and room for the most
+// units whatever the parameters, so that calls of different shapes can share a workspace.
+ffd_status make_plan(const ffd_kv4_params *p, Plan *pl) {
+    const ffd_status st = check_params(p);
+    if (st != FFD_OK) return st;
+    const int64_t units = (int64_t)p->batch * p->num_kv_heads;
+    const int64_t rows = (int64_t)p->max_q_len * (p->num_q_heads / p->num_kv_heads);
+    const int sms = current_sm_count();
+    int64_t ctas = p->num_splits;
+    if (ctas == 0) {
+        if (sms <= 0) return FFD_ERR_CUDA;
+        ctas = (units * p->max_blocks_per_seq + kMinPagesPerCta - 1) / kMinPagesPerCta;
+    }
+    if (sms > 0 && ctas > sms) ctas = sms;
+    pl->ctas = (int)ctas;
+    pl->cols = rows <= 8 ? 8 : rows <= 16 ? 16 : 0;
+    const size_t rec = decode_record_bytes(pl->cols);
+    size_t off = kAlign;
+    pl->tickets = off;
+    off = align_up(off + kMaxUnits * sizeof(int));
+    pl->records = off;
+    off = align_up(off + 2 * pl->ctas * rec);
+    pl->parked = off;
+    off = align_up(off + (size_t)pl->ctas * decode_warps() * rec);
+    pl->total = off;
+    return FFD_OK;
+}
 
 }  // namespace
 
@@ -124,7 +163,8 @@ ffd_status ffd_kv4_read(const ffd_cache_desc *cache, int32_t dtype, int32_t batc
 }
 
 size_t ffd_kv4_workspace_size(const ffd_kv4_params *params) {
-    return check_params(params) == FFD_OK ? workspace_bytes_of(params) : 0;
+    Plan pl;
+    return make_plan(params, &pl) == FFD_OK ? pl.total : 0;
 }
 
 ffd_status ffd_kv4_attention(const ffd_kv4_params *params, const void *q, const uint8_t *k4,
@@ -137,11 +177,12 @@ ffd_status ffd_kv4_attention(const ffd_kv4_params *params, const void *q, const 
         !aligned(seq_lens, 4) || !aligned(cu_q, 4) || !aligned(block_table, 4) || !aligned(lse, 4) ||
         !aligned(workspace, kAlign))
         return FFD_ERR_INVALID_ARG;
-    const ffd_status st = check_params(params);
+    Plan pl;
+    const ffd_status st = make_plan(params, &pl);
     if (st != FFD_OK) return st;
     const ffd_kv4_params &p = *params;
     if (!cu_q && p.total_q != (int64_t)p.batch * p.max_q_len) return FFD_ERR_INVALID_ARG;
-    if (workspace_bytes < workspace_bytes_of(params)) return FFD_ERR_WORKSPACE;
+    if (workspace_bytes < pl.total) return FFD_ERR_WORKSPACE;
     AttnArgs a{};
     a.B = p.batch;
     a.Hq = p.num_q_heads;
@@ -165,7 +206,8 @@ ffd_status ffd_kv4_attention(const ffd_kv4_params *params, const void *q, const 
     a.lse = lse;
     a.err = static_cast<int *>(workspace);
     a.wait_ns = p.wait_limit_us > 0 ? (uint64_t)p.wait_limit_us * 1000ull : kWaitTimeoutNs;
-    return cuda_status(launch_attention(a, p.dtype, static_cast<cudaStream_t>(stream)));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return cuda_status(pl.cols ? launch_decode(a, pl, p.dtype, s) : launch_rows(a, p.dtype, s));
 }
 
 }  // extern "C"

@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(128) kv4_rows_kernel(const AttnArgs a) {
 
 }  // namespace
 
-cudaError_t launch_attention(const AttnArgs &a, int dtype, cudaStream_t stream) {
+cudaError_t launch_rows(const AttnArgs &a, int dtype, cudaStream_t stream) {
     const int64_t grid = ((int64_t)a.total_q * a.Hq + 3) / 4;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
     if (dtype == FFD_DTYPE_BF16) kv4_rows_kernel<Bf16><<<(unsigned)grid, 128, 0, stream>>>(a);

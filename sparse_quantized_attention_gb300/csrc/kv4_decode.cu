@@ -1,0 +1,740 @@
+// kv4_decode.cu -- attention over the 4-bit cache for few query rows: up to 8 NT (row, head) pairs
+// share a KV head (NT = 1: one decode token of any GQA group; NT = 2: up to 16 pairs).
+//
+// The definition is the one of ffd.h. The pages of all (sequence, KV head) units, concatenated, are
+// cut into equal contiguous ranges, one per CTA, and each range into one per warp. A warp walks its
+// pages alone: it has room for one page's K record and one V record in shared memory, each refilled
+// by a bulk copy as soon as it has been read, computes
+//   S = K q^T   (16 tokens x 8 columns a matrix instruction, 8 of them over the 128 channels),
+//   P = 2^(S - m) against the running maximum m of each column,
+//   O^T += V^T P^T (16 channels x 8 columns, 8 of them over the 128 channels)
+// with K and V formed in registers from the codes (one shift, one logical operation and one fused
+// multiply-add a pair of values, exact by the format), and keeps m, the sum l and O^T in registers
+// throughout; no barrier stands in the loop. At the end a CTA's warps join their states through
+// shared memory, and the last CTA of a unit joins those of the CTAs (order fixed by page, so the
+// result does not depend on arrival).
+//
+// P is rounded to f16 against a reference of 2^14, so probabilities down to 2^-28 of the largest
+// keep all 11 bits. q enters as f16 scaled by a power of two per column (its largest magnitude in
+// [2^13, 2^14)): exact for bf16 and f16 queries apart from elements below 2^-27 of the largest.
+#include "kv4.cuh"
+#include "ptx.cuh"
+
+namespace ffd {
+namespace kv4 {
+namespace {
+
+constexpr int kWarps = 16;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kSlot = 2 * kRec;       // a warp's K record and V record
+constexpr int kStride = 130;          // floats of a joined column: o[128], m, l
+constexpr float kShift = 14.0f;       // P carries 2^14
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct Shared {
+    uint8_t ring[kWarps][kSlot];      // later each warp's last state
+    uint64_t full[kWarps][2];
+    int pre[kThreads + 1];            // items before each thread's chunk of sequences
+    int scan[kWarps];
+    int unit[kWarps][2];              // unit of a warp's parked and of its last state, or -1
+    int flag;
+};
+static_assert(sizeof(Shared) + 128 <= 232448, "shared memory per CTA");
+
+// One sequence as the walk sees it.
+struct Seq {
+    int n, t0, nq;  // tokens, first query row, query rows
+    int fp, np;     // first page any query sees, pages from there to the last
+};
+
+__device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, bool report) {
+    Seq s;
+    s.n = __ldg(a.seq_lens + b);
+    const int cap = a.max_blocks * kPage;
+    bool bad = s.n < 0 || s.n > cap;
+    s.n = s.n < 0 ? 0 : (s.n > cap ? cap : s.n);
+    s.t0 = b * a.max_q;
+    s.nq = a.max_q;
+    if (a.cu_q) {
+        s.t0 = __ldg(a.cu_q + b);
+        const int end = __ldg(a.cu_q + b + 1);
+        if (s.t0 < 0 || end < s.t0 || end > a.total_q || end - s.t0 > a.max_q) {
+            bad = true;
+            s.nq = 0;
+        } else {
+            s.nq = end - s.t0;
+        }
+    }
+    if (report && bad) raise_error(a.err, FFD_ERRBIT_BOUNDS);
+    s.fp = 0;
+    if (a.window > 0) {
+        const int64_t first = (int64_t)s.n - s.nq - a.window + 1;
+        s.fp = first > 0 ? (int)(first >> 6) : 0;
+    }
+    s.np = s.n > 0 && s.nq > 0 ? ((s.n + kPage - 1) >> 6) - s.fp : 0;
+    return s;
+}
+
+// Where an item lies: unit (b, h), page j of the unit's np.
+struct At {
+    int b, h, j;
+    Seq s;
+};
+
+__device__ __forceinline__ At locate(const AttnArgs &a, const Shared &sh, int chunk, int x) {
+    int lo = 0, hi = kThreads;  // the last chunk that starts at or before x
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sh.pre[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    At p;
+    int rem = x - sh.pre[lo];
+    for (p.b = lo * chunk; p.b < a.B; p.b++) {
+        p.s = seq_of(a, p.b, false);
+        const int span = p.s.np * a.Hkv;
+        if (rem < span) break;
+        rem -= span;
+    }
+    p.h = rem / p.s.np;
+    p.j = rem - p.h * p.s.np;
+    return p;
+}
+
+// Softmax state of a warp: columns 2 tig, 2 tig + 1 of each 8-column tile (tig = lane % 4). m is the
+// columns' reference (log2 units), the same in all lanes of a column; l sums this lane's rows;
+// o[t][c] is channel 16 g + c (and 16 g + 8 + c) of the two columns (g = lane / 4).
+template <int NT>
+struct State {
+    float m[NT][2], l[NT][2], o[NT][8][4];
+    __device__ void clear() {
+#pragma unroll
+        for (int t = 0; t < NT; t++) {
+            m[t][0] = m[t][1] = -INFINITY;
+            l[t][0] = l[t][1] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < 8; c++) o[t][c][0] = o[t][c][1] = o[t][c][2] = o[t][c][3] = 0.0f;
+        }
+    }
+    // l of the whole column in every lane
+    __device__ void close() {
+#pragma unroll
+        for (int t = 0; t < NT; t++)
+#pragma unroll
+            for (int e = 0; e < 2; e++)
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], x);
+    }
+};
+
+// A column's row of q, out and lse; false when the column has none.
+__device__ __forceinline__ bool column(const AttnArgs &a, const Seq &s, int h, int c, int &row,
+                                       int &hq, int &i) {
+    i = c / a.G;
+    row = s.t0 + i;
+    hq = h * a.G + c - i * a.G;
+    return i < s.nq;
+}
+
+// Query fragments of the NT tiles: column g of tile t, channels 32 tig .. 32 tig + 31, as f16 pairs
+// of q 2^(13 - e) (e: exponent of the column's largest magnitude); fs[t][2]: log2-unit factors
+// sm log2(e) 2^(e - 13) of columns 2 tig, 2 tig + 1.
+template <int NT, class T>
+__device__ __forceinline__ void load_queries(const AttnArgs &a, const Seq &s, int h, int lane,
+                                             uint32_t (&qf)[NT][16], float (&fs)[NT][2]) {
+    const int g = lane >> 2, tig = lane & 3;
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+        int row, hq, i;
+        const bool have = column(a, s, h, 8 * t + g, row, hq, i);
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            static_cast<const uint16_t *>(a.q) + (int64_t)(have ? row : 0) * a.q_stride +
+            (have ? hq : 0) * kD + 32 * tig);
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const uint4 u = have ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+            w[4 * j] = u.x;
+            w[4 * j + 1] = u.y;
+            w[4 * j + 2] = u.z;
+            w[4 * j + 3] = u.w;
+        }
+        float top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 16; j++) {
+            const float2 f = T::unpack(w[j]);
+            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        int e = (int)(__float_as_uint(top) >> 23) - 127;
+        e = e < -100 ? -100 : (e > 127 ? 127 : e);
+        const float mul = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
+        const float f = a.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 + e - 13) << 23);
+#pragma unroll
+        for (int j = 0; j < 16; j++) {
+            const float2 v = T::unpack(w[j]);
+            qf[t][j] = F16::pack(v.x * mul, v.y * mul);
+        }
+        fs[t][0] = __shfl_sync(0xffffffffu, f, 8 * tig);
+        fs[t][1] = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
+    }
+}
+
+// Scores of one page: x[t][4 tile + r] as in the matrix instruction's result (rows g, g + 8 of the
+// page's 16-token tile, columns 2 tig, 2 tig + 1). K of a row: the lane holds group tig of rows g and
+// g + 8 of a tile, 16 code bytes and one (scale, off) pair each.
+template <int NT>
+__device__ __forceinline__ void page_scores(const uint8_t *k, int lane, const uint32_t (&qf)[NT][16],
+                                            float (&x)[NT][4][4]) {
+    const int g = lane >> 2, tig = lane & 3;
+    const uint8_t *codes = k + (g >> 1) * 128 + (((2 * (g & 1) + (tig >> 1)) ^ (g >> 1)) << 5) +
+                           (tig & 1) * 16;
+    const uint8_t *par = k + kParamOff + 16 * g + 4 * tig;
+#pragma unroll
+    for (int tile = 0; tile < 4; tile++) {
+        const uint4 c0 = *reinterpret_cast<const uint4 *>(codes + tile * 1024);
+        const uint4 c1 = *reinterpret_cast<const uint4 *>(codes + tile * 1024 + 512);
+        const __half2 p0 = *reinterpret_cast<const __half2 *>(par + tile * 256);
+        const __half2 p1 = *reinterpret_cast<const __half2 *>(par + tile * 256 + 128);
+        const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w}, w1[4] = {c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+        for (int t = 0; t < NT; t++) x[t][tile][0] = x[t][tile][1] = x[t][tile][2] = x[t][tile][3] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            __half2 v0[4], v1[4];
+            decode_word(w0[j], p0, v0);
+            decode_word(w1[j], p1, v1);
+            const uint32_t *r0 = reinterpret_cast<const uint32_t *>(v0);
+            const uint32_t *r1 = reinterpret_cast<const uint32_t *>(v1);
+#pragma unroll
+            for (int t = 0; t < NT; t++) {
+                mma_f16(x[t][tile], r0[0], r1[0], r0[1], r1[1], qf[t][4 * j], qf[t][4 * j + 1]);
+                mma_f16(x[t][tile], r0[2], r1[2], r0[3], r1[3], qf[t][4 * j + 2], qf[t][4 * j + 3]);
+            }
+        }
+    }
+}
+
+// Value pairs (tokens of the low and the high half) of nibble pair i of prmt'ed code words.
+template <int NT>
+__device__ __forceinline__ void page_values(const uint8_t *v, int lane, int valid,
+                                            const uint32_t (&pf)[NT][4][2], State<NT> &st) {
+    const int g = lane >> 2, tig = lane & 3;
+    const uint8_t *par = v + kParamOff + 32 * tig + 4 * (g >> 1);
+    const uint8_t *codes[2];
+#pragma unroll
+    for (int e = 0; e < 2; e++)
+        codes[e] = v + tig * 128 + (((2 * e + (g >> 2)) ^ tig) << 5) + ((g >> 1) & 1) * 16 + (g & 1) * 8;
+#pragma unroll
+    for (int tile = 0; tile < 4; tile++) {
+        // [half of the tile] token pairs 16 tile + 8 half + 2 tig, + 1
+        uint32_t s[2], o[2];
+        uint2 c[2][2];
+#pragma unroll
+        for (int hi = 0; hi < 2; hi++) {
+            uint32_t q0 = *reinterpret_cast<const uint32_t *>(par + tile * 256 + hi * 128);
+            uint32_t q1 = *reinterpret_cast<const uint32_t *>(par + tile * 256 + hi * 128 + 16);
+            if (valid < kPage) {  // tokens past the sequence hold anything: make them 0
+                const int r = 16 * tile + 8 * hi + 2 * tig;
+                q0 = r < valid ? q0 : 0u;
+                q1 = r + 1 < valid ? q1 : 0u;
+            }
+            s[hi] = __byte_perm(q0, q1, 0x5410);
+            o[hi] = __byte_perm(q0, q1, 0x7632);
+#pragma unroll
+            for (int e = 0; e < 2; e++)
+                c[hi][e] = *reinterpret_cast<const uint2 *>(codes[e] + tile * 1024 + hi * 512);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; e++) {  // even channels of the words, then odd ones
+            const uint32_t sel = e ? 0x7632 : 0x5410;
+            uint32_t w[2][2];  // [word][half]
+#pragma unroll
+            for (int hi = 0; hi < 2; hi++) {
+                w[0][hi] = __byte_perm(c[hi][0].x, c[hi][1].x, sel);
+                w[1][hi] = __byte_perm(c[hi][0].y, c[hi][1].y, sel);
+            }
+            uint32_t f[4][4];  // [channel pair i][a0..a3]
+#pragma unroll
+            for (int word = 0; word < 2; word++)
+#pragma unroll
+                for (int hi = 0; hi < 2; hi++) {
+                    const __half2 ss = *reinterpret_cast<const __half2 *>(&s[hi]);
+                    const __half2 oo = *reinterpret_cast<const __half2 *>(&o[hi]);
+                    const uint32_t ww = w[word][hi];
+                    const __half2 r[4] = {__hfma2(code_pair<0>(ww), ss, oo),
+                                          __hfma2(code_pair<1>(ww), ss, oo),
+                                          __hfma2(code_pair<2>(ww), ss, oo),
+                                          __hfma2(code_pair<3>(ww), ss, oo)};
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        f[i][2 * hi + word] = *reinterpret_cast<const uint32_t *>(&r[i]);
+                }
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+#pragma unroll
+                for (int t = 0; t < NT; t++)
+                    mma_f16(st.o[t][2 * i + e], f[i][0], f[i][1], f[i][2], f[i][3], pf[t][tile][0],
+                            pf[t][tile][1]);
+        }
+    }
+}
+
+// Final value of a column: rows of out and lse.
+template <class T>
+__device__ __forceinline__ void write_pair(const AttnArgs &a, int row, int hq, int ch, float x,
+                                           float y) {
+    *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) +
+                                  ((int64_t)row * a.Hq + hq) * kD + ch) = T::pack(x, y);
+}
+
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l > 0.0f ? (m + log2f(l) - kShift) * kLn2 : -INFINITY;
+}
+
+// A unit that one warp walked whole: its rows, straight from the registers.
+template <int NT, class T>
+__device__ __forceinline__ void write_direct(const AttnArgs &a, const Seq &s, int h, int lane,
+                                             const State<NT> &st) {
+    const int g = lane >> 2, tig = lane & 3;
+#pragma unroll
+    for (int t = 0; t < NT; t++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            int row, hq, i;
+            if (!column(a, s, h, 8 * t + 2 * tig + e, row, hq, i)) continue;
+            const float l = st.l[t][e], inv = l == 0.0f ? 0.0f : 1.0f / l;
+            uint32_t w[8];
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                w[c] = T::pack(st.o[t][2 * c][e] * inv, st.o[t][2 * c + 1][e] * inv);
+                w[4 + c] = T::pack(st.o[t][2 * c][2 + e] * inv, st.o[t][2 * c + 1][2 + e] * inv);
+            }
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) +
+                                                   ((int64_t)row * a.Hq + hq) * kD + 16 * g);
+            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            if (a.lse && g == 0) a.lse[(int64_t)row * a.Hq + hq] = lse_of(st.m[t][e], l);
+        }
+}
+
+// A warp's state as 8 NT columns of kStride floats.
+template <int NT>
+__device__ __forceinline__ void park(float *rec, int lane, const State<NT> &st) {
+    const int g = lane >> 2, tig = lane & 3;
+#pragma unroll
+    for (int t = 0; t < NT; t++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            float *col = rec + (8 * t + 2 * tig + e) * kStride;
+#pragma unroll
+            for (int c = 0; c < 8; c += 2) {
+                *reinterpret_cast<float2 *>(col + 16 * g + c) =
+                    make_float2(st.o[t][c][e], st.o[t][c + 1][e]);
+                *reinterpret_cast<float2 *>(col + 16 * g + 8 + c) =
+                    make_float2(st.o[t][c][2 + e], st.o[t][c + 1][2 + e]);
+            }
+            if (g == 0) *reinterpret_cast<float2 *>(col + 128) = make_float2(st.m[t][e], st.l[t][e]);
+        }
+}
+
+// Bounded wait of a warp for one of its copies; `dead` once a wait ran out.
+__device__ __forceinline__ void wait_copy(const AttnArgs &a, uint64_t *bar, uint32_t parity,
+                                          bool &dead) {
+    if (mbar_try_wait(bar, parity)) return;
+    const uint64_t t0 = globaltimer_ns();
+    bool late = false;
+    while (!mbar_try_wait(bar, parity)) {
+        if (globaltimer_ns() - t0 > a.wait_ns) {
+            late = true;
+            break;
+        }
+    }
+    if (late) {
+        raise_error(a.err, FFD_ERRBIT_TIMEOUT);
+        dead = true;
+    }
+}
+
+template <int NT, class T>
+__global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const AttnArgs a, float *parked,
+                                                                 float *records, int *tickets) {
+    extern __shared__ uint8_t raw[];
+    Shared &sh = *reinterpret_cast<Shared *>(align_shared<128>(raw));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cols = 8 * NT;
+
+    // ---- items before each chunk of sequences -------------------------------------------------
+    const int chunk = (a.B + kThreads - 1) / kThreads;
+    int own = 0;
+    bool empty = false;  // a sequence has queries and nothing for them to see
+    for (int b = tid * chunk; b < (tid + 1) * chunk && b < a.B; b++) {
+        const Seq s = seq_of(a, b, blockIdx.x == 0);
+        own += s.np * a.Hkv;
+        empty |= s.np == 0 && s.nq > 0;
+    }
+    int inc = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) sh.scan[warp] = inc;
+    if (lane < 2) {
+        mbar_init(&sh.full[warp][lane], 1);
+        sh.unit[warp][lane] = -1;
+    }
+    fence_barrier_init();
+    const bool any_empty = __syncthreads_or(empty);
+    int base = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) {
+        const int v = sh.scan[w];
+        base += w < warp ? v : 0;
+        total += v;
+    }
+    sh.pre[tid] = base + inc - own;
+    __syncthreads();
+
+    if (any_empty) {
+        for (int u = blockIdx.x * kWarps + warp; u < a.B * a.Hkv; u += gridDim.x * kWarps) {
+            const int b = u / a.Hkv, h = u - b * a.Hkv;
+            const Seq s = seq_of(a, b, false);
+            if (s.np > 0) continue;
+            for (int c = 0; c < cols; c++) {
+                int row, hq, i;
+                if (!column(a, s, h, c, row, hq, i)) break;
+                write_pair<T>(a, row, hq, 4 * lane, 0.0f, 0.0f);
+                write_pair<T>(a, row, hq, 4 * lane + 2, 0.0f, 0.0f);
+                if (a.lse && lane == 0) a.lse[(int64_t)row * a.Hq + hq] = -INFINITY;
+            }
+        }
+    }
+    const int ncta = total < (int)gridDim.x ? total : (int)gridDim.x;
+    const int cta = blockIdx.x;
+    if (cta >= ncta) return;
+    const int c0 = (int)((int64_t)total * cta / ncta), c1 = (int)((int64_t)total * (cta + 1) / ncta);
+    int x = c0 + (int)((int64_t)(c1 - c0) * warp / kWarps);
+    const int xe = c0 + (int)((int64_t)(c1 - c0) * (warp + 1) / kWarps);
+
+    // ---- this warp's pages --------------------------------------------------------------------
+    uint8_t *kbuf = sh.ring[warp], *vbuf = kbuf + kRec;
+    uint64_t *kfull = &sh.full[warp][0], *vfull = &sh.full[warp][1];
+    uint32_t phase = 0, kissued = 0, vissued = 0;
+    bool dead = false;
+    if (x < xe) {
+        At at = locate(a, sh, chunk, x);
+        State<NT> st;
+        while (true) {
+            const int left = at.s.np - at.j;
+            const int cnt = left < xe - x ? left : xe - x;  // pages of this unit
+            const Seq s = at.s;
+            const int h = at.h, b = at.b, unit = b * a.Hkv + h;
+            uint32_t qf[NT][16];
+            float fs[NT][2];
+            const int j0 = s.fp + at.j, j1 = j0 + cnt;
+            const int32_t *bt = a.block_table + (int64_t)b * a.max_blocks;
+            const uint8_t *keep = a.keep_in ? a.keep_in + ((int64_t)unit) * a.max_blocks : nullptr;
+            // pages jb .. jb + 31 of the unit, one per lane (-1: dropped); the next 32 are read ahead
+            int jb = j0, page = -1, ahead = -1;
+            uint32_t todo;
+            auto look = [&](int j) {
+                int p = -1;
+                if (j < j1 && (!keep || __ldg(keep + j))) {
+                    p = __ldg(bt + j);
+                    if (p < 0 || p >= a.P) {
+                        raise_error(a.err, FFD_ERRBIT_BOUNDS);
+                        p = -1;
+                    }
+                }
+                return p;
+            };
+            page = look(jb + lane);
+            ahead = look(jb + 32 + lane);
+            todo = __ballot_sync(0xffffffffu, page >= 0);
+            // the next page to take: its index and number, -1 when there is none
+            auto pop = [&](int &pg) {
+                while (todo == 0) {
+                    jb += 32;
+                    if (jb >= j1) return -1;
+                    page = ahead;
+                    ahead = look(jb + 32 + lane);
+                    todo = __ballot_sync(0xffffffffu, page >= 0);
+                }
+                const int k = __ffs(todo) - 1;
+                todo &= todo - 1;
+                pg = __shfl_sync(0xffffffffu, page, k);
+                return jb + k;
+            };
+            auto fetch = [&](const uint8_t *from, uint8_t *to, uint64_t *bar, int pg) {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar, kRec);
+                    tma_load_1d(to, from + ((int64_t)pg * a.Hkv + h) * kRec, kRec, bar);
+                }
+            };
+            int pg = -1;
+            int j = pop(pg);
+            if (j >= 0 && !dead) {
+                fetch(a.k4, kbuf, kfull, pg);
+                fetch(a.v4, vbuf, vfull, pg);
+                kissued++, vissued++;
+            }
+            load_queries<NT, T>(a, s, h, lane, qf, fs);
+            st.clear();
+            const int low = s.n - s.nq;  // position of the first query
+            while (j >= 0 && !dead) {
+                int npg = -1;
+                const int nj = pop(npg);
+                wait_copy(a, kfull, phase, dead);
+                dead = __any_sync(0xffffffffu, dead);
+                float sc[NT][4][4];
+                page_scores<NT>(kbuf, lane, qf, sc);
+                __syncwarp();
+                const bool more = nj >= 0 && !dead;
+                if (more) {
+                    fetch(a.k4, kbuf, kfull, npg);
+                    kissued++;
+                }
+                // ---- masks, maxima, probabilities
+                const int t0 = 64 * j;
+                const bool whole =
+                    t0 + 63 <= low && (a.window == 0 || t0 > s.n - 1 - a.window);
+                uint32_t pf[NT][4][2];
+                float mx[NT][2];
+#pragma unroll
+                for (int t = 0; t < NT; t++) {
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        float top = -INFINITY;
+                        if (whole) {
+#pragma unroll
+                            for (int k = 0; k < 4; k++) {
+                                sc[t][k][e] *= fs[t][e];
+                                sc[t][k][2 + e] *= fs[t][e];
+                                top = fmaxf(top, fmaxf(sc[t][k][e], sc[t][k][2 + e]));
+                            }
+                        } else {
+                            const int pos = low + (8 * t + 2 * (lane & 3) + e) / a.G;
+                            const int from = a.window > 0 ? pos - a.window : -1;
+#pragma unroll
+                            for (int k = 0; k < 4; k++)
+#pragma unroll
+                                for (int r = 0; r < 2; r++) {
+                                    const int tok = t0 + 16 * k + 8 * r + (lane >> 2);
+                                    float &v = sc[t][k][2 * r + e];
+                                    v = tok <= pos && tok > from ? v * fs[t][e] : -INFINITY;
+                                    top = fmaxf(top, v);
+                                }
+                        }
+                        mx[t][e] = top;
+                    }
+                }
+                bool up = false;
+#pragma unroll
+                for (int t = 0; t < NT; t++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) up |= mx[t][e] > st.m[t][e];
+                if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+                    for (int t = 0; t < NT; t++)
+#pragma unroll
+                        for (int e = 0; e < 2; e++) {
+                            float top = fmaxf(mx[t][e], st.m[t][e]);
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1)
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                            const float al =
+                                top == -INFINITY ? 0.0f : ex2_approx(st.m[t][e] - top);
+                            st.m[t][e] = top;
+                            st.l[t][e] *= al;
+#pragma unroll
+                            for (int c = 0; c < 8; c++) {
+                                st.o[t][c][e] *= al;
+                                st.o[t][c][2 + e] *= al;
+                            }
+                        }
+                }
+#pragma unroll
+                for (int t = 0; t < NT; t++) {
+                    float sub[2];
+#pragma unroll
+                    for (int e = 0; e < 2; e++)
+                        sub[e] = (st.m[t][e] == -INFINITY ? 0.0f : st.m[t][e]) - kShift;
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+#pragma unroll
+                        for (int r = 0; r < 2; r++) {
+                            const float p0 = ex2_approx(sc[t][k][2 * r] - sub[0]);
+                            const float p1 = ex2_approx(sc[t][k][2 * r + 1] - sub[1]);
+                            st.l[t][0] += p0;
+                            st.l[t][1] += p1;
+                            pf[t][k][r] = movmatrix_trans(F16::pack(p0, p1));
+                        }
+                }
+                wait_copy(a, vfull, phase, dead);
+                dead = __any_sync(0xffffffffu, dead);
+                page_values<NT>(vbuf, lane, s.n - t0, pf, st);
+                __syncwarp();
+                if (more && !dead) {
+                    fetch(a.v4, vbuf, vfull, npg);
+                    vissued++;
+                }
+                phase ^= 1;
+                j = nj;
+            }
+            st.close();
+            x += cnt;
+            // ---- the unit's part is done
+            if (cnt == s.np) {
+                write_direct<NT, T>(a, s, h, lane, st);
+            } else if (x < xe) {  // more units follow: this state waits in the workspace
+                park<NT>(parked + ((int64_t)cta * kWarps + warp) * cols * kStride, lane, st);
+                if (lane == 0) sh.unit[warp][0] = unit;
+            } else {
+                __syncwarp();
+                park<NT>(reinterpret_cast<float *>(kbuf), lane, st);
+                if (lane == 0) sh.unit[warp][1] = unit;
+            }
+            if (x >= xe) break;
+            __syncwarp();
+            at.j = 0;
+            if (++at.h == a.Hkv) {
+                at.h = 0;
+                do {
+                    at.s = seq_of(a, ++at.b, false);
+                } while (at.s.np == 0);
+            }
+        }
+    }
+    if (dead) {  // leave no copy in flight
+        bool late = false;
+        if (kissued) wait_copy(a, kfull, (kissued - 1) & 1, late);
+        if (vissued) wait_copy(a, vfull, (vissued - 1) & 1, late);
+    }
+    __syncthreads();
+
+    // ---- join the warps' states of each unit, then the CTAs' ----------------------------------
+    auto state_of = [&](int i) -> const float * {  // entry i: warp i / 2, parked (0) or last (1)
+        const int w = i >> 1;
+        return (i & 1) ? reinterpret_cast<const float *>(sh.ring[w])
+                       : parked + ((int64_t)cta * kWarps + w) * cols * kStride;
+    };
+    for (int i0 = 0; i0 < 2 * kWarps;) {
+        const int u = sh.unit[i0 >> 1][i0 & 1];
+        if (u < 0) {
+            i0++;
+            continue;
+        }
+        int i1 = i0 + 1;  // entries i0 .. i1 - 1 that are not -1 belong to unit u
+        for (; i1 < 2 * kWarps; i1++) {
+            const int v = sh.unit[i1 >> 1][i1 & 1];
+            if (v >= 0 && v != u) break;
+        }
+        const int b = u / a.Hkv, h = u - b * a.Hkv;
+        const Seq s = seq_of(a, b, false);
+        int first = sh.pre[b / chunk] + h * s.np;  // the unit's first item
+        for (int q = b / chunk * chunk; q < b; q++) first += seq_of(a, q, false).np * a.Hkv;
+        const bool begins = first >= c0, complete = begins && first + s.np <= c1;
+        float *mine = records + (int64_t)(2 * cta + (begins ? 1 : 0)) * cols * kStride;
+        for (int k = tid; k < cols * 64; k += kThreads) {
+            const int c = k >> 6, ch = 2 * (k & 63);
+            float M = -INFINITY;
+            for (int i = i0; i < i1; i++)
+                if (sh.unit[i >> 1][i & 1] >= 0) M = fmaxf(M, state_of(i)[c * kStride + 128]);
+            float2 o = make_float2(0.0f, 0.0f);
+            float l = 0.0f;
+            for (int i = i0; i < i1; i++) {
+                if (sh.unit[i >> 1][i & 1] < 0) continue;
+                const float *col = state_of(i) + c * kStride;
+                const float2 ml = *reinterpret_cast<const float2 *>(col + 128);
+                const float2 v = *reinterpret_cast<const float2 *>(col + ch);
+                const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - M);
+                o.x = fmaf(f, v.x, o.x);
+                o.y = fmaf(f, v.y, o.y);
+                l = fmaf(f, ml.y, l);
+            }
+            if (complete) {
+                int row, hq, i;
+                if (!column(a, s, h, c, row, hq, i)) continue;
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                write_pair<T>(a, row, hq, ch, o.x * inv, o.y * inv);
+                if (a.lse && ch == 0) a.lse[(int64_t)row * a.Hq + hq] = lse_of(M, l);
+            } else {
+                *reinterpret_cast<float2 *>(mine + c * kStride + ch) = o;
+                if (ch == 0) *reinterpret_cast<float2 *>(mine + c * kStride + 128) = make_float2(M, l);
+            }
+        }
+        if (!complete) {
+            // CTAs first_cta .. last_cta share the unit; the last of them to come joins all
+            const int first_cta = (int)(((int64_t)(first + 1) * ncta - 1) / total);
+            const int last_cta = (int)(((int64_t)(first + s.np) * ncta - 1) / total);
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) sh.flag = atomicAdd(tickets + u, 1) == last_cta - first_cta;
+            __syncthreads();
+            if (sh.flag) {
+                __threadfence();
+                for (int k = tid; k < cols * 64; k += kThreads) {
+                    const int c = k >> 6, ch = 2 * (k & 63);
+                    int row, hq, i;
+                    if (!column(a, s, h, c, row, hq, i)) continue;
+                    const float *base0 = records + (int64_t)(2 * first_cta + 1) * cols * kStride +
+                                         c * kStride;
+                    const int64_t step = (int64_t)2 * cols * kStride;
+                    const int nrec = last_cta - first_cta + 1;
+                    // record r > 0 is the first one of its CTA: one record back
+                    auto rec = [&](int r) { return base0 + r * step - (r ? cols * kStride : 0); };
+                    float M = -INFINITY;
+#pragma unroll 8
+                    for (int r = 0; r < nrec; r++) M = fmaxf(M, __ldcg(rec(r) + 128));
+                    float2 o = make_float2(0.0f, 0.0f);
+                    float l = 0.0f;
+#pragma unroll 4
+                    for (int r = 0; r < nrec; r++) {
+                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(rec(r) + 128));
+                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(rec(r) + ch));
+                        const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - M);
+                        o.x = fmaf(f, v.x, o.x);
+                        o.y = fmaf(f, v.y, o.y);
+                        l = fmaf(f, ml.y, l);
+                    }
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                    write_pair<T>(a, row, hq, ch, o.x * inv, o.y * inv);
+                    if (a.lse && ch == 0) a.lse[(int64_t)row * a.Hq + hq] = lse_of(M, l);
+                }
+                if (tid == 0) tickets[u] = 0;  // ready for the next call
+            }
+            __syncthreads();
+        }
+        i0 = i1;
+    }
+}
+
+template <int NT, class T>
+cudaError_t launch(const AttnArgs &a, const Plan &pl, cudaStream_t stream) {
+    static int smem_set[kMaxDevicesTracked];
+    constexpr int bytes = sizeof(Shared) + 128;
+    const cudaError_t e = raise_smem_limit(kv4_decode_kernel<NT, T>, bytes, smem_set);
+    if (e != cudaSuccess) return e;
+    char *ws = reinterpret_cast<char *>(a.err);
+    kv4_decode_kernel<NT, T><<<pl.ctas, kThreads, bytes, stream>>>(
+        a, reinterpret_cast<float *>(ws + pl.parked), reinterpret_cast<float *>(ws + pl.records),
+        reinterpret_cast<int *>(ws + pl.tickets));
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t decode_record_bytes(int cols) { return (size_t)cols * kStride * sizeof(float); }
+int decode_warps() { return kWarps; }
+
+cudaError_t launch_decode(const AttnArgs &a, const Plan &pl, int dtype, cudaStream_t stream) {
+    const bool bf16 = dtype == FFD_DTYPE_BF16;
+    if (pl.cols == 8) return bf16 ? launch<1, Bf16>(a, pl, stream) : launch<1, F16>(a, pl, stream);
+    return bf16 ? launch<2, Bf16>(a, pl, stream) : launch<2, F16>(a, pl, stream);
+}
+
+}  // namespace kv4
+}  // namespace ffd
