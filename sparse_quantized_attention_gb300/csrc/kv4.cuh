@@ -10,6 +10,7 @@ namespace kv4 {
 constexpr int kRec = FFD_KV4_RECORD_BYTES;
 constexpr int kParamOff = 4096;  // (scale, off) pairs behind the codes
 static_assert(kRec == 5120, "record size");
+constexpr int kMaxCtas = 1024;  // of an attention launch (one per SM at most)
 constexpr float kMaxInput = 16384.0f;  // |off| <= |min| + 16/15 range stays inside f16
 
 // Byte offset, inside a record, of the 16 code bytes of group g (32 channels) of token r.
@@ -135,7 +136,7 @@ struct AttnArgs {
 
 // Launch shape and workspace of an attention call (byte offsets behind the error word).
 struct Plan {
-    int cols;  // query columns of the decode kernel (8 or 16), 0: rows go one by one
+    int cols;  // query columns of the decode kernel (8 or 16), 0: the chunk kernel
     int ctas;
     size_t tickets, records, parked, total;
 };

@@ -11,9 +11,11 @@ cudaError_t launch_write(const RowsArgs &a, int dtype, const void *k, const void
                          uint8_t *v4, cudaStream_t stream);
 cudaError_t launch_read(const RowsArgs &a, int dtype, const uint8_t *k4, const uint8_t *v4, void *k,
                         void *v, cudaStream_t stream);
-cudaError_t launch_rows(const AttnArgs &a, int dtype, cudaStream_t stream);
 cudaError_t launch_decode(const AttnArgs &a, const Plan &pl, int dtype, cudaStream_t stream);
+cudaError_t launch_chunk(const AttnArgs &a, const Plan &pl, int dtype, cudaStream_t stream);
 size_t decode_record_bytes(int cols);
+size_t chunk_record_bytes();
+int chunk_rows();
 int decode_warps();
 }  // namespace kv4
 }  // namespace ffd
@@ -85,42 +87,47 @@ ffd_status check_params(const ffd_kv4_params *p) {
     if (p->num_q_heads / p->num_kv_heads > kMaxG) return FFD_ERR_UNSUPPORTED;
     if ((int64_t)p->batch * p->num_kv_heads > (int64_t)kMaxUnits) return FFD_ERR_UNSUPPORTED;
     if ((int64_t)p->max_blocks_per_seq * kPage > INT32_MAX) return FFD_ERR_UNSUPPORTED;
-    // a page of a unit is named by an int32
-    if ((int64_t)p->batch * p->num_kv_heads * p->max_blocks_per_seq > INT32_MAX)
+    // a page of a unit, for each group of rows that takes it, is named by an int32
+    const int64_t pages = (int64_t)p->batch * p->num_kv_heads * p->max_blocks_per_seq;
+    const int64_t rows = (int64_t)p->max_q_len * (p->num_q_heads / p->num_kv_heads);
+    if (pages > INT32_MAX || pages > INT32_MAX / ((rows + chunk_rows() - 1) / chunk_rows()))
         return FFD_ERR_UNSUPPORTED;
     return FFD_OK;
 }
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
-// At least this many pages (upper bound from the table's width) for each CTA of the decode kernel.
-constexpr int64_t kMinPagesPerCta = 8;
+// At least this many pages (upper bound from the table's width) for each CTA.
+constexpr int64_t kMinDecodePages = 8, kMinChunkPages = 4;
 
-// Workspace: [error word | merge tickets per unit | two records per CTA | a parked state per warp].
-// The tickets, the only part that has to start at zero, have the same place and room for the most
-// units whatever the parameters, so that calls of different shapes can share a workspace.
+// Workspace: [error word | join tickets per CTA | two records per CTA | a parked state per warp of
+// the decode kernel]. The tickets, the only part that has to start at zero, have the same place and
+// size whatever the parameters, so that calls of different shapes can share a workspace.
 ffd_status make_plan(const ffd_kv4_params *p, Plan *pl) {
     const ffd_status st = check_params(p);
     if (st != FFD_OK) return st;
-    const int64_t units = (int64_t)p->batch * p->num_kv_heads;
     const int64_t rows = (int64_t)p->max_q_len * (p->num_q_heads / p->num_kv_heads);
+    pl->cols = rows <= 8 ? 8 : rows <= 16 ? 16 : 0;
     const int sms = current_sm_count();
     int64_t ctas = p->num_splits;
     if (ctas == 0) {
         if (sms <= 0) return FFD_ERR_CUDA;
-        ctas = (units * p->max_blocks_per_seq + kMinPagesPerCta - 1) / kMinPagesPerCta;
+        int64_t pages = (int64_t)p->batch * p->num_kv_heads * p->max_blocks_per_seq;
+        if (!pl->cols) pages *= (rows + chunk_rows() - 1) / chunk_rows();
+        const int64_t least = pl->cols ? kMinDecodePages : kMinChunkPages;
+        ctas = (pages + least - 1) / least;
     }
     if (sms > 0 && ctas > sms) ctas = sms;
+    if (ctas > kMaxCtas) ctas = kMaxCtas;
     pl->ctas = (int)ctas;
-    pl->cols = rows <= 8 ? 8 : rows <= 16 ? 16 : 0;
-    const size_t rec = decode_record_bytes(pl->cols);
+    const size_t rec = pl->cols ? decode_record_bytes(pl->cols) : chunk_record_bytes();
     size_t off = kAlign;
     pl->tickets = off;
-    off = align_up(off + kMaxUnits * sizeof(int));
+    off = align_up(off + kMaxCtas * sizeof(int));
     pl->records = off;
     off = align_up(off + 2 * pl->ctas * rec);
     pl->parked = off;
-    off = align_up(off + (size_t)pl->ctas * decode_warps() * rec);
+    if (pl->cols) off = align_up(off + (size_t)pl->ctas * decode_warps() * rec);
     pl->total = off;
     return FFD_OK;
 }
@@ -207,7 +214,8 @@ ffd_status ffd_kv4_attention(const ffd_kv4_params *params, const void *q, const 
     a.err = static_cast<int *>(workspace);
     a.wait_ns = p.wait_limit_us > 0 ? (uint64_t)p.wait_limit_us * 1000ull : kWaitTimeoutNs;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return cuda_status(pl.cols ? launch_decode(a, pl, p.dtype, s) : launch_rows(a, p.dtype, s));
+    return cuda_status(pl.cols ? launch_decode(a, pl, p.dtype, s)
+                               : launch_chunk(a, pl, p.dtype, s));
 }
 
 }  // extern "C"

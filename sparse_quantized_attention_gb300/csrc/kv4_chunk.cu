@@ -1,0 +1,710 @@
+// kv4_chunk.cu -- attention over the 4-bit cache for many query rows (drafted tokens, chunks of a
+// prompt) on the fifth-generation tensor cores. Definition in ffd.h.
+//
+// The query rows of a (sequence, KV head), nq tokens x G heads, are taken 256 at a time: an item is
+// one such group of rows over the pages that any of them sees. The pages of all items, concatenated,
+// are cut into equal contiguous ranges, one per CTA (one per SM), so the last CTA ends with the first
+// whatever the causal edges leave; an item cut by a range's end is joined by the last of its CTAs.
+// For each page of 64 tokens a CTA computes, for its two tiles of 128 rows,
+//   S = Q K^T   (M 128, N 64, K 128; f16, both operands in shared memory, S in tensor memory),
+//   P = 2^(S - m) in f16 against a reference m that follows the row's maximum lazily: it is raised,
+//       and O rescaled, only when a score passes it by 2^8,
+//   O += P V    (M 128, N 128, K 64; P in tensor memory, V^T in shared memory, O in tensor memory).
+// Roles: a copy warp fetches the pages' records; four warps form K and V^T tiles of f16 values from
+// them; one thread issues the matrix instructions; two groups of four warps, one row a thread, do
+// the softmax of one tile each while the tensor core works on the other's.
+//
+// K's rows, and with them the columns of S, P and V^T, are tokens in the order 8 (p % 8) + p / 8:
+// then the eight tokens that make 16 bytes of a V^T row come from eight different lanes' loads, and
+// neither side of the transposition meets a bank conflict.
+#include "kv4_walk.cuh"
+
+namespace ffd {
+namespace kv4 {
+namespace {
+
+constexpr int kTile = 128;             // rows of a tile
+constexpr int kRows = 2 * kTile;       // rows of an item
+constexpr int kThreads = 448;          // 2 x 4 softmax warps, 4 forming warps, issuer, copy warp
+constexpr int kCtaWarps = kThreads / 32;
+constexpr int kNK = 3, kNV = 3;        // f16 tiles of K and of V^T
+constexpr int kNS = 5;                 // record pairs in flight
+constexpr int kInfo = 16;              // steps whose page index is kept
+constexpr int kStride = 130;           // floats of a joined row: o[128], m, l
+constexpr float kShift = 7.0f;         // P carries 2^7: with the lazy reference at most 2^15
+constexpr float kLazy = 8.0f;
+constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;  // tensor memory columns, two tiles each
+constexpr uint32_t kIdescS = tc_idesc_f16(128, 64), kIdescO = tc_idesc_f16(128, 128);
+
+struct Shared {
+    uint8_t q[2][2 * 16384];           // tile: channels 0-63, then 64-127
+    uint8_t k[kNK][2 * 8192];          // the same for 64 rows
+    uint8_t v[kNV][16384];             // V^T: 128 channels x 64 tokens
+    uint8_t rec[kNS][2 * kRec];        // K record, V record
+    uint64_t rec_full[kNS], rec_free[kNS];
+    uint64_t k_full[kNK], k_free[kNK], v_full[kNV], v_free[kNV];
+    uint64_t s_full[2], p_full[2], drain;
+    uint32_t tmem, aborted;
+    int info[kInfo];                   // page index of a step, -1: the segment's end
+    int scan[kCtaWarps];
+    int flag;
+    int pre[kThreads];                 // pages of all items before each thread's chunk of sequences
+};
+static_assert(sizeof(Shared) + 1024 <= 232448, "shared memory per CTA");
+
+// Pages that the rows of item group rt of a sequence see: the first, and how many.
+__device__ __forceinline__ void item_pages(const AttnArgs &a, const Seq &s, int rt, int &fp,
+                                           int &np) {
+    const int64_t rows = (int64_t)s.nq * a.G;
+    const int64_t r1 = (int64_t)(rt + 1) * kRows < rows ? (int64_t)(rt + 1) * kRows : rows;
+    const int lo = s.n - s.nq + (int)((int64_t)rt * kRows / a.G);
+    const int hi = s.n - s.nq + (int)((r1 - 1) / a.G);
+    int64_t first = a.window > 0 ? (int64_t)lo - a.window + 1 : 0;
+    if (first < 0) first = 0;
+    fp = (int)(first >> 6);
+    np = hi < 0 ? 0 : (hi >> 6) - fp + 1;
+}
+
+__device__ __forceinline__ int item_groups(const AttnArgs &a, const Seq &s) {
+    return (int)(((int64_t)s.nq * a.G + kRows - 1) / kRows);
+}
+
+// Pages of one head's items of a sequence.
+__device__ __forceinline__ int head_pages(const AttnArgs &a, const Seq &s) {
+    int sum = 0;
+    for (int rt = 0; rt < item_groups(a, s); rt++) {
+        int fp, np;
+        item_pages(a, s, rt, fp, np);
+        sum += np;
+    }
+    return sum;
+}
+
+// Bounded waits: once one runs out the CTA stops (aborted) and drains what is in flight.
+__device__ __forceinline__ bool stopped(const Shared &sh) {
+    return *reinterpret_cast<const volatile uint32_t *>(&sh.aborted) != 0;
+}
+__device__ __forceinline__ void wait(const AttnArgs &a, Shared &sh, uint64_t *bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (stopped(sh)) return;
+        if (globaltimer_ns() - t0 > a.wait_ns) {
+            raise_error(a.err, FFD_ERRBIT_TIMEOUT);
+            *reinterpret_cast<volatile uint32_t *>(&sh.aborted) = 1;
+            return;
+        }
+    }
+}
+// The same for what this CTA has in flight, whether or not it has stopped.
+__device__ __forceinline__ void drain(const AttnArgs &a, uint64_t *bar, uint32_t parity) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer_ns() - t0 > a.wait_ns) {
+            raise_error(a.err, FFD_ERRBIT_TIMEOUT);
+            return;
+        }
+}
+
+// ---- forming the tiles --------------------------------------------------------------------------
+// K: thread t takes word t % 16 of tokens t / 16, t / 16 + 8, ...; row p = 8 (token % 8) + token / 8.
+__device__ __forceinline__ void form_k(const uint8_t *rec, uint8_t *tile, int t) {
+    const int J = t & 15, r0 = t >> 4;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const int r = r0 + 8 * i;
+        const uint32_t w =
+            *reinterpret_cast<const uint32_t *>(rec + code_offset(r, J >> 2) + 4 * (J & 3));
+        const __half2 p = *reinterpret_cast<const __half2 *>(rec + param_offset(r, J >> 2));
+        __half2 v[4];
+        decode_word(w, p, v);
+        const int row = 8 * r0 + i;  // r = 8 i + r0
+        *reinterpret_cast<uint4 *>(tile + (J >> 3) * 8192 + row * 128 + (((J & 7) ^ (row & 7)) << 4)) =
+            *reinterpret_cast<const uint4 *>(v);
+    }
+}
+
+// V^T: thread t takes word J = 4 (t / 32) + t % 32 / 8 of the tokens i * 8 + tg (i < 8), tg = t % 8,
+// which are positions 8 tg .. 8 tg + 7: 16 bytes of each of the word's eight channel rows. Tokens
+// from `valid` on hold anything and count as 0.
+__device__ __forceinline__ void form_v(const uint8_t *rec, uint8_t *tile, int t, int valid) {
+    const int tg = t & 7, J = 4 * (t >> 5) + ((t >> 3) & 3);
+    uint32_t out[8][4];  // [channel of the word][token pair]
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int r = 16 * i + tg;  // tokens r and r + 8: positions 8 tg + 2 i, + 1
+        const uint32_t w0 =
+            *reinterpret_cast<const uint32_t *>(rec + code_offset(r, J >> 2) + 4 * (J & 3));
+        const uint32_t w1 =
+            *reinterpret_cast<const uint32_t *>(rec + code_offset(r + 8, J >> 2) + 4 * (J & 3));
+        uint32_t p0 = *reinterpret_cast<const uint32_t *>(rec + param_offset(r, J >> 2));
+        uint32_t p1 = *reinterpret_cast<const uint32_t *>(rec + param_offset(r + 8, J >> 2));
+        if (valid < kPage) {
+            p0 = r < valid ? p0 : 0u;
+            p1 = r + 8 < valid ? p1 : 0u;
+        }
+        const uint32_t sw = __byte_perm(p0, p1, 0x5410), ow = __byte_perm(p0, p1, 0x7632);
+        const __half2 s = *reinterpret_cast<const __half2 *>(&sw);
+        const __half2 o = *reinterpret_cast<const __half2 *>(&ow);
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            const uint32_t w = __byte_perm(w0, w1, e ? 0x7632 : 0x5410);
+            const __half2 v[4] = {__hfma2(code_pair<0>(w), s, o), __hfma2(code_pair<1>(w), s, o),
+                                  __hfma2(code_pair<2>(w), s, o), __hfma2(code_pair<3>(w), s, o)};
+#pragma unroll
+            for (int c = 0; c < 4; c++)
+                out[2 * c + e][i] = *reinterpret_cast<const uint32_t *>(&v[c]);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 8; c++)
+        *reinterpret_cast<uint4 *>(tile + (8 * J + c) * 128 + ((tg ^ c) << 4)) =
+            make_uint4(out[c][0], out[c][1], out[c][2], out[c][3]);
+}
+
+// A row of q into its tile as scaled f16; returns the factor of its scores.
+template <class T>
+__device__ __forceinline__ float load_query(const AttnArgs &a, uint8_t *tile, int r, bool have,
+                                            int row, int hq) {
+    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) +
+                                                       (int64_t)row * a.q_stride + hq * kD);
+    float top = 0.0f;
+    if (have) {
+#pragma unroll 4
+        for (int j = 0; j < 16; j++) {
+            const uint4 u = __ldg(src + j);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const float2 f = T::unpack(w[k]);
+                top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+        }
+    }
+    float mul, f;
+    query_scale(a, top, mul, f);
+#pragma unroll 4
+    for (int j = 0; j < 16; j++) {
+        uint4 o = make_uint4(0, 0, 0, 0);
+        if (have) {
+            const uint4 u = __ldg(src + j);
+            const float2 x0 = T::unpack(u.x), x1 = T::unpack(u.y), x2 = T::unpack(u.z),
+                         x3 = T::unpack(u.w);
+            o = make_uint4(F16::pack(x0.x * mul, x0.y * mul), F16::pack(x1.x * mul, x1.y * mul),
+                           F16::pack(x2.x * mul, x2.y * mul), F16::pack(x3.x * mul, x3.y * mul));
+        }
+        *reinterpret_cast<uint4 *>(tile + (j >> 3) * 16384 + r * 128 + (((j & 7) ^ (r & 7)) << 4)) = o;
+    }
+    return f;
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a, float *records,
+                                                                int *tickets) {
+    extern __shared__ uint8_t raw[];
+    Shared &sh = *reinterpret_cast<Shared *>(align_shared<1024>(raw));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    // ---- pages before each chunk of sequences -------------------------------------------------
+    const int chunk = (a.B + kThreads - 1) / kThreads;
+    int own = 0;
+    bool empty = false;
+    for (int b = tid * chunk; b < (tid + 1) * chunk && b < a.B; b++) {
+        const Seq s = seq_of(a, b, blockIdx.x == 0);
+        own += head_pages(a, s) * a.Hkv;
+        empty |= s.n < s.nq;  // some rows see nothing: perhaps whole items
+    }
+    int inc = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) sh.scan[warp] = inc;
+    if (tid == 0) {
+        sh.aborted = 0;
+        for (int i = 0; i < kNS; i++) {
+            mbar_init(&sh.rec_full[i], 1);
+            mbar_init(&sh.rec_free[i], 4);
+        }
+        for (int i = 0; i < kNK; i++) {
+            mbar_init(&sh.k_full[i], 4);
+            mbar_init(&sh.k_free[i], 1);
+        }
+        for (int i = 0; i < kNV; i++) {
+            mbar_init(&sh.v_full[i], 4);
+            mbar_init(&sh.v_free[i], 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.p_full[i], 4);
+        }
+        mbar_init(&sh.drain, 1);
+        fence_barrier_init();
+    }
+    const bool any_empty = __syncthreads_or(empty);
+    int base = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kCtaWarps; w++) {
+        const int v = sh.scan[w];
+        base += w < warp ? v : 0;
+        total += v;
+    }
+    sh.pre[tid] = base + inc - own;
+    if (any_empty) {  // items that see nothing at all
+        for (int u = blockIdx.x; u < a.B * a.Hkv; u += gridDim.x) {
+            const int b = u / a.Hkv, h = u - b * a.Hkv;
+            const Seq s = seq_of(a, b, false);
+            for (int rt = 0; rt < item_groups(a, s); rt++) {
+                int fp, np;
+                item_pages(a, s, rt, fp, np);
+                if (np > 0) break;  // later items see more
+                for (int k = tid; k < kRows * 64; k += kThreads) {
+                    const int64_t r = (int64_t)rt * kRows + (k >> 6);
+                    const int i = (int)(r / a.G), hq = h * a.G + (int)(r - (int64_t)i * a.G);
+                    if (i >= s.nq) break;
+                    write_pair<T>(a, s.t0 + i, hq, 2 * (k & 63), 0.0f, 0.0f);
+                    if (a.lse && (k & 63) == 0) a.lse[(int64_t)(s.t0 + i) * a.Hq + hq] = -INFINITY;
+                }
+            }
+        }
+    }
+    const int ncta = total < (int)gridDim.x ? total : (int)gridDim.x;
+    const int cta = blockIdx.x;
+    if (cta >= ncta) return;
+    if (warp == 0) tmem_alloc(&sh.tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    const int c0 = (int)((int64_t)total * cta / ncta), c1 = (int)((int64_t)total * (cta + 1) / ncta);
+
+    // ---- where the range begins: sequence b, head h, group rt, page `at` of the item's ----------
+    int b, h, rt = 0, at;
+    Seq s;
+    {
+        int lo = 0, hi = kThreads;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (sh.pre[mid] <= c0) lo = mid;
+            else hi = mid;
+        }
+        int rem = c0 - sh.pre[lo], hp = 0;
+        for (b = lo * chunk; b < a.B; b++) {
+            s = seq_of(a, b, false);
+            hp = head_pages(a, s);
+            if (rem < hp * a.Hkv) break;
+            rem -= hp * a.Hkv;
+        }
+        h = rem / hp;
+        rem -= h * hp;
+        for (;; rt++) {
+            int fp, np;
+            item_pages(a, s, rt, fp, np);
+            if (rem < np) break;
+            rem -= np;
+        }
+        at = rem;
+    }
+
+    // steps of the whole kernel so far, per role
+    uint32_t steps = 0, vsteps = 0, turns = 0;
+    for (int x = c0; x < c1;) {
+        int fp, np;
+        item_pages(a, s, rt, fp, np);
+        const int cnt = np - at < c1 - x ? np - at : c1 - x;
+        const int j0 = fp + at, j1 = j0 + cnt;
+        const int64_t rows = (int64_t)s.nq * a.G - (int64_t)rt * kRows;  // of this item and later
+        const bool two = rows > kTile;
+        const bool begins = at == 0, complete = begins && cnt == np;
+        const int first = x - at;  // the item's first page among all
+
+        // ---- queries
+        const int grp = warp >> 2;  // 0, 1: softmax group
+        const int r = tid & (kTile - 1);
+        const int64_t rr = (int64_t)rt * kRows + grp * kTile + r;
+        const int qi = (int)(rr / a.G), hq = h * a.G + (int)(rr - (int64_t)qi * a.G);
+        const bool have = grp < 2 && qi < s.nq;
+        float fs = 0.0f;
+        if (grp < 2 && !stopped(sh)) {
+            fs = load_query<T>(a, sh.q[grp], r, have, have ? s.t0 + qi : 0, have ? hq : 0);
+            fence_proxy_async();
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        bool run = !stopped(sh);
+        __syncthreads();  // nobody stops between the reading of it and this
+
+        float m = -INFINITY, l = 0.0f;
+        bool any = false;
+        if (run && grp < 2) {
+            // ================= softmax of tile grp, one row a thread =================
+            const bool active = grp == 0 || two;
+            const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+            const uint32_t ts = tmem + lanes + kColS + grp * 64, tp = tmem + lanes + kColP + grp * 32,
+                           to = tmem + lanes + kColO + grp * 128;
+            const int pos = s.n - s.nq + qi;
+            const int from = a.window > 0 ? pos - a.window : -1;
+            // positions of the tile's first and last row
+            const int lo = s.n - s.nq + (int)(((int64_t)rt * kRows + grp * kTile) / a.G);
+            const int hi = s.n - 1 < lo + (kTile - 1) / a.G + 1 ? s.n - 1 : lo + (kTile - 1) / a.G + 1;
+            while (true) {
+                wait(a, sh, &sh.s_full[grp], turns & 1);
+                turns++;
+                if (__any_sync(0xffffffffu, stopped(sh))) break;
+                tc_fence_after();
+                const int j = *reinterpret_cast<volatile int *>(&sh.info[steps % kInfo]);
+                steps++;
+                if (j < 0) break;
+                if (active) {
+                    uint32_t x0[32], x1[32];
+                    __syncwarp();
+                    tmem_load32(x0, ts);
+                    tmem_load32(x1, ts + 32);
+                    tc_wait_load();
+                    const int t0 = 64 * j;
+                    if (!(t0 + 63 <= lo && (a.window == 0 || t0 > hi - a.window))) {
+#pragma unroll
+                        for (int c = 0; c < 32; c++) {
+                            const int k0 = t0 + 8 * (c & 7) + (c >> 3);
+                            if (k0 > pos || k0 <= from) x0[c] = 0xff800000u;
+                            if (k0 + 4 > pos || k0 + 4 <= from) x1[c] = 0xff800000u;
+                        }
+                    }
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 32; c++)
+                        top = fmaxf(top, fmaxf(__uint_as_float(x0[c]), __uint_as_float(x1[c])));
+                    top *= fs;
+                    const bool raise = top > m + kLazy || (m == -INFINITY && top > m);
+                    if (__any_sync(0xffffffffu, raise)) {
+                        const float mn = raise ? top : m;
+                        const float al = m == -INFINITY ? 0.0f : ex2_approx(m - mn);
+                        m = mn;
+                        l *= al;
+                        if (any) {
+#pragma unroll 1
+                            for (int c = 0; c < 4; c++) {
+                                uint32_t o[32];
+                                tmem_load32(o, to + 32 * c);
+                                tc_wait_load();
+#pragma unroll
+                                for (int e = 0; e < 32; e++)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                                tmem_store32(to + 32 * c, o);
+                            }
+                            tc_wait_store();
+                        }
+                    }
+                    const float sub = kShift - (m == -INFINITY ? 0.0f : m);
+                    float l0 = 0.0f, l1 = 0.0f;
+                    uint32_t p[32];
+#pragma unroll
+                    for (int c = 0; c < 16; c++) {
+                        const float p0 = ex2_approx(fmaf(__uint_as_float(x0[2 * c]), fs, sub));
+                        const float p1 = ex2_approx(fmaf(__uint_as_float(x0[2 * c + 1]), fs, sub));
+                        const float p2 = ex2_approx(fmaf(__uint_as_float(x1[2 * c]), fs, sub));
+                        const float p3 = ex2_approx(fmaf(__uint_as_float(x1[2 * c + 1]), fs, sub));
+                        l0 += p0 + p1;
+                        l1 += p2 + p3;
+                        p[c] = F16::pack(p0, p1);
+                        p[16 + c] = F16::pack(p2, p3);
+                    }
+                    l += l0 + l1;
+                    __syncwarp();
+                    tmem_store32(tp, p);
+                    tc_wait_store();
+                    any = true;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_full[grp]);
+            }
+        } else if (run && grp == 2) {
+            // ================= tiles of f16 values from the records =================
+            const int t = tid - 2 * kTile;
+            while (true) {
+                const uint32_t slot = steps % kNS, ks = steps % kNK, vs = vsteps % kNV;
+                wait(a, sh, &sh.rec_full[slot], (steps / kNS) & 1);
+                if (steps >= kNK) wait(a, sh, &sh.k_free[ks], (steps / kNK - 1) & 1);
+                if (__any_sync(0xffffffffu, stopped(sh))) break;
+                const int j = *reinterpret_cast<volatile int *>(&sh.info[steps % kInfo]);
+                steps++;
+                if (j < 0) {
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&sh.rec_free[slot]);
+                        mbar_arrive(&sh.k_full[ks]);
+                    }
+                    break;
+                }
+                form_k(sh.rec[slot], sh.k[ks], t);
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.k_full[ks]);
+                if (vsteps >= kNV) wait(a, sh, &sh.v_free[vs], (vsteps / kNV - 1) & 1);
+                if (__any_sync(0xffffffffu, stopped(sh))) break;
+                vsteps++;
+                form_v(sh.rec[slot] + kRec, sh.v[vs], t, s.n - 64 * j);
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sh.v_full[vs]);
+                    mbar_arrive(&sh.rec_free[slot]);
+                }
+            }
+        } else if (run && warp == 12) {
+            // ================= matrix instructions, one thread =================
+            if (lane == 0) {
+                auto scores = [&](int g, uint32_t ks) {
+                    const uint64_t qd = tc_desc(smem_u32(sh.q[g])), kd = tc_desc(smem_u32(sh.k[ks]));
+#pragma unroll
+                    for (int i = 0; i < 8; i++)  // 16 channels each
+                        tc_mma(tmem + kColS + g * 64, qd + (i >> 2) * 1024 + (i & 3) * 2,
+                               kd + (i >> 2) * 512 + (i & 3) * 2, kIdescS, i > 0);
+                };
+                auto values = [&](int g, uint32_t vs, bool add) {
+                    const uint64_t vd = tc_desc(smem_u32(sh.v[vs]));
+#pragma unroll
+                    for (int i = 0; i < 4; i++)  // 16 tokens each
+                        tc_mma_ta(tmem + kColO + g * 128, tmem + kColP + g * 32 + 8 * i, vd + 2 * i,
+                                  kIdescO, add || i > 0);
+                };
+                // the next step's page, once its K tile stands (-1: the end)
+                auto take = [&]() {
+                    wait(a, sh, &sh.k_full[steps % kNK], (steps / kNK) & 1);
+                    tc_fence_after();
+                    const int j = *reinterpret_cast<volatile int *>(&sh.info[steps % kInfo]);
+                    return stopped(sh) ? -1 : j;
+                };
+                int j = take();
+                if (j >= 0) scores(0, steps % kNK);
+                tc_commit(&sh.s_full[0]);
+                if (j >= 0 && two) scores(1, steps % kNK);
+                tc_commit(&sh.s_full[1]);
+                tc_commit(&sh.k_free[steps % kNK]);
+                steps++;
+                bool add = false;
+                while (j >= 0 && !stopped(sh)) {
+                    const uint32_t vs = vsteps % kNV;
+                    wait(a, sh, &sh.v_full[vs], (vsteps / kNV) & 1);
+                    wait(a, sh, &sh.p_full[0], turns & 1);
+                    if (stopped(sh)) break;
+                    tc_fence_after();
+                    values(0, vs, add);
+                    j = take();
+                    if (stopped(sh)) break;
+                    if (j >= 0) scores(0, steps % kNK);
+                    tc_commit(&sh.s_full[0]);
+                    wait(a, sh, &sh.p_full[1], turns & 1);
+                    if (stopped(sh)) break;
+                    tc_fence_after();
+                    if (two) {
+                        values(1, vs, add);
+                        if (j >= 0) scores(1, steps % kNK);
+                    }
+                    tc_commit(&sh.s_full[1]);
+                    tc_commit(&sh.v_free[vs]);
+                    tc_commit(&sh.k_free[steps % kNK]);
+                    steps++;
+                    vsteps++;
+                    turns++;
+                    add = true;
+                }
+            }
+            __syncwarp();
+        } else if (run && warp == 13) {
+            // ================= copies of the pages' records =================
+            const int32_t *bt = a.block_table + (int64_t)b * a.max_blocks;
+            const uint8_t *keep =
+                a.keep_in ? a.keep_in + ((int64_t)b * a.Hkv + h) * a.max_blocks : nullptr;
+            auto look = [&](int j) {
+                int p = -1;
+                if (j < j1 && (!keep || __ldg(keep + j))) {
+                    p = __ldg(bt + j);
+                    if (p < 0 || p >= a.P) {
+                        raise_error(a.err, FFD_ERRBIT_BOUNDS);
+                        p = -1;
+                    }
+                }
+                return p;
+            };
+            auto push = [&](int j, int page) {
+                const uint32_t slot = steps % kNS;
+                if (steps >= kNS) wait(a, sh, &sh.rec_free[slot], (steps / kNS - 1) & 1);
+                if (__any_sync(0xffffffffu, stopped(sh))) return false;
+                if (lane == 0) {
+                    *reinterpret_cast<volatile int *>(&sh.info[steps % kInfo]) = j;
+                    if (j >= 0) {
+                        const int64_t from = ((int64_t)page * a.Hkv + h) * kRec;
+                        mbar_arrive_expect_tx(&sh.rec_full[slot], 2 * kRec);
+                        tma_load_1d(sh.rec[slot], a.k4 + from, kRec, &sh.rec_full[slot]);
+                        tma_load_1d(sh.rec[slot] + kRec, a.v4 + from, kRec, &sh.rec_full[slot]);
+                    } else {
+                        mbar_arrive(&sh.rec_full[slot]);
+                    }
+                }
+                steps++;
+                return true;
+            };
+            int ahead = look(j0 + lane);
+            bool fine = true;
+            for (int jb = j0; jb < j1 && fine; jb += 32) {
+                const int page = ahead;
+                ahead = look(jb + 32 + lane);
+                for (uint32_t todo = __ballot_sync(0xffffffffu, page >= 0); todo && fine;
+                     todo &= todo - 1) {
+                    const int k = __ffs(todo) - 1;
+                    fine = push(jb + k, __shfl_sync(0xffffffffu, page, k));
+                }
+            }
+            if (fine) push(-1, -1);
+        }
+
+        // ---- the segment's results
+        float *mine = records + (int64_t)(2 * cta + (begins ? 1 : 0)) * kRows * kStride;
+        if (grp < 2 && run && (grp == 0 || two)) {
+            const uint32_t to = tmem + ((uint32_t)(warp & 3) << 21) + kColO + grp * 128;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            float *row = mine + (int64_t)(grp * kTile + r) * kStride;
+#pragma unroll 1
+            for (int c = 0; c < 4; c++) {
+                uint32_t o[32];
+                __syncwarp();
+                if (any) {  // warp-uniform
+                    tmem_load32(o, to + 32 * c);
+                    tc_wait_load();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e++) o[e] = 0;
+                }
+                if (have && complete) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(
+                        static_cast<uint16_t *>(a.out) +
+                        ((int64_t)(s.t0 + qi) * a.Hq + hq) * kD + 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; k++)
+                            w[k] = T::pack(__uint_as_float(o[8 * e + 2 * k]) * inv,
+                                           __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+                        dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else if (have) {
+#pragma unroll
+                    for (int e = 0; e < 16; e++)
+                        *reinterpret_cast<float2 *>(row + 32 * c + 2 * e) = make_float2(
+                            __uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+                }
+            }
+            if (have) {
+                if (!complete) *reinterpret_cast<float2 *>(row + 128) = make_float2(m, l);
+                else if (a.lse) a.lse[(int64_t)(s.t0 + qi) * a.Hq + hq] = lse_of(m - kShift, l);
+            }
+        }
+        if (!complete) {
+            // CTAs first_cta .. last_cta share the item; the last of them to come joins their records
+            const int first_cta = (int)(((int64_t)(first + 1) * ncta - 1) / total);
+            const int last_cta = (int)(((int64_t)(first + np) * ncta - 1) / total);
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) sh.flag = atomicAdd(tickets + first_cta, 1) == last_cta - first_cta;
+            __syncthreads();
+            if (sh.flag) {
+                __threadfence();
+                const int used = rows < kRows ? (int)rows : kRows;
+                const int64_t step = (int64_t)2 * kRows * kStride;
+                const float *rec0 = records + (int64_t)(2 * first_cta + 1) * kRows * kStride;
+                const int nrec = last_cta - first_cta + 1;
+                for (int k = tid; k < used * 64; k += kThreads) {
+                    const int q = k >> 6, ch = 2 * (k & 63);
+                    auto rec = [&](int n) {  // record n > 0 is the first one of its CTA
+                        return rec0 + n * step - (n ? (int64_t)kRows * kStride : 0) +
+                               (int64_t)q * kStride;
+                    };
+                    float M = -INFINITY;
+#pragma unroll 4
+                    for (int n = 0; n < nrec; n++) M = fmaxf(M, __ldcg(rec(n) + 128));
+                    float2 o = make_float2(0.0f, 0.0f);
+                    float ls = 0.0f;
+#pragma unroll 4
+                    for (int n = 0; n < nrec; n++) {
+                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(rec(n) + 128));
+                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(rec(n) + ch));
+                        const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - M);
+                        o.x = fmaf(f, v.x, o.x);
+                        o.y = fmaf(f, v.y, o.y);
+                        ls = fmaf(f, ml.y, ls);
+                    }
+                    const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+                    const int64_t g = (int64_t)rt * kRows + q;
+                    const int i = (int)(g / a.G), head = h * a.G + (int)(g - (int64_t)i * a.G);
+                    write_pair<T>(a, s.t0 + i, head, ch, o.x * inv, o.y * inv);
+                    if (a.lse && ch == 0)
+                        a.lse[(int64_t)(s.t0 + i) * a.Hq + head] = lse_of(M - kShift, ls);
+                }
+                if (tid == 0) tickets[first_cta] = 0;  // ready for the next call
+            }
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+
+        // ---- the next item
+        x += cnt;
+        at = 0;
+        if (x < c1) {
+            do {
+                if (++rt >= item_groups(a, s)) {
+                    rt = 0;
+                    if (++h == a.Hkv) {
+                        h = 0;
+                        do {
+                            s = seq_of(a, ++b, false);
+                        } while (s.nq == 0 || s.n == 0);
+                    }
+                }
+                item_pages(a, s, rt, fp, np);
+            } while (np == 0);
+        }
+    }
+    if (stopped(sh)) {  // leave nothing in flight
+        if (warp == 13 && lane == 0)
+            for (uint32_t i = 0; i < kNS && i < steps; i++) {
+                const uint32_t last = steps - 1 - i;
+                drain(a, &sh.rec_full[last % kNS], (last / kNS) & 1);
+            }
+        if (warp == 12 && lane == 0) {
+            tc_commit(&sh.drain);
+            drain(a, &sh.drain, 0);
+        }
+    }
+    __syncthreads();
+    if (warp == 0) tmem_free(tmem, 512);
+}
+
+template <class T>
+cudaError_t launch(const AttnArgs &a, const Plan &pl, cudaStream_t stream) {
+    static int smem_set[kMaxDevicesTracked];
+    constexpr int bytes = sizeof(Shared) + 1024;
+    const cudaError_t e = raise_smem_limit(kv4_chunk_kernel<T>, bytes, smem_set);
+    if (e != cudaSuccess) return e;
+    char *ws = reinterpret_cast<char *>(a.err);
+    kv4_chunk_kernel<T><<<pl.ctas, kThreads, bytes, stream>>>(
+        a, reinterpret_cast<float *>(ws + pl.records), reinterpret_cast<int *>(ws + pl.tickets));
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int chunk_rows() { return kRows; }
+size_t chunk_record_bytes() { return (size_t)kRows * kStride * sizeof(float); }
+
+cudaError_t launch_chunk(const AttnArgs &a, const Plan &pl, int dtype, cudaStream_t stream) {
+    return dtype == FFD_DTYPE_BF16 ? launch<Bf16>(a, pl, stream) : launch<F16>(a, pl, stream);
+}
+
+}  // namespace kv4
+}  // namespace ffd

@@ -17,8 +17,7 @@
 // P is rounded to f16 against a reference of 2^14, so probabilities down to 2^-28 of the largest
 // keep all 11 bits. q enters as f16 scaled by a power of two per column (its largest magnitude in
 // [2^13, 2^14)): exact for bf16 and f16 queries apart from elements below 2^-27 of the largest.
-#include "kv4.cuh"
-#include "ptx.cuh"
+#include "kv4_walk.cuh"
 
 namespace ffd {
 namespace kv4 {
@@ -29,8 +28,6 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kSlot = 2 * kRec;       // a warp's K record and V record
 constexpr int kStride = 130;          // floats of a joined column: o[128], m, l
 constexpr float kShift = 14.0f;       // P carries 2^14
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 struct Shared {
     uint8_t ring[kWarps][kSlot];      // later each warp's last state
@@ -41,40 +38,6 @@ struct Shared {
     int flag;
 };
 static_assert(sizeof(Shared) + 128 <= 232448, "shared memory per CTA");
-
-// One sequence as the walk sees it.
-struct Seq {
-    int n, t0, nq;  // tokens, first query row, query rows
-    int fp, np;     // first page any query sees, pages from there to the last
-};
-
-__device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, bool report) {
-    Seq s;
-    s.n = __ldg(a.seq_lens + b);
-    const int cap = a.max_blocks * kPage;
-    bool bad = s.n < 0 || s.n > cap;
-    s.n = s.n < 0 ? 0 : (s.n > cap ? cap : s.n);
-    s.t0 = b * a.max_q;
-    s.nq = a.max_q;
-    if (a.cu_q) {
-        s.t0 = __ldg(a.cu_q + b);
-        const int end = __ldg(a.cu_q + b + 1);
-        if (s.t0 < 0 || end < s.t0 || end > a.total_q || end - s.t0 > a.max_q) {
-            bad = true;
-            s.nq = 0;
-        } else {
-            s.nq = end - s.t0;
-        }
-    }
-    if (report && bad) raise_error(a.err, FFD_ERRBIT_BOUNDS);
-    s.fp = 0;
-    if (a.window > 0) {
-        const int64_t first = (int64_t)s.n - s.nq - a.window + 1;
-        s.fp = first > 0 ? (int)(first >> 6) : 0;
-    }
-    s.np = s.n > 0 && s.nq > 0 ? ((s.n + kPage - 1) >> 6) - s.fp : 0;
-    return s;
-}
 
 // Where an item lies: unit (b, h), page j of the unit's np.
 struct At {
@@ -168,10 +131,8 @@ __device__ __forceinline__ void load_queries(const AttnArgs &a, const Seq &s, in
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        int e = (int)(__float_as_uint(top) >> 23) - 127;
-        e = e < -100 ? -100 : (e > 127 ? 127 : e);
-        const float mul = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
-        const float f = a.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 + e - 13) << 23);
+        float mul, f;
+        query_scale(a, top, mul, f);
 #pragma unroll
         for (int j = 0; j < 16; j++) {
             const float2 v = T::unpack(w[j]);
@@ -282,18 +243,6 @@ __device__ __forceinline__ void page_values(const uint8_t *v, int lane, int vali
     }
 }
 
-// Final value of a column: rows of out and lse.
-template <class T>
-__device__ __forceinline__ void write_pair(const AttnArgs &a, int row, int hq, int ch, float x,
-                                           float y) {
-    *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) +
-                                  ((int64_t)row * a.Hq + hq) * kD + ch) = T::pack(x, y);
-}
-
-__device__ __forceinline__ float lse_of(float m, float l) {
-    return l > 0.0f ? (m + log2f(l) - kShift) * kLn2 : -INFINITY;
-}
-
 // A unit that one warp walked whole: its rows, straight from the registers.
 template <int NT, class T>
 __device__ __forceinline__ void write_direct(const AttnArgs &a, const Seq &s, int h, int lane,
@@ -316,7 +265,7 @@ __device__ __forceinline__ void write_direct(const AttnArgs &a, const Seq &s, in
                                                    ((int64_t)row * a.Hq + hq) * kD + 16 * g);
             dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
             dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-            if (a.lse && g == 0) a.lse[(int64_t)row * a.Hq + hq] = lse_of(st.m[t][e], l);
+            if (a.lse && g == 0) a.lse[(int64_t)row * a.Hq + hq] = lse_of(st.m[t][e] - kShift, l);
         }
 }
 
@@ -660,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const AttnArgs 
                 if (!column(a, s, h, c, row, hq, i)) continue;
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                 write_pair<T>(a, row, hq, ch, o.x * inv, o.y * inv);
-                if (a.lse && ch == 0) a.lse[(int64_t)row * a.Hq + hq] = lse_of(M, l);
+                if (a.lse && ch == 0) a.lse[(int64_t)row * a.Hq + hq] = lse_of(M - kShift, l);
             } else {
                 *reinterpret_cast<float2 *>(mine + c * kStride + ch) = o;
                 if (ch == 0) *reinterpret_cast<float2 *>(mine + c * kStride + 128) = make_float2(M, l);
@@ -672,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const AttnArgs 
             const int last_cta = (int)(((int64_t)(first + s.np) * ncta - 1) / total);
             __threadfence();
             __syncthreads();
-            if (tid == 0) sh.flag = atomicAdd(tickets + u, 1) == last_cta - first_cta;
+            if (tid == 0) sh.flag = atomicAdd(tickets + first_cta, 1) == last_cta - first_cta;
             __syncthreads();
             if (sh.flag) {
                 __threadfence();
@@ -702,9 +651,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const AttnArgs 
                     }
                     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                     write_pair<T>(a, row, hq, ch, o.x * inv, o.y * inv);
-                    if (a.lse && ch == 0) a.lse[(int64_t)row * a.Hq + hq] = lse_of(M, l);
+                    if (a.lse && ch == 0) a.lse[(int64_t)row * a.Hq + hq] = lse_of(M - kShift, l);
                 }
-                if (tid == 0) tickets[u] = 0;  // ready for the next call
+                if (tid == 0) tickets[first_cta] = 0;  // ready for the next call
             }
             __syncthreads();
         }

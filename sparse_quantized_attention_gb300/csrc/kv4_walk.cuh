@@ -1,0 +1,72 @@
+// kv4_walk.cuh -- what the attention kernels over the 4-bit cache share: the sequences as a walk over
+// their pages sees them, query scaling, and the forms that results are written in.
+#pragma once
+
+#include "kv4.cuh"
+#include "ptx.cuh"
+
+namespace ffd {
+namespace kv4 {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// One sequence as the walk sees it.
+struct Seq {
+    int n, t0, nq;  // tokens, first query row, query rows
+    int fp, np;     // first page any query sees, pages from there to the last
+};
+
+__device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, bool report) {
+    Seq s;
+    s.n = __ldg(a.seq_lens + b);
+    const int cap = a.max_blocks * kPage;
+    bool bad = s.n < 0 || s.n > cap;
+    s.n = s.n < 0 ? 0 : (s.n > cap ? cap : s.n);
+    s.t0 = b * a.max_q;
+    s.nq = a.max_q;
+    if (a.cu_q) {
+        s.t0 = __ldg(a.cu_q + b);
+        const int end = __ldg(a.cu_q + b + 1);
+        if (s.t0 < 0 || end < s.t0 || end > a.total_q || end - s.t0 > a.max_q) {
+            bad = true;
+            s.nq = 0;
+        } else {
+            s.nq = end - s.t0;
+        }
+    }
+    if (report && bad) raise_error(a.err, FFD_ERRBIT_BOUNDS);
+    s.fp = 0;
+    if (a.window > 0) {
+        const int64_t first = (int64_t)s.n - s.nq - a.window + 1;
+        s.fp = first > 0 ? (int)(first >> 6) : 0;
+    }
+    s.np = s.n > 0 && s.nq > 0 ? ((s.n + kPage - 1) >> 6) - s.fp : 0;
+    return s;
+}
+
+// A query enters the matrix instructions as f16 times the power of two that brings its largest
+// magnitude `top` into [2^13, 2^14): mul; f takes scores of it to log2 units (sm log2(e) / mul).
+__device__ __forceinline__ void query_scale(const AttnArgs &a, float top, float &mul, float &f) {
+    int e = (int)(__float_as_uint(top) >> 23) - 127;
+    e = e < -100 ? -100 : (e > 127 ? 127 : e);
+    mul = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
+    f = a.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 + e - 13) << 23);
+    f = fmaxf(f, 1.2e-38f);  // never 0: times -inf it has to stay -inf
+}
+
+// Two channels of a row of out.
+template <class T>
+__device__ __forceinline__ void write_pair(const AttnArgs &a, int row, int hq, int ch, float x,
+                                           float y) {
+    *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) +
+                                  ((int64_t)row * a.Hq + hq) * kD + ch) = T::pack(x, y);
+}
+
+// Log-sum-exp of a row: m the reference of l in log2 units.
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
+}  // namespace kv4
+}  // namespace ffd
