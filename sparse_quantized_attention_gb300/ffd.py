@@ -351,55 +351,57 @@ def alloc_kv4_cache(num_pages: int, num_kv_heads: int, device="cuda") -> Kv4Cach
                     torch.empty(shp, dtype=torch.uint8, device=device))
 
 
-def _need(ok: bool, where: str):
-    if not ok:
-        raise FFDError(1, where)
+# The checks below are in each call's path, which for a decode step takes about as long on the host
+# as on the GPU: they read each tensor's attributes once.
+def _refuse(where: str, what: str):
+    raise FFDError(1, f"{where}: {what}")
 
 
-def _on_one_gpu(where: str, *tensors) -> int:
-    """Index of the device that holds every given tensor (None ones aside)."""
-    dev = tensors[0].get_device()
+def _same_gpu(where: str, dev: int, *tensors):
+    """Every given tensor (None ones aside) is on GPU `dev`."""
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != dev):
-            raise FFDError(1, f"{where}: tensors on different devices, or not on a GPU")
-    return dev
+        if t is not None and t.get_device() != dev:
+            _refuse(where, "tensors on different devices")
+    if dev < 0:
+        _refuse(where, "tensors that are not on a GPU")
 
 
-def _rows_ok(x, num_kv_heads) -> bool:
-    """Rows [T, Hkv, 128] of bf16 or fp16 that lie whole, any distance apart."""
-    return (x.dim() == 3 and x.dtype in _DTYPES and x.shape[1] == num_kv_heads
-            and x.shape[2] == HEAD_DIM and (x.shape[0] == 0 or (
-                x.stride(2) == 1 and (x.shape[1] == 1 or x.stride(1) == HEAD_DIM))))
+def _row_stride(x, rows: int, heads: int, dtype):
+    """Elements between the rows of x [rows, heads, 128], or None when it is not such rows."""
+    if x.dtype != dtype or x.shape != (rows, heads, HEAD_DIM):
+        return None
+    t, h, c = x.stride()
+    if rows == 0:
+        return heads * HEAD_DIM
+    if c != 1 or (h != HEAD_DIM and heads > 1):
+        return None
+    return t if rows > 1 else heads * HEAD_DIM
 
 
-def _row_stride(x) -> int:
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * HEAD_DIM
-
-
-def _ints_ok(x, n) -> bool:
-    return x is None or (x.dtype == torch.int32 and x.dim() == 1 and x.shape[0] == n
-                         and x.is_contiguous())
-
-
-def _table_ok(x) -> bool:
-    return x.dtype == torch.int32 and x.dim() == 2 and x.is_contiguous()
+def _ints_ok(x, *shape) -> bool:
+    return x is None or (x.dtype == torch.int32 and x.shape == shape and x.is_contiguous())
 
 
 def _kv4_ok(cache) -> bool:
-    a, b = cache.k4, cache.v4
-    return (a.dtype == b.dtype == torch.uint8 and a.dim() == 3 and a.shape == b.shape
-            and a.shape[2] == KV4_RECORD_BYTES and a.is_contiguous() and b.is_contiguous())
+    a, b = cache
+    return (a.dtype == torch.uint8 and b.dtype == torch.uint8 and a.dim() == 3
+            and a.shape[2] == KV4_RECORD_BYTES and a.shape == b.shape
+            and a.is_contiguous() and b.is_contiguous())
 
 
-def _launch(dev: int, stream, call):
-    """call(stream pointer) on the tensors' device, on its current stream by default."""
+def _launch(fn, dev: int, stream, where: str, *args):
+    """fn(*args, stream) on the tensors' device, on its current stream by default."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    raw = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    if torch.cuda.current_device() == dev:
-        return call(raw)
-    with torch.cuda.device(dev):
-        return call(raw)
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        raw = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
+    if status != FFD_OK:
+        _check(status, where)
 
 
 def _addr(t):
@@ -412,18 +414,23 @@ def ffd_kv4_write(k_new, v_new, positions, block_table, cache: Kv4Cache, *, cu_t
     the 4-bit cache. Sequence b's rows are cu_tokens[b] .. cu_tokens[b+1]-1 (T / B each when None)
     and go to tokens positions[b], positions[b]+1, ... (negative: nothing for that sequence)."""
     where = "ffd_kv4_write"
-    dev = _on_one_gpu(where, k_new, v_new, positions, block_table, *cache, cu_tokens, error_word)
-    _need(_kv4_ok(cache) and _table_ok(block_table), where)
-    (P, Hkv, _), B = cache.k4.shape, block_table.shape[0]
-    _need(_rows_ok(k_new, Hkv) and _rows_ok(v_new, Hkv) and k_new.dtype == v_new.dtype
-          and k_new.shape[0] == v_new.shape[0] and positions is not None
-          and _ints_ok(positions, B) and _ints_ok(cu_tokens, B + 1), where)
-    desc = CacheDesc(P, Hkv, HEAD_DIM, PAGE)
-    _check(_launch(dev, stream, lambda s: lib().ffd_kv4_write(
-        ctypes.byref(desc), _DTYPES[k_new.dtype], B, block_table.shape[1], k_new.shape[0],
-        _addr(k_new), _row_stride(k_new), _addr(v_new), _row_stride(v_new), _addr(cu_tokens),
-        _addr(positions), _addr(block_table), _addr(cache.k4), _addr(cache.v4),
-        _addr(error_word), s)), where)
+    dev, (k4, v4) = k_new.get_device(), cache
+    _same_gpu(where, dev, v_new, positions, block_table, k4, v4, cu_tokens, error_word)
+    if not _kv4_ok(cache) or block_table.dim() != 2:
+        _refuse(where, "the cache or the block table")
+    P, Hkv, _ = k4.shape
+    B, width = block_table.shape
+    T, dtype = k_new.shape[0], k_new.dtype
+    ks, vs = _row_stride(k_new, T, Hkv, dtype), _row_stride(v_new, T, Hkv, dtype)
+    if ks is None or vs is None or dtype not in _DTYPES:
+        _refuse(where, "rows of bf16 or fp16 [T, Hkv, 128]")
+    if not (_ints_ok(block_table, B, width) and _ints_ok(positions, B)
+            and _ints_ok(cu_tokens, B + 1)):
+        _refuse(where, "int32 positions [B], cu_tokens [B + 1], block_table [B, width]")
+    _launch((_lib or lib()).ffd_kv4_write, dev, stream, where,
+            ctypes.byref(CacheDesc(P, Hkv, HEAD_DIM, PAGE)), _DTYPES[dtype], B, width, T,
+            k_new.data_ptr(), ks, v_new.data_ptr(), vs, _addr(cu_tokens), positions.data_ptr(),
+            block_table.data_ptr(), k4.data_ptr(), v4.data_ptr(), _addr(error_word))
 
 
 def ffd_kv4_read(cache: Kv4Cache, positions, block_table, k_out, v_out, *, cu_tokens=None,
@@ -431,20 +438,27 @@ def ffd_kv4_read(cache: Kv4Cache, positions, block_table, k_out, v_out, *, cu_to
     """The values the 4-bit cache holds, as rows k_out, v_out [T, Hkv, 128] (bf16 or fp16; either
     may be None). Rows and tokens are matched as in ffd_kv4_write."""
     where = "ffd_kv4_read"
-    dev = _on_one_gpu(where, cache.k4, cache.v4, positions, block_table, k_out, v_out, cu_tokens,
-                      error_word)
-    _need(_kv4_ok(cache) and _table_ok(block_table), where)
-    (P, Hkv, _), B = cache.k4.shape, block_table.shape[0]
-    rows = [x for x in (k_out, v_out) if x is not None]
-    _need(len(rows) > 0 and all(_rows_ok(x, Hkv) and x.dtype == rows[0].dtype
-                                and x.shape[0] == rows[0].shape[0] for x in rows)
-          and _ints_ok(positions, B) and _ints_ok(cu_tokens, B + 1), where)
-    desc = CacheDesc(P, Hkv, HEAD_DIM, PAGE)
-    ks, vs = (0 if x is None else _row_stride(x) for x in (k_out, v_out))
-    _check(_launch(dev, stream, lambda s: lib().ffd_kv4_read(
-        ctypes.byref(desc), _DTYPES[rows[0].dtype], B, block_table.shape[1], rows[0].shape[0],
-        _addr(cu_tokens), _addr(positions), _addr(block_table), _addr(cache.k4), _addr(cache.v4),
-        _addr(k_out), ks, _addr(v_out), vs, _addr(error_word), s)), where)
+    k4, v4 = cache
+    dev = k4.get_device()
+    _same_gpu(where, dev, v4, positions, block_table, k_out, v_out, cu_tokens, error_word)
+    if not _kv4_ok(cache) or block_table.dim() != 2:
+        _refuse(where, "the cache or the block table")
+    P, Hkv, _ = k4.shape
+    B, width = block_table.shape
+    one = k_out if k_out is not None else v_out
+    if one is None:
+        _refuse(where, "nothing to read into")
+    T, dtype = one.shape[0], one.dtype
+    ks, vs = (0 if x is None else _row_stride(x, T, Hkv, dtype) for x in (k_out, v_out))
+    if ks is None or vs is None or dtype not in _DTYPES:
+        _refuse(where, "rows of bf16 or fp16 [T, Hkv, 128]")
+    if not (_ints_ok(block_table, B, width) and _ints_ok(positions, B)
+            and _ints_ok(cu_tokens, B + 1)):
+        _refuse(where, "int32 positions [B], cu_tokens [B + 1], block_table [B, width]")
+    _launch((_lib or lib()).ffd_kv4_read, dev, stream, where,
+            ctypes.byref(CacheDesc(P, Hkv, HEAD_DIM, PAGE)), _DTYPES[dtype], B, width, T,
+            _addr(cu_tokens), positions.data_ptr(), block_table.data_ptr(), k4.data_ptr(),
+            v4.data_ptr(), _addr(k_out), ks, _addr(v_out), vs, _addr(error_word))
 
 
 def make_kv4_params(batch, num_q_heads, num_kv_heads, num_pages, max_blocks_per_seq, *,
@@ -476,24 +490,32 @@ def ffd_kv4_attention(params: Kv4Params, q, cache: Kv4Cache, seq_lens, block_tab
     """Attention of each sequence's newest tokens over its 4-bit cache: q [total_q, Hq, 128], rows
     params.q_stride elements apart, out [total_q, Hq, 128], lse fp32 [total_q, Hq] or None."""
     where = "ffd_kv4_attention"
-    dev = _on_one_gpu(where, q, *cache, seq_lens, block_table, out, workspace, cu_q, keep_in, lse)
+    dev, (k4, v4) = q.get_device(), cache
+    _same_gpu(where, dev, k4, v4, seq_lens, block_table, out, workspace, cu_q, keep_in, lse)
     B, Hq, Hkv, T = params.batch, params.num_q_heads, params.num_kv_heads, params.total_q
-    _need(_kv4_ok(cache) and cache.k4.shape[0] == params.num_pages and cache.k4.shape[1] == Hkv
-          and _table_ok(block_table) and block_table.shape == (B, params.max_blocks_per_seq)
-          and _rows_ok(q, Hq) and _rows_ok(out, Hq) and q.shape[0] == T and out.is_contiguous()
-          and out.shape[0] == T and q.dtype == out.dtype and _DTYPES[q.dtype] == params.dtype
-          and (T <= 1 or q.stride(0) == (params.q_stride or Hq * HEAD_DIM))
-          and _ints_ok(seq_lens, B) and _ints_ok(cu_q, B + 1)
-          and (keep_in is None or (
-              keep_in.dtype == torch.uint8 and keep_in.is_contiguous()
-              and keep_in.shape == (B, Hkv, params.max_blocks_per_seq)))
-          and (lse is None or (lse.dtype == torch.float32 and lse.is_contiguous()
-                               and lse.shape == (T, Hq)))
-          and workspace.is_contiguous(), where)
-    _check(_launch(dev, stream, lambda s: lib().ffd_kv4_attention(
-        ctypes.byref(params), _addr(q), _addr(cache.k4), _addr(cache.v4), _addr(seq_lens),
-        _addr(cu_q), _addr(block_table), _addr(keep_in), _addr(out), _addr(lse), _addr(workspace),
-        workspace.numel() * workspace.element_size(), s)), where)
+    width = params.max_blocks_per_seq
+    if not _kv4_ok(cache) or k4.shape[0] != params.num_pages or k4.shape[1] != Hkv:
+        _refuse(where, "the cache")
+    dtype, row = q.dtype, Hq * HEAD_DIM
+    stride = _row_stride(q, T, Hq, dtype)
+    if (_DTYPES.get(dtype) != params.dtype or stride is None
+            or (T > 1 and stride != (params.q_stride or row))
+            or _row_stride(out, T, Hq, dtype) != row):
+        _refuse(where, "q and out of params.dtype [total_q, Hq, 128]")
+    if not (_ints_ok(block_table, B, width) and _ints_ok(seq_lens, B) and _ints_ok(cu_q, B + 1)):
+        _refuse(where, "int32 seq_lens [B], cu_q [B + 1], block_table [B, max_blocks_per_seq]")
+    if keep_in is not None and not (keep_in.dtype == torch.uint8 and keep_in.is_contiguous()
+                                    and keep_in.shape == (B, Hkv, width)):
+        _refuse(where, "keep_in u8 [B, Hkv, max_blocks_per_seq]")
+    if lse is not None and not (lse.dtype == torch.float32 and lse.is_contiguous()
+                                and lse.shape == (T, Hq)):
+        _refuse(where, "lse fp32 [total_q, Hq]")
+    if not workspace.is_contiguous():
+        _refuse(where, "the workspace")
+    _launch((_lib or lib()).ffd_kv4_attention, dev, stream, where, ctypes.byref(params),
+            q.data_ptr(), k4.data_ptr(), v4.data_ptr(), seq_lens.data_ptr(), _addr(cu_q),
+            block_table.data_ptr(), _addr(keep_in), out.data_ptr(), _addr(lse),
+            workspace.data_ptr(), workspace.nbytes)
 
 
 def ffd_get_error(error_word, *, stream=None) -> int:

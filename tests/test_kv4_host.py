@@ -154,12 +154,18 @@ def test_binding_refuses_tensors(lib):
     q = torch.zeros((2, 8, 128), dtype=torch.bfloat16)
     with pytest.raises(ffd.FFDError):
         ffd.ffd_kv4_attention(p, q, cache, pos, bt, q.clone(), torch.zeros(1 << 20))
-    ok = ffd.ffd
-    assert ok._rows_ok(x, 2) and not ok._rows_ok(x, 1) and not ok._rows_ok(x.float(), 2)
-    assert not ok._rows_ok(x.transpose(1, 2), 128)
+    def stride(y, heads=2):
+        return ffd.ffd._row_stride(y, y.shape[0], heads, torch.bfloat16)
+
+    assert stride(x) == 256 and stride(x, heads=1) is None and stride(x.float()) is None
+    assert stride(x.transpose(1, 2), heads=128) is None
     wide = torch.zeros((2, 600), dtype=torch.bfloat16)
-    assert ok._rows_ok(wide[:, 8:264].unflatten(1, (2, 128)), 2)
-    assert not ok._rows_ok(wide[:, :512:2].unflatten(1, (2, 128)), 2)
-    assert not ok._ints_ok(pos.long(), 2) and not ok._ints_ok(pos, 3)
-    assert not ok._table_ok(bt[:, :2])
-    assert not ok._kv4_ok(ffd.Kv4Cache(cache.k4, cache.v4[:2]))
+    assert stride(wide[:, 8:264].unflatten(1, (2, 128))) == 600
+    assert stride(wide[:, :512:2].unflatten(1, (2, 128))) is None
+    assert stride(wide[:1, 8:264].unflatten(1, (2, 128))) == 256  # one row: any distance
+    ints = ffd.ffd._ints_ok
+    assert ints(pos, 2) and ints(None, 2) and not ints(pos.long(), 2) and not ints(pos, 3)
+    assert ints(bt, 2, 3) and not ints(bt[:, :2], 2, 2)
+    assert ffd.ffd._kv4_ok(cache)
+    assert not ffd.ffd._kv4_ok(ffd.Kv4Cache(cache.k4, cache.v4[:2]))
+    assert not ffd.ffd._kv4_ok(ffd.Kv4Cache(cache.k4[:, :, :64], cache.v4[:, :, :64]))
