@@ -485,7 +485,7 @@ typedef struct {
     int32_t num_kv_heads;       /* Hkv; G = Hq / Hkv in 1..8 */
     int32_t head_dim;           /* must be 128 */
     int32_t page_size;          /* must be 64 */
-    int32_t num_pages;          /* P, bound for block_table entries */
+    int32_t num_pages;          /* P, bound for block_table entries; P * Hkv <= INT32_MAX */
     int32_t max_blocks_per_seq; /* row stride of block_table; seq_lens[b] <= 64 * this; B * Hkv *
                                    this * ceil(max_q_len * G / 256) <= INT32_MAX */
     int32_t dtype;              /* FFD_DTYPE_BF16 or FFD_DTYPE_F16, of q and out */

@@ -10,7 +10,7 @@ namespace kv4 {
 constexpr int kRec = FFD_KV4_RECORD_BYTES;
 constexpr int kParamOff = 4096;  // (scale, off) pairs behind the codes
 static_assert(kRec == 5120, "record size");
-constexpr int kMaxCtas = 1024;  // of an attention launch (one per SM at most)
+constexpr int kMaxCtas = 1024;     // of an attention launch (one per SM at most)
 constexpr float kMaxInput = 16384.0f;  // |off| <= |min| + 16/15 range stays inside f16
 
 // Byte offset, inside a record, of the 16 code bytes of group g (32 channels) of token r.
@@ -59,7 +59,8 @@ __device__ __forceinline__ __half2 code_pair(uint32_t w) {
     if (i == 1) x = w << 2;
     if (i == 2) x = w >> 2;
     if (i == 3) x = w >> 6;
-    x = (x & 0x03c003c0u) | 0x4c004c00u;
+    // (x & mask) | exponent as one operation: two immediates would take two
+    asm("lop3.b32 %0, %0, %1, %2, 0xea;" : "+r"(x) : "r"(0x03c003c0u), "r"(0x4c004c00u));
     return *reinterpret_cast<const __half2 *>(&x);
 }
 

@@ -16,7 +16,7 @@ cudaError_t launch_chunk(const AttnArgs &a, const Plan &pl, int dtype, cudaStrea
 size_t decode_record_bytes(int cols);
 size_t chunk_record_bytes();
 int chunk_rows();
-int decode_warps();
+int decode_warps(int cols);
 }  // namespace kv4
 }  // namespace ffd
 
@@ -87,7 +87,8 @@ ffd_status check_params(const ffd_kv4_params *p) {
     if (p->num_q_heads / p->num_kv_heads > kMaxG) return FFD_ERR_UNSUPPORTED;
     if ((int64_t)p->batch * p->num_kv_heads > (int64_t)kMaxUnits) return FFD_ERR_UNSUPPORTED;
     if ((int64_t)p->max_blocks_per_seq * kPage > INT32_MAX) return FFD_ERR_UNSUPPORTED;
-    // a page of a unit, for each group of rows that takes it, is named by an int32
+    // a record is named by an int32, and so is a page of a unit for each group of rows that takes it
+    if ((int64_t)p->num_pages * p->num_kv_heads > INT32_MAX) return FFD_ERR_UNSUPPORTED;
     const int64_t pages = (int64_t)p->batch * p->num_kv_heads * p->max_blocks_per_seq;
     const int64_t rows = (int64_t)p->max_q_len * (p->num_q_heads / p->num_kv_heads);
     if (pages > INT32_MAX || pages > INT32_MAX / ((rows + chunk_rows() - 1) / chunk_rows()))
@@ -100,20 +101,21 @@ size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 // At least this many pages (upper bound from the table's width) for each CTA.
 constexpr int64_t kMinDecodePages = 8, kMinChunkPages = 4;
 
-// Workspace: [error word | join tickets per CTA | two records per CTA | a parked state per warp of
-// the decode kernel]. The tickets, the only part that has to start at zero, have the same place and
-// size whatever the parameters, so that calls of different shapes can share a workspace.
+// Workspace: [error word | a join ticket per CTA | records per CTA | a parked state per warp of the
+// decode kernel]. The tickets, the only part that has to start at zero, have the same place and size
+// whatever the parameters and are left at zero, so that calls of different shapes can share a
+// workspace.
 ffd_status make_plan(const ffd_kv4_params *p, Plan *pl) {
     const ffd_status st = check_params(p);
     if (st != FFD_OK) return st;
     const int64_t rows = (int64_t)p->max_q_len * (p->num_q_heads / p->num_kv_heads);
     pl->cols = rows <= 8 ? 8 : rows <= 16 ? 16 : 0;
     const int sms = current_sm_count();
+    int64_t pages = (int64_t)p->batch * p->num_kv_heads * p->max_blocks_per_seq;
+    if (!pl->cols) pages *= (rows + chunk_rows() - 1) / chunk_rows();
     int64_t ctas = p->num_splits;
     if (ctas == 0) {
         if (sms <= 0) return FFD_ERR_CUDA;
-        int64_t pages = (int64_t)p->batch * p->num_kv_heads * p->max_blocks_per_seq;
-        if (!pl->cols) pages *= (rows + chunk_rows() - 1) / chunk_rows();
         const int64_t least = pl->cols ? kMinDecodePages : kMinChunkPages;
         ctas = (pages + least - 1) / least;
     }
@@ -125,9 +127,9 @@ ffd_status make_plan(const ffd_kv4_params *p, Plan *pl) {
     pl->tickets = off;
     off = align_up(off + kMaxCtas * sizeof(int));
     pl->records = off;
-    off = align_up(off + 2 * pl->ctas * rec);
+    off = align_up(off + (pl->cols ? 4 : 2) * pl->ctas * rec);
     pl->parked = off;
-    if (pl->cols) off = align_up(off + (size_t)pl->ctas * decode_warps() * rec);
+    if (pl->cols) off = align_up(off + (size_t)pl->ctas * decode_warps(pl->cols) * rec);
     pl->total = off;
     return FFD_OK;
 }

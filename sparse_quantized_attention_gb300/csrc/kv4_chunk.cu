@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         __syncthreads();  // nobody stops between the reading of it and this
 
         float m = -INFINITY, l = 0.0f;
-        bool any = false;
+        bool any = false, far = false;
         if (run && grp < 2) {
             // ================= softmax of tile grp, one row a thread =================
             const bool active = grp == 0 || two;
@@ -383,6 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                         const float al = m == -INFINITY ? 0.0f : ex2_approx(m - mn);
                         m = mn;
                         l *= al;
+                        far = __any_sync(0xffffffffu, fabsf(m) > kFar && m != -INFINITY);
                         if (any) {
 #pragma unroll 1
                             for (int c = 0; c < 4; c++) {
@@ -398,14 +399,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                         }
                     }
                     const float sub = kShift - (m == -INFINITY ? 0.0f : m);
+                    // Where the reference is so large that its rounding is felt, the products are
+                    // rounded as it was: the exact ones could pass it by more than f16 can hold.
+                    const float fx = far ? 1.0f : fs;
+                    if (far) {
+#pragma unroll
+                        for (int c = 0; c < 32; c++) {
+                            x0[c] = __float_as_uint(__fmul_rn(__uint_as_float(x0[c]), fs));
+                            x1[c] = __float_as_uint(__fmul_rn(__uint_as_float(x1[c]), fs));
+                        }
+                    }
                     float l0 = 0.0f, l1 = 0.0f;
                     uint32_t p[32];
 #pragma unroll
                     for (int c = 0; c < 16; c++) {
-                        const float p0 = ex2_approx(fmaf(__uint_as_float(x0[2 * c]), fs, sub));
-                        const float p1 = ex2_approx(fmaf(__uint_as_float(x0[2 * c + 1]), fs, sub));
-                        const float p2 = ex2_approx(fmaf(__uint_as_float(x1[2 * c]), fs, sub));
-                        const float p3 = ex2_approx(fmaf(__uint_as_float(x1[2 * c + 1]), fs, sub));
+                        const float p0 = ex2_approx(fmaf(__uint_as_float(x0[2 * c]), fx, sub));
+                        const float p1 = ex2_approx(fmaf(__uint_as_float(x0[2 * c + 1]), fx, sub));
+                        const float p2 = ex2_approx(fmaf(__uint_as_float(x1[2 * c]), fx, sub));
+                        const float p3 = ex2_approx(fmaf(__uint_as_float(x1[2 * c + 1]), fx, sub));
                         l0 += p0 + p1;
                         l1 += p2 + p3;
                         p[c] = F16::pack(p0, p1);

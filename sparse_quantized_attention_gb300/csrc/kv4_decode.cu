@@ -2,8 +2,9 @@
 // share a KV head (NT = 1: one decode token of any GQA group; NT = 2: up to 16 pairs).
 //
 // The definition is the one of ffd.h. The pages of all (sequence, KV head) units, concatenated, are
-// cut into equal contiguous ranges, one per CTA, and each range into one per warp. A warp walks its
-// pages alone: it has room for one page's K record and one V record in shared memory, each refilled
+// cut into equal contiguous ranges, one per CTA (more when a range would not fit its list). The CTA
+// lists the pages of its range that a mask keeps, each warp takes an equal share of the list and
+// walks it alone: it has room for one page's K record and one V record in shared memory, each refilled
 // by a bulk copy as soon as it has been read, computes
 //   S = K q^T   (16 tokens x 8 columns a matrix instruction, 8 of them over the 128 channels),
 //   P = 2^(S - m) against the running maximum m of each column,
@@ -23,47 +24,36 @@ namespace ffd {
 namespace kv4 {
 namespace {
 
-constexpr int kWarps = 16;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kSlot = 2 * kRec;       // a warp's K record and V record
 constexpr int kStride = 130;          // floats of a joined column: o[128], m, l
 constexpr float kShift = 14.0f;       // P carries 2^14
+constexpr int kWindow = 2048;         // pages of a CTA's list
 
+// Warps of a CTA: what their registers allow (128 a thread for one column tile, 168 for two).
+template <int NT>
+constexpr int kWarpsOf = NT == 1 ? 16 : 12;
+
+// A page of a range's list.
+struct Entry {
+    int rec;    // page * Hkv + h; -1: dropped, listed because it is its unit's first in the window
+    int unit;   // b * Hkv + h
+    int j;      // block of the sequence
+    int first;  // the unit's first item
+};
+
+template <int NT>
 struct Shared {
-    uint8_t ring[kWarps][kSlot];      // later each warp's last state
-    uint64_t full[kWarps][2];
-    int pre[kThreads + 1];            // items before each thread's chunk of sequences
-    int scan[kWarps];
-    int unit[kWarps][2];              // unit of a warp's parked and of its last state, or -1
+    static constexpr int W = kWarpsOf<NT>;
+    uint8_t ring[W][kSlot];           // later each warp's last state
+    Entry list[kWindow];
+    uint64_t full[W][2];
+    int pre[32 * W];                  // items before each thread's chunk of sequences
+    int scan[W];
+    int unit[W][2], first[W][2];      // of a warp's parked and of its last state (unit -1: none)
     int flag;
 };
-static_assert(sizeof(Shared) + 128 <= 232448, "shared memory per CTA");
-
-// Where an item lies: unit (b, h), page j of the unit's np.
-struct At {
-    int b, h, j;
-    Seq s;
-};
-
-__device__ __forceinline__ At locate(const AttnArgs &a, const Shared &sh, int chunk, int x) {
-    int lo = 0, hi = kThreads;  // the last chunk that starts at or before x
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (sh.pre[mid] <= x) lo = mid;
-        else hi = mid;
-    }
-    At p;
-    int rem = x - sh.pre[lo];
-    for (p.b = lo * chunk; p.b < a.B; p.b++) {
-        p.s = seq_of(a, p.b, false);
-        const int span = p.s.np * a.Hkv;
-        if (rem < span) break;
-        rem -= span;
-    }
-    p.h = rem / p.s.np;
-    p.j = rem - p.h * p.s.np;
-    return p;
-}
+static_assert(sizeof(Shared<1>) + 128 <= 232448 && sizeof(Shared<2>) + 128 <= 232448,
+              "shared memory per CTA");
 
 // Softmax state of a warp: columns 2 tig, 2 tig + 1 of each 8-column tile (tig = lane % 4). m is the
 // columns' reference (log2 units), the same in all lanes of a column; l sums this lane's rows;
@@ -308,19 +298,20 @@ __device__ __forceinline__ void wait_copy(const AttnArgs &a, uint64_t *bar, uint
 }
 
 template <int NT, class T>
-__global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const AttnArgs a, float *parked,
-                                                                 float *records, int *tickets) {
+__global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
+    kv4_decode_kernel(const AttnArgs a, float *parked, float *records, int *tickets) {
+    constexpr int W = kWarpsOf<NT>, kThreads = 32 * W, cols = 8 * NT;
+    constexpr int kRecord = cols * kStride;
     extern __shared__ uint8_t raw[];
-    Shared &sh = *reinterpret_cast<Shared *>(align_shared<128>(raw));
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int cols = 8 * NT;
+    Shared<NT> &sh = *reinterpret_cast<Shared<NT> *>(align_shared<128>(raw));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
 
     // ---- items before each chunk of sequences -------------------------------------------------
     const int chunk = (a.B + kThreads - 1) / kThreads;
     int own = 0;
     bool empty = false;  // a sequence has queries and nothing for them to see
     for (int b = tid * chunk; b < (tid + 1) * chunk && b < a.B; b++) {
-        const Seq s = seq_of(a, b, blockIdx.x == 0);
+        const Seq s = seq_of(a, b, cta == 0);
         own += s.np * a.Hkv;
         empty |= s.np == 0 && s.nq > 0;
     }
@@ -331,24 +322,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const AttnArgs 
         if (lane >= o) inc += y;
     }
     if (lane == 31) sh.scan[warp] = inc;
-    if (lane < 2) {
-        mbar_init(&sh.full[warp][lane], 1);
-        sh.unit[warp][lane] = -1;
-    }
+    if (lane < 2) mbar_init(&sh.full[warp][lane], 1);
     fence_barrier_init();
     const bool any_empty = __syncthreads_or(empty);
-    int base = 0, total = 0;
+    int total;
+    {
+        const int v = lane < W ? sh.scan[lane] : 0;
+        int up = v;
 #pragma unroll
-    for (int w = 0; w < kWarps; w++) {
-        const int v = sh.scan[w];
-        base += w < warp ? v : 0;
-        total += v;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, up, o);
+            if (lane >= o) up += y;
+        }
+        total = __shfl_sync(0xffffffffu, up, 31);
+        const int before = __shfl_sync(0xffffffffu, up - v, warp);
+        sh.pre[tid] = before + inc - own;
     }
-    sh.pre[tid] = base + inc - own;
-    __syncthreads();
-
     if (any_empty) {
-        for (int u = blockIdx.x * kWarps + warp; u < a.B * a.Hkv; u += gridDim.x * kWarps) {
+        for (int u = cta * W + warp; u < a.B * a.Hkv; u += gridDim.x * W) {
             const int b = u / a.Hkv, h = u - b * a.Hkv;
             const Seq s = seq_of(a, b, false);
             if (s.np > 0) continue;
@@ -361,314 +352,359 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const AttnArgs 
             }
         }
     }
+    // the items are cut into equal ranges r0 .. r1 - 1, one per CTA
     const int ncta = total < (int)gridDim.x ? total : (int)gridDim.x;
-    const int cta = blockIdx.x;
     if (cta >= ncta) return;
-    const int c0 = (int)((int64_t)total * cta / ncta), c1 = (int)((int64_t)total * (cta + 1) / ncta);
-    int x = c0 + (int)((int64_t)(c1 - c0) * warp / kWarps);
-    const int xe = c0 + (int)((int64_t)(c1 - c0) * (warp + 1) / kWarps);
+    const int r0 = (int)((int64_t)total * cta / ncta), r1 = (int)((int64_t)total * (cta + 1) / ncta);
+    __syncthreads();
 
-    // ---- this warp's pages --------------------------------------------------------------------
     uint8_t *kbuf = sh.ring[warp], *vbuf = kbuf + kRec;
     uint64_t *kfull = &sh.full[warp][0], *vfull = &sh.full[warp][1];
-    uint32_t phase = 0, kissued = 0, vissued = 0;
+    uint32_t taken = 0;  // pages this warp has finished
     bool dead = false;
-    if (x < xe) {
-        At at = locate(a, sh, chunk, x);
-        State<NT> st;
-        while (true) {
-            const int left = at.s.np - at.j;
-            const int cnt = left < xe - x ? left : xe - x;  // pages of this unit
-            const Seq s = at.s;
-            const int h = at.h, b = at.b, unit = b * a.Hkv + h;
-            uint32_t qf[NT][16];
-            float fs[NT][2];
-            const int j0 = s.fp + at.j, j1 = j0 + cnt;
-            const int32_t *bt = a.block_table + (int64_t)b * a.max_blocks;
-            const uint8_t *keep = a.keep_in ? a.keep_in + ((int64_t)unit) * a.max_blocks : nullptr;
-            // pages jb .. jb + 31 of the unit, one per lane (-1: dropped); the next 32 are read ahead
-            int jb = j0, page = -1, ahead = -1;
-            uint32_t todo;
-            auto look = [&](int j) {
-                int p = -1;
-                if (j < j1 && (!keep || __ldg(keep + j))) {
-                    p = __ldg(bt + j);
-                    if (p < 0 || p >= a.P) {
-                        raise_error(a.err, FFD_ERRBIT_BOUNDS);
-                        p = -1;
-                    }
+    // a range is walked in windows w0 .. w1 - 1 that fit the list; a unit that goes on in the next
+    // window leaves its joined state in one of the CTA's two carry records
+    for (int w0 = r0, turn = 0; w0 < r1; w0 += kWindow, turn ^= 1) {
+        const int w1 = r1 - w0 < kWindow ? r1 : w0 + kWindow;
+
+        // ---- the window's pages, those that are dropped left out ------------------------------
+        int count = 0;
+        for (int x0 = w0; x0 < w1; x0 += kThreads) {
+            const int x = x0 + tid;
+            Entry e = {-1, 0, 0, 0};
+            bool in = false;
+            if (x < w1) {
+                int lo = 0, hi = a.B < kThreads ? a.B : kThreads;
+                while (hi - lo > 1) {  // the last chunk that starts at or before x
+                    const int mid = (lo + hi) >> 1;
+                    if (sh.pre[mid] <= x) lo = mid;
+                    else hi = mid;
                 }
-                return p;
-            };
-            page = look(jb + lane);
-            ahead = look(jb + 32 + lane);
-            todo = __ballot_sync(0xffffffffu, page >= 0);
-            // the next page to take: its index and number, -1 when there is none
-            auto pop = [&](int &pg) {
-                while (todo == 0) {
-                    jb += 32;
-                    if (jb >= j1) return -1;
-                    page = ahead;
-                    ahead = look(jb + 32 + lane);
-                    todo = __ballot_sync(0xffffffffu, page >= 0);
+                int rem = x - sh.pre[lo], b = lo * chunk;
+                Seq s = seq_of(a, b, false);
+                while (rem >= s.np * a.Hkv) {
+                    rem -= s.np * a.Hkv;
+                    s = seq_of(a, ++b, false);
                 }
-                const int k = __ffs(todo) - 1;
-                todo &= todo - 1;
-                pg = __shfl_sync(0xffffffffu, page, k);
-                return jb + k;
-            };
-            auto fetch = [&](const uint8_t *from, uint8_t *to, uint64_t *bar, int pg) {
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(bar, kRec);
-                    tma_load_1d(to, from + ((int64_t)pg * a.Hkv + h) * kRec, kRec, bar);
+                const int h = rem / s.np, j = rem - h * s.np;
+                e.unit = b * a.Hkv + h;
+                e.j = s.fp + j;
+                e.first = x - j;
+                if (!a.keep_in || __ldg(a.keep_in + (int64_t)e.unit * a.max_blocks + e.j)) {
+                    const int page = __ldg(a.block_table + (int64_t)b * a.max_blocks + e.j);
+                    if (page < 0 || page >= a.P) raise_error(a.err, FFD_ERRBIT_BOUNDS);
+                    else e.rec = page * a.Hkv + h;
                 }
-            };
-            int pg = -1;
-            int j = pop(pg);
-            if (j >= 0 && !dead) {
-                fetch(a.k4, kbuf, kfull, pg);
-                fetch(a.v4, vbuf, vfull, pg);
+                in = e.rec >= 0 || j == 0 || x == w0;
+            }
+            const uint32_t bal = __ballot_sync(0xffffffffu, in);
+            if (x0 != w0) __syncthreads();  // sh.scan is read no more
+            if (lane == 0) sh.scan[warp] = __popc(bal);
+            __syncthreads();
+            int before = 0, all = 0;
+#pragma unroll
+            for (int w = 0; w < W; w++) {
+                const int v = sh.scan[w];
+                before += w < warp ? v : 0;
+                all += v;
+            }
+            if (in) sh.list[count + before + __popc(bal & ((1u << lane) - 1u))] = e;
+            count += all;
+        }
+        if (lane < 2) sh.unit[warp][lane] = -1;
+        __syncthreads();
+
+        // ---- this warp's share of the list ----------------------------------------------------
+        const int i0 = count * warp / W, i1 = count * (warp + 1) / W;
+        auto next = [&](int i) {  // the next page to fetch from i on, i1 when there is none
+            while (i < i1 && sh.list[i].rec < 0) i++;
+            return i;
+        };
+        auto fetch = [&](const uint8_t *from, uint8_t *to, uint64_t *bar, int i) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar, kRec);
+                tma_load_1d(to, from + (int64_t)sh.list[i].rec * kRec, kRec, bar);
+            }
+        };
+        uint32_t kissued = taken, vissued = taken;
+        if (w0 != r0) fence_proxy_async();  // the room held the last window's states
+        {
+            const int i = next(i0);
+            if (i < i1 && !dead) {
+                fetch(a.k4, kbuf, kfull, i);
+                fetch(a.v4, vbuf, vfull, i);
                 kissued++, vissued++;
             }
+        }
+        for (int i = i0; i < i1;) {
+            // one unit's part of the share: entries i .. ie - 1
+            const int unit = sh.list[i].unit, first = sh.list[i].first, start = i;
+            const int b = unit / a.Hkv, h = unit - b * a.Hkv;
+            const Seq s = seq_of(a, b, false);
+            State<NT> st;
+            uint32_t qf[NT][16];
+            float fs[NT][2];
             load_queries<NT, T>(a, s, h, lane, qf, fs);
             st.clear();
+            bool far = false;
             const int low = s.n - s.nq;  // position of the first query
-            while (j >= 0 && !dead) {
-                int npg = -1;
-                const int nj = pop(npg);
-                wait_copy(a, kfull, phase, dead);
+            for (; i < i1; i++) {
+                const Entry e = sh.list[i];
+                if (e.unit != unit) break;
+                if (e.rec < 0 || dead) continue;
+                const int ni = next(i + 1);
+                wait_copy(a, kfull, taken & 1, dead);
                 dead = __any_sync(0xffffffffu, dead);
                 float sc[NT][4][4];
                 page_scores<NT>(kbuf, lane, qf, sc);
                 __syncwarp();
-                const bool more = nj >= 0 && !dead;
+                const bool more = ni < i1 && !dead;
                 if (more) {
-                    fetch(a.k4, kbuf, kfull, npg);
+                    fetch(a.k4, kbuf, kfull, ni);
                     kissued++;
                 }
-                // ---- masks, maxima, probabilities
-                const int t0 = 64 * j;
-                const bool whole =
-                    t0 + 63 <= low && (a.window == 0 || t0 > s.n - 1 - a.window);
-                uint32_t pf[NT][4][2];
-                float mx[NT][2];
+                // ---- masks, maxima, probabilities (scores still want their factor fs)
+                const int t0 = 64 * e.j;
+                if (!(t0 + 63 <= low && (a.window == 0 || t0 > s.n - 1 - a.window))) {
 #pragma unroll
-                for (int t = 0; t < NT; t++) {
+                    for (int t = 0; t < NT; t++)
 #pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        float top = -INFINITY;
-                        if (whole) {
-#pragma unroll
-                            for (int k = 0; k < 4; k++) {
-                                sc[t][k][e] *= fs[t][e];
-                                sc[t][k][2 + e] *= fs[t][e];
-                                top = fmaxf(top, fmaxf(sc[t][k][e], sc[t][k][2 + e]));
-                            }
-                        } else {
-                            const int pos = low + (8 * t + 2 * (lane & 3) + e) / a.G;
+                        for (int c = 0; c < 2; c++) {
+                            const int pos = low + (8 * t + 2 * (lane & 3) + c) / a.G;
                             const int from = a.window > 0 ? pos - a.window : -1;
 #pragma unroll
                             for (int k = 0; k < 4; k++)
 #pragma unroll
                                 for (int r = 0; r < 2; r++) {
                                     const int tok = t0 + 16 * k + 8 * r + (lane >> 2);
-                                    float &v = sc[t][k][2 * r + e];
-                                    v = tok <= pos && tok > from ? v * fs[t][e] : -INFINITY;
-                                    top = fmaxf(top, v);
+                                    if (tok > pos || tok <= from) sc[t][k][2 * r + c] = -INFINITY;
                                 }
                         }
-                        mx[t][e] = top;
-                    }
                 }
+                float mx[NT][2];
                 bool up = false;
 #pragma unroll
                 for (int t = 0; t < NT; t++)
 #pragma unroll
-                    for (int e = 0; e < 2; e++) up |= mx[t][e] > st.m[t][e];
+                    for (int c = 0; c < 2; c++) {
+                        float top = fmaxf(sc[t][0][c], sc[t][0][2 + c]);
+#pragma unroll
+                        for (int k = 1; k < 4; k++)
+                            top = fmaxf(top, fmaxf(sc[t][k][c], sc[t][k][2 + c]));
+                        mx[t][c] = top * fs[t][c];
+                        up |= mx[t][c] > st.m[t][c];
+                    }
                 if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
                     for (int t = 0; t < NT; t++)
 #pragma unroll
-                        for (int e = 0; e < 2; e++) {
-                            float top = fmaxf(mx[t][e], st.m[t][e]);
+                        for (int c = 0; c < 2; c++) {
+                            float top = fmaxf(mx[t][c], st.m[t][c]);
 #pragma unroll
                             for (int o = 4; o < 32; o <<= 1)
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                            const float al =
-                                top == -INFINITY ? 0.0f : ex2_approx(st.m[t][e] - top);
-                            st.m[t][e] = top;
-                            st.l[t][e] *= al;
+                            const float al = top == -INFINITY ? 0.0f : ex2_approx(st.m[t][c] - top);
+                            st.m[t][c] = top;
+                            far |= fabsf(top) > kFar && top != -INFINITY;
+                            st.l[t][c] *= al;
 #pragma unroll
-                            for (int c = 0; c < 8; c++) {
-                                st.o[t][c][e] *= al;
-                                st.o[t][c][2 + e] *= al;
+                            for (int k = 0; k < 8; k++) {
+                                st.o[t][k][c] *= al;
+                                st.o[t][k][2 + c] *= al;
                             }
                         }
                 }
+                // Where the reference is so large that its rounding is felt, the products are rounded
+                // as it was: the exact ones could pass it by more than f16 can hold.
+                const bool round = __any_sync(0xffffffffu, far);
+                uint32_t pf[NT][4][2];
 #pragma unroll
                 for (int t = 0; t < NT; t++) {
-                    float sub[2];
+                    const float f0 = round ? 1.0f : fs[t][0], f1 = round ? 1.0f : fs[t][1];
+                    if (round) {
 #pragma unroll
-                    for (int e = 0; e < 2; e++)
-                        sub[e] = (st.m[t][e] == -INFINITY ? 0.0f : st.m[t][e]) - kShift;
+                        for (int k = 0; k < 4; k++)
+#pragma unroll
+                            for (int r = 0; r < 4; r++)
+                                sc[t][k][r] = __fmul_rn(sc[t][k][r], fs[t][r & 1]);
+                    }
+                    float add[2];
+#pragma unroll
+                    for (int c = 0; c < 2; c++)
+                        add[c] = kShift - (st.m[t][c] == -INFINITY ? 0.0f : st.m[t][c]);
 #pragma unroll
                     for (int k = 0; k < 4; k++)
 #pragma unroll
                         for (int r = 0; r < 2; r++) {
-                            const float p0 = ex2_approx(sc[t][k][2 * r] - sub[0]);
-                            const float p1 = ex2_approx(sc[t][k][2 * r + 1] - sub[1]);
+                            const float p0 = ex2_approx(fmaf(sc[t][k][2 * r], f0, add[0]));
+                            const float p1 = ex2_approx(fmaf(sc[t][k][2 * r + 1], f1, add[1]));
                             st.l[t][0] += p0;
                             st.l[t][1] += p1;
                             pf[t][k][r] = movmatrix_trans(F16::pack(p0, p1));
                         }
                 }
-                wait_copy(a, vfull, phase, dead);
+                wait_copy(a, vfull, taken & 1, dead);
                 dead = __any_sync(0xffffffffu, dead);
                 page_values<NT>(vbuf, lane, s.n - t0, pf, st);
                 __syncwarp();
                 if (more && !dead) {
-                    fetch(a.v4, vbuf, vfull, npg);
+                    fetch(a.v4, vbuf, vfull, ni);
                     vissued++;
                 }
-                phase ^= 1;
-                j = nj;
+                taken++;
             }
             st.close();
-            x += cnt;
-            // ---- the unit's part is done
-            if (cnt == s.np) {
+            // ---- the part is done: written out when it is all of its unit, else kept for the join
+            const bool whole = first >= w0 && first + s.np <= w1 &&
+                               (start > i0 || i0 == 0 || sh.list[i0 - 1].unit != unit) &&
+                               (i < i1 || i1 == count || sh.list[i1].unit != unit);
+            if (whole) {
                 write_direct<NT, T>(a, s, h, lane, st);
-            } else if (x < xe) {  // more units follow: this state waits in the workspace
-                park<NT>(parked + ((int64_t)cta * kWarps + warp) * cols * kStride, lane, st);
-                if (lane == 0) sh.unit[warp][0] = unit;
             } else {
+                const int last = i == i1;  // else more units follow and the copies' room is in use
                 __syncwarp();
-                park<NT>(reinterpret_cast<float *>(kbuf), lane, st);
-                if (lane == 0) sh.unit[warp][1] = unit;
-            }
-            if (x >= xe) break;
-            __syncwarp();
-            at.j = 0;
-            if (++at.h == a.Hkv) {
-                at.h = 0;
-                do {
-                    at.s = seq_of(a, ++at.b, false);
-                } while (at.s.np == 0);
+                park<NT>(last ? reinterpret_cast<float *>(kbuf)
+                              : parked + ((int64_t)cta * W + warp) * kRecord,
+                         lane, st);
+                if (lane == 0) {
+                    sh.unit[warp][last] = unit;
+                    sh.first[warp][last] = first;
+                }
             }
         }
-    }
-    if (dead) {  // leave no copy in flight
-        bool late = false;
-        if (kissued) wait_copy(a, kfull, (kissued - 1) & 1, late);
-        if (vissued) wait_copy(a, vfull, (vissued - 1) & 1, late);
-    }
-    __syncthreads();
+        if (dead) {  // leave no copy in flight
+            bool late = false;
+            if (kissued) wait_copy(a, kfull, (kissued - 1) & 1, late);
+            if (vissued) wait_copy(a, vfull, (vissued - 1) & 1, late);
+        }
+        __syncthreads();
 
-    // ---- join the warps' states of each unit, then the CTAs' ----------------------------------
-    auto state_of = [&](int i) -> const float * {  // entry i: warp i / 2, parked (0) or last (1)
-        const int w = i >> 1;
-        return (i & 1) ? reinterpret_cast<const float *>(sh.ring[w])
-                       : parked + ((int64_t)cta * kWarps + w) * cols * kStride;
-    };
-    for (int i0 = 0; i0 < 2 * kWarps;) {
-        const int u = sh.unit[i0 >> 1][i0 & 1];
-        if (u < 0) {
-            i0++;
-            continue;
-        }
-        int i1 = i0 + 1;  // entries i0 .. i1 - 1 that are not -1 belong to unit u
-        for (; i1 < 2 * kWarps; i1++) {
-            const int v = sh.unit[i1 >> 1][i1 & 1];
-            if (v >= 0 && v != u) break;
-        }
-        const int b = u / a.Hkv, h = u - b * a.Hkv;
-        const Seq s = seq_of(a, b, false);
-        int first = sh.pre[b / chunk] + h * s.np;  // the unit's first item
-        for (int q = b / chunk * chunk; q < b; q++) first += seq_of(a, q, false).np * a.Hkv;
-        const bool begins = first >= c0, complete = begins && first + s.np <= c1;
-        float *mine = records + (int64_t)(2 * cta + (begins ? 1 : 0)) * cols * kStride;
-        for (int k = tid; k < cols * 64; k += kThreads) {
-            const int c = k >> 6, ch = 2 * (k & 63);
-            float M = -INFINITY;
-            for (int i = i0; i < i1; i++)
-                if (sh.unit[i >> 1][i & 1] >= 0) M = fmaxf(M, state_of(i)[c * kStride + 128]);
-            float2 o = make_float2(0.0f, 0.0f);
-            float l = 0.0f;
-            for (int i = i0; i < i1; i++) {
-                if (sh.unit[i >> 1][i & 1] < 0) continue;
-                const float *col = state_of(i) + c * kStride;
-                const float2 ml = *reinterpret_cast<const float2 *>(col + 128);
-                const float2 v = *reinterpret_cast<const float2 *>(col + ch);
+        // ---- join the warps' states of each unit, then the ranges' ----------------------------
+        // Lane i has entry i: warp i / 2, parked (even) or last (odd). A warp takes half a column.
+        const int eu = lane < 2 * W ? sh.unit[lane >> 1][lane & 1] : -1;
+        const int ef = lane < 2 * W ? sh.first[lane >> 1][lane & 1] : 0;
+        const float *es = (lane & 1) ? reinterpret_cast<const float *>(sh.ring[(lane >> 1) % W])
+                                     : parked + ((int64_t)cta * W + (lane >> 1) % W) * kRecord;
+        for (uint32_t todo = __ballot_sync(0xffffffffu, eu >= 0); todo;) {
+            const int lead = __ffs(todo) - 1;
+            const int u = __shfl_sync(0xffffffffu, eu, lead);
+            const int first = __shfl_sync(0xffffffffu, ef, lead);
+            const uint32_t run = __ballot_sync(0xffffffffu, eu == u);
+            todo &= ~run;
+            const int b = u / a.Hkv, h = u - b * a.Hkv;
+            const Seq s = seq_of(a, b, false);
+            const bool carried = first < w0 && w0 > r0;            // from the window before
+            const bool goes_on = first + s.np > w1 && w1 < r1;     // into the next one
+            const bool begins = first >= r0, complete = begins && first + s.np <= r1;
+            const float *carry = records + (int64_t)(4 * cta + 2 + (turn ^ 1)) * kRecord;
+            float *mine = records + (int64_t)(4 * cta + (goes_on ? 2 + turn : begins)) * kRecord;
+            for (int hc = warp; hc < 2 * cols; hc += W) {
+                const int c = hc >> 1, ch = 64 * (hc & 1) + 2 * lane;
+                float2 ml = make_float2(-INFINITY, 0.0f);
+                if (eu == u) ml = *reinterpret_cast<const float2 *>(es + c * kStride + 128);
+                float M = warp_max(ml.x);
+                float2 cm = make_float2(-INFINITY, 0.0f), o = make_float2(0.0f, 0.0f);
+                if (carried) {
+                    cm = *reinterpret_cast<const float2 *>(carry + c * kStride + 128);
+                    o = *reinterpret_cast<const float2 *>(carry + c * kStride + ch);
+                    M = fmaxf(M, cm.x);
+                }
+                const float cf = cm.x == -INFINITY ? 0.0f : ex2_approx(cm.x - M);
                 const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - M);
-                o.x = fmaf(f, v.x, o.x);
-                o.y = fmaf(f, v.y, o.y);
-                l = fmaf(f, ml.y, l);
+                const float l = fmaf(cf, cm.y, warp_sum(f * ml.y));
+                o.x *= cf;
+                o.y *= cf;
+                uint32_t left = run;
+                while (left) {
+                    float2 v[4];
+                    float w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {  // four states' loads at a time
+                        const int i = left ? __ffs(left) - 1 : 0;
+                        w[k] = left ? __shfl_sync(0xffffffffu, f, i) : 0.0f;
+                        const float *from = (i & 1) ? reinterpret_cast<const float *>(sh.ring[i >> 1])
+                                                    : parked + ((int64_t)cta * W + (i >> 1)) * kRecord;
+                        v[k] = left ? *reinterpret_cast<const float2 *>(from + c * kStride + ch)
+                                    : make_float2(0.0f, 0.0f);
+                        left &= left - 1;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        o.x = fmaf(w[k], v[k].x, o.x);
+                        o.y = fmaf(w[k], v[k].y, o.y);
+                    }
+                }
+                if (complete && !goes_on) {
+                    int row, hq, i;
+                    if (!column(a, s, h, c, row, hq, i)) continue;
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                    write_pair<T>(a, row, hq, ch, o.x * inv, o.y * inv);
+                    if (a.lse && ch == 0) a.lse[(int64_t)row * a.Hq + hq] = lse_of(M - kShift, l);
+                } else {
+                    *reinterpret_cast<float2 *>(mine + c * kStride + ch) = o;
+                    if (ch == 0)
+                        *reinterpret_cast<float2 *>(mine + c * kStride + 128) = make_float2(M, l);
+                }
             }
-            if (complete) {
-                int row, hq, i;
-                if (!column(a, s, h, c, row, hq, i)) continue;
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                write_pair<T>(a, row, hq, ch, o.x * inv, o.y * inv);
-                if (a.lse && ch == 0) a.lse[(int64_t)row * a.Hq + hq] = lse_of(M - kShift, l);
-            } else {
-                *reinterpret_cast<float2 *>(mine + c * kStride + ch) = o;
-                if (ch == 0) *reinterpret_cast<float2 *>(mine + c * kStride + 128) = make_float2(M, l);
-            }
-        }
-        if (!complete) {
-            // CTAs first_cta .. last_cta share the unit; the last of them to come joins all
-            const int first_cta = (int)(((int64_t)(first + 1) * ncta - 1) / total);
-            const int last_cta = (int)(((int64_t)(first + s.np) * ncta - 1) / total);
+            if (complete || goes_on) continue;
+            // CTAs p0 .. p1 share the unit; the last of them to come joins all
+            const int p0 = (int)(((int64_t)(first + 1) * ncta - 1) / total);
+            const int p1 = (int)(((int64_t)(first + s.np) * ncta - 1) / total);
             __threadfence();
             __syncthreads();
-            if (tid == 0) sh.flag = atomicAdd(tickets + first_cta, 1) == last_cta - first_cta;
+            if (tid == 0) sh.flag = atomicAdd(tickets + p0, 1) == p1 - p0;
             __syncthreads();
             if (sh.flag) {
                 __threadfence();
-                for (int k = tid; k < cols * 64; k += kThreads) {
-                    const int c = k >> 6, ch = 2 * (k & 63);
+                for (int hc = warp; hc < 2 * cols; hc += W) {
+                    const int c = hc >> 1, ch = 64 * (hc & 1) + 2 * lane;
                     int row, hq, i;
                     if (!column(a, s, h, c, row, hq, i)) continue;
-                    const float *base0 = records + (int64_t)(2 * first_cta + 1) * cols * kStride +
-                                         c * kStride;
-                    const int64_t step = (int64_t)2 * cols * kStride;
-                    const int nrec = last_cta - first_cta + 1;
                     // record r > 0 is the first one of its CTA: one record back
-                    auto rec = [&](int r) { return base0 + r * step - (r ? cols * kStride : 0); };
+                    const float *rec0 = records + (int64_t)(4 * p0 + 1) * kRecord + c * kStride;
+                    auto rec = [&](int r) { return rec0 + (int64_t)(4 * r - (r ? 1 : 0)) * kRecord; };
+                    const int nrec = p1 - p0 + 1;
                     float M = -INFINITY;
-#pragma unroll 8
-                    for (int r = 0; r < nrec; r++) M = fmaxf(M, __ldcg(rec(r) + 128));
+                    for (int r = lane; r < nrec; r += 32) M = fmaxf(M, __ldcg(rec(r) + 128));
+                    M = warp_max(M);
                     float2 o = make_float2(0.0f, 0.0f);
                     float l = 0.0f;
-#pragma unroll 4
-                    for (int r = 0; r < nrec; r++) {
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(rec(r) + 128));
-                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(rec(r) + ch));
+                    for (int k0 = 0; k0 < nrec; k0 += 32) {
+                        float2 ml = make_float2(-INFINITY, 0.0f);
+                        if (k0 + lane < nrec)
+                            ml = __ldcg(reinterpret_cast<const float2 *>(rec(k0 + lane) + 128));
                         const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - M);
-                        o.x = fmaf(f, v.x, o.x);
-                        o.y = fmaf(f, v.y, o.y);
-                        l = fmaf(f, ml.y, l);
+                        l += warp_sum(f * ml.y);
+                        const int cnt = nrec - k0 < 32 ? nrec - k0 : 32;
+#pragma unroll 8
+                        for (int k = 0; k < cnt; k++) {
+                            const float w = __shfl_sync(0xffffffffu, f, k);
+                            const float2 v =
+                                __ldcg(reinterpret_cast<const float2 *>(rec(k0 + k) + ch));
+                            o.x = fmaf(w, v.x, o.x);
+                            o.y = fmaf(w, v.y, o.y);
+                        }
                     }
                     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                     write_pair<T>(a, row, hq, ch, o.x * inv, o.y * inv);
                     if (a.lse && ch == 0) a.lse[(int64_t)row * a.Hq + hq] = lse_of(M - kShift, l);
                 }
-                if (tid == 0) tickets[first_cta] = 0;  // ready for the next call
+                if (tid == 0) tickets[p0] = 0;  // ready for the next call
             }
             __syncthreads();
         }
-        i0 = i1;
+        __syncthreads();
     }
 }
 
 template <int NT, class T>
 cudaError_t launch(const AttnArgs &a, const Plan &pl, cudaStream_t stream) {
     static int smem_set[kMaxDevicesTracked];
-    constexpr int bytes = sizeof(Shared) + 128;
+    constexpr int bytes = sizeof(Shared<NT>) + 128;
     const cudaError_t e = raise_smem_limit(kv4_decode_kernel<NT, T>, bytes, smem_set);
     if (e != cudaSuccess) return e;
     char *ws = reinterpret_cast<char *>(a.err);
-    kv4_decode_kernel<NT, T><<<pl.ctas, kThreads, bytes, stream>>>(
+    kv4_decode_kernel<NT, T><<<pl.ctas, 32 * kWarpsOf<NT>, bytes, stream>>>(
         a, reinterpret_cast<float *>(ws + pl.parked), reinterpret_cast<float *>(ws + pl.records),
         reinterpret_cast<int *>(ws + pl.tickets));
     return cudaGetLastError();
@@ -677,7 +713,7 @@ cudaError_t launch(const AttnArgs &a, const Plan &pl, cudaStream_t stream) {
 }  // namespace
 
 size_t decode_record_bytes(int cols) { return (size_t)cols * kStride * sizeof(float); }
-int decode_warps() { return kWarps; }
+int decode_warps(int cols) { return cols == 8 ? kWarpsOf<1> : kWarpsOf<2>; }
 
 cudaError_t launch_decode(const AttnArgs &a, const Plan &pl, int dtype, cudaStream_t stream) {
     const bool bf16 = dtype == FFD_DTYPE_BF16;

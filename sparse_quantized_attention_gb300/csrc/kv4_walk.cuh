@@ -10,6 +10,7 @@ namespace kv4 {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kFar = 4194304.0f;  // 2^22: a reference from here on is off by more than 2^-2
 
 // One sequence as the walk sees it.
 struct Seq {

@@ -275,6 +275,9 @@ DECODE = [
     ("no_queries", dict(lens=[300, 200, 100], qlens=[0, 1, 0], Hkv=2, G=4)),
     ("many_short", dict(lens=[1 + 7 * i % 150 for i in range(300)], qlens=[1] * 300, Hkv=2, G=4)),
     ("long", dict(lens=[131072 - 5], qlens=[1], Hkv=1, G=4)),
+    ("windows", dict(lens=[300000, 5, 100000], qlens=[1, 1, 1], Hkv=2, G=4, splits=3)),
+    ("windows_mask", dict(lens=[300000, 5, 100000], qlens=[1, 3, 2], Hkv=2, G=4, keep=0.05,
+                          splits=1)),
     ("long_ragged", dict(lens=[60000, 100, 33333], qlens=[1, 1, 1], Hkv=4, G=7)),
 ]
 SEVERAL = [
@@ -289,6 +292,8 @@ SEVERAL = [
     ("chunk_window", dict(lens=[2000, 300], qlens=[190, 300], Hkv=1, G=5, window=77)),
     ("chunk_mask", dict(lens=[2000, 300], qlens=[190, 300], Hkv=2, G=4, keep=0.4)),
     ("chunk_peaked", dict(lens=[1500], qlens=[257], Hkv=1, G=4, q_scale=10.0)),
+    ("chunk_large_q", dict(lens=[500], qlens=[100], Hkv=1, G=4, q_scale=1e9)),
+    ("chunk_tiny_q", dict(lens=[500], qlens=[100], Hkv=1, G=4, q_scale=1e-20)),
     ("chunk_long", dict(lens=[20000], qlens=[64], Hkv=2, G=7)),
     ("tails", dict(lens=[100, 90], qlens=[20, 30], Hkv=2, G=4, tail=11, max_q=77)),
     ("mixed", dict(lens=[9000, 77, 600, 128], qlens=[1, 40, 0, 128], Hkv=2, G=6, stride_pad=8)),
@@ -297,9 +302,11 @@ SEVERAL = [
 
 @pytest.mark.parametrize("name,kw", DECODE + SEVERAL, ids=[c[0] for c in DECODE + SEVERAL])
 def test_attention(name, kw):
+    kw = dict(kw)
+    splits = kw.pop("splits", 0)
     c = Case(seed=len(name) + 1, **kw)
     c.poison_unused()
-    out, lse = c.run()
+    out, lse = c.run(num_splits=splits)
     c.check(out, lse)
 
 
