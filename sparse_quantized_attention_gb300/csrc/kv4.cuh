@@ -81,18 +81,6 @@ __device__ __forceinline__ float boundary_level(float x, float lo, float scale, 
     return (x > b || (x == b && odd)) ? lo + 1.0f : lo;
 }
 
-// Level of x: the quotient by a product with the reciprocal (relative error below 2^-21), rounded;
-// within 2e-5 of a boundary (31 * 2^-21 = 1.5e-5) the side is decided exactly.
-__device__ __forceinline__ uint32_t level(float x, float scale, float off, float inv) {
-    const float t = fminf(fmaxf(__fmul_rn(__fsub_rn(x, off), inv), 16.0f), 31.0f);
-    float r = rintf(t);
-    if (fabsf(t - r) > 0.5f - 2e-5f) {
-        const float lo = floorf(t);
-        r = boundary_level(x, lo, scale, off);
-    }
-    return static_cast<uint32_t>(static_cast<int>(r)) & 15u;
-}
-
 // Sequence of row t and the row's place in it, from the offsets cu [B+1] (or uniform rows per
 // sequence when cu is null). False when the row belongs to nobody.
 __device__ __forceinline__ bool row_of(const int32_t *cu, int B, int per, int t, int &b, int &i) {

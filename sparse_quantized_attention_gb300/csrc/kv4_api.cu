@@ -48,8 +48,7 @@ ffd_status check_rows(const ffd_cache_desc *cache, int32_t dtype, int32_t batch,
         !aligned(cu, 4) || !aligned(positions, 4) || !aligned(block_table, 4))
         return FFD_ERR_INVALID_ARG;
     if ((int64_t)max_blocks * kPage > INT32_MAX) return FFD_ERR_UNSUPPORTED;
-    // the launch's blocks of 256 threads, 16 threads a (row, KV head) at most
-    if ((int64_t)total * cache->num_kv_heads > (int64_t)INT32_MAX * 16) return FFD_ERR_UNSUPPORTED;
+    if (cache->num_kv_heads > 65535) return FFD_ERR_UNSUPPORTED;  // grid.y
     return FFD_OK;
 }
 

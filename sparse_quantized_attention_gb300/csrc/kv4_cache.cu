@@ -1,5 +1,6 @@
 // kv4_cache.cu -- writing rows into the 4-bit cache and reading them back (format in ffd.h).
 #include "kv4.cuh"
+#include "ptx.cuh"
 
 namespace ffd {
 namespace kv4 {
@@ -24,127 +25,174 @@ __device__ __forceinline__ bool place(const RowsArgs &a, int t, int &page, int &
     return !bad;
 }
 
-// One thread per (row, KV head, tensor, group of 32 channels).
-template <class T>
+// Code word of eight values x: nibble i + 4 e is value 2 i + e. The levels are quotients by products
+// with the reciprocal (relative error below 2^-21), rounded by adding 1.5 * 2^23 - 16, whose sum's
+// low bits are the level - 16; where one of the eight lies within 2e-5 of a boundary (31 * 2^-21 =
+// 1.5e-5) all are decided by the side of the boundary that x lies on.
+__device__ __forceinline__ uint32_t encode_word(const float *x, float s, float o, float inv) {
+    constexpr float kRound = 12582912.0f - 16.0f;
+    float t[8], u[8], off = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        t[i] = fminf(fmaxf(__fmul_rn(__fsub_rn(x[i], o), inv), 16.0f), 31.0f);
+        u[i] = __fadd_rn(t[i], kRound);
+        off = fmaxf(off, fabsf(__fsub_rn(t[i], __fsub_rn(u[i], kRound))));
+    }
+    if (off > 0.5f - 2e-5f) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const float lo = floorf(t[i]);
+            if (fabsf(t[i] - lo - 0.5f) < 2e-5f)
+                u[i] = __fadd_rn(boundary_level(x[i], lo, s, o), kRound);
+        }
+    }
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) w += __float_as_uint(u[i]) << (4 * ((i >> 1) + 4 * (i & 1)));
+    return w - 0x4b400000u * 0x11111111u;  // the sums' common part
+}
+
+// Writing: a block takes 32 rows of one KV head, a thread one group of 32 channels of K or of V. The
+// eight threads of a row sit together and rows follow one another, so a prompt's records are written
+// in whole lines.
+template <class T, bool kWide>
 __global__ void __launch_bounds__(256) kv4_write_kernel(const RowsArgs a, const uint16_t *k,
                                                         const uint16_t *v, uint8_t *k4,
                                                         uint8_t *v4) {
-    const int64_t item = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    const int g = (int)(item & 3);
-    const bool is_v = (item >> 2) & 1;
-    const int64_t th = item >> 3;
-    const int t = (int)(th / a.Hkv), h = (int)(th - (int64_t)t * a.Hkv);
+    const int g = threadIdx.x & 3;
+    const bool is_v = (threadIdx.x >> 2) & 1;
+    const int t = blockIdx.x * 32 + (threadIdx.x >> 3), h = blockIdx.y;
     if (t >= a.T) return;
+    const uint16_t *row = (is_v ? v + t * a.v_stride : k + t * a.k_stride) + h * kD + g * 32;
+    uint32_t w[16];
+    if (kWide) {
+        load_32b(row, reinterpret_cast<uint32_t(&)[8]>(w[0]));
+        load_32b(row + 16, reinterpret_cast<uint32_t(&)[8]>(w[8]));
+    } else {
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(row) + c);
+            w[4 * c] = u.x;
+            w[4 * c + 1] = u.y;
+            w[4 * c + 2] = u.z;
+            w[4 * c + 3] = u.w;
+        }
+    }
     int page, r;
     bool bad;
     if (!place(a, t, page, r, bad)) {
         if (bad) raise_error(a.err, FFD_ERRBIT_BOUNDS);
         return;
     }
-    const uint16_t *src = is_v ? v + t * a.v_stride : k + t * a.k_stride;
-    const uint4 *row = reinterpret_cast<const uint4 *>(src + h * kD + g * 32);
     float x[32];
+    float lo = INFINITY, hi = -INFINITY, sum = 0.0f;
 #pragma unroll
-    for (int c = 0; c < 4; c++) {
-        const uint4 u = __ldg(row + c);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const float2 f = T::unpack(w[j]);
-            x[8 * c + 2 * j] = f.x;
-            x[8 * c + 2 * j + 1] = f.y;
-        }
+    for (int j = 0; j < 16; j++) {
+        const float2 f = T::unpack(w[j]);
+        x[2 * j] = f.x;
+        x[2 * j + 1] = f.y;
+        lo = fminf(lo, fminf(f.x, f.y));
+        hi = fmaxf(hi, fmaxf(f.x, f.y));
+        sum += f.x * 0.0f + f.y * 0.0f;  // NaN when one of them is NaN or infinite
     }
-    float lo = x[0], hi = x[0];
-    bool range = false;
-#pragma unroll
-    for (int c = 0; c < 32; c++) {
-        lo = fminf(lo, x[c]);
-        hi = fmaxf(hi, x[c]);
-        range |= !(fabsf(x[c]) <= kMaxInput);
-    }
-    if (range) raise_error(a.err, FFD_ERRBIT_RANGE);
+    if (!(lo >= -kMaxInput && hi <= kMaxInput && sum == 0.0f)) raise_error(a.err, FFD_ERRBIT_RANGE);
     const __half hs = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
     const float s = __half2float(hs);
     const __half ho = __float2half_rn(__fmaf_rn(-16.0f, s, lo));
     const float o = __half2float(ho);
     const float inv = s > 0.0f ? __frcp_rn(s) : 0.0f;  // 0: every level clamps to 16
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        w[j] = 0;
-#pragma unroll
-        for (int i = 0; i < 8; i++)
-            w[j] |= level(x[8 * j + i], s, o, inv) << (4 * ((i >> 1) + 4 * (i & 1)));
-    }
     uint8_t *rec = (is_v ? v4 : k4) + ((int64_t)page * a.Hkv + h) * kRec;
-    *reinterpret_cast<uint4 *>(rec + code_offset(r, g)) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(rec + code_offset(r, g)) =
+        make_uint4(encode_word(x, s, o, inv), encode_word(x + 8, s, o, inv),
+                   encode_word(x + 16, s, o, inv), encode_word(x + 24, s, o, inv));
     *reinterpret_cast<__half2 *>(rec + param_offset(r, g)) = __halves2half2(hs, ho);
 }
 
-// One thread per (row, KV head, word of 8 channels).
-template <class T>
+// Reading: a block takes 64 rows of one KV head, a thread sixteen channels of two rows (32 apart), of
+// K and of V.
+constexpr int kReadRows = 64;
+template <class T, bool kWide>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const RowsArgs a, const uint8_t *k4,
                                                        const uint8_t *v4, uint16_t *k,
                                                        uint16_t *v) {
-    const int64_t item = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    const int J = (int)(item & 15);
-    const int64_t th = item >> 4;
-    const int t = (int)(th / a.Hkv), h = (int)(th - (int64_t)t * a.Hkv);
-    if (t >= a.T) return;
-    int page, r;
-    bool bad;
-    const bool ok = place(a, t, page, r, bad);
-    if (!ok && !bad) return;
-    if (bad) raise_error(a.err, FFD_ERRBIT_BOUNDS);
+    const int c = threadIdx.x & 7, h = blockIdx.y;  // channels 16 c .. 16 c + 15
+    int t[2];
+    bool ok[2], mine[2];
+    uint2 code[2][2];
+    uint32_t par[2][2];
 #pragma unroll
-    for (int which = 0; which < 2; which++) {
-        uint16_t *dst = which ? (v ? v + t * a.v_stride : nullptr)
-                              : (k ? k + t * a.k_stride : nullptr);
-        if (!dst) continue;
-        uint4 o = make_uint4(0, 0, 0, 0);
-        if (ok) {
-            const uint8_t *rec = (which ? v4 : k4) + ((int64_t)page * a.Hkv + h) * kRec;
-            const uint32_t w =
-                __ldg(reinterpret_cast<const uint32_t *>(rec + code_offset(r, J >> 2)) + (J & 3));
-            const uint32_t pw =
-                __ldg(reinterpret_cast<const uint32_t *>(rec + param_offset(r, J >> 2)));
-            __half2 val[4];
-            decode_word(w, *reinterpret_cast<const __half2 *>(&pw), val);
-            o = make_uint4(T::from_half2(val[0]), T::from_half2(val[1]), T::from_half2(val[2]),
-                           T::from_half2(val[3]));
+    for (int i = 0; i < 2; i++) {
+        t[i] = blockIdx.x * kReadRows + 32 * i + (threadIdx.x >> 3);
+        int page = 0, r = 0;
+        bool bad = false;
+        ok[i] = t[i] < a.T && place(a, t[i], page, r, bad);
+        mine[i] = ok[i] || bad;
+        if (bad) raise_error(a.err, FFD_ERRBIT_BOUNDS);
+        const int64_t at = ((int64_t)page * a.Hkv + h) * kRec;
+        const int co = code_offset(r, c >> 1) + 8 * (c & 1), po = param_offset(r, c >> 1);
+#pragma unroll
+        for (int w = 0; w < 2; w++) {
+            const uint8_t *rec = (w ? v4 : k4) + at;
+            const bool want = ok[i] && (w ? v != nullptr : k != nullptr);
+            code[i][w] = want ? __ldg(reinterpret_cast<const uint2 *>(rec + co)) : make_uint2(0, 0);
+            par[i][w] = want ? __ldg(reinterpret_cast<const uint32_t *>(rec + po)) : 0u;
         }
-        *reinterpret_cast<uint4 *>(dst + h * kD + 8 * J) = o;
     }
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        if (!mine[i]) continue;  // a page out of range: zeros
+#pragma unroll
+        for (int w = 0; w < 2; w++) {
+            uint16_t *dst = w ? v : k;
+            if (!dst) continue;
+            dst += t[i] * (w ? a.v_stride : a.k_stride) + h * kD + 16 * c;
+            const __half2 p = *reinterpret_cast<const __half2 *>(&par[i][w]);
+            __half2 x[8];
+            decode_word(code[i][w].x, p, reinterpret_cast<__half2(&)[4]>(x[0]));
+            decode_word(code[i][w].y, p, reinterpret_cast<__half2(&)[4]>(x[4]));
+            uint32_t o[8];
+#pragma unroll
+            for (int e = 0; e < 8; e++) o[e] = T::from_half2(x[e]);
+            if (kWide) {
+                store_32b(dst, o);
+            } else {
+                reinterpret_cast<uint4 *>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                reinterpret_cast<uint4 *>(dst)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+        }
+    }
+}
+
+// Rows of 32-byte accesses: aligned base and stride (of the tensors that are there).
+bool wide(const void *k, int64_t ks, const void *v, int64_t vs) {
+    const bool kw = !k || ((reinterpret_cast<uintptr_t>(k) & 31) == 0 && ks % 16 == 0);
+    const bool vw = !v || ((reinterpret_cast<uintptr_t>(v) & 31) == 0 && vs % 16 == 0);
+    return kw && vw;
 }
 
 }  // namespace
 
 cudaError_t launch_write(const RowsArgs &a, int dtype, const void *k, const void *v, uint8_t *k4,
                          uint8_t *v4, cudaStream_t stream) {
-    const int64_t items = (int64_t)a.T * a.Hkv * 8;
-    if (items == 0) return cudaSuccess;
-    const int64_t grid = (items + 255) / 256;
-    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    if (a.T == 0) return cudaSuccess;
+    const dim3 grid((a.T + 31) / 32, a.Hkv);
     auto *kp = static_cast<const uint16_t *>(k), *vp = static_cast<const uint16_t *>(v);
-    if (dtype == FFD_DTYPE_BF16)
-        kv4_write_kernel<Bf16><<<(unsigned)grid, 256, 0, stream>>>(a, kp, vp, k4, v4);
-    else
-        kv4_write_kernel<F16><<<(unsigned)grid, 256, 0, stream>>>(a, kp, vp, k4, v4);
+    const bool w = wide(k, a.k_stride, v, a.v_stride);
+    auto run = [&](auto kernel) { kernel<<<grid, 256, 0, stream>>>(a, kp, vp, k4, v4); };
+    if (dtype == FFD_DTYPE_BF16) run(w ? kv4_write_kernel<Bf16, true> : kv4_write_kernel<Bf16, false>);
+    else run(w ? kv4_write_kernel<F16, true> : kv4_write_kernel<F16, false>);
     return cudaGetLastError();
 }
 
 cudaError_t launch_read(const RowsArgs &a, int dtype, const uint8_t *k4, const uint8_t *v4, void *k,
                         void *v, cudaStream_t stream) {
-    const int64_t items = (int64_t)a.T * a.Hkv * 16;
-    if (items == 0) return cudaSuccess;
-    const int64_t grid = (items + 255) / 256;
-    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    if (a.T == 0) return cudaSuccess;
+    const dim3 grid((a.T + kReadRows - 1) / kReadRows, a.Hkv);
     auto *kp = static_cast<uint16_t *>(k), *vp = static_cast<uint16_t *>(v);
-    if (dtype == FFD_DTYPE_BF16)
-        kv4_read_kernel<Bf16><<<(unsigned)grid, 256, 0, stream>>>(a, k4, v4, kp, vp);
-    else
-        kv4_read_kernel<F16><<<(unsigned)grid, 256, 0, stream>>>(a, k4, v4, kp, vp);
+    const bool w = wide(k, a.k_stride, v, a.v_stride);
+    auto run = [&](auto kernel) { kernel<<<grid, 256, 0, stream>>>(a, k4, v4, kp, vp); };
+    if (dtype == FFD_DTYPE_BF16) run(w ? kv4_read_kernel<Bf16, true> : kv4_read_kernel<Bf16, false>);
+    else run(w ? kv4_read_kernel<F16, true> : kv4_read_kernel<F16, false>);
     return cudaGetLastError();
 }
 
