@@ -50,7 +50,7 @@ struct Shared {
     int pre[32 * W];                  // items before each thread's chunk of sequences
     int scan[W];
     int unit[W][2], first[W][2];      // of a warp's parked and of its last state (unit -1: none)
-    int flag;
+    int flag[2];
 };
 static_assert(sizeof(Shared<1>) + 128 <= 232448 && sizeof(Shared<2>) + 128 <= 232448,
               "shared memory per CTA");
@@ -415,7 +415,9 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
         __syncthreads();
 
         // ---- this warp's share of the list ----------------------------------------------------
-        const int i0 = count * warp / W, i1 = count * (warp + 1) / W;
+        // (the first warps take the odd ones: neighbours lie on different schedulers)
+        const int each = count / W, odd = count - each * W;
+        const int i0 = each * warp + (warp < odd ? warp : odd), i1 = i0 + each + (warp < odd);
         auto next = [&](int i) {  // the next page to fetch from i on, i1 when there is none
             while (i < i1 && sh.list[i].rec < 0) i++;
             return i;
@@ -579,18 +581,21 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
         }
         __syncthreads();
 
-        // ---- join the warps' states of each unit, then the ranges' ----------------------------
-        // Lane i has entry i: warp i / 2, parked (even) or last (odd). A warp takes half a column.
+        // ---- join the warps' states of each unit, then the CTAs' ------------------------------
+        // Lane i has entry i: warp i / 2, parked (even) or last (odd); `same` are the entries of its
+        // unit. A warp takes half a column of a unit at a time.
         const int eu = lane < 2 * W ? sh.unit[lane >> 1][lane & 1] : -1;
         const int ef = lane < 2 * W ? sh.first[lane >> 1][lane & 1] : 0;
-        const float *es = (lane & 1) ? reinterpret_cast<const float *>(sh.ring[(lane >> 1) % W])
-                                     : parked + ((int64_t)cta * W + (lane >> 1) % W) * kRecord;
-        for (uint32_t todo = __ballot_sync(0xffffffffu, eu >= 0); todo;) {
-            const int lead = __ffs(todo) - 1;
+        const float *waiting = parked + (int64_t)cta * W * kRecord;
+        auto last_state = [&](int w) { return reinterpret_cast<const float *>(sh.ring[w]); };
+        const uint32_t same = __match_any_sync(0xffffffffu, eu);
+        const uint32_t leads = __ballot_sync(0xffffffffu, eu >= 0 && __ffs(same) - 1 == lane);
+        uint32_t units = leads;
+        for (int k = 0; units; k++, units &= units - 1) {
+            const int lead = __ffs(units) - 1;
             const int u = __shfl_sync(0xffffffffu, eu, lead);
             const int first = __shfl_sync(0xffffffffu, ef, lead);
-            const uint32_t run = __ballot_sync(0xffffffffu, eu == u);
-            todo &= ~run;
+            const uint32_t run = __shfl_sync(0xffffffffu, same, lead);
             const int b = u / a.Hkv, h = u - b * a.Hkv;
             const Seq s = seq_of(a, b, false);
             const bool carried = first < w0 && w0 > r0;            // from the window before
@@ -598,10 +603,15 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
             const bool begins = first >= r0, complete = begins && first + s.np <= r1;
             const float *carry = records + (int64_t)(4 * cta + 2 + (turn ^ 1)) * kRecord;
             float *mine = records + (int64_t)(4 * cta + (goes_on ? 2 + turn : begins)) * kRecord;
-            for (int hc = warp; hc < 2 * cols; hc += W) {
+            // units begin at different warps, so that a CTA of many of them keeps all warps busy
+            for (int hc = (warp + k * (W / 2)) % W; hc < 2 * cols; hc += W) {
                 const int c = hc >> 1, ch = 64 * (hc & 1) + 2 * lane;
                 float2 ml = make_float2(-INFINITY, 0.0f);
-                if (eu == u) ml = *reinterpret_cast<const float2 *>(es + c * kStride + 128);
+                if (eu == u && (lane & 1))
+                    ml = *reinterpret_cast<const float2 *>(last_state(lane >> 1) + c * kStride + 128);
+                if (eu == u && !(lane & 1))
+                    ml = *reinterpret_cast<const float2 *>(waiting + (lane >> 1) * kRecord +
+                                                           c * kStride + 128);
                 float M = warp_max(ml.x);
                 float2 cm = make_float2(-INFINITY, 0.0f), o = make_float2(0.0f, 0.0f);
                 if (carried) {
@@ -614,24 +624,30 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                 const float l = fmaf(cf, cm.y, warp_sum(f * ml.y));
                 o.x *= cf;
                 o.y *= cf;
-                uint32_t left = run;
-                while (left) {
+                for (uint32_t left = run & 0x55555555u; left; left &= left - 1) {
+                    const int i = __ffs(left) - 1;
+                    const float w = __shfl_sync(0xffffffffu, f, i);
+                    const float2 v = *reinterpret_cast<const float2 *>(
+                        waiting + (i >> 1) * kRecord + c * kStride + ch);
+                    o.x = fmaf(w, v.x, o.x);
+                    o.y = fmaf(w, v.y, o.y);
+                }
+                for (uint32_t left = run & 0xaaaaaaaau; left;) {
                     float2 v[4];
                     float w[4];
 #pragma unroll
-                    for (int k = 0; k < 4; k++) {  // four states' loads at a time
-                        const int i = left ? __ffs(left) - 1 : 0;
-                        w[k] = left ? __shfl_sync(0xffffffffu, f, i) : 0.0f;
-                        const float *from = (i & 1) ? reinterpret_cast<const float *>(sh.ring[i >> 1])
-                                                    : parked + ((int64_t)cta * W + (i >> 1)) * kRecord;
-                        v[k] = left ? *reinterpret_cast<const float2 *>(from + c * kStride + ch)
-                                    : make_float2(0.0f, 0.0f);
+                    for (int n = 0; n < 4; n++) {  // four states' loads at a time
+                        const int i = left ? __ffs(left) - 1 : 1;
+                        w[n] = __shfl_sync(0xffffffffu, f, i);
+                        if (!left) w[n] = 0.0f;
+                        v[n] = *reinterpret_cast<const float2 *>(last_state(i >> 1) + c * kStride + ch);
+                        if (!left) v[n] = make_float2(0.0f, 0.0f);
                         left &= left - 1;
                     }
 #pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        o.x = fmaf(w[k], v[k].x, o.x);
-                        o.y = fmaf(w[k], v[k].y, o.y);
+                    for (int n = 0; n < 4; n++) {
+                        o.x = fmaf(w[n], v[n].x, o.x);
+                        o.y = fmaf(w[n], v[n].y, o.y);
                     }
                 }
                 if (complete && !goes_on) {
@@ -646,16 +662,55 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                         *reinterpret_cast<float2 *>(mine + c * kStride + 128) = make_float2(M, l);
                 }
             }
-            if (complete || goes_on) continue;
-            // CTAs p0 .. p1 share the unit; the last of them to come joins all
-            const int p0 = (int)(((int64_t)(first + 1) * ncta - 1) / total);
-            const int p1 = (int)(((int64_t)(first + s.np) * ncta - 1) / total);
-            __threadfence();
+        }
+        // Units that other CTAs share, the first and the last at most: the last CTA to come joins
+        // their records (complete by the barrier and the ticket). One warp takes each ticket.
+        __syncthreads();
+        uint32_t shared_units = 0;
+        for (units = leads; units; units &= units - 1) {
+            const int lead = __ffs(units) - 1;
+            const int u = __shfl_sync(0xffffffffu, eu, lead);
+            const int first = __shfl_sync(0xffffffffu, ef, lead);
+            if (first >= r0) {  // it begins here: nobody else's when it ends here
+                const int end = first + seq_of(a, u / a.Hkv, false).np;
+                if (end <= r1 || w1 < r1) continue;
+            } else if (w1 < r1 && first + seq_of(a, u / a.Hkv, false).np > w1) {
+                continue;  // goes on in the next window
+            }
+            shared_units |= 1u << lead;
+        }
+        if (shared_units == 0) {
             __syncthreads();
-            if (tid == 0) sh.flag = atomicAdd(tickets + p0, 1) == p1 - p0;
-            __syncthreads();
-            if (sh.flag) {
-                __threadfence();
+            continue;
+        }
+        {
+            const uint32_t mine = warp == 0 ? shared_units : warp == 1 ? shared_units & (shared_units - 1) : 0;
+            if (mine) {
+                const int lead = __ffs(mine) - 1;
+                const int u = __shfl_sync(0xffffffffu, eu, lead);
+                const int first = __shfl_sync(0xffffffffu, ef, lead);
+                const int np = seq_of(a, u / a.Hkv, false).np;
+                const int p0 = (int)(((int64_t)(first + 1) * ncta - 1) / total);
+                const int p1 = (int)(((int64_t)(first + np) * ncta - 1) / total);
+                if (lane == 0) {
+                    const bool last = add_acq_rel_gpu(tickets + p0, 1) == p1 - p0;
+                    if (last) tickets[p0] = 0;  // ready for the next call
+                    sh.flag[warp] = last;
+                }
+            }
+        }
+        __syncthreads();
+        for (int k = 0; shared_units; k++, shared_units &= shared_units - 1) {
+            if (sh.flag[k]) {
+                const int lead = __ffs(shared_units) - 1;
+                const int u = __shfl_sync(0xffffffffu, eu, lead);
+                const int first = __shfl_sync(0xffffffffu, ef, lead);
+                const int b = u / a.Hkv, h = u - b * a.Hkv;
+                const Seq s = seq_of(a, b, false);
+                // CTAs p0 .. p1
+                const int p0 = (int)(((int64_t)(first + 1) * ncta - 1) / total);
+                const int p1 = (int)(((int64_t)(first + s.np) * ncta - 1) / total);
+                const int nrec = p1 - p0 + 1;
                 for (int hc = warp; hc < 2 * cols; hc += W) {
                     const int c = hc >> 1, ch = 64 * (hc & 1) + 2 * lane;
                     int row, hq, i;
@@ -663,18 +718,19 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                     // record r > 0 is the first one of its CTA: one record back
                     const float *rec0 = records + (int64_t)(4 * p0 + 1) * kRecord + c * kStride;
                     auto rec = [&](int r) { return rec0 + (int64_t)(4 * r - (r ? 1 : 0)) * kRecord; };
-                    const int nrec = p1 - p0 + 1;
-                    float M = -INFINITY;
-                    for (int r = lane; r < nrec; r += 32) M = fmaxf(M, __ldcg(rec(r) + 128));
-                    M = warp_max(M);
+                    float M = -INFINITY, l = 0.0f;
                     float2 o = make_float2(0.0f, 0.0f);
-                    float l = 0.0f;
-                    for (int k0 = 0; k0 < nrec; k0 += 32) {
+                    for (int k0 = 0; k0 < nrec; k0 += 32) {  // a running join, 32 records a round
                         float2 ml = make_float2(-INFINITY, 0.0f);
                         if (k0 + lane < nrec)
                             ml = __ldcg(reinterpret_cast<const float2 *>(rec(k0 + lane) + 128));
-                        const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - M);
-                        l += warp_sum(f * ml.y);
+                        const float Mn = fmaxf(M, warp_max(ml.x));
+                        const float al = M == -INFINITY ? 0.0f : ex2_approx(M - Mn);
+                        const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - Mn);
+                        M = Mn;
+                        l = fmaf(al, l, warp_sum(f * ml.y));
+                        o.x *= al;
+                        o.y *= al;
                         const int cnt = nrec - k0 < 32 ? nrec - k0 : 32;
 #pragma unroll 8
                         for (int k = 0; k < cnt; k++) {
@@ -689,9 +745,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                     write_pair<T>(a, row, hq, ch, o.x * inv, o.y * inv);
                     if (a.lse && ch == 0) a.lse[(int64_t)row * a.Hq + hq] = lse_of(M - kShift, l);
                 }
-                if (tid == 0) tickets[p0] = 0;  // ready for the next call
             }
-            __syncthreads();
         }
         __syncthreads();
     }

@@ -64,6 +64,17 @@ __device__ __forceinline__ int ld_acquire_gpu(const int *p) {
     return v;
 }
 
+// Add at GPU scope that publishes what this thread knows to be written and sees what the threads that
+// added before it published.
+__device__ __forceinline__ int add_acq_rel_gpu(int *p, int v) {
+    int r;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;"
+                 : "=r"(r)
+                 : "l"(p), "r"(v)
+                 : "memory");
+    return r;
+}
+
 // Nanosecond wall clock of the GPU.
 __device__ __forceinline__ uint64_t globaltimer_ns() {
     uint64_t t;
