@@ -125,7 +125,7 @@ struct AttnArgs {
 
 // Launch shape and workspace of an attention call (byte offsets behind the error word).
 struct Plan {
-    int cols;  // query columns of the decode kernel (8 or 16), 0: the chunk kernel
+    int cols;  // query columns of the decode kernel (8, 16, 24 or 32), 0: the chunk kernel
     int ctas;
     size_t tickets, records, parked, total;
 };

@@ -108,7 +108,7 @@ ffd_status make_plan(const ffd_kv4_params *p, Plan *pl) {
     const ffd_status st = check_params(p);
     if (st != FFD_OK) return st;
     const int64_t rows = (int64_t)p->max_q_len * (p->num_q_heads / p->num_kv_heads);
-    pl->cols = rows <= 8 ? 8 : rows <= 16 ? 16 : 0;
+    pl->cols = rows <= 32 ? (int)(rows + 7) / 8 * 8 : 0;
     const int sms = current_sm_count();
     int64_t pages = (int64_t)p->batch * p->num_kv_heads * p->max_blocks_per_seq;
     if (!pl->cols) pages *= (rows + chunk_rows() - 1) / chunk_rows();

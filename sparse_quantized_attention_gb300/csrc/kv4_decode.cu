@@ -1,5 +1,5 @@
 // kv4_decode.cu -- attention over the 4-bit cache for few query rows: up to 8 NT (row, head) pairs
-// share a KV head (NT = 1: one decode token of any GQA group; NT = 2: up to 16 pairs).
+// share a KV head (NT = 1: one decode token of any GQA group; NT = 2 and 4: drafted tokens).
 //
 // The definition is the one of ffd.h. The pages of all (sequence, KV head) units, concatenated, are
 // cut into equal contiguous ranges, one per CTA (more when a range would not fit its list). The CTA
@@ -15,8 +15,9 @@
 // shared memory, and the last CTA of a unit joins those of the CTAs (order fixed by page, so the
 // result does not depend on arrival).
 //
-// P is rounded to f16 against a reference of 2^14, so probabilities down to 2^-28 of the largest
-// keep all 11 bits. q enters as f16 scaled by a power of two per column (its largest magnitude in
+// P is rounded to f16 with 2^7 at the reference, so probabilities down to 2^-21 of it keep all 11
+// bits (and down to 2^-31 some). The reference follows the maximum lazily, which saves the rescaling
+// that a new maximum in any of a warp's columns would cost nearly every time. q enters as f16 scaled by a power of two per column (its largest magnitude in
 // [2^13, 2^14)): exact for bf16 and f16 queries apart from elements below 2^-27 of the largest.
 #include "kv4_walk.cuh"
 
@@ -25,13 +26,18 @@ namespace kv4 {
 namespace {
 
 constexpr int kSlot = 2 * kRec;       // a warp's K record and V record
-constexpr int kStride = 130;          // floats of a joined column: o[128], m, l
-constexpr float kShift = 14.0f;       // P carries 2^14
+constexpr int kStride = 132;          // floats of a joined column: o[128], m, l, two unused
+constexpr float kShift = 7.0f;        // P carries 2^7, and at most 2^15: a column's reference m is
+constexpr float kLazy = 8.0f;         // raised only when a score passes it by 2^8
 constexpr int kWindow = 2048;         // pages of a CTA's list
 
-// Warps of a CTA: what their registers allow (128 a thread for one column tile, 168 for two).
+// Warps of a CTA: what their registers allow (128 a thread for one column tile, 168 for two, 204
+// for three, 255 for four), and the 16-token tiles that a warp takes together: the more column tiles, the fewer tokens
+// it needs for its matrix instructions not to wait on one another.
 template <int NT>
-constexpr int kWarpsOf = NT == 1 ? 16 : 12;
+constexpr int kWarpsOf = NT == 1 ? 16 : NT == 2 ? 12 : 8;
+template <int NT>
+constexpr int kTogether = NT == 1 ? 4 : NT <= 3 ? 2 : 1;
 
 // A page of a range's list.
 struct Entry {
@@ -44,7 +50,8 @@ struct Entry {
 template <int NT>
 struct Shared {
     static constexpr int W = kWarpsOf<NT>;
-    uint8_t ring[W][kSlot];           // later each warp's last state
+    // a warp's K record and V record, later its last state
+    uint8_t ring[W][kSlot > 8 * NT * kStride * 4 ? kSlot : (8 * NT * kStride * 4 + 15) / 16 * 16];
     Entry list[kWindow];
     uint64_t full[W][2];
     int pre[32 * W];                  // items before each thread's chunk of sequences
@@ -52,7 +59,8 @@ struct Shared {
     int unit[W][2], first[W][2];      // of a warp's parked and of its last state (unit -1: none)
     int flag[2];
 };
-static_assert(sizeof(Shared<1>) + 128 <= 232448 && sizeof(Shared<2>) + 128 <= 232448,
+static_assert(sizeof(Shared<1>) + 128 <= 232448 && sizeof(Shared<2>) + 128 <= 232448 &&
+                  sizeof(Shared<3>) + 128 <= 232448 && sizeof(Shared<4>) + 128 <= 232448,
               "shared memory per CTA");
 
 // Softmax state of a warp: columns 2 tig, 2 tig + 1 of each 8-column tile (tig = lane % 4). m is the
@@ -133,18 +141,15 @@ __device__ __forceinline__ void load_queries(const AttnArgs &a, const Seq &s, in
     }
 }
 
-// Scores of one page: x[t][4 tile + r] as in the matrix instruction's result (rows g, g + 8 of the
-// page's 16-token tile, columns 2 tig, 2 tig + 1). K of a row: the lane holds group tig of rows g and
-// g + 8 of a tile, 16 code bytes and one (scale, off) pair each.
-template <int NT>
-__device__ __forceinline__ void page_scores(const uint8_t *k, int lane, const uint32_t (&qf)[NT][16],
-                                            float (&x)[NT][4][4]) {
-    const int g = lane >> 2, tig = lane & 3;
-    const uint8_t *codes = k + (g >> 1) * 128 + (((2 * (g & 1) + (tig >> 1)) ^ (g >> 1)) << 5) +
-                           (tig & 1) * 16;
-    const uint8_t *par = k + kParamOff + 16 * g + 4 * tig;
+// Scores of TT 16-token tiles of a page: x[t][tile] as in the matrix instruction's result (rows g,
+// g + 8 of the tile, columns 2 tig, 2 tig + 1). K of a row: the lane holds group tig of rows g and
+// g + 8 of a tile, 16 code bytes and one (scale, off) pair each; codes and par point at row g's of the
+// first tile.
+template <int NT, int TT>
+__device__ __forceinline__ void tile_scores(const uint8_t *codes, const uint8_t *par,
+                                            const uint32_t (&qf)[NT][16], float (&x)[NT][TT][4]) {
 #pragma unroll
-    for (int tile = 0; tile < 4; tile++) {
+    for (int tile = 0; tile < TT; tile++) {
         const uint4 c0 = *reinterpret_cast<const uint4 *>(codes + tile * 1024);
         const uint4 c1 = *reinterpret_cast<const uint4 *>(codes + tile * 1024 + 512);
         const __half2 p0 = *reinterpret_cast<const __half2 *>(par + tile * 256);
@@ -168,18 +173,16 @@ __device__ __forceinline__ void page_scores(const uint8_t *k, int lane, const ui
     }
 }
 
-// Value pairs (tokens of the low and the high half) of nibble pair i of prmt'ed code words.
-template <int NT>
-__device__ __forceinline__ void page_values(const uint8_t *v, int lane, int valid,
-                                            const uint32_t (&pf)[NT][4][2], State<NT> &st) {
-    const int g = lane >> 2, tig = lane & 3;
-    const uint8_t *par = v + kParamOff + 32 * tig + 4 * (g >> 1);
-    const uint8_t *codes[2];
+// O^T += V^T P^T over TT tiles. The lane holds words 2 g, 2 g + 1 of tokens 2 tig, 2 tig + 1 of a tile
+// and of the two eight further on: codes[e] and par point at token 2 tig (+ e for the codes) of the
+// first tile. Tokens from `valid` on (counted from token 2 tig) hold anything and count as 0. A
+// permutation of bytes puts two tokens' nibbles of one channel into one register's halves.
+template <int NT, int TT>
+__device__ __forceinline__ void tile_values(const uint8_t *const (&codes)[2], const uint8_t *par,
+                                            int valid, const uint32_t (&pf)[NT][TT][2],
+                                            State<NT> &st) {
 #pragma unroll
-    for (int e = 0; e < 2; e++)
-        codes[e] = v + tig * 128 + (((2 * e + (g >> 2)) ^ tig) << 5) + ((g >> 1) & 1) * 16 + (g & 1) * 8;
-#pragma unroll
-    for (int tile = 0; tile < 4; tile++) {
+    for (int tile = 0; tile < TT; tile++) {
         // [half of the tile] token pairs 16 tile + 8 half + 2 tig, + 1
         uint32_t s[2], o[2];
         uint2 c[2][2];
@@ -187,11 +190,8 @@ __device__ __forceinline__ void page_values(const uint8_t *v, int lane, int vali
         for (int hi = 0; hi < 2; hi++) {
             uint32_t q0 = *reinterpret_cast<const uint32_t *>(par + tile * 256 + hi * 128);
             uint32_t q1 = *reinterpret_cast<const uint32_t *>(par + tile * 256 + hi * 128 + 16);
-            if (valid < kPage) {  // tokens past the sequence hold anything: make them 0
-                const int r = 16 * tile + 8 * hi + 2 * tig;
-                q0 = r < valid ? q0 : 0u;
-                q1 = r + 1 < valid ? q1 : 0u;
-            }
+            q0 = 16 * tile + 8 * hi < valid ? q0 : 0u;
+            q1 = 16 * tile + 8 * hi + 1 < valid ? q1 : 0u;
             s[hi] = __byte_perm(q0, q1, 0x5410);
             o[hi] = __byte_perm(q0, q1, 0x7632);
 #pragma unroll
@@ -257,6 +257,18 @@ __device__ __forceinline__ void write_direct(const AttnArgs &a, const Seq &s, in
             dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
             if (a.lse && g == 0) a.lse[(int64_t)row * a.Hq + hq] = lse_of(st.m[t][e] - kShift, l);
         }
+}
+
+__device__ __forceinline__ float4 scaled(float4 v, float f) {
+    return make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+}
+__device__ __forceinline__ float4 plus(float4 o, float f, float4 v) {
+    return make_float4(fmaf(f, v.x, o.x), fmaf(f, v.y, o.y), fmaf(f, v.z, o.z), fmaf(f, v.w, o.w));
+}
+template <class T>
+__device__ __forceinline__ void write_four(const AttnArgs &a, int row, int hq, int ch, float4 v) {
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + ((int64_t)row * a.Hq + hq) * kD + ch) =
+        make_uint2(T::pack(v.x, v.y), T::pack(v.z, v.w));
 }
 
 // A warp's state as 8 NT columns of kStride floats.
@@ -359,6 +371,12 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
     __syncthreads();
 
     uint8_t *kbuf = sh.ring[warp], *vbuf = kbuf + kRec;
+    // where this lane's parts of a tile's K and V stand (rows 16 tile + ...)
+    const int g = lane >> 2, tig = lane & 3;
+    const uint8_t *kcodes = kbuf + code_offset(g, tig), *kpar = kbuf + param_offset(g, tig);
+    const uint8_t *const vcodes[2] = {vbuf + code_offset(2 * tig, g >> 1) + 8 * (g & 1),
+                                      vbuf + code_offset(2 * tig + 1, g >> 1) + 8 * (g & 1)};
+    const uint8_t *vpar = vbuf + param_offset(2 * tig, g >> 1);
     uint64_t *kfull = &sh.full[warp][0], *vfull = &sh.full[warp][1];
     uint32_t taken = 0;  // pages this warp has finished
     bool dead = false;
@@ -455,101 +473,109 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                 if (e.unit != unit) break;
                 if (e.rec < 0 || dead) continue;
                 const int ni = next(i + 1);
-                wait_copy(a, kfull, taken & 1, dead);
-                dead = __any_sync(0xffffffffu, dead);
-                float sc[NT][4][4];
-                page_scores<NT>(kbuf, lane, qf, sc);
-                __syncwarp();
-                const bool more = ni < i1 && !dead;
-                if (more) {
-                    fetch(a.k4, kbuf, kfull, ni);
-                    kissued++;
-                }
-                // ---- masks, maxima, probabilities (scores still want their factor fs)
                 const int t0 = 64 * e.j;
-                if (!(t0 + 63 <= low && (a.window == 0 || t0 > s.n - 1 - a.window))) {
-#pragma unroll
-                    for (int t = 0; t < NT; t++)
-#pragma unroll
-                        for (int c = 0; c < 2; c++) {
-                            const int pos = low + (8 * t + 2 * (lane & 3) + c) / a.G;
-                            const int from = a.window > 0 ? pos - a.window : -1;
-#pragma unroll
-                            for (int k = 0; k < 4; k++)
-#pragma unroll
-                                for (int r = 0; r < 2; r++) {
-                                    const int tok = t0 + 16 * k + 8 * r + (lane >> 2);
-                                    if (tok > pos || tok <= from) sc[t][k][2 * r + c] = -INFINITY;
-                                }
+                const bool open = t0 + 63 <= low && (a.window == 0 || t0 > s.n - 1 - a.window);
+                wait_copy(a, kfull, taken & 1, dead);
+                constexpr int TT = kTogether<NT>;
+#pragma unroll 1
+                for (int tile = 0; tile < 4; tile += TT) {
+                    float sc[NT][TT][4];
+                    tile_scores<NT, TT>(kcodes + tile * 1024, kpar + tile * 256, qf, sc);
+                    if (tile + TT == 4) {
+                        __syncwarp();
+                        if (ni < i1 && !__any_sync(0xffffffffu, dead)) {
+                            fetch(a.k4, kbuf, kfull, ni);
+                            kissued++;
                         }
-                }
-                float mx[NT][2];
-                bool up = false;
-#pragma unroll
-                for (int t = 0; t < NT; t++)
-#pragma unroll
-                    for (int c = 0; c < 2; c++) {
-                        float top = fmaxf(sc[t][0][c], sc[t][0][2 + c]);
-#pragma unroll
-                        for (int k = 1; k < 4; k++)
-                            top = fmaxf(top, fmaxf(sc[t][k][c], sc[t][k][2 + c]));
-                        mx[t][c] = top * fs[t][c];
-                        up |= mx[t][c] > st.m[t][c];
                     }
-                if (__any_sync(0xffffffffu, up)) {
+                    // ---- masks, maxima, probabilities (scores still want their factor fs)
+                    if (!open) {
 #pragma unroll
-                    for (int t = 0; t < NT; t++)
+                        for (int t = 0; t < NT; t++)
 #pragma unroll
-                        for (int c = 0; c < 2; c++) {
-                            float top = fmaxf(mx[t][c], st.m[t][c]);
+                            for (int c = 0; c < 2; c++) {
+                                const int pos = low + (8 * t + 2 * tig + c) / a.G;
+                                const int from = a.window > 0 ? pos - a.window : -1;
 #pragma unroll
-                            for (int o = 4; o < 32; o <<= 1)
-                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                            const float al = top == -INFINITY ? 0.0f : ex2_approx(st.m[t][c] - top);
-                            st.m[t][c] = top;
-                            far |= fabsf(top) > kFar && top != -INFINITY;
-                            st.l[t][c] *= al;
+                                for (int k = 0; k < TT; k++)
 #pragma unroll
-                            for (int k = 0; k < 8; k++) {
-                                st.o[t][k][c] *= al;
-                                st.o[t][k][2 + c] *= al;
+                                    for (int r = 0; r < 2; r++) {
+                                        const int tok = t0 + 16 * (tile + k) + 8 * r + g;
+                                        if (tok > pos || tok <= from) sc[t][k][2 * r + c] = -INFINITY;
+                                    }
                             }
-                        }
-                }
-                // Where the reference is so large that its rounding is felt, the products are rounded
-                // as it was: the exact ones could pass it by more than f16 can hold.
-                const bool round = __any_sync(0xffffffffu, far);
-                uint32_t pf[NT][4][2];
-#pragma unroll
-                for (int t = 0; t < NT; t++) {
-                    const float f0 = round ? 1.0f : fs[t][0], f1 = round ? 1.0f : fs[t][1];
-                    if (round) {
-#pragma unroll
-                        for (int k = 0; k < 4; k++)
-#pragma unroll
-                            for (int r = 0; r < 4; r++)
-                                sc[t][k][r] = __fmul_rn(sc[t][k][r], fs[t][r & 1]);
                     }
-                    float add[2];
+                    float mx[NT][2];
+                    bool up = false;
 #pragma unroll
-                    for (int c = 0; c < 2; c++)
-                        add[c] = kShift - (st.m[t][c] == -INFINITY ? 0.0f : st.m[t][c]);
+                    for (int t = 0; t < NT; t++)
 #pragma unroll
-                    for (int k = 0; k < 4; k++)
+                        for (int c = 0; c < 2; c++) {
+                            float top = fmaxf(sc[t][0][c], sc[t][0][2 + c]);
 #pragma unroll
-                        for (int r = 0; r < 2; r++) {
-                            const float p0 = ex2_approx(fmaf(sc[t][k][2 * r], f0, add[0]));
-                            const float p1 = ex2_approx(fmaf(sc[t][k][2 * r + 1], f1, add[1]));
-                            st.l[t][0] += p0;
-                            st.l[t][1] += p1;
-                            pf[t][k][r] = movmatrix_trans(F16::pack(p0, p1));
+                            for (int k = 1; k < TT; k++)
+                                top = fmaxf(top, fmaxf(sc[t][k][c], sc[t][k][2 + c]));
+                            mx[t][c] = top * fs[t][c];
+                            up |= mx[t][c] > st.m[t][c] + kLazy;
                         }
+                    if (__any_sync(0xffffffffu, up)) {
+                        bool any_far = false;
+#pragma unroll
+                        for (int t = 0; t < NT; t++)
+#pragma unroll
+                            for (int c = 0; c < 2; c++) {
+                                float top = fmaxf(mx[t][c], st.m[t][c]);
+#pragma unroll
+                                for (int o = 4; o < 32; o <<= 1)
+                                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                                const float al =
+                                    top == -INFINITY ? 0.0f : ex2_approx(st.m[t][c] - top);
+                                st.m[t][c] = top;
+                                any_far |= fabsf(top) > kFar && top != -INFINITY;
+                                st.l[t][c] *= al;
+#pragma unroll
+                                for (int k = 0; k < 8; k++) {
+                                    st.o[t][k][c] *= al;
+                                    st.o[t][k][2 + c] *= al;
+                                }
+                            }
+                        far = __any_sync(0xffffffffu, any_far);
+                    }
+                    // Where the reference is so large that its rounding is felt, the products are
+                    // rounded as it was: the exact ones could pass it by more than f16 can hold.
+                    uint32_t pf[NT][TT][2];
+#pragma unroll
+                    for (int t = 0; t < NT; t++) {
+                        float f[2], add[2];
+#pragma unroll
+                        for (int c = 0; c < 2; c++) {
+                            f[c] = far ? 1.0f : fs[t][c];
+                            add[c] = kShift - (st.m[t][c] == -INFINITY ? 0.0f : st.m[t][c]);
+                        }
+                        if (far) {
+#pragma unroll
+                            for (int k = 0; k < TT; k++)
+#pragma unroll
+                                for (int r = 0; r < 4; r++)
+                                    sc[t][k][r] = __fmul_rn(sc[t][k][r], fs[t][r & 1]);
+                        }
+#pragma unroll
+                        for (int k = 0; k < TT; k++)
+#pragma unroll
+                            for (int r = 0; r < 2; r++) {
+                                const float p0 = ex2_approx(fmaf(sc[t][k][2 * r], f[0], add[0]));
+                                const float p1 = ex2_approx(fmaf(sc[t][k][2 * r + 1], f[1], add[1]));
+                                st.l[t][0] += p0;
+                                st.l[t][1] += p1;
+                                pf[t][k][r] = movmatrix_trans(F16::pack(p0, p1));
+                            }
+                    }
+                    if (tile == 0) wait_copy(a, vfull, taken & 1, dead);
+                    const uint8_t *const vc[2] = {vcodes[0] + tile * 1024, vcodes[1] + tile * 1024};
+                    tile_values<NT, TT>(vc, vpar + tile * 256, s.n - t0 - 16 * tile - 2 * tig, pf, st);
                 }
-                wait_copy(a, vfull, taken & 1, dead);
                 dead = __any_sync(0xffffffffu, dead);
-                page_values<NT>(vbuf, lane, s.n - t0, pf, st);
-                __syncwarp();
-                if (more && !dead) {
+                if (ni < i1 && !dead) {
                     fetch(a.v4, vbuf, vfull, ni);
                     vissued++;
                 }
@@ -583,7 +609,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
 
         // ---- join the warps' states of each unit, then the CTAs' ------------------------------
         // Lane i has entry i: warp i / 2, parked (even) or last (odd); `same` are the entries of its
-        // unit. A warp takes half a column of a unit at a time.
+        // unit. A warp takes a column of a unit at a time, four channels a lane.
         const int eu = lane < 2 * W ? sh.unit[lane >> 1][lane & 1] : -1;
         const int ef = lane < 2 * W ? sh.first[lane >> 1][lane & 1] : 0;
         const float *waiting = parked + (int64_t)cta * W * kRecord;
@@ -604,8 +630,9 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
             const float *carry = records + (int64_t)(4 * cta + 2 + (turn ^ 1)) * kRecord;
             float *mine = records + (int64_t)(4 * cta + (goes_on ? 2 + turn : begins)) * kRecord;
             // units begin at different warps, so that a CTA of many of them keeps all warps busy
-            for (int hc = (warp + k * (W / 2)) % W; hc < 2 * cols; hc += W) {
-                const int c = hc >> 1, ch = 64 * (hc & 1) + 2 * lane;
+            const int live = s.nq * a.G < cols ? s.nq * a.G : cols;
+            for (int c = (warp + k * (W / 2)) % W; c < live; c += W) {
+                const int ch = 4 * lane;
                 float2 ml = make_float2(-INFINITY, 0.0f);
                 if (eu == u && (lane & 1))
                     ml = *reinterpret_cast<const float2 *>(last_state(lane >> 1) + c * kStride + 128);
@@ -613,52 +640,46 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                     ml = *reinterpret_cast<const float2 *>(waiting + (lane >> 1) * kRecord +
                                                            c * kStride + 128);
                 float M = warp_max(ml.x);
-                float2 cm = make_float2(-INFINITY, 0.0f), o = make_float2(0.0f, 0.0f);
+                float2 cm = make_float2(-INFINITY, 0.0f);
+                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 if (carried) {
                     cm = *reinterpret_cast<const float2 *>(carry + c * kStride + 128);
-                    o = *reinterpret_cast<const float2 *>(carry + c * kStride + ch);
+                    o = *reinterpret_cast<const float4 *>(carry + c * kStride + ch);
                     M = fmaxf(M, cm.x);
                 }
                 const float cf = cm.x == -INFINITY ? 0.0f : ex2_approx(cm.x - M);
                 const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - M);
                 const float l = fmaf(cf, cm.y, warp_sum(f * ml.y));
-                o.x *= cf;
-                o.y *= cf;
+                o = scaled(o, cf);
                 for (uint32_t left = run & 0x55555555u; left; left &= left - 1) {
                     const int i = __ffs(left) - 1;
                     const float w = __shfl_sync(0xffffffffu, f, i);
-                    const float2 v = *reinterpret_cast<const float2 *>(
-                        waiting + (i >> 1) * kRecord + c * kStride + ch);
-                    o.x = fmaf(w, v.x, o.x);
-                    o.y = fmaf(w, v.y, o.y);
+                    o = plus(o, w, *reinterpret_cast<const float4 *>(waiting + (i >> 1) * kRecord +
+                                                                     c * kStride + ch));
                 }
                 for (uint32_t left = run & 0xaaaaaaaau; left;) {
-                    float2 v[4];
+                    float4 v[4];
                     float w[4];
 #pragma unroll
                     for (int n = 0; n < 4; n++) {  // four states' loads at a time
                         const int i = left ? __ffs(left) - 1 : 1;
                         w[n] = __shfl_sync(0xffffffffu, f, i);
                         if (!left) w[n] = 0.0f;
-                        v[n] = *reinterpret_cast<const float2 *>(last_state(i >> 1) + c * kStride + ch);
-                        if (!left) v[n] = make_float2(0.0f, 0.0f);
+                        v[n] = *reinterpret_cast<const float4 *>(last_state(i >> 1) + c * kStride + ch);
+                        if (!left) v[n] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                         left &= left - 1;
                     }
 #pragma unroll
-                    for (int n = 0; n < 4; n++) {
-                        o.x = fmaf(w[n], v[n].x, o.x);
-                        o.y = fmaf(w[n], v[n].y, o.y);
-                    }
+                    for (int n = 0; n < 4; n++) o = plus(o, w[n], v[n]);
                 }
                 if (complete && !goes_on) {
                     int row, hq, i;
-                    if (!column(a, s, h, c, row, hq, i)) continue;
-                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                    write_pair<T>(a, row, hq, ch, o.x * inv, o.y * inv);
-                    if (a.lse && ch == 0) a.lse[(int64_t)row * a.Hq + hq] = lse_of(M - kShift, l);
+                    column(a, s, h, c, row, hq, i);
+                    write_four<T>(a, row, hq, ch, scaled(o, l == 0.0f ? 0.0f : 1.0f / l));
+                    if (a.lse && lane == 0) a.lse[(int64_t)row * a.Hq + hq] = lse_of(M - kShift, l);
                 } else {
-                    *reinterpret_cast<float2 *>(mine + c * kStride + ch) = o;
-                    if (ch == 0)
+                    *reinterpret_cast<float4 *>(mine + c * kStride + ch) = o;
+                    if (lane == 0)
                         *reinterpret_cast<float2 *>(mine + c * kStride + 128) = make_float2(M, l);
                 }
             }
@@ -711,15 +732,16 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                 const int p0 = (int)(((int64_t)(first + 1) * ncta - 1) / total);
                 const int p1 = (int)(((int64_t)(first + s.np) * ncta - 1) / total);
                 const int nrec = p1 - p0 + 1;
-                for (int hc = warp; hc < 2 * cols; hc += W) {
-                    const int c = hc >> 1, ch = 64 * (hc & 1) + 2 * lane;
+                const int live = s.nq * a.G < cols ? s.nq * a.G : cols;
+                for (int c = warp; c < live; c += W) {
+                    const int ch = 4 * lane;
                     int row, hq, i;
-                    if (!column(a, s, h, c, row, hq, i)) continue;
+                    column(a, s, h, c, row, hq, i);
                     // record r > 0 is the first one of its CTA: one record back
                     const float *rec0 = records + (int64_t)(4 * p0 + 1) * kRecord + c * kStride;
                     auto rec = [&](int r) { return rec0 + (int64_t)(4 * r - (r ? 1 : 0)) * kRecord; };
                     float M = -INFINITY, l = 0.0f;
-                    float2 o = make_float2(0.0f, 0.0f);
+                    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     for (int k0 = 0; k0 < nrec; k0 += 32) {  // a running join, 32 records a round
                         float2 ml = make_float2(-INFINITY, 0.0f);
                         if (k0 + lane < nrec)
@@ -729,21 +751,16 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                         const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - Mn);
                         M = Mn;
                         l = fmaf(al, l, warp_sum(f * ml.y));
-                        o.x *= al;
-                        o.y *= al;
+                        o = scaled(o, al);
                         const int cnt = nrec - k0 < 32 ? nrec - k0 : 32;
 #pragma unroll 8
                         for (int k = 0; k < cnt; k++) {
                             const float w = __shfl_sync(0xffffffffu, f, k);
-                            const float2 v =
-                                __ldcg(reinterpret_cast<const float2 *>(rec(k0 + k) + ch));
-                            o.x = fmaf(w, v.x, o.x);
-                            o.y = fmaf(w, v.y, o.y);
+                            o = plus(o, w, __ldcg(reinterpret_cast<const float4 *>(rec(k0 + k) + ch)));
                         }
                     }
-                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                    write_pair<T>(a, row, hq, ch, o.x * inv, o.y * inv);
-                    if (a.lse && ch == 0) a.lse[(int64_t)row * a.Hq + hq] = lse_of(M - kShift, l);
+                    write_four<T>(a, row, hq, ch, scaled(o, l == 0.0f ? 0.0f : 1.0f / l));
+                    if (a.lse && lane == 0) a.lse[(int64_t)row * a.Hq + hq] = lse_of(M - kShift, l);
                 }
             }
         }
@@ -767,12 +784,16 @@ cudaError_t launch(const AttnArgs &a, const Plan &pl, cudaStream_t stream) {
 }  // namespace
 
 size_t decode_record_bytes(int cols) { return (size_t)cols * kStride * sizeof(float); }
-int decode_warps(int cols) { return cols == 8 ? kWarpsOf<1> : kWarpsOf<2>; }
+int decode_warps(int cols) {
+    return cols == 8 ? kWarpsOf<1> : cols == 16 ? kWarpsOf<2> : cols == 24 ? kWarpsOf<3> : kWarpsOf<4>;
+}
 
 cudaError_t launch_decode(const AttnArgs &a, const Plan &pl, int dtype, cudaStream_t stream) {
     const bool bf16 = dtype == FFD_DTYPE_BF16;
     if (pl.cols == 8) return bf16 ? launch<1, Bf16>(a, pl, stream) : launch<1, F16>(a, pl, stream);
-    return bf16 ? launch<2, Bf16>(a, pl, stream) : launch<2, F16>(a, pl, stream);
+    if (pl.cols == 16) return bf16 ? launch<2, Bf16>(a, pl, stream) : launch<2, F16>(a, pl, stream);
+    if (pl.cols == 24) return bf16 ? launch<3, Bf16>(a, pl, stream) : launch<3, F16>(a, pl, stream);
+    return bf16 ? launch<4, Bf16>(a, pl, stream) : launch<4, F16>(a, pl, stream);
 }
 
 }  // namespace kv4

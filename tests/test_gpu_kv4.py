@@ -285,6 +285,11 @@ SEVERAL = [
     ("verify", dict(lens=[300, 650, 64, 4], qlens=[3, 4, 1, 4], Hkv=2, G=4)),
     ("verify_g1", dict(lens=[300, 650], qlens=[16, 9], Hkv=2, G=1)),
     ("verify_g7_fp16", dict(lens=[1300, 65], qlens=[6, 5], Hkv=2, G=7, dtype=F16)),
+    ("verify_25_rows", dict(lens=[1300, 65, 64], qlens=[5, 4, 1], Hkv=2, G=5)),
+    ("verify_32_rows", dict(lens=[130, 6500], qlens=[4, 3], Hkv=2, G=8, window=100)),
+    ("verify_33_rows", dict(lens=[130, 650], qlens=[11, 3], Hkv=2, G=3, dtype=F16)),
+    ("verify_mask", dict(lens=[3000, 700], qlens=[4, 8], Hkv=2, G=4, keep=0.3)),
+    ("verify_windows", dict(lens=[300000, 5, 100000], qlens=[4, 3, 2], Hkv=2, G=7, splits=2)),
     ("more_queries_than_tokens", dict(lens=[3, 0, 70], qlens=[5, 2, 80], Hkv=2, G=4)),
     ("chunk", dict(lens=[513, 200], qlens=[200, 200], Hkv=1, G=4)),
     ("chunk_g8", dict(lens=[1000], qlens=[333], Hkv=2, G=8)),
@@ -311,7 +316,7 @@ def test_attention(name, kw):
 
 
 @pytest.mark.parametrize("splits", [1, 2, 3, 17, 1000])
-@pytest.mark.parametrize("q", [1, 3, 60])
+@pytest.mark.parametrize("q", [1, 3, 7, 60])
 def test_any_split_count_and_repeats(splits, q):
     c = Case([2500, 63, 700], [q, min(q, 63), q], 2, 4, seed=9)
     p = c.params(num_splits=splits)
