@@ -466,65 +466,75 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                 }
             }
         } else if (run && warp == 12) {
-            // ================= matrix instructions, one thread =================
-            if (lane == 0) {
-                auto scores = [&](int g, uint32_t ks) {
-                    const uint64_t qd = tc_desc(smem_u32(sh.q[g])), kd = tc_desc(smem_u32(sh.k[ks]));
+            // ================= matrix instructions =================
+            // The whole warp goes through the steps, so that operand addresses stay warp-uniform;
+            // one lane issues.
+            const bool issuer = elect_one();
+            const uint32_t q0 = smem_u32(sh.q[0]), k0 = smem_u32(sh.k[0]), v0 = smem_u32(sh.v[0]);
+            auto scores = [&](int g, uint32_t ks) {
+                const uint64_t qd = tc_desc(q0 + g * 32768), kd = tc_desc(k0 + ks * 16384);
+                if (issuer) {
 #pragma unroll
                     for (int i = 0; i < 8; i++)  // 16 channels each
                         tc_mma(tmem + kColS + g * 64, qd + (i >> 2) * 1024 + (i & 3) * 2,
                                kd + (i >> 2) * 512 + (i & 3) * 2, kIdescS, i > 0);
-                };
-                auto values = [&](int g, uint32_t vs, bool add) {
-                    const uint64_t vd = tc_desc(smem_u32(sh.v[vs]));
+                }
+            };
+            auto values = [&](int g, uint32_t vs, bool add) {
+                const uint64_t vd = tc_desc(v0 + vs * 16384);
+                if (issuer) {
 #pragma unroll
                     for (int i = 0; i < 4; i++)  // 16 tokens each
                         tc_mma_ta(tmem + kColO + g * 128, tmem + kColP + g * 32 + 8 * i, vd + 2 * i,
                                   kIdescO, add || i > 0);
-                };
-                // the next step's page, once its K tile stands (-1: the end)
-                auto take = [&]() {
-                    wait(a, sh, &sh.k_full[steps % kNK], (steps / kNK) & 1);
-                    tc_fence_after();
-                    const int j = *reinterpret_cast<volatile int *>(&sh.info[steps % kInfo]);
-                    return stopped(sh) ? -1 : j;
-                };
-                int j = take();
-                if (j >= 0) scores(0, steps % kNK);
-                tc_commit(&sh.s_full[0]);
-                if (j >= 0 && two) scores(1, steps % kNK);
-                tc_commit(&sh.s_full[1]);
-                tc_commit(&sh.k_free[steps % kNK]);
-                steps++;
-                bool add = false;
-                while (j >= 0 && !stopped(sh)) {
-                    const uint32_t vs = vsteps % kNV;
-                    wait(a, sh, &sh.v_full[vs], (vsteps / kNV) & 1);
-                    wait(a, sh, &sh.p_full[0], turns & 1);
-                    if (stopped(sh)) break;
-                    tc_fence_after();
-                    values(0, vs, add);
-                    j = take();
-                    if (stopped(sh)) break;
-                    if (j >= 0) scores(0, steps % kNK);
-                    tc_commit(&sh.s_full[0]);
-                    wait(a, sh, &sh.p_full[1], turns & 1);
-                    if (stopped(sh)) break;
-                    tc_fence_after();
-                    if (two) {
-                        values(1, vs, add);
-                        if (j >= 0) scores(1, steps % kNK);
-                    }
-                    tc_commit(&sh.s_full[1]);
-                    tc_commit(&sh.v_free[vs]);
-                    tc_commit(&sh.k_free[steps % kNK]);
-                    steps++;
-                    vsteps++;
-                    turns++;
-                    add = true;
                 }
+            };
+            auto commit = [&](uint64_t *bar) {
+                if (issuer) tc_commit(bar);
+            };
+            // wait, and whether the CTA has stopped
+            auto waited = [&](uint64_t *bar, uint32_t parity) {
+                wait(a, sh, bar, parity);
+                return !__any_sync(0xffffffffu, stopped(sh));
+            };
+            // whether there is a next step, once its K tile stands
+            auto take = [&]() {
+                const bool fine = waited(&sh.k_full[steps % kNK], (steps / kNK) & 1);
+                tc_fence_after();
+                const int j = *reinterpret_cast<volatile int *>(&sh.info[steps % kInfo]);
+                return fine && __any_sync(0xffffffffu, j >= 0);
+            };
+            bool more = take();
+            if (more) scores(0, steps % kNK);
+            commit(&sh.s_full[0]);
+            if (more && two) scores(1, steps % kNK);
+            commit(&sh.s_full[1]);
+            commit(&sh.k_free[steps % kNK]);
+            steps++;
+            bool add = false;
+            while (more) {
+                const uint32_t vs = vsteps % kNV;
+                if (!waited(&sh.v_full[vs], (vsteps / kNV) & 1)) break;
+                if (!waited(&sh.p_full[0], turns & 1)) break;
+                tc_fence_after();
+                values(0, vs, add);
+                more = take();
+                if (more) scores(0, steps % kNK);
+                commit(&sh.s_full[0]);
+                if (!waited(&sh.p_full[1], turns & 1)) break;
+                tc_fence_after();
+                if (two) {
+                    values(1, vs, add);
+                    if (more) scores(1, steps % kNK);
+                }
+                commit(&sh.s_full[1]);
+                commit(&sh.v_free[vs]);
+                commit(&sh.k_free[steps % kNK]);
+                steps++;
+                vsteps++;
+                turns++;
+                add = true;
             }
-            __syncwarp();
         } else if (run && warp == 13) {
             // ================= copies of the pages' records =================
             const int32_t *bt = a.block_table + (int64_t)b * a.max_blocks;
@@ -687,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                 const uint32_t last = steps - 1 - i;
                 drain(a, &sh.rec_full[last % kNS], (last / kNS) & 1);
             }
-        if (warp == 12 && lane == 0) {
+        if (warp == 12 && elect_one()) {
             tc_commit(&sh.drain);
             drain(a, &sh.drain, 0);
         }
