@@ -30,10 +30,13 @@ constexpr int kCtaWarps = kThreads / 32;
 constexpr int kNK = 3, kNV = 3;        // f16 tiles of K and of V^T
 constexpr int kNS = 5;                 // record pairs in flight
 constexpr int kInfo = 16;              // steps whose page index is kept
-constexpr int kStride = 130;           // floats of a joined row: o[128], m, l
+constexpr int kRecord = 130 * kRows;   // floats of a joined item: o[128][row], m[row], l[row]
 constexpr float kShift = 7.0f;         // P carries 2^7: with the lazy reference at most 2^15
 constexpr float kLazy = 8.0f;
-constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;  // tensor memory columns, two tiles each
+// Tensor memory columns: S of tile g and step j at 64 (2 g + j % 2), its first 32 columns P's place
+// once S is read; O of tile g at kColO + 128 g.
+constexpr uint32_t kColO = 256;
+__device__ __forceinline__ uint32_t col_s(int g, uint32_t step) { return 64 * (2 * g + (step & 1)); }
 constexpr uint32_t kIdescS = tc_idesc_f16(128, 64), kIdescO = tc_idesc_f16(128, 128);
 
 struct Shared {
@@ -43,7 +46,8 @@ struct Shared {
     uint8_t rec[kNS][2 * kRec];        // K record, V record
     uint64_t rec_full[kNS], rec_free[kNS];
     uint64_t k_full[kNK], k_free[kNK], v_full[kNV], v_free[kNV];
-    uint64_t s_full[2], p_full[2], drain;
+    uint64_t s_full[2][2], p_full[2][2];  // [tile][step % 2]: scores stand, probabilities stand
+    uint64_t o_done[2], drain;            // P V of a tile's step is done
     uint32_t tmem, aborted;
     int info[kInfo];                   // page index of a step, -1: the segment's end
     int scan[kCtaWarps];
@@ -236,8 +240,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
             mbar_init(&sh.v_free[i], 1);
         }
         for (int i = 0; i < 2; i++) {
-            mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.p_full[i], 4);
+            for (int j = 0; j < 2; j++) {
+                mbar_init(&sh.s_full[i][j], 1);
+                mbar_init(&sh.p_full[i][j], 4);
+            }
+            mbar_init(&sh.o_done[i], 1);
         }
         mbar_init(&sh.drain, 1);
         fence_barrier_init();
@@ -307,7 +314,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         at = rem;
     }
 
-    // steps of the whole kernel so far, per role
+    // so far in the whole kernel, per role: steps (segments' ends among them), and pages (V tiles and
+    // P V products)
     uint32_t steps = 0, vsteps = 0, turns = 0;
     for (int x = c0; x < c1;) {
         int fp, np;
@@ -342,21 +350,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
             // ================= softmax of tile grp, one row a thread =================
             const bool active = grp == 0 || two;
             const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-            const uint32_t ts = tmem + lanes + kColS + grp * 64, tp = tmem + lanes + kColP + grp * 32,
-                           to = tmem + lanes + kColO + grp * 128;
+            const uint32_t to = tmem + lanes + kColO + grp * 128;
             const int pos = s.n - s.nq + qi;
             const int from = a.window > 0 ? pos - a.window : -1;
             // positions of the tile's first and last row
             const int lo = s.n - s.nq + (int)(((int64_t)rt * kRows + grp * kTile) / a.G);
             const int hi = s.n - 1 < lo + (kTile - 1) / a.G + 1 ? s.n - 1 : lo + (kTile - 1) / a.G + 1;
             while (true) {
-                wait(a, sh, &sh.s_full[grp], turns & 1);
-                turns++;
+                const uint32_t buf = steps & 1;
+                wait(a, sh, &sh.s_full[grp][buf], (steps >> 1) & 1);
                 if (__any_sync(0xffffffffu, stopped(sh))) break;
                 tc_fence_after();
                 const int j = *reinterpret_cast<volatile int *>(&sh.info[steps % kInfo]);
+                const uint32_t ts = tmem + lanes + col_s(grp, steps);
                 steps++;
-                if (j < 0) break;
+                if (j < 0) {  // arrived at like any other step, so that the phases go by steps
+                    if (lane == 0) mbar_arrive(&sh.p_full[grp][buf]);
+                    break;
+                }
                 if (active) {
                     uint32_t x0[32], x1[32];
                     __syncwarp();
@@ -385,6 +396,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                         l *= al;
                         far = __any_sync(0xffffffffu, fabsf(m) > kFar && m != -INFINITY);
                         if (any) {
+                            wait(a, sh, &sh.o_done[grp], (turns - 1) & 1);  // the last step's P V
+                            __syncwarp();
+                            tc_fence_after();
 #pragma unroll 1
                             for (int c = 0; c < 4; c++) {
                                 uint32_t o[32];
@@ -409,28 +423,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                             x1[c] = __float_as_uint(__fmul_rn(__uint_as_float(x1[c]), fs));
                         }
                     }
-                    float l0 = 0.0f, l1 = 0.0f;
+                    const float2 f2 = make_float2(fx, fx), s2 = make_float2(sub, sub);
+                    float2 l0 = make_float2(0.0f, 0.0f), l1 = l0;
                     uint32_t p[32];
 #pragma unroll
                     for (int c = 0; c < 16; c++) {
-                        const float p0 = ex2_approx(fmaf(__uint_as_float(x0[2 * c]), fx, sub));
-                        const float p1 = ex2_approx(fmaf(__uint_as_float(x0[2 * c + 1]), fx, sub));
-                        const float p2 = ex2_approx(fmaf(__uint_as_float(x1[2 * c]), fx, sub));
-                        const float p3 = ex2_approx(fmaf(__uint_as_float(x1[2 * c + 1]), fx, sub));
-                        l0 += p0 + p1;
-                        l1 += p2 + p3;
-                        p[c] = F16::pack(p0, p1);
-                        p[16 + c] = F16::pack(p2, p3);
+                        float2 e0 = __ffma2_rn(make_float2(__uint_as_float(x0[2 * c]),
+                                                           __uint_as_float(x0[2 * c + 1])), f2, s2);
+                        float2 e1 = __ffma2_rn(make_float2(__uint_as_float(x1[2 * c]),
+                                                           __uint_as_float(x1[2 * c + 1])), f2, s2);
+                        e0 = make_float2(ex2_approx(e0.x), ex2_approx(e0.y));
+                        e1 = make_float2(ex2_approx(e1.x), ex2_approx(e1.y));
+                        l0 = __fadd2_rn(l0, e0);
+                        l1 = __fadd2_rn(l1, e1);
+                        p[c] = F16::pack(e0.x, e0.y);
+                        p[16 + c] = F16::pack(e1.x, e1.y);
                     }
-                    l += l0 + l1;
+                    l += (l0.x + l0.y) + (l1.x + l1.y);
                     __syncwarp();
-                    tmem_store32(tp, p);
+                    tmem_store32(ts, p);
                     tc_wait_store();
                     any = true;
                 }
+                turns++;
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_full[grp]);
+                if (lane == 0) mbar_arrive(&sh.p_full[grp][buf]);
+            }
+            if (any) {  // the last step's P V
+                wait(a, sh, &sh.o_done[grp], (turns - 1) & 1);
+                __syncwarp();
+                tc_fence_after();
             }
         } else if (run && grp == 2) {
             // ================= tiles of f16 values from the records =================
@@ -470,70 +493,72 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
             // The whole warp goes through the steps, so that operand addresses stay warp-uniform;
             // one lane issues.
             const bool issuer = elect_one();
+            uint32_t pstep = steps;  // the step whose values come next
             const uint32_t q0 = smem_u32(sh.q[0]), k0 = smem_u32(sh.k[0]), v0 = smem_u32(sh.v[0]);
-            auto scores = [&](int g, uint32_t ks) {
+            auto scores = [&](int g) {
+                const uint32_t ks = steps % kNK, d = tmem + col_s(g, steps);
                 const uint64_t qd = tc_desc(q0 + g * 32768), kd = tc_desc(k0 + ks * 16384);
                 if (issuer) {
 #pragma unroll
                     for (int i = 0; i < 8; i++)  // 16 channels each
-                        tc_mma(tmem + kColS + g * 64, qd + (i >> 2) * 1024 + (i & 3) * 2,
-                               kd + (i >> 2) * 512 + (i & 3) * 2, kIdescS, i > 0);
+                        tc_mma(d, qd + (i >> 2) * 1024 + (i & 3) * 2, kd + (i >> 2) * 512 + (i & 3) * 2,
+                               kIdescS, i > 0);
                 }
             };
-            auto values = [&](int g, uint32_t vs, bool add) {
-                const uint64_t vd = tc_desc(v0 + vs * 16384);
+            auto values = [&](int g, bool add) {
+                const uint32_t p = tmem + col_s(g, pstep), d = tmem + kColO + g * 128;
+                const uint64_t vd = tc_desc(v0 + vsteps % kNV * 16384);
                 if (issuer) {
 #pragma unroll
                     for (int i = 0; i < 4; i++)  // 16 tokens each
-                        tc_mma_ta(tmem + kColO + g * 128, tmem + kColP + g * 32 + 8 * i, vd + 2 * i,
-                                  kIdescO, add || i > 0);
+                        tc_mma_ta(d, p + 8 * i, vd + 2 * i, kIdescO, add || i > 0);
                 }
             };
             auto commit = [&](uint64_t *bar) {
                 if (issuer) tc_commit(bar);
             };
-            // wait, and whether the CTA has stopped
+            // wait, and whether the CTA goes on
             auto waited = [&](uint64_t *bar, uint32_t parity) {
                 wait(a, sh, bar, parity);
                 return !__any_sync(0xffffffffu, stopped(sh));
             };
-            // whether there is a next step, once its K tile stands
-            auto take = [&]() {
-                const bool fine = waited(&sh.k_full[steps % kNK], (steps / kNK) & 1);
+            // The scores of the next step, two ahead of the values: their place was P's of two steps
+            // ago. False at the segment's end, which the softmax groups learn of in the same way.
+            auto next_scores = [&](bool wait_o) {
+                bool fine = waited(&sh.k_full[steps % kNK], (steps / kNK) & 1);
                 tc_fence_after();
                 const int j = *reinterpret_cast<volatile int *>(&sh.info[steps % kInfo]);
-                return fine && __any_sync(0xffffffffu, j >= 0);
-            };
-            bool more = take();
-            if (more) scores(0, steps % kNK);
-            commit(&sh.s_full[0]);
-            if (more && two) scores(1, steps % kNK);
-            commit(&sh.s_full[1]);
-            commit(&sh.k_free[steps % kNK]);
-            steps++;
-            bool add = false;
-            while (more) {
-                const uint32_t vs = vsteps % kNV;
-                if (!waited(&sh.v_full[vs], (vsteps / kNV) & 1)) break;
-                if (!waited(&sh.p_full[0], turns & 1)) break;
-                tc_fence_after();
-                values(0, vs, add);
-                more = take();
-                if (more) scores(0, steps % kNK);
-                commit(&sh.s_full[0]);
-                if (!waited(&sh.p_full[1], turns & 1)) break;
-                tc_fence_after();
-                if (two) {
-                    values(1, vs, add);
-                    if (more) scores(1, steps % kNK);
+                const bool more = __any_sync(0xffffffffu, j >= 0);
+                for (int g = 0; g < 2; g++) {
+                    if (fine && wait_o) fine = waited(&sh.o_done[g], (turns - 1) & 1);
+                    tc_fence_after();
+                    if (fine && more && (g == 0 || two)) scores(g);
+                    commit(&sh.s_full[g][steps & 1]);
                 }
-                commit(&sh.s_full[1]);
-                commit(&sh.v_free[vs]);
                 commit(&sh.k_free[steps % kNK]);
                 steps++;
+                return fine && more;
+            };
+            bool cur = next_scores(false), nxt = cur && next_scores(false);
+            bool add = false;
+            while (cur) {
+                if (!waited(&sh.v_full[vsteps % kNV], (vsteps / kNV) & 1)) break;
+                bool fine = true;
+                for (int g = 0; g < 2 && fine; g++) {
+                    fine = waited(&sh.p_full[g][pstep & 1], (pstep >> 1) & 1);
+                    tc_fence_after();
+                    if (fine && (g == 0 || two)) values(g, add);
+                    commit(&sh.o_done[g]);
+                }
+                if (!fine) break;
+                commit(&sh.v_free[vsteps % kNV]);
                 vsteps++;
                 turns++;
+                pstep++;
                 add = true;
+                const bool third = nxt && next_scores(true);
+                cur = nxt;
+                nxt = third;
             }
         } else if (run && warp == 13) {
             // ================= copies of the pages' records =================
@@ -584,11 +609,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         }
 
         // ---- the segment's results
-        float *mine = records + (int64_t)(2 * cta + (begins ? 1 : 0)) * kRows * kStride;
+        float *mine = records + (int64_t)(2 * cta + (begins ? 1 : 0)) * kRecord;
         if (grp < 2 && run && (grp == 0 || two)) {
             const uint32_t to = tmem + ((uint32_t)(warp & 3) << 21) + kColO + grp * 128;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            float *row = mine + (int64_t)(grp * kTile + r) * kStride;
+            float *row = mine + grp * kTile + r;
 #pragma unroll 1
             for (int c = 0; c < 4; c++) {
                 uint32_t o[32];
@@ -615,13 +640,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                     }
                 } else if (have) {
 #pragma unroll
-                    for (int e = 0; e < 16; e++)
-                        *reinterpret_cast<float2 *>(row + 32 * c + 2 * e) = make_float2(
-                            __uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+                    for (int e = 0; e < 32; e++) row[(32 * c + e) * kRows] = __uint_as_float(o[e]);
                 }
             }
             if (have) {
-                if (!complete) *reinterpret_cast<float2 *>(row + 128) = make_float2(m, l);
+                if (!complete) row[128 * kRows] = m, row[129 * kRows] = l;
                 else if (a.lse) a.lse[(int64_t)(s.t0 + qi) * a.Hq + hq] = lse_of(m - kShift, l);
             }
         }
@@ -629,44 +652,51 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
             // CTAs first_cta .. last_cta share the item; the last of them to come joins their records
             const int first_cta = (int)(((int64_t)(first + 1) * ncta - 1) / total);
             const int last_cta = (int)(((int64_t)(first + np) * ncta - 1) / total);
-            __threadfence();
             __syncthreads();
-            if (tid == 0) sh.flag = atomicAdd(tickets + first_cta, 1) == last_cta - first_cta;
+            if (tid == 0) {
+                sh.flag = add_acq_rel_gpu(tickets + first_cta, 1) == last_cta - first_cta;
+                if (sh.flag) tickets[first_cta] = 0;  // ready for the next call
+            }
             __syncthreads();
             if (sh.flag) {
-                __threadfence();
+                // 32 rows (one a lane) and 16 channels at a time
                 const int used = rows < kRows ? (int)rows : kRows;
-                const int64_t step = (int64_t)2 * kRows * kStride;
-                const float *rec0 = records + (int64_t)(2 * first_cta + 1) * kRows * kStride;
                 const int nrec = last_cta - first_cta + 1;
-                for (int k = tid; k < used * 64; k += kThreads) {
-                    const int q = k >> 6, ch = 2 * (k & 63);
+                const float *rec0 = records + (int64_t)(2 * first_cta + 1) * kRecord;
+                for (int k = warp; k < 8 * ((used + 31) / 32); k += kCtaWarps) {
+                    const int q = 32 * (k >> 3) + lane, ch = 16 * (k & 7);
                     auto rec = [&](int n) {  // record n > 0 is the first one of its CTA
-                        return rec0 + n * step - (n ? (int64_t)kRows * kStride : 0) +
-                               (int64_t)q * kStride;
+                        return rec0 + (int64_t)(2 * n - (n ? 1 : 0)) * kRecord + q;
                     };
                     float M = -INFINITY;
 #pragma unroll 4
-                    for (int n = 0; n < nrec; n++) M = fmaxf(M, __ldcg(rec(n) + 128));
-                    float2 o = make_float2(0.0f, 0.0f);
-                    float ls = 0.0f;
-#pragma unroll 4
+                    for (int n = 0; n < nrec; n++) M = fmaxf(M, __ldcg(rec(n) + 128 * kRows));
+                    float o[16] = {}, ls = 0.0f;
                     for (int n = 0; n < nrec; n++) {
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(rec(n) + 128));
-                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(rec(n) + ch));
-                        const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - M);
-                        o.x = fmaf(f, v.x, o.x);
-                        o.y = fmaf(f, v.y, o.y);
-                        ls = fmaf(f, ml.y, ls);
+                        const float *from = rec(n);
+                        float v[16];
+#pragma unroll
+                        for (int c = 0; c < 16; c++) v[c] = __ldcg(from + (ch + c) * kRows);
+                        const float mn = __ldcg(from + 128 * kRows), ln = __ldcg(from + 129 * kRows);
+                        const float f = mn == -INFINITY ? 0.0f : ex2_approx(mn - M);
+#pragma unroll
+                        for (int c = 0; c < 16; c++) o[c] = fmaf(f, v[c], o[c]);
+                        ls = fmaf(f, ln, ls);
                     }
+                    if (q >= used) continue;
                     const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
                     const int64_t g = (int64_t)rt * kRows + q;
                     const int i = (int)(g / a.G), head = h * a.G + (int)(g - (int64_t)i * a.G);
-                    write_pair<T>(a, s.t0 + i, head, ch, o.x * inv, o.y * inv);
-                    if (a.lse && ch == 0)
-                        a.lse[(int64_t)(s.t0 + i) * a.Hq + head] = lse_of(M - kShift, ls);
+                    const int64_t at_row = (int64_t)(s.t0 + i) * a.Hq + head;
+                    uint32_t w[8];
+#pragma unroll
+                    for (int c = 0; c < 8; c++) w[c] = T::pack(o[2 * c] * inv, o[2 * c + 1] * inv);
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) +
+                                                           at_row * kD + ch);
+                    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    if (a.lse && ch == 0) a.lse[at_row] = lse_of(M - kShift, ls);
                 }
-                if (tid == 0) tickets[first_cta] = 0;  // ready for the next call
             }
         }
         tc_fence_before();
@@ -721,7 +751,7 @@ cudaError_t launch(const AttnArgs &a, const Plan &pl, cudaStream_t stream) {
 }  // namespace
 
 int chunk_rows() { return kRows; }
-size_t chunk_record_bytes() { return (size_t)kRows * kStride * sizeof(float); }
+size_t chunk_record_bytes() { return kRecord * sizeof(float); }
 
 cudaError_t launch_chunk(const AttnArgs &a, const Plan &pl, int dtype, cudaStream_t stream) {
     return dtype == FFD_DTYPE_BF16 ? launch<Bf16>(a, pl, stream) : launch<F16>(a, pl, stream);
