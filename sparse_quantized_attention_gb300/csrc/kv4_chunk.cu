@@ -11,8 +11,8 @@
 //       and O rescaled, only when a score passes it by 2^8,
 //   O += P V    (M 128, N 128, K 64; P in tensor memory, V^T in shared memory, O in tensor memory).
 // Roles: a copy warp fetches the pages' records; four warps form K and V^T tiles of f16 values from
-// them; one thread issues the matrix instructions; two groups of four warps, one row a thread, do
-// the softmax of one tile each while the tensor core works on the other's.
+// them; one thread a tile issues its matrix instructions; two groups of four warps, one row a thread,
+// do the softmax of one tile each.
 //
 // K's rows, and with them the columns of S, P and V^T, are tokens in the order 8 (p % 8) + p / 8:
 // then the eight tokens that make 16 bytes of a V^T row come from eight different lanes' loads, and
@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kTile = 128;             // rows of a tile
 constexpr int kRows = 2 * kTile;       // rows of an item
-constexpr int kThreads = 448;          // 2 x 4 softmax warps, 4 forming warps, issuer, copy warp
+constexpr int kThreads = 480;          // 2 x 4 softmax warps, 4 forming warps, 2 issuers, copy warp
 constexpr int kCtaWarps = kThreads / 32;
 constexpr int kNK = 3, kNV = 3;        // f16 tiles of K and of V^T
 constexpr int kNS = 5;                 // record pairs in flight
@@ -233,11 +233,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         }
         for (int i = 0; i < kNK; i++) {
             mbar_init(&sh.k_full[i], 4);
-            mbar_init(&sh.k_free[i], 1);
+            mbar_init(&sh.k_free[i], 2);
         }
         for (int i = 0; i < kNV; i++) {
             mbar_init(&sh.v_full[i], 4);
-            mbar_init(&sh.v_free[i], 1);
+            mbar_init(&sh.v_free[i], 2);
         }
         for (int i = 0; i < 2; i++) {
             for (int j = 0; j < 2; j++) {
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
             }
             mbar_init(&sh.o_done[i], 1);
         }
-        mbar_init(&sh.drain, 1);
+        mbar_init(&sh.drain, 2);
         fence_barrier_init();
     }
     const bool any_empty = __syncthreads_or(empty);
@@ -488,70 +488,61 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                     mbar_arrive(&sh.rec_free[slot]);
                 }
             }
-        } else if (run && warp == 12) {
+        } else if (run && (warp == 12 || warp == 13)) {
             // ================= matrix instructions =================
-            // The whole warp goes through the steps, so that operand addresses stay warp-uniform;
-            // one lane issues.
-            const bool issuer = elect_one();
-            uint32_t pstep = steps;  // the step whose values come next
-            const uint32_t q0 = smem_u32(sh.q[0]), k0 = smem_u32(sh.k[0]), v0 = smem_u32(sh.v[0]);
-            auto scores = [&](int g) {
-                const uint32_t ks = steps % kNK, d = tmem + col_s(g, steps);
-                const uint64_t qd = tc_desc(q0 + g * 32768), kd = tc_desc(k0 + ks * 16384);
-                if (issuer) {
-#pragma unroll
-                    for (int i = 0; i < 8; i++)  // 16 channels each
-                        tc_mma(d, qd + (i >> 2) * 1024 + (i & 3) * 2, kd + (i >> 2) * 512 + (i & 3) * 2,
-                               kIdescS, i > 0);
-                }
-            };
-            auto values = [&](int g, bool add) {
-                const uint32_t p = tmem + col_s(g, pstep), d = tmem + kColO + g * 128;
-                const uint64_t vd = tc_desc(v0 + vsteps % kNV * 16384);
-                if (issuer) {
-#pragma unroll
-                    for (int i = 0; i < 4; i++)  // 16 tokens each
-                        tc_mma_ta(d, p + 8 * i, vd + 2 * i, kIdescO, add || i > 0);
-                }
-            };
-            auto commit = [&](uint64_t *bar) {
-                if (issuer) tc_commit(bar);
-            };
+            // One warp a tile. The whole warp goes through the steps, so that operand addresses stay
+            // warp-uniform; one lane issues.
+            const int g = warp - 12;
+            const bool live = g == 0 || two, issuer = elect_one();
+            const uint32_t k0 = smem_u32(sh.k[0]), v0 = smem_u32(sh.v[0]);
+            const uint64_t qd = tc_desc(smem_u32(sh.q[0]) + g * 32768);
             // wait, and whether the CTA goes on
             auto waited = [&](uint64_t *bar, uint32_t parity) {
                 wait(a, sh, bar, parity);
                 return !__any_sync(0xffffffffu, stopped(sh));
             };
             // The scores of the next step, two ahead of the values: their place was P's of two steps
-            // ago. False at the segment's end, which the softmax groups learn of in the same way.
+            // ago. False at the segment's end, which the softmax group learns of in the same way.
             auto next_scores = [&](bool wait_o) {
-                bool fine = waited(&sh.k_full[steps % kNK], (steps / kNK) & 1);
-                tc_fence_after();
+                const uint32_t ks = steps % kNK, d = tmem + col_s(g, steps);
+                bool fine = waited(&sh.k_full[ks], (steps / kNK) & 1);
                 const int j = *reinterpret_cast<volatile int *>(&sh.info[steps % kInfo]);
                 const bool more = __any_sync(0xffffffffu, j >= 0);
-                for (int g = 0; g < 2; g++) {
-                    if (fine && wait_o) fine = waited(&sh.o_done[g], (turns - 1) & 1);
-                    tc_fence_after();
-                    if (fine && more && (g == 0 || two)) scores(g);
-                    commit(&sh.s_full[g][steps & 1]);
+                if (fine && wait_o) fine = waited(&sh.o_done[g], (turns - 1) & 1);
+                tc_fence_after();
+                const uint64_t kd = tc_desc(k0 + ks * 16384);
+                if (issuer) {
+                    if (fine && more && live) {
+#pragma unroll
+                        for (int i = 0; i < 8; i++)  // 16 channels each
+                            tc_mma(d, qd + (i >> 2) * 1024 + (i & 3) * 2,
+                                   kd + (i >> 2) * 512 + (i & 3) * 2, kIdescS, i > 0);
+                    }
+                    tc_commit(&sh.s_full[g][steps & 1]);
+                    tc_commit(&sh.k_free[ks]);
                 }
-                commit(&sh.k_free[steps % kNK]);
                 steps++;
                 return fine && more;
             };
+            uint32_t pstep = steps;  // the step whose values come next
             bool cur = next_scores(false), nxt = cur && next_scores(false);
             bool add = false;
             while (cur) {
-                if (!waited(&sh.v_full[vsteps % kNV], (vsteps / kNV) & 1)) break;
-                bool fine = true;
-                for (int g = 0; g < 2 && fine; g++) {
-                    fine = waited(&sh.p_full[g][pstep & 1], (pstep >> 1) & 1);
-                    tc_fence_after();
-                    if (fine && (g == 0 || two)) values(g, add);
-                    commit(&sh.o_done[g]);
+                const uint32_t vs = vsteps % kNV;
+                if (!waited(&sh.v_full[vs], (vsteps / kNV) & 1)) break;
+                if (!waited(&sh.p_full[g][pstep & 1], (pstep >> 1) & 1)) break;
+                tc_fence_after();
+                const uint32_t p = tmem + col_s(g, pstep), d = tmem + kColO + g * 128;
+                const uint64_t vd = tc_desc(v0 + vs * 16384);
+                if (issuer) {
+                    if (live) {
+#pragma unroll
+                        for (int i = 0; i < 4; i++)  // 16 tokens each
+                            tc_mma_ta(d, p + 8 * i, vd + 2 * i, kIdescO, add || i > 0);
+                    }
+                    tc_commit(&sh.o_done[g]);
+                    tc_commit(&sh.v_free[vs]);
                 }
-                if (!fine) break;
-                commit(&sh.v_free[vsteps % kNV]);
                 vsteps++;
                 turns++;
                 pstep++;
@@ -560,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                 cur = nxt;
                 nxt = third;
             }
-        } else if (run && warp == 13) {
+        } else if (run && warp == 14) {
             // ================= copies of the pages' records =================
             const int32_t *bt = a.block_table + (int64_t)b * a.max_blocks;
             const uint8_t *keep =
@@ -722,12 +713,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         }
     }
     if (stopped(sh)) {  // leave nothing in flight
-        if (warp == 13 && lane == 0)
+        if (warp == 14 && lane == 0)
             for (uint32_t i = 0; i < kNS && i < steps; i++) {
                 const uint32_t last = steps - 1 - i;
                 drain(a, &sh.rec_full[last % kNS], (last / kNS) & 1);
             }
-        if (warp == 12 && elect_one()) {
+        if ((warp == 12 || warp == 13) && elect_one()) {
             tc_commit(&sh.drain);
             drain(a, &sh.drain, 0);
         }
