@@ -88,17 +88,23 @@ __device__ __forceinline__ int head_pages(const AttnArgs &a, const Seq &s) {
 __device__ __forceinline__ bool stopped(const Shared &sh) {
     return *reinterpret_cast<const volatile uint32_t *>(&sh.aborted) != 0;
 }
-__device__ __forceinline__ void wait(const AttnArgs &a, Shared &sh, uint64_t *bar, uint32_t parity) {
-    if (mbar_try_wait(bar, parity)) return;
+__device__ __forceinline__ bool wait_long(const AttnArgs &a, Shared &sh, uint64_t *bar, uint32_t parity) {
     const uint64_t t0 = globaltimer_ns();
     while (!mbar_try_wait(bar, parity)) {
-        if (stopped(sh)) return;
+        if (stopped(sh)) return false;
         if (globaltimer_ns() - t0 > a.wait_ns) {
             raise_error(a.err, FFD_ERRBIT_TIMEOUT);
             *reinterpret_cast<volatile uint32_t *>(&sh.aborted) = 1;
-            return;
+            return false;
         }
     }
+    return true;
+}
+// By a whole warp: true once the phase is complete, false when the CTA has stopped.
+__device__ __forceinline__ bool waited(const AttnArgs &a, Shared &sh, uint64_t *bar, uint32_t parity) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) ok = wait_long(a, sh, bar, parity);
+    return __all_sync(0xffffffffu, ok);
 }
 // The same for what this CTA has in flight, whether or not it has stopped.
 __device__ __forceinline__ void drain(const AttnArgs &a, uint64_t *bar, uint32_t parity) {
@@ -279,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
     const int ncta = total < (int)gridDim.x ? total : (int)gridDim.x;
     const int cta = blockIdx.x;
     if (cta >= ncta) return;
+    __syncwarp();
     if (warp == 0) tmem_alloc(&sh.tmem, 512);
     tc_fence_before();
     __syncthreads();
@@ -358,8 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
             const int hi = s.n - 1 < lo + (kTile - 1) / a.G + 1 ? s.n - 1 : lo + (kTile - 1) / a.G + 1;
             while (true) {
                 const uint32_t buf = steps & 1;
-                wait(a, sh, &sh.s_full[grp][buf], (steps >> 1) & 1);
-                if (__any_sync(0xffffffffu, stopped(sh))) break;
+                if (!waited(a, sh, &sh.s_full[grp][buf], (steps >> 1) & 1)) break;
                 tc_fence_after();
                 const int j = *reinterpret_cast<volatile int *>(&sh.info[steps % kInfo]);
                 const uint32_t ts = tmem + lanes + col_s(grp, steps);
@@ -396,7 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                         l *= al;
                         far = __any_sync(0xffffffffu, fabsf(m) > kFar && m != -INFINITY);
                         if (any) {
-                            wait(a, sh, &sh.o_done[grp], (turns - 1) & 1);  // the last step's P V
+                            // the last step's P V (a stop is met at the next wait)
+                            waited(a, sh, &sh.o_done[grp], (turns - 1) & 1);
                             __syncwarp();
                             tc_fence_after();
 #pragma unroll 1
@@ -451,8 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                 if (lane == 0) mbar_arrive(&sh.p_full[grp][buf]);
             }
             if (any) {  // the last step's P V
-                wait(a, sh, &sh.o_done[grp], (turns - 1) & 1);
-                __syncwarp();
+                waited(a, sh, &sh.o_done[grp], (turns - 1) & 1);
                 tc_fence_after();
             }
         } else if (run && grp == 2) {
@@ -460,12 +466,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
             const int t = tid - 2 * kTile;
             while (true) {
                 const uint32_t slot = steps % kNS, ks = steps % kNK, vs = vsteps % kNV;
-                wait(a, sh, &sh.rec_full[slot], (steps / kNS) & 1);
-                if (steps >= kNK) wait(a, sh, &sh.k_free[ks], (steps / kNK - 1) & 1);
-                if (__any_sync(0xffffffffu, stopped(sh))) break;
+                if (!waited(a, sh, &sh.rec_full[slot], (steps / kNS) & 1)) break;
+                if (steps >= kNK && !waited(a, sh, &sh.k_free[ks], (steps / kNK - 1) & 1)) break;
                 const int j = *reinterpret_cast<volatile int *>(&sh.info[steps % kInfo]);
                 steps++;
-                if (j < 0) {
+                if (j < 0) {  // arrived at like any other step
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(&sh.rec_free[slot]);
@@ -477,8 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.k_full[ks]);
-                if (vsteps >= kNV) wait(a, sh, &sh.v_free[vs], (vsteps / kNV - 1) & 1);
-                if (__any_sync(0xffffffffu, stopped(sh))) break;
+                if (vsteps >= kNV && !waited(a, sh, &sh.v_free[vs], (vsteps / kNV - 1) & 1)) break;
                 vsteps++;
                 form_v(sh.rec[slot] + kRec, sh.v[vs], t, s.n - 64 * j);
                 fence_proxy_async();
@@ -496,41 +500,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
             const bool live = g == 0 || two, issuer = elect_one();
             const uint32_t k0 = smem_u32(sh.k[0]), v0 = smem_u32(sh.v[0]);
             const uint64_t qd = tc_desc(smem_u32(sh.q[0]) + g * 32768);
-            // wait, and whether the CTA goes on
-            auto waited = [&](uint64_t *bar, uint32_t parity) {
-                wait(a, sh, bar, parity);
-                return !__any_sync(0xffffffffu, stopped(sh));
-            };
             // The scores of the next step, two ahead of the values: their place was P's of two steps
             // ago. False at the segment's end, which the softmax group learns of in the same way.
-            auto next_scores = [&](bool wait_o) {
+            auto next_scores = [&]() {
                 const uint32_t ks = steps % kNK, d = tmem + col_s(g, steps);
-                bool fine = waited(&sh.k_full[ks], (steps / kNK) & 1);
+                if (!waited(a, sh, &sh.k_full[ks], (steps / kNK) & 1)) return false;
+                tc_fence_after();
                 const int j = *reinterpret_cast<volatile int *>(&sh.info[steps % kInfo]);
                 const bool more = __any_sync(0xffffffffu, j >= 0);
-                if (fine && wait_o) fine = waited(&sh.o_done[g], (turns - 1) & 1);
-                tc_fence_after();
                 const uint64_t kd = tc_desc(k0 + ks * 16384);
                 if (issuer) {
-                    if (fine && more && live) {
+                    if (more && live) {
 #pragma unroll
                         for (int i = 0; i < 8; i++)  // 16 channels each
                             tc_mma(d, qd + (i >> 2) * 1024 + (i & 3) * 2,
                                    kd + (i >> 2) * 512 + (i & 3) * 2, kIdescS, i > 0);
                     }
                     tc_commit(&sh.s_full[g][steps & 1]);
-                    tc_commit(&sh.k_free[ks]);
                 }
                 steps++;
-                return fine && more;
+                return more;
             };
+            // K's tile of a step is free once its scores have been read, V's once P V is done: both are
+            // known here, and a plain arrival costs less than a commit.
             uint32_t pstep = steps;  // the step whose values come next
-            bool cur = next_scores(false), nxt = cur && next_scores(false);
+            bool cur = next_scores(), nxt = cur && next_scores();
             bool add = false;
             while (cur) {
                 const uint32_t vs = vsteps % kNV;
-                if (!waited(&sh.v_full[vs], (vsteps / kNV) & 1)) break;
-                if (!waited(&sh.p_full[g][pstep & 1], (pstep >> 1) & 1)) break;
+                if (!waited(a, sh, &sh.v_full[vs], (vsteps / kNV) & 1)) break;
+                if (!waited(a, sh, &sh.p_full[g][pstep & 1], (pstep >> 1) & 1)) break;
                 tc_fence_after();
                 const uint32_t p = tmem + col_s(g, pstep), d = tmem + kColO + g * 128;
                 const uint64_t vd = tc_desc(v0 + vs * 16384);
@@ -541,16 +540,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                             tc_mma_ta(d, p + 8 * i, vd + 2 * i, kIdescO, add || i > 0);
                     }
                     tc_commit(&sh.o_done[g]);
-                    tc_commit(&sh.v_free[vs]);
+                    mbar_arrive(&sh.k_free[pstep % kNK]);
                 }
+                if (!waited(a, sh, &sh.o_done[g], turns & 1)) break;
+                if (issuer) mbar_arrive(&sh.v_free[vs]);
                 vsteps++;
                 turns++;
                 pstep++;
                 add = true;
-                const bool third = nxt && next_scores(true);
+                const bool third = nxt && next_scores();
                 cur = nxt;
                 nxt = third;
             }
+            if (issuer) mbar_arrive(&sh.k_free[pstep % kNK]);  // the end's step
         } else if (run && warp == 14) {
             // ================= copies of the pages' records =================
             const int32_t *bt = a.block_table + (int64_t)b * a.max_blocks;
@@ -569,8 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
             };
             auto push = [&](int j, int page) {
                 const uint32_t slot = steps % kNS;
-                if (steps >= kNS) wait(a, sh, &sh.rec_free[slot], (steps / kNS - 1) & 1);
-                if (__any_sync(0xffffffffu, stopped(sh))) return false;
+                if (steps >= kNS && !waited(a, sh, &sh.rec_free[slot], (steps / kNS - 1) & 1)) return false;
                 if (lane == 0) {
                     *reinterpret_cast<volatile int *>(&sh.info[steps % kInfo]) = j;
                     if (j >= 0) {
@@ -724,6 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         }
     }
     __syncthreads();
+    __syncwarp();
     if (warp == 0) tmem_free(tmem, 512);
 }
 
