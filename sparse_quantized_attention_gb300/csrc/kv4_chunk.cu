@@ -10,7 +10,7 @@
 //   P = 2^(S - m) in f16 against a reference m that follows the row's maximum lazily: it is raised,
 //       and O rescaled, only when a score passes it by 2^8,
 //   O += P V    (M 128, N 128, K 64; P in tensor memory, V^T in shared memory, O in tensor memory).
-// Roles: a copy warp fetches the pages' records; four warps form K and V^T tiles of f16 values from
+// Roles: a copy warp fetches the pages' records; four warps form K and four V^T tiles of f16 values from
 // them; one thread a tile issues its matrix instructions; two groups of four warps, one row a thread,
 // do the softmax of one tile each.
 //
@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kTile = 128;             // rows of a tile
 constexpr int kRows = 2 * kTile;       // rows of an item
-constexpr int kThreads = 480;          // 2 x 4 softmax warps, 4 forming warps, 2 issuers, copy warp
+constexpr int kThreads = 608;  // 2 x 4 softmax warps, 4 warps forming K, 4 forming V, 2 issuers, copy
 constexpr int kCtaWarps = kThreads / 32;
 constexpr int kNK = 3, kNV = 3;        // f16 tiles of K and of V^T
 constexpr int kNS = 5;                 // record pairs in flight
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         sh.aborted = 0;
         for (int i = 0; i < kNS; i++) {
             mbar_init(&sh.rec_full[i], 1);
-            mbar_init(&sh.rec_free[i], 4);
+            mbar_init(&sh.rec_free[i], 8);
         }
         for (int i = 0; i < kNK; i++) {
             mbar_init(&sh.k_full[i], 4);
@@ -375,24 +375,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                     break;
                 }
                 if (active) {
-                    uint32_t x0[32], x1[32];
-                    __syncwarp();
-                    tmem_load32(x0, ts);
-                    tmem_load32(x1, ts + 32);
-                    tc_wait_load();
+                    // S in halves of 32 columns, the first read twice: a row's 64 scores at once would
+                    // leave no registers for the warps that form the tiles
                     const int t0 = 64 * j;
-                    if (!(t0 + 63 <= lo && (a.window == 0 || t0 > hi - a.window))) {
+                    const bool open = t0 + 63 <= lo && (a.window == 0 || t0 > hi - a.window);
+                    auto half = [&](uint32_t (&x)[32], int n) {
+                        __syncwarp();
+                        tmem_load32(x, ts + 32 * n);
+                        tc_wait_load();
+                        if (!open) {
 #pragma unroll
-                        for (int c = 0; c < 32; c++) {
-                            const int k0 = t0 + 8 * (c & 7) + (c >> 3);
-                            if (k0 > pos || k0 <= from) x0[c] = 0xff800000u;
-                            if (k0 + 4 > pos || k0 + 4 <= from) x1[c] = 0xff800000u;
+                            for (int c = 0; c < 32; c++) {
+                                const int k = t0 + 8 * (c & 7) + (c >> 3) + 4 * n;
+                                if (k > pos || k <= from) x[c] = 0xff800000u;
+                            }
                         }
-                    }
+                    };
+                    uint32_t x[32];
+                    half(x, 0);
                     float top = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < 32; c++)
-                        top = fmaxf(top, fmaxf(__uint_as_float(x0[c]), __uint_as_float(x1[c])));
+                    for (int c = 0; c < 32; c += 2)
+                        top = fmaxf(top, fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 1])));
+                    half(x, 1);
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2)
+                        top = fmaxf(top, fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 1])));
                     top *= fs;
                     const bool raise = top > m + kLazy || (m == -INFINITY && top > m);
                     if (__any_sync(0xffffffffu, raise)) {
@@ -423,30 +431,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                     // Where the reference is so large that its rounding is felt, the products are
                     // rounded as it was: the exact ones could pass it by more than f16 can hold.
                     const float fx = far ? 1.0f : fs;
-                    if (far) {
-#pragma unroll
-                        for (int c = 0; c < 32; c++) {
-                            x0[c] = __float_as_uint(__fmul_rn(__uint_as_float(x0[c]), fs));
-                            x1[c] = __float_as_uint(__fmul_rn(__uint_as_float(x1[c]), fs));
-                        }
-                    }
                     const float2 f2 = make_float2(fx, fx), s2 = make_float2(sub, sub);
-                    float2 l0 = make_float2(0.0f, 0.0f), l1 = l0;
+                    float2 l2 = make_float2(0.0f, 0.0f);
                     uint32_t p[32];
 #pragma unroll
-                    for (int c = 0; c < 16; c++) {
-                        float2 e0 = __ffma2_rn(make_float2(__uint_as_float(x0[2 * c]),
-                                                           __uint_as_float(x0[2 * c + 1])), f2, s2);
-                        float2 e1 = __ffma2_rn(make_float2(__uint_as_float(x1[2 * c]),
-                                                           __uint_as_float(x1[2 * c + 1])), f2, s2);
-                        e0 = make_float2(ex2_approx(e0.x), ex2_approx(e0.y));
-                        e1 = make_float2(ex2_approx(e1.x), ex2_approx(e1.y));
-                        l0 = __fadd2_rn(l0, e0);
-                        l1 = __fadd2_rn(l1, e1);
-                        p[c] = F16::pack(e0.x, e0.y);
-                        p[16 + c] = F16::pack(e1.x, e1.y);
+                    for (int n = 1; n >= 0; n--) {
+                        if (n == 0) half(x, 0);
+                        if (far) {
+#pragma unroll
+                            for (int c = 0; c < 32; c++)
+                                x[c] = __float_as_uint(__fmul_rn(__uint_as_float(x[c]), fs));
+                        }
+#pragma unroll
+                        for (int c = 0; c < 16; c++) {
+                            float2 e = __ffma2_rn(make_float2(__uint_as_float(x[2 * c]),
+                                                              __uint_as_float(x[2 * c + 1])), f2, s2);
+                            e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+                            l2 = __fadd2_rn(l2, e);
+                            p[16 * n + c] = F16::pack(e.x, e.y);
+                        }
                     }
-                    l += (l0.x + l0.y) + (l1.x + l1.y);
+                    l += l2.x + l2.y;
                     __syncwarp();
                     tmem_store32(ts, p);
                     tc_wait_store();
@@ -461,42 +466,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                 waited(a, sh, &sh.o_done[grp], (turns - 1) & 1);
                 tc_fence_after();
             }
-        } else if (run && grp == 2) {
-            // ================= tiles of f16 values from the records =================
-            const int t = tid - 2 * kTile;
+        } else if (run && (grp == 2 || grp == 3)) {
+            // ================= tiles of f16 values from the records: K, V^T =================
+            const int t = tid & 127;
+            const bool keys = grp == 2;
             while (true) {
                 const uint32_t slot = steps % kNS, ks = steps % kNK, vs = vsteps % kNV;
                 if (!waited(a, sh, &sh.rec_full[slot], (steps / kNS) & 1)) break;
-                if (steps >= kNK && !waited(a, sh, &sh.k_free[ks], (steps / kNK - 1) & 1)) break;
+                if (keys) {
+                    if (steps >= kNK && !waited(a, sh, &sh.k_free[ks], (steps / kNK - 1) & 1)) break;
+                } else {
+                    if (vsteps >= kNV && !waited(a, sh, &sh.v_free[vs], (vsteps / kNV - 1) & 1)) break;
+                }
                 const int j = *reinterpret_cast<volatile int *>(&sh.info[steps % kInfo]);
                 steps++;
-                if (j < 0) {  // arrived at like any other step
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&sh.rec_free[slot]);
-                        mbar_arrive(&sh.k_full[ks]);
-                    }
-                    break;
+                if (j >= 0) {
+                    if (keys) form_k(sh.rec[slot], sh.k[ks], t);
+                    else form_v(sh.rec[slot] + kRec, sh.v[vs], t, s.n - 64 * j);
+                    fence_proxy_async();
                 }
-                form_k(sh.rec[slot], sh.k[ks], t);
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.k_full[ks]);
-                if (vsteps >= kNV && !waited(a, sh, &sh.v_free[vs], (vsteps / kNV - 1) & 1)) break;
-                vsteps++;
-                form_v(sh.rec[slot] + kRec, sh.v[vs], t, s.n - 64 * j);
-                fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&sh.v_full[vs]);
+                    if (keys) mbar_arrive(&sh.k_full[ks]);  // at the end too: it is a step
+                    else if (j >= 0) mbar_arrive(&sh.v_full[vs]);
                     mbar_arrive(&sh.rec_free[slot]);
                 }
+                if (j < 0) break;
+                vsteps++;
             }
-        } else if (run && (warp == 12 || warp == 13)) {
+        } else if (run && (warp == 16 || warp == 17)) {
             // ================= matrix instructions =================
             // One warp a tile. The whole warp goes through the steps, so that operand addresses stay
             // warp-uniform; one lane issues.
-            const int g = warp - 12;
+            const int g = warp - 16;
             const bool live = g == 0 || two, issuer = elect_one();
             const uint32_t k0 = smem_u32(sh.k[0]), v0 = smem_u32(sh.v[0]);
             const uint64_t qd = tc_desc(smem_u32(sh.q[0]) + g * 32768);
@@ -553,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                 nxt = third;
             }
             if (issuer) mbar_arrive(&sh.k_free[pstep % kNK]);  // the end's step
-        } else if (run && warp == 14) {
+        } else if (run && warp == 18) {
             // ================= copies of the pages' records =================
             const int32_t *bt = a.block_table + (int64_t)b * a.max_blocks;
             const uint8_t *keep =
@@ -714,12 +716,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         }
     }
     if (stopped(sh)) {  // leave nothing in flight
-        if (warp == 14 && lane == 0)
+        if (warp == 18 && lane == 0)
             for (uint32_t i = 0; i < kNS && i < steps; i++) {
                 const uint32_t last = steps - 1 - i;
                 drain(a, &sh.rec_full[last % kNS], (last / kNS) & 1);
             }
-        if ((warp == 12 || warp == 13) && elect_one()) {
+        if ((warp == 16 || warp == 17) && elect_one()) {
             tc_commit(&sh.drain);
             drain(a, &sh.drain, 0);
         }
