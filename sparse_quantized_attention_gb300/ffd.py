@@ -351,19 +351,29 @@ def alloc_kv4_cache(num_pages: int, num_kv_heads: int, device="cuda") -> Kv4Cach
                     torch.empty(shp, dtype=torch.uint8, device=device))
 
 
-# The checks below are in each call's path, which for a decode step takes about as long on the host
-# as on the GPU: they read each tensor's attributes once.
+# The three calls below check their tensors in one flat expression each: a decode step takes about as
+# long on the host as on the GPU, and every function call and attribute that is read counts.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_I32, _U8, _F32 = torch.int32, torch.uint8, torch.float32
+_descs = {}  # (P, Hkv) -> a reference to its CacheDesc
+
+
 def _refuse(where: str, what: str):
     raise FFDError(1, f"{where}: {what}")
 
 
-def _same_gpu(where: str, dev: int, *tensors):
-    """Every given tensor (None ones aside) is on GPU `dev`."""
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            _refuse(where, "tensors on different devices")
-    if dev < 0:
-        _refuse(where, "tensors that are not on a GPU")
+def _desc(P: int, Hkv: int):
+    ref = _descs.get((P, Hkv))
+    if ref is None:
+        ref = _descs[(P, Hkv)] = ctypes.byref(CacheDesc(P, Hkv, HEAD_DIM, PAGE))
+    return ref
+
+
+def _stream_of(stream, dev: int) -> int:
+    if stream is None:
+        return _raw_stream(dev)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _row_stride(x, rows: int, heads: int, dtype):
@@ -378,30 +388,37 @@ def _row_stride(x, rows: int, heads: int, dtype):
     return t if rows > 1 else heads * HEAD_DIM
 
 
-def _ints_ok(x, *shape) -> bool:
-    return x is None or (x.dtype == torch.int32 and x.shape == shape and x.is_contiguous())
-
-
-def _kv4_ok(cache) -> bool:
-    a, b = cache
-    return (a.dtype == torch.uint8 and b.dtype == torch.uint8 and a.dim() == 3
-            and a.shape[2] == KV4_RECORD_BYTES and a.shape == b.shape
-            and a.is_contiguous() and b.is_contiguous())
-
-
-def _launch(fn, dev: int, stream, where: str, *args):
-    """fn(*args, stream) on the tensors' device, on its current stream by default."""
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev)
-    else:
-        raw = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    if torch._C._cuda_getDevice() == dev:
-        status = fn(*args, raw)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, raw)
-    if status != FFD_OK:
-        _check(status, where)
+def _kv4_rows(where, cache, positions, block_table, k, v, cu_tokens, error_word):
+    """Checks of a write or a read: (device, P, Hkv, B, table width, rows, dtype, strides of k, v)."""
+    k4, v4 = cache
+    one = v if k is None else k
+    if one is None:
+        _refuse(where, "no rows")
+    dev = k4.get_device()
+    if not (dev >= 0 and v4.get_device() == dev and positions.get_device() == dev
+            and block_table.get_device() == dev and (k is None or k.get_device() == dev)
+            and (v is None or v.get_device() == dev)
+            and (cu_tokens is None or cu_tokens.get_device() == dev)
+            and (error_word is None or error_word.get_device() == dev)):
+        _refuse(where, "tensors on different devices, or not on a GPU")
+    shape, table = k4.shape, block_table.shape
+    if not (k4.dtype == _U8 and v4.dtype == _U8 and len(shape) == 3 and shape[2] == KV4_RECORD_BYTES
+            and v4.shape == shape and k4.is_contiguous() and v4.is_contiguous()):
+        _refuse(where, "the cache")
+    if len(table) != 2 or not (
+            block_table.dtype == _I32 and positions.dtype == _I32
+            and positions.shape == table[:1] and block_table.is_contiguous()
+            and positions.is_contiguous()
+            and (cu_tokens is None or (cu_tokens.dtype == _I32 and cu_tokens.is_contiguous()
+                                       and cu_tokens.shape == (table[0] + 1,)))):
+        _refuse(where, "int32 positions [B], cu_tokens [B + 1], block_table [B, width]")
+    P, Hkv, _ = shape
+    T, dtype = one.shape[0], one.dtype
+    ks = 0 if k is None else _row_stride(k, T, Hkv, dtype)
+    vs = 0 if v is None else _row_stride(v, T, Hkv, dtype)
+    if ks is None or vs is None or dtype not in _DTYPES:
+        _refuse(where, "rows of bf16 or fp16 [T, Hkv, 128]")
+    return dev, P, Hkv, table[0], table[1], T, dtype, ks, vs
 
 
 def _addr(t):
@@ -414,23 +431,20 @@ def ffd_kv4_write(k_new, v_new, positions, block_table, cache: Kv4Cache, *, cu_t
     the 4-bit cache. Sequence b's rows are cu_tokens[b] .. cu_tokens[b+1]-1 (T / B each when None)
     and go to tokens positions[b], positions[b]+1, ... (negative: nothing for that sequence)."""
     where = "ffd_kv4_write"
-    dev, (k4, v4) = k_new.get_device(), cache
-    _same_gpu(where, dev, v_new, positions, block_table, k4, v4, cu_tokens, error_word)
-    if not _kv4_ok(cache) or block_table.dim() != 2:
-        _refuse(where, "the cache or the block table")
-    P, Hkv, _ = k4.shape
-    B, width = block_table.shape
-    T, dtype = k_new.shape[0], k_new.dtype
-    ks, vs = _row_stride(k_new, T, Hkv, dtype), _row_stride(v_new, T, Hkv, dtype)
-    if ks is None or vs is None or dtype not in _DTYPES:
-        _refuse(where, "rows of bf16 or fp16 [T, Hkv, 128]")
-    if not (_ints_ok(block_table, B, width) and _ints_ok(positions, B)
-            and _ints_ok(cu_tokens, B + 1)):
-        _refuse(where, "int32 positions [B], cu_tokens [B + 1], block_table [B, width]")
-    _launch((_lib or lib()).ffd_kv4_write, dev, stream, where,
-            ctypes.byref(CacheDesc(P, Hkv, HEAD_DIM, PAGE)), _DTYPES[dtype], B, width, T,
-            k_new.data_ptr(), ks, v_new.data_ptr(), vs, _addr(cu_tokens), positions.data_ptr(),
-            block_table.data_ptr(), k4.data_ptr(), v4.data_ptr(), _addr(error_word))
+    if k_new is None or v_new is None:
+        _refuse(where, "no rows")
+    dev, P, Hkv, B, width, T, dtype, ks, vs = _kv4_rows(where, cache, positions, block_table, k_new,
+                                                        v_new, cu_tokens, error_word)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return ffd_kv4_write(k_new, v_new, positions, block_table, cache, cu_tokens=cu_tokens,
+                                 error_word=error_word, stream=stream)
+    status = (_lib or lib()).ffd_kv4_write(
+        _desc(P, Hkv), _DTYPES[dtype], B, width, T, k_new.data_ptr(), ks, v_new.data_ptr(), vs,
+        _addr(cu_tokens), positions.data_ptr(), block_table.data_ptr(), cache[0].data_ptr(),
+        cache[1].data_ptr(), _addr(error_word), _stream_of(stream, dev))
+    if status != FFD_OK:
+        _check(status, where)
 
 
 def ffd_kv4_read(cache: Kv4Cache, positions, block_table, k_out, v_out, *, cu_tokens=None,
@@ -438,27 +452,18 @@ def ffd_kv4_read(cache: Kv4Cache, positions, block_table, k_out, v_out, *, cu_to
     """The values the 4-bit cache holds, as rows k_out, v_out [T, Hkv, 128] (bf16 or fp16; either
     may be None). Rows and tokens are matched as in ffd_kv4_write."""
     where = "ffd_kv4_read"
-    k4, v4 = cache
-    dev = k4.get_device()
-    _same_gpu(where, dev, v4, positions, block_table, k_out, v_out, cu_tokens, error_word)
-    if not _kv4_ok(cache) or block_table.dim() != 2:
-        _refuse(where, "the cache or the block table")
-    P, Hkv, _ = k4.shape
-    B, width = block_table.shape
-    one = k_out if k_out is not None else v_out
-    if one is None:
-        _refuse(where, "nothing to read into")
-    T, dtype = one.shape[0], one.dtype
-    ks, vs = (0 if x is None else _row_stride(x, T, Hkv, dtype) for x in (k_out, v_out))
-    if ks is None or vs is None or dtype not in _DTYPES:
-        _refuse(where, "rows of bf16 or fp16 [T, Hkv, 128]")
-    if not (_ints_ok(block_table, B, width) and _ints_ok(positions, B)
-            and _ints_ok(cu_tokens, B + 1)):
-        _refuse(where, "int32 positions [B], cu_tokens [B + 1], block_table [B, width]")
-    _launch((_lib or lib()).ffd_kv4_read, dev, stream, where,
-            ctypes.byref(CacheDesc(P, Hkv, HEAD_DIM, PAGE)), _DTYPES[dtype], B, width, T,
-            _addr(cu_tokens), positions.data_ptr(), block_table.data_ptr(), k4.data_ptr(),
-            v4.data_ptr(), _addr(k_out), ks, _addr(v_out), vs, _addr(error_word))
+    dev, P, Hkv, B, width, T, dtype, ks, vs = _kv4_rows(where, cache, positions, block_table, k_out,
+                                                        v_out, cu_tokens, error_word)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return ffd_kv4_read(cache, positions, block_table, k_out, v_out, cu_tokens=cu_tokens,
+                                error_word=error_word, stream=stream)
+    status = (_lib or lib()).ffd_kv4_read(
+        _desc(P, Hkv), _DTYPES[dtype], B, width, T, _addr(cu_tokens), positions.data_ptr(),
+        block_table.data_ptr(), cache[0].data_ptr(), cache[1].data_ptr(), _addr(k_out), ks,
+        _addr(v_out), vs, _addr(error_word), _stream_of(stream, dev))
+    if status != FFD_OK:
+        _check(status, where)
 
 
 def make_kv4_params(batch, num_q_heads, num_kv_heads, num_pages, max_blocks_per_seq, *,
@@ -490,32 +495,52 @@ def ffd_kv4_attention(params: Kv4Params, q, cache: Kv4Cache, seq_lens, block_tab
     """Attention of each sequence's newest tokens over its 4-bit cache: q [total_q, Hq, 128], rows
     params.q_stride elements apart, out [total_q, Hq, 128], lse fp32 [total_q, Hq] or None."""
     where = "ffd_kv4_attention"
-    dev, (k4, v4) = q.get_device(), cache
-    _same_gpu(where, dev, k4, v4, seq_lens, block_table, out, workspace, cu_q, keep_in, lse)
+    k4, v4 = cache
+    dev = q.get_device()
+    if not (dev >= 0 and k4.get_device() == dev and v4.get_device() == dev
+            and seq_lens.get_device() == dev and block_table.get_device() == dev
+            and out.get_device() == dev and workspace.get_device() == dev
+            and (cu_q is None or cu_q.get_device() == dev)
+            and (keep_in is None or keep_in.get_device() == dev)
+            and (lse is None or lse.get_device() == dev)):
+        _refuse(where, "tensors on different devices, or not on a GPU")
     B, Hq, Hkv, T = params.batch, params.num_q_heads, params.num_kv_heads, params.total_q
-    width = params.max_blocks_per_seq
-    if not _kv4_ok(cache) or k4.shape[0] != params.num_pages or k4.shape[1] != Hkv:
+    width, dtype, row = params.max_blocks_per_seq, q.dtype, Hq * HEAD_DIM
+    shape = (params.num_pages, Hkv, KV4_RECORD_BYTES)
+    if not (k4.dtype == _U8 and v4.dtype == _U8 and k4.shape == shape and v4.shape == shape
+            and k4.is_contiguous() and v4.is_contiguous()):
         _refuse(where, "the cache")
-    dtype, row = q.dtype, Hq * HEAD_DIM
-    stride = _row_stride(q, T, Hq, dtype)
-    if (_DTYPES.get(dtype) != params.dtype or stride is None
-            or (T > 1 and stride != (params.q_stride or row))
-            or _row_stride(out, T, Hq, dtype) != row):
+    shape = (T, Hq, HEAD_DIM)
+    if not (q.shape == shape and out.shape == shape and out.dtype == dtype and out.is_contiguous()
+            and _DTYPES.get(dtype) == params.dtype):
         _refuse(where, "q and out of params.dtype [total_q, Hq, 128]")
-    if not (_ints_ok(block_table, B, width) and _ints_ok(seq_lens, B) and _ints_ok(cu_q, B + 1)):
+    stride = q.stride()
+    if (stride[2] != 1 or (stride[1] != HEAD_DIM and Hq > 1)
+            or (T > 1 and stride[0] != (params.q_stride or row))):
+        _refuse(where, "q's rows, params.q_stride elements apart")
+    if not (block_table.dtype == _I32 and block_table.shape == (B, width)
+            and block_table.is_contiguous() and seq_lens.dtype == _I32 and seq_lens.shape == (B,)
+            and seq_lens.is_contiguous()
+            and (cu_q is None or (cu_q.dtype == _I32 and cu_q.shape == (B + 1,)
+                                  and cu_q.is_contiguous()))):
         _refuse(where, "int32 seq_lens [B], cu_q [B + 1], block_table [B, max_blocks_per_seq]")
-    if keep_in is not None and not (keep_in.dtype == torch.uint8 and keep_in.is_contiguous()
-                                    and keep_in.shape == (B, Hkv, width)):
+    if keep_in is not None and not (keep_in.dtype == _U8 and keep_in.shape == (B, Hkv, width)
+                                    and keep_in.is_contiguous()):
         _refuse(where, "keep_in u8 [B, Hkv, max_blocks_per_seq]")
-    if lse is not None and not (lse.dtype == torch.float32 and lse.is_contiguous()
-                                and lse.shape == (T, Hq)):
+    if lse is not None and not (lse.dtype == _F32 and lse.shape == (T, Hq) and lse.is_contiguous()):
         _refuse(where, "lse fp32 [total_q, Hq]")
     if not workspace.is_contiguous():
         _refuse(where, "the workspace")
-    _launch((_lib or lib()).ffd_kv4_attention, dev, stream, where, ctypes.byref(params),
-            q.data_ptr(), k4.data_ptr(), v4.data_ptr(), seq_lens.data_ptr(), _addr(cu_q),
-            block_table.data_ptr(), _addr(keep_in), out.data_ptr(), _addr(lse),
-            workspace.data_ptr(), workspace.nbytes)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return ffd_kv4_attention(params, q, cache, seq_lens, block_table, out, workspace,
+                                     cu_q=cu_q, keep_in=keep_in, lse=lse, stream=stream)
+    status = (_lib or lib()).ffd_kv4_attention(
+        ctypes.byref(params), q.data_ptr(), k4.data_ptr(), v4.data_ptr(), seq_lens.data_ptr(),
+        _addr(cu_q), block_table.data_ptr(), _addr(keep_in), out.data_ptr(), _addr(lse),
+        workspace.data_ptr(), workspace.nbytes, _stream_of(stream, dev))
+    if status != FFD_OK:
+        _check(status, where)
 
 
 def ffd_get_error(error_word, *, stream=None) -> int:

@@ -165,9 +165,78 @@ def test_binding_refuses_tensors(lib):
     assert stride(wide[:, 8:264].unflatten(1, (2, 128))) == 600
     assert stride(wide[:, :512:2].unflatten(1, (2, 128))) is None
     assert stride(wide[:1, 8:264].unflatten(1, (2, 128))) == 256  # one row: any distance
-    ints = ffd.ffd._ints_ok
-    assert ints(pos, 2) and ints(None, 2) and not ints(pos.long(), 2) and not ints(pos, 3)
-    assert ints(bt, 2, 3) and not ints(bt[:, :2], 2, 2)
-    assert ffd.ffd._kv4_ok(cache)
-    assert not ffd.ffd._kv4_ok(ffd.Kv4Cache(cache.k4, cache.v4[:2]))
-    assert not ffd.ffd._kv4_ok(ffd.Kv4Cache(cache.k4[:, :, :64], cache.v4[:, :, :64]))
+    with pytest.raises(ffd.FFDError):
+        ffd.ffd_kv4_write(None, x, pos, bt, cache)
+    with pytest.raises(ffd.FFDError):
+        ffd.ffd_kv4_read(cache, pos, bt, None, None)
+
+
+class OnGpu:
+    """A CPU tensor that says it is on GPU 0: what the checks after the devices' see."""
+
+    def __init__(self, t):
+        self.t = t
+
+    def get_device(self):
+        return 0
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def test_binding_refuses_shapes_and_types(lib):
+    P, Hkv, B, T = 4, 2, 2, 3
+    z = dict(k4=torch.zeros((P, Hkv, 5120), dtype=torch.uint8),
+             v4=torch.zeros((P, Hkv, 5120), dtype=torch.uint8),
+             pos=torch.zeros(B, dtype=torch.int32), bt=torch.zeros((B, 3), dtype=torch.int32),
+             k=torch.zeros((T, Hkv, 128), dtype=torch.float16),
+             v=torch.zeros((T, Hkv, 128), dtype=torch.float16),
+             cu=torch.zeros(B + 1, dtype=torch.int32))
+
+    def rows(**kw):
+        a = {n: OnGpu(t) for n, t in {**z, **kw}.items()}
+        with pytest.raises(ffd.FFDError) as e:
+            ffd.ffd_kv4_read((a["k4"], a["v4"]), a["pos"], a["bt"], a["k"], a["v"],
+                             cu_tokens=a["cu"])
+        return str(e.value)
+
+    assert "the cache" in rows(k4=z["k4"][:, :, :64])
+    assert "the cache" in rows(v4=z["v4"][:2])
+    assert "the cache" in rows(v4=z["v4"].float())
+    assert "the cache" in rows(k4=z["k4"].transpose(0, 1))
+    assert "int32" in rows(pos=z["pos"].long())
+    assert "int32" in rows(pos=torch.zeros(3, dtype=torch.int32))
+    assert "int32" in rows(bt=torch.zeros((B, 6), dtype=torch.int32)[:, ::2])
+    assert "int32" in rows(bt=torch.zeros(6, dtype=torch.int32))
+    assert "int32" in rows(cu=torch.zeros(B, dtype=torch.int32))
+    assert "rows" in rows(k=z["k"].float())
+    assert "rows" in rows(v=z["v"].bfloat16())
+    assert "rows" in rows(v=z["v"][:2])
+    assert "rows" in rows(k=torch.zeros((T, Hkv, 256), dtype=torch.float16)[..., ::2])
+
+    Hq = 8
+    p = ffd.make_kv4_params(B, Hq, Hkv, P, 3, total_q=T, max_q_len=2, num_splits=1)
+    y = dict(z, q=torch.zeros((T, Hq, 128), dtype=torch.bfloat16),
+             out=torch.zeros((T, Hq, 128), dtype=torch.bfloat16),
+             sl=torch.zeros(B, dtype=torch.int32), ws=torch.zeros(64, dtype=torch.uint8),
+             keep=torch.zeros((B, Hkv, 3), dtype=torch.uint8), lse=torch.zeros((T, Hq)))
+
+    def attend(**kw):
+        a = {n: OnGpu(t) for n, t in {**y, **kw}.items()}
+        with pytest.raises(ffd.FFDError) as e:
+            ffd.ffd_kv4_attention(p, a["q"], (a["k4"], a["v4"]), a["sl"], a["bt"], a["out"],
+                                  a["ws"], cu_q=a["cu"], keep_in=a["keep"], lse=a["lse"])
+        return str(e.value)
+
+    assert "the cache" in attend(k4=torch.zeros((P + 1, Hkv, 5120), dtype=torch.uint8))
+    assert "q and out" in attend(q=y["q"].half())
+    assert "q and out" in attend(out=y["out"][:2])
+    assert "q and out" in attend(out=torch.zeros((T, Hq, 256), dtype=torch.bfloat16)[..., :128])
+    assert "q's rows" in attend(q=torch.zeros((T, 2 * Hq, 128), dtype=torch.bfloat16)[:, :Hq])
+    assert "q's rows" in attend(q=torch.zeros((T, Hq, 256), dtype=torch.bfloat16)[..., ::2])
+    assert "int32" in attend(sl=torch.zeros(3, dtype=torch.int32))
+    assert "int32" in attend(bt=torch.zeros((B, 4), dtype=torch.int32))
+    assert "int32" in attend(cu=torch.zeros(B + 1))
+    assert "keep_in" in attend(keep=y["keep"].bool())
+    assert "lse" in attend(lse=y["lse"].double())
+    assert "workspace" in attend(ws=torch.zeros(64, dtype=torch.uint8)[::2])
