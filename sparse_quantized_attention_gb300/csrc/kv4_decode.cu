@@ -54,7 +54,11 @@ struct Shared {
     uint8_t ring[W][kSlot > 8 * NT * kStride * 4 ? kSlot : (8 * NT * kStride * 4 + 15) / 16 * 16];
     Entry list[kWindow];
     uint64_t full[W][2];
-    int pre[32 * W];                  // items before each thread's chunk of sequences
+    // Up to 32 sequences: each warp's own table of them and of the items before them, so that a short
+    // call's warps begin without a barrier. More: items before each thread's chunk of sequences.
+    Seq seqs[W][32];
+    int start[W][32];
+    int pre[32 * W];
     int scan[W];
     int unit[W][2], first[W][2];      // of a warp's parked and of its last state (unit -1: none)
     int flag[2];
@@ -318,42 +322,56 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
     Shared<NT> &sh = *reinterpret_cast<Shared<NT> *>(align_shared<128>(raw));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
 
-    // ---- items before each chunk of sequences -------------------------------------------------
-    const int chunk = (a.B + kThreads - 1) / kThreads;
-    int own = 0;
-    bool empty = false;  // a sequence has queries and nothing for them to see
-    for (int b = tid * chunk; b < (tid + 1) * chunk && b < a.B; b++) {
-        const Seq s = seq_of(a, b, cta == 0);
-        own += s.np * a.Hkv;
-        empty |= s.np == 0 && s.nq > 0;
+    if (lane < 2) {
+        mbar_init(&sh.full[warp][lane], 1);
+        sh.unit[warp][lane] = -1;
     }
-    int inc = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-    }
-    if (lane == 31) sh.scan[warp] = inc;
-    if (lane < 2) mbar_init(&sh.full[warp][lane], 1);
     fence_barrier_init();
-    const bool any_empty = __syncthreads_or(empty);
-    int total;
-    {
-        const int v = lane < W ? sh.scan[lane] : 0;
-        int up = v;
+
+    // ---- items before each sequence, or before each chunk of them -----------------------------
+    const bool few = a.B <= 32;
+    const int chunk = few ? 1 : (a.B + kThreads - 1) / kThreads;
+    int own = 0, total;
+    bool empty = false;  // a sequence has queries and nothing for them to see
+    auto scan = [&](int v) {  // sum over the lanes up to this one
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, up, o);
-            if (lane >= o) up += y;
+            const int y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
         }
+        return v;
+    };
+    if (few) {
+        Seq s = {0, 0, 0, 0, 0};
+        if (lane < a.B) s = seq_of(a, lane, cta == 0 && warp == 0);
+        own = s.np * a.Hkv;
+        empty = s.np == 0 && s.nq > 0;
+        const int inc = scan(own);
+        sh.seqs[warp][lane] = s;
+        sh.start[warp][lane] = inc - own;
+        total = __shfl_sync(0xffffffffu, inc, 31);
+        empty = __any_sync(0xffffffffu, empty);
+    } else {
+        for (int b = tid * chunk; b < (tid + 1) * chunk && b < a.B; b++) {
+            const Seq s = seq_of(a, b, cta == 0);
+            own += s.np * a.Hkv;
+            empty |= s.np == 0 && s.nq > 0;
+        }
+        const int inc = scan(own);
+        if (lane == 31) sh.scan[warp] = inc;
+        empty = __syncthreads_or(empty);
+        const int v = lane < W ? sh.scan[lane] : 0;
+        const int up = scan(v);
         total = __shfl_sync(0xffffffffu, up, 31);
-        const int before = __shfl_sync(0xffffffffu, up - v, warp);
-        sh.pre[tid] = before + inc - own;
+        sh.pre[tid] = __shfl_sync(0xffffffffu, up - v, warp) + inc - own;
+        __syncthreads();
     }
-    if (any_empty) {
+    __syncwarp();
+    auto seq = [&](int b) { return few ? sh.seqs[warp][b] : seq_of(a, b, false); };
+    if (empty) {
         for (int u = cta * W + warp; u < a.B * a.Hkv; u += gridDim.x * W) {
             const int b = u / a.Hkv, h = u - b * a.Hkv;
-            const Seq s = seq_of(a, b, false);
+            const Seq s = seq(b);
             if (s.np > 0) continue;
             for (int c = 0; c < cols; c++) {
                 int row, hq, i;
@@ -368,7 +386,41 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
     const int ncta = total < (int)gridDim.x ? total : (int)gridDim.x;
     if (cta >= ncta) return;
     const int r0 = (int)((int64_t)total * cta / ncta), r1 = (int)((int64_t)total * (cta + 1) / ncta);
-    __syncthreads();
+    // item x as an entry: its unit, its block, its record when the block is to be taken
+    auto entry_of = [&](int x) {
+        Entry e = {-1, 0, 0, 0};
+        int b = 0, rem;
+        if (few) {
+#pragma unroll
+            for (int step = 16; step > 0; step >>= 1)  // the last sequence that starts at or before x
+                if (b + step < a.B && sh.start[warp][b + step] <= x) b += step;
+            rem = x - sh.start[warp][b];
+        } else {
+            int lo = 0, hi = a.B < kThreads ? a.B : kThreads;
+            while (hi - lo > 1) {  // the last chunk that starts at or before x
+                const int mid = (lo + hi) >> 1;
+                if (sh.pre[mid] <= x) lo = mid;
+                else hi = mid;
+            }
+            b = lo * chunk;
+            rem = x - sh.pre[lo];
+        }
+        Seq s = seq(b);
+        while (rem >= s.np * a.Hkv) {
+            rem -= s.np * a.Hkv;
+            s = seq(++b);
+        }
+        const int h = rem / s.np, j = rem - h * s.np;
+        e.unit = b * a.Hkv + h;
+        e.j = s.fp + j;
+        e.first = x - j;
+        if (!a.keep_in || __ldg(a.keep_in + (int64_t)e.unit * a.max_blocks + e.j)) {
+            const int page = __ldg(a.block_table + (int64_t)b * a.max_blocks + e.j);
+            if (page < 0 || page >= a.P) raise_error(a.err, FFD_ERRBIT_BOUNDS);
+            else e.rec = page * a.Hkv + h;
+        }
+        return e;
+    };
 
     uint8_t *kbuf = sh.ring[warp], *vbuf = kbuf + kRec;
     // where this lane's parts of a tile's K and V stand (rows 16 tile + ...)
@@ -385,57 +437,52 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
     for (int w0 = r0, turn = 0; w0 < r1; w0 += kWindow, turn ^= 1) {
         const int w1 = r1 - w0 < kWindow ? r1 : w0 + kWindow;
 
-        // ---- the window's pages, those that are dropped left out ------------------------------
-        int count = 0;
-        for (int x0 = w0; x0 < w1; x0 += kThreads) {
-            const int x = x0 + tid;
-            Entry e = {-1, 0, 0, 0};
-            bool in = false;
-            if (x < w1) {
-                int lo = 0, hi = a.B < kThreads ? a.B : kThreads;
-                while (hi - lo > 1) {  // the last chunk that starts at or before x
-                    const int mid = (lo + hi) >> 1;
-                    if (sh.pre[mid] <= x) lo = mid;
-                    else hi = mid;
+        // ---- the window's pages ---------------------------------------------------------------
+        // A share of the list is the same number of entries, the odd ones with the first warps (so
+        // that a short list reaches all schedulers).
+        int count = w1 - w0, i0, i1;
+        auto share = [&]() {
+            const int each = count / W, odd = count - each * W;
+            i0 = each * warp + (warp < odd ? warp : odd);
+            i1 = i0 + each + (warp < odd);
+        };
+        if (!a.keep_in) {  // every page is listed: a warp lists its own share
+            share();
+            for (int i = i0 + lane; i < i1; i += 32) sh.list[i] = entry_of(w0 + i);
+            __syncwarp();
+        } else {  // the pages that the mask drops are left out
+            count = 0;
+            for (int x0 = w0; x0 < w1; x0 += kThreads) {
+                const int x = x0 + tid;
+                Entry e = {-1, 0, 0, 0};
+                bool in = false;
+                if (x < w1) {
+                    e = entry_of(x);
+                    in = e.rec >= 0 || x == e.first || x == w0;
                 }
-                int rem = x - sh.pre[lo], b = lo * chunk;
-                Seq s = seq_of(a, b, false);
-                while (rem >= s.np * a.Hkv) {
-                    rem -= s.np * a.Hkv;
-                    s = seq_of(a, ++b, false);
-                }
-                const int h = rem / s.np, j = rem - h * s.np;
-                e.unit = b * a.Hkv + h;
-                e.j = s.fp + j;
-                e.first = x - j;
-                if (!a.keep_in || __ldg(a.keep_in + (int64_t)e.unit * a.max_blocks + e.j)) {
-                    const int page = __ldg(a.block_table + (int64_t)b * a.max_blocks + e.j);
-                    if (page < 0 || page >= a.P) raise_error(a.err, FFD_ERRBIT_BOUNDS);
-                    else e.rec = page * a.Hkv + h;
-                }
-                in = e.rec >= 0 || j == 0 || x == w0;
-            }
-            const uint32_t bal = __ballot_sync(0xffffffffu, in);
-            if (x0 != w0) __syncthreads();  // sh.scan is read no more
-            if (lane == 0) sh.scan[warp] = __popc(bal);
-            __syncthreads();
-            int before = 0, all = 0;
+                const uint32_t bal = __ballot_sync(0xffffffffu, in);
+                if (x0 != w0) __syncthreads();  // sh.scan is read no more
+                if (lane == 0) sh.scan[warp] = __popc(bal);
+                __syncthreads();
+                int before = 0, all = 0;
 #pragma unroll
-            for (int w = 0; w < W; w++) {
-                const int v = sh.scan[w];
-                before += w < warp ? v : 0;
-                all += v;
+                for (int w = 0; w < W; w++) {
+                    const int v = sh.scan[w];
+                    before += w < warp ? v : 0;
+                    all += v;
+                }
+                if (in) sh.list[count + before + __popc(bal & ((1u << lane) - 1u))] = e;
+                count += all;
             }
-            if (in) sh.list[count + before + __popc(bal & ((1u << lane) - 1u))] = e;
-            count += all;
+            __syncthreads();
+            share();
         }
-        if (lane < 2) sh.unit[warp][lane] = -1;
-        __syncthreads();
+        if (w0 != r0) {  // the last window's states have been joined
+            if (lane < 2) sh.unit[warp][lane] = -1;
+            __syncwarp();
+        }
 
-        // ---- this warp's share of the list ----------------------------------------------------
-        // (the first warps take the odd ones: neighbours lie on different schedulers)
-        const int each = count / W, odd = count - each * W;
-        const int i0 = each * warp + (warp < odd ? warp : odd), i1 = i0 + each + (warp < odd);
+        // ---- this warp's share ----------------------------------------------------------------
         auto next = [&](int i) {  // the next page to fetch from i on, i1 when there is none
             while (i < i1 && sh.list[i].rec < 0) i++;
             return i;
@@ -460,7 +507,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
             // one unit's part of the share: entries i .. ie - 1
             const int unit = sh.list[i].unit, first = sh.list[i].first, start = i;
             const int b = unit / a.Hkv, h = unit - b * a.Hkv;
-            const Seq s = seq_of(a, b, false);
+            const Seq s = seq(b);
             State<NT> st;
             uint32_t qf[NT][16];
             float fs[NT][2];
@@ -583,9 +630,11 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
             }
             st.close();
             // ---- the part is done: written out when it is all of its unit, else kept for the join
-            const bool whole = first >= w0 && first + s.np <= w1 &&
-                               (start > i0 || i0 == 0 || sh.list[i0 - 1].unit != unit) &&
-                               (i < i1 || i1 == count || sh.list[i1].unit != unit);
+            const bool whole =
+                a.keep_in ? first >= w0 && first + s.np <= w1 &&
+                                (start > i0 || i0 == 0 || sh.list[i0 - 1].unit != unit) &&
+                                (i < i1 || i1 == count || sh.list[i1].unit != unit)
+                          : first >= w0 + i0 && first + s.np <= w0 + i1;
             if (whole) {
                 write_direct<NT, T>(a, s, h, lane, st);
             } else {
@@ -623,7 +672,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
             const int first = __shfl_sync(0xffffffffu, ef, lead);
             const uint32_t run = __shfl_sync(0xffffffffu, same, lead);
             const int b = u / a.Hkv, h = u - b * a.Hkv;
-            const Seq s = seq_of(a, b, false);
+            const Seq s = seq(b);
             const bool carried = first < w0 && w0 > r0;            // from the window before
             const bool goes_on = first + s.np > w1 && w1 < r1;     // into the next one
             const bool begins = first >= r0, complete = begins && first + s.np <= r1;
@@ -693,9 +742,9 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
             const int u = __shfl_sync(0xffffffffu, eu, lead);
             const int first = __shfl_sync(0xffffffffu, ef, lead);
             if (first >= r0) {  // it begins here: nobody else's when it ends here
-                const int end = first + seq_of(a, u / a.Hkv, false).np;
+                const int end = first + seq(u / a.Hkv).np;
                 if (end <= r1 || w1 < r1) continue;
-            } else if (w1 < r1 && first + seq_of(a, u / a.Hkv, false).np > w1) {
+            } else if (w1 < r1 && first + seq(u / a.Hkv).np > w1) {
                 continue;  // goes on in the next window
             }
             shared_units |= 1u << lead;
@@ -710,7 +759,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                 const int lead = __ffs(mine) - 1;
                 const int u = __shfl_sync(0xffffffffu, eu, lead);
                 const int first = __shfl_sync(0xffffffffu, ef, lead);
-                const int np = seq_of(a, u / a.Hkv, false).np;
+                const int np = seq(u / a.Hkv).np;
                 const int p0 = (int)(((int64_t)(first + 1) * ncta - 1) / total);
                 const int p1 = (int)(((int64_t)(first + np) * ncta - 1) / total);
                 if (lane == 0) {
@@ -727,7 +776,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                 const int u = __shfl_sync(0xffffffffu, eu, lead);
                 const int first = __shfl_sync(0xffffffffu, ef, lead);
                 const int b = u / a.Hkv, h = u - b * a.Hkv;
-                const Seq s = seq_of(a, b, false);
+                const Seq s = seq(b);
                 // CTAs p0 .. p1
                 const int p0 = (int)(((int64_t)(first + 1) * ncta - 1) / total);
                 const int p1 = (int)(((int64_t)(first + s.np) * ncta - 1) / total);
@@ -742,22 +791,25 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                     auto rec = [&](int r) { return rec0 + (int64_t)(4 * r - (r ? 1 : 0)) * kRecord; };
                     float M = -INFINITY, l = 0.0f;
                     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    for (int k0 = 0; k0 < nrec; k0 += 32) {  // a running join, 32 records a round
+                    for (int k0 = 0; k0 < nrec; k0 += 8) {  // a running join, eight records a round
                         float2 ml = make_float2(-INFINITY, 0.0f);
-                        if (k0 + lane < nrec)
+                        if (lane < 8 && k0 + lane < nrec)
                             ml = __ldcg(reinterpret_cast<const float2 *>(rec(k0 + lane) + 128));
+                        float4 v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; k++)
+                            v[k] = k0 + k < nrec
+                                       ? __ldcg(reinterpret_cast<const float4 *>(rec(k0 + k) + ch))
+                                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                         const float Mn = fmaxf(M, warp_max(ml.x));
                         const float al = M == -INFINITY ? 0.0f : ex2_approx(M - Mn);
                         const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - Mn);
                         M = Mn;
                         l = fmaf(al, l, warp_sum(f * ml.y));
                         o = scaled(o, al);
-                        const int cnt = nrec - k0 < 32 ? nrec - k0 : 32;
-#pragma unroll 8
-                        for (int k = 0; k < cnt; k++) {
-                            const float w = __shfl_sync(0xffffffffu, f, k);
-                            o = plus(o, w, __ldcg(reinterpret_cast<const float4 *>(rec(k0 + k) + ch)));
-                        }
+#pragma unroll
+                        for (int k = 0; k < 8; k++)
+                            o = plus(o, __shfl_sync(0xffffffffu, f, k), v[k]);
                     }
                     write_four<T>(a, row, hq, ch, scaled(o, l == 0.0f ? 0.0f : 1.0f / l));
                     if (a.lse && lane == 0) a.lse[(int64_t)row * a.Hq + hq] = lse_of(M - kShift, l);
