@@ -15,6 +15,8 @@ cudaError_t launch_decode(const AttnArgs &a, const Plan &pl, int dtype, cudaStre
 cudaError_t launch_chunk(const AttnArgs &a, const Plan &pl, int dtype, cudaStream_t stream);
 size_t decode_record_bytes(int cols);
 size_t chunk_record_bytes();
+int decode_slots();
+int chunk_slots();
 int chunk_rows();
 int decode_warps(int cols);
 }  // namespace kv4
@@ -98,10 +100,10 @@ ffd_status check_params(const ffd_kv4_params *p) {
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 // At least this many pages (upper bound from the table's width) for each CTA.
-constexpr int64_t kMinDecodePages = 8, kMinChunkPages = 4;
+constexpr int64_t kMinDecodePages = 8, kMinChunkPages = 8;
 
-// Workspace: [error word | a join ticket per CTA | records per CTA | a parked state per warp of the
-// decode kernel]. The tickets, the only part that has to start at zero, have the same place and size
+// Workspace: [error word | three join tickets per CTA | records per CTA | a parked state per warp of
+// the decode kernel]. The tickets, the only part that has to start at zero, have the same place and size
 // whatever the parameters and are left at zero, so that calls of different shapes can share a
 // workspace.
 ffd_status make_plan(const ffd_kv4_params *p, Plan *pl) {
@@ -110,13 +112,18 @@ ffd_status make_plan(const ffd_kv4_params *p, Plan *pl) {
     const int64_t rows = (int64_t)p->max_q_len * (p->num_q_heads / p->num_kv_heads);
     pl->cols = rows <= 32 ? (int)(rows + 7) / 8 * 8 : 0;
     const int sms = current_sm_count();
-    int64_t pages = (int64_t)p->batch * p->num_kv_heads * p->max_blocks_per_seq;
-    if (!pl->cols) pages *= (rows + chunk_rows() - 1) / chunk_rows();
     int64_t ctas = p->num_splits;
     if (ctas == 0) {
         if (sms <= 0) return FFD_ERR_CUDA;
-        const int64_t least = pl->cols ? kMinDecodePages : kMinChunkPages;
-        ctas = (pages + least - 1) / least;
+        const int64_t pages = (int64_t)p->batch * p->num_kv_heads * p->max_blocks_per_seq;
+        if (pl->cols) {
+            ctas = (pages + kMinDecodePages - 1) / kMinDecodePages;
+        } else {  // one for each group of rows in any case
+            const int64_t groups = (rows + chunk_rows() - 1) / chunk_rows();
+            const int64_t items = groups * p->batch * p->num_kv_heads;
+            ctas = (pages * groups + kMinChunkPages - 1) / kMinChunkPages;
+            if (ctas < items) ctas = items;
+        }
     }
     if (sms > 0 && ctas > sms) ctas = sms;
     if (ctas > kMaxCtas) ctas = kMaxCtas;
@@ -124,9 +131,9 @@ ffd_status make_plan(const ffd_kv4_params *p, Plan *pl) {
     const size_t rec = pl->cols ? decode_record_bytes(pl->cols) : chunk_record_bytes();
     size_t off = kAlign;
     pl->tickets = off;
-    off = align_up(off + kMaxCtas * sizeof(int));
+    off = align_up(off + 3 * kMaxCtas * sizeof(int));
     pl->records = off;
-    off = align_up(off + (pl->cols ? 4 : 2) * pl->ctas * rec);
+    off = align_up(off + (size_t)(pl->cols ? decode_slots() : chunk_slots()) * pl->ctas * rec);
     pl->parked = off;
     if (pl->cols) off = align_up(off + (size_t)pl->ctas * decode_warps(pl->cols) * rec);
     pl->total = off;

@@ -31,6 +31,9 @@ constexpr int kNK = 3, kNV = 3;        // f16 tiles of K and of V^T
 constexpr int kNS = 5;                 // record pairs in flight
 constexpr int kInfo = 16;              // steps whose page index is kept
 constexpr int kRecord = 130 * kRows;   // floats of a joined item: o[128][row], m[row], l[row]
+// Records of a CTA: of the item that goes on from before, of the one that begins there; of a group of
+// CTAs whose first one this is, where the item begins or goes on.
+constexpr int kSlots = 4;
 constexpr float kShift = 7.0f;         // P carries 2^7: with the lazy reference at most 2^15
 constexpr float kLazy = 8.0f;
 // Tensor memory columns: S of tile g and step j at 64 (2 g + j % 2), its first 32 columns P's place
@@ -603,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         }
 
         // ---- the segment's results
-        float *mine = records + (int64_t)(2 * cta + (begins ? 1 : 0)) * kRecord;
+        float *mine = records + (int64_t)(kSlots * cta + (begins ? 1 : 0)) * kRecord;
         if (grp < 2 && run && (grp == 0 || two)) {
             const uint32_t to = tmem + ((uint32_t)(warp & 3) << 21) + kColO + grp * 128;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -643,31 +646,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
             }
         }
         if (!complete) {
-            // CTAs first_cta .. last_cta share the item; the last of them to come joins their records
-            const int first_cta = (int)(((int64_t)(first + 1) * ncta - 1) / total);
-            const int last_cta = (int)(((int64_t)(first + np) * ncta - 1) / total);
+            // the last of the CTAs that share the item joins their records (of many: in two steps)
+            const Shares p(first, np, ncta, total, cta);
             __syncthreads();
-            if (tid == 0) {
-                sh.flag = add_acq_rel_gpu(tickets + first_cta, 1) == last_cta - first_cta;
-                if (sh.flag) tickets[first_cta] = 0;  // ready for the next call
-            }
+            if (tid == 0) sh.flag = p.last_of_group(tickets);
             __syncthreads();
-            if (sh.flag) {
-                // 32 rows (one a lane) and 16 channels at a time
-                const int used = rows < kRows ? (int)rows : kRows;
-                const int nrec = last_cta - first_cta + 1;
-                const float *rec0 = records + (int64_t)(2 * first_cta + 1) * kRecord;
+            const int used = rows < kRows ? (int)rows : kRows;
+            // join records rec(0) .. rec(n - 1): 32 rows (one a lane) and 16 channels at a time
+            auto join = [&](auto rec, int n, auto done) {
                 for (int k = warp; k < 8 * ((used + 31) / 32); k += kCtaWarps) {
                     const int q = 32 * (k >> 3) + lane, ch = 16 * (k & 7);
-                    auto rec = [&](int n) {  // record n > 0 is the first one of its CTA
-                        return rec0 + (int64_t)(2 * n - (n ? 1 : 0)) * kRecord + q;
-                    };
-                    float M = -INFINITY;
+                    float M = -INFINITY, ls = 0.0f, o[16] = {};
 #pragma unroll 4
-                    for (int n = 0; n < nrec; n++) M = fmaxf(M, __ldcg(rec(n) + 128 * kRows));
-                    float o[16] = {}, ls = 0.0f;
-                    for (int n = 0; n < nrec; n++) {
-                        const float *from = rec(n);
+                    for (int i = 0; i < n; i++) M = fmaxf(M, __ldcg(rec(i) + 128 * kRows + q));
+#pragma unroll 2
+                    for (int i = 0; i < n; i++) {
+                        const float *from = rec(i) + q;
                         float v[16];
 #pragma unroll
                         for (int c = 0; c < 16; c++) v[c] = __ldcg(from + (ch + c) * kRows);
@@ -677,19 +671,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                         for (int c = 0; c < 16; c++) o[c] = fmaf(f, v[c], o[c]);
                         ls = fmaf(f, ln, ls);
                     }
-                    if (q >= used) continue;
-                    const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
-                    const int64_t g = (int64_t)rt * kRows + q;
-                    const int i = (int)(g / a.G), head = h * a.G + (int)(g - (int64_t)i * a.G);
-                    const int64_t at_row = (int64_t)(s.t0 + i) * a.Hq + head;
-                    uint32_t w[8];
+                    if (q < used) done(q, ch, M, ls, o);
+                }
+            };
+            auto finish = [&](int q, int ch, float M, float ls, const float (&o)[16]) {
+                const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+                const int64_t g = (int64_t)rt * kRows + q;
+                const int i = (int)(g / a.G), head = h * a.G + (int)(g - (int64_t)i * a.G);
+                const int64_t at_row = (int64_t)(s.t0 + i) * a.Hq + head;
+                uint32_t w[8];
 #pragma unroll
-                    for (int c = 0; c < 8; c++) w[c] = T::pack(o[2 * c] * inv, o[2 * c + 1] * inv);
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) +
-                                                           at_row * kD + ch);
-                    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                    if (a.lse && ch == 0) a.lse[at_row] = lse_of(M - kShift, ls);
+                for (int c = 0; c < 8; c++) w[c] = T::pack(o[2 * c] * inv, o[2 * c + 1] * inv);
+                uint4 *dst =
+                    reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at_row * kD + ch);
+                dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                if (a.lse && ch == 0) a.lse[at_row] = lse_of(M - kShift, ls);
+            };
+            auto slot = [&](int c, int n) { return records + (int64_t)(kSlots * c + n) * kRecord; };
+            if (sh.flag) {
+                // a CTA's record: its second one when the item begins there, else its first
+                auto member = [&](int n) { return slot(p.g0 + n, p.g0 + n == p.p0); };
+                if (p.groups == 1) {
+                    join(member, p.members, finish);
+                } else {
+                    float *group = slot(p.g0, p.g0 == p.p0 ? 2 : 3);
+                    join(member, p.members, [&](int q, int ch, float M, float ls, const float (&o)[16]) {
+#pragma unroll
+                        for (int c = 0; c < 16; c++) group[(ch + c) * kRows + q] = o[c];
+                        if (ch == 0) group[128 * kRows + q] = M, group[129 * kRows + q] = ls;
+                    });
+                    __syncthreads();
+                    if (tid == 0) sh.flag = p.last_group(tickets);
+                    __syncthreads();
+                    if (sh.flag)
+                        join([&](int n) { return slot(p.p0 + n * kJoin, n ? 3 : 2); }, p.groups, finish);
                 }
             }
         }
@@ -746,6 +762,7 @@ cudaError_t launch(const AttnArgs &a, const Plan &pl, cudaStream_t stream) {
 }  // namespace
 
 int chunk_rows() { return kRows; }
+int chunk_slots() { return kSlots; }
 size_t chunk_record_bytes() { return kRecord * sizeof(float); }
 
 cudaError_t launch_chunk(const AttnArgs &a, const Plan &pl, int dtype, cudaStream_t stream) {

@@ -30,6 +30,9 @@ constexpr int kStride = 132;          // floats of a joined column: o[128], m, l
 constexpr float kShift = 7.0f;        // P carries 2^7, and at most 2^15: a column's reference m is
 constexpr float kLazy = 8.0f;         // raised only when a score passes it by 2^8
 constexpr int kWindow = 2048;         // pages of a CTA's list
+// Records of a CTA: of the unit that goes on from before, of the one that begins there; two carries
+// between windows; of a group of CTAs whose first one this is, where the unit begins or goes on.
+constexpr int kSlots = 6;
 
 // Warps of a CTA: what their registers allow (128 a thread for one column tile, 168 for two, 204
 // for three, 255 for four), and the 16-token tiles that a warp takes together: the more column tiles, the fewer tokens
@@ -179,11 +182,11 @@ __device__ __forceinline__ void tile_scores(const uint8_t *codes, const uint8_t 
 
 // O^T += V^T P^T over TT tiles. The lane holds words 2 g, 2 g + 1 of tokens 2 tig, 2 tig + 1 of a tile
 // and of the two eight further on: codes[e] and par point at token 2 tig (+ e for the codes) of the
-// first tile. Tokens from `valid` on (counted from token 2 tig) hold anything and count as 0. A
-// permutation of bytes puts two tokens' nibbles of one channel into one register's halves.
+// first tile. In a sequence's last page (tail) tokens from `valid` on (counted from token 2 tig) hold
+// anything and count as 0. A permutation of bytes puts two tokens' nibbles of one channel into one register's halves.
 template <int NT, int TT>
 __device__ __forceinline__ void tile_values(const uint8_t *const (&codes)[2], const uint8_t *par,
-                                            int valid, const uint32_t (&pf)[NT][TT][2],
+                                            bool tail, int valid, const uint32_t (&pf)[NT][TT][2],
                                             State<NT> &st) {
 #pragma unroll
     for (int tile = 0; tile < TT; tile++) {
@@ -194,8 +197,10 @@ __device__ __forceinline__ void tile_values(const uint8_t *const (&codes)[2], co
         for (int hi = 0; hi < 2; hi++) {
             uint32_t q0 = *reinterpret_cast<const uint32_t *>(par + tile * 256 + hi * 128);
             uint32_t q1 = *reinterpret_cast<const uint32_t *>(par + tile * 256 + hi * 128 + 16);
-            q0 = 16 * tile + 8 * hi < valid ? q0 : 0u;
-            q1 = 16 * tile + 8 * hi + 1 < valid ? q1 : 0u;
+            if (tail) {
+                q0 = 16 * tile + 8 * hi < valid ? q0 : 0u;
+                q1 = 16 * tile + 8 * hi + 1 < valid ? q1 : 0u;
+            }
             s[hi] = __byte_perm(q0, q1, 0x5410);
             o[hi] = __byte_perm(q0, q1, 0x7632);
 #pragma unroll
@@ -619,7 +624,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                     }
                     if (tile == 0) wait_copy(a, vfull, taken & 1, dead);
                     const uint8_t *const vc[2] = {vcodes[0] + tile * 1024, vcodes[1] + tile * 1024};
-                    tile_values<NT, TT>(vc, vpar + tile * 256, s.n - t0 - 16 * tile - 2 * tig, pf, st);
+                    tile_values<NT, TT>(vc, vpar + tile * 256, s.n - t0 < kPage,
+                                        s.n - t0 - 16 * tile - 2 * tig, pf, st);
                 }
                 dead = __any_sync(0xffffffffu, dead);
                 if (ni < i1 && !dead) {
@@ -676,8 +682,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
             const bool carried = first < w0 && w0 > r0;            // from the window before
             const bool goes_on = first + s.np > w1 && w1 < r1;     // into the next one
             const bool begins = first >= r0, complete = begins && first + s.np <= r1;
-            const float *carry = records + (int64_t)(4 * cta + 2 + (turn ^ 1)) * kRecord;
-            float *mine = records + (int64_t)(4 * cta + (goes_on ? 2 + turn : begins)) * kRecord;
+            const float *carry = records + (int64_t)(kSlots * cta + 2 + (turn ^ 1)) * kRecord;
+            float *mine = records + (int64_t)(kSlots * cta + (goes_on ? 2 + turn : begins)) * kRecord;
             // units begin at different warps, so that a CTA of many of them keeps all warps busy
             const int live = s.nq * a.G < cols ? s.nq * a.G : cols;
             for (int c = (warp + k * (W / 2)) % W; c < live; c += W) {
@@ -734,7 +740,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
             }
         }
         // Units that other CTAs share, the first and the last at most: the last CTA to come joins
-        // their records (complete by the barrier and the ticket). One warp takes each ticket.
+        // their records (complete by the barrier and the ticket). One warp takes each ticket. Of more
+        // than kJoin CTAs, each kJoin neighbours join first, and the last of these groups the groups.
         __syncthreads();
         uint32_t shared_units = 0;
         for (units = leads; units; units &= units - 1) {
@@ -759,48 +766,36 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                 const int lead = __ffs(mine) - 1;
                 const int u = __shfl_sync(0xffffffffu, eu, lead);
                 const int first = __shfl_sync(0xffffffffu, ef, lead);
-                const int np = seq(u / a.Hkv).np;
-                const int p0 = (int)(((int64_t)(first + 1) * ncta - 1) / total);
-                const int p1 = (int)(((int64_t)(first + np) * ncta - 1) / total);
-                if (lane == 0) {
-                    const bool last = add_acq_rel_gpu(tickets + p0, 1) == p1 - p0;
-                    if (last) tickets[p0] = 0;  // ready for the next call
-                    sh.flag[warp] = last;
-                }
+                const Shares p(first, seq(u / a.Hkv).np, ncta, total, cta);
+                if (lane == 0) sh.flag[warp] = p.last_of_group(tickets);
             }
         }
         __syncthreads();
         for (int k = 0; shared_units; k++, shared_units &= shared_units - 1) {
-            if (sh.flag[k]) {
-                const int lead = __ffs(shared_units) - 1;
-                const int u = __shfl_sync(0xffffffffu, eu, lead);
-                const int first = __shfl_sync(0xffffffffu, ef, lead);
-                const int b = u / a.Hkv, h = u - b * a.Hkv;
-                const Seq s = seq(b);
-                // CTAs p0 .. p1
-                const int p0 = (int)(((int64_t)(first + 1) * ncta - 1) / total);
-                const int p1 = (int)(((int64_t)(first + s.np) * ncta - 1) / total);
-                const int nrec = p1 - p0 + 1;
-                const int live = s.nq * a.G < cols ? s.nq * a.G : cols;
+            if (!sh.flag[k]) continue;
+            const int lead = __ffs(shared_units) - 1;
+            const int u = __shfl_sync(0xffffffffu, eu, lead);
+            const int first = __shfl_sync(0xffffffffu, ef, lead);
+            const int b = u / a.Hkv, h = u - b * a.Hkv;
+            const Seq s = seq(b);
+            const Shares p(first, s.np, ncta, total, cta);
+            const int live = s.nq * a.G < cols ? s.nq * a.G : cols;
+            // join records rec(0) .. rec(n - 1), eight a round, column by column
+            auto join = [&](auto rec, int n, auto done) {
                 for (int c = warp; c < live; c += W) {
-                    const int ch = 4 * lane;
-                    int row, hq, i;
-                    column(a, s, h, c, row, hq, i);
-                    // record r > 0 is the first one of its CTA: one record back
-                    const float *rec0 = records + (int64_t)(4 * p0 + 1) * kRecord + c * kStride;
-                    auto rec = [&](int r) { return rec0 + (int64_t)(4 * r - (r ? 1 : 0)) * kRecord; };
                     float M = -INFINITY, l = 0.0f;
                     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    for (int k0 = 0; k0 < nrec; k0 += 8) {  // a running join, eight records a round
+                    for (int k0 = 0; k0 < n; k0 += 8) {
                         float2 ml = make_float2(-INFINITY, 0.0f);
-                        if (lane < 8 && k0 + lane < nrec)
-                            ml = __ldcg(reinterpret_cast<const float2 *>(rec(k0 + lane) + 128));
+                        if (lane < 8 && k0 + lane < n)
+                            ml = __ldcg(reinterpret_cast<const float2 *>(rec(k0 + lane) + c * kStride +
+                                                                         128));
                         float4 v[8];
 #pragma unroll
-                        for (int k = 0; k < 8; k++)
-                            v[k] = k0 + k < nrec
-                                       ? __ldcg(reinterpret_cast<const float4 *>(rec(k0 + k) + ch))
-                                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        for (int i = 0; i < 8; i++)
+                            v[i] = k0 + i < n ? __ldcg(reinterpret_cast<const float4 *>(
+                                                    rec(k0 + i) + c * kStride + 4 * lane))
+                                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                         const float Mn = fmaxf(M, warp_max(ml.x));
                         const float al = M == -INFINITY ? 0.0f : ex2_approx(M - Mn);
                         const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - Mn);
@@ -808,13 +803,35 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                         l = fmaf(al, l, warp_sum(f * ml.y));
                         o = scaled(o, al);
 #pragma unroll
-                        for (int k = 0; k < 8; k++)
-                            o = plus(o, __shfl_sync(0xffffffffu, f, k), v[k]);
+                        for (int i = 0; i < 8; i++)
+                            o = plus(o, __shfl_sync(0xffffffffu, f, i), v[i]);
                     }
-                    write_four<T>(a, row, hq, ch, scaled(o, l == 0.0f ? 0.0f : 1.0f / l));
-                    if (a.lse && lane == 0) a.lse[(int64_t)row * a.Hq + hq] = lse_of(M - kShift, l);
+                    done(c, M, l, o);
                 }
+            };
+            auto finish = [&](int c, float M, float l, float4 o) {
+                int row, hq, i;
+                column(a, s, h, c, row, hq, i);
+                write_four<T>(a, row, hq, 4 * lane, scaled(o, l == 0.0f ? 0.0f : 1.0f / l));
+                if (a.lse && lane == 0) a.lse[(int64_t)row * a.Hq + hq] = lse_of(M - kShift, l);
+            };
+            auto slot = [&](int c, int n) { return records + (int64_t)(kSlots * c + n) * kRecord; };
+            // a CTA's record: its second one when the unit begins there, else its first
+            auto member = [&](int n) { return slot(p.g0 + n, p.g0 + n == p.p0); };
+            if (p.groups == 1) {
+                join(member, p.members, finish);
+                continue;
             }
+            float *mine = slot(p.g0, p.g0 == p.p0 ? 4 : 5);
+            join(member, p.members, [&](int c, float M, float l, float4 o) {
+                *reinterpret_cast<float4 *>(mine + c * kStride + 4 * lane) = o;
+                if (lane == 0) *reinterpret_cast<float2 *>(mine + c * kStride + 128) = make_float2(M, l);
+            });
+            __syncthreads();
+            if (tid == 0) sh.flag[k] = p.last_group(tickets);
+            __syncthreads();
+            if (sh.flag[k])
+                join([&](int n) { return slot(p.p0 + n * kJoin, n ? 5 : 4); }, p.groups, finish);
         }
         __syncthreads();
     }
@@ -836,6 +853,7 @@ cudaError_t launch(const AttnArgs &a, const Plan &pl, cudaStream_t stream) {
 }  // namespace
 
 size_t decode_record_bytes(int cols) { return (size_t)cols * kStride * sizeof(float); }
+int decode_slots() { return kSlots; }
 int decode_warps(int cols) {
     return cols == 8 ? kWarpsOf<1> : cols == 16 ? kWarpsOf<2> : cols == 24 ? kWarpsOf<3> : kWarpsOf<4>;
 }

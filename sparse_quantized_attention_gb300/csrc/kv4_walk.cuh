@@ -56,6 +56,38 @@ __device__ __forceinline__ void query_scale(const AttnArgs &a, float top, float 
     f = fmaxf(f, 1.2e-38f);  // never 0: times -inf it has to stay -inf
 }
 
+// The CTAs that share a run of pages: items first .. first + np - 1 of `total`, cut into ncta equal
+// ranges. CTAs p0 .. p1 have parts of it; with more than kJoin of them, kJoin neighbours make a group.
+// Three arrays of kMaxCtas tickets count who has come: to the group of p0 (or to all), to the groups
+// that begin at a later CTA, and the groups that are joined. Each is indexed by a CTA in which at most
+// one such run begins, or goes on from before.
+constexpr int kJoin = 16;
+struct Shares {
+    int p0, p1, groups, g0, members;  // groups; this CTA's: its first CTA, its CTAs
+    __device__ Shares(int first, int np, int ncta, int total, int cta) {
+        p0 = (int)(((int64_t)(first + 1) * ncta - 1) / total);
+        p1 = (int)(((int64_t)(first + np) * ncta - 1) / total);
+        const int n = p1 - p0 + 1;
+        groups = (n + kJoin - 1) / kJoin;
+        const int at = (cta - p0) / kJoin * kJoin;
+        g0 = p0 + at;
+        members = n - at < kJoin ? n - at : kJoin;
+    }
+    // One thread, after a barrier behind the CTA's writes. The last to come leaves the ticket at 0
+    // for the next call.
+    __device__ bool come(int *ticket, int of) const {
+        const bool last = add_acq_rel_gpu(ticket, 1) == of - 1;
+        if (last) *ticket = 0;
+        return last;
+    }
+    __device__ bool last_of_group(int *tickets) const {
+        return come(tickets + (g0 == p0 ? 0 : kMaxCtas) + g0, members);
+    }
+    __device__ bool last_group(int *tickets) const {
+        return come(tickets + 2 * kMaxCtas + p0, groups);
+    }
+};
+
 // Two channels of a row of out.
 template <class T>
 __device__ __forceinline__ void write_pair(const AttnArgs &a, int row, int hq, int ch, float x,

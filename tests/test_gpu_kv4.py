@@ -315,7 +315,20 @@ def test_attention(name, kw):
     c.check(out, lse)
 
 
-@pytest.mark.parametrize("splits", [1, 2, 3, 17, 1000])
+@pytest.mark.parametrize("q,length", [(1, 70000), (5, 70000), (70, 40000)])
+def test_one_sequence_over_every_cta(q, length):
+    """More CTAs share a unit than are joined at once, twice with the same workspace."""
+    c = Case([length, 200], [q, 1], 1, 5, seed=17)
+    p = c.params()
+    ws = ffd.alloc_kv4_workspace(p)
+    for _ in range(2):
+        out, lse = c.buffers()
+        c.call(out, lse, ws, p)
+        assert ffd.ffd_get_error(ws) == 0
+        c.check(out, lse)
+
+
+@pytest.mark.parametrize("splits", [1, 2, 3, 17, 40, 1000])
 @pytest.mark.parametrize("q", [1, 3, 7, 60])
 def test_any_split_count_and_repeats(splits, q):
     c = Case([2500, 63, 700], [q, min(q, 63), q], 2, 4, seed=9)
