@@ -112,6 +112,7 @@ struct RowsArgs {
 // Arguments of an attention call.
 struct AttnArgs {
     int B, Hq, Hkv, G, P, max_blocks, max_q, total_q, window;
+    int whole_items;  // chunk kernel: items are not cut
     int64_t q_stride;
     float sm_scale;
     const void *q;
@@ -127,6 +128,7 @@ struct AttnArgs {
 struct Plan {
     int cols;  // query columns of the decode kernel (8, 16, 24 or 32), 0: the chunk kernel
     int ctas;
+    int whole_items;  // chunk kernel: items are not cut
     size_t tickets, records, parked, total;
 };
 

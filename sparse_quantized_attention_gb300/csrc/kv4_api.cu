@@ -101,6 +101,8 @@ size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 // At least this many pages (upper bound from the table's width) for each CTA.
 constexpr int64_t kMinDecodePages = 8, kMinChunkPages = 8;
+// Pages' time that cutting items costs a CTA of the chunk kernel (a second start, records, joins).
+constexpr int64_t kJoinPages = 16;
 
 // Workspace: [error word | three join tickets per CTA | records per CTA | a parked state per warp of
 // the decode kernel]. The tickets, the only part that has to start at zero, have the same place and size
@@ -112,17 +114,24 @@ ffd_status make_plan(const ffd_kv4_params *p, Plan *pl) {
     const int64_t rows = (int64_t)p->max_q_len * (p->num_q_heads / p->num_kv_heads);
     pl->cols = rows <= 32 ? (int)(rows + 7) / 8 * 8 : 0;
     const int sms = current_sm_count();
+    const int64_t units = (int64_t)p->batch * p->num_kv_heads;
     int64_t ctas = p->num_splits;
+    pl->whole_items = 0;
     if (ctas == 0) {
         if (sms <= 0) return FFD_ERR_CUDA;
-        const int64_t pages = (int64_t)p->batch * p->num_kv_heads * p->max_blocks_per_seq;
         if (pl->cols) {
-            ctas = (pages + kMinDecodePages - 1) / kMinDecodePages;
-        } else {  // one for each group of rows in any case
-            const int64_t groups = (rows + chunk_rows() - 1) / chunk_rows();
-            const int64_t items = groups * p->batch * p->num_kv_heads;
-            ctas = (pages * groups + kMinChunkPages - 1) / kMinChunkPages;
-            if (ctas < items) ctas = items;
+            ctas = (units * p->max_blocks_per_seq + kMinDecodePages - 1) / kMinDecodePages;
+        } else {
+            // An item (256 rows over the pages they see) goes to one CTA when the pages that the
+            // longest-working CTA then has beyond an equal share cost less than cutting items does.
+            const int64_t items = units * ((rows + chunk_rows() - 1) / chunk_rows());
+            const int64_t rounds = (items + sms - 1) / sms;
+            if ((rounds * sms - items) * p->max_blocks_per_seq <= kJoinPages * sms) {
+                pl->whole_items = 1;
+                ctas = items;
+            } else {
+                ctas = (items * p->max_blocks_per_seq + kMinChunkPages - 1) / kMinChunkPages;
+            }
         }
     }
     if (sms > 0 && ctas > sms) ctas = sms;
@@ -208,6 +217,7 @@ ffd_status ffd_kv4_attention(const ffd_kv4_params *params, const void *q, const 
     a.max_q = p.max_q_len;
     a.total_q = p.total_q;
     a.window = p.window;
+    a.whole_items = pl.whole_items;
     a.q_stride = p.q_stride ? p.q_stride : (int64_t)p.num_q_heads * kD;
     a.sm_scale = p.sm_scale;
     a.q = q;

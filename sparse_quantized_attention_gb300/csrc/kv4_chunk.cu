@@ -5,6 +5,7 @@
 // one such group of rows over the pages that any of them sees. The pages of all items, concatenated,
 // are cut into equal contiguous ranges, one per CTA (one per SM), so the last CTA ends with the first
 // whatever the causal edges leave; an item cut by a range's end is joined by the last of its CTAs.
+// Where items are short, whole ones are dealt out instead: a join costs more than the imbalance.
 // For each page of 64 tokens a CTA computes, for its two tiles of 128 rows,
 //   S = Q K^T   (M 128, N 64, K 128; f16, both operands in shared memory, S in tensor memory),
 //   P = 2^(S - m) in f16 against a reference m that follows the row's maximum lazily: it is raised,
@@ -34,6 +35,7 @@ constexpr int kRecord = 130 * kRows;   // floats of a joined item: o[128][row], 
 // Records of a CTA: of the item that goes on from before, of the one that begins there; of a group of
 // CTAs whose first one this is, where the item begins or goes on.
 constexpr int kSlots = 4;
+constexpr int kOnce = 5;               // records (133 KB each) that one CTA joins at once
 constexpr float kShift = 7.0f;         // P carries 2^7: with the lazy reference at most 2^15
 constexpr float kLazy = 8.0f;
 // Tensor memory columns: S of tile g and step j at 64 (2 g + j % 2), its first 32 columns P's place
@@ -76,8 +78,9 @@ __device__ __forceinline__ int item_groups(const AttnArgs &a, const Seq &s) {
     return (int)(((int64_t)s.nq * a.G + kRows - 1) / kRows);
 }
 
-// Pages of one head's items of a sequence.
+// What one head's items of a sequence weigh when the work is cut: their pages, or one each.
 __device__ __forceinline__ int head_pages(const AttnArgs &a, const Seq &s) {
+    if (a.whole_items) return item_groups(a, s);
     int sum = 0;
     for (int rt = 0; rt < item_groups(a, s); rt++) {
         int fp, np;
@@ -315,13 +318,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         }
         h = rem / hp;
         rem -= h * hp;
-        for (;; rt++) {
+        for (; !a.whole_items; rt++) {
             int fp, np;
             item_pages(a, s, rt, fp, np);
             if (rem < np) break;
             rem -= np;
         }
-        at = rem;
+        at = a.whole_items ? 0 : rem;
+        if (a.whole_items) rt = rem;
     }
 
     // so far in the whole kernel, per role: steps (segments' ends among them), and pages (V tiles and
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
     for (int x = c0; x < c1;) {
         int fp, np;
         item_pages(a, s, rt, fp, np);
-        const int cnt = np - at < c1 - x ? np - at : c1 - x;
+        const int cnt = a.whole_items || np - at < c1 - x ? np - at : c1 - x;
         const int j0 = fp + at, j1 = j0 + cnt;
         const int64_t rows = (int64_t)s.nq * a.G - (int64_t)rt * kRows;  // of this item and later
         const bool two = rows > kTile;
@@ -607,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
 
         // ---- the segment's results
         float *mine = records + (int64_t)(kSlots * cta + (begins ? 1 : 0)) * kRecord;
-        if (grp < 2 && run && (grp == 0 || two)) {
+        if (grp < 2 && run && (grp == 0 || two) && np > 0) {
             const uint32_t to = tmem + ((uint32_t)(warp & 3) << 21) + kColO + grp * 128;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             float *row = mine + grp * kTile + r;
@@ -647,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         }
         if (!complete) {
             // the last of the CTAs that share the item joins their records (of many: in two steps)
-            const Shares p(first, np, ncta, total, cta);
+            const Shares p(first, np, ncta, total, cta, kOnce);
             __syncthreads();
             if (tid == 0) sh.flag = p.last_of_group(tickets);
             __syncthreads();
@@ -705,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                     if (tid == 0) sh.flag = p.last_group(tickets);
                     __syncthreads();
                     if (sh.flag)
-                        join([&](int n) { return slot(p.p0 + n * kJoin, n ? 3 : 2); }, p.groups, finish);
+                        join([&](int n) { return slot(p.p0 + n * p.size, n ? 3 : 2); }, p.groups, finish);
                 }
             }
         }
@@ -714,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         tc_fence_after();
 
         // ---- the next item
-        x += cnt;
+        x += a.whole_items ? 1 : cnt;
         at = 0;
         if (x < c1) {
             do {
@@ -724,11 +728,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                         h = 0;
                         do {
                             s = seq_of(a, ++b, false);
-                        } while (s.nq == 0 || s.n == 0);
+                        } while (s.nq == 0 || (s.n == 0 && !a.whole_items));
                     }
                 }
                 item_pages(a, s, rt, fp, np);
-            } while (np == 0);
+            } while (np == 0 && !a.whole_items);
         }
     }
     if (stopped(sh)) {  // leave nothing in flight

@@ -33,6 +33,7 @@ constexpr int kWindow = 2048;         // pages of a CTA's list
 // Records of a CTA: of the unit that goes on from before, of the one that begins there; two carries
 // between windows; of a group of CTAs whose first one this is, where the unit begins or goes on.
 constexpr int kSlots = 6;
+constexpr int kOnce = 16;             // records that one CTA joins at once
 
 // Warps of a CTA: what their registers allow (128 a thread for one column tile, 168 for two, 204
 // for three, 255 for four), and the 16-token tiles that a warp takes together: the more column tiles, the fewer tokens
@@ -741,7 +742,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
         }
         // Units that other CTAs share, the first and the last at most: the last CTA to come joins
         // their records (complete by the barrier and the ticket). One warp takes each ticket. Of more
-        // than kJoin CTAs, each kJoin neighbours join first, and the last of these groups the groups.
+        // than kOnce CTAs, groups of neighbours join first, and the last of the groups joins these.
         __syncthreads();
         uint32_t shared_units = 0;
         for (units = leads; units; units &= units - 1) {
@@ -766,7 +767,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                 const int lead = __ffs(mine) - 1;
                 const int u = __shfl_sync(0xffffffffu, eu, lead);
                 const int first = __shfl_sync(0xffffffffu, ef, lead);
-                const Shares p(first, seq(u / a.Hkv).np, ncta, total, cta);
+                const Shares p(first, seq(u / a.Hkv).np, ncta, total, cta, kOnce);
                 if (lane == 0) sh.flag[warp] = p.last_of_group(tickets);
             }
         }
@@ -778,7 +779,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
             const int first = __shfl_sync(0xffffffffu, ef, lead);
             const int b = u / a.Hkv, h = u - b * a.Hkv;
             const Seq s = seq(b);
-            const Shares p(first, s.np, ncta, total, cta);
+            const Shares p(first, s.np, ncta, total, cta, kOnce);
             const int live = s.nq * a.G < cols ? s.nq * a.G : cols;
             // join records rec(0) .. rec(n - 1), eight a round, column by column
             auto join = [&](auto rec, int n, auto done) {
@@ -831,7 +832,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
             if (tid == 0) sh.flag[k] = p.last_group(tickets);
             __syncthreads();
             if (sh.flag[k])
-                join([&](int n) { return slot(p.p0 + n * kJoin, n ? 5 : 4); }, p.groups, finish);
+                join([&](int n) { return slot(p.p0 + n * p.size, n ? 5 : 4); }, p.groups, finish);
         }
         __syncthreads();
     }

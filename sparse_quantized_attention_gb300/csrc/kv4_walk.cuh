@@ -57,21 +57,22 @@ __device__ __forceinline__ void query_scale(const AttnArgs &a, float top, float 
 }
 
 // The CTAs that share a run of pages: items first .. first + np - 1 of `total`, cut into ncta equal
-// ranges. CTAs p0 .. p1 have parts of it; with more than kJoin of them, kJoin neighbours make a group.
+// ranges. CTAs p0 .. p1 have parts of it. Up to kOnce of them are joined at once; more in groups of
+// about their number's root, then group by group, so that many CTAs read the records side by side.
 // Three arrays of kMaxCtas tickets count who has come: to the group of p0 (or to all), to the groups
 // that begin at a later CTA, and the groups that are joined. Each is indexed by a CTA in which at most
 // one such run begins, or goes on from before.
-constexpr int kJoin = 16;
 struct Shares {
-    int p0, p1, groups, g0, members;  // groups; this CTA's: its first CTA, its CTAs
-    __device__ Shares(int first, int np, int ncta, int total, int cta) {
+    int p0, p1, size, groups, g0, members;  // groups of `size`; this CTA's: its first CTA, its CTAs
+    __device__ Shares(int first, int np, int ncta, int total, int cta, int once) {
         p0 = (int)(((int64_t)(first + 1) * ncta - 1) / total);
         p1 = (int)(((int64_t)(first + np) * ncta - 1) / total);
         const int n = p1 - p0 + 1;
-        groups = (n + kJoin - 1) / kJoin;
-        const int at = (cta - p0) / kJoin * kJoin;
+        size = n <= once ? n : (int)ceilf(sqrtf((float)n));
+        groups = (n + size - 1) / size;
+        const int at = (cta - p0) / size * size;
         g0 = p0 + at;
-        members = n - at < kJoin ? n - at : kJoin;
+        members = n - at < size ? n - at : size;
     }
     // One thread, after a barrier behind the CTA's writes. The last to come leaves the ticket at 0
     // for the next call.
