@@ -28,6 +28,7 @@ using namespace ffd::kv4;
 namespace {
 
 constexpr size_t kAlign = 256;
+constexpr int64_t kMaxRows = 1 << 28;  // query tokens of a sequence x G
 constexpr size_t kMaxUnits = 65535;  // (sequence, KV head) pairs of an attention call
 
 bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
@@ -92,7 +93,8 @@ ffd_status check_params(const ffd_kv4_params *p) {
     if ((int64_t)p->num_pages * p->num_kv_heads > INT32_MAX) return FFD_ERR_UNSUPPORTED;
     const int64_t pages = (int64_t)p->batch * p->num_kv_heads * p->max_blocks_per_seq;
     const int64_t rows = (int64_t)p->max_q_len * (p->num_q_heads / p->num_kv_heads);
-    if (pages > INT32_MAX || pages > INT32_MAX / ((rows + chunk_rows() - 1) / chunk_rows()))
+    if (rows > kMaxRows || pages > INT32_MAX ||
+        pages > INT32_MAX / ((rows + chunk_rows() - 1) / chunk_rows()))
         return FFD_ERR_UNSUPPORTED;
     return FFD_OK;
 }

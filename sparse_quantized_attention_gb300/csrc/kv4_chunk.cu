@@ -57,37 +57,54 @@ struct Shared {
     int info[kInfo];                   // page index of a step, -1: the segment's end
     int scan[kCtaWarps];
     int flag;
-    int pre[kThreads];                 // pages of all items before each thread's chunk of sequences
+    float factor[kRows];               // of the rows' scores
+    int pre[kThreads];                 // weight of all items before each chunk of sequences
 };
 static_assert(sizeof(Shared) + 1024 <= 232448, "shared memory per CTA");
+
+// x / G for 0 <= x < 2^29 (m = ceil(2^32 / G) is off by less than G).
+__device__ __forceinline__ int div_g(const AttnArgs &a, int x) {
+    return a.G == 1 ? x : (int)__umulhi((uint32_t)x, 0xffffffffu / (uint32_t)a.G + 1u);
+}
+
+__device__ __forceinline__ int item_groups(const AttnArgs &a, const Seq &s) {
+    return (s.nq * a.G + kRows - 1) / kRows;
+}
 
 // Pages that the rows of item group rt of a sequence see: the first, and how many.
 __device__ __forceinline__ void item_pages(const AttnArgs &a, const Seq &s, int rt, int &fp,
                                            int &np) {
-    const int64_t rows = (int64_t)s.nq * a.G;
-    const int64_t r1 = (int64_t)(rt + 1) * kRows < rows ? (int64_t)(rt + 1) * kRows : rows;
-    const int lo = s.n - s.nq + (int)((int64_t)rt * kRows / a.G);
-    const int hi = s.n - s.nq + (int)((r1 - 1) / a.G);
-    int64_t first = a.window > 0 ? (int64_t)lo - a.window + 1 : 0;
-    if (first < 0) first = 0;
-    fp = (int)(first >> 6);
+    const int rows = s.nq * a.G;
+    const int r1 = (rt + 1) * kRows < rows ? (rt + 1) * kRows : rows;
+    const int lo = s.n - s.nq + div_g(a, rt * kRows), hi = s.n - s.nq + div_g(a, r1 - 1);
+    const int first = a.window > 0 && lo >= a.window ? lo - a.window + 1 : 0;
+    fp = first >> 6;
     np = hi < 0 ? 0 : (hi >> 6) - fp + 1;
 }
 
-__device__ __forceinline__ int item_groups(const AttnArgs &a, const Seq &s) {
-    return (int)(((int64_t)s.nq * a.G + kRows - 1) / kRows);
+// What one item weighs when the work is cut: its pages, or one each; 0 behind the last one.
+__device__ __forceinline__ int item_weight(const AttnArgs &a, const Seq &s, int rt) {
+    if (rt >= item_groups(a, s)) return 0;
+    if (a.whole_items) return 1;
+    int fp, np;
+    item_pages(a, s, rt, fp, np);
+    return np;
 }
 
-// What one head's items of a sequence weigh when the work is cut: their pages, or one each.
-__device__ __forceinline__ int head_pages(const AttnArgs &a, const Seq &s) {
-    if (a.whole_items) return item_groups(a, s);
-    int sum = 0;
-    for (int rt = 0; rt < item_groups(a, s); rt++) {
-        int fp, np;
-        item_pages(a, s, rt, fp, np);
-        sum += np;
+__device__ __forceinline__ int lane_scan(int v, int lane) {  // sum over the lanes up to this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
     }
-    return sum;
+    return v;
+}
+
+// One head's items of a sequence, weighed by a warp.
+__device__ __forceinline__ int head_weight(const AttnArgs &a, const Seq &s, int lane) {
+    int sum = 0;
+    for (int rt = 0; rt < item_groups(a, s); rt += 32) sum += item_weight(a, s, rt + lane);
+    return __reduce_add_sync(0xffffffffu, sum);
 }
 
 // Bounded waits: once one runs out the CTA stops (aborted) and drains what is in flight.
@@ -178,40 +195,34 @@ __device__ __forceinline__ void form_v(const uint8_t *rec, uint8_t *tile, int t,
             make_uint4(out[c][0], out[c][1], out[c][2], out[c][3]);
 }
 
-// A row of q into its tile as scaled f16; returns the factor of its scores.
+// The item's rows of q into the tiles as scaled f16, half a warp a row, and their scores' factors.
 template <class T>
-__device__ __forceinline__ float load_query(const AttnArgs &a, uint8_t *tile, int r, bool have,
-                                            int row, int hq) {
-    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) +
-                                                       (int64_t)row * a.q_stride + hq * kD);
-    float top = 0.0f;
-    if (have) {
+__device__ __forceinline__ void load_queries(const AttnArgs &a, Shared &sh, const Seq &s, int h,
+                                             int row0, int rows, int warp, int lane) {
+    const int j = lane & 15;  // channels 8 j .. 8 j + 7
 #pragma unroll 4
-        for (int j = 0; j < 16; j++) {
-            const uint4 u = __ldg(src + j);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    for (int p = warp; p < rows / 2; p += kCtaWarps) {
+        const int r = 2 * p + (lane >> 4), i = div_g(a, row0 + r);
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (i < s.nq)
+            u = __ldg(reinterpret_cast<const uint4 *>(
+                          static_cast<const uint16_t *>(a.q) + (int64_t)(s.t0 + i) * a.q_stride +
+                          (h * a.G + row0 + r - i * a.G) * kD) + j);
+        const float2 x0 = T::unpack(u.x), x1 = T::unpack(u.y), x2 = T::unpack(u.z),
+                     x3 = T::unpack(u.w);
+        float top = fmaxf(fmaxf(fmaxf(fabsf(x0.x), fabsf(x0.y)), fmaxf(fabsf(x1.x), fabsf(x1.y))),
+                          fmaxf(fmaxf(fabsf(x2.x), fabsf(x2.y)), fmaxf(fabsf(x3.x), fabsf(x3.y))));
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
-                const float2 f = T::unpack(w[k]);
-                top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-            }
-        }
+        for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float mul, f;
+        query_scale(a, top, mul, f);
+        const int tr = r & (kTile - 1);
+        *reinterpret_cast<uint4 *>(sh.q[r / kTile] + (j >> 3) * 16384 + tr * 128 +
+                                   (((j & 7) ^ (tr & 7)) << 4)) =
+            make_uint4(F16::pack(x0.x * mul, x0.y * mul), F16::pack(x1.x * mul, x1.y * mul),
+                       F16::pack(x2.x * mul, x2.y * mul), F16::pack(x3.x * mul, x3.y * mul));
+        if (j == 0) sh.factor[r] = f;
     }
-    float mul, f;
-    query_scale(a, top, mul, f);
-#pragma unroll 4
-    for (int j = 0; j < 16; j++) {
-        uint4 o = make_uint4(0, 0, 0, 0);
-        if (have) {
-            const uint4 u = __ldg(src + j);
-            const float2 x0 = T::unpack(u.x), x1 = T::unpack(u.y), x2 = T::unpack(u.z),
-                         x3 = T::unpack(u.w);
-            o = make_uint4(F16::pack(x0.x * mul, x0.y * mul), F16::pack(x1.x * mul, x1.y * mul),
-                           F16::pack(x2.x * mul, x2.y * mul), F16::pack(x3.x * mul, x3.y * mul));
-        }
-        *reinterpret_cast<uint4 *>(tile + (j >> 3) * 16384 + r * 128 + (((j & 7) ^ (r & 7)) << 4)) = o;
-    }
-    return f;
 }
 
 template <class T>
@@ -221,22 +232,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
     Shared &sh = *reinterpret_cast<Shared *>(align_shared<1024>(raw));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    // ---- pages before each chunk of sequences -------------------------------------------------
-    const int chunk = (a.B + kThreads - 1) / kThreads;
-    int own = 0;
-    bool empty = false;
-    for (int b = tid * chunk; b < (tid + 1) * chunk && b < a.B; b++) {
-        const Seq s = seq_of(a, b, blockIdx.x == 0);
-        own += head_pages(a, s) * a.Hkv;
-        empty |= s.n < s.nq;  // some rows see nothing: perhaps whole items
-    }
-    int inc = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-    }
-    if (lane == 31) sh.scan[warp] = inc;
+    __syncwarp();
+    if (warp == 0) tmem_alloc(&sh.tmem, 512);
     if (tid == 0) {
         sh.aborted = 0;
         for (int i = 0; i < kNS; i++) {
@@ -261,15 +258,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         mbar_init(&sh.drain, 2);
         fence_barrier_init();
     }
-    const bool any_empty = __syncthreads_or(empty);
-    int base = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kCtaWarps; w++) {
-        const int v = sh.scan[w];
-        base += w < warp ? v : 0;
-        total += v;
+    // ---- weight of the items before each chunk of sequences: a warp for each of a few, else a thread
+    const bool few = a.B <= 4 * kCtaWarps;
+    const int chunk = few ? 1 : (a.B + kThreads - 1) / kThreads;
+    int own = 0;
+    bool empty = false;  // some rows see nothing: perhaps whole items
+    if (few) {
+        for (int b = warp; b < a.B; b += kCtaWarps) {
+            const Seq s = seq_of(a, b, blockIdx.x == 0);
+            const int w = head_weight(a, s, lane) * a.Hkv;
+            if (lane == 0) sh.pre[b] = w;
+            empty |= s.n < s.nq;
+        }
+        empty = __syncthreads_or(empty);
+        if (tid < a.B) own = sh.pre[tid];
+    } else {
+        for (int b = tid * chunk; b < (tid + 1) * chunk && b < a.B; b++) {
+            const Seq s = seq_of(a, b, blockIdx.x == 0);
+            for (int rt = 0; rt < item_groups(a, s); rt++) own += item_weight(a, s, rt) * a.Hkv;
+            empty |= s.n < s.nq;
+        }
+        empty = __syncthreads_or(empty);
     }
-    sh.pre[tid] = base + inc - own;
+    const int inc = lane_scan(own, lane);
+    if (lane == 31) sh.scan[warp] = inc;
+    __syncthreads();
+    const int of_warp = lane_scan(lane < kCtaWarps ? sh.scan[lane] : 0, lane);
+    const int total = __shfl_sync(0xffffffffu, of_warp, 31);
+    const int before = __shfl_sync(0xffffffffu, of_warp, warp == 0 ? 0 : warp - 1);
+    sh.pre[tid] = (warp == 0 ? 0 : before) + inc - own;
+    const bool any_empty = empty;
     if (any_empty) {  // items that see nothing at all
         for (int u = blockIdx.x; u < a.B * a.Hkv; u += gridDim.x) {
             const int b = u / a.Hkv, h = u - b * a.Hkv;
@@ -279,8 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                 item_pages(a, s, rt, fp, np);
                 if (np > 0) break;  // later items see more
                 for (int k = tid; k < kRows * 64; k += kThreads) {
-                    const int64_t r = (int64_t)rt * kRows + (k >> 6);
-                    const int i = (int)(r / a.G), hq = h * a.G + (int)(r - (int64_t)i * a.G);
+                    const int r = rt * kRows + (k >> 6), i = div_g(a, r), hq = h * a.G + r - i * a.G;
                     if (i >= s.nq) break;
                     write_pair<T>(a, s.t0 + i, hq, 2 * (k & 63), 0.0f, 0.0f);
                     if (a.lse && (k & 63) == 0) a.lse[(int64_t)(s.t0 + i) * a.Hq + hq] = -INFINITY;
@@ -290,12 +307,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
     }
     const int ncta = total < (int)gridDim.x ? total : (int)gridDim.x;
     const int cta = blockIdx.x;
-    if (cta >= ncta) return;
-    __syncwarp();
-    if (warp == 0) tmem_alloc(&sh.tmem, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (cta >= ncta) {
+        __syncwarp();
+        if (warp == 0) tmem_free(sh.tmem, 512);
+        return;
+    }
     const uint32_t tmem = sh.tmem;
     const int c0 = (int)((int64_t)total * cta / ncta), c1 = (int)((int64_t)total * (cta + 1) / ncta);
 
@@ -312,20 +331,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         int rem = c0 - sh.pre[lo], hp = 0;
         for (b = lo * chunk; b < a.B; b++) {
             s = seq_of(a, b, false);
-            hp = head_pages(a, s);
+            hp = head_weight(a, s, lane);
             if (rem < hp * a.Hkv) break;
             rem -= hp * a.Hkv;
         }
         h = rem / hp;
         rem -= h * hp;
-        for (; !a.whole_items; rt++) {
-            int fp, np;
-            item_pages(a, s, rt, fp, np);
-            if (rem < np) break;
-            rem -= np;
+        for (;; rt += 32) {  // 32 items at a time
+            const int w = item_weight(a, s, rt + lane), upto = lane_scan(w, lane);
+            const uint32_t past = __ballot_sync(0xffffffffu, upto > rem);
+            if (past) {
+                const int k = __ffs(past) - 1;
+                rem -= __shfl_sync(0xffffffffu, upto - w, k);
+                rt += k;
+                break;
+            }
+            rem -= __shfl_sync(0xffffffffu, upto, 31);
         }
         at = a.whole_items ? 0 : rem;
-        if (a.whole_items) rt = rem;
     }
 
     // so far in the whole kernel, per role: steps (segments' ends among them), and pages (V tiles and
@@ -336,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         item_pages(a, s, rt, fp, np);
         const int cnt = a.whole_items || np - at < c1 - x ? np - at : c1 - x;
         const int j0 = fp + at, j1 = j0 + cnt;
-        const int64_t rows = (int64_t)s.nq * a.G - (int64_t)rt * kRows;  // of this item and later
+        const int row0 = rt * kRows, rows = s.nq * a.G - row0;  // rows: of this item and later
         const bool two = rows > kTile;
         const bool begins = at == 0, complete = begins && cnt == np;
         const int first = x - at;  // the item's first page among all
@@ -344,12 +367,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         // ---- queries
         const int grp = warp >> 2;  // 0, 1: softmax group
         const int r = tid & (kTile - 1);
-        const int64_t rr = (int64_t)rt * kRows + grp * kTile + r;
-        const int qi = (int)(rr / a.G), hq = h * a.G + (int)(rr - (int64_t)qi * a.G);
+        const int rr = row0 + grp * kTile + r, qi = div_g(a, rr);
         const bool have = grp < 2 && qi < s.nq;
-        float fs = 0.0f;
-        if (grp < 2 && !stopped(sh)) {
-            fs = load_query<T>(a, sh.q[grp], r, have, have ? s.t0 + qi : 0, have ? hq : 0);
+        if (!stopped(sh)) {
+            load_queries<T>(a, sh, s, h, row0, two ? kRows : kTile, warp, lane);
             fence_proxy_async();
         }
         tc_fence_before();
@@ -357,6 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         tc_fence_after();
         bool run = !stopped(sh);
         __syncthreads();  // nobody stops between the reading of it and this
+        const float fs = grp < 2 ? sh.factor[grp * kTile + r] : 0.0f;
 
         float m = -INFINITY, l = 0.0f;
         bool any = false, far = false;
@@ -368,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
             const int pos = s.n - s.nq + qi;
             const int from = a.window > 0 ? pos - a.window : -1;
             // positions of the tile's first and last row
-            const int lo = s.n - s.nq + (int)(((int64_t)rt * kRows + grp * kTile) / a.G);
+            const int lo = s.n - s.nq + div_g(a, row0 + grp * kTile);
             const int hi = s.n - 1 < lo + (kTile - 1) / a.G + 1 ? s.n - 1 : lo + (kTile - 1) / a.G + 1;
             while (true) {
                 const uint32_t buf = steps & 1;
@@ -610,11 +632,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         }
 
         // ---- the segment's results
+        // (a whole item's rows by way of the tile's queries, which are read no more, so that lines of
+        // out are written whole)
         float *mine = records + (int64_t)(kSlots * cta + (begins ? 1 : 0)) * kRecord;
         if (grp < 2 && run && (grp == 0 || two) && np > 0) {
             const uint32_t to = tmem + ((uint32_t)(warp & 3) << 21) + kColO + grp * 128;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             float *row = mine + grp * kTile + r;
+            uint8_t *stage = sh.q[grp];
 #pragma unroll 1
             for (int c = 0; c < 4; c++) {
                 uint32_t o[32];
@@ -626,10 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
 #pragma unroll
                     for (int e = 0; e < 32; e++) o[e] = 0;
                 }
-                if (have && complete) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(
-                        static_cast<uint16_t *>(a.out) +
-                        ((int64_t)(s.t0 + qi) * a.Hq + hq) * kD + 32 * c);
+                if (complete) {
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
                         uint32_t w[4];
@@ -637,16 +659,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                         for (int k = 0; k < 4; k++)
                             w[k] = T::pack(__uint_as_float(o[8 * e + 2 * k]) * inv,
                                            __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
-                        dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4 *>(stage + r * 256 + (((4 * c + e) ^ (r & 7)) << 4)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 } else if (have) {
 #pragma unroll
                     for (int e = 0; e < 32; e++) row[(32 * c + e) * kRows] = __uint_as_float(o[e]);
                 }
             }
+            if (complete) {
+                named_barrier_sync(1 + grp, kTile);
+#pragma unroll 4
+                for (int k = 0; k < 16; k++) {
+                    const int q = 32 * (warp & 3) + 2 * k + (lane >> 4), c = lane & 15;
+                    const int i = div_g(a, row0 + grp * kTile + q);
+                    if (i < s.nq)
+                        *reinterpret_cast<uint4 *>(
+                            static_cast<uint16_t *>(a.out) +
+                            ((int64_t)(s.t0 + i) * a.Hq + h * a.G + row0 + grp * kTile + q - i * a.G) *
+                                kD + 8 * c) =
+                            *reinterpret_cast<const uint4 *>(stage + q * 256 + ((c ^ (q & 7)) << 4));
+                }
+            }
             if (have) {
                 if (!complete) row[128 * kRows] = m, row[129 * kRows] = l;
-                else if (a.lse) a.lse[(int64_t)(s.t0 + qi) * a.Hq + hq] = lse_of(m - kShift, l);
+                else if (a.lse)
+                    a.lse[(int64_t)(s.t0 + qi) * a.Hq + h * a.G + rr - qi * a.G] = lse_of(m - kShift, l);
             }
         }
         if (!complete) {
@@ -655,41 +693,51 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
             __syncthreads();
             if (tid == 0) sh.flag = p.last_of_group(tickets);
             __syncthreads();
-            const int used = rows < kRows ? (int)rows : kRows;
-            // join records rec(0) .. rec(n - 1): 32 rows (one a lane) and 16 channels at a time
+            const int used = rows < kRows ? rows : kRows;
+            // join records rec(0) .. rec(n - 1): 32 rows (one a lane) and 8 channels at a time, the
+            // loads of five records together
             auto join = [&](auto rec, int n, auto done) {
-                for (int k = warp; k < 8 * ((used + 31) / 32); k += kCtaWarps) {
-                    const int q = 32 * (k >> 3) + lane, ch = 16 * (k & 7);
-                    float M = -INFINITY, ls = 0.0f, o[16] = {};
-#pragma unroll 4
-                    for (int i = 0; i < n; i++) M = fmaxf(M, __ldcg(rec(i) + 128 * kRows + q));
-#pragma unroll 2
-                    for (int i = 0; i < n; i++) {
-                        const float *from = rec(i) + q;
-                        float v[16];
+                for (int k = warp; k < 16 * ((used + 31) / 32); k += kCtaWarps) {
+                    const int q = 32 * (k >> 4) + lane, ch = 8 * (k & 15);
+                    float M = -INFINITY, ls = 0.0f, o[8] = {};
+                    for (int i0 = 0; i0 < n; i0 += 5) {
+                        float v[5][8], mn[5], ln[5];
 #pragma unroll
-                        for (int c = 0; c < 16; c++) v[c] = __ldcg(from + (ch + c) * kRows);
-                        const float mn = __ldcg(from + 128 * kRows), ln = __ldcg(from + 129 * kRows);
-                        const float f = mn == -INFINITY ? 0.0f : ex2_approx(mn - M);
+                        for (int i = 0; i < 5; i++) {
+                            const bool in = i0 + i < n;
+                            const float *from = rec(in ? i0 + i : i0) + q;
 #pragma unroll
-                        for (int c = 0; c < 16; c++) o[c] = fmaf(f, v[c], o[c]);
-                        ls = fmaf(f, ln, ls);
+                            for (int c = 0; c < 8; c++) v[i][c] = __ldcg(from + (ch + c) * kRows);
+                            mn[i] = in ? __ldcg(from + 128 * kRows) : -INFINITY;
+                            ln[i] = __ldcg(from + 129 * kRows);
+                        }
+                        float Mn = M;
+#pragma unroll
+                        for (int i = 0; i < 5; i++) Mn = fmaxf(Mn, mn[i]);
+                        const float al = M == -INFINITY ? 0.0f : ex2_approx(M - Mn);
+                        M = Mn;
+                        ls *= al;
+#pragma unroll
+                        for (int c = 0; c < 8; c++) o[c] *= al;
+#pragma unroll
+                        for (int i = 0; i < 5; i++) {
+                            if (mn[i] == -INFINITY) continue;  // nothing in it: o and l are 0
+                            const float f = ex2_approx(mn[i] - M);
+                            ls = fmaf(f, ln[i], ls);
+#pragma unroll
+                            for (int c = 0; c < 8; c++) o[c] = fmaf(f, v[i][c], o[c]);
+                        }
                     }
                     if (q < used) done(q, ch, M, ls, o);
                 }
             };
-            auto finish = [&](int q, int ch, float M, float ls, const float (&o)[16]) {
+            auto finish = [&](int q, int ch, float M, float ls, const float (&o)[8]) {
                 const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
-                const int64_t g = (int64_t)rt * kRows + q;
-                const int i = (int)(g / a.G), head = h * a.G + (int)(g - (int64_t)i * a.G);
+                const int i = div_g(a, row0 + q), head = h * a.G + row0 + q - i * a.G;
                 const int64_t at_row = (int64_t)(s.t0 + i) * a.Hq + head;
-                uint32_t w[8];
-#pragma unroll
-                for (int c = 0; c < 8; c++) w[c] = T::pack(o[2 * c] * inv, o[2 * c + 1] * inv);
-                uint4 *dst =
-                    reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at_row * kD + ch);
-                dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at_row * kD + ch) =
+                    make_uint4(T::pack(o[0] * inv, o[1] * inv), T::pack(o[2] * inv, o[3] * inv),
+                               T::pack(o[4] * inv, o[5] * inv), T::pack(o[6] * inv, o[7] * inv));
                 if (a.lse && ch == 0) a.lse[at_row] = lse_of(M - kShift, ls);
             };
             auto slot = [&](int c, int n) { return records + (int64_t)(kSlots * c + n) * kRecord; };
@@ -700,9 +748,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                     join(member, p.members, finish);
                 } else {
                     float *group = slot(p.g0, p.g0 == p.p0 ? 2 : 3);
-                    join(member, p.members, [&](int q, int ch, float M, float ls, const float (&o)[16]) {
+                    join(member, p.members, [&](int q, int ch, float M, float ls, const float (&o)[8]) {
 #pragma unroll
-                        for (int c = 0; c < 16; c++) group[(ch + c) * kRows + q] = o[c];
+                        for (int c = 0; c < 8; c++) group[(ch + c) * kRows + q] = o[c];
                         if (ch == 0) group[128 * kRows + q] = M, group[129 * kRows + q] = ls;
                     });
                     __syncthreads();

@@ -115,6 +115,7 @@ def attend(lib, p, ws_bytes=1 << 40, **kw):
     (dict(q_stride=1028), 1),
     (dict(batch=40000), 2),
     (dict(num_pages=1 << 30), 2),
+    (dict(max_q_len=1 << 27), 2),
     (dict(max_blocks_per_seq=1 << 24, batch=200, total_q=600), 2),
 ])
 def test_attention_refuses_params(lib, kw, status):
