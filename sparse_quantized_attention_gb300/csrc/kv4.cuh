@@ -113,6 +113,7 @@ struct RowsArgs {
 struct AttnArgs {
     int B, Hq, Hkv, G, P, max_blocks, max_q, total_q, window;
     int whole_items;  // chunk kernel: items are not cut
+    uint32_t over_g;  // ceil(2^32 / G), too large by less than G / 2^32 of it (G > 1)
     int64_t q_stride;
     float sm_scale;
     const void *q;

@@ -17,6 +17,7 @@ size_t decode_record_bytes(int cols);
 size_t chunk_record_bytes();
 int decode_slots();
 int chunk_slots();
+int chunk_once();
 int chunk_rows();
 int decode_warps(int cols);
 }  // namespace kv4
@@ -102,9 +103,28 @@ ffd_status check_params(const ffd_kv4_params *p) {
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 // At least this many pages (upper bound from the table's width) for each CTA.
-constexpr int64_t kMinDecodePages = 8, kMinChunkPages = 8;
+constexpr int64_t kMinDecodePages = 8, kMinChunkPages = 4;
 // Pages' time that cutting items costs a CTA of the chunk kernel (a second start, records, joins).
 constexpr int64_t kJoinPages = 16;
+
+// Pages of a cut item that a CTA of the chunk kernel takes at least, for items of n pages: cut in k
+// they take n / k pages' time and then that of the records that are joined one after another, k of
+// them or, cut in more than chunk_once(), about 2 sqrt(k) in two steps. A record of 256 rows is
+// written and joined in about 1.8 pages' time (2200 cycles a page, 4000 a record measured).
+int64_t chunk_pages(int64_t n, int64_t rows) {
+    const double record = 1.8 * (double)rows / chunk_rows() + 0.2;
+    double best = INFINITY;
+    int64_t pages = n;
+    for (int64_t k = 1; k <= 128 && k * kMinChunkPages <= n; k += k < 8 ? 1 : k / 4) {
+        const double joins = k == 1 ? 0.0 : k <= chunk_once() ? k : 2.0 * sqrt((double)k) + 2.0;
+        const double time = (double)n / k + record * joins;
+        if (time < best) {
+            best = time;
+            pages = (n + k - 1) / k;
+        }
+    }
+    return pages;
+}
 
 // Workspace: [error word | three join tickets per CTA | records per CTA | a parked state per warp of
 // the decode kernel]. The tickets, the only part that has to start at zero, have the same place and size
@@ -132,7 +152,13 @@ ffd_status make_plan(const ffd_kv4_params *p, Plan *pl) {
                 pl->whole_items = 1;
                 ctas = items;
             } else {
-                ctas = (items * p->max_blocks_per_seq + kMinChunkPages - 1) / kMinChunkPages;
+                int64_t most = p->max_blocks_per_seq;
+                if (p->window > 0) {
+                    const int64_t seen = ((int64_t)p->window + p->max_q_len) / kPage + 2;
+                    most = most < seen ? most : seen;
+                }
+                const int64_t least = chunk_pages(most, rows < chunk_rows() ? rows : chunk_rows());
+                ctas = (items * most + least - 1) / least;
             }
         }
     }
@@ -220,6 +246,7 @@ ffd_status ffd_kv4_attention(const ffd_kv4_params *params, const void *q, const 
     a.total_q = p.total_q;
     a.window = p.window;
     a.whole_items = pl.whole_items;
+    a.over_g = (uint32_t)(((uint64_t)1 << 32) / a.G + (((uint64_t)1 << 32) % a.G != 0));
     a.q_stride = p.q_stride ? p.q_stride : (int64_t)p.num_q_heads * kD;
     a.sm_scale = p.sm_scale;
     a.q = q;

@@ -35,7 +35,7 @@ constexpr int kRecord = 130 * kRows;   // floats of a joined item: o[128][row], 
 // Records of a CTA: of the item that goes on from before, of the one that begins there; of a group of
 // CTAs whose first one this is, where the item begins or goes on.
 constexpr int kSlots = 4;
-constexpr int kOnce = 5;               // records (133 KB each) that one CTA joins at once
+constexpr int kOnce = 8;               // records (133 KB each) that one CTA joins at once
 constexpr float kShift = 7.0f;         // P carries 2^7: with the lazy reference at most 2^15
 constexpr float kLazy = 8.0f;
 // Tensor memory columns: S of tile g and step j at 64 (2 g + j % 2), its first 32 columns P's place
@@ -62,9 +62,9 @@ struct Shared {
 };
 static_assert(sizeof(Shared) + 1024 <= 232448, "shared memory per CTA");
 
-// x / G for 0 <= x < 2^29 (m = ceil(2^32 / G) is off by less than G).
+// x / G for 0 <= x < 2^29.
 __device__ __forceinline__ int div_g(const AttnArgs &a, int x) {
-    return a.G == 1 ? x : (int)__umulhi((uint32_t)x, 0xffffffffu / (uint32_t)a.G + 1u);
+    return a.G == 1 ? x : (int)__umulhi((uint32_t)x, a.over_g);
 }
 
 __device__ __forceinline__ int item_groups(const AttnArgs &a, const Seq &s) {
@@ -815,6 +815,7 @@ cudaError_t launch(const AttnArgs &a, const Plan &pl, cudaStream_t stream) {
 
 int chunk_rows() { return kRows; }
 int chunk_slots() { return kSlots; }
+int chunk_once() { return kOnce; }
 size_t chunk_record_bytes() { return kRecord * sizeof(float); }
 
 cudaError_t launch_chunk(const AttnArgs &a, const Plan &pl, int dtype, cudaStream_t stream) {
