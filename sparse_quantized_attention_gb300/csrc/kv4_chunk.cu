@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
             const int g = warp - 16;
             const bool live = g == 0 || two, issuer = elect_one();
             const uint32_t k0 = smem_u32(sh.k[0]), v0 = smem_u32(sh.v[0]);
-            const uint64_t qd = tc_desc(smem_u32(sh.q[0]) + g * 32768);
+            const uint32_t qd = tc_desc(smem_u32(sh.q[0]) + g * 32768);
             // The scores of the next step, two ahead of the values: their place was P's of two steps
             // ago. False at the segment's end, which the softmax group learns of in the same way.
             auto next_scores = [&]() {
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                 tc_fence_after();
                 const int j = *reinterpret_cast<volatile int *>(&sh.info[steps % kInfo]);
                 const bool more = __any_sync(0xffffffffu, j >= 0);
-                const uint64_t kd = tc_desc(k0 + ks * 16384);
+                const uint32_t kd = tc_desc(k0 + ks * 16384);
                 if (issuer) {
                     if (more && live) {
 #pragma unroll
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                 if (!waited(a, sh, &sh.p_full[g][pstep & 1], (pstep >> 1) & 1)) break;
                 tc_fence_after();
                 const uint32_t p = tmem + col_s(g, pstep), d = tmem + kColO + g * 128;
-                const uint64_t vd = tc_desc(v0 + vs * 16384);
+                const uint32_t vd = tc_desc(v0 + vs * 16384);
                 if (issuer) {
                     if (live) {
 #pragma unroll

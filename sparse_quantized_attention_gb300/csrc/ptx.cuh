@@ -251,32 +251,33 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&x)[
 }
 
 // Shared-memory operand of a matrix instruction: K-major rows of 128 bytes with the 128-byte swizzle
-// (16-byte chunk c of row r at c ^ (r % 8)), groups of eight rows 1024 bytes apart; addr: the
-// operand's first byte, in a tile that is aligned to 1024 bytes.
-__device__ __forceinline__ uint64_t tc_desc(uint32_t addr) {
-    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
+// (16-byte chunk c of row r at c ^ (r % 8)), groups of eight rows 1024 bytes apart. The low word holds
+// the operand's first byte / 16 (in a tile that is aligned to 1024 bytes), the high one is the same for
+// all.
+__device__ __forceinline__ uint32_t tc_desc(uint32_t addr) { return (addr & 0x3ffff) >> 4 | 1u << 16; }
+constexpr uint32_t kTcDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
 // Instruction word of f16 x f16 -> f32, both operands K-major, M x N.
 constexpr uint32_t tc_idesc_f16(int m, int n) {
     return 1u << 4 | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
 }
 
 // D[tmem] (+)= A B^T of one 16-deep step, A and B in shared memory; one thread issues.
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "n"(kTcDescHigh)
         : "memory");
 }
 // The same with A in tensor memory (f16 pairs, one column per pair).
-__device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                           bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "n"(kTcDescHigh)
         : "memory");
 }
 // Arrive on `bar` once every matrix instruction that this thread has issued is done.
