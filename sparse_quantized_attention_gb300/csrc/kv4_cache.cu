@@ -25,31 +25,41 @@ __device__ __forceinline__ bool place(const RowsArgs &a, int t, int &page, int &
     return !bad;
 }
 
-// Code word of eight values x: nibble i + 4 e is value 2 i + e. The levels are quotients by products
-// with the reciprocal (relative error below 2^-21), rounded by adding 1.5 * 2^23 - 16, whose sum's
-// low bits are the level - 16; where one of the eight lies within 2e-5 of a boundary (31 * 2^-21 =
-// 1.5e-5) all are decided by the side of the boundary that x lies on.
-__device__ __forceinline__ uint32_t encode_word(const float *x, float s, float o, float inv) {
-    constexpr float kRound = 12582912.0f - 16.0f;
-    float t[8], u[8], off = 0.0f;
+// Code word of eight values: x[i] holds values 2 i and 2 i + 1, nibbles i and i + 4. With inv15 =
+// 1 / (15 scale), y = sat((x - off) inv15 - 16 / 15) is the clamped code / 15, off by less than 7e-7 (four
+// roundings of 2^-24 on a product below 2.1, two on the sum); 15 y is rounded by adding 1.5 * 2^23.
+// Where one of the eight lies within 2e-5 of a boundary (15 * 7e-7 = 1.1e-5) it is decided by the side
+// of the boundary that x lies on. Codes are put together as numbers of 16 bits.
+__device__ __forceinline__ uint32_t encode_word(const float2 *x, float s, float o, float inv15) {
+    constexpr float kRound = 12582912.0f;
+    const float2 round = make_float2(kRound, kRound), back = make_float2(-kRound, -kRound);
+    const float2 no = make_float2(-o, -o), fifteen = make_float2(15.0f, 15.0f);
+    float2 y[4], r[4];
+    float off = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        t[i] = fminf(fmaxf(__fmul_rn(__fsub_rn(x[i], o), inv), 16.0f), 31.0f);
-        u[i] = __fadd_rn(t[i], kRound);
-        off = fmaxf(off, fabsf(__fsub_rn(t[i], __fsub_rn(u[i], kRound))));
+    for (int i = 0; i < 4; i++) {
+        const float2 d = __fadd2_rn(x[i], no);
+        y[i] = make_float2(fma_sat(d.x, inv15, -16.0f / 15.0f), fma_sat(d.y, inv15, -16.0f / 15.0f));
+        r[i] = __fadd2_rn(__ffma2_rn(y[i], fifteen, round), back);
+        const float2 e = __ffma2_rn(y[i], fifteen, make_float2(-r[i].x, -r[i].y));
+        off = fmaxf(off, fmaxf(fabsf(e.x), fabsf(e.y)));
     }
     if (off > 0.5f - 2e-5f) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const float lo = floorf(t[i]);
-            if (fabsf(t[i] - lo - 0.5f) < 2e-5f)
-                u[i] = __fadd_rn(boundary_level(x[i], lo, s, o), kRound);
-        }
-    }
-    uint32_t w = 0;
+        for (int i = 0; i < 4; i++)
 #pragma unroll
-    for (int i = 0; i < 8; i++) w += __float_as_uint(u[i]) << (4 * ((i >> 1) + 4 * (i & 1)));
-    return w - 0x4b400000u * 0x11111111u;  // the sums' common part
+            for (int e = 0; e < 2; e++) {
+                const float t = 15.0f * (e ? y[i].y : y[i].x), lo = floorf(t);
+                if (fabsf(t - lo - 0.5f) < 2e-5f)
+                    (e ? r[i].y : r[i].x) =
+                        boundary_level(e ? x[i].y : x[i].x, lo + 16.0f, s, o) - 16.0f;
+            }
+    }
+    float2 h = __ffma2_rn(r[1], make_float2(16.0f, 16.0f), r[0]);
+    h = __ffma2_rn(r[2], make_float2(256.0f, 256.0f), h);
+    h = __ffma2_rn(r[3], make_float2(4096.0f, 4096.0f), h);
+    h = __fadd2_rn(h, round);  // the low 16 bits are the number
+    return __byte_perm(__float_as_uint(h.x), __float_as_uint(h.y), 0x5410);
 }
 
 // Writing: a block takes 32 rows of one KV head, a thread one group of 32 channels of K or of V. The
@@ -84,27 +94,25 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const RowsArgs a, const 
         if (bad) raise_error(a.err, FFD_ERRBIT_BOUNDS);
         return;
     }
-    float x[32];
-    float lo = INFINITY, hi = -INFINITY, sum = 0.0f;
+    float2 x[16];
+#pragma unroll
+    for (int j = 0; j < 16; j++) x[j] = T::unpack(w[j]);
+    float lo = x[0].x, hi = x[0].x;
 #pragma unroll
     for (int j = 0; j < 16; j++) {
-        const float2 f = T::unpack(w[j]);
-        x[2 * j] = f.x;
-        x[2 * j + 1] = f.y;
-        lo = fminf(lo, fminf(f.x, f.y));
-        hi = fmaxf(hi, fmaxf(f.x, f.y));
-        sum += f.x * 0.0f + f.y * 0.0f;  // NaN when one of them is NaN or infinite
+        lo = min3(lo, x[j].x, x[j].y);
+        hi = max3_nan(hi, x[j].x, x[j].y);
     }
-    if (!(lo >= -kMaxInput && hi <= kMaxInput && sum == 0.0f)) raise_error(a.err, FFD_ERRBIT_RANGE);
+    if (!(lo >= -kMaxInput && hi <= kMaxInput)) raise_error(a.err, FFD_ERRBIT_RANGE);
     const __half hs = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
     const float s = __half2float(hs);
     const __half ho = __float2half_rn(__fmaf_rn(-16.0f, s, lo));
     const float o = __half2float(ho);
-    const float inv = s > 0.0f ? __frcp_rn(s) : 0.0f;  // 0: every level clamps to 16
+    const float inv15 = s > 0.0f ? __frcp_rn(s) * (1.0f / 15.0f) : 0.0f;  // 0: every code is 0
     uint8_t *rec = (is_v ? v4 : k4) + ((int64_t)page * a.Hkv + h) * kRec;
     *reinterpret_cast<uint4 *>(rec + code_offset(r, g)) =
-        make_uint4(encode_word(x, s, o, inv), encode_word(x + 8, s, o, inv),
-                   encode_word(x + 16, s, o, inv), encode_word(x + 24, s, o, inv));
+        make_uint4(encode_word(x, s, o, inv15), encode_word(x + 4, s, o, inv15),
+                   encode_word(x + 8, s, o, inv15), encode_word(x + 12, s, o, inv15));
     *reinterpret_cast<__half2 *>(rec + param_offset(r, g)) = __halves2half2(hs, ho);
 }
 

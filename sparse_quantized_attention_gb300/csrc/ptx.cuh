@@ -178,6 +178,25 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     return y;
 }
 
+// Smallest, and largest (NaN when one of them is), of three.
+__device__ __forceinline__ float min3(float x, float y, float z) {
+    float r;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+__device__ __forceinline__ float max3_nan(float x, float y, float z) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
+// x y + z clamped to [0, 1] (NaN: 0).
+__device__ __forceinline__ float fma_sat(float x, float y, float z) {
+    float r;
+    asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
 // 2^x from the special-function unit (approximate, relative error about 2^-22; 2^-inf = +0).
 __device__ __forceinline__ float ex2_approx(float x) {
     float y;
