@@ -31,6 +31,17 @@ struct Bf16 {
         const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
         return *reinterpret_cast<const uint32_t *>(&v);
     }
+    // of pairs, each half for itself: the smaller, and the larger (NaN when one of them is)
+    static __device__ __forceinline__ uint32_t min2(uint32_t x, uint32_t y) {
+        uint32_t r;
+        asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t max2_nan(uint32_t x, uint32_t y) {
+        uint32_t r;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+        return r;
+    }
     // the f16 pair h, rounded to this type
     static __device__ __forceinline__ uint32_t from_half2(__half2 h) {
         const float2 f = __half22float2(h);
@@ -44,6 +55,17 @@ struct F16 {
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
         const __half2 v = __floats2half2_rn(lo, hi);
         return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    // of pairs, each half for itself: the smaller, and the larger (NaN when one of them is)
+    static __device__ __forceinline__ uint32_t min2(uint32_t x, uint32_t y) {
+        uint32_t r;
+        asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t max2_nan(uint32_t x, uint32_t y) {
+        uint32_t r;
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+        return r;
     }
     static __device__ __forceinline__ uint32_t from_half2(__half2 h) {
         return *reinterpret_cast<const uint32_t *>(&h);

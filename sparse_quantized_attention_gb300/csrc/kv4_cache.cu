@@ -25,12 +25,13 @@ __device__ __forceinline__ bool place(const RowsArgs &a, int t, int &page, int &
     return !bad;
 }
 
-// Code word of eight values: x[i] holds values 2 i and 2 i + 1, nibbles i and i + 4. With inv15 =
+// Code word of eight values: w[i] holds values 2 i and 2 i + 1, nibbles i and i + 4. With inv15 =
 // 1 / (15 scale), y = sat((x - off) inv15 - 16 / 15) is the clamped code / 15, off by less than 7e-7 (four
 // roundings of 2^-24 on a product below 2.1, two on the sum); 15 y is rounded by adding 1.5 * 2^23.
 // Where one of the eight lies within 2e-5 of a boundary (15 * 7e-7 = 1.1e-5) it is decided by the side
 // of the boundary that x lies on. Codes are put together as numbers of 16 bits.
-__device__ __forceinline__ uint32_t encode_word(const float2 *x, float s, float o, float inv15) {
+template <class T>
+__device__ __forceinline__ uint32_t encode_word(const uint32_t *w, float s, float o, float inv15) {
     constexpr float kRound = 12582912.0f;
     const float2 round = make_float2(kRound, kRound), back = make_float2(-kRound, -kRound);
     const float2 no = make_float2(-o, -o), fifteen = make_float2(15.0f, 15.0f);
@@ -38,7 +39,7 @@ __device__ __forceinline__ uint32_t encode_word(const float2 *x, float s, float 
     float off = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        const float2 d = __fadd2_rn(x[i], no);
+        const float2 d = __fadd2_rn(T::unpack(w[i]), no);
         y[i] = make_float2(fma_sat(d.x, inv15, -16.0f / 15.0f), fma_sat(d.y, inv15, -16.0f / 15.0f));
         r[i] = __fadd2_rn(__ffma2_rn(y[i], fifteen, round), back);
         const float2 e = __ffma2_rn(y[i], fifteen, make_float2(-r[i].x, -r[i].y));
@@ -46,14 +47,15 @@ __device__ __forceinline__ uint32_t encode_word(const float2 *x, float s, float 
     }
     if (off > 0.5f - 2e-5f) {
 #pragma unroll
-        for (int i = 0; i < 4; i++)
+        for (int i = 0; i < 4; i++) {
+            const float2 x = T::unpack(w[i]);
 #pragma unroll
             for (int e = 0; e < 2; e++) {
                 const float t = 15.0f * (e ? y[i].y : y[i].x), lo = floorf(t);
                 if (fabsf(t - lo - 0.5f) < 2e-5f)
-                    (e ? r[i].y : r[i].x) =
-                        boundary_level(e ? x[i].y : x[i].x, lo + 16.0f, s, o) - 16.0f;
+                    (e ? r[i].y : r[i].x) = boundary_level(e ? x.y : x.x, lo + 16.0f, s, o) - 16.0f;
             }
+        }
     }
     float2 h = __ffma2_rn(r[1], make_float2(16.0f, 16.0f), r[0]);
     h = __ffma2_rn(r[2], make_float2(256.0f, 256.0f), h);
@@ -94,15 +96,14 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const RowsArgs a, const 
         if (bad) raise_error(a.err, FFD_ERRBIT_BOUNDS);
         return;
     }
-    float2 x[16];
+    uint32_t least = w[0], most = w[0];
 #pragma unroll
-    for (int j = 0; j < 16; j++) x[j] = T::unpack(w[j]);
-    float lo = x[0].x, hi = x[0].x;
-#pragma unroll
-    for (int j = 0; j < 16; j++) {
-        lo = min3(lo, x[j].x, x[j].y);
-        hi = max3_nan(hi, x[j].x, x[j].y);
+    for (int j = 1; j < 16; j++) {
+        least = T::min2(least, w[j]);
+        most = T::max2_nan(most, w[j]);
     }
+    const float2 l2 = T::unpack(least), m2 = T::unpack(most);
+    const float lo = fminf(l2.x, l2.y), hi = max_nan(m2.x, m2.y);
     if (!(lo >= -kMaxInput && hi <= kMaxInput)) raise_error(a.err, FFD_ERRBIT_RANGE);
     const __half hs = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
     const float s = __half2float(hs);
@@ -111,8 +112,8 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const RowsArgs a, const 
     const float inv15 = s > 0.0f ? __frcp_rn(s) * (1.0f / 15.0f) : 0.0f;  // 0: every code is 0
     uint8_t *rec = (is_v ? v4 : k4) + ((int64_t)page * a.Hkv + h) * kRec;
     *reinterpret_cast<uint4 *>(rec + code_offset(r, g)) =
-        make_uint4(encode_word(x, s, o, inv15), encode_word(x + 4, s, o, inv15),
-                   encode_word(x + 8, s, o, inv15), encode_word(x + 12, s, o, inv15));
+        make_uint4(encode_word<T>(w, s, o, inv15), encode_word<T>(w + 4, s, o, inv15),
+                   encode_word<T>(w + 8, s, o, inv15), encode_word<T>(w + 12, s, o, inv15));
     *reinterpret_cast<__half2 *>(rec + param_offset(r, g)) = __halves2half2(hs, ho);
 }
 

@@ -178,15 +178,10 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     return y;
 }
 
-// Smallest, and largest (NaN when one of them is), of three.
-__device__ __forceinline__ float min3(float x, float y, float z) {
+// Larger of two, NaN when one of them is.
+__device__ __forceinline__ float max_nan(float x, float y) {
     float r;
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
-    return r;
-}
-__device__ __forceinline__ float max3_nan(float x, float y, float z) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
     return r;
 }
 
