@@ -142,6 +142,53 @@ def test_special_groups(kind):
         assert torch.equal(out.cpu().double(), R.held64(y)), kind
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
+def test_values_next_to_a_boundary(dtype):
+    """Values a step of the type below, at and above every boundary between two codes, for many
+    scales that are no powers of two."""
+    gen = torch.Generator().manual_seed(8)
+    T, Hkv = 500, 3
+    lo = torch.randn((T, Hkv, 4, 1), generator=gen)
+    hi = lo + 2.0 ** (6 * torch.rand((T, Hkv, 4, 1), generator=gen) - 4)
+    lo, hi = lo.to(dtype), hi.to(dtype)
+    scale = ((hi.float() - lo.float()) / 15).half().double()
+    off = (lo.double() - 16 * scale).half().double()
+    x = off + (16.5 + torch.randint(0, 15, (T, Hkv, 4, 32), generator=gen)) * scale
+    x = x.to(dtype)
+    bits = x.view(torch.int16) + torch.randint(-1, 2, x.shape, generator=gen).to(torch.int16)
+    x = torch.where(x.float().abs() > 1e-3, bits.view(dtype), x)
+    x = torch.maximum(torch.minimum(x, hi), lo)
+    x[..., 5:6], x[..., 20:21] = lo, hi
+    x = x.reshape(T, Hkv, 128)
+    bt, P = table([T], gen)
+    cache = ffd.alloc_kv4_cache(P, Hkv)
+    ffd.ffd_kv4_write(x.cuda(), x.cuda(), i32([0]), bt.cuda(), cache)
+    out = torch.empty((2, T, Hkv, 128), dtype=F16, device="cuda")
+    ffd.ffd_kv4_read(cache, i32([0]), bt.cuda(), out[0], out[1])
+    want = R.held64(x)
+    assert torch.equal(out[0].cpu().double(), want) and torch.equal(out[1].cpu().double(), want)
+
+
+@pytest.mark.parametrize("shift", [0, 8])
+def test_rows_at_any_alignment(shift):
+    """Rows 16 or 32 bytes aligned, of both widths, give the same records and values."""
+    gen = torch.Generator().manual_seed(9)
+    T, Hkv = 130, 2
+    x = torch.randn((T, Hkv, 128), generator=gen).to(BF16)
+    bt, P = table([T], gen)
+    for pad in (0, 8, 16):
+        wide = torch.zeros((T, Hkv * 128 + pad + shift), dtype=BF16, device="cuda")
+        rows = wide[:, shift:shift + Hkv * 128].unflatten(1, (Hkv, 128))
+        rows.copy_(x)
+        cache = ffd.alloc_kv4_cache(P, Hkv)
+        ffd.ffd_kv4_write(rows, rows, i32([0]), bt.cuda(), cache)
+        back = torch.full_like(wide, 7.0)
+        out = back[:, shift:shift + Hkv * 128].unflatten(1, (Hkv, 128))
+        ffd.ffd_kv4_read(cache, i32([0]), bt.cuda(), None, out)
+        assert torch.equal(out.cpu().double(), R.held64(x).half().to(BF16).double())
+        assert bool((back[:, :shift] == 7).all()) and bool((back[:, shift + Hkv * 128:] == 7).all())
+
+
 def test_write_and_read_skip_and_report():
     gen = torch.Generator().manual_seed(6)
     Hkv, B = 2, 3
@@ -274,6 +321,8 @@ DECODE = [
     ("mask_none", dict(lens=[3000, 64], qlens=[1, 1], Hkv=2, G=4, keep=0.0)),
     ("no_queries", dict(lens=[300, 200, 100], qlens=[0, 1, 0], Hkv=2, G=4)),
     ("many_short", dict(lens=[1 + 7 * i % 150 for i in range(300)], qlens=[1] * 300, Hkv=2, G=4)),
+    ("very_many", dict(lens=[5 * i % 97 for i in range(1100)], qlens=[i % 3 for i in range(1100)],
+                       Hkv=2, G=2)),
     ("long", dict(lens=[131072 - 5], qlens=[1], Hkv=1, G=4)),
     ("windows", dict(lens=[300000, 5, 100000], qlens=[1, 1, 1], Hkv=2, G=4, splits=3)),
     ("windows_mask", dict(lens=[300000, 5, 100000], qlens=[1, 3, 2], Hkv=2, G=4, keep=0.05,
@@ -300,6 +349,11 @@ SEVERAL = [
     ("chunk_large_q", dict(lens=[500], qlens=[100], Hkv=1, G=4, q_scale=1e9)),
     ("chunk_tiny_q", dict(lens=[500], qlens=[100], Hkv=1, G=4, q_scale=1e-20)),
     ("chunk_long", dict(lens=[20000], qlens=[64], Hkv=2, G=7)),
+    ("chunk_many", dict(lens=[1 + 11 * i % 170 for i in range(100)],
+                        qlens=[41 * i % 50 for i in range(100)], Hkv=2, G=3)),
+    ("chunk_very_many", dict(lens=[3 * i % 130 for i in range(700)],
+                             qlens=[i % 40 for i in range(700)], Hkv=1, G=2)),
+    ("chunk_many_long", dict(lens=[40 * i for i in range(90)], qlens=[40] * 90, Hkv=1, G=4)),
     ("tails", dict(lens=[100, 90], qlens=[20, 30], Hkv=2, G=4, tail=11, max_q=77)),
     ("mixed", dict(lens=[9000, 77, 600, 128], qlens=[1, 40, 0, 128], Hkv=2, G=6, stride_pad=8)),
 ]
