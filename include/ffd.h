@@ -441,7 +441,7 @@ ffd_status ffd_decode_attention_static(const ffd_decode_params *params, const vo
  *   k_new, v_new  device [T][Hkv][128], rows k_stride / v_stride elements apart (>= Hkv * 128 and a
  *                 multiple of 8, so that they may lie inside a fused projection), 16-byte aligned
  *   cu_tokens     device int32 [B+1], non-decreasing: sequence b has rows cu[b] .. cu[b+1]-1. Rows
- *                 before cu[0] and from cu[B] on belong to nobody and are not read. NULL: T is a
+ *                 before cu[0] and from cu[B] on belong to nobody and go nowhere. NULL: T is a
  *                 multiple of B and every sequence has T / B rows.
  *   positions     device int32 [B]: token index of the sequence's first row; a negative entry
  *                 writes nothing for that sequence
@@ -527,7 +527,7 @@ size_t ffd_kv4_workspace_size(const ffd_kv4_params *params);
  *               sequence sees (past n, behind the window, dropped by keep_in) are not read
  *   keep_in     device u8 [B][Hkv][max_blocks_per_seq] or NULL: nonzero = the block may be seen
  *               (for instance ffd_select_blocks's mask, or a decode step's keep_mask)
- *   out         device [total_q][Hq][128] of dtype, 16-byte aligned
+ *   out         device [total_q][Hq][128] of dtype, 16-byte aligned; it must not overlap q
  *   lse         device fp32 [total_q][Hq] or NULL
  *   workspace   device, >= ffd_kv4_workspace_size(params) bytes, 256-byte aligned; its first 4
  *               bytes are the device error word. Zero-fill it once before first use; each call

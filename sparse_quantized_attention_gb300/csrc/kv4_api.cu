@@ -134,6 +134,9 @@ ffd_status make_plan(const ffd_kv4_params *p, Plan *pl) {
     const ffd_status st = check_params(p);
     if (st != FFD_OK) return st;
     const int64_t rows = (int64_t)p->max_q_len * (p->num_q_heads / p->num_kv_heads);
+    // Up to 32 rows a KV head the kernel whose warps walk pages alone is the faster one, above it the one
+    // that forms tiles for tcgen05: eight sequences of 5000 to 16384 tokens take 58 us for 24 rows and
+    // 86 us for 32 in the first, and 98 to 100 us for 24 as for 36 rows in the second.
     pl->cols = rows <= 32 ? (int)(rows + 7) / 8 * 8 : 0;
     const int sms = current_sm_count();
     const int64_t units = (int64_t)p->batch * p->num_kv_heads;
@@ -145,7 +148,9 @@ ffd_status make_plan(const ffd_kv4_params *p, Plan *pl) {
             ctas = (units * p->max_blocks_per_seq + kMinDecodePages - 1) / kMinDecodePages;
         } else {
             // An item (256 rows over the pages they see) goes to one CTA when the pages that the
-            // longest-working CTA then has beyond an equal share cost less than cutting items does.
+            // longest-working CTA then has beyond an equal share cost less than cutting items does
+            // (three prompts of 362 tokens, 4 heads: 25 us whole, 55 us cut; 256 rows of one
+            // sequence of 32768: 243 us whole, 107 us cut, before records were joined in groups).
             const int64_t items = units * ((rows + chunk_rows() - 1) / chunk_rows());
             const int64_t rounds = (items + sms - 1) / sms;
             if ((rounds * sms - items) * p->max_blocks_per_seq <= kJoinPages * sms) {
@@ -235,6 +240,11 @@ ffd_status ffd_kv4_attention(const ffd_kv4_params *params, const void *q, const 
     const ffd_kv4_params &p = *params;
     if (!cu_q && p.total_q != (int64_t)p.batch * p.max_q_len) return FFD_ERR_INVALID_ARG;
     if (workspace_bytes < pl.total) return FFD_ERR_WORKSPACE;
+    const int64_t row = (int64_t)p.num_q_heads * kD, stride = p.q_stride ? p.q_stride : row;
+    const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
+    if (q0 < o0 + (uintptr_t)(2 * p.total_q * row) &&
+        o0 < q0 + (uintptr_t)(2 * ((p.total_q - 1) * stride + row)))
+        return FFD_ERR_INVALID_ARG;  // q is read by several CTAs, at their own times
     AttnArgs a{};
     a.B = p.batch;
     a.Hq = p.num_q_heads;
@@ -247,7 +257,7 @@ ffd_status ffd_kv4_attention(const ffd_kv4_params *params, const void *q, const 
     a.window = p.window;
     a.whole_items = pl.whole_items;
     a.over_g = (uint32_t)(((uint64_t)1 << 32) / a.G + (((uint64_t)1 << 32) % a.G != 0));
-    a.q_stride = p.q_stride ? p.q_stride : (int64_t)p.num_q_heads * kD;
+    a.q_stride = stride;
     a.sm_scale = p.sm_scale;
     a.q = q;
     a.k4 = k4;

@@ -143,6 +143,15 @@ def test_attention_refuses_shapes_and_pointers(lib):
     assert attend(lib, params(total_q=5), cu=None) == 1
 
 
+def test_attention_refuses_out_over_q(lib):
+    p = params()                        # q and out are 6 rows of 8 heads: 12288 bytes each
+    assert attend(lib, p) == 1
+    assert attend(lib, p, out=FAKE + 12288 - 16) == 1
+    assert attend(lib, p, q=FAKE + 12288 - 16) == 1
+    p = params(q_stride=2048)           # out between the first and the second row of q
+    assert attend(lib, p, out=FAKE + 2048) == 1
+
+
 def test_binding_refuses_tensors(lib):
     """CPU tensors and wrong shapes or types never reach a kernel."""
     bt = torch.zeros((2, 3), dtype=torch.int32)
