@@ -487,7 +487,7 @@ typedef struct {
     int32_t page_size;          /* must be 64 */
     int32_t num_pages;          /* P, bound for block_table entries; P * Hkv <= INT32_MAX */
     int32_t max_blocks_per_seq; /* row stride of block_table; seq_lens[b] <= 64 * this; B * Hkv *
-                                   this * ceil(max_q_len * G / 256) <= INT32_MAX */
+                                   (this + 9) * ceil(max_q_len * G / 256) <= INT32_MAX */
     int32_t dtype;              /* FFD_DTYPE_BF16 or FFD_DTYPE_F16, of q and out */
     int32_t max_q_len;          /* >= 1, the most query tokens of one sequence; this * G <= 2^28 */
     int32_t total_q;            /* >= 1, rows of q, out and lse */

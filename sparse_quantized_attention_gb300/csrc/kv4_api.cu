@@ -92,7 +92,7 @@ ffd_status check_params(const ffd_kv4_params *p) {
     if ((int64_t)p->max_blocks_per_seq * kPage > INT32_MAX) return FFD_ERR_UNSUPPORTED;
     // a record is named by an int32, and so is a page of a unit for each group of rows that takes it
     if ((int64_t)p->num_pages * p->num_kv_heads > INT32_MAX) return FFD_ERR_UNSUPPORTED;
-    const int64_t pages = (int64_t)p->batch * p->num_kv_heads * p->max_blocks_per_seq;
+    const int64_t pages = (int64_t)p->batch * p->num_kv_heads * ((int64_t)p->max_blocks_per_seq + kChunkLead);
     const int64_t rows = (int64_t)p->max_q_len * (p->num_q_heads / p->num_kv_heads);
     if (rows > kMaxRows || pages > INT32_MAX ||
         pages > INT32_MAX / ((rows + chunk_rows() - 1) / chunk_rows()))
@@ -104,8 +104,9 @@ size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 // At least this many pages (upper bound from the table's width) for each CTA.
 constexpr int64_t kMinDecodePages = 8, kMinChunkPages = 4;
-// Pages' time that cutting items costs a CTA of the chunk kernel (a second start, records, joins).
-constexpr int64_t kJoinPages = 16;
+// Pages' time that cutting items costs a CTA of the chunk kernel (a second start, records, joins): when
+// it takes one item, and when it takes several and has two of them cut.
+constexpr double kJoinPages = 24.0, kJoinPagesSeveral = 39.0;
 
 // Pages of a cut item that a CTA of the chunk kernel takes at least, for items of n pages: cut in k
 // they take n / k pages' time and then that of the records that are joined one after another, k of
@@ -126,6 +127,27 @@ int64_t chunk_pages(int64_t n, int64_t rows) {
     return pages;
 }
 
+// Where whole items (256 rows over the pages they see) are dealt out, `rounds` consecutive ones to a CTA:
+// the pages' time that the longest-working CTA has beyond an equal share. Some CTAs have an item
+// fewer, and the groups of rows of a unit see from first to last as many more pages as there are query
+// tokens (less behind a window). While that is less than what cutting costs, whole items are the
+// faster way. Measured, us whole and cut, 8 heads and 4 query heads for each:
+//   9 sequences of 1024 tokens, their last 128     2 beyond           33   56
+//   2 of 4096, 512                                17                  83   89
+//   1 of 4096, 1024                               23                  82   92
+//   3 of 4096, 256                                28                  82   77
+//   8 of 2048, 512                                38, several items   143  158
+//   3 of 1024, 1024                               41, several         88   76
+//   1 of 8192, 8192                               over 600, several   1030 592
+double longest_beyond(const ffd_kv4_params *p, int64_t rounds, int64_t groups, int64_t items, int sms) {
+    const int64_t tokens = (int64_t)p->max_blocks_per_seq * kPage;
+    const int64_t seen = p->window > 0 && p->window < tokens ? p->window : tokens;
+    const int64_t before = tokens > p->max_q_len ? tokens - p->max_q_len : 0;
+    const double rise = (double)(seen - (seen < before ? seen : before)) / kPage;
+    const double fewer = (double)(rounds * sms - items) * ((double)seen / kPage + kChunkLead) / sms;
+    return fewer + (rounds < groups ? 0.75 * rounds * rise * (1.0 - (double)rounds / groups) : 0.0);
+}
+
 // Workspace: [error word | three join tickets per CTA | records per CTA | a parked state per warp of
 // the decode kernel]. The tickets, the only part that has to start at zero, have the same place and size
 // whatever the parameters and are left at zero, so that calls of different shapes can share a
@@ -134,9 +156,9 @@ ffd_status make_plan(const ffd_kv4_params *p, Plan *pl) {
     const ffd_status st = check_params(p);
     if (st != FFD_OK) return st;
     const int64_t rows = (int64_t)p->max_q_len * (p->num_q_heads / p->num_kv_heads);
-    // Up to 32 rows a KV head the kernel whose warps walk pages alone is the faster one, above it the one
-    // that forms tiles for tcgen05: eight sequences of 5000 to 16384 tokens take 58 us for 24 rows and
-    // 86 us for 32 in the first, and 98 to 100 us for 24 as for 36 rows in the second.
+    // Up to 32 rows a KV head the kernel whose warps walk pages alone is the faster one, above it only the
+    // one that forms tiles for tcgen05 is left: eight sequences of 5000 to 16384 tokens, 8 heads, take
+    // 36, 50, 58 and 86 us for 8, 16, 24 and 32 rows in the first and 96 to 97 us in the second (98 for 36).
     pl->cols = rows <= 32 ? (int)(rows + 7) / 8 * 8 : 0;
     const int sms = current_sm_count();
     const int64_t units = (int64_t)p->batch * p->num_kv_heads;
@@ -147,21 +169,19 @@ ffd_status make_plan(const ffd_kv4_params *p, Plan *pl) {
         if (pl->cols) {
             ctas = (units * p->max_blocks_per_seq + kMinDecodePages - 1) / kMinDecodePages;
         } else {
-            // An item (256 rows over the pages they see) goes to one CTA when the pages that the
-            // longest-working CTA then has beyond an equal share cost less than cutting items does
-            // (three prompts of 362 tokens, 4 heads: 25 us whole, 55 us cut; 256 rows of one
-            // sequence of 32768: 243 us whole, 107 us cut, before records were joined in groups).
-            const int64_t items = units * ((rows + chunk_rows() - 1) / chunk_rows());
+            const int64_t blocks = p->max_blocks_per_seq;
+            const int64_t groups = (rows + chunk_rows() - 1) / chunk_rows(), items = units * groups;
             const int64_t rounds = (items + sms - 1) / sms;
-            if ((rounds * sms - items) * p->max_blocks_per_seq <= kJoinPages * sms) {
+            int64_t most = blocks;  // pages that an item sees at most
+            if (p->window > 0) {
+                const int64_t seen = ((int64_t)p->window + p->max_q_len) / kPage + 2;
+                most = most < seen ? most : seen;
+            }
+            if (longest_beyond(p, rounds, groups, items, sms) <=
+                (rounds > 1 ? kJoinPagesSeveral : kJoinPages)) {
                 pl->whole_items = 1;
                 ctas = items;
             } else {
-                int64_t most = p->max_blocks_per_seq;
-                if (p->window > 0) {
-                    const int64_t seen = ((int64_t)p->window + p->max_q_len) / kPage + 2;
-                    most = most < seen ? most : seen;
-                }
                 const int64_t least = chunk_pages(most, rows < chunk_rows() ? rows : chunk_rows());
                 ctas = (items * most + least - 1) / least;
             }

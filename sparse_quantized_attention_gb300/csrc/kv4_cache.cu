@@ -64,9 +64,15 @@ __device__ __forceinline__ uint32_t encode_word(const uint32_t *w, float s, floa
     return __byte_perm(__float_as_uint(h.x), __float_as_uint(h.y), 0x5410);
 }
 
-// Writing: a block takes 32 rows of one KV head, a thread one group of 32 channels of K or of V. The
-// eight threads of a row sit together and rows follow one another, so a prompt's records are written
-// in whole lines.
+// Writing: a block takes 32 rows of one KV head, a thread one group of 32 channels of K or of V: its
+// least and largest value need no other thread. The eight threads of a row sit together and rows
+// follow one another, so a prompt's records are written in whole lines.
+//
+// What has to move is 256 B of a tensor's row in and 80 B out; what bounds it is issue: about 10.5 thread
+// instructions a value (54 % of DRAM's rate, 2.8 instructions a cycle). So the least and largest are
+// taken of packed pairs, sums and products of coding are packed too, the clamp is a product's saturation,
+// and values are unpacked again where they are coded, which keeps to 48 registers and five blocks an
+// SM (40 registers, six blocks: spills, 4 % slower).
 template <class T, bool kWide>
 __global__ void __launch_bounds__(256) kv4_write_kernel(const RowsArgs a, const uint16_t *k,
                                                         const uint16_t *v, uint8_t *k4,
@@ -118,7 +124,8 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const RowsArgs a, const 
 }
 
 // Reading: a block takes 64 rows of one KV head, a thread sixteen channels of two rows (32 apart), of
-// K and of V.
+// K and of V: four loads in flight a thread, and eight threads write a row's 256 B. Bound by memory:
+// four sequences of 131072 tokens, 4 heads, in 216 us, 6.5 TB/s or 96 % of the measured copy rate.
 constexpr int kReadRows = 64;
 template <class T, bool kWide>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const RowsArgs a, const uint8_t *k4,
@@ -173,6 +180,8 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const RowsArgs a, const u
 }
 
 // Rows of 32-byte accesses: aligned base and stride (of the tensors that are there).
+// 131072 tokens of 8 heads are written in 130 us with them (5.4 TB/s) and 144 us with 16-byte ones, read
+// back in 110 us (6.4 TB/s) and 224 us: rows off the 32 bytes make two threads write each sector.
 bool wide(const void *k, int64_t ks, const void *v, int64_t vs) {
     const bool kw = !k || ((reinterpret_cast<uintptr_t>(k) & 31) == 0 && ks % 16 == 0);
     const bool vw = !v || ((reinterpret_cast<uintptr_t>(v) & 31) == 0 && vs % 16 == 0);

@@ -2,9 +2,10 @@
 // prompt) on the fifth-generation tensor cores. Definition in ffd.h.
 //
 // The query rows of a (sequence, KV head), nq tokens x G heads, are taken 256 at a time: an item is
-// one such group of rows over the pages that any of them sees. The pages of all items, concatenated,
-// are cut into equal contiguous ranges, one per CTA (one per SM), so the last CTA ends with the first
-// whatever the causal edges leave; an item cut by a range's end is joined by the last of its CTAs.
+// one such group of rows over the pages that any of them sees. The pages of all items, concatenated with
+// what each item costs besides, are cut into equal contiguous ranges, one per CTA (one per SM), so the
+// last CTA ends with the first whatever the causal edges leave; an item cut by a range's end is joined
+// by the last of its CTAs.
 // Where items are short, whole ones are dealt out instead: a join costs more than the imbalance.
 // For each page of 64 tokens a CTA computes, for its two tiles of 128 rows,
 //   S = Q K^T   (M 128, N 64, K 128; f16, both operands in shared memory, S in tensor memory),
@@ -14,6 +15,15 @@
 // Roles: a copy warp fetches the pages' records; four warps form K and four V^T tiles of f16 values from
 // them; one thread a tile issues its matrix instructions; two groups of four warps, one row a thread,
 // do the softmax of one tile each.
+//
+// What bounds it. A page takes 2090 cycles for two tiles (2048 query tokens over 32768, 32/8 heads:
+// 955 us, 1.11 PFLOP/s, 57 % of the measured matrix rate; 1280 cycles are the matrix instructions' own: 8 x
+// 48 a tile for S, whose Q is read again from shared memory every time, and 4 x 64 for P V) and 1780
+// for one. Within a step the softmax of a row (2020 cycles with both groups at work, 1680 with one) and
+// the way S -> P -> P V -> next S through barriers cover each other, but little is left between. Q
+// partly in tensor memory (S at 40 cycles an instruction) leaves room for three places of S and
+// ties the tiles to each other: 1287 us. A CTA of 480 threads that reads S once into 128 registers
+// forms K and V^T with four warps, and waits for them: 961 us.
 //
 // K's rows, and with them the columns of S, P and V^T, are tokens in the order 8 (p % 8) + p / 8:
 // then the eight tokens that make 16 bytes of a V^T row come from eight different lanes' loads, and
@@ -36,6 +46,7 @@ constexpr int kRecord = 130 * kRows;   // floats of a joined item: o[128][row], 
 // CTAs whose first one this is, where the item begins or goes on.
 constexpr int kSlots = 4;
 constexpr int kOnce = 8;               // records (133 KB each) that one CTA joins at once
+constexpr int kLead = kChunkLead;      // pages' time that an item costs besides its pages
 constexpr float kShift = 7.0f;         // P carries 2^7: with the lazy reference at most 2^15
 constexpr float kLazy = 8.0f;
 // Tensor memory columns: S of tile g and step j at 64 (2 g + j % 2), its first 32 columns P's place
@@ -82,13 +93,14 @@ __device__ __forceinline__ void item_pages(const AttnArgs &a, const Seq &s, int 
     np = hi < 0 ? 0 : (hi >> 6) - fp + 1;
 }
 
-// What one item weighs when the work is cut: its pages, or one each; 0 behind the last one.
+// What one item weighs when the work is cut: kLead before its first page and one for each, or one in
+// all; 0 behind the last one.
 __device__ __forceinline__ int item_weight(const AttnArgs &a, const Seq &s, int rt) {
     if (rt >= item_groups(a, s)) return 0;
     if (a.whole_items) return 1;
     int fp, np;
     item_pages(a, s, rt, fp, np);
-    return np;
+    return np > 0 ? np + kLead : 0;
 }
 
 __device__ __forceinline__ int lane_scan(int v, int lane) {  // sum over the lanes up to this one
@@ -200,7 +212,7 @@ template <class T>
 __device__ __forceinline__ void load_queries(const AttnArgs &a, Shared &sh, const Seq &s, int h,
                                              int row0, int rows, int warp, int lane) {
     const int j = lane & 15;  // channels 8 j .. 8 j + 7
-#pragma unroll 4
+#pragma unroll 7
     for (int p = warp; p < rows / 2; p += kCtaWarps) {
         const int r = 2 * p + (lane >> 4), i = div_g(a, row0 + r);
         uint4 u = make_uint4(0, 0, 0, 0);
@@ -318,8 +330,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
     const uint32_t tmem = sh.tmem;
     const int c0 = (int)((int64_t)total * cta / ncta), c1 = (int)((int64_t)total * (cta + 1) / ncta);
 
-    // ---- where the range begins: sequence b, head h, group rt, page `at` of the item's ----------
-    int b, h, rt = 0, at;
+    // ---- where the range begins: sequence b, head h, group rt, `into` the item's weight ----------
+    int b, h, rt = 0, into;
     Seq s;
     {
         int lo = 0, hi = kThreads;
@@ -348,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
             }
             rem -= __shfl_sync(0xffffffffu, upto, 31);
         }
-        at = a.whole_items ? 0 : rem;
+        into = a.whole_items ? 0 : rem;
     }
 
     // so far in the whole kernel, per role: steps (segments' ends among them), and pages (V tiles and
@@ -357,12 +369,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
     for (int x = c0; x < c1;) {
         int fp, np;
         item_pages(a, s, rt, fp, np);
-        const int cnt = a.whole_items || np - at < c1 - x ? np - at : c1 - x;
+        const int first = x - into + kLead;  // the item's first page in the cut's scale
+        const int at = into > kLead ? into - kLead : 0;
+        const int cnt = (a.whole_items || np < c1 - first ? np : c1 - first) - at;
+        if (cnt <= 0 && !a.whole_items) break;  // the item's pages are the next CTA's
         const int j0 = fp + at, j1 = j0 + cnt;
         const int row0 = rt * kRows, rows = s.nq * a.G - row0;  // rows: of this item and later
         const bool two = rows > kTile;
         const bool begins = at == 0, complete = begins && cnt == np;
-        const int first = x - at;  // the item's first page among all
 
         // ---- queries
         const int grp = warp >> 2;  // 0, 1: softmax group
@@ -766,8 +780,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         tc_fence_after();
 
         // ---- the next item
-        x += a.whole_items ? 1 : cnt;
-        at = 0;
+        x = a.whole_items ? x + 1 : first + at + cnt;
+        into = 0;
         if (x < c1) {
             do {
                 if (++rt >= item_groups(a, s)) {

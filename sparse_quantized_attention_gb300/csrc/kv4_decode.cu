@@ -17,8 +17,18 @@
 //
 // P is rounded to f16 with 2^7 at the reference, so probabilities down to 2^-21 of it keep all 11
 // bits (and down to 2^-31 some). The reference follows the maximum lazily, which saves the rescaling
-// that a new maximum in any of a warp's columns would cost nearly every time. q enters as f16 scaled by a power of two per column (its largest magnitude in
-// [2^13, 2^14)): exact for bf16 and f16 queries apart from elements below 2^-27 of the largest.
+// that a new maximum in any of a warp's columns would cost nearly every time. q enters as f16 scaled
+// by a power of two per column (its largest magnitude in [2^13, 2^14)): exact for bf16 and f16 queries
+// apart from elements below 2^-27 of the largest.
+//
+// What bounds it. A page of a head is 10 KB for 64 x 8 NT scores. With one column tile a long cache is
+// read at 5.0 TB/s (4 x 131072 tokens, 28/4 heads: 68 us, 73 % of the measured copy rate; forming K and
+// V takes most of the issue slots then, a matrix instruction 8 cycles of a scheduler's), a batch of 32
+// sequences at 5.2 TB/s. A short cache waits instead: about 3.5 us until the first copy is asked
+// for, 2 us for it, 4 to 5 us for the join of the warps, the records and the tickets (4096 tokens:
+// 12 us, 32768: 23 us). With more column tiles eight warps are all that the registers allow, and their
+// instructions wait on one another (0.3 issued a cycle of a scheduler): 24 rows behind a window of 4096
+// take 40 us, 16 % of the copy rate.
 #include "kv4_walk.cuh"
 
 namespace ffd {
@@ -35,9 +45,9 @@ constexpr int kWindow = 2048;         // pages of a CTA's list
 constexpr int kSlots = 6;
 constexpr int kOnce = 16;             // records that one CTA joins at once
 
-// Warps of a CTA: what their registers allow (128 a thread for one column tile, 168 for two, 204
-// for three, 255 for four), and the 16-token tiles that a warp takes together: the more column tiles, the fewer tokens
-// it needs for its matrix instructions not to wait on one another.
+// Warps of a CTA: what their registers allow (128 a thread for one column tile, 168 for two, 251
+// for three, 255 for four), and the 16-token tiles that a warp takes together: the more column tiles,
+// the fewer tokens it needs for its matrix instructions not to wait on one another.
 template <int NT>
 constexpr int kWarpsOf = NT == 1 ? 16 : NT == 2 ? 12 : 8;
 template <int NT>

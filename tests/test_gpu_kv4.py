@@ -354,6 +354,8 @@ SEVERAL = [
     ("chunk_very_many", dict(lens=[3 * i % 130 for i in range(700)],
                              qlens=[i % 40 for i in range(700)], Hkv=1, G=2)),
     ("chunk_many_long", dict(lens=[40 * i for i in range(90)], qlens=[40] * 90, Hkv=1, G=4)),
+    ("chunk_prompt", dict(lens=[2500, 130], qlens=[2500, 130], Hkv=2, G=8)),
+    ("chunk_prompt_window", dict(lens=[2700], qlens=[2600], Hkv=2, G=8, window=300)),
     ("tails", dict(lens=[100, 90], qlens=[20, 30], Hkv=2, G=4, tail=11, max_q=77)),
     ("mixed", dict(lens=[9000, 77, 600, 128], qlens=[1, 40, 0, 128], Hkv=2, G=6, stride_pad=8)),
 ]
