@@ -12,8 +12,7 @@ constexpr int kParamOff = 4096;  // (scale, off) pairs behind the codes
 static_assert(kRec == 5120, "record size");
 constexpr int kMaxCtas = 1024;     // of an attention launch (one per SM at most)
 // Pages' time that an item of the chunk kernel costs besides its pages (queries, first copies, results:
-// 19000 to 20000 cycles, 2100 a page). Counted where work is cut, it keeps a prompt's many short first
-// items from coming together in a few CTAs: 8192 tokens, 32/8 heads, 806 -> 592 us.
+// 19000 to 20000 cycles, 2100 a page).
 constexpr int kChunkLead = 9;
 constexpr float kMaxInput = 16384.0f;  // |off| <= |min| + 16/15 range stays inside f16
 
@@ -139,6 +138,7 @@ struct RowsArgs {
 struct AttnArgs {
     int B, Hq, Hkv, G, P, max_blocks, max_q, total_q, window;
     int whole_items;  // chunk kernel: items are not cut
+    int lead;         // chunk kernel: pages' time that an item counts for besides its pages
     uint32_t over_g;  // ceil(2^32 / G), too large by less than G / 2^32 of it (G > 1)
     int64_t q_stride;
     float sm_scale;
@@ -155,7 +155,7 @@ struct AttnArgs {
 struct Plan {
     int cols;  // query columns of the decode kernel (8, 16, 24 or 32), 0: the chunk kernel
     int ctas;
-    int whole_items;  // chunk kernel: items are not cut
+    int whole_items, lead;  // chunk kernel, as in AttnArgs
     size_t tickets, records, parked, total;
 };
 

@@ -46,7 +46,6 @@ constexpr int kRecord = 130 * kRows;   // floats of a joined item: o[128][row], 
 // CTAs whose first one this is, where the item begins or goes on.
 constexpr int kSlots = 4;
 constexpr int kOnce = 8;               // records (133 KB each) that one CTA joins at once
-constexpr int kLead = kChunkLead;      // pages' time that an item costs besides its pages
 constexpr float kShift = 7.0f;         // P carries 2^7: with the lazy reference at most 2^15
 constexpr float kLazy = 8.0f;
 // Tensor memory columns: S of tile g and step j at 64 (2 g + j % 2), its first 32 columns P's place
@@ -93,14 +92,14 @@ __device__ __forceinline__ void item_pages(const AttnArgs &a, const Seq &s, int 
     np = hi < 0 ? 0 : (hi >> 6) - fp + 1;
 }
 
-// What one item weighs when the work is cut: kLead before its first page and one for each, or one in
+// What one item weighs when the work is cut: `lead` before its first page and one for each, or one in
 // all; 0 behind the last one.
 __device__ __forceinline__ int item_weight(const AttnArgs &a, const Seq &s, int rt) {
     if (rt >= item_groups(a, s)) return 0;
     if (a.whole_items) return 1;
     int fp, np;
     item_pages(a, s, rt, fp, np);
-    return np > 0 ? np + kLead : 0;
+    return np > 0 ? np + a.lead : 0;
 }
 
 __device__ __forceinline__ int lane_scan(int v, int lane) {  // sum over the lanes up to this one
@@ -369,8 +368,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
     for (int x = c0; x < c1;) {
         int fp, np;
         item_pages(a, s, rt, fp, np);
-        const int first = x - into + kLead;  // the item's first page in the cut's scale
-        const int at = into > kLead ? into - kLead : 0;
+        const int first = x - into + a.lead;  // the item's first page in the cut's scale
+        const int at = into > a.lead ? into - a.lead : 0;
         const int cnt = (a.whole_items || np < c1 - first ? np : c1 - first) - at;
         if (cnt <= 0 && !a.whole_items) break;  // the item's pages are the next CTA's
         const int j0 = fp + at, j1 = j0 + cnt;
