@@ -211,14 +211,22 @@ template <class T>
 __device__ __forceinline__ void load_queries(const AttnArgs &a, Shared &sh, const Seq &s, int h,
                                              int row0, int rows, int warp, int lane) {
     const int j = lane & 15;  // channels 8 j .. 8 j + 7
-#pragma unroll 7
-    for (int p = warp; p < rows / 2; p += kCtaWarps) {
-        const int r = 2 * p + (lane >> 4), i = div_g(a, row0 + r);
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (i < s.nq)
-            u = __ldg(reinterpret_cast<const uint4 *>(
-                          static_cast<const uint16_t *>(a.q) + (int64_t)(s.t0 + i) * a.q_stride +
-                          (h * a.G + row0 + r - i * a.G) * kD) + j);
+    constexpr int kEach = (kRows / 2 + kCtaWarps - 1) / kCtaWarps;
+    uint4 got[kEach];  // all loads are under way before the first is waited for
+#pragma unroll
+    for (int k = 0; k < kEach; k++) {
+        const int r = 2 * (warp + k * kCtaWarps) + (lane >> 4), i = div_g(a, row0 + r);
+        got[k] = make_uint4(0, 0, 0, 0);
+        if (r < rows && i < s.nq)
+            got[k] = __ldg(reinterpret_cast<const uint4 *>(
+                               static_cast<const uint16_t *>(a.q) + (int64_t)(s.t0 + i) * a.q_stride +
+                               (h * a.G + row0 + r - i * a.G) * kD) + j);
+    }
+#pragma unroll
+    for (int k = 0; k < kEach; k++) {
+        const int r = 2 * (warp + k * kCtaWarps) + (lane >> 4);
+        if (r >= rows) break;  // warp-uniform: rows is even
+        const uint4 u = got[k];
         const float2 x0 = T::unpack(u.x), x1 = T::unpack(u.y), x2 = T::unpack(u.z),
                      x3 = T::unpack(u.w);
         float top = fmaxf(fmaxf(fmaxf(fabsf(x0.x), fabsf(x0.y)), fmaxf(fabsf(x1.x), fabsf(x1.y))),
