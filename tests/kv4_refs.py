@@ -103,14 +103,15 @@ def unpack64(rec):
 
 
 def attention64(q, k4, v4, seq_lens, cu_q, block_table, Hkv, *, window=0, keep=None, sm=None):
-    """out f64 [T, Hq, 128], lse f64 [T, Hq], and per row and head the two magnitudes that rounding
-    errors scale with: A = max_j sm sum_c |q_c K_jc| and, per channel, W = sum_j p_j |V_j|.
+    """out f64 [T, Hq, 128], lse f64 [T, Hq], and per row and head the magnitudes that rounding
+    errors scale with: A = max_j sm sum_c |q_c K_jc| and, per channel, W = sum_j p_j |V_j| and
+    U = sum_j |V_j| over the tokens j that the row sees.
     Rows that belong to nobody are nan. Lists of python ints: seq_lens, cu_q."""
     T, Hq, _ = q.shape
     G = Hq // Hkv
     sm = 1 / math.sqrt(D) if sm is None else sm
     out = torch.full((T, Hq, D), math.nan, dtype=torch.float64, device=q.device)
-    wabs = torch.zeros_like(out)
+    wabs, usum = torch.zeros_like(out), torch.zeros_like(out)
     lse = torch.full((T, Hq), math.nan, dtype=torch.float64, device=q.device)
     amax = torch.zeros_like(lse)
     P = k4.shape[0]
@@ -146,22 +147,25 @@ def attention64(q, k4, v4, seq_lens, cu_q, block_table, Hkv, *, window=0, keep=N
                                                                z)[:, None]), torch.zeros_like(s))
                 out[t0:t1, h * G + g] = p @ V
                 wabs[t0:t1, h * G + g] = p @ V.abs()
+                usum[t0:t1, h * G + g] = see.double() @ V.abs()
                 lse[t0:t1, h * G + g] = z
                 amax[t0:t1, h * G + g] = a.max(-1).values if n else 0.0
-    return out, lse, amax, wabs
+    return out, lse, amax, wabs, usum
 
 
-def tolerance(out, lse, amax, wabs, dtype):
+def tolerance(out, lse, amax, wabs, usum, dtype):
     """Bounds of |library - 64 bits| for the output and the log-sum-exp.
 
     Scores: products of f16 values and 128 fp32 additions, each off by at most 2^-23 of the sum of
     magnitudes (the matrix unit truncates): ds = 128 * 2^-23 A = 2^-16 A. Probabilities: e^ds - 1
     (numerator and denominator: twice), one rounding to f16 (half step 2^-11) and the exponential's
-    own 2^-20. Output: one rounding to its type. The sum l is over positives in fp32: 2^-18 covers
-    its additions and the logarithm."""
+    own 2^-20. A probability enters as f16 of 2^7 at a reference that is at most the largest score, so
+    that l >= 2^7 in the same unit; below 2^-14 it is rounded by half of f16's least step, 2^-25, or
+    2^-32 of the row's largest: 2^-32 U. Output: one rounding to its type. The sum l is over positives
+    in fp32: 2^-18 covers its additions and the logarithm."""
     ds = amax * 2.0 ** -16
     rel = (2.0 ** -11 + 2.0 ** -18 + 2.2 * ds)[..., None]
     half = torch.finfo(dtype).eps / 2
     tiny = torch.finfo(dtype).tiny if dtype == torch.bfloat16 else 2.0 ** -25
-    return (half * out.abs() + rel * wabs * (1 + half) + tiny,
+    return (half * out.abs() + (rel * wabs + 2.0 ** -32 * usum) * (1 + half) + tiny,
             ds * 1.1 + 2.0 ** -18 + 2.0 ** -22 * lse.abs())

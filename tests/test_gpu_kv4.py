@@ -371,6 +371,16 @@ def test_attention(name, kw):
     c.check(out, lse)
 
 
+def test_probabilities_below_the_least_step():
+    """Peaked rows, one of them with a V of exactly 0 in a channel at its largest score: what is left
+    there are probabilities that f16 holds with few bits or none."""
+    c = Case([70, 58, 55, 9, 1, 0, 70, 0, 68, 0, 64, 70, 15, 2, 1, 52, 70, 70, 1, 70],
+             [100, 0, 0, 1, 82, 1, 1, 0, 1, 7, 81, 75, 15, 1, 100, 52, 1, 0, 0, 33], 2, 6,
+             window=50, seed=839755, q_scale=8.0)
+    out, lse = c.run()
+    c.check(out, lse)
+
+
 @pytest.mark.parametrize("q,length", [(1, 70000), (5, 70000), (70, 40000)])
 def test_one_sequence_over_every_cta(q, length):
     """More CTAs share a unit than are joined at once, twice with the same workspace."""

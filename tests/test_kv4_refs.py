@@ -62,7 +62,7 @@ def test_attention_against_the_definition():
     v4 = R.pack64(torch.randn((2, Hkv, 64, 128), generator=g))
     q = torch.randn((nq, Hkv * G, 128), generator=g)
     bt = torch.tensor([[1, 0]], dtype=torch.int32)
-    out, lse, _, _ = R.attention64(q, k4, v4, [n], [0, nq], bt, Hkv, window=9)
+    out, lse, *_ = R.attention64(q, k4, v4, [n], [0, nq], bt, Hkv, window=9)
     K = torch.cat((R.unpack64(k4[1, 0]), R.unpack64(k4[0, 0])))
     V = torch.cat((R.unpack64(v4[1, 0]), R.unpack64(v4[0, 0])))
     for i in range(nq):
@@ -74,6 +74,6 @@ def test_attention_against_the_definition():
             assert torch.allclose(out[i, h], want, rtol=1e-12, atol=1e-12)
             assert abs(float(lse[i, h]) - math.log(sum(w))) < 1e-12
     # a row that sees nothing
-    out, lse, _, _ = R.attention64(q, k4, v4, [1], [0, nq], bt, Hkv)
+    out, lse, *_ = R.attention64(q, k4, v4, [1], [0, nq], bt, Hkv)
     assert out[0].abs().sum() == 0 and lse[0].tolist() == [-math.inf] * 2
     assert torch.equal(out[2, 0], V[0])
