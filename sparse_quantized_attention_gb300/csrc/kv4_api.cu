@@ -132,13 +132,13 @@ int64_t chunk_pages(int64_t n, int64_t rows) {
 // fewer, and the groups of rows of a unit see from first to last as many more pages as there are query
 // tokens (less behind a window). While that is less than what cutting costs, whole items are the
 // faster way. Measured, us whole and cut, 8 heads and 4 query heads for each:
-//   9 sequences of 1024 tokens, their last 128     2 beyond           33   56
-//   2 of 4096, 512                                17                  83   89
-//   1 of 4096, 1024                               23                  82   92
-//   3 of 4096, 256                                28                  82   77
-//   8 of 2048, 512                                38, several items   143  158
-//   3 of 1024, 1024                               41, several         88   76
-//   1 of 8192, 8192                               over 600, several   1030 592
+//   9 sequences of 1024 tokens, their last 128     2 beyond           32   53
+//   2 of 4096, 512                                17                  81   84
+//   1 of 4096, 1024                               23                  82   88
+//   3 of 4096, 256                                28                  82   74
+//   8 of 2048, 512                                38, several items   138  149
+//   3 of 1024, 1024                               41, several         83   72
+//   1 of 8192, 8192                               over 600, several   1024 575
 double longest_beyond(const ffd_kv4_params *p, int64_t rounds, int64_t groups, int64_t items, int sms) {
     const int64_t tokens = (int64_t)p->max_blocks_per_seq * kPage;
     const int64_t seen = p->window > 0 && p->window < tokens ? p->window : tokens;
@@ -158,7 +158,7 @@ ffd_status make_plan(const ffd_kv4_params *p, Plan *pl) {
     const int64_t rows = (int64_t)p->max_q_len * (p->num_q_heads / p->num_kv_heads);
     // Up to 32 rows a KV head the kernel whose warps walk pages alone is the faster one, above it only the
     // one that forms tiles for tcgen05 is left: eight sequences of 5000 to 16384 tokens, 8 heads, take
-    // 36, 50, 58 and 86 us for 8, 16, 24 and 32 rows in the first and 96 to 97 us in the second (98 for 36).
+    // 36, 49, 58 and 86 us for 8, 16, 24 and 32 rows in the first and 90 to 91 us in the second (92 for 36).
     pl->cols = rows <= 32 ? (int)(rows + 7) / 8 * 8 : 0;
     const int sms = current_sm_count();
     const int64_t units = (int64_t)p->batch * p->num_kv_heads;
@@ -191,10 +191,10 @@ ffd_status make_plan(const ffd_kv4_params *p, Plan *pl) {
     if (ctas > kMaxCtas) ctas = kMaxCtas;
     pl->ctas = (int)ctas;
     // Where work is cut, what an item costs besides its pages counts as well, so that a prompt's many short
-    // first items do not come together in a few CTAs (8192 tokens, 32/8 heads: 806 us without, 592 with;
-    // 256 rows a head of eight sequences: 125 and 119). Every CTA that begins within an item has such a
+    // first items do not come together in a few CTAs (8192 tokens, 32/8 heads: 752 us without, 574 with;
+    // 256 rows a head of eight sequences of 5000 to 16384: 122 and 117). Every CTA that begins within an item has such a
     // cost too; with few long items that is nearly all of them, and only those that begin with an item
-    // would get fewer pages (256 rows a head of one sequence of 32768: 68.5 us without, 70.2 with).
+    // would get fewer pages (256 rows a head of one sequence of 32768: 67.2 us without, 68.6 with).
     pl->lead = pl->cols || pl->whole_items || 8 * items <= ctas ? 0 : kChunkLead;
     const size_t rec = pl->cols ? decode_record_bytes(pl->cols) : chunk_record_bytes();
     size_t off = kAlign;
