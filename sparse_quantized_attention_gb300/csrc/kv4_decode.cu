@@ -791,8 +791,16 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
             const Seq s = seq(b);
             const Shares p(first, s.np, ncta, total, cta, kOnce);
             const int live = s.nq * a.G < cols ? s.nq * a.G : cols;
-            // join records rec(0) .. rec(n - 1), eight a round, column by column
-            auto join = [&](auto rec, int n, auto done) {
+            // Record i stands at from + i * step, and `skip` further from the second on: a CTA's own is
+            // its second one when the unit begins there, else its first. Eight are joined a round, column
+            // by column; of groups, the joined ones once more.
+            const int64_t own = (int64_t)kSlots * kRecord;
+            const bool at_start = p.g0 == p.p0;
+            const float *from = records + p.g0 * own + (at_start ? kRecord : 0);
+            int64_t step = own, skip = at_start ? -kRecord : 0;
+            int n = p.members;
+            for (bool last = p.groups == 1;; last = true) {
+                auto rec = [&](int i) { return from + i * step + (i ? skip : 0); };
                 for (int c = warp; c < live; c += W) {
                     float M = -INFINITY, l = 0.0f;
                     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -817,32 +825,27 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                         for (int i = 0; i < 8; i++)
                             o = plus(o, __shfl_sync(0xffffffffu, f, i), v[i]);
                     }
-                    done(c, M, l, o);
+                    if (last) {
+                        int row, hq, i;
+                        column(a, s, h, c, row, hq, i);
+                        write_four<T>(a, row, hq, 4 * lane, scaled(o, l == 0.0f ? 0.0f : 1.0f / l));
+                        if (a.lse && lane == 0) a.lse[(int64_t)row * a.Hq + hq] = lse_of(M - kShift, l);
+                    } else {
+                        float *col = records + p.g0 * own + (at_start ? 4 : 5) * kRecord + c * kStride;
+                        *reinterpret_cast<float4 *>(col + 4 * lane) = o;
+                        if (lane == 0) *reinterpret_cast<float2 *>(col + 128) = make_float2(M, l);
+                    }
                 }
-            };
-            auto finish = [&](int c, float M, float l, float4 o) {
-                int row, hq, i;
-                column(a, s, h, c, row, hq, i);
-                write_four<T>(a, row, hq, 4 * lane, scaled(o, l == 0.0f ? 0.0f : 1.0f / l));
-                if (a.lse && lane == 0) a.lse[(int64_t)row * a.Hq + hq] = lse_of(M - kShift, l);
-            };
-            auto slot = [&](int c, int n) { return records + (int64_t)(kSlots * c + n) * kRecord; };
-            // a CTA's record: its second one when the unit begins there, else its first
-            auto member = [&](int n) { return slot(p.g0 + n, p.g0 + n == p.p0); };
-            if (p.groups == 1) {
-                join(member, p.members, finish);
-                continue;
+                if (last) break;
+                __syncthreads();
+                if (tid == 0) sh.flag[k] = p.last_group(tickets);
+                __syncthreads();
+                if (!sh.flag[k]) break;
+                from = records + p.p0 * own + 4 * kRecord;
+                step = p.size * own;
+                skip = kRecord;
+                n = p.groups;
             }
-            float *mine = slot(p.g0, p.g0 == p.p0 ? 4 : 5);
-            join(member, p.members, [&](int c, float M, float l, float4 o) {
-                *reinterpret_cast<float4 *>(mine + c * kStride + 4 * lane) = o;
-                if (lane == 0) *reinterpret_cast<float2 *>(mine + c * kStride + 128) = make_float2(M, l);
-            });
-            __syncthreads();
-            if (tid == 0) sh.flag[k] = p.last_group(tickets);
-            __syncthreads();
-            if (sh.flag[k])
-                join([&](int n) { return slot(p.p0 + n * p.size, n ? 5 : 4); }, p.groups, finish);
         }
         __syncthreads();
     }

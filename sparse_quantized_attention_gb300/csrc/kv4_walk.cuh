@@ -68,7 +68,11 @@ struct Shares {
         p0 = (int)(((int64_t)(first + 1) * ncta - 1) / total);
         p1 = (int)(((int64_t)(first + np) * ncta - 1) / total);
         const int n = p1 - p0 + 1;
-        size = n <= once ? n : (int)ceilf(sqrtf((float)n));
+        size = members = n;
+        groups = 1;
+        g0 = p0;
+        if (n <= once) return;
+        size = (int)ceilf(sqrtf((float)n));
         groups = (n + size - 1) / size;
         const int at = (cta - p0) / size * size;
         g0 = p0 + at;
