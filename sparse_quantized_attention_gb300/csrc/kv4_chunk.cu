@@ -46,8 +46,6 @@ constexpr int kRecord = 130 * kRows;   // floats of a joined item: o[128][row], 
 // CTAs whose first one this is, where the item begins or goes on.
 constexpr int kSlots = 4;
 constexpr int kOnce = 8;               // records (133 KB each) that one CTA joins at once
-constexpr float kShift = 7.0f;         // P carries 2^7: with the lazy reference at most 2^15
-constexpr float kLazy = 8.0f;
 // Tensor memory columns: S of tile g and step j at 64 (2 g + j % 2), its first 32 columns P's place
 // once S is read; O of tile g at kColO + 128 g.
 constexpr uint32_t kColO = 256;
@@ -452,13 +450,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                     for (int c = 0; c < 32; c += 2)
                         top = fmaxf(top, fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 1])));
                     top *= fs;
-                    const bool raise = top > m + kLazy || (m == -INFINITY && top > m);
+                    const bool raise = top > m + (is_far(m) ? 0.0f : kLazy);  // (m is -inf at first)
                     if (__any_sync(0xffffffffu, raise)) {
                         const float mn = raise ? top : m;
                         const float al = m == -INFINITY ? 0.0f : ex2_approx(m - mn);
                         m = mn;
                         l *= al;
-                        far = __any_sync(0xffffffffu, fabsf(m) > kFar && m != -INFINITY);
+                        far = __any_sync(0xffffffffu, is_far(m));
                         if (any) {
                             // the last step's P V (a stop is met at the next wait)
                             waited(a, sh, &sh.o_done[grp], (turns - 1) & 1);
@@ -478,8 +476,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                         }
                     }
                     const float sub = kShift - (m == -INFINITY ? 0.0f : m);
-                    // Where the reference is so large that its rounding is felt, the products are
-                    // rounded as it was: the exact ones could pass it by more than f16 can hold.
                     const float fx = far ? 1.0f : fs;
                     const float2 f2 = make_float2(fx, fx), s2 = make_float2(sub, sub);
                     float2 l2 = make_float2(0.0f, 0.0f);

@@ -37,8 +37,6 @@ namespace {
 
 constexpr int kSlot = 2 * kRec;       // a warp's K record and V record
 constexpr int kStride = 132;          // floats of a joined column: o[128], m, l, two unused
-constexpr float kShift = 7.0f;        // P carries 2^7, and at most 2^15: a column's reference m is
-constexpr float kLazy = 8.0f;         // raised only when a score passes it by 2^8
 constexpr int kWindow = 2048;         // pages of a CTA's list
 // Records of a CTA: of the unit that goes on from before, of the one that begins there; two carries
 // between windows; of a group of CTAs whose first one this is, where the unit begins or goes on.
@@ -529,7 +527,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
             float fs[NT][2];
             load_queries<NT, T>(a, s, h, lane, qf, fs);
             st.clear();
-            bool far = false;
+            bool far = false;  // one of the warp's references is
             const int low = s.n - s.nq;  // position of the first query
             for (; i < i1; i++) {
                 const Entry e = sh.list[i];
@@ -570,6 +568,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                     }
                     float mx[NT][2];
                     bool up = false;
+                    const float lazy = far ? 0.0f : kLazy;
 #pragma unroll
                     for (int t = 0; t < NT; t++)
 #pragma unroll
@@ -579,7 +578,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                             for (int k = 1; k < TT; k++)
                                 top = fmaxf(top, fmaxf(sc[t][k][c], sc[t][k][2 + c]));
                             mx[t][c] = top * fs[t][c];
-                            up |= mx[t][c] > st.m[t][c] + kLazy;
+                            up |= mx[t][c] > st.m[t][c] + lazy;
                         }
                     if (__any_sync(0xffffffffu, up)) {
                         bool any_far = false;
@@ -594,7 +593,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                                 const float al =
                                     top == -INFINITY ? 0.0f : ex2_approx(st.m[t][c] - top);
                                 st.m[t][c] = top;
-                                any_far |= fabsf(top) > kFar && top != -INFINITY;
+                                any_far |= is_far(top);
                                 st.l[t][c] *= al;
 #pragma unroll
                                 for (int k = 0; k < 8; k++) {
@@ -604,8 +603,6 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                             }
                         far = __any_sync(0xffffffffu, any_far);
                     }
-                    // Where the reference is so large that its rounding is felt, the products are
-                    // rounded as it was: the exact ones could pass it by more than f16 can hold.
                     uint32_t pf[NT][TT][2];
 #pragma unroll
                     for (int t = 0; t < NT; t++) {

@@ -10,7 +10,16 @@ namespace kv4 {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kFar = 4194304.0f;  // 2^22: a reference from here on is off by more than 2^-2
+// A column's (or row's) reference m is raised only when a score passes it by 2^kLazy: P, which carries
+// 2^kShift at the reference, then reaches 2^15 and f16 holds it. That asks for kShift - m and m + kLazy to
+// be exact to a fraction. Past kFar a reference is rounded by more than 2^-2, and from 2^24 (log2 units)
+// on 7 - m may come out as 8 - m and m + 8 as m + 16: a score could stand 2^16 above m and not raise it. So
+// there any larger score raises m (no product then passes it, and P is at most 2^8), and the products
+// that the powers are taken of are rounded as m was. An infinite m belongs to a query with an infinity.
+constexpr float kShift = 7.0f;
+constexpr float kLazy = 8.0f;
+constexpr float kFar = 4194304.0f;  // 2^22
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) > kFar && fabsf(m) < INFINITY; }
 
 // One sequence as the walk sees it.
 struct Seq {

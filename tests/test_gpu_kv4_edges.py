@@ -1,0 +1,54 @@
+"""The 4-bit cache's attention where its arithmetic, its inputs or its plan come to an edge. Bounds as
+in tests/kv4_refs.py."""
+import math
+
+import pytest
+import torch
+
+import sparse_quantized_attention_gb300 as ffd
+from tests import kv4_refs as R
+from tests.test_gpu_kv4 import BF16, F16, i32, offsets, table
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("octave", [22, 23, 24, 25, 26, 27])
+@pytest.mark.parametrize("nq", [1, 3, 40])
+def test_scores_past_2_to_the_24(nq, octave, dtype):
+    """Scores of 2^octave (log2 units) whose largest grows by a little from page to page: where fp32 holds
+    no reference that much below or above them, no probability may leave f16's range. All V rows are
+    alike, so a row's output is its V whatever the weights: each product and the sum l carry at most
+    f16's half step, 2^-11, or 2^-25 of probabilities of which the largest is at least 1."""
+    G, B, n = 8, 4, 64 * 64
+    gen = torch.Generator().manual_seed(octave)
+    bt, P = table([n] * B, gen)
+    # every token's K is (16384, 0, ..); the first of each page has one of 5 codes in channel 1
+    k = torch.zeros((B, n, 1, 128))
+    k[..., 0] = 16384.0
+    k[:, ::64, 0, 1] = 1092.0 * (torch.arange(n // 64) % 5)
+    v = torch.randn((1, 1, 1, 128), generator=gen).expand(B, n, 1, 128)
+    cache = ffd.alloc_kv4_cache(P, 1)
+    ffd.ffd_kv4_write(k.to(F16).reshape(-1, 1, 128).cuda(), v.to(F16).reshape(-1, 1, 128).cuda(),
+                      i32([0] * B), bt.cuda(), cache)
+    unit = math.log2(math.e) / math.sqrt(128)  # log2 units of a score
+    q = torch.zeros((B * nq, G, 128))
+    rows = B * nq * G
+    q[..., 0] = 2.0 ** octave * torch.linspace(1.0, 1.9, rows).reshape(-1, G) / (16384 * unit)
+    q[..., 1] = torch.linspace(0.5, 24.0, rows).reshape(-1, G).flip(0) / (1092 * unit)
+    q = q.clamp(max=65504.0).to(dtype).cuda()
+    for splits in (B, 0):
+        p = ffd.make_kv4_params(B, G, 1, P, bt.shape[1], max_q_len=nq, dtype=dtype, num_splits=splits)
+        ws = ffd.alloc_kv4_workspace(p)
+        out = torch.empty_like(q)
+        lse = torch.empty((B * nq, G), device="cuda")
+        ffd.ffd_kv4_attention(p, q, cache, i32([n] * B), bt.cuda(), out, ws, lse=lse)
+        assert ffd.ffd_get_error(ws) == 0
+        assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+        want = R.held64(v[0, 0, 0].to(F16)).cuda()
+        half = torch.finfo(dtype).eps / 2
+        rel = half + (1 + half) * (2.0 ** -11 + n * 2.0 ** -25 + 2.0 ** -18)
+        assert bool(((out.double() - want).abs() <= rel * want.abs() + 2.0 ** -25).all())
+    ref = R.attention64(q, cache.k4, cache.v4, [n] * B, offsets([nq] * B), bt, 1, sm=float(p.sm_scale))
+    tol = R.tolerance(*ref, dtype)[1]
+    assert bool(((lse.double() - ref[1]).abs() <= tol).all())
