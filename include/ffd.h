@@ -451,7 +451,8 @@ ffd_status ffd_decode_attention_static(const ffd_decode_params *params, const vo
  *   error_word    device int32, or NULL: FFD_ERRBIT_BOUNDS for a token index >=
  *                 64 * max_blocks_per_seq or a page outside [0, P) (that token is skipped),
  *                 FFD_ERRBIT_RANGE for an input with |x| > 16384 or NaN (its group is written; what
- *                 it then holds is unspecified)
+ *                 it then holds is unspecified but finite, so that attention rows which do not
+ *                 see the token are what they are without it)
  * Two rows that name the same (page, token) race; the caller's block table must not do that.
  * Returns FFD_OK, FFD_ERR_INVALID_ARG, FFD_ERR_UNSUPPORTED or FFD_ERR_CUDA.
  */

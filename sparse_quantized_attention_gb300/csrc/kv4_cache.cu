@@ -109,8 +109,14 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const RowsArgs a, const 
         most = T::max2_nan(most, w[j]);
     }
     const float2 l2 = T::unpack(least), m2 = T::unpack(most);
-    const float lo = fminf(l2.x, l2.y), hi = max_nan(m2.x, m2.y);
-    if (!(lo >= -kMaxInput && hi <= kMaxInput)) raise_error(a.err, FFD_ERRBIT_RANGE);
+    float lo = fminf(l2.x, l2.y), hi = max_nan(m2.x, m2.y);
+    if (!(lo >= -kMaxInput && hi <= kMaxInput)) {
+        // the group holds finite values all the same (a NaN codes as the least): attention multiplies
+        // them by 0 in the rows that do not see the token
+        raise_error(a.err, FFD_ERRBIT_RANGE);
+        lo = fminf(fmaxf(lo, -kMaxInput), kMaxInput);
+        hi = fmaxf(fminf(hi, kMaxInput), -kMaxInput);
+    }
     const __half hs = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
     const float s = __half2float(hs);
     const __half ho = __float2half_rn(__fmaf_rn(-16.0f, s, lo));

@@ -52,3 +52,38 @@ def test_scores_past_2_to_the_24(nq, octave, dtype):
     ref = R.attention64(q, cache.k4, cache.v4, [n] * B, offsets([nq] * B), bt, 1, sm=float(p.sm_scale))
     tol = R.tolerance(*ref, dtype)[1]
     assert bool(((lse.double() - ref[1]).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf, 60000.0])
+@pytest.mark.parametrize("nq,window", [(4, 0), (100, 0), (1, 40), (6, 40), (100, 40)])
+def test_a_token_out_of_range_reaches_only_rows_that_see_it(nq, window, bad):
+    """The rows before it, and those whose window has passed it, are what they are without it."""
+    gen = torch.Generator().manual_seed(nq + window)
+    Hkv, G, n = 2, 4, 300
+    at = n - (45 if nq <= 6 and window else min(nq, 60) // 2 + 1)  # the token, in the last two pages
+    bt, P = table([n], gen)
+    x = torch.randn((2, n, Hkv, 128), generator=gen).to(F16)
+    q = torch.randn((nq, Hkv * G, 128), generator=gen).to(F16).cuda()
+    p = ffd.make_kv4_params(1, Hkv * G, Hkv, P, bt.shape[1], max_q_len=nq, dtype=F16, window=window)
+    cache = ffd.alloc_kv4_cache(P, Hkv)
+    ffd.ffd_kv4_write(x[0].cuda(), x[1].cuda(), i32([0]), bt.cuda(), cache)
+    ref = R.attention64(q, cache.k4, cache.v4, [n], [0, nq], bt, Hkv, window=window,
+                        sm=float(p.sm_scale))
+    tol, tol_lse = R.tolerance(*ref, F16)
+    x[0, at, 0, 5] = bad
+    x[1, at, :, 77] = bad
+    err = i32([0])
+    ffd.ffd_kv4_write(x[0].cuda(), x[1].cuda(), i32([0]), bt.cuda(), cache, error_word=err)
+    assert ffd.ffd_get_error(err) == 6
+    ws = ffd.alloc_kv4_workspace(p)
+    out, lse = torch.empty_like(q), torch.empty((nq, Hkv * G), device="cuda")
+    ffd.ffd_kv4_attention(p, q, cache, i32([n]), bt.cuda(), out, ws, lse=lse)
+    assert ffd.ffd_get_error(ws) == 0
+    pos = torch.arange(n - nq, n, device="cuda")
+    blind = (pos < at) | ((pos - window >= at) if window else (pos < 0))
+    assert bool(blind.any())
+    assert bool(((out.double() - ref[0]).abs() <= tol)[blind].all())
+    assert bool(((lse.double() - ref[1]).abs() <= tol_lse)[blind].all())
+    held = torch.empty((2, n, Hkv, 128), dtype=F16, device="cuda")
+    ffd.ffd_kv4_read(cache, i32([0]), bt.cuda(), held[0], held[1])
+    assert bool(torch.isfinite(held).all())
