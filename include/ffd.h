@@ -518,8 +518,9 @@ size_t ffd_kv4_workspace_size(const ffd_kv4_params *params);
  * (row, head) unspecified and no other.
  *   q           device [total_q][Hq][128] of dtype, rows params->q_stride elements apart, 16-byte
  *               aligned
- *   k4, v4      device records of the cache, 16-byte aligned. Tokens at or past n are never used:
- *               their bytes may be anything.
+ *   k4, v4      device records of the cache, 16-byte aligned. Tokens that no query of the sequence
+ *               can see by its length and window (at or past n, behind the first query's window)
+ *               are never used: their bytes may be anything.
  *   seq_lens    device int32 [B], 0 <= seq_lens[b] <= 64 * max_blocks_per_seq
  *   cu_q        device int32 [B+1]: sequence b's query tokens are rows cu_q[b] .. cu_q[b+1]-1, at
  *               most max_q_len of them (none is fine). NULL: every sequence has max_q_len, and

@@ -168,8 +168,8 @@ __device__ __forceinline__ void form_k(const uint8_t *rec, uint8_t *tile, int t)
 
 // V^T: thread t takes word J = 4 (t / 32) + t % 32 / 8 of the tokens i * 8 + tg (i < 8), tg = t % 8,
 // which are positions 8 tg .. 8 tg + 7: 16 bytes of each of the word's eight channel rows. Tokens
-// from `valid` on hold anything and count as 0.
-__device__ __forceinline__ void form_v(const uint8_t *rec, uint8_t *tile, int t, int valid) {
+// before `from` and from `valid` on, which no query sees, may hold anything and count as 0.
+__device__ __forceinline__ void form_v(const uint8_t *rec, uint8_t *tile, int t, int from, int valid) {
     const int tg = t & 7, J = 4 * (t >> 5) + ((t >> 3) & 3);
     uint32_t out[8][4];  // [channel of the word][token pair]
 #pragma unroll
@@ -181,9 +181,9 @@ __device__ __forceinline__ void form_v(const uint8_t *rec, uint8_t *tile, int t,
             *reinterpret_cast<const uint32_t *>(rec + code_offset(r + 8, J >> 2) + 4 * (J & 3));
         uint32_t p0 = *reinterpret_cast<const uint32_t *>(rec + param_offset(r, J >> 2));
         uint32_t p1 = *reinterpret_cast<const uint32_t *>(rec + param_offset(r + 8, J >> 2));
-        if (valid < kPage) {
-            p0 = r < valid ? p0 : 0u;
-            p1 = r + 8 < valid ? p1 : 0u;
+        if (from > 0 || valid < kPage) {
+            p0 = r >= from && r < valid ? p0 : 0u;
+            p1 = r + 8 >= from && r + 8 < valid ? p1 : 0u;
         }
         const uint32_t sw = __byte_perm(p0, p1, 0x5410), ow = __byte_perm(p0, p1, 0x7632);
         const __half2 s = *reinterpret_cast<const __half2 *>(&sw);
@@ -516,6 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
             // ================= tiles of f16 values from the records: K, V^T =================
             const int t = tid & 127;
             const bool keys = grp == 2;
+            const int seen = first_seen(a, s);
             while (true) {
                 const uint32_t slot = steps % kNS, ks = steps % kNK, vs = vsteps % kNV;
                 if (!waited(a, sh, &sh.rec_full[slot], (steps / kNS) & 1)) break;
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                 steps++;
                 if (j >= 0) {
                     if (keys) form_k(sh.rec[slot], sh.k[ks], t);
-                    else form_v(sh.rec[slot] + kRec, sh.v[vs], t, s.n - 64 * j);
+                    else form_v(sh.rec[slot] + kRec, sh.v[vs], t, seen - 64 * j, s.n - 64 * j);
                     fence_proxy_async();
                 }
                 __syncwarp();

@@ -191,12 +191,13 @@ __device__ __forceinline__ void tile_scores(const uint8_t *codes, const uint8_t 
 
 // O^T += V^T P^T over TT tiles. The lane holds words 2 g, 2 g + 1 of tokens 2 tig, 2 tig + 1 of a tile
 // and of the two eight further on: codes[e] and par point at token 2 tig (+ e for the codes) of the
-// first tile. In a sequence's last page (tail) tokens from `valid` on (counted from token 2 tig) hold
-// anything and count as 0. A permutation of bytes puts two tokens' nibbles of one channel into one register's halves.
+// first tile. In a page that begins or ends outside of what any query sees (edge), tokens before `from` and
+// from `valid` on (counted from token 2 tig) may hold anything and count as 0. A permutation of bytes puts
+// two tokens' nibbles of one channel into one register's halves.
 template <int NT, int TT>
 __device__ __forceinline__ void tile_values(const uint8_t *const (&codes)[2], const uint8_t *par,
-                                            bool tail, int valid, const uint32_t (&pf)[NT][TT][2],
-                                            State<NT> &st) {
+                                            bool edge, int from, int valid,
+                                            const uint32_t (&pf)[NT][TT][2], State<NT> &st) {
 #pragma unroll
     for (int tile = 0; tile < TT; tile++) {
         // [half of the tile] token pairs 16 tile + 8 half + 2 tig, + 1
@@ -206,9 +207,10 @@ __device__ __forceinline__ void tile_values(const uint8_t *const (&codes)[2], co
         for (int hi = 0; hi < 2; hi++) {
             uint32_t q0 = *reinterpret_cast<const uint32_t *>(par + tile * 256 + hi * 128);
             uint32_t q1 = *reinterpret_cast<const uint32_t *>(par + tile * 256 + hi * 128 + 16);
-            if (tail) {
-                q0 = 16 * tile + 8 * hi < valid ? q0 : 0u;
-                q1 = 16 * tile + 8 * hi + 1 < valid ? q1 : 0u;
+            if (edge) {
+                const int t = 16 * tile + 8 * hi;
+                q0 = t >= from && t < valid ? q0 : 0u;
+                q1 = t + 1 >= from && t + 1 < valid ? q1 : 0u;
             }
             s[hi] = __byte_perm(q0, q1, 0x5410);
             o[hi] = __byte_perm(q0, q1, 0x7632);
@@ -529,6 +531,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
             st.clear();
             bool far = false;  // one of the warp's references is
             const int low = s.n - s.nq;  // position of the first query
+            const int seen = first_seen(a, s);
             for (; i < i1; i++) {
                 const Entry e = sh.list[i];
                 if (e.unit != unit) break;
@@ -632,8 +635,9 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                     }
                     if (tile == 0) wait_copy(a, vfull, taken & 1, dead);
                     const uint8_t *const vc[2] = {vcodes[0] + tile * 1024, vcodes[1] + tile * 1024};
-                    tile_values<NT, TT>(vc, vpar + tile * 256, s.n - t0 < kPage,
-                                        s.n - t0 - 16 * tile - 2 * tig, pf, st);
+                    const int at = t0 + 16 * tile + 2 * tig;
+                    tile_values<NT, TT>(vc, vpar + tile * 256, s.n - t0 < kPage || t0 < seen, seen - at,
+                                        s.n - at, pf, st);
                 }
                 dead = __any_sync(0xffffffffu, dead);
                 if (ni < i1 && !dead) {

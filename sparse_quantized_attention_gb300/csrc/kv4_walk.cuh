@@ -27,6 +27,12 @@ struct Seq {
     int fp, np;     // first page any query sees, pages from there to the last
 };
 
+// The first token that any query of the sequence sees.
+__device__ __forceinline__ int first_seen(const AttnArgs &a, const Seq &s) {
+    const int low = s.n - s.nq;
+    return a.window > 0 && low >= a.window ? low - a.window + 1 : 0;
+}
+
 __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, bool report) {
     Seq s;
     s.n = __ldg(a.seq_lens + b);
@@ -46,11 +52,7 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, bool report) {
         }
     }
     if (report && bad) raise_error(a.err, FFD_ERRBIT_BOUNDS);
-    s.fp = 0;
-    if (a.window > 0) {
-        const int64_t first = (int64_t)s.n - s.nq - a.window + 1;
-        s.fp = first > 0 ? (int)(first >> 6) : 0;
-    }
+    s.fp = first_seen(a, s) >> 6;
     s.np = s.n > 0 && s.nq > 0 ? ((s.n + kPage - 1) >> 6) - s.fp : 0;
     return s;
 }

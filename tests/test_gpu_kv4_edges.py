@@ -7,7 +7,7 @@ import torch
 
 import sparse_quantized_attention_gb300 as ffd
 from tests import kv4_refs as R
-from tests.test_gpu_kv4 import BF16, F16, i32, offsets, table
+from tests.test_gpu_kv4 import BF16, F16, Case, i32, offsets, table
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +87,20 @@ def test_a_token_out_of_range_reaches_only_rows_that_see_it(nq, window, bad):
     held = torch.empty((2, n, Hkv, 128), dtype=F16, device="cuda")
     ffd.ffd_kv4_read(cache, i32([0]), bt.cuda(), held[0], held[1])
     assert bool(torch.isfinite(held).all())
+
+
+@pytest.mark.parametrize("nq", [1, 3, 6, 20, 100])
+@pytest.mark.parametrize("window", [1, 40, 64, 130])
+def test_tokens_behind_every_window_may_be_anything(nq, window):
+    """A page at the window's edge may hold tokens that were never written (a long prompt of which only
+    the part that the window reaches was)."""
+    lens = [300, 64, 1000, 65]
+    c = Case(lens, [min(nq, n) for n in lens], 2, 4, window=window, seed=nq + window)
+    c.poison_unused()
+    for b, n in enumerate(lens):
+        for t in range(0, max(0, n - c.qlens[b] - window + 1)):
+            page = int(c.bt[b, t // 64])
+            for rec in (c.k4, c.v4):
+                rec[page, :, 4096 + 16 * (t % 64):4112 + 16 * (t % 64)] = 0xff
+    out, lse = c.run()
+    c.check(out, lse)
