@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         __syncthreads();  // nobody stops between the reading of it and this
         const float fs = grp < 2 ? sh.factor[grp * kTile + r] : 0.0f;
 
-        float m = -INFINITY, l = 0.0f;
+        float m = -INFINITY, limit = -INFINITY, l = 0.0f;  // limit: a larger score raises m
         bool any = false, far = false;
         if (run && grp < 2) {
             // ================= softmax of tile grp, one row a thread =================
@@ -450,11 +450,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                     for (int c = 0; c < 32; c += 2)
                         top = fmaxf(top, fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 1])));
                     top *= fs;
-                    const bool raise = top > m + (is_far(m) ? 0.0f : kLazy);  // (m is -inf at first)
+                    const bool raise = top > limit;
                     if (__any_sync(0xffffffffu, raise)) {
                         const float mn = raise ? top : m;
                         const float al = m == -INFINITY ? 0.0f : ex2_approx(m - mn);
                         m = mn;
+                        limit = m + (is_far(m) ? 0.0f : kLazy);
                         l *= al;
                         far = __any_sync(0xffffffffu, is_far(m));
                         if (any) {
