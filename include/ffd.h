@@ -103,7 +103,8 @@ typedef struct {
                                    this call (a CTA waiting for a copy, for another warp or for
                                    another CTA); 0 takes the default of 2 s. A wait that runs out
                                    sets FFD_ERRBIT_TIMEOUT, the CTA stops waiting and drains its
-                                   own copies, and the kernel ends (results invalid). */
+                                   own copies (for 2 s at most, or this limit if it is longer),
+                                   and the kernel ends (results invalid). */
     int32_t schedule;           /* the order of the work of ffd_decode_attention(_static), with
                                    the same results: FFD_SCHEDULE_FUSED (0) or
                                    FFD_SCHEDULE_SCAN_REFINE (1), below; ignored by the masked,
@@ -536,7 +537,8 @@ size_t ffd_kv4_workspace_size(const ffd_kv4_params *params);
  *               leaves it ready for the next one. Calls that share a workspace must be ordered.
  * Errors: host-side statuses; FFD_ERRBIT_BOUNDS for a block-table entry outside [0, P) (the block
  * is treated as dropped), a sequence length out of range (clamped), or a cu_q entry out of range
- * (that sequence's rows are left as they were).
+ * (that sequence's rows are left as they were); FFD_ERRBIT_TIMEOUT for a wait that ran out
+ * (the call's results are invalid, the workspace is ready for the next one).
  */
 ffd_status ffd_kv4_attention(const ffd_kv4_params *params, const void *q, const uint8_t *k4,
                              const uint8_t *v4, const int32_t *seq_lens, const int32_t *cu_q,

@@ -60,7 +60,7 @@ struct Shared {
     uint64_t rec_full[kNS], rec_free[kNS];
     uint64_t k_full[kNK], k_free[kNK], v_full[kNV], v_free[kNV];
     uint64_t s_full[2][2], p_full[2][2];  // [tile][step % 2]: scores stand, probabilities stand
-    uint64_t o_done[2], drain;            // P V of a tile's step is done
+    uint64_t o_done[2], drain[2];         // P V of a tile's step is done
     uint32_t tmem, aborted;
     int info[kInfo];                   // page index of a step, -1: the segment's end
     int scan[kCtaWarps];
@@ -137,15 +137,6 @@ __device__ __forceinline__ bool waited(const AttnArgs &a, Shared &sh, uint64_t *
     bool ok = mbar_try_wait(bar, parity);
     if (!ok) ok = wait_long(a, sh, bar, parity);
     return __all_sync(0xffffffffu, ok);
-}
-// The same for what this CTA has in flight, whether or not it has stopped.
-__device__ __forceinline__ void drain(const AttnArgs &a, uint64_t *bar, uint32_t parity) {
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity))
-        if (globaltimer_ns() - t0 > a.wait_ns) {
-            raise_error(a.err, FFD_ERRBIT_TIMEOUT);
-            return;
-        }
 }
 
 // ---- forming the tiles --------------------------------------------------------------------------
@@ -271,8 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
                 mbar_init(&sh.p_full[i][j], 4);
             }
             mbar_init(&sh.o_done[i], 1);
+            mbar_init(&sh.drain[i], 1);
         }
-        mbar_init(&sh.drain, 2);
         fence_barrier_init();
     }
     // ---- weight of the items before each chunk of sequences: a warp for each of a few, else a thread
@@ -803,15 +794,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         }
     }
     if (stopped(sh)) {  // leave nothing in flight
+        bool done = true;
         if (warp == 18 && lane == 0)
             for (uint32_t i = 0; i < kNS && i < steps; i++) {
                 const uint32_t last = steps - 1 - i;
-                drain(a, &sh.rec_full[last % kNS], (last / kNS) & 1);
+                done &= mbar_drain(&sh.rec_full[last % kNS], (last / kNS) & 1, a.wait_ns);
             }
         if ((warp == 16 || warp == 17) && elect_one()) {
-            tc_commit(&sh.drain);
-            drain(a, &sh.drain, 0);
+            tc_commit(&sh.drain[warp - 16]);
+            done = mbar_drain(&sh.drain[warp - 16], 0, a.wait_ns);
         }
+        if (!done) raise_error(a.err, FFD_ERRBIT_TIMEOUT);
     }
     __syncthreads();
     __syncwarp();

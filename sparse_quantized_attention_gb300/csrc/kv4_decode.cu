@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                                       vbuf + code_offset(2 * tig + 1, g >> 1) + 8 * (g & 1)};
     const uint8_t *vpar = vbuf + param_offset(2 * tig, g >> 1);
     uint64_t *kfull = &sh.full[warp][0], *vfull = &sh.full[warp][1];
-    uint32_t taken = 0;  // pages this warp has finished
+    uint32_t taken = 0, kissued = 0, vissued = 0;  // pages this warp has finished, copies asked for
     bool dead = false;
     // a range is walked in windows w0 .. w1 - 1 that fit the list; a unit that goes on in the next
     // window leaves its joined state in one of the CTA's two carry records
@@ -509,7 +509,6 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                 tma_load_1d(to, from + (int64_t)sh.list[i].rec * kRec, kRec, bar);
             }
         };
-        uint32_t kissued = taken, vissued = taken;
         if (w0 != r0) fence_proxy_async();  // the room held the last window's states
         {
             const int i = next(i0);
@@ -668,9 +667,10 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
             }
         }
         if (dead) {  // leave no copy in flight
-            bool late = false;
-            if (kissued) wait_copy(a, kfull, (kissued - 1) & 1, late);
-            if (vissued) wait_copy(a, vfull, (vissued - 1) & 1, late);
+            bool done = true;
+            if (kissued) done = mbar_drain(kfull, (kissued - 1) & 1, a.wait_ns);
+            if (vissued) done &= mbar_drain(vfull, (vissued - 1) & 1, a.wait_ns);
+            if (!done) raise_error(a.err, FFD_ERRBIT_TIMEOUT);
         }
         __syncthreads();
 

@@ -86,6 +86,18 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 // another one per call).
 constexpr uint64_t kWaitTimeoutNs = 2000000000ull;
 
+// Wait for what this CTA has in flight into its own shared or tensor memory, before it leaves or reuses
+// that: bounded by the default or the caller's limit, whichever is longer, since a limit below a copy's
+// time (about 2 us) is one that the caller may set. False when the bound ran out.
+__device__ __forceinline__ bool mbar_drain(uint64_t *bar, uint32_t parity, uint64_t wait_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t bound = wait_ns > kWaitTimeoutNs ? wait_ns : kWaitTimeoutNs;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer_ns() - t0 > bound) return false;
+    return true;
+}
+
 // ---- TMA ------------------------------------------------------------------------------------
 // 1-D bulk copy global -> shared, completion counted on `bar` (16-byte aligned, size % 16 == 0).
 __device__ __forceinline__ void tma_load_1d(void *dst, const void *src, uint32_t bytes,

@@ -104,3 +104,33 @@ def test_tokens_behind_every_window_may_be_anything(nq, window):
                 rec[page, :, 4096 + 16 * (t % 64):4112 + 16 * (t % 64)] = 0xff
     out, lse = c.run()
     c.check(out, lse)
+
+
+@pytest.mark.parametrize("q", [1, 3, 6, 40, 400])
+@pytest.mark.parametrize("splits", [0, 3])
+def test_a_wait_that_runs_out(q, splits):
+    """The shortest limit, below the time of a copy: the call ends, reports it or is right, and leaves the
+    workspace to the next call. (The time of all 20 calls is bounded: nothing waits for what never comes.)"""
+    c = Case([9000, 100, 2500], [q, min(q, 100), q], 2, 4, seed=q)
+    p, short = c.params(num_splits=splits), c.params(num_splits=splits, wait_limit_us=1)
+    ws = ffd.alloc_kv4_workspace(p)
+    good = c.buffers()
+    c.call(*good, ws, p)
+    assert ffd.ffd_get_error(ws) == 0
+    c.check(*good)
+    e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    e0.record()
+    for _ in range(20):
+        out, lse = c.buffers()
+        c.call(out, lse, ws, short)
+        status = ffd.ffd_get_error(ws)
+        assert status in (0, 7)
+        if status == 0:
+            assert torch.equal(out, good[0])
+        out, lse = c.buffers()
+        c.call(out, lse, ws, p)
+        assert ffd.ffd_get_error(ws) == 0
+        assert torch.equal(out, good[0]) and torch.equal(lse, good[1])
+    e1.record()
+    torch.cuda.synchronize()
+    assert e0.elapsed_time(e1) < 1500.0  # ms; a drain alone may take 2 s when its copy never lands
