@@ -268,13 +268,8 @@ __global__ void __launch_bounds__(kArtThreads) art_kernel(const __grid_constant_
         // leave no copy in flight: the group's stages still being filled
         for (int s = 0; s < 2; s++) {
             if (!((issued >> s) & 1)) continue;
-            const uint64_t t0 = globaltimer_ns();
-            while (!mbar_try_wait(&ctl.full[g * 2 + s], (fph >> s) & 1u)) {
-                if (globaltimer_ns() - t0 > a.wait_ns) {
-                    if (mt == 0 && lane == 0) raise_error(a.err, FFD_ERRBIT_TIMEOUT);
-                    break;
-                }
-            }
+            if (!mbar_drain(&ctl.full[g * 2 + s], (fph >> s) & 1u, a.wait_ns) && mt == 0 && lane == 0)
+                raise_error(a.err, FFD_ERRBIT_TIMEOUT);
         }
         return;
     }

@@ -102,12 +102,10 @@ __global__ void __launch_bounds__(128) block_stats_kernel(DecodeArgs a, float *i
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(&full[warp][st], (phases >> st) & 1u)) {
             if (globaltimer_ns() - t0 > a.wait_ns) {
-                phases ^= 1u << st;
                 if (lane == 0) raise_error(a.err, FFD_ERRBIT_TIMEOUT);
                 return false;
             }
         }
-        phases ^= 1u << st;
         return true;
     };
     ThumbOps Q;
@@ -127,7 +125,8 @@ __global__ void __launch_bounds__(128) block_stats_kernel(DecodeArgs a, float *i
         const bool good = (have >> st) & 1u;
         if (good) {
             ok = __all_sync(0xffffffffu, wait_stage(st));
-            if (!ok) break;
+            if (!ok) break;  // the stage's phase is still to come: drained below
+            phases ^= 1u << st;
         }
         const int rows = n - c * kPage < kPage ? n - c * kPage : kPage;
         float x[4][4];
@@ -188,7 +187,9 @@ __global__ void __launch_bounds__(128) block_stats_kernel(DecodeArgs a, float *i
     }
     // copies still in flight into this warp's stages are waited for (bounded) before it exits
     for (int k = 0; k < 2; k++)
-        if ((have >> k) & 1u) __all_sync(0xffffffffu, wait_stage(k));
+        if (((have >> k) & 1u) && !mbar_drain(&full[warp][k], (phases >> k) & 1u, a.wait_ns) &&
+            lane == 0)
+            raise_error(a.err, FFD_ERRBIT_TIMEOUT);
 }
 
 // Float -> unsigned key whose unsigned order is the float's order (NaN never occurs here).

@@ -131,16 +131,10 @@ __device__ __forceinline__ void wait_bar(const DecodeArgs &a, M *m, uint64_t *ba
     }
 }
 
-// Wait for a copy this CTA issued, ignoring the abort flag (still bounded in time): no CTA exits
-// with a copy into its shared memory in flight.
+// Wait for a copy this CTA issued, ignoring the abort flag (bounded, but not by a caller's limit that
+// is shorter than a copy takes): no CTA exits with a copy into its shared memory in flight.
 __device__ __forceinline__ void drain_bar(const DecodeArgs &a, uint64_t *bar, uint32_t parity) {
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (globaltimer_ns() - t0 > a.wait_ns) {
-            raise_error(a.err, FFD_ERRBIT_TIMEOUT);
-            return;
-        }
-    }
+    if (!mbar_drain(bar, parity, a.wait_ns)) raise_error(a.err, FFD_ERRBIT_TIMEOUT);
 }
 
 template <class M>
