@@ -438,7 +438,7 @@ ffd_status ffd_decode_attention_static(const ffd_decode_params *params, const vo
  *   dtype         FFD_DTYPE_BF16 or FFD_DTYPE_F16, of k_new and v_new
  *   batch         B >= 1 sequences
  *   max_blocks_per_seq  row stride of block_table (>= 1)
- *   total_tokens  T >= 0 rows of k_new and v_new
+ *   total_tokens  T >= 0 rows of k_new and v_new; with T = 0 nothing is done, and both may be NULL
  *   k_new, v_new  device [T][Hkv][128], rows k_stride / v_stride elements apart (>= Hkv * 128 and a
  *                 multiple of 8, so that they may lie inside a fused projection), 16-byte aligned
  *   cu_tokens     device int32 [B+1], non-decreasing: sequence b has rows cu[b] .. cu[b+1]-1. Rows
@@ -470,7 +470,7 @@ ffd_status ffd_kv4_write(const ffd_cache_desc *cache, int32_t dtype, int32_t bat
  * ffd_kv4_write; rows of k_out / v_out that belong to nobody, and those of a sequence with a
  * negative position, are left as they were.
  *   k_out, v_out  device [T][Hkv][128] of dtype, or NULL for the tensor that is not wanted (not
- *                 both); the f16 value held, rounded once more for FFD_DTYPE_BF16
+ *                 both unless T = 0); the f16 value held, rounded once more for FFD_DTYPE_BF16
  *   error_word    device int32, or NULL: FFD_ERRBIT_BOUNDS for a token index >=
  *                 64 * max_blocks_per_seq or a page outside [0, P): the token's rows become 0
  */

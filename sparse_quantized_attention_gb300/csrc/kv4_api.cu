@@ -218,7 +218,7 @@ ffd_status ffd_kv4_write(const ffd_cache_desc *cache, int32_t dtype, int32_t bat
                          const int32_t *cu_tokens, const int32_t *positions,
                          const int32_t *block_table, uint8_t *k4, uint8_t *v4,
                          int32_t *error_word, void *stream) {
-    if (!k_new || !v_new) return FFD_ERR_INVALID_ARG;
+    if ((!k_new || !v_new) && total_tokens != 0) return FFD_ERR_INVALID_ARG;
     const ffd_status st =
         check_rows(cache, dtype, batch, max_blocks_per_seq, total_tokens, k_new, k_stride, v_new,
                    v_stride, cu_tokens, positions, block_table, k4, v4);
@@ -234,7 +234,7 @@ ffd_status ffd_kv4_read(const ffd_cache_desc *cache, int32_t dtype, int32_t batc
                         const int32_t *positions, const int32_t *block_table, const uint8_t *k4,
                         const uint8_t *v4, void *k_out, int64_t k_stride, void *v_out,
                         int64_t v_stride, int32_t *error_word, void *stream) {
-    if (!k_out && !v_out) return FFD_ERR_INVALID_ARG;
+    if (!k_out && !v_out && total_tokens != 0) return FFD_ERR_INVALID_ARG;
     const ffd_status st =
         check_rows(cache, dtype, batch, max_blocks_per_seq, total_tokens, k_out, k_stride, v_out,
                    v_stride, cu_tokens, positions, block_table, k4, v4);
