@@ -38,7 +38,8 @@ bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(
 ffd_status check_rows(const ffd_cache_desc *cache, int32_t dtype, int32_t batch, int32_t max_blocks,
                       int32_t total, const void *k, int64_t k_stride, const void *v,
                       int64_t v_stride, const int32_t *cu, const int32_t *positions,
-                      const int32_t *block_table, const uint8_t *k4, const uint8_t *v4) {
+                      const int32_t *block_table, const uint8_t *k4, const uint8_t *v4,
+                      const int32_t *error_word) {
     if (!cache || !positions || !block_table) return FFD_ERR_INVALID_ARG;
     if (cache->num_pages < 1 || cache->num_kv_heads < 1 || batch < 1 || max_blocks < 1 || total < 0)
         return FFD_ERR_INVALID_ARG;
@@ -49,7 +50,7 @@ ffd_status check_rows(const ffd_cache_desc *cache, int32_t dtype, int32_t batch,
     if (k && (k_stride < row || k_stride % 8 != 0 || !k4)) return FFD_ERR_INVALID_ARG;
     if (v && (v_stride < row || v_stride % 8 != 0 || !v4)) return FFD_ERR_INVALID_ARG;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k4, 16) || !aligned(v4, 16) ||
-        !aligned(cu, 4) || !aligned(positions, 4) || !aligned(block_table, 4))
+        !aligned(cu, 4) || !aligned(positions, 4) || !aligned(block_table, 4) || !aligned(error_word, 4))
         return FFD_ERR_INVALID_ARG;
     if ((int64_t)max_blocks * kPage > INT32_MAX) return FFD_ERR_UNSUPPORTED;
     if (cache->num_kv_heads > 65535) return FFD_ERR_UNSUPPORTED;  // grid.y
@@ -221,7 +222,7 @@ ffd_status ffd_kv4_write(const ffd_cache_desc *cache, int32_t dtype, int32_t bat
     if ((!k_new || !v_new) && total_tokens != 0) return FFD_ERR_INVALID_ARG;
     const ffd_status st =
         check_rows(cache, dtype, batch, max_blocks_per_seq, total_tokens, k_new, k_stride, v_new,
-                   v_stride, cu_tokens, positions, block_table, k4, v4);
+                   v_stride, cu_tokens, positions, block_table, k4, v4, error_word);
     if (st != FFD_OK) return st;
     const RowsArgs a = rows_args(cache, batch, max_blocks_per_seq, total_tokens, k_stride, v_stride,
                                  cu_tokens, positions, block_table, error_word);
@@ -237,7 +238,7 @@ ffd_status ffd_kv4_read(const ffd_cache_desc *cache, int32_t dtype, int32_t batc
     if (!k_out && !v_out && total_tokens != 0) return FFD_ERR_INVALID_ARG;
     const ffd_status st =
         check_rows(cache, dtype, batch, max_blocks_per_seq, total_tokens, k_out, k_stride, v_out,
-                   v_stride, cu_tokens, positions, block_table, k4, v4);
+                   v_stride, cu_tokens, positions, block_table, k4, v4, error_word);
     if (st != FFD_OK) return st;
     const RowsArgs a = rows_args(cache, batch, max_blocks_per_seq, total_tokens, k_stride, v_stride,
                                  cu_tokens, positions, block_table, error_word);

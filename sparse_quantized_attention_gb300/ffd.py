@@ -412,6 +412,8 @@ def _kv4_rows(where, cache, positions, block_table, k, v, cu_tokens, error_word)
             and (cu_tokens is None or (cu_tokens.dtype == _I32 and cu_tokens.is_contiguous()
                                        and cu_tokens.shape == (table[0] + 1,)))):
         _refuse(where, "int32 positions [B], cu_tokens [B + 1], block_table [B, width]")
+    if error_word is not None and error_word.nbytes < 4:
+        _refuse(where, "an error word of 4 bytes")
     P, Hkv, _ = shape
     T, dtype = one.shape[0], one.dtype
     ks = 0 if k is None else _row_stride(k, T, Hkv, dtype)

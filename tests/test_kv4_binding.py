@@ -1,9 +1,11 @@
 """What the 4-bit cache's binding and entries take and refuse besides shapes (no GPU needed)."""
+import ctypes
+
 import pytest
 import torch
 
 import sparse_quantized_attention_gb300 as ffd
-from tests.test_kv4_host import lib, rows_call  # noqa: F401  (lib is a fixture)
+from tests.test_kv4_host import FAKE, OnGpu, lib, rows_call  # noqa: F401  (lib is a fixture)
 
 
 @pytest.mark.parametrize("read", [False, True], ids=["write", "read"])
@@ -18,6 +20,32 @@ def test_no_rows_without_storage(lib, read):
     assert rows_call(lib, read, total=0, k=None, v=None, pos=None) == 1
     assert rows_call(lib, read, total=0, k=None, v=None, desc=(4, 2, 64, 64)) == 2
     assert rows_call(lib, read, total=0, k=None, v=None, dtype=2) == 1
+
+
+@pytest.mark.parametrize("read", [False, True], ids=["write", "read"])
+def test_error_word(lib, read):
+    """A kernel adds to four bytes at it: it has to be aligned and as large."""
+    d = ctypes.byref(ffd.CacheDesc(4, 2, 128, 64))
+
+    def call(err):  # of no rows: nothing is launched when all is well
+        if read:
+            return lib.ffd_kv4_read(d, 0, 2, 3, 0, None, FAKE, FAKE, FAKE, FAKE, None, 256, None, 256,
+                                    err, None)
+        return lib.ffd_kv4_write(d, 0, 2, 3, 0, None, 256, None, 256, None, FAKE, FAKE, FAKE, FAKE, err,
+                                 None)
+    assert call(None) == 0 and call(FAKE + 4) == 0
+    assert call(FAKE + 1) == 1 and call(FAKE + 2) == 1
+    bt, pos = OnGpu(torch.zeros((2, 3), dtype=torch.int32)), OnGpu(torch.zeros(2, dtype=torch.int32))
+    x = OnGpu(torch.zeros((2, 2, 128), dtype=torch.bfloat16))
+    cache = tuple(OnGpu(torch.zeros((4, 2, 5120), dtype=torch.uint8)) for _ in range(2))
+    for bad in (torch.zeros(3, dtype=torch.uint8), torch.zeros(1, dtype=torch.float16),
+                torch.zeros(0, dtype=torch.int32)):
+        with pytest.raises(ffd.FFDError) as e:
+            if read:
+                ffd.ffd_kv4_read(cache, pos, bt, x, x, error_word=OnGpu(bad))
+            else:
+                ffd.ffd_kv4_write(x, x, pos, bt, cache, error_word=OnGpu(bad))
+        assert "error word" in str(e.value)
 
 
 @pytest.mark.gpu
