@@ -353,8 +353,8 @@ def alloc_kv4_cache(num_pages: int, num_kv_heads: int, device="cuda") -> Kv4Cach
 
 # The three calls below check their tensors in one flat expression each: a decode step takes about as
 # long on the host as on the GPU, and every function call and attribute that is read counts.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# (torch._C's two lookups are there in CUDA builds alone, which importing this does not ask for)
+_C = torch._C
 _I32, _U8, _F32 = torch.int32, torch.uint8, torch.float32
 _descs = {}  # (P, Hkv) -> a reference to its CacheDesc
 
@@ -372,7 +372,7 @@ def _desc(P: int, Hkv: int):
 
 def _stream_of(stream, dev: int) -> int:
     if stream is None:
-        return _raw_stream(dev)
+        return _C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
@@ -437,7 +437,7 @@ def ffd_kv4_write(k_new, v_new, positions, block_table, cache: Kv4Cache, *, cu_t
         _refuse(where, "no rows")
     dev, P, Hkv, B, width, T, dtype, ks, vs = _kv4_rows(where, cache, positions, block_table, k_new,
                                                         v_new, cu_tokens, error_word)
-    if _current_device() != dev:
+    if _C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return ffd_kv4_write(k_new, v_new, positions, block_table, cache, cu_tokens=cu_tokens,
                                  error_word=error_word, stream=stream)
@@ -456,7 +456,7 @@ def ffd_kv4_read(cache: Kv4Cache, positions, block_table, k_out, v_out, *, cu_to
     where = "ffd_kv4_read"
     dev, P, Hkv, B, width, T, dtype, ks, vs = _kv4_rows(where, cache, positions, block_table, k_out,
                                                         v_out, cu_tokens, error_word)
-    if _current_device() != dev:
+    if _C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return ffd_kv4_read(cache, positions, block_table, k_out, v_out, cu_tokens=cu_tokens,
                                 error_word=error_word, stream=stream)
@@ -533,7 +533,7 @@ def ffd_kv4_attention(params: Kv4Params, q, cache: Kv4Cache, seq_lens, block_tab
         _refuse(where, "lse fp32 [total_q, Hq]")
     if not workspace.is_contiguous():
         _refuse(where, "the workspace")
-    if _current_device() != dev:
+    if _C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return ffd_kv4_attention(params, q, cache, seq_lens, block_table, out, workspace,
                                      cu_q=cu_q, keep_in=keep_in, lse=lse, stream=stream)

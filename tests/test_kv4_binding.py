@@ -1,11 +1,16 @@
 """What the 4-bit cache's binding and entries take and refuse besides shapes (no GPU needed)."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
 
 import sparse_quantized_attention_gb300 as ffd
 from tests.test_kv4_host import FAKE, OnGpu, lib, rows_call  # noqa: F401  (lib is a fixture)
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.mark.parametrize("read", [False, True], ids=["write", "read"])
@@ -46,6 +51,17 @@ def test_error_word(lib, read):
             else:
                 ffd.ffd_kv4_write(x, x, pos, bt, cache, error_word=OnGpu(bad))
         assert "error word" in str(e.value)
+
+
+def test_import_without_a_cuda_build():
+    """The package is imported where PyTorch has no CUDA, for its constants and parameters."""
+    code = ("import torch\n"
+            "for name in [n for n in dir(torch._C) if n.startswith('_cuda_')]:\n"
+            "    delattr(torch._C, name)\n"
+            "import sparse_quantized_attention_gb300 as ffd\n"
+            "assert ffd.make_kv4_params(1, 8, 2, 4, 2).max_q_len == 1\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
 
 
 @pytest.mark.gpu
