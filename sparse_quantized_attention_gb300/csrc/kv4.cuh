@@ -14,6 +14,9 @@ constexpr int kMaxCtas = 1024;     // of an attention launch (one per SM at most
 // Pages' time that an item of the chunk kernel costs besides its pages (queries, first copies, results:
 // 19000 to 20000 cycles, 2100 a page).
 constexpr int kChunkLead = 9;
+// Pages' time that cutting items costs a CTA of the chunk kernel (a second start, records, joins): when
+// it takes one item, and when it takes several and has two of them cut.
+constexpr int kJoinPages = 24, kJoinPagesSeveral = 39;
 constexpr float kMaxInput = 16384.0f;  // |off| <= |min| + 16/15 range stays inside f16
 
 // Byte offset, inside a record, of the 16 code bytes of group g (32 channels) of token r.
@@ -137,7 +140,7 @@ struct RowsArgs {
 // Arguments of an attention call.
 struct AttnArgs {
     int B, Hq, Hkv, G, P, max_blocks, max_q, total_q, window;
-    int whole_items;  // chunk kernel: items are not cut
+    int whole_items;  // chunk kernel: items are not cut if the lengths are even enough
     int lead;         // chunk kernel: pages' time that an item counts for besides its pages
     uint32_t over_g;  // ceil(2^32 / G), too large by less than G / 2^32 of it (G > 1)
     int64_t q_stride;

@@ -105,9 +105,6 @@ size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 // At least this many pages (upper bound from the table's width) for each CTA.
 constexpr int64_t kMinDecodePages = 8, kMinChunkPages = 4;
-// Pages' time that cutting items costs a CTA of the chunk kernel (a second start, records, joins): when
-// it takes one item, and when it takes several and has two of them cut.
-constexpr double kJoinPages = 24.0, kJoinPagesSeveral = 39.0;
 
 // Pages of a cut item that a CTA of the chunk kernel takes at least, for items of n pages: cut in k
 // they take n / k pages' time and then that of the records that are joined one after another, k of
@@ -129,7 +126,8 @@ int64_t chunk_pages(int64_t n, int64_t rows) {
 }
 
 // Where whole items (256 rows over the pages they see) are dealt out, `rounds` consecutive ones to a CTA:
-// the pages' time that the longest-working CTA has beyond an equal share. Some CTAs have an item
+// the pages' time that the longest-working CTA has beyond an equal share if all sequences fill the block
+// table (the kernel looks at how unequal they are, and cuts the items all the same if they are too much). Some CTAs have an item
 // fewer, and the groups of rows of a unit see from first to last as many more pages as there are query
 // tokens (less behind a window). While that is less than what cutting costs, whole items are the
 // faster way. Measured, us whole and cut, 8 heads and 4 query heads for each:
@@ -196,7 +194,7 @@ ffd_status make_plan(const ffd_kv4_params *p, Plan *pl) {
     // 256 rows a head of eight sequences of 5000 to 16384: 122 and 117). Every CTA that begins within an item has such a
     // cost too; with few long items that is nearly all of them, and only those that begin with an item
     // would get fewer pages (256 rows a head of one sequence of 32768: 67.2 us without, 68.6 with).
-    pl->lead = pl->cols || pl->whole_items || 8 * items <= ctas ? 0 : kChunkLead;
+    pl->lead = pl->cols || 8 * items <= ctas ? 0 : kChunkLead;
     const size_t rec = pl->cols ? decode_record_bytes(pl->cols) : chunk_record_bytes();
     size_t off = kAlign;
     pl->tickets = off;

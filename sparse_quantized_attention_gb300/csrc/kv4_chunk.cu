@@ -63,10 +63,11 @@ struct Shared {
     uint64_t o_done[2], drain[2];         // P V of a tile's step is done
     uint32_t tmem, aborted;
     int info[kInfo];                   // page index of a step, -1: the segment's end
-    int scan[kCtaWarps];
+    int scan[2][kCtaWarps], heaviest[kCtaWarps];
     int flag;
     float factor[kRows];               // of the rows' scores
-    int pre[kThreads];                 // weight of all items before each chunk of sequences
+    // weight and number of all items before each chunk of sequences
+    int pre[kThreads], pre_items[kThreads];
 };
 static_assert(sizeof(Shared) + 1024 <= 232448, "shared memory per CTA");
 
@@ -90,11 +91,9 @@ __device__ __forceinline__ void item_pages(const AttnArgs &a, const Seq &s, int 
     np = hi < 0 ? 0 : (hi >> 6) - fp + 1;
 }
 
-// What one item weighs when the work is cut: `lead` before its first page and one for each, or one in
-// all; 0 behind the last one.
+// What one item weighs: `lead` before its first page and one for each; 0 behind the last one.
 __device__ __forceinline__ int item_weight(const AttnArgs &a, const Seq &s, int rt) {
     if (rt >= item_groups(a, s)) return 0;
-    if (a.whole_items) return 1;
     int fp, np;
     item_pages(a, s, rt, fp, np);
     return np > 0 ? np + a.lead : 0;
@@ -114,6 +113,20 @@ __device__ __forceinline__ int head_weight(const AttnArgs &a, const Seq &s, int 
     int sum = 0;
     for (int rt = 0; rt < item_groups(a, s); rt += 32) sum += item_weight(a, s, rt + lane);
     return __reduce_add_sync(0xffffffffu, sum);
+}
+
+// Whether whole items may be dealt out where the host has found that the block table's width and the
+// numbers of rows allow it (it cannot see the lengths): `heaviest` is the greatest of the sequences' mean
+// items. The longest-working CTA has at most `rounds` such items; when that is more than an equal share by
+// what cutting costs, the lengths are too unequal. Measured, us whole and cut, 8 heads, 4 query heads each:
+//   19 sequences of 1024 tokens, their last 9                        31   32
+//   18 of them, and one of 32768                                    471   74
+//   18 of them, and one of 131072                                  1831  152
+//   37 of 512 tokens, their last 64, and one of 16384               560   90
+__device__ __forceinline__ bool even_enough(int items, int weight, int heaviest, int ctas) {
+    const int rounds = (items + ctas - 1) / ctas, share = items < ctas ? items : ctas;
+    const int beyond = rounds * heaviest - (rounds > 1 ? kJoinPagesSeveral : kJoinPages);
+    return (int64_t)beyond * share <= weight;
 }
 
 // Bounded waits: once one runs out the CTA stops (aborted) and drains what is in flight.
@@ -269,32 +282,56 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
     // ---- weight of the items before each chunk of sequences: a warp for each of a few, else a thread
     const bool few = a.B <= 4 * kCtaWarps;
     const int chunk = few ? 1 : (a.B + kThreads - 1) / kThreads;
-    int own = 0;
+    int own = 0, own_items = 0, heaviest = 0;
     bool empty = false;  // some rows see nothing: perhaps whole items
     if (few) {
         for (int b = warp; b < a.B; b += kCtaWarps) {
             const Seq s = seq_of(a, b, blockIdx.x == 0);
-            const int w = head_weight(a, s, lane) * a.Hkv;
-            if (lane == 0) sh.pre[b] = w;
+            const int w = head_weight(a, s, lane), n = item_groups(a, s);
+            if (lane == 0) sh.pre[b] = w * a.Hkv, sh.pre_items[b] = n * a.Hkv;
+            if (n > 0) heaviest = max(heaviest, (w + n - 1) / n);
             empty |= s.n < s.nq;
         }
-        empty = __syncthreads_or(empty);
-        if (tid < a.B) own = sh.pre[tid];
     } else {
         for (int b = tid * chunk; b < (tid + 1) * chunk && b < a.B; b++) {
             const Seq s = seq_of(a, b, blockIdx.x == 0);
-            for (int rt = 0; rt < item_groups(a, s); rt++) own += item_weight(a, s, rt) * a.Hkv;
+            const int n = item_groups(a, s);
+            int w = 0;
+            for (int rt = 0; rt < n; rt++) w += item_weight(a, s, rt);
+            own += w * a.Hkv;
+            own_items += n * a.Hkv;
+            if (n > 0) heaviest = max(heaviest, (w + n - 1) / n);
             empty |= s.n < s.nq;
         }
-        empty = __syncthreads_or(empty);
     }
+    if (a.whole_items) {
+        heaviest = __reduce_max_sync(0xffffffffu, heaviest);
+        if (lane == 0) sh.heaviest[warp] = heaviest;
+    }
+    empty = __syncthreads_or(empty);
+    if (few && tid < a.B) own = sh.pre[tid], own_items = sh.pre_items[tid];
     const int inc = lane_scan(own, lane);
-    if (lane == 31) sh.scan[warp] = inc;
+    if (lane == 31) sh.scan[0][warp] = inc;
+    int inc_items = 0;
+    if (a.whole_items) {
+        inc_items = lane_scan(own_items, lane);
+        if (lane == 31) sh.scan[1][warp] = inc_items;
+    }
     __syncthreads();
-    const int of_warp = lane_scan(lane < kCtaWarps ? sh.scan[lane] : 0, lane);
-    const int total = __shfl_sync(0xffffffffu, of_warp, 31);
-    const int before = __shfl_sync(0xffffffffu, of_warp, warp == 0 ? 0 : warp - 1);
-    sh.pre[tid] = (warp == 0 ? 0 : before) + inc - own;
+    int total, total_items = 0;
+    auto prefix = [&](int which, int before, int *pre, int &all) {
+        const int of_warp = lane_scan(lane < kCtaWarps ? sh.scan[which][lane] : 0, lane);
+        all = __shfl_sync(0xffffffffu, of_warp, 31);
+        const int warps = __shfl_sync(0xffffffffu, of_warp, warp == 0 ? 0 : warp - 1);
+        pre[tid] = (warp == 0 ? 0 : warps) + before;
+    };
+    prefix(0, inc - own, sh.pre, total);
+    bool whole = false;
+    if (a.whole_items) {
+        prefix(1, inc_items - own_items, sh.pre_items, total_items);
+        heaviest = __reduce_max_sync(0xffffffffu, lane < kCtaWarps ? sh.heaviest[lane] : 0);
+        whole = even_enough(total_items, total, heaviest, gridDim.x);
+    }
     const bool any_empty = empty;
     if (any_empty) {  // items that see nothing at all
         for (int u = blockIdx.x; u < a.B * a.Hkv; u += gridDim.x) {
@@ -313,7 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
             }
         }
     }
-    const int ncta = total < (int)gridDim.x ? total : (int)gridDim.x;
+    const int shares = whole ? total_items : total;
+    const int ncta = shares < (int)gridDim.x ? shares : (int)gridDim.x;
     const int cta = blockIdx.x;
     tc_fence_before();
     __syncthreads();
@@ -324,18 +362,51 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         return;
     }
     const uint32_t tmem = sh.tmem;
-    const int c0 = (int)((int64_t)total * cta / ncta), c1 = (int)((int64_t)total * (cta + 1) / ncta);
-
-    // ---- where the range begins: sequence b, head h, group rt, `into` the item's weight ----------
-    int b, h, rt = 0, into;
-    Seq s;
-    {
+    int c0 = (int)((int64_t)shares * cta / ncta), c1 = (int)((int64_t)shares * (cta + 1) / ncta);
+    auto chunk_of = [&](const int *pre, int x) {  // the last chunk of sequences that begins at or before x
         int lo = 0, hi = kThreads;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (sh.pre[mid] <= c0) lo = mid;
+            if (pre[mid] <= x) lo = mid;
             else hi = mid;
         }
+        return lo;
+    };
+    // ---- where the range begins: sequence b, head h, group rt, `into` the item's weight ----------
+    int b = 0, h = 0, rt = 0, into = 0;
+    Seq s = {0, 0, 0, 0, 0};
+    auto next_item = [&]() {
+        if (++rt < item_groups(a, s)) return;
+        rt = 0;
+        if (++h < a.Hkv) return;
+        h = 0;
+        do {
+            s = seq_of(a, ++b, false);
+        } while (s.nq == 0);
+    };
+    if (whole) {  // items c0 .. c1 - 1: then a range of weight from the first that has some
+        const int lo = chunk_of(sh.pre_items, c0), items = c1 - c0;
+        int rem = c0 - sh.pre_items[lo], n = 0;
+        for (b = lo * chunk; b < a.B; b++) {
+            s = seq_of(a, b, false);
+            n = item_groups(a, s);
+            if (rem < n * a.Hkv) break;
+            rem -= n * a.Hkv;
+        }
+        h = rem / n;
+        rt = rem - h * n;
+        c0 = c1 = 0;
+        int b0 = b, h0 = h, rt0 = rt;
+        Seq s0 = s;
+        for (int i = 0; i < items; i++) {
+            if (i > 0) next_item();
+            const int w = item_weight(a, s, rt);
+            if (c1 == 0) b0 = b, h0 = h, rt0 = rt, s0 = s;
+            c1 += w;
+        }
+        b = b0, h = h0, rt = rt0, s = s0;
+    } else {
+        const int lo = chunk_of(sh.pre, c0);
         int rem = c0 - sh.pre[lo], hp = 0;
         for (b = lo * chunk; b < a.B; b++) {
             s = seq_of(a, b, false);
@@ -356,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
             }
             rem -= __shfl_sync(0xffffffffu, upto, 31);
         }
-        into = a.whole_items ? 0 : rem;
+        into = rem;
     }
 
     // so far in the whole kernel, per role: steps (segments' ends among them), and pages (V tiles and
@@ -367,8 +438,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         item_pages(a, s, rt, fp, np);
         const int first = x - into + a.lead;  // the item's first page in the cut's scale
         const int at = into > a.lead ? into - a.lead : 0;
-        const int cnt = (a.whole_items || np < c1 - first ? np : c1 - first) - at;
-        if (cnt <= 0 && !a.whole_items) break;  // the item's pages are the next CTA's
+        const int cnt = (np < c1 - first ? np : c1 - first) - at;
+        if (cnt <= 0) break;  // the item's pages are the next CTA's
         const int j0 = fp + at, j1 = j0 + cnt;
         const int row0 = rt * kRows, rows = s.nq * a.G - row0;  // rows: of this item and later
         const bool two = rows > kTile;
@@ -645,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         // (a whole item's rows by way of the tile's queries, which are read no more, so that lines of
         // out are written whole)
         float *mine = records + (int64_t)(kSlots * cta + (begins ? 1 : 0)) * kRecord;
-        if (grp < 2 && run && (grp == 0 || two) && np > 0) {
+        if (grp < 2 && run && (grp == 0 || two)) {
             const uint32_t to = tmem + ((uint32_t)(warp & 3) << 21) + kColO + grp * 128;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             float *row = mine + grp * kTile + r;
@@ -776,21 +847,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         tc_fence_after();
 
         // ---- the next item
-        x = a.whole_items ? x + 1 : first + at + cnt;
+        x = first + at + cnt;
         into = 0;
         if (x < c1) {
             do {
-                if (++rt >= item_groups(a, s)) {
-                    rt = 0;
-                    if (++h == a.Hkv) {
-                        h = 0;
-                        do {
-                            s = seq_of(a, ++b, false);
-                        } while (s.nq == 0 || (s.n == 0 && !a.whole_items));
-                    }
-                }
+                next_item();
                 item_pages(a, s, rt, fp, np);
-            } while (np == 0 && !a.whole_items);
+            } while (np == 0);
         }
     }
     if (stopped(sh)) {  // leave nothing in flight

@@ -134,3 +134,30 @@ def test_a_wait_that_runs_out(q, splits):
     e1.record()
     torch.cuda.synchronize()
     assert e0.elapsed_time(e1) < 1500.0  # ms; a drain alone may take 2 s when its copy never lands
+
+
+@pytest.mark.parametrize("lens,q", [([32768] + [1024] * 18, 9), ([700] * 37 + [16384], 64),
+                                    ([300, 9000] + [200] * 80, 30)])
+def test_unequal_lengths_are_cut(lens, q):
+    """One long sequence among short ones, as many units as there are SMs or more: its items are not
+    left to a few CTAs. The same call with cut items forced takes about as long (it took a sixth)."""
+    c = Case(lens, [q] * len(lens), 8, 4, seed=len(lens))
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    times = []
+    for splits in (0, sms):
+        p = c.params(num_splits=splits)
+        ws = ffd.alloc_kv4_workspace(p)
+        out, lse = c.buffers()
+        best = math.inf
+        for _ in range(8):
+            e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            torch.cuda._sleep(1_000_000)  # the host is ahead when the first event is reached
+            e0.record()
+            c.call(out, lse, ws, p)
+            e1.record()
+            torch.cuda.synchronize()
+            best = min(best, e0.elapsed_time(e1))
+        assert ffd.ffd_get_error(ws) == 0
+        c.check(out, lse)
+        times.append(best)
+    assert times[0] < 2.0 * times[1]
