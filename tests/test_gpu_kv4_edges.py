@@ -161,3 +161,53 @@ def test_unequal_lengths_are_cut(lens, q):
         c.check(out, lse)
         times.append(best)
     assert times[0] < 2.0 * times[1]
+
+
+@pytest.mark.parametrize("q", [1, 2, 6, 20, 90])
+def test_bad_offsets_and_lengths_of_any_row_count(q):
+    """A sequence whose offsets are out of order keeps its rows as they were, one whose length is out of
+    range is clamped; the others are what they are."""
+    lens = [300, 200, 100]
+    c = Case(lens, [q] * 3, 2, 4, seed=q, tail=3)
+    cache, T = ffd.Kv4Cache(c.k4, c.v4), c.T
+    p = c.params()
+    ws = ffd.alloc_kv4_workspace(p)
+
+    def check(lens, cu, good):
+        out, lse = c.buffers()
+        ffd.ffd_kv4_attention(p, c.q, cache, i32(lens), c.bt, out, ws, cu_q=i32(cu), lse=lse)
+        assert ffd.ffd_get_error(ws) == 5
+        mine = torch.zeros(T, dtype=torch.bool, device="cuda")
+        for b in good:
+            n, t0, t1 = min(max(lens[b], 0), 64 * c.bt.shape[1]), cu[b], cu[b + 1]
+            mine[t0:t1] = True
+            ref = R.attention64(c.q[t0:t1], c.k4, c.v4, [n], [0, t1 - t0], c.bt[b:b + 1], 2,
+                                sm=float(p.sm_scale))
+            tol, tol_lse = R.tolerance(*ref, BF16)
+            sees = ref[1] > -math.inf
+            assert bool(((out[t0:t1].double() - ref[0]).abs() <= tol)[sees].all())
+            assert bool(((lse[t0:t1].double() - ref[1]).abs() <= tol_lse)[sees].all())
+            assert bool((out[t0:t1][~sees] == 0).all())
+            assert bool((lse[t0:t1][~sees] == -math.inf).all())
+        assert bool((out[~mine] == 3.0).all()) and bool((lse[~mine] == 3.0).all())
+
+    check(lens, [0, q, T + 1, 2 * q], [0])          # an end past total_q, then offsets that fall
+    check(lens, [-1, q, 2 * q, 3 * q], [1, 2])
+    check(lens, [0, q, 2 * q + 1, 3 * q], [0, 2])   # one row more than max_q_len
+    check([300, -5, 100], c.cu, [0, 1, 2])
+    check([300, 2 ** 31 - 1, 100], c.cu, [0, 1, 2])  # clamped; its pages past the table are dropped
+
+
+@pytest.mark.parametrize("q,G", [(3, 4), (6, 4), (4, 8), (20, 4), (90, 8)])
+def test_a_bad_query_stays_in_its_row(q, G):
+    c = Case([500, 300], [q, q], 2, G, seed=q)
+    good, good_lse = c.run()
+    bad = [(0, 3, math.nan), (q - 1, 2 * G - 1, math.inf), (q, 0, -math.inf), (2 * q - 1, G, math.nan)]
+    for t, h, x in bad:
+        c.q[t, h, 17] = x
+    out, lse = c.run()
+    same = torch.ones(out.shape[:2], dtype=torch.bool, device="cuda")
+    for t, h, x in bad:
+        assert not bool(torch.isfinite(out[t, h]).all())
+        same[t, h] = False
+    assert torch.equal(out[same], good[same]) and torch.equal(lse[same], good_lse[same])
