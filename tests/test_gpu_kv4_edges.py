@@ -1,6 +1,9 @@
 """The 4-bit cache's attention where its arithmetic, its inputs or its plan come to an edge. Bounds as
 in tests/kv4_refs.py."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -211,3 +214,93 @@ def test_a_bad_query_stays_in_its_row(q, G):
         assert not bool(torch.isfinite(out[t, h]).all())
         same[t, h] = False
     assert torch.equal(out[same], good[same]) and torch.equal(lse[same], good_lse[same])
+
+
+FIRST_CALL = """
+import torch
+import sparse_quantized_attention_gb300 as ffd
+B, Hkv, G, n, P = 2, 2, 4, 130, 8
+gen = torch.Generator(device="cuda").manual_seed(1)
+x = torch.randn((2, B * n, Hkv, 128), generator=gen, device="cuda").bfloat16()
+bt = torch.arange(6, dtype=torch.int32, device="cuda").reshape(B, 3)
+first = torch.zeros(B, dtype=torch.int32, device="cuda")
+lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+cache = ffd.alloc_kv4_cache(P, Hkv)
+back = torch.empty_like(x)
+calls = []
+for nq in (1, 3, 5, 8, 40):
+    p = ffd.make_kv4_params(B, Hkv * G, Hkv, P, 3, max_q_len=nq)
+    q = torch.randn((B * nq, Hkv * G, 128), generator=gen, device="cuda").bfloat16()
+    calls.append((p, q, torch.empty_like(q), ffd.alloc_kv4_workspace(p)))
+
+def run():
+    ffd.ffd_kv4_write(x[0], x[1], first, bt, cache)
+    ffd.ffd_kv4_read(cache, first, bt, back[0], back[1])
+    for p, q, out, ws in calls:
+        ffd.ffd_kv4_attention(p, q, cache, lens, bt, out, ws)
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    run()
+graph.replay()
+torch.cuda.synchronize()
+got = [back.clone()] + [c[2].clone() for c in calls]
+for t in [back] + [c[2] for c in calls]:
+    t.zero_()
+run()
+assert all(torch.equal(a, b) for a, b in zip(got, [back] + [c[2] for c in calls]))
+assert all(ffd.ffd_get_error(c[3]) == 0 for c in calls)
+"""
+
+
+def test_a_first_call_may_be_captured():
+    """Every kernel is called for the first time in its process under a graph's capture."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("q", [1, 3, 20, 100])
+@pytest.mark.parametrize("kw", [dict(window=150, keep=0.5), dict(window=2 ** 31 - 1),
+                                dict(window=2 ** 31 - 1, keep=0.3)],
+                         ids=["window_mask", "largest_window", "largest_window_mask"])
+def test_windows(q, kw):
+    """A window and a mask together; a window as large as can be named, with more queries than tokens."""
+    c = Case([1000, 65, 2, 0], [q] * 4, 2, 4, seed=q, **kw)
+    c.poison_unused()
+    out, lse = c.run()
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("B", [1, 3, 100, 700])
+@pytest.mark.parametrize("q", [1, 3, 20])
+def test_nothing_to_see(q, B):
+    """Empty sequences alone, and one token among them."""
+    for last in (0, 1):
+        c = Case([0] * (B - 1) + [last], [q] * B, 2, 4, seed=q)
+        out, lse = c.run()
+        c.check(out, lse)
+
+
+def test_offsets_out_of_order_write_inside_the_cache():
+    """cu_tokens that fall and pass the rows' number: rows go where they name a place or nowhere."""
+    gen = torch.Generator().manual_seed(1)
+    Hkv, T, width = 2, 12, 2
+    bt, P = table([128, 128, 128], gen, spare=2)
+    x = torch.randn((T, Hkv, 128), generator=gen).to(BF16).cuda()
+    cache = ffd.alloc_kv4_cache(P, Hkv)
+    used = set(bt.flatten().tolist())
+    spare = [i for i in range(P) if i not in used]
+    for t in cache:
+        t.fill_(9)
+    err = i32([0])
+    for cu in ([0, 9, 3, 12], [5, 2, 1, 0], [-8, 4, 100, 20], [20, 30, 40, 50]):
+        ffd.ffd_kv4_write(x, x, i32([0, 60, 126]), bt.cuda(), cache, cu_tokens=i32(cu), error_word=err)
+        assert ffd.ffd_get_error(err) in (0, 5)
+        out = torch.full_like(x, 5.0)
+        ffd.ffd_kv4_read(cache, i32([0, 60, 126]), bt.cuda(), out, None, cu_tokens=i32(cu),
+                         error_word=err)
+        assert ffd.ffd_get_error(err) in (0, 5)
+    assert all(bool((t[spare] == 9).all()) for t in cache)
