@@ -1,13 +1,14 @@
 // kv4_decode.cu -- attention over the 4-bit cache for few query rows: up to 8 NT (row, head) pairs
-// share a KV head (NT = 1: one decode token of any GQA group; NT = 2 and 4: drafted tokens).
+// share a KV head (NT = 1: one decode token of any GQA group; NT = 2 to 4: drafted tokens).
 //
 // The definition is the one of ffd.h. The pages of all (sequence, KV head) units, concatenated, are
-// cut into equal contiguous ranges, one per CTA (more when a range would not fit its list). The CTA
-// lists the pages of its range that a mask keeps, each warp takes an equal share of the list and
+// cut into equal contiguous ranges, one per CTA, and a range is walked in windows of kWindow pages: what
+// its list has room for (a unit that goes on in the next window leaves its state in a carry record). The
+// CTA lists the window's pages that a mask keeps, each warp takes an equal share of the list and
 // walks it alone: it has room for one page's K record and one V record in shared memory, each refilled
 // by a bulk copy as soon as it has been read, computes
 //   S = K q^T   (16 tokens x 8 columns a matrix instruction, 8 of them over the 128 channels),
-//   P = 2^(S - m) against the running maximum m of each column,
+//   P = 2^(S - m) against a reference m of each column, raised when a score passes it by 2^8,
 //   O^T += V^T P^T (16 channels x 8 columns, 8 of them over the 128 channels)
 // with K and V formed in registers from the codes (one shift, one logical operation and one fused
 // multiply-add a pair of values, exact by the format), and keeps m, the sum l and O^T in registers
@@ -43,9 +44,10 @@ constexpr int kWindow = 2048;         // pages of a CTA's list
 constexpr int kSlots = 6;
 constexpr int kOnce = 16;             // records that one CTA joins at once
 
-// Warps of a CTA: what their registers allow (128 a thread for one column tile, 168 for two, 251
-// for three, 255 for four), and the 16-token tiles that a warp takes together: the more column tiles,
-// the fewer tokens it needs for its matrix instructions not to wait on one another.
+// Warps of a CTA: what their registers allow (128 a thread for one column tile, 168 for two, 251 for three,
+// 255 for four; 44, 84, 0 and 280 bytes a thread are spilled all the same), and the 16-token tiles that a
+// warp takes together: the more column tiles, the fewer tokens it needs for its matrix instructions not to
+// wait on one another.
 template <int NT>
 constexpr int kWarpsOf = NT == 1 ? 16 : NT == 2 ? 12 : 8;
 template <int NT>
@@ -191,12 +193,12 @@ __device__ __forceinline__ void tile_scores(const uint8_t *codes, const uint8_t 
 
 // O^T += V^T P^T over TT tiles. The lane holds words 2 g, 2 g + 1 of tokens 2 tig, 2 tig + 1 of a tile
 // and of the two eight further on: codes[e] and par point at token 2 tig (+ e for the codes) of the
-// first tile. In a page that begins or ends outside of what any query sees (edge), tokens before `from` and
-// from `valid` on (counted from token 2 tig) may hold anything and count as 0. A permutation of bytes puts
-// two tokens' nibbles of one channel into one register's halves.
+// first tile. In a page that some query does not see whole, tokens before `seen` and from n on, which none sees
+// (positions in the sequence, as `at` is token 2 tig's), may hold anything and count as 0. A permutation of
+// bytes puts two tokens' nibbles of one channel into one register's halves.
 template <int NT, int TT>
 __device__ __forceinline__ void tile_values(const uint8_t *const (&codes)[2], const uint8_t *par,
-                                            bool edge, int from, int valid,
+                                            const AttnArgs &a, const Seq &sq, bool open, int at,
                                             const uint32_t (&pf)[NT][TT][2], State<NT> &st) {
 #pragma unroll
     for (int tile = 0; tile < TT; tile++) {
@@ -207,10 +209,10 @@ __device__ __forceinline__ void tile_values(const uint8_t *const (&codes)[2], co
         for (int hi = 0; hi < 2; hi++) {
             uint32_t q0 = *reinterpret_cast<const uint32_t *>(par + tile * 256 + hi * 128);
             uint32_t q1 = *reinterpret_cast<const uint32_t *>(par + tile * 256 + hi * 128 + 16);
-            if (edge) {
-                const int t = 16 * tile + 8 * hi;
-                q0 = t >= from && t < valid ? q0 : 0u;
-                q1 = t + 1 >= from && t + 1 < valid ? q1 : 0u;
+            if (!open) {
+                const int t = at + 16 * tile + 8 * hi, seen = first_seen(a, sq);
+                q0 = t >= seen && t < sq.n ? q0 : 0u;
+                q1 = t + 1 >= seen && t + 1 < sq.n ? q1 : 0u;
             }
             s[hi] = __byte_perm(q0, q1, 0x5410);
             o[hi] = __byte_perm(q0, q1, 0x7632);
@@ -446,7 +448,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                                       vbuf + code_offset(2 * tig + 1, g >> 1) + 8 * (g & 1)};
     const uint8_t *vpar = vbuf + param_offset(2 * tig, g >> 1);
     uint64_t *kfull = &sh.full[warp][0], *vfull = &sh.full[warp][1];
-    uint32_t taken = 0, kissued = 0, vissued = 0;  // pages this warp has finished, copies asked for
+    uint32_t taken = 0;  // pages this warp has finished
     bool dead = false;
     // a range is walked in windows w0 .. w1 - 1 that fit the list; a unit that goes on in the next
     // window leaves its joined state in one of the CTA's two carry records
@@ -509,6 +511,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                 tma_load_1d(to, from + (int64_t)sh.list[i].rec * kRec, kRec, bar);
             }
         };
+        const uint32_t was = taken;
+        uint32_t kissued = taken, vissued = taken;  // copies asked for, all but this window's done
         if (w0 != r0) fence_proxy_async();  // the room held the last window's states
         {
             const int i = next(i0);
@@ -530,7 +534,6 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
             st.clear();
             bool far = false;  // one of the warp's references is
             const int low = s.n - s.nq;  // position of the first query
-            const int seen = first_seen(a, s);
             for (; i < i1; i++) {
                 const Entry e = sh.list[i];
                 if (e.unit != unit) break;
@@ -634,9 +637,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                     }
                     if (tile == 0) wait_copy(a, vfull, taken & 1, dead);
                     const uint8_t *const vc[2] = {vcodes[0] + tile * 1024, vcodes[1] + tile * 1024};
-                    const int at = t0 + 16 * tile + 2 * tig;
-                    tile_values<NT, TT>(vc, vpar + tile * 256, s.n - t0 < kPage || t0 < seen, seen - at,
-                                        s.n - at, pf, st);
+                    tile_values<NT, TT>(vc, vpar + tile * 256, a, s, open, t0 + 16 * tile + 2 * tig, pf, st);
                 }
                 dead = __any_sync(0xffffffffu, dead);
                 if (ni < i1 && !dead) {
@@ -668,8 +669,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
         }
         if (dead) {  // leave no copy in flight
             bool done = true;
-            if (kissued) done = mbar_drain(kfull, (kissued - 1) & 1, a.wait_ns);
-            if (vissued) done &= mbar_drain(vfull, (vissued - 1) & 1, a.wait_ns);
+            if (kissued != was) done = mbar_drain(kfull, (kissued - 1) & 1, a.wait_ns);
+            if (vissued != was) done &= mbar_drain(vfull, (vissued - 1) & 1, a.wait_ns);
             if (!done) raise_error(a.err, FFD_ERRBIT_TIMEOUT);
         }
         __syncthreads();
