@@ -68,9 +68,10 @@ __device__ __forceinline__ uint32_t encode_word(const uint32_t *w, float s, floa
 // least and largest value need no other thread. The eight threads of a row sit together and rows
 // follow one another, so a prompt's records are written in whole lines.
 //
-// What has to move is 256 B of a tensor's row in and 80 B out; what bounds it is issue: about 10.5 thread
-// instructions a value (54 % of DRAM's rate, 2.8 instructions a cycle). So the least and largest are
-// taken of packed pairs, sums and products of coding are packed too, the clamp is a product's saturation,
+// What has to move is 256 B of a tensor's row in and 80 B out: 26 us for 32768 tokens of 8 heads, which take
+// 36. No unit is full (54 % of DRAM's rate, 69 % of the issue slots, at about 10.5 thread instructions a
+// value): a thread loads, waits, codes and ends, with half the warps resident. So the least and largest
+// are taken of packed pairs, sums and products of coding are packed too, the clamp is a product's saturation,
 // and values are unpacked again where they are coded, which keeps to 48 registers and five blocks an
 // SM (40 registers, six blocks: spills, 4 % slower).
 template <class T, bool kWide>

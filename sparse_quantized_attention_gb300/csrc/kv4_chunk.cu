@@ -6,7 +6,8 @@
 // what each item costs besides, are cut into equal contiguous ranges, one per CTA (one per SM), so the
 // last CTA ends with the first whatever the causal edges leave; an item cut by a range's end is joined
 // by the last of its CTAs.
-// Where items are short, whole ones are dealt out instead: a join costs more than the imbalance.
+// Where items are short, whole ones are dealt out instead (a join costs more than the imbalance), if the
+// sequences' lengths are even enough.
 // For each page of 64 tokens a CTA computes, for its two tiles of 128 rows,
 //   S = Q K^T   (M 128, N 64, K 128; f16, both operands in shared memory, S in tensor memory),
 //   P = 2^(S - m) in f16 against a reference m that follows the row's maximum lazily: it is raised,
@@ -16,14 +17,14 @@
 // them; one thread a tile issues its matrix instructions; two groups of four warps, one row a thread,
 // do the softmax of one tile each.
 //
-// What bounds it. A page takes 2090 cycles for two tiles (2048 query tokens over 32768, 32/8 heads:
-// 955 us, 1.11 PFLOP/s, 57 % of the measured matrix rate; 1280 cycles are the matrix instructions' own: 8 x
+// What bounds it. A page takes 2040 cycles for two tiles (2048 query tokens over 32768, 32/8 heads:
+// 932 us, 1.14 PFLOP/s, 59 % of the measured matrix rate; 1280 cycles are the matrix instructions' own: 8 x
 // 48 a tile for S, whose Q is read again from shared memory every time, and 4 x 64 for P V) and 1780
 // for one. Within a step the softmax of a row (2020 cycles with both groups at work, 1680 with one) and
 // the way S -> P -> P V -> next S through barriers cover each other, but little is left between. Q
 // partly in tensor memory (S at 40 cycles an instruction) leaves room for three places of S and
-// ties the tiles to each other: 1287 us. A CTA of 480 threads that reads S once into 128 registers
-// forms K and V^T with four warps, and waits for them: 961 us.
+// ties the tiles to each other: 1287 us, when this form took 955. A CTA of 480 threads that reads S once into
+// 128 registers forms K and V^T with four warps, and waits for them: 961 us then.
 //
 // K's rows, and with them the columns of S, P and V^T, are tokens in the order 8 (p % 8) + p / 8:
 // then the eight tokens that make 16 bytes of a V^T row come from eight different lanes' loads, and
@@ -36,7 +37,8 @@ namespace {
 
 constexpr int kTile = 128;             // rows of a tile
 constexpr int kRows = 2 * kTile;       // rows of an item
-constexpr int kThreads = 608;  // 2 x 4 softmax warps, 4 warps forming K, 4 forming V, 2 issuers, copy
+// 2 x 4 softmax warps, 4 warps forming K, 4 forming V, 2 issuers, copy: 96 registers a thread, 48 bytes spilled
+constexpr int kThreads = 608;
 constexpr int kCtaWarps = kThreads / 32;
 constexpr int kNK = 3, kNV = 3;        // f16 tiles of K and of V^T
 constexpr int kNS = 5;                 // record pairs in flight

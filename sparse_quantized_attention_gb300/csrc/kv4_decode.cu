@@ -23,9 +23,9 @@
 // apart from elements below 2^-27 of the largest.
 //
 // What bounds it. A page of a head is 10 KB for 64 x 8 NT scores. With one column tile a long cache is
-// read at 5.0 TB/s (4 x 131072 tokens, 28/4 heads: 68 us, 73 % of the measured copy rate; forming K and
+// read at 4.9 TB/s (4 x 131072 tokens, 28/4 heads: 68 to 69 us, 72 % of the measured copy rate; forming K and
 // V takes most of the issue slots then, a matrix instruction 8 cycles of a scheduler's), a batch of 32
-// sequences at 5.2 TB/s. A short cache waits instead: about 3.5 us until the first copy is asked
+// sequences at 5.1 TB/s (86 us). A short cache waits instead: about 3.5 us until the first copy is asked
 // for, 2 us for it, 4 to 5 us for the join of the warps, the records and the tickets (4096 tokens:
 // 12 us, 32768: 23 us). With more column tiles eight warps are all that the registers allow, and their
 // instructions wait on one another (0.3 issued a cycle of a scheduler): 24 rows behind a window of 4096
