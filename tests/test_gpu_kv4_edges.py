@@ -113,7 +113,7 @@ def test_tokens_behind_every_window_may_be_anything(nq, window):
 @pytest.mark.parametrize("splits", [0, 3])
 def test_a_wait_that_runs_out(q, splits):
     """The shortest limit, below the time of a copy: the call ends, reports it or is right, and leaves the
-    workspace to the next call. (The time of all 20 calls is bounded: nothing waits for what never comes.)"""
+    workspace to the next call. (The time of a call is bounded: nothing waits for what never comes.)"""
     c = Case([9000, 100, 2500], [q, min(q, 100), q], 2, 4, seed=q)
     p, short = c.params(num_splits=splits), c.params(num_splits=splits, wait_limit_us=1)
     ws = ffd.alloc_kv4_workspace(p)
@@ -122,11 +122,13 @@ def test_a_wait_that_runs_out(q, splits):
     assert ffd.ffd_get_error(ws) == 0
     c.check(*good)
     e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
-    e0.record()
     for _ in range(20):
         out, lse = c.buffers()
+        e0.record()
         c.call(out, lse, ws, short)
+        e1.record()
         status = ffd.ffd_get_error(ws)
+        assert e0.elapsed_time(e1) < 1500.0  # ms; a drain may take 2 s when its copy never lands
         assert status in (0, 7)
         if status == 0:
             assert torch.equal(out, good[0])
@@ -134,9 +136,6 @@ def test_a_wait_that_runs_out(q, splits):
         c.call(out, lse, ws, p)
         assert ffd.ffd_get_error(ws) == 0
         assert torch.equal(out, good[0]) and torch.equal(lse, good[1])
-    e1.record()
-    torch.cuda.synchronize()
-    assert e0.elapsed_time(e1) < 1500.0  # ms; a drain alone may take 2 s when its copy never lands
 
 
 @pytest.mark.parametrize("lens,q", [([32768] + [1024] * 18, 9), ([700] * 37 + [16384], 64),
