@@ -207,6 +207,7 @@ DecodeArgs make_args(const ffd_decode_params *p, const Plan &pl, void *ws) {
     a.delta = p->delta;
     a.sm_scale = p->sm_scale;
     a.wait_ns = wait_bound_ns(p);
+    a.drain_ns = drain_bound_ns(a.wait_ns);
     char *base = static_cast<char *>(ws);
     a.err = reinterpret_cast<int *>(base);
     a.ws_m1 = reinterpret_cast<float *>(base + pl.m1_off);
@@ -411,6 +412,7 @@ ffd_status ffd_select_blocks(const ffd_decode_params *params, int32_t selector, 
     a.L = params->local_tokens;
     a.sm_scale = params->sm_scale;
     a.wait_ns = wait_bound_ns(params);
+    a.drain_ns = drain_bound_ns(a.wait_ns);
     a.q = static_cast<const __nv_bfloat16 *>(q_bf16);
     a.thumb = thumb;
     a.seq_lens = seq_lens;
@@ -484,6 +486,7 @@ ffd_status ffd_art_attention(const ffd_decode_params *params, float tau, float p
     a.max_blocks = params->max_blocks_per_seq;
     a.sm_scale = params->sm_scale;
     a.wait_ns = wait_bound_ns(params);
+    a.drain_ns = drain_bound_ns(a.wait_ns);
     a.q = static_cast<const __nv_bfloat16 *>(q_bf16);
     a.thumb = thumb;
     a.resid = resid;

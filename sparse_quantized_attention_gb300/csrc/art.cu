@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kArtThreads) art_kernel(const __grid_constant_
         // leave no copy in flight: the group's stages still being filled
         for (int s = 0; s < 2; s++) {
             if (!((issued >> s) & 1)) continue;
-            if (!mbar_drain(&ctl.full[g * 2 + s], (fph >> s) & 1u, a.wait_ns) && mt == 0 && lane == 0)
+            if (!mbar_drain(&ctl.full[g * 2 + s], (fph >> s) & 1u, a.drain_ns) && mt == 0 && lane == 0)
                 raise_error(a.err, FFD_ERRBIT_TIMEOUT);
         }
         return;

@@ -60,6 +60,7 @@ struct DecodeArgs {
                      // declarations; zero between calls
     cudaEvent_t prof_start, prof_stop;  // optional: recorded around the main kernel
     uint64_t wait_ns;  // bound of every device wait (mbarrier, counter) before FFD_ERRBIT_TIMEOUT
+    uint64_t drain_ns; // bound of a wait for the CTA's own copies in flight
 };
 
 // Sink / local block bookkeeping of one sequence (Methodology §2: the pseudo-max uses the sink

@@ -863,11 +863,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const AttnArgs a
         if (warp == 18 && lane == 0)
             for (uint32_t i = 0; i < kNS && i < steps; i++) {
                 const uint32_t last = steps - 1 - i;
-                done &= mbar_drain(&sh.rec_full[last % kNS], (last / kNS) & 1, a.wait_ns);
+                done &= mbar_drain(&sh.rec_full[last % kNS], (last / kNS) & 1, drain_bound_ns(a.wait_ns));
             }
         if ((warp == 16 || warp == 17) && elect_one()) {
             tc_commit(&sh.drain[warp - 16]);
-            done = mbar_drain(&sh.drain[warp - 16], 0, a.wait_ns);
+            done = mbar_drain(&sh.drain[warp - 16], 0, drain_bound_ns(a.wait_ns));
         }
         if (!done) raise_error(a.err, FFD_ERRBIT_TIMEOUT);
     }

@@ -669,8 +669,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
         }
         if (dead) {  // leave no copy in flight
             bool done = true;
-            if (kissued != was) done = mbar_drain(kfull, (kissued - 1) & 1, a.wait_ns);
-            if (vissued != was) done &= mbar_drain(vfull, (vissued - 1) & 1, a.wait_ns);
+            if (kissued != was) done = mbar_drain(kfull, (kissued - 1) & 1, drain_bound_ns(a.wait_ns));
+            if (vissued != was) done &= mbar_drain(vfull, (vissued - 1) & 1, drain_bound_ns(a.wait_ns));
             if (!done) raise_error(a.err, FFD_ERRBIT_TIMEOUT);
         }
         __syncthreads();

@@ -86,15 +86,17 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 // another one per call).
 constexpr uint64_t kWaitTimeoutNs = 2000000000ull;
 
-// Wait for what this CTA has in flight into its own shared or tensor memory, before it leaves or reuses
-// that: bounded by the default or the caller's limit, whichever is longer, since a limit below a copy's
-// time (about 2 us) is one that the caller may set. False when the bound ran out.
-__device__ __forceinline__ bool mbar_drain(uint64_t *bar, uint32_t parity, uint64_t wait_ns) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t bound = wait_ns > kWaitTimeoutNs ? wait_ns : kWaitTimeoutNs;
+// Bound of a wait for what a CTA has in flight into its own shared or tensor memory, before it leaves or
+// reuses that: the default or the caller's limit, whichever is longer, since a limit below a copy's time
+// (about 2 us) is one that the caller may set.
+__host__ __device__ inline uint64_t drain_bound_ns(uint64_t wait_ns) {
+    return wait_ns > kWaitTimeoutNs ? wait_ns : kWaitTimeoutNs;
+}
+// That wait: false when the bound ran out.
+__device__ __forceinline__ bool mbar_drain(uint64_t *bar, uint32_t parity, uint64_t bound_ns) {
     const uint64_t t0 = globaltimer_ns();
     while (!mbar_try_wait(bar, parity))
-        if (globaltimer_ns() - t0 > bound) return false;
+        if (globaltimer_ns() - t0 > bound_ns) return false;
     return true;
 }
 

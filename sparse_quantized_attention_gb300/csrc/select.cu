@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(128) block_stats_kernel(DecodeArgs a, float *i
     }
     // copies still in flight into this warp's stages are waited for (bounded) before it exits
     for (int k = 0; k < 2; k++)
-        if (((have >> k) & 1u) && !mbar_drain(&full[warp][k], (phases >> k) & 1u, a.wait_ns) &&
+        if (((have >> k) & 1u) && !mbar_drain(&full[warp][k], (phases >> k) & 1u, a.drain_ns) &&
             lane == 0)
             raise_error(a.err, FFD_ERRBIT_TIMEOUT);
 }

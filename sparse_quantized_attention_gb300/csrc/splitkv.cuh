@@ -134,7 +134,7 @@ __device__ __forceinline__ void wait_bar(const DecodeArgs &a, M *m, uint64_t *ba
 // Wait for a copy this CTA issued, ignoring the abort flag (bounded, but not by a caller's limit that
 // is shorter than a copy takes): no CTA exits with a copy into its shared memory in flight.
 __device__ __forceinline__ void drain_bar(const DecodeArgs &a, uint64_t *bar, uint32_t parity) {
-    if (!mbar_drain(bar, parity, a.wait_ns)) raise_error(a.err, FFD_ERRBIT_TIMEOUT);
+    if (!mbar_drain(bar, parity, a.drain_ns)) raise_error(a.err, FFD_ERRBIT_TIMEOUT);
 }
 
 template <class M>
