@@ -551,6 +551,184 @@ ffd_status ffd_kv4_attention(const ffd_kv4_params *params, const void *q, const 
                              const int32_t *block_table, const uint8_t *keep_in, void *out,
                              float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Speculative decoding over the 16-bit cache (the K and V pages of ffd_dense_decode, and the records
+ * that ffd_decode_attention reads beside them): the drafted tokens' keys and values are rotated and
+ * appended, their queries attend to the cache and to each other as a tree, and the path that the model
+ * confirms is moved to where the sequence goes on. The pages describe one decode step of a drop-in
+ * attention kernel (Significance 2); these are the calls around it. K and V pages are bf16 or fp16
+ * [P][Hkv][64][128]; the records go with bf16 alone.
+ * --------------------------------------------------------------------------------------------- */
+
+/* Shape of an append. */
+typedef struct {
+    int32_t batch;              /* B >= 1 sequences */
+    int32_t num_q_heads;        /* Hq >= 1 heads of q and q_out (any number; 0 where q is NULL) */
+    int32_t num_kv_heads;       /* Hkv >= 1 */
+    int32_t head_dim;           /* must be 128 */
+    int32_t page_size;          /* must be 64 */
+    int32_t num_pages;          /* P >= 1, bound for block_table entries */
+    int32_t max_blocks_per_seq; /* row stride of block_table; 64 times it <= INT32_MAX */
+    int32_t dtype;              /* FFD_DTYPE_BF16 or FFD_DTYPE_F16, of every 16-bit tensor */
+    int32_t total_tokens;       /* T >= 0 rows */
+    int32_t rot_dim;            /* channels 0 .. rot_dim - 1 are rotated: a multiple of 16, 0 .. 128 */
+    int32_t interleaved;        /* 0: channels (i, i + rot_dim / 2) are a pair, 1: (2i, 2i + 1) */
+    float rot_scale;            /* finite factor on the rotated channels, normally 1 */
+    int64_t q_stride, q_out_stride, k_stride, v_stride; /* elements between rows: >= heads * 128, a
+                                                           multiple of 8 */
+} ffd_rope_params;
+
+/*
+ * ffd_rope_append -- rotate the new tokens' queries and keys by their positions and append keys and
+ * values to the paged cache: a decode step's one token per sequence, drafted tokens, or whole prompts,
+ * in one launch. Pair i < rot_dim / 2 of a row at position p turns by the angle p * inv_freq[i]:
+ *   (x, y) -> rot_scale (x cos - y sin, x sin + y cos),
+ * the angle being the product of the integer and the fp32 number without a rounding, taken to within
+ * 1e-6 turns' accuracy or better at any position (2e-7 below 2^20); the turn is computed in fp32 and
+ * rounded to dtype once. Channels from rot_dim on pass as they are. Quantised keys are those that
+ * ffd_quantize_keys writes for the rotated, rounded key.
+ *   q, q_out     device [T][Hq][128], or both NULL; q_out may be q itself (same stride), and may not
+ *                overlap it, k_new or v_new otherwise
+ *   k_new, v_new device [T][Hkv][128]
+ *   inv_freq     device fp32 [rot_dim / 2] (any scaling is in it); NULL where rot_dim is 0
+ *   rope_positions  device int32 [T], 0 <= p < 2^24: the position that a row is rotated by (of a
+ *                drafted token: the tokens before the tree + its depth). NULL: its token index.
+ *   cu_tokens    device int32 [B+1], non-decreasing: sequence b has rows cu[b] .. cu[b+1]-1. Rows that
+ *                belong to nobody are neither rotated nor appended. NULL: T is a multiple of B and
+ *                every sequence has T / B rows.
+ *   positions    device int32 [B]: token index of the sequence's first row; a negative entry
+ *                rotates and appends nothing for that sequence
+ *   block_table  device int32 [B][max_blocks_per_seq]
+ *   k, v         device [P][Hkv][64][128], the tokens' rows are rewritten; k may be NULL where the
+ *                records are given
+ *   thumb, resid device records as for ffd_append_kv, or both NULL (dtype must be FFD_DTYPE_BF16)
+ *   error_word   device int32, or NULL: FFD_ERRBIT_BOUNDS for a token index >= 64 *
+ *                max_blocks_per_seq or a page outside [0, P) (the token is not appended, its query is
+ *                rotated all the same); FFD_ERRBIT_RANGE for a rotary position outside [0, 2^24) (its
+ *                rotated channels are unspecified) or, with records, a key outside the fp16 range
+ * Tensors are 16-byte aligned. Two rows that name the same (page, token) race.
+ * Returns FFD_OK, FFD_ERR_INVALID_ARG, FFD_ERR_UNSUPPORTED or FFD_ERR_CUDA.
+ */
+ffd_status ffd_rope_append(const ffd_rope_params *params, const void *q, const void *k_new,
+                           const void *v_new, const float *inv_freq, const int32_t *rope_positions,
+                           const int32_t *cu_tokens, const int32_t *positions,
+                           const int32_t *block_table, void *q_out, void *k, void *v, uint8_t *thumb,
+                           uint8_t *resid, int32_t *error_word, void *stream);
+
+/* Most nodes of a tree. */
+#define FFD_TREE_MAX_NODES 256
+
+/* One attention call over the 16-bit cache. */
+typedef struct {
+    int32_t batch;              /* B >= 1 sequences; B * Hkv <= 65535 */
+    int32_t num_q_heads;        /* Hq, a multiple of num_kv_heads */
+    int32_t num_kv_heads;       /* Hkv; G = Hq / Hkv in 1..8 */
+    int32_t head_dim;           /* must be 128 */
+    int32_t page_size;          /* must be 64 */
+    int32_t num_pages;          /* P, bound for block_table entries; 64 * P * Hkv <= INT32_MAX */
+    int32_t max_blocks_per_seq; /* row stride of block_table; seq_lens[b] <= 64 * this, which
+                                   is <= INT32_MAX as well as
+                                   B * Hkv * (this + 9) * ceil(max_q_len * G / 128) */
+    int32_t dtype;              /* FFD_DTYPE_BF16 or FFD_DTYPE_F16, of q, k, v and out */
+    int32_t max_q_len;          /* >= 1, the most nodes of one sequence; this * G <= 2^28 */
+    int32_t total_q;            /* >= 1, rows of q, out, lse and parents */
+    int32_t window;             /* 0: every earlier token is visible; w > 0: those at the last w
+                                   positions are (the node's own included) */
+    int32_t num_splits;         /* 0: library's choice; else the number of KV partitions (at most one
+                                   CTA per SM) */
+    int64_t q_stride;           /* elements between the rows of q: >= Hq * 128, a multiple of 8; 0
+                                   means Hq * 128 */
+    float sm_scale;             /* score scale, finite and > 0; normally 1/sqrt(head_dim) */
+    int32_t wait_limit_us;      /* as in ffd_decode_params */
+} ffd_tree_params;
+
+/* Bytes of device workspace that ffd_tree_attention needs for these parameters on the current
+ * device (0 for parameters that it would reject). */
+size_t ffd_tree_workspace_size(const ffd_tree_params *params);
+
+/*
+ * ffd_tree_attention -- softmax attention of each sequence's newest tokens, the nodes of a tree of
+ * drafted tokens, over its 16-bit cache. Sequence b has n = seq_lens[b] cached tokens, of which the last
+ * nq are the nodes in order (their K and V written first, as by ffd_rope_append). Node i hangs on node
+ * parents[i] < i, or (-1) on the token before the tree; its depth is the number of its ancestors, its
+ * position n - nq + depth, and it sees itself, its ancestors and the tokens j < n - nq before the
+ * tree; of these, with window > 0, those whose position is greater than its own less window, and,
+ * where keep_in is given, those whose block's entry is nonzero:
+ *   s_j = sm_scale q . K_j,  lse = log sum_j e^(s_j),  out = sum_j e^(s_j - lse) V_j.
+ * Without parents the nodes are a chain (node i hangs on i - 1): causal attention of drafts in a row or
+ * of a chunk of a prompt. A row that sees no token gets out = 0 and lse = -inf. Scores and sums are
+ * fp32; a probability enters the product with V as one number of dtype (off by up to 2^-8 of itself in
+ * bf16, 2^-11 in fp16), so that relative L2 errors of out against 64 bits over normal data are 2.0e-3
+ * (its own rounding: 1.65e-3) and 2.9e-4 (2.1e-4). A query with an infinity or a NaN in it
+ * leaves its own (row, head) unspecified and no other; so does one whose scores times log2(e) pass
+ * fp32's range. A key with one makes the rows that see it unspecified and no other, and so does a value,
+ * which makes what they hold infinite or NaN.
+ *   q           device [total_q][Hq][128] of dtype, rows params->q_stride elements apart, 16-byte
+ *               aligned
+ *   k, v        device [P][Hkv][64][128] of dtype, 16-byte aligned. Tokens that no node of the sequence
+ *               sees are never used: their bytes may be anything.
+ *   seq_lens    device int32 [B], nq <= seq_lens[b] <= 64 * max_blocks_per_seq
+ *   cu_q        device int32 [B+1]: sequence b's nodes are rows cu_q[b] .. cu_q[b+1]-1, at
+ *               most max_q_len of them (none is fine). NULL: every sequence has max_q_len, and
+ *               total_q = B * max_q_len. Rows that belong to nobody are left as they were.
+ *   parents     device int32 [total_q] or NULL; with it max_q_len <= FFD_TREE_MAX_NODES (else
+ *               FFD_ERR_UNSUPPORTED)
+ *   block_table device int32 [B][max_blocks_per_seq]; entries of blocks that no node of the
+ *               sequence sees (past n, behind the window, dropped by keep_in) are not read
+ *   keep_in     device u8 [B][Hkv][max_blocks_per_seq] or NULL: nonzero = the block may be seen
+ *               (for instance ffd_select_blocks's mask, or a decode step's keep_mask)
+ *   out         device [total_q][Hq][128] of dtype, 16-byte aligned; it must not overlap q
+ *   lse         device fp32 [total_q][Hq] or NULL
+ *   workspace   device, >= ffd_tree_workspace_size(params) bytes, 256-byte aligned; its first 4
+ *               bytes are the device error word. Zero-fill it once before first use; each call
+ *               leaves it ready for the next one. Calls that share a workspace must be ordered.
+ * Errors: host-side statuses; FFD_ERRBIT_BOUNDS for a block-table entry outside [0, P) (the block
+ * is treated as dropped), a sequence length above the table's (clamped) or below nq (its rows see
+ * nothing), a cu_q entry out of range (that sequence's rows are left as they were) or a parent that
+ * is neither -1 nor an earlier node (taken as -1); FFD_ERRBIT_TIMEOUT for a wait that ran out
+ * (the call's results are invalid, the workspace is ready for the next one).
+ */
+ffd_status ffd_tree_attention(const ffd_tree_params *params, const void *q, const void *k,
+                              const void *v, const int32_t *seq_lens, const int32_t *cu_q,
+                              const int32_t *parents, const int32_t *block_table,
+                              const uint8_t *keep_in, void *out, float *lse, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/*
+ * ffd_tree_commit -- find the drafted path that the model confirms and make it the sequence's end.
+ * The first node of a sequence is accepted; any other is when its parent is and its token is the model's
+ * token behind its parent (draft[i] == target[parent]). The deepest accepted node, of several the one
+ * of the lowest index, ends the path. The path's rows of the cache, at tokens n - nq + node, are moved to
+ * tokens n - nq, n - nq + 1, ...; rows behind the path keep what they hold. (A sampled verification sets
+ * target to the tokens that it accepts.)
+ *   cache         shape of the cache (head_dim 128, page_size 64)
+ *   batch, max_blocks_per_seq, block_table   as for ffd_rope_append
+ *   total_nodes   T >= 0 rows of draft, target, parents and path
+ *   draft, target device int64 [T]: the nodes' tokens, and the model's token behind each
+ *   parents       device int32 [T] as for ffd_tree_attention, or NULL (chains)
+ *   cu_nodes      device int32 [B+1] as cu_q, or NULL (T / B nodes each); at most FFD_TREE_MAX_NODES
+ *                 nodes of a sequence
+ *   seq_lens      device int32 [B]: cached tokens, the nodes among them
+ *   k, v          device [P][Hkv][64][128] of 16-bit elements, or NULL for one that is not kept
+ *   thumb, resid  device records, or both NULL
+ *   path          device int32 [T]: the path's nodes in order at the sequence's first rows, -1 in the
+ *                 others; rows that belong to nobody are left as they were
+ *   accepted      device int32 [B]: the path's length (0 for a sequence without nodes)
+ *   next_token    device int64 [B]: the model's token behind the path (-1 for no nodes)
+ *   new_lens      device int32 [B]: n - nq + accepted; it must not overlap seq_lens
+ *   error_word    device int32, or NULL: FFD_ERRBIT_BOUNDS for a length, an offset or a number of nodes
+ *                 out of range (nothing is moved: accepted 0, next_token -1, new_lens the length
+ *                 as given, path -1 where the offsets allow it), a parent as in ffd_tree_attention, or a
+ *                 page outside [0, P) (a row from or to it is not moved)
+ * One launch; no workspace. Returns FFD_OK, FFD_ERR_INVALID_ARG, FFD_ERR_UNSUPPORTED or FFD_ERR_CUDA.
+ */
+ffd_status ffd_tree_commit(const ffd_cache_desc *cache, int32_t batch, int32_t max_blocks_per_seq,
+                           int32_t total_nodes, const int64_t *draft, const int64_t *target,
+                           const int32_t *parents, const int32_t *cu_nodes, const int32_t *seq_lens,
+                           const int32_t *block_table, void *k, void *v, uint8_t *thumb,
+                           uint8_t *resid, int32_t *path, int32_t *accepted, int64_t *next_token,
+                           int32_t *new_lens, int32_t *error_word, void *stream);
+
 /*
  * ffd_set_profile_events -- optional instrumentation. While both events are non-NULL, every
  * ffd_decode_attention / ffd_dense_decode call records `start` on its stream right before its

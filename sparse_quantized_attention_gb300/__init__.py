@@ -14,7 +14,9 @@ from .ffd import (CacheDesc, DecodeParams, FFDError, QuantizedCache, alloc_quant
                   ffd_suggest_schedule, ffd_last_cuda_error, SCHEDULE_FUSED,
                   SCHEDULE_SCAN_REFINE, Kv4Cache, Kv4Params, alloc_kv4_cache, alloc_kv4_workspace,
                   ffd_kv4_attention, ffd_kv4_read, ffd_kv4_workspace_size, ffd_kv4_write,
-                  make_kv4_params)
+                  make_kv4_params, RopeParams, TreeParams, TREE_MAX_NODES, alloc_tree_workspace,
+                  ffd_rope_append, ffd_tree_attention, ffd_tree_commit, ffd_tree_workspace_size,
+                  make_tree_params)
 
 __all__ = ["CacheDesc", "DecodeParams", "FFDError", "QuantizedCache", "alloc_quantized_cache",
            "alloc_workspace", "ffd_append_kv", "ffd_decode_attention", "ffd_decode_attention_static",
@@ -27,4 +29,6 @@ __all__ = ["CacheDesc", "DecodeParams", "FFDError", "QuantizedCache", "alloc_qua
            "ffd_art_attention", "ffd_suggest_schedule", "ffd_last_cuda_error", "SCHEDULE_FUSED",
            "SCHEDULE_SCAN_REFINE", "Kv4Cache", "Kv4Params", "alloc_kv4_cache",
            "alloc_kv4_workspace", "ffd_kv4_attention", "ffd_kv4_read", "ffd_kv4_workspace_size",
-           "ffd_kv4_write", "make_kv4_params"]
+           "ffd_kv4_write", "make_kv4_params", "RopeParams", "TreeParams", "TREE_MAX_NODES",
+           "alloc_tree_workspace", "ffd_rope_append", "ffd_tree_attention", "ffd_tree_commit",
+           "ffd_tree_workspace_size", "make_tree_params"]

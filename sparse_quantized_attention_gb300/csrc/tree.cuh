@@ -1,0 +1,81 @@
+// tree.cuh -- speculative decoding over the 16-bit cache: argument bundles and what its kernels share.
+#pragma once
+
+#include "common.cuh"
+
+namespace ffd {
+namespace tree {
+
+constexpr int kMaxNodes = FFD_TREE_MAX_NODES;
+constexpr int kMaxPlace = 1 << 24;  // rotary positions are below
+
+// Arguments of an append.
+struct RopeArgs {
+    int B, Hq, Hkv, P, max_blocks, T, each, rot, interleaved;
+    int parts, per;  // warps of a token, rows of each
+    float scale;
+    int64_t q_stride, q_out_stride, k_stride, v_stride;  // elements
+    const uint16_t *q, *k_new, *v_new;
+    const float *inv_freq;
+    const int32_t *places, *cu, *positions, *block_table;
+    uint16_t *q_out, *k, *v;
+    uint8_t *thumb, *resid;
+    int *err;
+};
+
+// Arguments of a commit.
+struct CommitArgs {
+    int B, Hkv, P, max_blocks, T, each;
+    const int64_t *draft, *target;
+    const int32_t *parents, *cu, *seq_lens, *block_table;
+    uint8_t *k, *v, *thumb, *resid;
+    int32_t *path, *accepted, *new_lens;
+    int64_t *next_token;
+    int *err;
+};
+
+// Arguments of an attention call.
+struct AttnArgs {
+    int B, Hq, Hkv, G, P, max_blocks, max_q, total_q, window;
+    int64_t q_stride;
+    float sm_scale;
+    const uint16_t *q, *k, *v;
+    const uint8_t *keep_in;
+    const int32_t *seq_lens, *cu_q, *block_table, *parents;
+    uint16_t *out;
+    float *lse;
+    int *err;  // the workspace: error word first
+    uint64_t wait_ns;
+};
+
+// Launch shape and workspace of an attention call.
+struct Plan {
+    int ctas;
+    size_t total;
+};
+
+// Sequence of row t and the row's place in it, by a whole warp: the offsets cu [B+1] are searched 32
+// at a time (or rows are `each` a sequence when cu is null). False when the row belongs to nobody.
+__device__ __forceinline__ bool row_of_warp(const int32_t *cu, int B, int each, int t, int lane, int &b,
+                                            int &i) {
+    if (!cu) {
+        b = t / each;
+        i = t - b * each;
+        return true;
+    }
+    int lo = 0, hi = B;  // the largest b in [lo, hi) with cu[b] <= t
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) >> 5;
+        const int at = lo + lane * step;
+        const uint32_t below = __ballot_sync(0xffffffffu, lane == 0 || (at < hi && __ldg(cu + at) <= t));
+        lo += (31 - __clz((int)below)) * step;
+        hi = lo + step < hi ? lo + step : hi;
+    }
+    b = lo;
+    const int c = __ldg(cu + lo);
+    i = t - c;
+    return c >= 0 && c <= t && t < __ldg(cu + lo + 1);
+}
+
+}  // namespace tree
+}  // namespace ffd

@@ -1,0 +1,257 @@
+// tree_api.cu -- C entries of speculative decoding over the 16-bit cache (declared in include/ffd.h):
+// argument checks, workspace planning and launches.
+#include <math.h>
+
+#include "ptx.cuh"
+#include "tree.cuh"
+
+namespace ffd {
+namespace tree {
+cudaError_t launch_rope_append(RopeArgs a, int dtype, cudaStream_t stream);
+cudaError_t launch_tree_commit(const CommitArgs &a, cudaStream_t stream);
+cudaError_t launch_tree_attention(const AttnArgs &a, const Plan &pl, int dtype, cudaStream_t stream);
+}  // namespace tree
+}  // namespace ffd
+
+using namespace ffd;
+using namespace ffd::tree;
+
+namespace {
+
+constexpr size_t kAlign = 256;
+constexpr int64_t kMaxRows = 1 << 28;  // nodes of a sequence x G
+constexpr int64_t kMaxUnits = 65535;   // (sequence, KV head) pairs of an attention call
+constexpr int kTileRows = 128;         // smallest group of rows that walks the cache together
+constexpr int kItemPages = 9;          // pages' time that a group of rows may count for besides its pages
+
+bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+// Whether n bytes at p and m bytes at q share any.
+bool overlap(const void *p, int64_t n, const void *q, int64_t m) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q);
+    return x < y + (uintptr_t)m && y < x + (uintptr_t)n;
+}
+
+// Bytes from the first to the last of T rows of 16-bit elements.
+int64_t span(int64_t T, int64_t stride, int64_t heads) { return T > 0 ? 2 * ((T - 1) * stride + heads * kD) : 0; }
+
+bool known(int32_t dtype) { return dtype == FFD_DTYPE_BF16 || dtype == FFD_DTYPE_F16; }
+
+bool row_stride(int64_t stride, int64_t heads) { return stride >= heads * kD && stride % 8 == 0; }
+
+ffd_status check_params(const ffd_tree_params *p) {
+    if (!p) return FFD_ERR_INVALID_ARG;
+    if (p->batch < 1 || p->num_q_heads < 1 || p->num_kv_heads < 1 || p->num_pages < 1 ||
+        p->max_blocks_per_seq < 1 || p->max_q_len < 1 || p->total_q < 1 || p->window < 0 ||
+        p->num_splits < 0 || p->wait_limit_us < 0)
+        return FFD_ERR_INVALID_ARG;
+    if (!known(p->dtype)) return FFD_ERR_INVALID_ARG;
+    if (p->num_q_heads % p->num_kv_heads != 0) return FFD_ERR_INVALID_ARG;
+    if (!isfinite(p->sm_scale) || !(p->sm_scale > 0.0f)) return FFD_ERR_INVALID_ARG;
+    if (p->q_stride != 0 && !row_stride(p->q_stride, p->num_q_heads)) return FFD_ERR_INVALID_ARG;
+    if (p->head_dim != kD || p->page_size != kPage) return FFD_ERR_UNSUPPORTED;
+    if (p->num_q_heads / p->num_kv_heads > kMaxG) return FFD_ERR_UNSUPPORTED;
+    if ((int64_t)p->batch * p->num_kv_heads > kMaxUnits) return FFD_ERR_UNSUPPORTED;
+    if ((int64_t)p->max_blocks_per_seq * kPage > INT32_MAX) return FFD_ERR_UNSUPPORTED;
+    // the cache's rows, and the pages that groups of rows walk, are counted by int32
+    if ((int64_t)p->num_pages * p->num_kv_heads > INT32_MAX / kPage) return FFD_ERR_UNSUPPORTED;
+    const int64_t pages = (int64_t)p->batch * p->num_kv_heads * ((int64_t)p->max_blocks_per_seq + kItemPages);
+    const int64_t rows = (int64_t)p->max_q_len * (p->num_q_heads / p->num_kv_heads);
+    if (rows > kMaxRows || pages > INT32_MAX ||
+        pages > INT32_MAX / ((rows + kTileRows - 1) / kTileRows))
+        return FFD_ERR_UNSUPPORTED;
+    return FFD_OK;
+}
+
+ffd_status make_plan(const ffd_tree_params *p, Plan *pl) {
+    const ffd_status st = check_params(p);
+    if (st != FFD_OK) return st;
+    pl->ctas = 0;
+    pl->total = kAlign;
+    return FFD_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ffd_status ffd_rope_append(const ffd_rope_params *params, const void *q, const void *k_new,
+                           const void *v_new, const float *inv_freq, const int32_t *rope_positions,
+                           const int32_t *cu_tokens, const int32_t *positions,
+                           const int32_t *block_table, void *q_out, void *k, void *v, uint8_t *thumb,
+                           uint8_t *resid, int32_t *error_word, void *stream) {
+    if (!params || !positions || !block_table) return FFD_ERR_INVALID_ARG;
+    const ffd_rope_params &p = *params;
+    if (p.batch < 1 || p.num_q_heads < 0 || p.num_kv_heads < 1 || p.num_pages < 1 ||
+        p.max_blocks_per_seq < 1 || p.total_tokens < 0 || !known(p.dtype))
+        return FFD_ERR_INVALID_ARG;
+    if (p.rot_dim < 0 || p.rot_dim > kD || p.rot_dim % 16 != 0 || (p.interleaved & ~1) ||
+        !isfinite(p.rot_scale) || (p.rot_dim > 0 && !inv_freq))
+        return FFD_ERR_INVALID_ARG;
+    const int64_t T = p.total_tokens;
+    if (!cu_tokens && T % p.batch != 0) return FFD_ERR_INVALID_ARG;
+    if ((q == nullptr) != (q_out == nullptr) && T > 0) return FFD_ERR_INVALID_ARG;
+    if (!v || (!k && !thumb) || (thumb == nullptr) != (resid == nullptr)) return FFD_ERR_INVALID_ARG;
+    if (T > 0 && (!k_new || !v_new)) return FFD_ERR_INVALID_ARG;
+    const bool queries = q && p.num_q_heads > 0;
+    if (q && p.num_q_heads == 0) return FFD_ERR_INVALID_ARG;
+    if (!row_stride(p.k_stride, p.num_kv_heads) || !row_stride(p.v_stride, p.num_kv_heads) ||
+        (queries && (!row_stride(p.q_stride, p.num_q_heads) || !row_stride(p.q_out_stride, p.num_q_heads))))
+        return FFD_ERR_INVALID_ARG;
+    for (const void *x : {q, k_new, v_new, (const void *)q_out, (const void *)k, (const void *)v,
+                          (const void *)thumb, (const void *)resid})
+        if (!aligned(x, 16)) return FFD_ERR_INVALID_ARG;
+    for (const void *x : {(const void *)inv_freq, (const void *)rope_positions, (const void *)cu_tokens,
+                          (const void *)positions, (const void *)block_table, (const void *)error_word})
+        if (!aligned(x, 4)) return FFD_ERR_INVALID_ARG;
+    if (p.head_dim != kD || p.page_size != kPage) return FFD_ERR_UNSUPPORTED;
+    if ((int64_t)p.max_blocks_per_seq * kPage > INT32_MAX) return FFD_ERR_UNSUPPORTED;
+    if (thumb && p.dtype != FFD_DTYPE_BF16) return FFD_ERR_UNSUPPORTED;
+    const int64_t heads = (int64_t)p.num_q_heads + 2 * (int64_t)p.num_kv_heads;
+    if (heads > 65536 || T * ((heads + 7) / 8) > (int64_t)INT32_MAX * 4) return FFD_ERR_UNSUPPORTED;
+    if (queries) {
+        const int64_t out = span(T, p.q_out_stride, p.num_q_heads);
+        const bool same = q == q_out && (p.q_stride == p.q_out_stride || T <= 1);
+        if (!same && overlap(q_out, out, q, span(T, p.q_stride, p.num_q_heads))) {
+            // rows of q and q_out may lie between each other's only where they are the same ones
+            return FFD_ERR_INVALID_ARG;
+        }
+    }
+    RopeArgs a{};
+    a.B = p.batch;
+    a.Hq = queries ? p.num_q_heads : 0;
+    a.Hkv = p.num_kv_heads;
+    a.P = p.num_pages;
+    a.max_blocks = p.max_blocks_per_seq;
+    a.T = p.total_tokens;
+    a.each = cu_tokens ? 0 : p.total_tokens / p.batch;
+    a.rot = p.rot_dim;
+    a.interleaved = p.interleaved;
+    a.scale = p.rot_scale;
+    a.q_stride = p.q_stride;
+    a.q_out_stride = p.q_out_stride;
+    a.k_stride = p.k_stride;
+    a.v_stride = p.v_stride;
+    a.q = static_cast<const uint16_t *>(q);
+    a.k_new = static_cast<const uint16_t *>(k_new);
+    a.v_new = static_cast<const uint16_t *>(v_new);
+    a.inv_freq = inv_freq;
+    a.places = rope_positions;
+    a.cu = cu_tokens;
+    a.positions = positions;
+    a.block_table = block_table;
+    a.q_out = static_cast<uint16_t *>(q_out);
+    a.k = static_cast<uint16_t *>(k);
+    a.v = static_cast<uint16_t *>(v);
+    a.thumb = thumb;
+    a.resid = resid;
+    a.err = error_word;
+    return cuda_status(launch_rope_append(a, p.dtype, static_cast<cudaStream_t>(stream)));
+}
+
+size_t ffd_tree_workspace_size(const ffd_tree_params *params) {
+    Plan pl;
+    return make_plan(params, &pl) == FFD_OK ? pl.total : 0;
+}
+
+ffd_status ffd_tree_attention(const ffd_tree_params *params, const void *q, const void *k,
+                              const void *v, const int32_t *seq_lens, const int32_t *cu_q,
+                              const int32_t *parents, const int32_t *block_table,
+                              const uint8_t *keep_in, void *out, float *lse, void *workspace,
+                              size_t workspace_bytes, void *stream) {
+    if (!q || !k || !v || !seq_lens || !block_table || !out || !workspace) return FFD_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
+        !aligned(seq_lens, 4) || !aligned(cu_q, 4) || !aligned(parents, 4) || !aligned(block_table, 4) ||
+        !aligned(lse, 4) || !aligned(workspace, kAlign))
+        return FFD_ERR_INVALID_ARG;
+    Plan pl;
+    const ffd_status st = make_plan(params, &pl);
+    if (st != FFD_OK) return st;
+    const ffd_tree_params &p = *params;
+    if (parents && p.max_q_len > kMaxNodes) return FFD_ERR_UNSUPPORTED;
+    if (!cu_q && p.total_q != (int64_t)p.batch * p.max_q_len) return FFD_ERR_INVALID_ARG;
+    if (workspace_bytes < pl.total) return FFD_ERR_WORKSPACE;
+    const int64_t row = (int64_t)p.num_q_heads * kD, stride = p.q_stride ? p.q_stride : row;
+    if (overlap(q, span(p.total_q, stride, p.num_q_heads), out, span(p.total_q, row, p.num_q_heads)))
+        return FFD_ERR_INVALID_ARG;  // q is read by several CTAs, at their own times
+    AttnArgs a{};
+    a.B = p.batch;
+    a.Hq = p.num_q_heads;
+    a.Hkv = p.num_kv_heads;
+    a.G = p.num_q_heads / p.num_kv_heads;
+    a.P = p.num_pages;
+    a.max_blocks = p.max_blocks_per_seq;
+    a.max_q = p.max_q_len;
+    a.total_q = p.total_q;
+    a.window = p.window;
+    a.q_stride = stride;
+    a.sm_scale = p.sm_scale;
+    a.q = static_cast<const uint16_t *>(q);
+    a.k = static_cast<const uint16_t *>(k);
+    a.v = static_cast<const uint16_t *>(v);
+    a.keep_in = keep_in;
+    a.seq_lens = seq_lens;
+    a.cu_q = cu_q;
+    a.block_table = block_table;
+    a.parents = parents;
+    a.out = static_cast<uint16_t *>(out);
+    a.lse = lse;
+    a.err = static_cast<int *>(workspace);
+    a.wait_ns = p.wait_limit_us > 0 ? (uint64_t)p.wait_limit_us * 1000ull : kWaitTimeoutNs;
+    return cuda_status(launch_tree_attention(a, pl, p.dtype, static_cast<cudaStream_t>(stream)));
+}
+
+ffd_status ffd_tree_commit(const ffd_cache_desc *cache, int32_t batch, int32_t max_blocks_per_seq,
+                           int32_t total_nodes, const int64_t *draft, const int64_t *target,
+                           const int32_t *parents, const int32_t *cu_nodes, const int32_t *seq_lens,
+                           const int32_t *block_table, void *k, void *v, uint8_t *thumb,
+                           uint8_t *resid, int32_t *path, int32_t *accepted, int64_t *next_token,
+                           int32_t *new_lens, int32_t *error_word, void *stream) {
+    if (!cache || !seq_lens || !block_table || !accepted || !next_token || !new_lens)
+        return FFD_ERR_INVALID_ARG;
+    if (cache->num_pages < 1 || cache->num_kv_heads < 1 || batch < 1 || max_blocks_per_seq < 1 ||
+        total_nodes < 0)
+        return FFD_ERR_INVALID_ARG;
+    if (total_nodes > 0 && (!draft || !target || !path)) return FFD_ERR_INVALID_ARG;
+    if (!cu_nodes && total_nodes % batch != 0) return FFD_ERR_INVALID_ARG;
+    if ((thumb == nullptr) != (resid == nullptr)) return FFD_ERR_INVALID_ARG;
+    for (const void *x : {(const void *)k, (const void *)v, (const void *)thumb, (const void *)resid})
+        if (!aligned(x, 16)) return FFD_ERR_INVALID_ARG;
+    for (const void *x : {(const void *)draft, (const void *)target, (const void *)next_token})
+        if (!aligned(x, 8)) return FFD_ERR_INVALID_ARG;
+    for (const void *x : {(const void *)parents, (const void *)cu_nodes, (const void *)seq_lens,
+                          (const void *)block_table, (const void *)path, (const void *)accepted,
+                          (const void *)new_lens, (const void *)error_word})
+        if (!aligned(x, 4)) return FFD_ERR_INVALID_ARG;
+    if (overlap(seq_lens, 4 * (int64_t)batch, new_lens, 4 * (int64_t)batch))
+        return FFD_ERR_INVALID_ARG;  // every KV head's block reads the length, at its own time
+    if (cache->head_dim != kD || cache->page_size != kPage) return FFD_ERR_UNSUPPORTED;
+    if ((int64_t)max_blocks_per_seq * kPage > INT32_MAX) return FFD_ERR_UNSUPPORTED;
+    if ((int64_t)batch * cache->num_kv_heads > INT32_MAX) return FFD_ERR_UNSUPPORTED;  // grid.x
+    if (!cu_nodes && total_nodes / batch > kMaxNodes) return FFD_ERR_UNSUPPORTED;
+    CommitArgs a{};
+    a.B = batch;
+    a.Hkv = cache->num_kv_heads;
+    a.P = cache->num_pages;
+    a.max_blocks = max_blocks_per_seq;
+    a.T = total_nodes;
+    a.each = cu_nodes ? 0 : total_nodes / batch;
+    a.draft = draft;
+    a.target = target;
+    a.parents = parents;
+    a.cu = cu_nodes;
+    a.seq_lens = seq_lens;
+    a.block_table = block_table;
+    a.k = static_cast<uint8_t *>(k);
+    a.v = static_cast<uint8_t *>(v);
+    a.thumb = thumb;
+    a.resid = resid;
+    a.path = path;
+    a.accepted = accepted;
+    a.next_token = next_token;
+    a.new_lens = new_lens;
+    a.err = error_word;
+    return cuda_status(launch_tree_commit(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -64,6 +64,21 @@ class Kv4Params(ctypes.Structure):
                 ("wait_limit_us", ctypes.c_int32)]
 
 
+class RopeParams(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("max_blocks_per_seq", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("total_tokens", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("rot_scale", ctypes.c_float),
+                ("q_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
+
+
+class TreeParams(ctypes.Structure):
+    _fields_ = Kv4Params._fields_
+
+
 def make_params(batch, num_q_heads, num_kv_heads, num_pages, max_blocks_per_seq, *, sink=64,
                 local=1024, delta=5.0, sm_scale=None, num_splits=0,
                 wait_limit_us=0, schedule=0) -> DecodeParams:
@@ -142,6 +157,15 @@ def lib() -> ctypes.CDLL:
             L.ffd_kv4_attention.argtypes = [ctypes.POINTER(Kv4Params)] + [P] * 10 + \
                 [ctypes.c_size_t, P]
             L.ffd_kv4_attention.restype = st
+            L.ffd_rope_append.argtypes = [ctypes.POINTER(RopeParams)] + [P] * 15
+            L.ffd_rope_append.restype = st
+            L.ffd_tree_workspace_size.argtypes = [ctypes.POINTER(TreeParams)]
+            L.ffd_tree_workspace_size.restype = ctypes.c_size_t
+            L.ffd_tree_attention.argtypes = [ctypes.POINTER(TreeParams)] + [P] * 11 + \
+                [ctypes.c_size_t, P]
+            L.ffd_tree_attention.restype = st
+            L.ffd_tree_commit.argtypes = [ctypes.POINTER(CacheDesc), i32, i32, i32] + [P] * 16
+            L.ffd_tree_commit.restype = st
             L.ffd_set_profile_events.argtypes = [P, P]
             L.ffd_set_profile_events.restype = st
             L.ffd_get_error.argtypes = [P, P]
@@ -541,6 +565,247 @@ def ffd_kv4_attention(params: Kv4Params, q, cache: Kv4Cache, seq_lens, block_tab
         ctypes.byref(params), q.data_ptr(), k4.data_ptr(), v4.data_ptr(), seq_lens.data_ptr(),
         _addr(cu_q), block_table.data_ptr(), _addr(keep_in), out.data_ptr(), _addr(lse),
         workspace.data_ptr(), workspace.nbytes, _stream_of(stream, dev))
+    if status != FFD_OK:
+        _check(status, where)
+
+
+# ---- speculative decoding over the 16-bit cache -------------------------------------------------
+TREE_MAX_NODES = 256
+_I64 = torch.int64
+_rope_shapes = {}  # shape of an append -> a reference to its RopeParams
+
+
+def _pages(x, heads=None):
+    """Whether x is a cache of K or V pages."""
+    shape = x.shape
+    return (len(shape) == 4 and shape[2] == PAGE and shape[3] == HEAD_DIM and x.is_contiguous()
+            and (heads is None or shape[1] == heads))
+
+
+def _records(quantized, P, Hkv, dev):
+    thumb, resid = quantized
+    return (thumb.dtype == _U8 and resid.dtype == _U8 and thumb.shape == (P, Hkv, THUMB_RECORD_BYTES)
+            and resid.shape == (P, Hkv, RESID_RECORD_BYTES) and thumb.is_contiguous()
+            and resid.is_contiguous() and thumb.get_device() == dev and resid.get_device() == dev)
+
+
+def ffd_rope_append(q, k_new, v_new, inv_freq, positions, block_table, q_out, k_cache, v_cache, *,
+                    cu_tokens=None, rope_positions=None, interleaved=False, rot_scale=1.0,
+                    quantized=None, error_word=None, stream=None) -> None:
+    """Rotate q [T, Hq, 128] into q_out (both None: no queries; the same tensor: in place) and
+    k_new [T, Hkv, 128] into the cache, and append v_new: k_cache, v_cache [P, Hkv, 64, 128] of the rows'
+    dtype (k_cache may be None where ``quantized``, a QuantizedCache, is given). The first
+    2 * inv_freq.numel() channels are rotated (inv_freq fp32 or None), by rope_positions int32 [T] or
+    the tokens' own indices. Rows and tokens are matched as in ffd_kv4_write."""
+    where = "ffd_rope_append"
+    if k_new is None or v_new is None or v_cache is None or (q is None) != (q_out is None):
+        _refuse(where, "no rows")
+    if k_cache is None and quantized is None:
+        _refuse(where, "no cache for the keys")
+    dev = v_cache.get_device()
+    if not (dev >= 0 and k_new.get_device() == dev and v_new.get_device() == dev
+            and positions.get_device() == dev and block_table.get_device() == dev
+            and (k_cache is None or k_cache.get_device() == dev)
+            and (q is None or (q.get_device() == dev and q_out.get_device() == dev))
+            and (inv_freq is None or inv_freq.get_device() == dev)
+            and (rope_positions is None or rope_positions.get_device() == dev)
+            and (cu_tokens is None or cu_tokens.get_device() == dev)
+            and (error_word is None or error_word.get_device() == dev)):
+        _refuse(where, "tensors on different devices, or not on a GPU")
+    dtype = k_new.dtype
+    if dtype not in _DTYPES or v_cache.dtype != dtype or not _pages(v_cache) or (
+            k_cache is not None and not (k_cache.dtype == dtype and k_cache.shape == v_cache.shape
+                                         and k_cache.is_contiguous())):
+        _refuse(where, "k_cache and v_cache [P, Hkv, 64, 128] of the rows' dtype, bf16 or fp16")
+    P, Hkv, _, _ = v_cache.shape
+    if quantized is not None and not _records(quantized, P, Hkv, dev):
+        _refuse(where, "the quantised cache")
+    table = block_table.shape
+    if len(table) != 2 or not (
+            block_table.dtype == _I32 and positions.dtype == _I32 and positions.shape == table[:1]
+            and block_table.is_contiguous() and positions.is_contiguous()
+            and (cu_tokens is None or (cu_tokens.dtype == _I32 and cu_tokens.is_contiguous()
+                                       and cu_tokens.shape == (table[0] + 1,)))):
+        _refuse(where, "int32 positions [B], cu_tokens [B + 1], block_table [B, width]")
+    T = k_new.shape[0] if k_new.dim() == 3 else -1
+    if rope_positions is not None and not (rope_positions.dtype == _I32 and rope_positions.shape == (T,)
+                                           and rope_positions.is_contiguous()):
+        _refuse(where, "int32 rope_positions [T]")
+    rot = 0
+    if inv_freq is not None:
+        if not (inv_freq.dtype == _F32 and inv_freq.dim() == 1 and inv_freq.is_contiguous()):
+            _refuse(where, "inv_freq fp32 [rotated channels / 2]")
+        rot = 2 * inv_freq.shape[0]
+    if error_word is not None and error_word.nbytes < 4:
+        _refuse(where, "an error word of 4 bytes")
+    Hq, qs, qos = 0, 0, 0
+    if q is not None:
+        Hq = q.shape[1] if q.dim() == 3 else 0
+        qs, qos = _row_stride(q, T, Hq, dtype), _row_stride(q_out, T, Hq, dtype)
+    ks, vs = _row_stride(k_new, T, Hkv, dtype), _row_stride(v_new, T, Hkv, dtype)
+    if qs is None or qos is None or ks is None or vs is None:
+        _refuse(where, "rows of one dtype: q, q_out [T, Hq, 128], k_new, v_new [T, Hkv, 128]")
+    if _C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return ffd_rope_append(q, k_new, v_new, inv_freq, positions, block_table, q_out, k_cache,
+                                   v_cache, cu_tokens=cu_tokens, rope_positions=rope_positions,
+                                   interleaved=interleaved, rot_scale=rot_scale, quantized=quantized,
+                                   error_word=error_word, stream=stream)
+    shape = (table[0], Hq, Hkv, HEAD_DIM, PAGE, P, table[1], _DTYPES[dtype], T, rot,
+             1 if interleaved else 0, rot_scale, qs, qos, ks, vs)
+    ref = _rope_shapes.get(shape)
+    if ref is None:
+        if len(_rope_shapes) >= 1024:  # ragged batches come in many sizes
+            _rope_shapes.clear()
+        ref = _rope_shapes[shape] = ctypes.byref(RopeParams(*shape))
+    thumb, resid = (None, None) if quantized is None else quantized
+    status = (_lib or lib()).ffd_rope_append(
+        ref, _addr(q), k_new.data_ptr(), v_new.data_ptr(), _addr(inv_freq), _addr(rope_positions),
+        _addr(cu_tokens), positions.data_ptr(), block_table.data_ptr(), _addr(q_out), _addr(k_cache),
+        v_cache.data_ptr(), _addr(thumb), _addr(resid), _addr(error_word), _stream_of(stream, dev))
+    if status != FFD_OK:
+        _check(status, where)
+
+
+def make_tree_params(batch, num_q_heads, num_kv_heads, num_pages, max_blocks_per_seq, *,
+                     max_q_len=1, total_q=None, dtype=torch.bfloat16, window=0, sm_scale=None,
+                     num_splits=0, q_stride=0, wait_limit_us=0) -> TreeParams:
+    """total_q None: every sequence has max_q_len nodes."""
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(HEAD_DIM)
+    if total_q is None:
+        total_q = batch * max_q_len
+    return TreeParams(batch, num_q_heads, num_kv_heads, HEAD_DIM, PAGE, num_pages,
+                      max_blocks_per_seq, _DTYPES[dtype], max_q_len, total_q, window, num_splits,
+                      q_stride, sm_scale, wait_limit_us)
+
+
+def ffd_tree_workspace_size(params: TreeParams) -> int:
+    return int(lib().ffd_tree_workspace_size(ctypes.byref(params)))
+
+
+def alloc_tree_workspace(params: TreeParams, device="cuda") -> torch.Tensor:
+    n = ffd_tree_workspace_size(params)
+    if n == 0:
+        raise FFDError(1, "tree attention workspace size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def ffd_tree_attention(params: TreeParams, q, k, v, seq_lens, block_table, out, workspace, *,
+                       parents=None, cu_q=None, keep_in=None, lse=None, stream=None) -> None:
+    """Attention of each sequence's newest tokens, a tree of drafted tokens (parents int32 [total_q],
+    -1 or an earlier node of the sequence; None: a chain), over k, v [P, Hkv, 64, 128]:
+    q [total_q, Hq, 128], rows params.q_stride elements apart, out [total_q, Hq, 128], lse fp32
+    [total_q, Hq] or None."""
+    where = "ffd_tree_attention"
+    dev = q.get_device()
+    if not (dev >= 0 and k.get_device() == dev and v.get_device() == dev
+            and seq_lens.get_device() == dev and block_table.get_device() == dev
+            and out.get_device() == dev and workspace.get_device() == dev
+            and (parents is None or parents.get_device() == dev)
+            and (cu_q is None or cu_q.get_device() == dev)
+            and (keep_in is None or keep_in.get_device() == dev)
+            and (lse is None or lse.get_device() == dev)):
+        _refuse(where, "tensors on different devices, or not on a GPU")
+    B, Hq, Hkv, T = params.batch, params.num_q_heads, params.num_kv_heads, params.total_q
+    width, dtype, row = params.max_blocks_per_seq, q.dtype, Hq * HEAD_DIM
+    shape = (params.num_pages, Hkv, PAGE, HEAD_DIM)
+    if not (k.dtype == dtype and v.dtype == dtype and k.shape == shape and v.shape == shape
+            and k.is_contiguous() and v.is_contiguous()):
+        _refuse(where, "k and v [num_pages, Hkv, 64, 128] of q's dtype")
+    shape = (T, Hq, HEAD_DIM)
+    if not (q.shape == shape and out.shape == shape and out.dtype == dtype and out.is_contiguous()
+            and _DTYPES.get(dtype) == params.dtype):
+        _refuse(where, "q and out of params.dtype [total_q, Hq, 128]")
+    stride = q.stride()
+    if (stride[2] != 1 or (stride[1] != HEAD_DIM and Hq > 1)
+            or (T > 1 and stride[0] != (params.q_stride or row))):
+        _refuse(where, "q's rows, params.q_stride elements apart")
+    if not (block_table.dtype == _I32 and block_table.shape == (B, width)
+            and block_table.is_contiguous() and seq_lens.dtype == _I32 and seq_lens.shape == (B,)
+            and seq_lens.is_contiguous()
+            and (parents is None or (parents.dtype == _I32 and parents.shape == (T,)
+                                     and parents.is_contiguous()))
+            and (cu_q is None or (cu_q.dtype == _I32 and cu_q.shape == (B + 1,)
+                                  and cu_q.is_contiguous()))):
+        _refuse(where, "int32 seq_lens [B], parents [total_q], cu_q [B + 1], block_table [B, "
+                       "max_blocks_per_seq]")
+    if keep_in is not None and not (keep_in.dtype == _U8 and keep_in.shape == (B, Hkv, width)
+                                    and keep_in.is_contiguous()):
+        _refuse(where, "keep_in u8 [B, Hkv, max_blocks_per_seq]")
+    if lse is not None and not (lse.dtype == _F32 and lse.shape == (T, Hq) and lse.is_contiguous()):
+        _refuse(where, "lse fp32 [total_q, Hq]")
+    if not workspace.is_contiguous():
+        _refuse(where, "the workspace")
+    if _C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return ffd_tree_attention(params, q, k, v, seq_lens, block_table, out, workspace,
+                                      parents=parents, cu_q=cu_q, keep_in=keep_in, lse=lse,
+                                      stream=stream)
+    status = (_lib or lib()).ffd_tree_attention(
+        ctypes.byref(params), q.data_ptr(), k.data_ptr(), v.data_ptr(), seq_lens.data_ptr(),
+        _addr(cu_q), _addr(parents), block_table.data_ptr(), _addr(keep_in), out.data_ptr(),
+        _addr(lse), workspace.data_ptr(), workspace.nbytes, _stream_of(stream, dev))
+    if status != FFD_OK:
+        _check(status, where)
+
+
+def ffd_tree_commit(draft, target, seq_lens, block_table, k_cache, v_cache, path, accepted, next_token,
+                    new_lens, *, parents=None, cu_nodes=None, quantized=None, error_word=None,
+                    stream=None) -> None:
+    """Accept the drafted tokens that the model confirms (draft int64 [T], target int64 [T]: the
+    model's token behind each node) and move their rows to the sequences' ends. k_cache (or None)
+    and v_cache [P, Hkv, 64, 128], ``quantized`` a QuantizedCache or None; outputs path int32 [T],
+    accepted and new_lens int32 [B], next_token int64 [B]."""
+    where = "ffd_tree_commit"
+    dev = v_cache.get_device()
+    if not (dev >= 0 and draft.get_device() == dev and target.get_device() == dev
+            and seq_lens.get_device() == dev and block_table.get_device() == dev
+            and path.get_device() == dev and accepted.get_device() == dev
+            and next_token.get_device() == dev and new_lens.get_device() == dev
+            and (k_cache is None or k_cache.get_device() == dev)
+            and (parents is None or parents.get_device() == dev)
+            and (cu_nodes is None or cu_nodes.get_device() == dev)
+            and (error_word is None or error_word.get_device() == dev)):
+        _refuse(where, "tensors on different devices, or not on a GPU")
+    if not (_pages(v_cache) and v_cache.dtype in _DTYPES
+            and (k_cache is None or (k_cache.dtype == v_cache.dtype and k_cache.shape == v_cache.shape
+                                     and k_cache.is_contiguous()))):
+        _refuse(where, "k_cache and v_cache [P, Hkv, 64, 128], bf16 or fp16")
+    P, Hkv, _, _ = v_cache.shape
+    if quantized is not None and not _records(quantized, P, Hkv, dev):
+        _refuse(where, "the quantised cache")
+    table, nodes = block_table.shape, draft.shape
+    if len(table) != 2 or not (
+            block_table.dtype == _I32 and block_table.is_contiguous() and seq_lens.dtype == _I32
+            and seq_lens.shape == table[:1] and seq_lens.is_contiguous() and accepted.dtype == _I32
+            and accepted.shape == table[:1] and accepted.is_contiguous() and new_lens.dtype == _I32
+            and new_lens.shape == table[:1] and new_lens.is_contiguous() and next_token.dtype == _I64
+            and next_token.shape == table[:1] and next_token.is_contiguous()
+            and (cu_nodes is None or (cu_nodes.dtype == _I32 and cu_nodes.is_contiguous()
+                                      and cu_nodes.shape == (table[0] + 1,)))):
+        _refuse(where, "int32 seq_lens, accepted, new_lens [B], cu_nodes [B + 1], block_table [B, width],"
+                       " int64 next_token [B]")
+    if len(nodes) != 1 or not (
+            draft.dtype == _I64 and draft.is_contiguous() and target.dtype == _I64
+            and target.shape == nodes and target.is_contiguous() and path.dtype == _I32
+            and path.shape == nodes and path.is_contiguous()
+            and (parents is None or (parents.dtype == _I32 and parents.shape == nodes
+                                     and parents.is_contiguous()))):
+        _refuse(where, "int64 draft, target [T], int32 path, parents [T]")
+    if error_word is not None and error_word.nbytes < 4:
+        _refuse(where, "an error word of 4 bytes")
+    if _C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return ffd_tree_commit(draft, target, seq_lens, block_table, k_cache, v_cache, path,
+                                   accepted, next_token, new_lens, parents=parents, cu_nodes=cu_nodes,
+                                   quantized=quantized, error_word=error_word, stream=stream)
+    thumb, resid = (None, None) if quantized is None else quantized
+    status = (_lib or lib()).ffd_tree_commit(
+        _desc(P, Hkv), table[0], table[1], nodes[0], draft.data_ptr(), target.data_ptr(),
+        _addr(parents), _addr(cu_nodes), seq_lens.data_ptr(), block_table.data_ptr(), _addr(k_cache),
+        v_cache.data_ptr(), _addr(thumb), _addr(resid), path.data_ptr(), accepted.data_ptr(),
+        next_token.data_ptr(), new_lens.data_ptr(), _addr(error_word), _stream_of(stream, dev))
     if status != FFD_OK:
         _check(status, where)
 
