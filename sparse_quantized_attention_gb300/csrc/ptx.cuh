@@ -284,10 +284,19 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&x)[
 // all.
 __device__ __forceinline__ uint32_t tc_desc(uint32_t addr) { return (addr & 0x3ffff) >> 4 | 1u << 16; }
 constexpr uint32_t kTcDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
+// The same for an operand whose other direction is contiguous (MN-major): rows of 64 elements, swizzled
+// alike, one for each index of the sum; the next 64 elements are `wide` bytes on, groups of eight rows
+// 1024 bytes.
+__device__ __forceinline__ uint32_t tc_desc_mn(uint32_t addr, uint32_t wide) {
+    return (addr & 0x3ffff) >> 4 | (wide >> 4) << 16;
+}
 // Instruction word of f16 x f16 -> f32, both operands K-major, M x N.
 constexpr uint32_t tc_idesc_f16(int m, int n) {
     return 1u << 4 | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
 }
+
+// Of bf16 operands, and of a B that is MN-major: to be added.
+constexpr uint32_t kTcBf16 = 1u << 7 | 1u << 10, kTcBMn = 1u << 16;
 
 // D[tmem] (+)= A B^T of one 16-deep step, A and B in shared memory; one thread issues.
 __device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {

@@ -37,8 +37,10 @@ struct CommitArgs {
 // Arguments of an attention call.
 struct AttnArgs {
     int B, Hq, Hkv, G, P, max_blocks, max_q, total_q, window;
+    int lead;         // as in Plan
+    uint32_t over_g;  // ceil(2^32 / G), too large by less than G / 2^32 of it (G > 1)
     int64_t q_stride;
-    float sm_scale;
+    float factor;     // of scores, to log2 units
     const uint16_t *q, *k, *v;
     const uint8_t *keep_in;
     const int32_t *seq_lens, *cu_q, *block_table, *parents;
@@ -48,10 +50,12 @@ struct AttnArgs {
     uint64_t wait_ns;
 };
 
-// Launch shape and workspace of an attention call.
+// Launch shape and workspace of an attention call (byte offsets behind the error word).
 struct Plan {
+    int tiles;  // of 128 rows that walk the cache together: 1 or 2
     int ctas;
-    size_t total;
+    int lead;   // pages' time that an item counts for besides its pages
+    size_t tickets, records, total;
 };
 
 // Sequence of row t and the row's place in it, by a whole warp: the offsets cu [B+1] are searched 32

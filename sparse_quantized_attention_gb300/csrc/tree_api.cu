@@ -2,6 +2,7 @@
 // argument checks, workspace planning and launches.
 #include <math.h>
 
+#include "kv4.cuh"
 #include "ptx.cuh"
 #include "tree.cuh"
 
@@ -10,6 +11,8 @@ namespace tree {
 cudaError_t launch_rope_append(RopeArgs a, int dtype, cudaStream_t stream);
 cudaError_t launch_tree_commit(const CommitArgs &a, cudaStream_t stream);
 cudaError_t launch_tree_attention(const AttnArgs &a, const Plan &pl, int dtype, cudaStream_t stream);
+int tree_slots();
+size_t tree_record_bytes(int tiles);
 }  // namespace tree
 }  // namespace ffd
 
@@ -63,11 +66,41 @@ ffd_status check_params(const ffd_tree_params *p) {
     return FFD_OK;
 }
 
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+constexpr int64_t kMinPages = 4;  // of a CTA, at least (upper bound from the table's width)
+
+// Workspace: [error word | three join tickets per CTA | records per CTA]. The tickets, the only part that
+// has to start at zero, have the same place and size whatever the parameters and are left at zero, so that
+// calls of different shapes can share a workspace.
 ffd_status make_plan(const ffd_tree_params *p, Plan *pl) {
     const ffd_status st = check_params(p);
     if (st != FFD_OK) return st;
-    pl->ctas = 0;
-    pl->total = kAlign;
+    const int64_t rows = (int64_t)p->max_q_len * (p->num_q_heads / p->num_kv_heads);
+    pl->tiles = rows <= kTileRows ? 1 : 2;
+    const int64_t each = kTileRows * pl->tiles, groups = (rows + each - 1) / each;
+    const int64_t items = (int64_t)p->batch * p->num_kv_heads * groups;
+    const int sms = current_sm_count();
+    int64_t ctas = p->num_splits;
+    if (ctas == 0) {
+        if (sms <= 0) return FFD_ERR_CUDA;
+        int64_t most = p->max_blocks_per_seq;  // pages that an item sees at most
+        if (p->window > 0) {
+            const int64_t seen = ((int64_t)p->window + p->max_q_len) / kPage + 2;
+            most = most < seen ? most : seen;
+        }
+        ctas = (items * most + kMinPages - 1) / kMinPages;
+    }
+    if (sms > 0 && ctas > sms) ctas = sms;
+    if (ctas > kv4::kMaxCtas) ctas = kv4::kMaxCtas;
+    pl->ctas = (int)ctas;
+    pl->lead = 8 * items <= ctas ? 0 : kItemPages;
+    size_t off = kAlign;
+    pl->tickets = off;
+    off = align_up(off + 3 * kv4::kMaxCtas * sizeof(int));
+    pl->records = off;
+    off = align_up(off + (size_t)tree_slots() * pl->ctas * tree_record_bytes(pl->tiles));
+    pl->total = off;
     return FFD_OK;
 }
 
@@ -185,7 +218,9 @@ ffd_status ffd_tree_attention(const ffd_tree_params *params, const void *q, cons
     a.total_q = p.total_q;
     a.window = p.window;
     a.q_stride = stride;
-    a.sm_scale = p.sm_scale;
+    a.lead = pl.lead;
+    a.over_g = (uint32_t)(((uint64_t)1 << 32) / a.G + (((uint64_t)1 << 32) % a.G != 0));
+    a.factor = fmaxf(p.sm_scale * 1.4426950408889634f, 1.2e-38f);  // never 0: times -inf it has to stay -inf
     a.q = static_cast<const uint16_t *>(q);
     a.k = static_cast<const uint16_t *>(k);
     a.v = static_cast<const uint16_t *>(v);
