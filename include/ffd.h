@@ -686,7 +686,9 @@ size_t ffd_tree_workspace_size(const ffd_tree_params *params);
  * is treated as dropped), a sequence length above the table's (clamped) or below nq (its rows see
  * nothing), a cu_q entry out of range (that sequence's rows are left as they were) or a parent that
  * is neither -1 nor an earlier node (taken as -1); FFD_ERRBIT_TIMEOUT for a wait that ran out
- * (the call's results are invalid, the workspace is ready for the next one).
+ * (the call's results are invalid; zero-fill the workspace again).
+ * Launch: one cooperative kernel of at most one CTA per SM whose CTAs wait for each other's parts, so all
+ * of them must be resident at once; a launch that cannot be fails with FFD_ERR_CUDA and enqueues nothing.
  */
 ffd_status ffd_tree_attention(const ffd_tree_params *params, const void *q, const void *k,
                               const void *v, const int32_t *seq_lens, const int32_t *cu_q,

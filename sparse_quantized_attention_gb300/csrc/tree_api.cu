@@ -70,7 +70,7 @@ size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 constexpr int64_t kMinPages = 4;  // of a CTA, at least (upper bound from the table's width)
 
-// Workspace: [error word | three join tickets per CTA | records per CTA]. The tickets, the only part that
+// Workspace: [error word | two counters per CTA | records per CTA]. The counters, the only part that
 // has to start at zero, have the same place and size whatever the parameters and are left at zero, so that
 // calls of different shapes can share a workspace.
 ffd_status make_plan(const ffd_tree_params *p, Plan *pl) {
@@ -97,7 +97,7 @@ ffd_status make_plan(const ffd_tree_params *p, Plan *pl) {
     pl->lead = 8 * items <= ctas ? 0 : kItemPages;
     size_t off = kAlign;
     pl->tickets = off;
-    off = align_up(off + 3 * kv4::kMaxCtas * sizeof(int));
+    off = align_up(off + 2 * kv4::kMaxCtas * sizeof(int));
     pl->records = off;
     off = align_up(off + (size_t)tree_slots() * pl->ctas * tree_record_bytes(pl->tiles));
     pl->total = off;

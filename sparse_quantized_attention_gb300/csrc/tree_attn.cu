@@ -4,12 +4,13 @@
 // The query rows of a (sequence, KV head), nq nodes x G heads, are taken kRows = 128 or 256 at a time: an
 // item is one such group of rows over the pages that any of them sees. The pages of all items,
 // concatenated with what each item costs besides, are cut into equal contiguous ranges, one per CTA (one per
-// SM); an item cut by a range's end is joined by the last of its CTAs. In steps of two pages, 128 tokens,
-// a CTA computes for each tile of 128 rows
-//   S = Q K^T   (M 128, N 128, K 128; both operands in shared memory, S in tensor memory),
+// SM). CTAs that share an item write their parts as records and, once all have come to their range's end, join
+// a part of its rows and channels each. In steps of one page (two tiles) or two pages (one tile) a CTA
+// computes for each tile of 128 rows
+//   S = Q K^T   (M 128, N 64 or 128, K 128; both operands in shared memory, S in tensor memory),
 //   P = 2^(S - m) in the inputs' type against a reference m that follows the row's maximum lazily: it is
 //       raised, and O rescaled, only when a score passes it by 2^8,
-//   O += P V    (M 128, N 128, K 128; P in tensor memory over S, V in shared memory, O in tensor memory).
+//   O += P V    (M 128, N 128, K 64 a page; P in tensor memory over S, V in shared memory, O in tensor memory).
 // Both K and V lie in shared memory as the cache holds them, tokens by channels: K is read along its rows,
 // V across them.
 //
@@ -33,14 +34,11 @@ using kv4::kLazy;
 using kv4::kMaxCtas;
 using kv4::kShift;
 using kv4::lse_of;
-using kv4::Shares;
 
 constexpr int kTile = 128;       // rows of a tile
-constexpr int kStep = 2;         // pages of a step
 constexpr int kPageBytes = kPage * kD * 2;
 constexpr int kInfo = 8;         // steps whose pages are kept
-constexpr int kSlots = 4;        // records of a CTA, as in the 4-bit chunk kernel
-constexpr int kOnce = 8;         // records that one CTA joins at once
+constexpr int kSlots = 2;        // records of a CTA: of the item that goes on from before, and that goes on
 constexpr uint32_t kColO = 256;  // O of tile g at kColO + 128 g
 
 template <class T>
@@ -57,13 +55,13 @@ struct Shape {
     static constexpr int kRows = kTile * kTiles;
     static constexpr int kSoft = 4 * kTiles;               // softmax warps
     static constexpr int kThreads = 32 * (kSoft + 4);      // copy, two issuers, cleaner
-    static constexpr int kNK = kTiles == 1 ? 3 : 2;        // steps' K in shared memory
+    static constexpr int kStep = kTiles == 1 ? 2 : 1;      // pages of a step
+    static constexpr int kNK = kTiles == 1 ? 3 : 4;        // steps' K in shared memory
     static constexpr int kNV = 5;                          // pages' V
     static constexpr int kRecord = 130 * kRows;            // floats of a joined item: o[128][row], m, l
-    static constexpr int kAhead = 3 - kTiles;              // steps whose S is under way before P V
-    // tensor memory columns of S (P over its first half): one tile has two places in turn
+    // tensor memory columns of S (P over its first half): a tile has two places in turn
     static __device__ __forceinline__ uint32_t col_s(int g, uint32_t step) {
-        return kTiles == 1 ? 128 * (step & 1) : 128 * g;
+        return 64 * kStep * (2 * g + (step & 1));
     }
 };
 
@@ -72,11 +70,17 @@ struct Step {  // a step's pages: block indexes (first -1: the segment's end, se
     int edge;  // some row does not see all of it
 };
 
+struct Cut {  // an item that several CTAs share
+    int p0, p1;          // the CTAs, first and last
+    int row0, rows;      // its group's first row, rows of it (and of later groups)
+    int h, t0;
+};
+
 template <int kTiles>
 struct Shared {
     using H = Shape<kTiles>;
     uint8_t q[kTiles][2 * 16384];               // tile: channels 0-63, then 64-127
-    uint8_t k[H::kNK][kStep * kPageBytes];      // the same for 128 tokens
+    uint8_t k[H::kNK][H::kStep * kPageBytes];   // the same for a step's tokens
     uint8_t v[H::kNV][kPageBytes];              // the same for 64 tokens
     uint32_t bits[kMaxNodes / 32][H::kRows];    // nodes that a row sees
     int parent[kTiles][kMaxNodes];
@@ -88,7 +92,7 @@ struct Shared {
     uint32_t tmem, aborted;
     int scan[H::kThreads / 32];
     int pre[H::kThreads];                       // weight of all items before each chunk of sequences
-    int flag;
+    Cut cut[2];                                 // the first item, if it began before, and the last, if it goes on
 };
 
 struct Params {
@@ -249,6 +253,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     tree_kernel(const __grid_constant__ Params prm) {
     using H = Shape<kTiles>;
     constexpr int kRows = H::kRows, kThreads = H::kThreads, kCtaWarps = kThreads / 32;
+    constexpr int kStep = H::kStep;
     constexpr uint32_t kIdescS128 = tc_idesc_f16(128, 128) | Idesc<T>::kType;
     constexpr uint32_t kIdescS64 = tc_idesc_f16(128, 64) | Idesc<T>::kType;
     constexpr uint32_t kIdescO = tc_idesc_f16(128, 128) | Idesc<T>::kType | kTcBMn;
@@ -263,6 +268,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     if (warp == 0) tmem_alloc(&sh.tmem, 512);
     if (tid == 0) {
         sh.aborted = 0;
+        sh.cut[0].p0 = sh.cut[1].p0 = -1;
         for (int i = 0; i < H::kNK; i++) {
             mbar_init(&sh.k_full[i], 1);
             mbar_init(&sh.k_free[i], kTiles);
@@ -477,15 +483,15 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                     if (lane == 0) mbar_arrive(&sh.p_full[grp][buf]);
                     break;
                 }
-                const bool both = j1 >= 0;
+                const bool both = kStep == 2 && j1 >= 0;
                 if (active) {
                     uint64_t see0 = ~0ull, see1 = ~0ull;
                     if (edge) {
                         see0 = visible(j0);
                         if (both) see1 = visible(j1);
                     }
-                    // S in halves of 64 columns (a page), read twice
-                    auto half = [&](uint32_t (&x)[64], int n) {
+                    // S by pages, 64 columns; of two pages the second is read twice
+                    auto page = [&](uint32_t (&x)[64], int n) {
                         __syncwarp();
                         tmem_load32(reinterpret_cast<uint32_t(&)[32]>(x[0]), ts + 64 * n);
                         tmem_load32(reinterpret_cast<uint32_t(&)[32]>(x[32]), ts + 64 * n + 32);
@@ -503,15 +509,20 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                     uint32_t x[64];
                     float top = -INFINITY;
                     auto largest = [&]() {
+                        float t[4] = {top, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int c = 0; c < 64; c += 2)
-                            top = fmaxf(top, fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 1])));
+                        for (int c = 0; c < 64; c += 8)
+#pragma unroll
+                            for (int e = 0; e < 4; e++)
+                                t[e] = fmaxf(t[e], fmaxf(__uint_as_float(x[c + 2 * e]),
+                                                         __uint_as_float(x[c + 2 * e + 1])));
+                        top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
                     };
                     if (both) {
-                        half(x, 1);
+                        page(x, 1);
                         largest();
                     }
-                    half(x, 0);
+                    page(x, 0);
                     largest();
                     top *= fs;
                     const bool raise = top > limit;
@@ -543,7 +554,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                     const float sub = kShift - (m == -INFINITY ? 0.0f : m);
                     const float fx = far ? 1.0f : fs;
                     const float2 f2 = make_float2(fx, fx), s2 = make_float2(sub, sub);
-                    float2 l2 = make_float2(0.0f, 0.0f);
+                    float2 l2 = make_float2(0.0f, 0.0f), l3 = l2;
                     auto powers = [&](int n) {
                         if (far) {
 #pragma unroll
@@ -556,7 +567,8 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                             float2 e = __ffma2_rn(make_float2(__uint_as_float(x[2 * c]),
                                                               __uint_as_float(x[2 * c + 1])), f2, s2);
                             e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-                            l2 = __fadd2_rn(l2, e);
+                            if (c & 1) l3 = __fadd2_rn(l3, e);
+                            else l2 = __fadd2_rn(l2, e);
                             p[c] = T::pack(e.x, e.y);
                         }
                         __syncwarp();
@@ -564,10 +576,10 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                     };
                     powers(0);  // P's first 32 columns lie over S's first half, which has been read
                     if (both) {
-                        half(x, 1);
+                        page(x, 1);
                         powers(1);
                     }
-                    l += l2.x + l2.y;
+                    l += (l2.x + l2.y) + (l3.x + l3.y);
                     if (edge) {
                         for (int n = 0; n < (both ? 2 : 1); n++) {
                             const uint32_t vs = (vsteps + n) % H::kNV;
@@ -593,10 +605,9 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
 
             // ---- the segment's results (a whole item's rows by way of the tile's queries, which are
             // read no more, so that lines of out are written whole)
-            auto slot = [&](int c, int n) { return prm.records + (int64_t)(kSlots * c + n) * H::kRecord; };
             if (active && run) {
                 const float inv = tainted ? NAN : l == 0.0f ? 0.0f : 1.0f / l;
-                float *row = slot(cta, begins ? 1 : 0) + grp * kTile + r;
+                float *row = prm.records + (int64_t)(kSlots * cta + begins) * H::kRecord + grp * kTile + r;
                 uint8_t *stage = sh.q[grp];
 #pragma unroll 1
                 for (int c = 0; c < 4; c++) {
@@ -646,80 +657,108 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                         a.lse[(int64_t)(s.t0 + qi) * a.Hq + h * a.G + rr - qi * a.G] = lse_of(m - kShift, l);
                 }
             }
-            if (!complete) {
-                // the last of the CTAs that share the item joins their records (of many: in two steps)
-                const Shares p(w.item, w.np, ncta, total, cta, kOnce);
+            if (!complete) {  // joined below
+                const int p0 = (int)(((int64_t)(w.item + 1) * ncta - 1) / total);
+                const int p1 = (int)(((int64_t)(w.item + w.np) * ncta - 1) / total);
+                if (tid == 0) sh.cut[begins] = Cut{p0, p1, row0, rows, h, s.t0};
                 named_barrier_sync(3, kRows);
-                if (tid == 0) sh.flag = p.last_of_group(prm.tickets);
-                named_barrier_sync(3, kRows);
-                const int used = rows < kRows ? rows : kRows;
-                // join records rec(0) .. rec(n - 1): 32 rows (one a lane) and 8 channels at a time, the
-                // loads of five records together
-                auto join = [&](auto rec, int n, auto done) {
-                    for (int k = warp; k < 16 * ((used + 31) / 32); k += H::kSoft) {
-                        const int q = 32 * (k >> 4) + lane, ch = 8 * (k & 15);
-                        float M = -INFINITY, ls = 0.0f, o[8] = {};
-                        for (int i0 = 0; i0 < n; i0 += 5) {
-                            float v[5][8], mn[5], ln[5];
+                if (tid == 0) add_acq_rel_gpu(prm.tickets + p0, 1);
+            }
+        }
+        // ---- items that several CTAs share: all of them join a part of the rows and channels each
+        named_barrier_sync(3, kRows);
+#pragma unroll 1
+        for (int e = 0; e < 2; e++) {
+            const Cut c = sh.cut[e];
+            if (c.p0 < 0) continue;
+            const int n = c.p1 - c.p0 + 1, place = cta - c.p0;
+            if (tid == 0) {
+                const uint64_t t0 = globaltimer_ns();
+                bool ok = true;
+                while (ok && ld_acquire_gpu(prm.tickets + c.p0) < n) ok = globaltimer_ns() - t0 <= a.wait_ns;
+                if (!ok) raise_error(a.err, FFD_ERRBIT_TIMEOUT);
+            }
+            named_barrier_sync(3, kRows);
+            const int used = c.rows < kRows ? c.rows : kRows;
+            // a unit is 32 rows, one a lane, and 8 channels; `split` warps share one unit's records
+            const int units = 16 * ((used + 31) / 32);
+            const int mine = units > place ? (units - place + n - 1) / n : 0;  // units place, place + n, ...
+            int split = 1;
+            while (2 * split * mine <= H::kSoft && 2 * split <= n) split *= 2;
+            const int teams = H::kSoft / split, team = warp / split, part = warp % split;
+#pragma unroll 1
+            for (int u0 = 0; u0 < mine; u0 += teams) {
+                const int unit = place + (u0 + team) * n;
+                const bool has = u0 + team < mine;
+                const int q = 32 * (unit >> 4) + lane, ch = 8 * (unit & 15);
+                float M = -INFINITY, ls = 0.0f, o[8] = {};
+                // the loads of five records together
+                for (int i0 = part; has && i0 < n; i0 += 5 * split) {
+                    float v[5][8], mn[5], ln[5];
 #pragma unroll
-                            for (int i = 0; i < 5; i++) {
-                                const bool in = i0 + i < n;
-                                const float *src = rec(in ? i0 + i : i0) + q;
+                    for (int i = 0; i < 5; i++) {
+                        const bool in = i0 + i * split < n;
+                        const int r = in ? i0 + i * split : i0;
+                        // a CTA's record: its second one where the item begins, else its first
+                        const float *src =
+                            prm.records + (int64_t)(kSlots * (c.p0 + r) + (r == 0)) * H::kRecord + q;
 #pragma unroll
-                                for (int c = 0; c < 8; c++) v[i][c] = __ldcg(src + (ch + c) * kRows);
-                                mn[i] = in ? __ldcg(src + 128 * kRows) : -INFINITY;
-                                ln[i] = __ldcg(src + 129 * kRows);
-                            }
-                            float Mn = M;
-#pragma unroll
-                            for (int i = 0; i < 5; i++) Mn = fmaxf(Mn, mn[i]);
-                            const float al = M == -INFINITY ? 0.0f : ex2_approx(M - Mn);
-                            M = Mn;
-                            ls *= al;
-#pragma unroll
-                            for (int c = 0; c < 8; c++) o[c] *= al;
-#pragma unroll
-                            for (int i = 0; i < 5; i++) {
-                                if (mn[i] == -INFINITY) continue;  // nothing in it: o and l are 0
-                                const float f = ex2_approx(mn[i] - M);
-                                ls = fmaf(f, ln[i], ls);
-#pragma unroll
-                                for (int c = 0; c < 8; c++) o[c] = fmaf(f, v[i][c], o[c]);
-                            }
-                        }
-                        if (q < used) done(q, ch, M, ls, o);
+                        for (int k = 0; k < 8; k++) v[i][k] = __ldcg(src + (ch + k) * kRows);
+                        mn[i] = in ? __ldcg(src + 128 * kRows) : -INFINITY;
+                        ln[i] = __ldcg(src + 129 * kRows);
                     }
-                };
-                auto finish = [&](int q, int ch, float M, float ls, const float (&o)[8]) {
-                    const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
-                    const int i = div_g(a, row0 + q), head = h * a.G + row0 + q - i * a.G;
-                    const int64_t at_row = (int64_t)(s.t0 + i) * a.Hq + head;
-                    *reinterpret_cast<uint4 *>(a.out + at_row * kD + ch) =
-                        make_uint4(T::pack(o[0] * inv, o[1] * inv), T::pack(o[2] * inv, o[3] * inv),
-                                   T::pack(o[4] * inv, o[5] * inv), T::pack(o[6] * inv, o[7] * inv));
-                    if (a.lse && ch == 0) a.lse[at_row] = lse_of(M - kShift, ls);
-                };
-                if (sh.flag) {
-                    // a CTA's record: its second one when the item begins there, else its first
-                    auto member = [&](int n) { return slot(p.g0 + n, p.g0 + n == p.p0); };
-                    if (p.groups == 1) {
-                        join(member, p.members, finish);
-                    } else {
-                        float *group = slot(p.g0, p.g0 == p.p0 ? 2 : 3);
-                        join(member, p.members, [&](int q, int ch, float M, float ls, const float (&o)[8]) {
+                    float Mn = M;
 #pragma unroll
-                            for (int c = 0; c < 8; c++) group[(ch + c) * kRows + q] = o[c];
-                            if (ch == 0) group[128 * kRows + q] = M, group[129 * kRows + q] = ls;
-                        });
-                        named_barrier_sync(3, kRows);
-                        if (tid == 0) sh.flag = p.last_group(prm.tickets);
-                        named_barrier_sync(3, kRows);
-                        if (sh.flag)
-                            join([&](int n) { return slot(p.p0 + n * p.size, n ? 3 : 2); }, p.groups, finish);
+                    for (int i = 0; i < 5; i++) Mn = fmaxf(Mn, mn[i]);
+                    const float al = M == -INFINITY ? 0.0f : ex2_approx(M - Mn);
+                    M = Mn;
+                    ls *= al;
+#pragma unroll
+                    for (int k = 0; k < 8; k++) o[k] *= al;
+#pragma unroll
+                    for (int i = 0; i < 5; i++) {
+                        if (mn[i] == -INFINITY) continue;  // nothing in it: o and l are 0
+                        const float f = ex2_approx(mn[i] - M);
+                        ls = fmaf(f, ln[i], ls);
+#pragma unroll
+                        for (int k = 0; k < 8; k++) o[k] = fmaf(f, v[i][k], o[k]);
                     }
                 }
-                named_barrier_sync(3, kRows);  // the flag has been read
+                if (split > 1) {  // the warps' parts, through the space of the queries (one round of units)
+                    float *mem = reinterpret_cast<float *>(sh.q[0]) + 32 * 10 * warp + lane;
+                    named_barrier_sync(3, kRows);
+#pragma unroll
+                    for (int k = 0; k < 8; k++) mem[32 * k] = o[k];
+                    mem[32 * 8] = M;
+                    mem[32 * 9] = ls;
+                    named_barrier_sync(3, kRows);
+                    if (part > 0) continue;
+                    for (int k = 1; k < split; k++) {
+                        const float *from = mem + 32 * 10 * k;
+                        const float m1 = from[32 * 8];
+                        if (m1 == -INFINITY) continue;
+                        const float Mn = fmaxf(M, m1);
+                        const float f0 = M == -INFINITY ? 0.0f : ex2_approx(M - Mn), f1 = ex2_approx(m1 - Mn);
+                        M = Mn;
+                        ls = ls * f0 + from[32 * 9] * f1;
+#pragma unroll
+                        for (int y = 0; y < 8; y++) o[y] = o[y] * f0 + from[32 * y] * f1;
+                    }
+                }
+                if (has && q < used) {
+                    const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+                    const int i = div_g(a, c.row0 + q), head = c.h * a.G + c.row0 + q - i * a.G;
+                    const int64_t at = (int64_t)(c.t0 + i) * a.Hq + head;
+                    *reinterpret_cast<uint4 *>(a.out + at * kD + ch) =
+                        make_uint4(T::pack(o[0] * inv, o[1] * inv), T::pack(o[2] * inv, o[3] * inv),
+                                   T::pack(o[4] * inv, o[5] * inv), T::pack(o[6] * inv, o[7] * inv));
+                    if (a.lse && ch == 0) a.lse[at] = lse_of(M - kShift, ls);
+                }
             }
+            named_barrier_sync(3, kRows);  // all records have been read
+            // the last CTA to come leaves both counters at 0 for the next call
+            if (tid == 0 && add_acq_rel_gpu(prm.tickets + kMaxCtas + c.p0, 1) == n - 1)
+                prm.tickets[c.p0] = prm.tickets[kMaxCtas + c.p0] = 0;
         }
     } else if (warp == H::kSoft) {
         // ================= copies of the pages =================
@@ -760,13 +799,17 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                     info.edge = j0 >= 0 && (edge(j0) || (j1 >= 0 && edge(j1)));
                     if (j0 >= 0) {
                         mbar_arrive_expect_tx(&sh.k_full[ks], (j1 >= 0 ? 2 : 1) * kPageBytes);
+                        if (kStep == 1) {
+                            tma_load_3d(sh.k[ks], &prm.tm_k, 0, (p0 * a.Hkv + w.h) * kPage, 0, &sh.k_full[ks]);
+                        } else {
 #pragma unroll
-                        for (int c = 0; c < 2; c++) {  // channel halves
-                            tma_load_3d(sh.k[ks] + c * 16384, &prm.tm_k, 0, (p0 * a.Hkv + w.h) * kPage, c,
-                                        &sh.k_full[ks]);
-                            if (j1 >= 0)
-                                tma_load_3d(sh.k[ks] + c * 16384 + 8192, &prm.tm_k, 0,
-                                            (p1 * a.Hkv + w.h) * kPage, c, &sh.k_full[ks]);
+                            for (int c = 0; c < 2; c++) {  // channel halves
+                                tma_load_3d(sh.k[ks] + c * 16384, &prm.tm_k, 0, (p0 * a.Hkv + w.h) * kPage, c,
+                                            &sh.k_full[ks]);
+                                if (j1 >= 0)
+                                    tma_load_3d(sh.k[ks] + c * 16384 + 8192, &prm.tm_k, 0,
+                                                (p1 * a.Hkv + w.h) * kPage, c, &sh.k_full[ks]);
+                            }
                         }
                     } else {
                         mbar_arrive(&sh.k_full[ks]);
@@ -796,7 +839,9 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 ahead = look(jb + 32 + lane);
                 for (uint32_t todo = __ballot_sync(0xffffffffu, page >= 0); todo && fine; todo &= todo - 1) {
                     const int k = __ffs(todo) - 1, p = __shfl_sync(0xffffffffu, page, k);
-                    if (held < 0) {
+                    if (kStep == 1) {
+                        fine = push(jb + k, p, -1, -1);
+                    } else if (held < 0) {
                         held = jb + k;
                         held_page = p;
                     } else {
@@ -845,11 +890,11 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 const uint32_t kd = tc_desc(k0 + ks * (kStep * kPageBytes));
                 if (issuer) {
                     if (pages && live) {
-                        const uint32_t idesc = pages == 2 ? kIdescS128 : kIdescS64;
+                        const uint32_t idesc = kStep == 2 && pages == 2 ? kIdescS128 : kIdescS64;
 #pragma unroll
                         for (int i = 0; i < 8; i++)  // 16 channels each
-                            tc_mma(d, qd + (i >> 2) * 1024 + (i & 3) * 2, kd + (i >> 2) * 1024 + (i & 3) * 2,
-                                   idesc, i > 0);
+                            tc_mma(d, qd + (i >> 2) * 1024 + (i & 3) * 2,
+                                   kd + (i >> 2) * (512 * kStep) + (i & 3) * 2, idesc, i > 0);
                     }
                     tc_commit(&sh.s_full[g][steps & 1]);
                     tc_commit(&sh.k_free[ks]);
@@ -859,7 +904,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             };
             uint32_t pstep = steps;  // the step whose values come next
             int cur = fine ? next_scores() : -1, nxt = 0;
-            if (H::kAhead == 2 && cur > 0) nxt = next_scores();
+            if (cur > 0) nxt = next_scores();  // two steps' scores are under way before the first P V
             bool add = false;
             while (cur > 0) {
                 fine = false;
@@ -894,13 +939,9 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 pstep++;
                 add = true;
                 fine = true;
-                if (H::kAhead == 2) {
-                    const int third = nxt > 0 ? next_scores() : nxt;
-                    cur = nxt;
-                    nxt = third;
-                } else {
-                    cur = next_scores();
-                }
+                const int third = nxt > 0 ? next_scores() : nxt;
+                cur = nxt;
+                nxt = third;
             }
             if (cur < 0) fine = false;
             if (fine) {  // the end's V place
@@ -992,10 +1033,21 @@ template <class T, int kTiles>
 cudaError_t launch(const Params &prm, const Plan &pl, cudaStream_t stream) {
     static int smem_set[kMaxDevicesTracked];
     constexpr int bytes = sizeof(Shared<kTiles>) + 1024;
-    const cudaError_t e = raise_smem_limit(tree_kernel<T, kTiles>, bytes, smem_set);
+    cudaError_t e = raise_smem_limit(tree_kernel<T, kTiles>, bytes, smem_set);
     if (e != cudaSuccess) return e;
-    tree_kernel<T, kTiles><<<pl.ctas, Shape<kTiles>::kThreads, bytes, stream>>>(prm);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = pl.ctas;
+    cfg.blockDim = Shape<kTiles>::kThreads;
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = stream;
+    // CTAs that share an item wait for each other's records: all of them must be resident
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, tree_kernel<T, kTiles>, prm);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
@@ -1008,7 +1060,7 @@ size_t tree_record_bytes(int tiles) {
 cudaError_t launch_tree_attention(const AttnArgs &a, const Plan &pl, int dtype, cudaStream_t stream) {
     Params prm;
     const uint64_t rows = (uint64_t)a.P * a.Hkv * kPage;
-    if (!page_map(&prm.tm_k, a.k, rows, dtype, 1) || !page_map(&prm.tm_v, a.v, rows, dtype, 2))
+    if (!page_map(&prm.tm_k, a.k, rows, dtype, pl.tiles == 1 ? 1 : 2) || !page_map(&prm.tm_v, a.v, rows, dtype, 2))
         return cudaErrorInvalidValue;
     prm.a = a;
     char *ws = reinterpret_cast<char *>(a.err);
