@@ -38,6 +38,8 @@ struct CommitArgs {
 struct AttnArgs {
     int B, Hq, Hkv, G, P, max_blocks, max_q, total_q, window;
     int lead;         // as in Plan
+    int tile_nodes, item_nodes;  // of a tile of 128 rows, of an item
+    int wide_out;     // out is aligned to 32 bytes
     uint32_t over_g;  // ceil(2^32 / G), too large by less than G / 2^32 of it (G > 1)
     int64_t q_stride;
     float factor;     // of scores, to log2 units

@@ -61,7 +61,7 @@ ffd_status check_params(const ffd_tree_params *p) {
     const int64_t pages = (int64_t)p->batch * p->num_kv_heads * ((int64_t)p->max_blocks_per_seq + kItemPages);
     const int64_t rows = (int64_t)p->max_q_len * (p->num_q_heads / p->num_kv_heads);
     if (rows > kMaxRows || pages > INT32_MAX ||
-        pages > INT32_MAX / ((rows + kTileRows - 1) / kTileRows))
+        pages > INT32_MAX / (rows / 64 + 1))  // a tile has more than 64 rows
         return FFD_ERR_UNSUPPORTED;
     return FFD_OK;
 }
@@ -76,9 +76,9 @@ constexpr int64_t kMinPages = 4;  // of a CTA, at least (upper bound from the ta
 ffd_status make_plan(const ffd_tree_params *p, Plan *pl) {
     const ffd_status st = check_params(p);
     if (st != FFD_OK) return st;
-    const int64_t rows = (int64_t)p->max_q_len * (p->num_q_heads / p->num_kv_heads);
-    pl->tiles = rows <= kTileRows ? 1 : 2;
-    const int64_t each = kTileRows * pl->tiles, groups = (rows + each - 1) / each;
+    const int64_t nodes = kTileRows / (p->num_q_heads / p->num_kv_heads);  // of a tile
+    pl->tiles = p->max_q_len <= nodes ? 1 : 2;
+    const int64_t groups = (p->max_q_len + pl->tiles * nodes - 1) / (pl->tiles * nodes);
     const int64_t items = (int64_t)p->batch * p->num_kv_heads * groups;
     const int sms = current_sm_count();
     int64_t ctas = p->num_splits;
@@ -219,6 +219,9 @@ ffd_status ffd_tree_attention(const ffd_tree_params *params, const void *q, cons
     a.window = p.window;
     a.q_stride = stride;
     a.lead = pl.lead;
+    a.tile_nodes = kTileRows / a.G;
+    a.item_nodes = a.tile_nodes * pl.tiles;
+    a.wide_out = aligned(out, 32);
     a.over_g = (uint32_t)(((uint64_t)1 << 32) / a.G + (((uint64_t)1 << 32) % a.G != 0));
     a.factor = fmaxf(p.sm_scale * 1.4426950408889634f, 1.2e-38f);  // never 0: times -inf it has to stay -inf
     a.q = static_cast<const uint16_t *>(q);

@@ -1,12 +1,12 @@
 // tree_attn.cu -- attention of a tree of drafted tokens over the 16-bit cache on the fifth-generation
 // tensor cores (ffd_tree_attention in ffd.h).
 //
-// The query rows of a (sequence, KV head), nq nodes x G heads, are taken kRows = 128 or 256 at a time: an
-// item is one such group of rows over the pages that any of them sees. The pages of all items,
-// concatenated with what each item costs besides, are cut into equal contiguous ranges, one per CTA (one per
-// SM). CTAs that share an item write their parts as records and, once all have come to their range's end, join
-// a part of its rows and channels each. In steps of one page (two tiles) or two pages (one tile) a CTA
-// computes for each tile of 128 rows
+// The query rows of a (sequence, KV head), nq nodes x G heads, are taken a tile of 128 / G whole nodes, or two
+// such tiles, at a time: an item is one such group of rows over the pages that any of them sees. The pages
+// of all items, concatenated with what each item costs besides, are cut into equal contiguous ranges, one
+// per CTA (one per SM). CTAs that share an item write their parts as records, and those in whose range it
+// does not begin join some of its channels each. In steps of one page (two tiles) or two pages (one tile) a
+// CTA computes for each tile of 128 rows
 //   S = Q K^T   (M 128, N 64 or 128, K 128; both operands in shared memory, S in tensor memory),
 //   P = 2^(S - m) in the inputs' type against a reference m that follows the row's maximum lazily: it is
 //       raised, and O rescaled, only when a score passes it by 2^8,
@@ -14,11 +14,12 @@
 // Both K and V lie in shared memory as the cache holds them, tokens by channels: K is read along its rows,
 // V across them.
 //
-// Roles: a copy warp lists the pages and fetches them (TMA), running on into the next item while this one
-// ends; one warp a tile issues its matrix instructions; four warps a tile do its softmax, a row a thread;
-// one warp looks through V where rows see different tokens: a token that some row does not see may hold
-// an infinity or a NaN, which a probability of 0 would not silence, so it is zeroed and the rows that do
-// see it are marked.
+// Roles: a copy warp goes through the CTA's range, describes each segment (a run of an item's pages) to the
+// others and fetches queries and pages (TMA), running on into the next segment while this one ends; for each
+// tile one warp issues the products for S, up to two steps ahead, and one those with V; four warps a tile do
+// its softmax, a row a thread; one warp looks through V where rows see different tokens: a token that some
+// row does not see may hold an infinity or a NaN, which a probability of 0 would not silence, so it is
+// zeroed and the rows that do see it are marked.
 #include "kv4_walk.cuh"
 #include "splitkv.cuh"
 #include "tree.cuh"
@@ -38,6 +39,7 @@ using kv4::lse_of;
 constexpr int kTile = 128;       // rows of a tile
 constexpr int kPageBytes = kPage * kD * 2;
 constexpr int kInfo = 8;         // steps whose pages are kept
+constexpr int kSegs = 8;         // segments that are kept: copies run at most six ahead of any reader
 constexpr int kSlots = 2;        // records of a CTA: of the item that goes on from before, and that goes on
 constexpr uint32_t kColO = 256;  // O of tile g at kColO + 128 g
 
@@ -53,12 +55,15 @@ struct Idesc<Bf16> {
 template <int kTiles>
 struct Shape {
     static constexpr int kRows = kTile * kTiles;
-    static constexpr int kSoft = 4 * kTiles;               // softmax warps
-    static constexpr int kThreads = 32 * (kSoft + 4);      // copy, two issuers, cleaner
-    static constexpr int kStep = kTiles == 1 ? 2 : 1;      // pages of a step
-    static constexpr int kNK = kTiles == 1 ? 3 : 4;        // steps' K in shared memory
-    static constexpr int kNV = 5;                          // pages' V
-    static constexpr int kRecord = 130 * kRows;            // floats of a joined item: o[128][row], m, l
+    static constexpr int kSoft = 4 * kTiles;                 // softmax warps; then
+    static constexpr int kCopy = kSoft, kScores = kCopy + 1; // copies, an issuer of S a tile,
+    static constexpr int kValues = kScores + kTiles;         // an issuer of P V a tile,
+    static constexpr int kClean = kValues + kTiles;          // V's infinities
+    static constexpr int kThreads = 32 * (kClean + 1);
+    static constexpr int kStep = kTiles == 1 ? 2 : 1;        // pages of a step
+    static constexpr int kNK = kTiles == 1 ? 3 : 4;          // steps' K in shared memory
+    static constexpr int kNV = 5;                            // pages' V
+    static constexpr int kRecord = 130 * kRows;              // floats of a record: o[128][row], m[row], l[row]
     // tensor memory columns of S (P over its first half): a tile has two places in turn
     static __device__ __forceinline__ uint32_t col_s(int g, uint32_t step) {
         return 64 * kStep * (2 * g + (step & 1));
@@ -70,10 +75,12 @@ struct Step {  // a step's pages: block indexes (first -1: the segment's end, se
     int edge;  // some row does not see all of it
 };
 
-struct Cut {  // an item that several CTAs share
-    int p0, p1;          // the CTAs, first and last
-    int row0, rows;      // its group's first row, rows of it (and of later groups)
-    int h, t0;
+struct Segment {  // pages 0: there is none any more
+    int pages, end;        // how many, and the token behind the last
+    int h, t0, nq, first;  // KV head, first node's row, nodes, tokens before the tree
+    int node0;             // the item's first node
+    int p0, p1;            // CTAs that share the item
+    int begins;            // whether the segment holds the item's first page
 };
 
 template <int kTiles>
@@ -84,25 +91,28 @@ struct Shared {
     uint8_t v[H::kNV][kPageBytes];              // the same for 64 tokens
     uint32_t bits[kMaxNodes / 32][H::kRows];    // nodes that a row sees
     int parent[kTiles][kMaxNodes];
+    uint64_t seg_full[kSegs];
     uint64_t k_full[H::kNK], k_free[H::kNK];
     uint64_t v_full[H::kNV], v_ready[H::kNV], v_free[H::kNV];
-    uint64_t q_full[kTiles], s_full[kTiles][2], p_full[kTiles][2], o_done[kTiles], drain[kTiles];
+    uint64_t q_full, q_free, joined;
+    uint64_t s_full[kTiles][2], p_full[kTiles][2], o_done[kTiles][2], drain[2 * kTiles];
     uint64_t bad[H::kNV];                       // tokens of a page whose V is not finite
     Step info[kInfo];
+    Segment seg[kSegs];
     uint32_t tmem, aborted;
     int scan[H::kThreads / 32];
     int pre[H::kThreads];                       // weight of all items before each chunk of sequences
-    Cut cut[2];                                 // the first item, if it began before, and the last, if it goes on
+    Segment shared_item;                        // the item that began before this CTA's range (pages 0: none)
 };
 
 struct Params {
-    CUtensorMap tm_k, tm_v;
+    CUtensorMap tm_q, tm_k, tm_v;
     AttnArgs a;
     float *records;
     int *tickets;
 };
 
-// x / G for 0 <= x < 2^29.
+// x / G for a row x of a tile.
 __device__ __forceinline__ int div_g(const AttnArgs &a, int x) {
     return a.G == 1 ? x : (int)__umulhi((uint32_t)x, a.over_g);
 }
@@ -131,36 +141,31 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, bool report) {
     return s;
 }
 
-template <int kRows>
 __device__ __forceinline__ int item_groups(const AttnArgs &a, const Seq &s) {
-    return (s.nq * a.G + kRows - 1) / kRows;
+    return (s.nq + a.item_nodes - 1) / a.item_nodes;
 }
 
 // Positions of an item's rows: at least lo, at most hi. A node's position is not known here; its
 // index bounds its depth.
-template <int kRows>
 __device__ __forceinline__ void item_span(const AttnArgs &a, const Seq &s, int rt, int &lo, int &hi) {
-    const int rows = s.nq * a.G;
-    const int r1 = (rt + 1) * kRows < rows ? (rt + 1) * kRows : rows;
-    lo = s.first() + (a.parents ? 0 : div_g(a, rt * kRows));
-    hi = s.first() + div_g(a, r1 - 1);
+    const int i0 = rt * a.item_nodes, i1 = i0 + a.item_nodes;
+    lo = s.first() + (a.parents ? 0 : i0);
+    hi = s.first() + (i1 < s.nq ? i1 : s.nq) - 1;
 }
 
 // Pages that the rows of item group rt of a sequence see: the first, and how many.
-template <int kRows>
 __device__ __forceinline__ void item_pages(const AttnArgs &a, const Seq &s, int rt, int &fp, int &np) {
     int lo, hi;
-    item_span<kRows>(a, s, rt, lo, hi);
+    item_span(a, s, rt, lo, hi);
     fp = a.window > 0 && lo >= a.window ? (lo - a.window + 1) >> 6 : 0;
     np = hi < 0 ? 0 : (hi >> 6) - fp + 1;
 }
 
 // What one item weighs: `lead` before its first page and one for each; 0 behind the last one.
-template <int kRows>
-__device__ __forceinline__ int item_weight(const AttnArgs &a, const Seq &s, int rt) {
-    if (rt >= item_groups<kRows>(a, s)) return 0;
+__device__ __forceinline__ int item_weight(const AttnArgs &a, const Seq &s, int rt, int groups) {
+    if (rt >= groups) return 0;
     int fp, np;
-    item_pages<kRows>(a, s, rt, fp, np);
+    item_pages(a, s, rt, fp, np);
     return np > 0 ? np + a.lead : 0;
 }
 
@@ -174,46 +179,30 @@ __device__ __forceinline__ int lane_scan(int v, int lane) {  // sum over the lan
 }
 
 // One head's items of a sequence, weighed by a warp.
-template <int kRows>
 __device__ __forceinline__ int head_weight(const AttnArgs &a, const Seq &s, int lane) {
     int sum = 0;
-    for (int rt = 0; rt < item_groups<kRows>(a, s); rt += 32) sum += item_weight<kRows>(a, s, rt + lane);
+    const int groups = item_groups(a, s);
+    for (int rt = 0; rt < groups; rt += 32) sum += item_weight(a, s, rt + lane, groups);
     return __reduce_add_sync(0xffffffffu, sum);
 }
 
-// A CTA's way through its range of weight [c0, c1): one segment (a run of an item's pages) after another.
-template <int kRows>
-struct Walk {
-    int x, c1;              // where the segment begins in the cut's scale, the range's end
-    int b, h, rt, into;     // sequence, KV head, group of rows; weight of the item before x
-    Seq s;
-    int fp, np, item;       // the item's pages; its first page in the cut's scale
-    int at, cnt;            // the segment's pages: at .. at + cnt - 1 of the item's
+// Rows that a channel has in a record of an item that is `left` nodes from its sequence's end: both tiles'
+// places up to the last row, in 16 bytes.
+__device__ __forceinline__ int record_rows(const AttnArgs &a, int left) {
+    const int more = left - a.tile_nodes;
+    const int used = more <= 0 || a.item_nodes == a.tile_nodes
+                         ? min(left, a.tile_nodes) * a.G : kTile + min(more, a.tile_nodes) * a.G;
+    return (used + 3) & ~3;
+}
 
-    // The segment at x; false at the range's end.
-    __device__ __forceinline__ bool segment(const AttnArgs &a) {
-        if (x >= c1) return false;
-        item_pages<kRows>(a, s, rt, fp, np);
-        item = x - into + a.lead;
-        at = into > a.lead ? into - a.lead : 0;
-        cnt = (np < c1 - item ? np : c1 - item) - at;
-        return cnt > 0;  // else the item's pages are the next CTA's
-    }
-    __device__ __forceinline__ void next(const AttnArgs &a) {
-        x = item + at + cnt;
-        into = 0;
-        if (x >= c1) return;
-        do {
-            if (++rt >= item_groups<kRows>(a, s)) {
-                rt = 0;
-                if (++h >= a.Hkv) {
-                    h = 0;
-                    do s = seq_of(a, ++b, false);
-                    while (s.nq == 0);
-                }
-            }
-            item_pages<kRows>(a, s, rt, fp, np);
-        } while (np == 0);
+// The weights cut into ncta ranges, the first `more` of them longer by one.
+struct Ranges {
+    int each, more;
+    __device__ __forceinline__ Ranges(int total, int ncta) : each(total / ncta), more(total % ncta) {}
+    __device__ __forceinline__ int begin(int cta) const { return cta * each + (cta < more ? cta : more); }
+    __device__ __forceinline__ int owner(int x) const {  // the CTA whose range holds x
+        const int split = more * (each + 1);
+        return x < split ? x / (each + 1) : more + (x - split) / each;
     }
 };
 
@@ -223,7 +212,7 @@ __device__ __forceinline__ bool stopped(const S &sh) {
     return *reinterpret_cast<const volatile uint32_t *>(&sh.aborted) != 0;
 }
 template <class S>
-__device__ __forceinline__ bool wait_long(const AttnArgs &a, S &sh, uint64_t *bar, uint32_t parity) {
+__device__ __noinline__ bool wait_long(const AttnArgs &a, S &sh, uint64_t *bar, uint32_t parity) {
     const uint64_t t0 = globaltimer_ns();
     while (!mbar_try_wait(bar, parity)) {
         if (stopped(sh)) return false;
@@ -254,9 +243,6 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     using H = Shape<kTiles>;
     constexpr int kRows = H::kRows, kThreads = H::kThreads, kCtaWarps = kThreads / 32;
     constexpr int kStep = H::kStep;
-    constexpr uint32_t kIdescS128 = tc_idesc_f16(128, 128) | Idesc<T>::kType;
-    constexpr uint32_t kIdescS64 = tc_idesc_f16(128, 64) | Idesc<T>::kType;
-    constexpr uint32_t kIdescO = tc_idesc_f16(128, 128) | Idesc<T>::kType | kTcBMn;
     extern __shared__ uint8_t raw[];
     using Sh = Shared<kTiles>;
     Sh &sh = *reinterpret_cast<Sh *>(align_shared<1024>(raw));
@@ -266,9 +252,10 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
 
     __syncwarp();
     if (warp == 0) tmem_alloc(&sh.tmem, 512);
-    if (tid == 0) {
+    if (tid == 32) {
         sh.aborted = 0;
-        sh.cut[0].p0 = sh.cut[1].p0 = -1;
+        sh.shared_item.pages = 0;
+        for (int i = 0; i < kSegs; i++) mbar_init(&sh.seg_full[i], 1);
         for (int i = 0; i < H::kNK; i++) {
             mbar_init(&sh.k_full[i], 1);
             mbar_init(&sh.k_free[i], kTiles);
@@ -278,15 +265,17 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             mbar_init(&sh.v_ready[i], 1);
             mbar_init(&sh.v_free[i], kTiles);
         }
+        mbar_init(&sh.q_full, 1);
+        mbar_init(&sh.q_free, kTiles);
+        mbar_init(&sh.joined, 1);
         for (int g = 0; g < kTiles; g++) {
-            mbar_init(&sh.q_full[g], 4);
             for (int j = 0; j < 2; j++) {
                 mbar_init(&sh.s_full[g][j], 1);
                 mbar_init(&sh.p_full[g][j], 4);
+                mbar_init(&sh.o_done[g][j], 1);
             }
-            mbar_init(&sh.o_done[g], 1);
-            mbar_init(&sh.drain[g], 1);
         }
+        for (int g = 0; g < 2 * kTiles; g++) mbar_init(&sh.drain[g], 1);
         fence_barrier_init();
     }
     // ---- weight of the items before each chunk of sequences: a warp for each of a few, else a thread
@@ -295,17 +284,20 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     int own = 0;
     bool empty = false;  // some sequence's rows see nothing
     if (few) {
+#pragma unroll 1
         for (int b = warp; b < a.B; b += kCtaWarps) {
             const Seq s = seq_of(a, b, blockIdx.x == 0 && lane == 0);
-            const int w = head_weight<kRows>(a, s, lane);
+            const int w = head_weight(a, s, lane);
             if (lane == 0) sh.pre[b] = w * a.Hkv;
             empty |= s.n == 0 && s.nq > 0;
         }
     } else {
+#pragma unroll 1
         for (int b = tid * chunk; b < (tid + 1) * chunk && b < a.B; b++) {
             const Seq s = seq_of(a, b, blockIdx.x == 0);
             int w = 0;
-            for (int rt = 0; rt < item_groups<kRows>(a, s); rt++) w += item_weight<kRows>(a, s, rt);
+            const int groups = item_groups(a, s);
+            for (int rt = 0; rt < groups; rt++) w += item_weight(a, s, rt, groups);
             own += w * a.Hkv;
             empty |= s.n == 0 && s.nq > 0;
         }
@@ -324,11 +316,12 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             const int b = u / a.Hkv, h = u - b * a.Hkv;
             const Seq s = seq_of(a, b, false);
             if (s.n > 0) continue;
-            for (int k = tid; k < s.nq * a.G * 16; k += kThreads) {
-                const int r = k >> 4, i = div_g(a, r);
-                const int64_t at = (int64_t)(s.t0 + i) * a.Hq + h * a.G + r - i * a.G;
-                reinterpret_cast<uint4 *>(a.out + at * kD)[k & 15] = make_uint4(0, 0, 0, 0);
-                if (a.lse && (k & 15) == 0) a.lse[at] = -INFINITY;
+            for (int i = tid >> 4; i < s.nq; i += kThreads / 16) {  // 16 threads a node
+                const int64_t at = (int64_t)(s.t0 + i) * a.Hq + h * a.G;
+                for (int g = 0; g < a.G; g++) {
+                    reinterpret_cast<uint4 *>(a.out + (at + g) * kD)[tid & 15] = make_uint4(0, 0, 0, 0);
+                    if (a.lse && (tid & 15) == 0) a.lse[at + g] = -INFINITY;
+                }
             }
         }
     }
@@ -336,94 +329,42 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    const uint32_t tmem = sh.tmem;
     if (cta >= ncta) {
         __syncwarp();
-        if (warp == 0) tmem_free(sh.tmem, 512);
+        if (warp == 0) tmem_free(tmem, 512);
         return;
-    }
-    const uint32_t tmem = sh.tmem;
-    Walk<kRows> w;
-    w.x = (int)((int64_t)total * cta / ncta);
-    w.c1 = (int)((int64_t)total * (cta + 1) / ncta);
-    {   // ---- where the range begins
-        int lo = 0, hi = kThreads;  // the last chunk of sequences that begins at or before x
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (sh.pre[mid] <= w.x) lo = mid;
-            else hi = mid;
-        }
-        int rem = w.x - sh.pre[lo], hp = 1;
-        for (w.b = lo * chunk; w.b < a.B; w.b++) {
-            w.s = seq_of(a, w.b, false);
-            hp = head_weight<kRows>(a, w.s, lane);
-            if (rem < hp * a.Hkv) break;
-            rem -= hp * a.Hkv;
-        }
-        w.h = rem / hp;
-        rem -= w.h * hp;
-        for (w.rt = 0;; w.rt += 32) {  // 32 items at a time
-            const int wt = item_weight<kRows>(a, w.s, w.rt + lane), sum = lane_scan(wt, lane);
-            const uint32_t past = __ballot_sync(0xffffffffu, sum > rem);
-            if (past) {
-                const int k = __ffs(past) - 1;
-                rem -= __shfl_sync(0xffffffffu, sum - wt, k);
-                w.rt += k;
-                break;
-            }
-            rem -= __shfl_sync(0xffffffffu, sum, 31);
-        }
-        w.into = rem;
     }
 
     uint32_t steps = 0, vsteps = 0, turns = 0;  // so far: steps and V pages (ends among them), P V products
+    uint32_t segs = 0;
+    // The next segment's description; null at the range's end or when the CTA has stopped.
+    auto next_segment = [&]() -> const Segment * {
+        const uint32_t at = segs % kSegs, parity = (segs / kSegs) & 1;
+        segs++;
+        if (!waited(a, sh, &sh.seg_full[at], parity)) return nullptr;
+        return sh.seg[at].pages > 0 ? &sh.seg[at] : nullptr;
+    };
     if (warp < H::kSoft) {
         // ================= softmax of tile grp, one row a thread =================
         const int grp = warp >> 2, r = tid & (kTile - 1);
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const uint32_t to = tmem + lanes + kColO + grp * 128;
+        const int rn = div_g(a, r), rg = r - rn * a.G;  // the row's node in the tile, and head
         const float fs = a.factor;
-        bool run = true;  // once a wait has run out, only the tickets are still taken
-        for (; w.segment(a); w.next(a)) {
-            const Seq s = w.s;
-            const int h = w.h, first = s.first();
-            const int row0 = w.rt * kRows, rows = s.nq * a.G - row0;  // rows: of this item and later
-            const bool active = grp == 0 || rows > kTile;
-            const bool begins = w.at == 0, complete = begins && w.cnt == w.np;
-            const int rr = row0 + grp * kTile + r, qi = div_g(a, rr);
-            const bool have = qi < s.nq;
-            // ---- queries, half a warp a row (the last item's scores have all been formed)
-            if (active && run) {
-                const int j = lane & 15;  // channels 8 j .. 8 j + 7
-#pragma unroll
-                for (int k0 = 0; k0 < 16; k0 += 8) {
-                    uint4 got[8];
-#pragma unroll
-                    for (int k = 0; k < 8; k++) {
-                        const int tr = 32 * (warp & 3) + 2 * (k0 + k) + (lane >> 4);
-                        const int row = row0 + grp * kTile + tr, i = div_g(a, row);
-                        got[k] = make_uint4(0, 0, 0, 0);
-                        if (i < s.nq)
-                            got[k] = __ldg(reinterpret_cast<const uint4 *>(
-                                               a.q + (int64_t)(s.t0 + i) * a.q_stride +
-                                               (h * a.G + row - i * a.G) * kD) + j);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 8; k++) {
-                        const int tr = 32 * (warp & 3) + 2 * (k0 + k) + (lane >> 4);
-                        *reinterpret_cast<uint4 *>(sh.q[grp] + (j >> 3) * 16384 + tr * 128 +
-                                                   (((j & 7) ^ (tr & 7)) << 4)) = got[k];
-                    }
-                }
-            }
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.q_full[grp]);
+        while (true) {
+            const Segment *sg = next_segment();
+            if (named_barrier_or(3, kRows, sg == nullptr)) break;
+            const int first = sg->first, nq = sg->nq, node0 = sg->node0, t0 = sg->t0;
+            const bool active = grp == 0 || nq - node0 > a.tile_nodes;
+            const bool complete = sg->p0 == sg->p1;
+            const int qi = node0 + grp * a.tile_nodes + rn;
+            const bool have = rn < a.tile_nodes && qi < nq;
             // ---- the nodes that the row sees, and its position
             int pos = first + qi;
-            const bool treed = a.parents && (w.fp + w.at + w.cnt) * kPage > first;
-            if (run && a.parents && (treed || a.window > 0)) {
-                for (int i = r; i < s.nq; i += kTile) {
-                    int p = __ldg(a.parents + s.t0 + i);
+            if (a.parents && (sg->end > first || a.window > 0)) {
+                for (int i = r; i < nq; i += kTile) {
+                    int p = __ldg(a.parents + t0 + i);
                     if (p < -1 || p >= i) {
                         raise_error(a.err, FFD_ERRBIT_BOUNDS);
                         p = -1;
@@ -452,10 +393,10 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             const int from = a.window > 0 ? pos - a.window : -1;
             // Tokens of page j that the row sees.
             auto visible = [&](int j) -> uint64_t {
-                const int t0 = 64 * j;
-                if (!a.parents) return upto(pos - t0) & ~upto(from - t0);
-                uint64_t see = upto(first - 1 - t0) & ~upto(from - t0);
-                const int x = t0 - first;  // the page's first token as a node
+                const int t = 64 * j;
+                if (!a.parents) return upto(pos - t) & ~upto(from - t);
+                uint64_t see = upto(first - 1 - t) & ~upto(from - t);
+                const int x = t - first;  // the page's first token as a node
                 if (x + 63 >= 0) {
                     // nodes x .. x + 63: three words
                     const int k = x >> 5;
@@ -470,7 +411,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
 
             float m = -INFINITY, limit = -INFINITY, l = 0.0f;  // limit: a larger score raises m
             bool any = false, far = false, tainted = false;
-            while (run) {
+            while (true) {
                 const uint32_t buf = steps & 1;
                 if (!waited(a, sh, &sh.s_full[grp][buf], (steps >> 1) & 1)) break;
                 tc_fence_after();
@@ -535,7 +476,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                         far = __any_sync(0xffffffffu, is_far(m));
                         if (any) {
                             // the last step's P V (a stop is met at the next wait)
-                            waited(a, sh, &sh.o_done[grp], (turns - 1) & 1);
+                            waited(a, sh, &sh.o_done[grp][(turns - 1) & 1], ((turns - 1) >> 1) & 1);
                             __syncwarp();
                             tc_fence_after();
 #pragma unroll 1
@@ -598,17 +539,18 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 if (lane == 0) mbar_arrive(&sh.p_full[grp][buf]);
             }
             if (any) {  // the last step's P V
-                waited(a, sh, &sh.o_done[grp], (turns - 1) & 1);
+                waited(a, sh, &sh.o_done[grp][(turns - 1) & 1], ((turns - 1) >> 1) & 1);
                 tc_fence_after();
             }
-            run = !named_barrier_or(3, kRows, !run || stopped(sh));
+            if (named_barrier_or(3, kRows, stopped(sh))) break;
 
-            // ---- the segment's results (a whole item's rows by way of the tile's queries, which are
-            // read no more, so that lines of out are written whole)
-            if (active && run) {
+            // ---- the segment's results
+            const int begins = sg->begins;
+            if (active) {
                 const float inv = tainted ? NAN : l == 0.0f ? 0.0f : 1.0f / l;
+                const int pad = record_rows(a, nq - node0);
                 float *row = prm.records + (int64_t)(kSlots * cta + begins) * H::kRecord + grp * kTile + r;
-                uint8_t *stage = sh.q[grp];
+                const int64_t at = (int64_t)(t0 + qi) * a.Hq + sg->h * a.G + rg;
 #pragma unroll 1
                 for (int c = 0; c < 4; c++) {
                     uint32_t o[32];
@@ -620,160 +562,220 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 32; e++) o[e] = 0;
                     }
+                    if (!have) continue;
                     if (complete) {
 #pragma unroll
-                        for (int e = 0; e < 4; e++) {
-                            uint32_t y[4];
+                        for (int e = 0; e < 2; e++) {
+                            uint32_t y[8];
 #pragma unroll
-                            for (int k = 0; k < 4; k++)
-                                y[k] = T::pack(__uint_as_float(o[8 * e + 2 * k]) * inv,
-                                               __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
-                            *reinterpret_cast<uint4 *>(stage + r * 256 + (((4 * c + e) ^ (r & 7)) << 4)) =
-                                make_uint4(y[0], y[1], y[2], y[3]);
+                            for (int k = 0; k < 8; k++)
+                                y[k] = T::pack(__uint_as_float(o[16 * e + 2 * k]) * inv,
+                                               __uint_as_float(o[16 * e + 2 * k + 1]) * inv);
+                            uint16_t *dst = a.out + at * kD + 32 * c + 16 * e;
+                            if (a.wide_out) {
+                                store_32b(dst, y);
+                            } else {
+                                reinterpret_cast<uint4 *>(dst)[0] = make_uint4(y[0], y[1], y[2], y[3]);
+                                reinterpret_cast<uint4 *>(dst)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+                            }
                         }
-                    } else if (have) {
+                    } else {
 #pragma unroll
                         for (int e = 0; e < 32; e++)
-                            row[(32 * c + e) * kRows] = tainted ? NAN : __uint_as_float(o[e]);
+                            row[(32 * c + e) * pad] = tainted ? NAN : __uint_as_float(o[e]);
                     }
-                }
-                if (complete) {
-                    __syncwarp();
-#pragma unroll 4
-                    for (int k = 0; k < 16; k++) {
-                        const int q = 32 * (warp & 3) + 2 * k + (lane >> 4), c = lane & 15;
-                        const int i = div_g(a, row0 + grp * kTile + q);
-                        if (i < s.nq)
-                            *reinterpret_cast<uint4 *>(
-                                a.out + ((int64_t)(s.t0 + i) * a.Hq + h * a.G + row0 + grp * kTile + q -
-                                         i * a.G) * kD + 8 * c) =
-                                *reinterpret_cast<const uint4 *>(stage + q * 256 + ((c ^ (q & 7)) << 4));
-                    }
-                    __syncwarp();
                 }
                 if (have) {
-                    if (!complete) row[128 * kRows] = m, row[129 * kRows] = l;
-                    else if (a.lse)
-                        a.lse[(int64_t)(s.t0 + qi) * a.Hq + h * a.G + rr - qi * a.G] = lse_of(m - kShift, l);
+                    if (!complete) row[128 * pad] = m, row[129 * pad] = l;
+                    else if (a.lse) a.lse[at] = lse_of(m - kShift, l);
                 }
             }
             if (!complete) {  // joined below
-                const int p0 = (int)(((int64_t)(w.item + 1) * ncta - 1) / total);
-                const int p1 = (int)(((int64_t)(w.item + w.np) * ncta - 1) / total);
-                if (tid == 0) sh.cut[begins] = Cut{p0, p1, row0, rows, h, s.t0};
+                fence_proxy_async_all();  // the records are read by bulk copies
+                if (tid == 0 && !begins) sh.shared_item = *sg;
                 named_barrier_sync(3, kRows);
-                if (tid == 0) add_acq_rel_gpu(prm.tickets + p0, 1);
+                if (tid == 0) add_acq_rel_gpu(prm.tickets + sg->p0, 1);
             }
         }
-        // ---- items that several CTAs share: all of them join a part of the rows and channels each
-        named_barrier_sync(3, kRows);
-#pragma unroll 1
-        for (int e = 0; e < 2; e++) {
-            const Cut c = sh.cut[e];
-            if (c.p0 < 0) continue;
-            const int n = c.p1 - c.p0 + 1, place = cta - c.p0;
+        // ---- the item that began before this CTA's range: joined by the CTAs that have such a part
+        if (!named_barrier_or(3, kRows, stopped(sh)) && sh.shared_item.pages > 0) {
+            const Segment &c = sh.shared_item;
+            const int n = c.p1 - c.p0 + 1, place = cta - c.p0 - 1, of = n - 1;
+            // channels by eights, of many CTAs by twos: at most eight of them then
+            const int unit = of <= 16 ? 8 : 2, units = kD / unit;
+            const int ch0 = units * place / of * unit, chs = units * (place + 1) / of * unit - ch0;
+            const int pad = record_rows(a, c.nq - c.node0);
+            float *buf = reinterpret_cast<float *>(sh.q[0]);
+            constexpr int kRoom = (sizeof(sh.q) + sizeof(sh.k) + sizeof(sh.v)) / 4;
+            // Channels that are joined together: as many of this CTA's as have room with all records, in
+            // eights; eight at least, in several rounds of records where need be.
+            const int most = (kRoom / (n * pad) - 2) & ~7;
+            const int block = min(chs, most < 8 ? 8 : most);
+            const int once = min(n, kRoom / ((block + 2) * pad));
             if (tid == 0) {
                 const uint64_t t0 = globaltimer_ns();
                 bool ok = true;
                 while (ok && ld_acquire_gpu(prm.tickets + c.p0) < n) ok = globaltimer_ns() - t0 <= a.wait_ns;
-                if (!ok) raise_error(a.err, FFD_ERRBIT_TIMEOUT);
+                if (!ok) {
+                    raise_error(a.err, FFD_ERRBIT_TIMEOUT);
+                    *reinterpret_cast<volatile uint32_t *>(&sh.aborted) = 1;
+                } else if (atomicAdd(prm.tickets + kMaxCtas + c.p0, 1) == of - 1) {
+                    // nobody waits any more: both counters are left at 0 for the next call
+                    prm.tickets[c.p0] = prm.tickets[kMaxCtas + c.p0] = 0;
+                }
             }
-            named_barrier_sync(3, kRows);
-            const int used = c.rows < kRows ? c.rows : kRows;
-            // a unit is 32 rows, one a lane, and 8 channels; `split` warps share one unit's records
-            const int units = 16 * ((used + 31) / 32);
-            const int mine = units > place ? (units - place + n - 1) / n : 0;  // units place, place + n, ...
-            int split = 1;
-            while (2 * split * mine <= H::kSoft && 2 * split <= n) split *= 2;
-            const int teams = H::kSoft / split, team = warp / split, part = warp % split;
+            const bool run = !named_barrier_or(3, kRows, stopped(sh));
+            const int i = c.node0 + grp * a.tile_nodes + rn;
+            const bool have = rn < a.tile_nodes && i < c.nq;
+            const int64_t at = (int64_t)(c.t0 + i) * a.Hq + c.h * a.G + rg;
+            uint32_t rounds = 0;
 #pragma unroll 1
-            for (int u0 = 0; u0 < mine; u0 += teams) {
-                const int unit = place + (u0 + team) * n;
-                const bool has = u0 + team < mine;
-                const int q = 32 * (unit >> 4) + lane, ch = 8 * (unit & 15);
+            for (int b0 = 0; run && b0 < chs; b0 += block) {
+                const int width = min(block, chs - b0), rec = (width + 2) * pad;  // rec: a record's floats
                 float M = -INFINITY, ls = 0.0f, o[8] = {};
-                // the loads of five records together
-                for (int i0 = part; has && i0 < n; i0 += 5 * split) {
-                    float v[5][8], mn[5], ln[5];
+                auto write = [&](int x0) {
+                    const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+                    uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + at * kD + ch0 + b0 + x0);
+                    const uint32_t y[4] = {T::pack(o[0] * inv, o[1] * inv), T::pack(o[2] * inv, o[3] * inv),
+                                           T::pack(o[4] * inv, o[5] * inv), T::pack(o[6] * inv, o[7] * inv)};
+                    if (unit == 8) {
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 5; i++) {
-                        const bool in = i0 + i * split < n;
-                        const int r = in ? i0 + i * split : i0;
-                        // a CTA's record: its second one where the item begins, else its first
-                        const float *src =
-                            prm.records + (int64_t)(kSlots * (c.p0 + r) + (r == 0)) * H::kRecord + q;
-#pragma unroll
-                        for (int k = 0; k < 8; k++) v[i][k] = __ldcg(src + (ch + k) * kRows);
-                        mn[i] = in ? __ldcg(src + 128 * kRows) : -INFINITY;
-                        ln[i] = __ldcg(src + 129 * kRows);
+                        for (int k = 0; k < 4; k++)
+                            if (2 * k < width) dst[k] = y[k];
                     }
+                };
+#pragma unroll 1
+                for (int r0 = 0; r0 < n; r0 += once) {
+                    const int count = min(once, n - r0);
+                    fence_proxy_async();
+                    named_barrier_sync(3, kRows);  // the space has been read
+                    if (warp == 0) {
+                        if (lane == 0) mbar_arrive_expect_tx(&sh.joined, count * rec * 4);
+                        __syncwarp();
+                        fence_proxy_async_all();
+#pragma unroll 1
+                        for (int k = lane; k < count; k += 32) {
+                            const int p = r0 + k;
+                            const float *src =  // a CTA's second record where the item begins, else its first
+                                prm.records + (int64_t)(kSlots * (c.p0 + p) + (p == 0)) * H::kRecord;
+                            tma_load_1d(buf + k * rec, src + (ch0 + b0) * pad, width * pad * 4, &sh.joined);
+                            tma_load_1d(buf + k * rec + width * pad, src + kD * pad, 2 * pad * 4, &sh.joined);
+                        }
+                    }
+                    if (!mbar_drain(&sh.joined, rounds & 1, drain_bound_ns(a.wait_ns)))
+                        raise_error(a.err, FFD_ERRBIT_TIMEOUT);
+                    rounds++;
+                    if (!have) continue;
+                    const float *mine = buf + grp * kTile + r, *ms = mine + width * pad;
                     float Mn = M;
-#pragma unroll
-                    for (int i = 0; i < 5; i++) Mn = fmaxf(Mn, mn[i]);
+#pragma unroll 4
+                    for (int k = 0; k < count; k++) Mn = fmaxf(Mn, ms[k * rec]);
                     const float al = M == -INFINITY ? 0.0f : ex2_approx(M - Mn);
                     M = Mn;
                     ls *= al;
+                    const float ref = M == -INFINITY ? 0.0f : M;  // nothing in any: o and l are 0
+#pragma unroll 1
+                    for (int x0 = 0; x0 < width; x0 += 8) {
 #pragma unroll
-                    for (int k = 0; k < 8; k++) o[k] *= al;
+                        for (int x = 0; x < 8; x++) o[x] = r0 == 0 ? 0.0f : o[x] * al;
+#pragma unroll 2
+                        for (int k = 0; k < count; k++) {
+                            const float f = ex2_approx(ms[k * rec] - ref);
+                            if (x0 == 0) ls = fmaf(f, ms[k * rec + pad], ls);
+                            if (f == 0.0f) continue;  // of an empty record, o may hold anything but is 0
 #pragma unroll
-                    for (int i = 0; i < 5; i++) {
-                        if (mn[i] == -INFINITY) continue;  // nothing in it: o and l are 0
-                        const float f = ex2_approx(mn[i] - M);
-                        ls = fmaf(f, ln[i], ls);
-#pragma unroll
-                        for (int k = 0; k < 8; k++) o[k] = fmaf(f, v[i][k], o[k]);
+                            for (int x = 0; x < 8; x++)
+                                if (x0 + x < width) o[x] = fmaf(f, mine[k * rec + (x0 + x) * pad], o[x]);
+                        }
+                        if (width > 8) write(x0);  // one round then
                     }
                 }
-                if (split > 1) {  // the warps' parts, through the space of the queries (one round of units)
-                    float *mem = reinterpret_cast<float *>(sh.q[0]) + 32 * 10 * warp + lane;
-                    named_barrier_sync(3, kRows);
-#pragma unroll
-                    for (int k = 0; k < 8; k++) mem[32 * k] = o[k];
-                    mem[32 * 8] = M;
-                    mem[32 * 9] = ls;
-                    named_barrier_sync(3, kRows);
-                    if (part > 0) continue;
-                    for (int k = 1; k < split; k++) {
-                        const float *from = mem + 32 * 10 * k;
-                        const float m1 = from[32 * 8];
-                        if (m1 == -INFINITY) continue;
-                        const float Mn = fmaxf(M, m1);
-                        const float f0 = M == -INFINITY ? 0.0f : ex2_approx(M - Mn), f1 = ex2_approx(m1 - Mn);
-                        M = Mn;
-                        ls = ls * f0 + from[32 * 9] * f1;
-#pragma unroll
-                        for (int y = 0; y < 8; y++) o[y] = o[y] * f0 + from[32 * y] * f1;
-                    }
-                }
-                if (has && q < used) {
-                    const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
-                    const int i = div_g(a, c.row0 + q), head = c.h * a.G + c.row0 + q - i * a.G;
-                    const int64_t at = (int64_t)(c.t0 + i) * a.Hq + head;
-                    *reinterpret_cast<uint4 *>(a.out + at * kD + ch) =
-                        make_uint4(T::pack(o[0] * inv, o[1] * inv), T::pack(o[2] * inv, o[3] * inv),
-                                   T::pack(o[4] * inv, o[5] * inv), T::pack(o[6] * inv, o[7] * inv));
-                    if (a.lse && ch == 0) a.lse[at] = lse_of(M - kShift, ls);
-                }
+                if (have && width <= 8) write(0);
+                if (have && a.lse && ch0 + b0 == 0) a.lse[at] = lse_of(M - kShift, ls);
             }
-            named_barrier_sync(3, kRows);  // all records have been read
-            // the last CTA to come leaves both counters at 0 for the next call
-            if (tid == 0 && add_acq_rel_gpu(prm.tickets + kMaxCtas + c.p0, 1) == n - 1)
-                prm.tickets[c.p0] = prm.tickets[kMaxCtas + c.p0] = 0;
         }
-    } else if (warp == H::kSoft) {
-        // ================= copies of the pages =================
+    } else if (warp == H::kCopy) {
+        // ================= the range's segments, copies of their queries and pages =================
         if (lane == 0) {
+            prefetch_tensormap(&prm.tm_q);
             prefetch_tensormap(&prm.tm_k);
             prefetch_tensormap(&prm.tm_v);
         }
+        const Ranges ranges(total, ncta);
+        int x = ranges.begin(cta), b, h, rt, into;
+        const int c1 = ranges.begin(cta + 1);
+        Seq s = {0, 0, 0};
+        {   // where the range begins: sequence b, head h, group rt, `into` the item's weight
+            int lo = 0, hi = kThreads;  // the last chunk of sequences that begins at or before x
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (sh.pre[mid] <= x) lo = mid;
+                else hi = mid;
+            }
+            int rem = x - sh.pre[lo], hp = 1;
+#pragma unroll 1
+            for (b = lo * chunk; b < a.B; b++) {
+                s = seq_of(a, b, false);
+                hp = head_weight(a, s, lane);
+                if (rem < hp * a.Hkv) break;
+                rem -= hp * a.Hkv;
+            }
+            h = rem / hp;
+            rem -= h * hp;
+            const int groups = item_groups(a, s);
+#pragma unroll 1
+            for (rt = 0;; rt += 32) {  // 32 items at a time
+                const int wt = item_weight(a, s, rt + lane, groups), sum = lane_scan(wt, lane);
+                const uint32_t past = __ballot_sync(0xffffffffu, sum > rem);
+                if (past) {
+                    const int k = __ffs(past) - 1;
+                    rem -= __shfl_sync(0xffffffffu, sum - wt, k);
+                    rt += k;
+                    break;
+                }
+                rem -= __shfl_sync(0xffffffffu, sum, 31);
+            }
+            into = rem;
+        }
         bool fine = true;
-        for (; fine && w.segment(a); w.next(a)) {
-            const int32_t *bt = a.block_table + (int64_t)w.b * a.max_blocks;
-            const uint8_t *keep =
-                a.keep_in ? a.keep_in + ((int64_t)w.b * a.Hkv + w.h) * a.max_blocks : nullptr;
-            const int begin = w.fp + w.at, end = begin + w.cnt;
+        while (fine) {
+            int fp = 0, np = 0, item = 0, at = 0, cnt = 0;  // item: its first page in the cut's scale
+            if (x < c1) {
+                item_pages(a, s, rt, fp, np);
+                item = x - into + a.lead;
+                at = into > a.lead ? into - a.lead : 0;
+                cnt = min(np, c1 - item) - at;  // not above 0: the item's pages are the next CTA's
+            }
+            const int begin = fp + at, end = begin + cnt, node0 = rt * a.item_nodes;
+            if (lane == 0) {
+                Segment &d = sh.seg[segs % kSegs];
+                d.pages = cnt > 0 ? cnt : 0;
+                if (cnt > 0) {
+                    d.end = end * kPage;
+                    d.h = h, d.t0 = s.t0, d.nq = s.nq, d.first = s.first(), d.node0 = node0;
+                    d.p0 = ranges.owner(item), d.p1 = ranges.owner(item + np - 1);
+                    d.begins = at == 0;
+                }
+                mbar_arrive(&sh.seg_full[segs % kSegs]);
+            }
+            if (cnt <= 0) break;
+            if (segs > 0 && !waited(a, sh, &sh.q_free, (segs - 1) & 1)) break;
+            if (lane == 0) {  // rows of tile g: nodes by heads, as a box of {64 channels, G heads, nodes}
+                const int tiles = kTiles == 2 && s.nq - node0 > a.tile_nodes ? 2 : 1;
+                mbar_arrive_expect_tx(&sh.q_full, tiles * a.tile_nodes * a.G * kD * 2);
+                for (int g = 0; g < tiles; g++)
+#pragma unroll
+                    for (int c = 0; c < 2; c++)
+                        tma_load_3d(sh.q[g] + c * 16384, &prm.tm_q, 64 * c, h * a.G,
+                                    s.t0 + node0 + g * a.tile_nodes, &sh.q_full);
+            }
+            segs++;
+            const int32_t *bt = a.block_table + (int64_t)b * a.max_blocks;
+            const uint8_t *keep = a.keep_in ? a.keep_in + ((int64_t)b * a.Hkv + h) * a.max_blocks : nullptr;
             int lo, hi;
-            item_span<kRows>(a, w.s, w.rt, lo, hi);
+            item_span(a, s, rt, lo, hi);
             const int seen = a.parents ? lo - 1 : lo;  // tokens up to here are seen by all, but for a window
             const int from = a.window > 0 ? hi - a.window : -1;  // and those behind here
             auto look = [&](int j) {
@@ -800,15 +802,15 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                     if (j0 >= 0) {
                         mbar_arrive_expect_tx(&sh.k_full[ks], (j1 >= 0 ? 2 : 1) * kPageBytes);
                         if (kStep == 1) {
-                            tma_load_3d(sh.k[ks], &prm.tm_k, 0, (p0 * a.Hkv + w.h) * kPage, 0, &sh.k_full[ks]);
+                            tma_load_3d(sh.k[ks], &prm.tm_k, 0, (p0 * a.Hkv + h) * kPage, 0, &sh.k_full[ks]);
                         } else {
 #pragma unroll
                             for (int c = 0; c < 2; c++) {  // channel halves
-                                tma_load_3d(sh.k[ks] + c * 16384, &prm.tm_k, 0, (p0 * a.Hkv + w.h) * kPage, c,
+                                tma_load_3d(sh.k[ks] + c * 16384, &prm.tm_k, 0, (p0 * a.Hkv + h) * kPage, c,
                                             &sh.k_full[ks]);
                                 if (j1 >= 0)
                                     tma_load_3d(sh.k[ks] + c * 16384 + 8192, &prm.tm_k, 0,
-                                                (p1 * a.Hkv + w.h) * kPage, c, &sh.k_full[ks]);
+                                                (p1 * a.Hkv + h) * kPage, c, &sh.k_full[ks]);
                             }
                         }
                     } else {
@@ -823,7 +825,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                     if (lane == 0) {
                         if (j0 >= 0) {
                             mbar_arrive_expect_tx(&sh.v_full[vs], kPageBytes);
-                            tma_load_3d(sh.v[vs], &prm.tm_v, 0, ((n ? p1 : p0) * a.Hkv + w.h) * kPage, 0,
+                            tma_load_3d(sh.v[vs], &prm.tm_v, 0, ((n ? p1 : p0) * a.Hkv + h) * kPage, 0,
                                         &sh.v_full[vs]);
                         } else {
                             mbar_arrive(&sh.v_full[vs]);
@@ -833,28 +835,52 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 }
                 return true;
             };
+            // The listed pages one by one, the last followed by what is held back and the end (j -1, twice).
             int ahead = look(begin + lane), held = -1, held_page = 0;  // a page that waits for a second one
-            for (int jb = begin; jb < end && fine; jb += 32) {
+            for (int jb = begin; fine; jb += 32) {
                 const int page = ahead;
-                ahead = look(jb + 32 + lane);
-                for (uint32_t todo = __ballot_sync(0xffffffffu, page >= 0); todo && fine; todo &= todo - 1) {
-                    const int k = __ffs(todo) - 1, p = __shfl_sync(0xffffffffu, page, k);
-                    if (kStep == 1) {
-                        fine = push(jb + k, p, -1, -1);
-                    } else if (held < 0) {
-                        held = jb + k;
+                uint32_t todo = 0;
+                if (jb < end) {
+                    ahead = look(jb + 32 + lane);
+                    todo = __ballot_sync(0xffffffffu, page >= 0);
+                    if (todo == 0) continue;
+                }
+                do {
+                    const int k = __ffs(todo) - 1;  // -1: there are no more pages
+                    const int p = __shfl_sync(0xffffffffu, page, k & 31), j = todo ? jb + k : -1;
+                    if (kStep == 2 && held < 0 && j >= 0) {
+                        held = j;
                         held_page = p;
-                    } else {
-                        fine = push(held, held_page, jb + k, p);
+                    } else if (kStep == 2 && held >= 0) {
+                        fine = push(held, held_page, j, p);
                         held = -1;
+                        if (j < 0) continue;  // then the end
+                    } else {
+                        fine = push(j, p, -1, -1);
+                    }
+                    todo &= todo - 1;
+                    if (j < 0) break;
+                } while (fine && (todo || jb >= end));
+                if (jb >= end) break;
+            }
+            // ---- the next item that has pages
+            x = item + at + cnt;
+            into = 0;
+            if (x >= c1) continue;
+            do {
+                if (++rt >= item_groups(a, s)) {
+                    rt = 0;
+                    if (++h >= a.Hkv) {
+                        h = 0;
+                        do s = seq_of(a, ++b, false);
+                        while (s.nq == 0);
                     }
                 }
-            }
-            if (fine && held >= 0) fine = push(held, held_page, -1, -1);
-            if (fine) fine = push(-1, -1, -1, -1);
+                item_pages(a, s, rt, fp, np);
+            } while (np == 0);
         }
         if (stopped(sh) && lane == 0) {  // leave nothing in flight
-            bool done = true;
+            bool done = segs == 0 || mbar_drain(&sh.q_full, (segs - 1) & 1, drain_bound_ns(a.wait_ns));
             for (uint32_t i = 0; i < H::kNK && i < steps; i++) {
                 const uint32_t last = steps - 1 - i;
                 done &= mbar_drain(&sh.k_full[last % H::kNK], (last / H::kNK) & 1, drain_bound_ns(a.wait_ns));
@@ -865,144 +891,147 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             }
             if (!done) raise_error(a.err, FFD_ERRBIT_TIMEOUT);
         }
-    } else if (warp < H::kSoft + 1 + kTiles) {
+    } else if (warp < H::kClean) {
         // ================= matrix instructions of one tile =================
         // The whole warp goes through the steps, so that operand addresses stay warp-uniform; one lane
         // issues.
-        const int g = warp - H::kSoft - 1;
         const bool issuer = elect_one();
-        const uint32_t k0 = smem_u32(sh.k[0]), v0 = smem_u32(sh.v[0]);
-        const uint32_t qd = tc_desc(smem_u32(sh.q[g]));
-        uint32_t items = 0;
-        bool fine = true;
-        for (; fine && w.segment(a); w.next(a)) {
-            const bool live = g == 0 || w.s.nq * a.G - w.rt * kRows > kTile;
-            fine = waited(a, sh, &sh.q_full[g], items++ & 1);
-            // The scores of the next step. 0 at the segment's end, which the softmax group learns of in the
-            // same way; else its pages. Negative: stopped.
-            auto next_scores = [&]() {
-                const uint32_t ks = steps % H::kNK, d = tmem + H::col_s(g, steps);
-                if (!waited(a, sh, &sh.k_full[ks], (steps / H::kNK) & 1)) return -1;
-                tc_fence_after();
-                const volatile Step &info = sh.info[steps % kInfo];
-                int pages = info.j0 < 0 ? 0 : info.j1 < 0 ? 1 : 2;
-                pages = __shfl_sync(0xffffffffu, pages, 0);
-                const uint32_t kd = tc_desc(k0 + ks * (kStep * kPageBytes));
-                if (issuer) {
-                    if (pages && live) {
-                        const uint32_t idesc = kStep == 2 && pages == 2 ? kIdescS128 : kIdescS64;
+        const bool scores = warp < H::kValues;
+        const int g = warp - (scores ? H::kScores : H::kValues);
+        if (scores) {
+            const uint32_t k0 = smem_u32(sh.k[0]), qd = tc_desc(smem_u32(sh.q[g]));
+            int last0 = -1, last1 = -1;  // the product with V that has P at each of S's places, not waited for
+            bool fine = true;
+            while (fine) {
+                const Segment *sg = next_segment();
+                if (!sg) break;
+                const bool live = g == 0 || sg->nq - sg->node0 > a.tile_nodes;
+                fine = waited(a, sh, &sh.q_full, (segs - 1) & 1);
+                while (fine) {
+                    const uint32_t ks = steps % H::kNK, buf = steps & 1, d = tmem + H::col_s(g, steps);
+                    const int t = buf ? last1 : last0;
+                    if (t >= 0 && !(fine = waited(a, sh, &sh.o_done[g][t & 1], (t >> 1) & 1))) break;
+                    if (!(fine = waited(a, sh, &sh.k_full[ks], (steps / H::kNK) & 1))) break;
+                    tc_fence_after();
+                    const volatile Step &info = sh.info[steps % kInfo];
+                    const int pages = __shfl_sync(0xffffffffu, info.j0 < 0 ? 0 : info.j1 < 0 ? 1 : 2, 0);
+                    const uint32_t kd = tc_desc(k0 + ks * (kStep * kPageBytes));
+                    const uint32_t idesc =
+                        (kStep == 2 && pages == 2 ? tc_idesc_f16(128, 128) : tc_idesc_f16(128, 64)) |
+                        Idesc<T>::kType;
+                    if (issuer) {
+                        if (pages && live) {
 #pragma unroll
-                        for (int i = 0; i < 8; i++)  // 16 channels each
-                            tc_mma(d, qd + (i >> 2) * 1024 + (i & 3) * 2,
-                                   kd + (i >> 2) * (512 * kStep) + (i & 3) * 2, idesc, i > 0);
-                    }
-                    tc_commit(&sh.s_full[g][steps & 1]);
-                    tc_commit(&sh.k_free[ks]);
-                }
-                steps++;
-                return pages;
-            };
-            uint32_t pstep = steps;  // the step whose values come next
-            int cur = fine ? next_scores() : -1, nxt = 0;
-            if (cur > 0) nxt = next_scores();  // two steps' scores are under way before the first P V
-            bool add = false;
-            while (cur > 0) {
-                fine = false;
-                const uint32_t vs0 = vsteps % H::kNV, vs1 = (vsteps + 1) % H::kNV;
-                if (!waited(a, sh, &sh.v_ready[vs0], (vsteps / H::kNV) & 1)) break;
-                if (cur == 2 && !waited(a, sh, &sh.v_ready[vs1], ((vsteps + 1) / H::kNV) & 1)) break;
-                if (!waited(a, sh, &sh.p_full[g][pstep & 1], (pstep >> 1) & 1)) break;
-                tc_fence_after();
-                const uint32_t p = tmem + H::col_s(g, pstep), d = tmem + kColO + g * 128;
-                if (issuer) {
-                    if (live) {
-                        const uint32_t vd0 = tc_desc_mn(v0 + vs0 * kPageBytes, 8192);
-                        const uint32_t vd1 = tc_desc_mn(v0 + vs1 * kPageBytes, 8192);
-#pragma unroll
-                        for (int i = 0; i < 4; i++)  // 16 tokens each
-                            tc_mma_ta(d, p + 8 * i, vd0 + 128 * i, kIdescO, add || i > 0);
-                        if (cur == 2) {
-#pragma unroll
-                            for (int i = 0; i < 4; i++)
-                                tc_mma_ta(d, p + 32 + 8 * i, vd1 + 128 * i, kIdescO, true);
+                            for (int i = 0; i < 8; i++)  // 16 channels each
+                                tc_mma(d, qd + (i >> 2) * 1024 + (i & 3) * 2,
+                                       kd + (i >> 2) * (512 * kStep) + (i & 3) * 2, idesc, i > 0);
                         }
+                        tc_commit(&sh.s_full[g][buf]);
+                        tc_commit(&sh.k_free[ks]);
+                        if (!pages) tc_commit(&sh.q_free);
                     }
-                    tc_commit(&sh.o_done[g]);
+                    steps++;
+                    (buf ? last1 : last0) = pages ? (int)turns++ : -1;
+                    if (!pages) {  // the softmax group has seen the end: it is at most one behind
+                        fine = waited(a, sh, &sh.p_full[g][buf], ((steps - 1) >> 1) & 1);
+                        break;
+                    }
                 }
-                if (!waited(a, sh, &sh.o_done[g], turns & 1)) break;
-                if (issuer) {
-                    mbar_arrive(&sh.v_free[vs0]);
-                    if (cur == 2) mbar_arrive(&sh.v_free[vs1]);
-                }
-                vsteps += cur;
-                turns++;
-                pstep++;
-                add = true;
-                fine = true;
-                const int third = nxt > 0 ? next_scores() : nxt;
-                cur = nxt;
-                nxt = third;
             }
-            if (cur < 0) fine = false;
-            if (fine) {  // the end's V place
-                fine = waited(a, sh, &sh.v_ready[vsteps % H::kNV], (vsteps / H::kNV) & 1);
-                if (fine && issuer) mbar_arrive(&sh.v_free[vsteps % H::kNV]);
-                vsteps++;
+        } else {
+            const uint32_t v0 = smem_u32(sh.v[0]), d = tmem + kColO + g * 128;
+            constexpr uint32_t kIdescO = tc_idesc_f16(128, 128) | Idesc<T>::kType | kTcBMn;
+            bool fine = true;
+            while (fine) {
+                const Segment *sg = next_segment();
+                if (!sg) break;
+                const bool live = g == 0 || sg->nq - sg->node0 > a.tile_nodes;
+                bool add = false;
+                while (true) {
+                    const uint32_t vs0 = vsteps % H::kNV, vs1 = (vsteps + 1) % H::kNV;
+                    if (!(fine = waited(a, sh, &sh.v_ready[vs0], (vsteps / H::kNV) & 1))) break;
+                    const volatile Step &info = sh.info[steps % kInfo];
+                    const int pages = __shfl_sync(0xffffffffu, info.j0 < 0 ? 0 : info.j1 < 0 ? 1 : 2, 0);
+                    if (pages == 2 && !(fine = waited(a, sh, &sh.v_ready[vs1], ((vsteps + 1) / H::kNV) & 1)))
+                        break;
+                    if (pages && !(fine = waited(a, sh, &sh.p_full[g][steps & 1], (steps >> 1) & 1))) break;
+                    tc_fence_after();
+                    const uint32_t p = tmem + H::col_s(g, steps);
+                    if (issuer) {
+                        if (pages && live) {
+                            const uint32_t vd0 = tc_desc_mn(v0 + vs0 * kPageBytes, 8192);
+                            const uint32_t vd1 = tc_desc_mn(v0 + vs1 * kPageBytes, 8192);
+#pragma unroll
+                            for (int i = 0; i < 4; i++)  // 16 tokens each
+                                tc_mma_ta(d, p + 8 * i, vd0 + 128 * i, kIdescO, add || i > 0);
+                            if (kStep == 2 && pages == 2) {
+#pragma unroll
+                                for (int i = 0; i < 4; i++)
+                                    tc_mma_ta(d, p + 32 + 8 * i, vd1 + 128 * i, kIdescO, true);
+                            }
+                        }
+                        if (pages) tc_commit(&sh.o_done[g][turns & 1]);
+                        tc_commit(&sh.v_free[vs0]);
+                        if (pages == 2) tc_commit(&sh.v_free[vs1]);
+                    }
+                    vsteps += pages == 2 ? 2 : 1;
+                    steps++;
+                    if (!pages) break;
+                    turns++;
+                    add = true;
+                }
             }
         }
         if (stopped(sh) && issuer) {
-            tc_commit(&sh.drain[g]);
-            if (!mbar_drain(&sh.drain[g], 0, drain_bound_ns(a.wait_ns))) raise_error(a.err, FFD_ERRBIT_TIMEOUT);
+            uint64_t *bar = &sh.drain[warp - H::kScores];
+            tc_commit(bar);
+            if (!mbar_drain(bar, 0, drain_bound_ns(a.wait_ns))) raise_error(a.err, FFD_ERRBIT_TIMEOUT);
         }
-    } else if (warp == kCtaWarps - 1) {
+    } else {
         // ================= values that are not finite =================
         bool fine = true;
-        for (; fine && w.segment(a); w.next(a)) {
-            while (true) {
-                fine = waited(a, sh, &sh.v_full[vsteps % H::kNV], (vsteps / H::kNV) & 1);
-                if (!fine) break;
+        while (fine && next_segment()) {
+            bool end = false;
+            while (fine && !end) {
+                const uint32_t vs = vsteps % H::kNV;
+                if (!(fine = waited(a, sh, &sh.v_full[vs], (vsteps / H::kNV) & 1))) break;
                 const volatile Step &info = sh.info[steps % kInfo];
-                const bool end = info.j0 < 0, edge = info.edge != 0;
-                const int pages = info.j1 >= 0 ? 2 : 1;
-                steps++;
-                for (int n = 0; n < pages; n++) {
-                    const uint32_t vs = vsteps % H::kNV;
-                    if (n > 0 && !(fine = waited(a, sh, &sh.v_full[vs], (vsteps / H::kNV) & 1))) break;
-                    if (edge) {
-                        uint64_t bad = 0;
-                        uint8_t *tile = sh.v[vs];
+                const bool edge = info.edge != 0, second = turns > 0;  // turns: pages of the step that are done
+                end = info.j0 < 0;
+                if (edge) {
+                    uint64_t bad = 0;
+                    uint8_t *tile = sh.v[vs];
 #pragma unroll 1
-                        for (int i0 = 0; i0 < 32; i0 += 8) {  // four rows of a channel half at a time
-                            uint4 x[8];
+                    for (int i0 = 0; i0 < 32; i0 += 8) {  // four rows of a channel half at a time
+                        uint4 x[8];
 #pragma unroll
-                            for (int i = 0; i < 8; i++)
-                                x[i] = *reinterpret_cast<const uint4 *>(tile + (i0 + i) * 512 + 16 * lane);
+                        for (int i = 0; i < 8; i++)
+                            x[i] = *reinterpret_cast<const uint4 *>(tile + (i0 + i) * 512 + 16 * lane);
 #pragma unroll
-                            for (int i = 0; i < 8; i++) {
-                                uint32_t most = T::max2_nan(
-                                    T::max2_nan(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                                    T::max2_nan(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
-                                const float2 f = T::unpack(most);
-                                const bool wrong = !(f.x < INFINITY && f.y < INFINITY);
-                                if (wrong)
-                                    *reinterpret_cast<uint4 *>(tile + (i0 + i) * 512 + 16 * lane) =
-                                        make_uint4(0, 0, 0, 0);
-                                uint32_t who = __ballot_sync(0xffffffffu, wrong);
-                                if (who) {
-                                    for (int q = 0; q < 4; q++)
-                                        if ((who >> (8 * q)) & 0xffu)
-                                            bad |= 1ull << (((i0 + i) & 15) * 4 + q);
-                                }
+                        for (int i = 0; i < 8; i++) {
+                            const uint32_t most = T::max2_nan(
+                                T::max2_nan(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                T::max2_nan(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+                            const float2 f = T::unpack(most);
+                            const bool wrong = !(f.x < INFINITY && f.y < INFINITY);
+                            if (wrong)
+                                *reinterpret_cast<uint4 *>(tile + (i0 + i) * 512 + 16 * lane) =
+                                    make_uint4(0, 0, 0, 0);
+                            const uint32_t who = __ballot_sync(0xffffffffu, wrong);
+                            if (who) {
+                                for (int q = 0; q < 4; q++)
+                                    if ((who >> (8 * q)) & 0xffu) bad |= 1ull << (((i0 + i) & 15) * 4 + q);
                             }
                         }
-                        if (lane == 0) *reinterpret_cast<volatile uint64_t *>(&sh.bad[vs]) = bad;
-                        fence_proxy_async();
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.v_ready[vs]);
-                    vsteps++;
+                    if (lane == 0) *reinterpret_cast<volatile uint64_t *>(&sh.bad[vs]) = bad;
+                    fence_proxy_async();
                 }
-                if (end || !fine) break;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.v_ready[vs]);
+                vsteps++;
+                turns = !second && info.j1 >= 0 ? 1 : 0;
+                steps += turns == 0;
             }
         }
     }
@@ -1025,6 +1054,22 @@ bool page_map(CUtensorMap *map, const void *ptr, uint64_t rows, int dtype, uint3
     return fn(map,
               dtype == FFD_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
               const_cast<void *>(ptr), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The queries as a tensor {channels, heads, rows}; a copy takes half of the channels of G heads and `nodes`
+// rows and lands them as rows of 128 B, node by node.
+bool query_map(CUtensorMap *map, const AttnArgs &a, int dtype) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {kD, (cuuint64_t)a.Hq, (cuuint64_t)a.total_q};
+    const cuuint64_t strides[2] = {kD * 2, (cuuint64_t)a.q_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)a.G, (cuuint32_t)a.tile_nodes};
+    const cuuint32_t step[3] = {1, 1, 1};
+    return fn(map,
+              dtype == FFD_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+              const_cast<uint16_t *>(a.q), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1060,7 +1105,7 @@ size_t tree_record_bytes(int tiles) {
 cudaError_t launch_tree_attention(const AttnArgs &a, const Plan &pl, int dtype, cudaStream_t stream) {
     Params prm;
     const uint64_t rows = (uint64_t)a.P * a.Hkv * kPage;
-    if (!page_map(&prm.tm_k, a.k, rows, dtype, pl.tiles == 1 ? 1 : 2) || !page_map(&prm.tm_v, a.v, rows, dtype, 2))
+    if (!query_map(&prm.tm_q, a, dtype) || !page_map(&prm.tm_k, a.k, rows, dtype, pl.tiles == 1 ? 1 : 2) || !page_map(&prm.tm_v, a.v, rows, dtype, 2))
         return cudaErrorInvalidValue;
     prm.a = a;
     char *ws = reinterpret_cast<char *>(a.err);

@@ -428,3 +428,17 @@ def test_random_batches():
         if pick(0, 2) == 0:
             keep = (torch.rand((B, Hkv, x.bt.shape[1]), generator=gen) < 0.6).to(torch.uint8)
         x.check(keep=keep, window=pick(1, 2000) if pick(0, 2) == 0 else 0)
+
+
+@pytest.mark.parametrize("splits", [0, 1, 3])
+@pytest.mark.parametrize("nq", [3, 70])
+def test_many_items_without_a_page(splits, nq):
+    """One CTA meets items one after another whose blocks are all dropped, and others between them."""
+    B = 12
+    x = Problem(8, 2, [100 + 64 * (b % 3) for b in range(B)], [nq] * B, BF16, seed=22)
+    keep = torch.zeros((B, 2, x.bt.shape[1]), dtype=torch.uint8)
+    got, z = x.check(keep=keep, num_splits=splits)
+    assert bool((got == 0).all())
+    keep[5, 1] = 1
+    keep[11, 0, 1] = 1
+    x.check(keep=keep, num_splits=splits)
