@@ -674,7 +674,7 @@ size_t ffd_tree_workspace_size(const ffd_tree_params *params);
  *   parents     device int32 [total_q] or NULL; with it max_q_len <= FFD_TREE_MAX_NODES (else
  *               FFD_ERR_UNSUPPORTED)
  *   block_table device int32 [B][max_blocks_per_seq]; entries of blocks that no node of the
- *               sequence sees (past n, behind the window, dropped by keep_in) are not read
+ *               sequence sees (past n, behind the window, dropped by keep_in) are not used
  *   keep_in     device u8 [B][Hkv][max_blocks_per_seq] or NULL: nonzero = the block may be seen
  *               (for instance ffd_select_blocks's mask, or a decode step's keep_mask)
  *   out         device [total_q][Hq][128] of dtype, 16-byte aligned; it must not overlap q

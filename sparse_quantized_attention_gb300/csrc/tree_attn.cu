@@ -79,8 +79,8 @@ struct Segment {  // pages 0: there is none any more
     int pages, end;        // how many, and the token behind the last
     int h, t0, nq, first;  // KV head, first node's row, nodes, tokens before the tree
     int node0;             // the item's first node
-    int p0, p1;            // CTAs that share the item
-    int begins;            // whether the segment holds the item's first page
+    int begins, complete;  // whether the segment holds the item's first page, and all of them
+    int p0, p1;            // CTAs that share the item (known at the segment's end)
 };
 
 template <int kTiles>
@@ -91,11 +91,11 @@ struct Shared {
     uint8_t v[H::kNV][kPageBytes];              // the same for 64 tokens
     uint32_t bits[kMaxNodes / 32][H::kRows];    // nodes that a row sees
     int parent[kTiles][kMaxNodes];
-    uint64_t seg_full[kSegs];
-    uint64_t k_full[H::kNK], k_free[H::kNK];
-    uint64_t v_full[H::kNV], v_ready[H::kNV], v_free[H::kNV];
-    uint64_t q_full, q_free, joined;
-    uint64_t s_full[kTiles][2], p_full[kTiles][2], o_done[kTiles][2], drain[2 * kTiles];
+    // barriers, by the number of arrivals: one, kTiles, four
+    uint64_t seg_full[kSegs], k_full[H::kNK], v_full[H::kNV], v_ready[H::kNV], q_full, joined;
+    uint64_t s_full[kTiles][2], o_done[kTiles][2], drain[2 * kTiles];
+    uint64_t k_free[H::kNK], v_free[H::kNV], q_free;
+    uint64_t p_full[kTiles][2], end_of_barriers;
     uint64_t bad[H::kNV];                       // tokens of a page whose V is not finite
     Step info[kInfo];
     Segment seg[kSegs];
@@ -186,6 +186,16 @@ __device__ __forceinline__ int head_weight(const AttnArgs &a, const Seq &s, int 
     return __reduce_add_sync(0xffffffffu, sum);
 }
 
+// Output of a sequence's rows that see nothing, a share of them for each CTA.
+__device__ __noinline__ void write_empty(const AttnArgs &a, int t0, int nq, int thread, int threads) {
+    const int64_t rows = (int64_t)nq * a.Hq, first = (int64_t)t0 * a.Hq;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        for (int c = thread; c < kD / 8; c += threads)
+            reinterpret_cast<uint4 *>(a.out + (first + r) * kD)[c] = make_uint4(0, 0, 0, 0);
+        if (a.lse && thread == 0) a.lse[first + r] = -INFINITY;
+    }
+}
+
 // Rows that a channel has in a record of an item that is `left` nodes from its sequence's end: both tiles'
 // places up to the last row, in 16 bytes.
 __device__ __forceinline__ int record_rows(const AttnArgs &a, int left) {
@@ -252,89 +262,67 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
 
     __syncwarp();
     if (warp == 0) tmem_alloc(&sh.tmem, 512);
-    if (tid == 32) {
-        sh.aborted = 0;
-        sh.shared_item.pages = 0;
-        for (int i = 0; i < kSegs; i++) mbar_init(&sh.seg_full[i], 1);
-        for (int i = 0; i < H::kNK; i++) {
-            mbar_init(&sh.k_full[i], 1);
-            mbar_init(&sh.k_free[i], kTiles);
-        }
-        for (int i = 0; i < H::kNV; i++) {
-            mbar_init(&sh.v_full[i], 1);
-            mbar_init(&sh.v_ready[i], 1);
-            mbar_init(&sh.v_free[i], kTiles);
-        }
-        mbar_init(&sh.q_full, 1);
-        mbar_init(&sh.q_free, kTiles);
-        mbar_init(&sh.joined, 1);
-        for (int g = 0; g < kTiles; g++) {
-            for (int j = 0; j < 2; j++) {
-                mbar_init(&sh.s_full[g][j], 1);
-                mbar_init(&sh.p_full[g][j], 4);
-                mbar_init(&sh.o_done[g][j], 1);
-            }
-        }
-        for (int g = 0; g < 2 * kTiles; g++) mbar_init(&sh.drain[g], 1);
+    if (warp == 1) {
+        uint64_t *one = sh.seg_full, *tiles = sh.k_free, *four = sh.p_full[0], *end = &sh.end_of_barriers;
+        for (uint64_t *bar = one + lane; bar < end; bar += 32)
+            mbar_init(bar, bar >= four ? 4 : bar >= tiles ? kTiles : 1);
+        if (lane == 0) sh.aborted = 0, sh.shared_item.pages = 0;
         fence_barrier_init();
     }
-    // ---- weight of the items before each chunk of sequences: a warp for each of a few, else a thread
-    const bool few = a.B <= 4 * kCtaWarps;
-    const int chunk = few ? 1 : (a.B + kThreads - 1) / kThreads;
-    int own = 0;
-    bool empty = false;  // some sequence's rows see nothing
+    // ---- weight of all items: up to 32 sequences by the copy warp alone, a lane each; more by all threads, a
+    // run of sequences each
+    const bool few = a.B <= 32;
+    const int chunk = (a.B + kThreads - 1) / kThreads;  // sequences of a thread
+    int total = 0, own = 0;
+    Seq s = {0, 0, 0};
     if (few) {
-#pragma unroll 1
-        for (int b = warp; b < a.B; b += kCtaWarps) {
-            const Seq s = seq_of(a, b, blockIdx.x == 0 && lane == 0);
-            const int w = head_weight(a, s, lane);
-            if (lane == 0) sh.pre[b] = w * a.Hkv;
-            empty |= s.n == 0 && s.nq > 0;
+        if (warp == H::kCopy) {
+            if (lane < a.B) {
+                s = seq_of(a, lane, blockIdx.x == 0);
+                const int groups = item_groups(a, s);
+                for (int rt = 0; rt < groups; rt++) own += item_weight(a, s, rt, groups);
+                own *= a.Hkv;
+            }
+        } else if (warp == H::kClean) {
+            Seq e = {1, 0, 0};
+            if (lane < a.B) e = seq_of(a, lane, false);
+            for (uint32_t todo = __ballot_sync(0xffffffffu, e.n == 0 && e.nq > 0); todo; todo &= todo - 1) {
+                const int b = __ffs(todo) - 1;
+                write_empty(a, __shfl_sync(0xffffffffu, e.t0, b), __shfl_sync(0xffffffffu, e.nq, b), lane, 32);
+            }
         }
     } else {
+        bool empty = false;  // some sequence's rows see nothing
 #pragma unroll 1
         for (int b = tid * chunk; b < (tid + 1) * chunk && b < a.B; b++) {
-            const Seq s = seq_of(a, b, blockIdx.x == 0);
+            const Seq e = seq_of(a, b, blockIdx.x == 0);
             int w = 0;
-            const int groups = item_groups(a, s);
-            for (int rt = 0; rt < groups; rt++) w += item_weight(a, s, rt, groups);
+            const int groups = item_groups(a, e);
+            for (int rt = 0; rt < groups; rt++) w += item_weight(a, e, rt, groups);
             own += w * a.Hkv;
-            empty |= s.n == 0 && s.nq > 0;
+            empty |= e.n == 0 && e.nq > 0;
         }
-    }
-    empty = __syncthreads_or(empty);
-    if (few && tid < a.B) own = sh.pre[tid];
-    const int inc = lane_scan(own, lane);
-    if (lane == 31) sh.scan[warp] = inc;
-    __syncthreads();
-    const int of_warp = lane_scan(lane < kCtaWarps ? sh.scan[lane] : 0, lane);
-    const int total = __shfl_sync(0xffffffffu, of_warp, 31);
-    const int warps = __shfl_sync(0xffffffffu, of_warp, warp == 0 ? 0 : warp - 1);
-    sh.pre[tid] = (warp == 0 ? 0 : warps) + inc - own;
-    if (empty) {
-        for (int u = blockIdx.x; u < a.B * a.Hkv; u += gridDim.x) {
-            const int b = u / a.Hkv, h = u - b * a.Hkv;
-            const Seq s = seq_of(a, b, false);
-            if (s.n > 0) continue;
-            for (int i = tid >> 4; i < s.nq; i += kThreads / 16) {  // 16 threads a node
-                const int64_t at = (int64_t)(s.t0 + i) * a.Hq + h * a.G;
-                for (int g = 0; g < a.G; g++) {
-                    reinterpret_cast<uint4 *>(a.out + (at + g) * kD)[tid & 15] = make_uint4(0, 0, 0, 0);
-                    if (a.lse && (tid & 15) == 0) a.lse[at + g] = -INFINITY;
-                }
+        empty = __syncthreads_or(empty);
+        const int inc = lane_scan(own, lane);
+        if (lane == 31) sh.scan[warp] = inc;
+        __syncthreads();
+        const int of_warp = lane_scan(lane < kCtaWarps ? sh.scan[lane] : 0, lane);
+        total = __shfl_sync(0xffffffffu, of_warp, 31);
+        const int warps = __shfl_sync(0xffffffffu, of_warp, warp == 0 ? 0 : warp - 1);
+        sh.pre[tid] = (warp == 0 ? 0 : warps) + inc - own;
+        if (empty) {
+#pragma unroll 1
+            for (int b = 0; b < a.B; b++) {
+                const Seq e = seq_of(a, b, false);
+                if (e.n == 0) write_empty(a, e.t0, e.nq, tid, kThreads);
             }
         }
     }
-    const int ncta = total < (int)gridDim.x ? total : (int)gridDim.x, cta = blockIdx.x;
+    const int cta = blockIdx.x;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    if (cta >= ncta) {
-        __syncwarp();
-        if (warp == 0) tmem_free(tmem, 512);
-        return;
-    }
 
     uint32_t steps = 0, vsteps = 0, turns = 0;  // so far: steps and V pages (ends among them), P V products
     uint32_t segs = 0;
@@ -357,7 +345,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             if (named_barrier_or(3, kRows, sg == nullptr)) break;
             const int first = sg->first, nq = sg->nq, node0 = sg->node0, t0 = sg->t0;
             const bool active = grp == 0 || nq - node0 > a.tile_nodes;
-            const bool complete = sg->p0 == sg->p1;
+            const bool complete = sg->complete;
             const int qi = node0 + grp * a.tile_nodes + rn;
             const bool have = rn < a.tile_nodes && qi < nq;
             // ---- the nodes that the row sees, and its position
@@ -703,39 +691,53 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             prefetch_tensormap(&prm.tm_k);
             prefetch_tensormap(&prm.tm_v);
         }
-        const Ranges ranges(total, ncta);
-        int x = ranges.begin(cta), b, h, rt, into;
-        const int c1 = ranges.begin(cta + 1);
-        Seq s = {0, 0, 0};
-        {   // where the range begins: sequence b, head h, group rt, `into` the item's weight
-            int lo = 0, hi = kThreads;  // the last chunk of sequences that begins at or before x
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (sh.pre[mid] <= x) lo = mid;
-                else hi = mid;
-            }
-            int rem = x - sh.pre[lo], hp = 1;
+        const int inc = lane_scan(own, lane);
+        if (few) total = __shfl_sync(0xffffffffu, inc, 31);
+        const int ncta = min(total, (int)gridDim.x);
+        const Ranges ranges(total, max(ncta, 1));
+        int x = ranges.begin(cta), b = 0, h = 0, rt = 0, into = 0;
+        const int c1 = cta < ncta ? ranges.begin(cta + 1) : x;
+        if (cta < ncta) {  // where the range begins: sequence b, head h, group rt, `into` the item's weight
+            int rem = x, hp = 1;
+            if (few) {
+                b = __ffs(__ballot_sync(0xffffffffu, inc > x)) - 1;
+                rem -= __shfl_sync(0xffffffffu, inc - own, b);
+                hp = __shfl_sync(0xffffffffu, own, b) / a.Hkv;
+                s.n = __shfl_sync(0xffffffffu, s.n, b);
+                s.t0 = __shfl_sync(0xffffffffu, s.t0, b);
+                s.nq = __shfl_sync(0xffffffffu, s.nq, b);
+            } else {
+                int lo = 0, hi = kThreads;  // the last chunk of sequences that begins at or before x
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (sh.pre[mid] <= x) lo = mid;
+                    else hi = mid;
+                }
+                rem -= sh.pre[lo];
 #pragma unroll 1
-            for (b = lo * chunk; b < a.B; b++) {
-                s = seq_of(a, b, false);
-                hp = head_weight(a, s, lane);
-                if (rem < hp * a.Hkv) break;
-                rem -= hp * a.Hkv;
+                for (b = lo * chunk; b < a.B; b++) {
+                    s = seq_of(a, b, false);
+                    hp = head_weight(a, s, lane);
+                    if (rem < hp * a.Hkv) break;
+                    rem -= hp * a.Hkv;
+                }
             }
             h = rem / hp;
             rem -= h * hp;
             const int groups = item_groups(a, s);
+            if (groups > 1) {
 #pragma unroll 1
-            for (rt = 0;; rt += 32) {  // 32 items at a time
-                const int wt = item_weight(a, s, rt + lane, groups), sum = lane_scan(wt, lane);
-                const uint32_t past = __ballot_sync(0xffffffffu, sum > rem);
-                if (past) {
-                    const int k = __ffs(past) - 1;
-                    rem -= __shfl_sync(0xffffffffu, sum - wt, k);
-                    rt += k;
-                    break;
+                for (;; rt += 32) {  // 32 items at a time
+                    const int wt = item_weight(a, s, rt + lane, groups), sum = lane_scan(wt, lane);
+                    const uint32_t past = __ballot_sync(0xffffffffu, sum > rem);
+                    if (past) {
+                        const int k = __ffs(past) - 1;
+                        rem -= __shfl_sync(0xffffffffu, sum - wt, k);
+                        rt += k;
+                        break;
+                    }
+                    rem -= __shfl_sync(0xffffffffu, sum, 31);
                 }
-                rem -= __shfl_sync(0xffffffffu, sum, 31);
             }
             into = rem;
         }
@@ -755,8 +757,8 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 if (cnt > 0) {
                     d.end = end * kPage;
                     d.h = h, d.t0 = s.t0, d.nq = s.nq, d.first = s.first(), d.node0 = node0;
-                    d.p0 = ranges.owner(item), d.p1 = ranges.owner(item + np - 1);
                     d.begins = at == 0;
+                    d.complete = at == 0 && cnt == np;
                 }
                 mbar_arrive(&sh.seg_full[segs % kSegs]);
             }
@@ -780,9 +782,11 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             const int from = a.window > 0 ? hi - a.window : -1;  // and those behind here
             auto look = [&](int j) {
                 int p = -1;
-                if (j < end && (!keep || __ldg(keep + j))) {
-                    p = __ldg(bt + j);
-                    if (p < 0 || p >= a.P) {
+                if (j < end) {
+                    p = __ldg(bt + j);  // beside the mask: it has the same way to go
+                    if (keep && !__ldg(keep + j)) {
+                        p = -1;
+                    } else if (p < 0 || p >= a.P) {
                         raise_error(a.err, FFD_ERRBIT_BOUNDS);
                         p = -1;
                     }
@@ -848,6 +852,10 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 do {
                     const int k = __ffs(todo) - 1;  // -1: there are no more pages
                     const int p = __shfl_sync(0xffffffffu, page, k & 31), j = todo ? jb + k : -1;
+                    if (j < 0 && lane == 0) {  // before the end is told of
+                        Segment &d = sh.seg[(segs - 1) % kSegs];
+                        d.p0 = ranges.owner(item), d.p1 = ranges.owner(item + np - 1);
+                    }
                     if (kStep == 2 && held < 0 && j >= 0) {
                         held = j;
                         held_page = p;
