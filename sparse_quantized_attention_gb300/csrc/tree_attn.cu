@@ -419,15 +419,36 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                         see0 = visible(j0);
                         if (both) see1 = visible(j1);
                     }
+                    // One tile: rare changes of S are made in tensor memory, which keeps the ordinary way short
+                    // (32 sequences' drafts with a window: 110 us with them in line, 103 so). Two tiles wait
+                    // longer for that than they gain (eight ragged trees 93 in line, 97 so).
+                    auto rewrite = [&](auto change) {
+                        __syncwarp();
+#pragma unroll 1
+                        for (int n = 0; n < (both ? 4 : 2); n++) {
+                            uint32_t y[32];
+                            tmem_load32(y, ts + 32 * n);
+                            tc_wait_load();
+                            change(y, n);
+                            tmem_store32(ts + 32 * n, y);
+                        }
+                        tc_wait_store();
+                    };
+                    if (kTiles == 1 && edge)
+                        rewrite([&](uint32_t (&y)[32], int n) {
+                            const uint32_t see = (uint32_t)((n & 2 ? see1 : see0) >> (32 * (n & 1)));
+#pragma unroll
+                            for (int c = 0; c < 32; c++)
+                                if (!((see >> c) & 1u)) y[c] = 0xff800000u;
+                        });
                     // S by pages, 64 columns; of two pages the second is read twice
                     auto page = [&](uint32_t (&x)[64], int n) {
                         __syncwarp();
                         tmem_load32(reinterpret_cast<uint32_t(&)[32]>(x[0]), ts + 64 * n);
                         tmem_load32(reinterpret_cast<uint32_t(&)[32]>(x[32]), ts + 64 * n + 32);
                         tc_wait_load();
-                        if (edge) {
-                            const uint64_t see = n ? see1 : see0;
-                            const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
+                        if (kTiles == 2 && edge) {
+                            const uint32_t lo = (uint32_t)see0, hi = (uint32_t)(see0 >> 32);
 #pragma unroll
                             for (int c = 0; c < 32; c++) {
                                 if (!((lo >> c) & 1u)) x[c] = 0xff800000u;
@@ -485,11 +506,6 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                     const float2 f2 = make_float2(fx, fx), s2 = make_float2(sub, sub);
                     float2 l2 = make_float2(0.0f, 0.0f), l3 = l2;
                     auto powers = [&](int n) {
-                        if (far) {
-#pragma unroll
-                            for (int c = 0; c < 64; c++)
-                                x[c] = __float_as_uint(__fmul_rn(__uint_as_float(x[c]), fs));
-                        }
                         uint32_t p[32];
 #pragma unroll
                         for (int c = 0; c < 32; c++) {
@@ -503,6 +519,20 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                         __syncwarp();
                         tmem_store32(ts + 32 * n, p);
                     };
+                    if (far) {
+                        if (kTiles == 1) {
+                            rewrite([&](uint32_t (&y)[32], int) {
+#pragma unroll
+                                for (int c = 0; c < 32; c++)
+                                    y[c] = __float_as_uint(__fmul_rn(__uint_as_float(y[c]), fs));
+                            });
+                            page(x, 0);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 64; c++)
+                                x[c] = __float_as_uint(__fmul_rn(__uint_as_float(x[c]), fs));
+                        }
+                    }
                     powers(0);  // P's first 32 columns lie over S's first half, which has been read
                     if (both) {
                         page(x, 1);

@@ -575,13 +575,6 @@ _I64 = torch.int64
 _rope_shapes = {}  # shape of an append -> a reference to its RopeParams
 
 
-def _pages(x, heads=None):
-    """Whether x is a cache of K or V pages."""
-    shape = x.shape
-    return (len(shape) == 4 and shape[2] == PAGE and shape[3] == HEAD_DIM and x.is_contiguous()
-            and (heads is None or shape[1] == heads))
-
-
 def _records(quantized, P, Hkv, dev):
     thumb, resid = quantized
     return (thumb.dtype == _U8 and resid.dtype == _U8 and thumb.shape == (P, Hkv, THUMB_RECORD_BYTES)
@@ -589,6 +582,7 @@ def _records(quantized, P, Hkv, dev):
             and resid.is_contiguous() and thumb.get_device() == dev and resid.get_device() == dev)
 
 
+# (checks are written out flat here too, see above)
 def ffd_rope_append(q, k_new, v_new, inv_freq, positions, block_table, q_out, k_cache, v_cache, *,
                     cu_tokens=None, rope_positions=None, interleaved=False, rot_scale=1.0,
                     quantized=None, error_word=None, stream=None) -> None:
@@ -598,11 +592,11 @@ def ffd_rope_append(q, k_new, v_new, inv_freq, positions, block_table, q_out, k_
     2 * inv_freq.numel() channels are rotated (inv_freq fp32 or None), by rope_positions int32 [T] or
     the tokens' own indices. Rows and tokens are matched as in ffd_kv4_write."""
     where = "ffd_rope_append"
-    if k_new is None or v_new is None or v_cache is None or (q is None) != (q_out is None):
-        _refuse(where, "no rows")
-    if k_cache is None and quantized is None:
-        _refuse(where, "no cache for the keys")
-    dev = v_cache.get_device()
+    if (k_new is None or v_new is None or v_cache is None or (q is None) != (q_out is None)
+            or (k_cache is None and quantized is None)):
+        _refuse(where, "rows, or a cache for them, missing")
+    dev, dtype, cache, new, table = (v_cache.get_device(), k_new.dtype, v_cache.shape, k_new.shape,
+                                     block_table.shape)
     if not (dev >= 0 and k_new.get_device() == dev and v_new.get_device() == dev
             and positions.get_device() == dev and block_table.get_device() == dev
             and (k_cache is None or k_cache.get_device() == dev)
@@ -612,38 +606,53 @@ def ffd_rope_append(q, k_new, v_new, inv_freq, positions, block_table, q_out, k_
             and (cu_tokens is None or cu_tokens.get_device() == dev)
             and (error_word is None or error_word.get_device() == dev)):
         _refuse(where, "tensors on different devices, or not on a GPU")
-    dtype = k_new.dtype
-    if dtype not in _DTYPES or v_cache.dtype != dtype or not _pages(v_cache) or (
-            k_cache is not None and not (k_cache.dtype == dtype and k_cache.shape == v_cache.shape
-                                         and k_cache.is_contiguous())):
+    code = _DTYPES.get(dtype)
+    if not (code is not None and len(cache) == 4 and cache[2] == PAGE and cache[3] == HEAD_DIM
+            and v_cache.dtype is dtype and v_cache.is_contiguous()
+            and (k_cache is None or (k_cache.dtype is dtype and k_cache.shape == cache
+                                     and k_cache.is_contiguous()))):
         _refuse(where, "k_cache and v_cache [P, Hkv, 64, 128] of the rows' dtype, bf16 or fp16")
-    P, Hkv, _, _ = v_cache.shape
+    P, Hkv = cache[0], cache[1]
     if quantized is not None and not _records(quantized, P, Hkv, dev):
         _refuse(where, "the quantised cache")
-    table = block_table.shape
     if len(table) != 2 or not (
-            block_table.dtype == _I32 and positions.dtype == _I32 and positions.shape == table[:1]
-            and block_table.is_contiguous() and positions.is_contiguous()
-            and (cu_tokens is None or (cu_tokens.dtype == _I32 and cu_tokens.is_contiguous()
+            block_table.dtype is _I32 and block_table.is_contiguous() and positions.dtype is _I32
+            and positions.shape == table[:1] and positions.is_contiguous()
+            and (cu_tokens is None or (cu_tokens.dtype is _I32 and cu_tokens.is_contiguous()
                                        and cu_tokens.shape == (table[0] + 1,)))):
         _refuse(where, "int32 positions [B], cu_tokens [B + 1], block_table [B, width]")
-    T = k_new.shape[0] if k_new.dim() == 3 else -1
-    if rope_positions is not None and not (rope_positions.dtype == _I32 and rope_positions.shape == (T,)
+    if not (len(new) == 3 and new[1] == Hkv and new[2] == HEAD_DIM and v_new.dtype is dtype
+            and v_new.shape == new):
+        _refuse(where, "rows of one dtype: k_new, v_new [T, Hkv, 128]")
+    T, rot = new[0], 0
+    if rope_positions is not None and not (rope_positions.dtype is _I32 and rope_positions.shape == (T,)
                                            and rope_positions.is_contiguous()):
         _refuse(where, "int32 rope_positions [T]")
-    rot = 0
     if inv_freq is not None:
-        if not (inv_freq.dtype == _F32 and inv_freq.dim() == 1 and inv_freq.is_contiguous()):
+        if not (inv_freq.dtype is _F32 and inv_freq.dim() == 1 and inv_freq.is_contiguous()):
             _refuse(where, "inv_freq fp32 [rotated channels / 2]")
-        rot = 2 * inv_freq.shape[0]
+        rot = 2 * inv_freq.numel()
     if error_word is not None and error_word.nbytes < 4:
         _refuse(where, "an error word of 4 bytes")
-    Hq, qs, qos = 0, 0, 0
-    if q is not None:
-        Hq = q.shape[1] if q.dim() == 3 else 0
-        qs, qos = _row_stride(q, T, Hq, dtype), _row_stride(q_out, T, Hq, dtype)
-    ks, vs = _row_stride(k_new, T, Hkv, dtype), _row_stride(v_new, T, Hkv, dtype)
-    if qs is None or qos is None or ks is None or vs is None:
+    # elements between rows, which may lie inside wider ones
+    ks, a, b = k_new.stride()
+    vs, c, d = v_new.stride()
+    row, fine = Hkv * HEAD_DIM, b == 1 and d == 1 and (Hkv == 1 or a == c == HEAD_DIM)
+    if T <= 1:
+        ks, vs, fine = row, row, fine or T == 0
+    Hq = qs = qos = 0
+    if q is not None and fine:
+        shape = q.shape
+        fine = (len(shape) == 3 and shape[0] == T and shape[2] == HEAD_DIM and q.dtype is dtype
+                and q_out.dtype is dtype and q_out.shape == shape)
+        if fine:
+            Hq = shape[1]
+            qs, a, b = q.stride()
+            qos, c, d = q_out.stride()
+            fine = b == 1 and d == 1 and (Hq == 1 or a == c == HEAD_DIM)
+            if T <= 1:
+                qs, qos, fine = Hq * HEAD_DIM, Hq * HEAD_DIM, fine or T == 0
+    if not fine:
         _refuse(where, "rows of one dtype: q, q_out [T, Hq, 128], k_new, v_new [T, Hkv, 128]")
     if _C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
@@ -651,18 +660,23 @@ def ffd_rope_append(q, k_new, v_new, inv_freq, positions, block_table, q_out, k_
                                    v_cache, cu_tokens=cu_tokens, rope_positions=rope_positions,
                                    interleaved=interleaved, rot_scale=rot_scale, quantized=quantized,
                                    error_word=error_word, stream=stream)
-    shape = (table[0], Hq, Hkv, HEAD_DIM, PAGE, P, table[1], _DTYPES[dtype], T, rot,
-             1 if interleaved else 0, rot_scale, qs, qos, ks, vs)
+    shape = (table[0], Hq, Hkv, HEAD_DIM, PAGE, P, table[1], code, T, rot, 1 if interleaved else 0,
+             rot_scale, qs, qos, ks, vs)
     ref = _rope_shapes.get(shape)
     if ref is None:
         if len(_rope_shapes) >= 1024:  # ragged batches come in many sizes
             _rope_shapes.clear()
         ref = _rope_shapes[shape] = ctypes.byref(RopeParams(*shape))
-    thumb, resid = (None, None) if quantized is None else quantized
+    thumb, resid = (None, None) if quantized is None else (t.data_ptr() for t in quantized)
     status = (_lib or lib()).ffd_rope_append(
-        ref, _addr(q), k_new.data_ptr(), v_new.data_ptr(), _addr(inv_freq), _addr(rope_positions),
-        _addr(cu_tokens), positions.data_ptr(), block_table.data_ptr(), _addr(q_out), _addr(k_cache),
-        v_cache.data_ptr(), _addr(thumb), _addr(resid), _addr(error_word), _stream_of(stream, dev))
+        ref, None if q is None else q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+        None if inv_freq is None else inv_freq.data_ptr(),
+        None if rope_positions is None else rope_positions.data_ptr(),
+        None if cu_tokens is None else cu_tokens.data_ptr(), positions.data_ptr(),
+        block_table.data_ptr(), None if q is None else q_out.data_ptr(),
+        None if k_cache is None else k_cache.data_ptr(), v_cache.data_ptr(), thumb, resid,
+        None if error_word is None else error_word.data_ptr(),
+        _C._cuda_getCurrentRawStream(dev) if stream is None else _stream_of(stream, dev))
     if status != FFD_OK:
         _check(status, where)
 
@@ -758,7 +772,7 @@ def ffd_tree_commit(draft, target, seq_lens, block_table, k_cache, v_cache, path
     and v_cache [P, Hkv, 64, 128], ``quantized`` a QuantizedCache or None; outputs path int32 [T],
     accepted and new_lens int32 [B], next_token int64 [B]."""
     where = "ffd_tree_commit"
-    dev = v_cache.get_device()
+    dev, cache, table, nodes = v_cache.get_device(), v_cache.shape, block_table.shape, draft.shape
     if not (dev >= 0 and draft.get_device() == dev and target.get_device() == dev
             and seq_lens.get_device() == dev and block_table.get_device() == dev
             and path.get_device() == dev and accepted.get_device() == dev
@@ -768,29 +782,28 @@ def ffd_tree_commit(draft, target, seq_lens, block_table, k_cache, v_cache, path
             and (cu_nodes is None or cu_nodes.get_device() == dev)
             and (error_word is None or error_word.get_device() == dev)):
         _refuse(where, "tensors on different devices, or not on a GPU")
-    if not (_pages(v_cache) and v_cache.dtype in _DTYPES
-            and (k_cache is None or (k_cache.dtype == v_cache.dtype and k_cache.shape == v_cache.shape
+    if not (len(cache) == 4 and cache[2] == PAGE and cache[3] == HEAD_DIM and v_cache.dtype in _DTYPES
+            and v_cache.is_contiguous()
+            and (k_cache is None or (k_cache.dtype is v_cache.dtype and k_cache.shape == cache
                                      and k_cache.is_contiguous()))):
         _refuse(where, "k_cache and v_cache [P, Hkv, 64, 128], bf16 or fp16")
-    P, Hkv, _, _ = v_cache.shape
-    if quantized is not None and not _records(quantized, P, Hkv, dev):
+    if quantized is not None and not _records(quantized, cache[0], cache[1], dev):
         _refuse(where, "the quantised cache")
-    table, nodes = block_table.shape, draft.shape
     if len(table) != 2 or not (
-            block_table.dtype == _I32 and block_table.is_contiguous() and seq_lens.dtype == _I32
-            and seq_lens.shape == table[:1] and seq_lens.is_contiguous() and accepted.dtype == _I32
-            and accepted.shape == table[:1] and accepted.is_contiguous() and new_lens.dtype == _I32
-            and new_lens.shape == table[:1] and new_lens.is_contiguous() and next_token.dtype == _I64
-            and next_token.shape == table[:1] and next_token.is_contiguous()
-            and (cu_nodes is None or (cu_nodes.dtype == _I32 and cu_nodes.is_contiguous()
+            block_table.dtype is _I32 and block_table.is_contiguous()
+            and seq_lens.dtype is _I32 and seq_lens.shape == table[:1] and seq_lens.is_contiguous()
+            and accepted.dtype is _I32 and accepted.shape == table[:1] and accepted.is_contiguous()
+            and new_lens.dtype is _I32 and new_lens.shape == table[:1] and new_lens.is_contiguous()
+            and next_token.dtype is _I64 and next_token.shape == table[:1] and next_token.is_contiguous()
+            and (cu_nodes is None or (cu_nodes.dtype is _I32 and cu_nodes.is_contiguous()
                                       and cu_nodes.shape == (table[0] + 1,)))):
         _refuse(where, "int32 seq_lens, accepted, new_lens [B], cu_nodes [B + 1], block_table [B, width],"
                        " int64 next_token [B]")
     if len(nodes) != 1 or not (
-            draft.dtype == _I64 and draft.is_contiguous() and target.dtype == _I64
-            and target.shape == nodes and target.is_contiguous() and path.dtype == _I32
+            draft.dtype is _I64 and draft.is_contiguous() and target.dtype is _I64
+            and target.shape == nodes and target.is_contiguous() and path.dtype is _I32
             and path.shape == nodes and path.is_contiguous()
-            and (parents is None or (parents.dtype == _I32 and parents.shape == nodes
+            and (parents is None or (parents.dtype is _I32 and parents.shape == nodes
                                      and parents.is_contiguous()))):
         _refuse(where, "int64 draft, target [T], int32 path, parents [T]")
     if error_word is not None and error_word.nbytes < 4:
@@ -800,12 +813,16 @@ def ffd_tree_commit(draft, target, seq_lens, block_table, k_cache, v_cache, path
             return ffd_tree_commit(draft, target, seq_lens, block_table, k_cache, v_cache, path,
                                    accepted, next_token, new_lens, parents=parents, cu_nodes=cu_nodes,
                                    quantized=quantized, error_word=error_word, stream=stream)
-    thumb, resid = (None, None) if quantized is None else quantized
+    thumb, resid = (None, None) if quantized is None else (t.data_ptr() for t in quantized)
+    ref = _descs.get(cache[:2])
     status = (_lib or lib()).ffd_tree_commit(
-        _desc(P, Hkv), table[0], table[1], nodes[0], draft.data_ptr(), target.data_ptr(),
-        _addr(parents), _addr(cu_nodes), seq_lens.data_ptr(), block_table.data_ptr(), _addr(k_cache),
-        v_cache.data_ptr(), _addr(thumb), _addr(resid), path.data_ptr(), accepted.data_ptr(),
-        next_token.data_ptr(), new_lens.data_ptr(), _addr(error_word), _stream_of(stream, dev))
+        _desc(cache[0], cache[1]) if ref is None else ref, table[0], table[1], nodes[0],
+        draft.data_ptr(), target.data_ptr(), None if parents is None else parents.data_ptr(),
+        None if cu_nodes is None else cu_nodes.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
+        None if k_cache is None else k_cache.data_ptr(), v_cache.data_ptr(), thumb, resid,
+        path.data_ptr(), accepted.data_ptr(), next_token.data_ptr(), new_lens.data_ptr(),
+        None if error_word is None else error_word.data_ptr(),
+        _C._cuda_getCurrentRawStream(dev) if stream is None else _stream_of(stream, dev))
     if status != FFD_OK:
         _check(status, where)
 
