@@ -643,27 +643,13 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 }
             }
             const bool run = !named_barrier_or(3, kRows, stopped(sh));
-            const int i = c.node0 + grp * a.tile_nodes + rn;
-            const bool have = rn < a.tile_nodes && i < c.nq;
-            const int64_t at = (int64_t)(c.t0 + i) * a.Hq + c.h * a.G + rg;
             uint32_t rounds = 0;
+            // A thread takes a row and eight channels at a time, rows along the threads. Several rounds of
+            // records come where there are eight channels at most, and no more units than threads.
+            float M = -INFINITY, ls = 0.0f, o[8];
 #pragma unroll 1
             for (int b0 = 0; run && b0 < chs; b0 += block) {
                 const int width = min(block, chs - b0), rec = (width + 2) * pad;  // rec: a record's floats
-                float M = -INFINITY, ls = 0.0f, o[8] = {};
-                auto write = [&](int x0) {
-                    const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
-                    uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + at * kD + ch0 + b0 + x0);
-                    const uint32_t y[4] = {T::pack(o[0] * inv, o[1] * inv), T::pack(o[2] * inv, o[3] * inv),
-                                           T::pack(o[4] * inv, o[5] * inv), T::pack(o[6] * inv, o[7] * inv)};
-                    if (unit == 8) {
-                        *reinterpret_cast<uint4 *>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 4; k++)
-                            if (2 * k < width) dst[k] = y[k];
-                    }
-                };
 #pragma unroll 1
                 for (int r0 = 0; r0 < n; r0 += once) {
                     const int count = min(once, n - r0);
@@ -685,33 +671,49 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                     if (!mbar_drain(&sh.joined, rounds & 1, drain_bound_ns(a.wait_ns)))
                         raise_error(a.err, FFD_ERRBIT_TIMEOUT);
                     rounds++;
-                    if (!have) continue;
-                    const float *mine = buf + grp * kTile + r, *ms = mine + width * pad;
-                    float Mn = M;
-#pragma unroll 4
-                    for (int k = 0; k < count; k++) Mn = fmaxf(Mn, ms[k * rec]);
-                    const float al = M == -INFINITY ? 0.0f : ex2_approx(M - Mn);
-                    M = Mn;
-                    ls *= al;
-                    const float ref = M == -INFINITY ? 0.0f : M;  // nothing in any: o and l are 0
+                    int x0 = 0, q = tid;  // the unit's first channel and row
+                    while (q >= pad) q -= pad, x0 += 8;
 #pragma unroll 1
-                    for (int x0 = 0; x0 < width; x0 += 8) {
+                    while (x0 < width) {
+                        const float *mine = buf + x0 * pad + q, *ms = buf + width * pad + q;
+                        if (r0 == 0) {
+                            M = -INFINITY, ls = 0.0f;
 #pragma unroll
-                        for (int x = 0; x < 8; x++) o[x] = r0 == 0 ? 0.0f : o[x] * al;
+                            for (int x = 0; x < 8; x++) o[x] = 0.0f;
+                        }
 #pragma unroll 2
                         for (int k = 0; k < count; k++) {
-                            const float f = ex2_approx(ms[k * rec] - ref);
-                            if (x0 == 0) ls = fmaf(f, ms[k * rec + pad], ls);
-                            if (f == 0.0f) continue;  // of an empty record, o may hold anything but is 0
+                            const float m = ms[k * rec], Mn = fmaxf(M, m);
+                            if (m == -INFINITY) continue;  // nothing in it: o and l are 0
+                            const float f = ex2_approx(m - Mn), al = ex2_approx(M - Mn);
+                            M = Mn;
+                            ls = fmaf(f, ms[k * rec + pad], ls * al);
 #pragma unroll
                             for (int x = 0; x < 8; x++)
-                                if (x0 + x < width) o[x] = fmaf(f, mine[k * rec + (x0 + x) * pad], o[x]);
+                                if (x0 + x < width) o[x] = fmaf(f, mine[k * rec + x * pad], o[x] * al);
                         }
-                        if (width > 8) write(x0);  // one round then
+                        const int g = q >= kTile, rr = q - g * kTile, node = div_g(a, rr);
+                        const int i = c.node0 + g * a.tile_nodes + node;
+                        if (r0 + count >= n && node < a.tile_nodes && i < c.nq) {
+                            const int64_t at = (int64_t)(c.t0 + i) * a.Hq + c.h * a.G + rr - node * a.G;
+                            const int ch = ch0 + b0 + x0;
+                            const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+                            uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + at * kD + ch);
+                            const uint32_t y[4] = {T::pack(o[0] * inv, o[1] * inv), T::pack(o[2] * inv, o[3] * inv),
+                                                   T::pack(o[4] * inv, o[5] * inv), T::pack(o[6] * inv, o[7] * inv)};
+                            if (unit == 8) {
+                                *reinterpret_cast<uint4 *>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 4; k++)
+                                    if (2 * k < width) dst[k] = y[k];
+                            }
+                            if (a.lse && ch == 0) a.lse[at] = lse_of(M - kShift, ls);
+                        }
+                        q += kRows;
+                        while (q >= pad) q -= pad, x0 += 8;
                     }
                 }
-                if (have && width <= 8) write(0);
-                if (have && a.lse && ch0 + b0 == 0) a.lse[at] = lse_of(M - kShift, ls);
             }
         }
     } else if (warp == H::kCopy) {
