@@ -653,20 +653,15 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
 #pragma unroll 1
                 for (int r0 = 0; r0 < n; r0 += once) {
                     const int count = min(once, n - r0);
-                    fence_proxy_async();
+                    fence_proxy_async_all();
+                    if (tid == 0) mbar_arrive_expect_tx(&sh.joined, count * rec * 4);
                     named_barrier_sync(3, kRows);  // the space has been read
-                    if (warp == 0) {
-                        if (lane == 0) mbar_arrive_expect_tx(&sh.joined, count * rec * 4);
-                        __syncwarp();
-                        fence_proxy_async_all();
-#pragma unroll 1
-                        for (int k = lane; k < count; k += 32) {
-                            const int p = r0 + k;
-                            const float *src =  // a CTA's second record where the item begins, else its first
-                                prm.records + (int64_t)(kSlots * (c.p0 + p) + (p == 0)) * H::kRecord;
-                            tma_load_1d(buf + k * rec, src + (ch0 + b0) * pad, width * pad * 4, &sh.joined);
-                            tma_load_1d(buf + k * rec + width * pad, src + kD * pad, 2 * pad * 4, &sh.joined);
-                        }
+                    for (int k = tid; k < count; k += kRows) {  // a record each
+                        const int p = r0 + k;
+                        const float *src =  // a CTA's second record where the item begins, else its first
+                            prm.records + (int64_t)(kSlots * (c.p0 + p) + (p == 0)) * H::kRecord;
+                        tma_load_1d(buf + k * rec, src + (ch0 + b0) * pad, width * pad * 4, &sh.joined);
+                        tma_load_1d(buf + k * rec + width * pad, src + kD * pad, 2 * pad * 4, &sh.joined);
                     }
                     if (!mbar_drain(&sh.joined, rounds & 1, drain_bound_ns(a.wait_ns)))
                         raise_error(a.err, FFD_ERRBIT_TIMEOUT);
@@ -681,16 +676,24 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
 #pragma unroll
                             for (int x = 0; x < 8; x++) o[x] = 0.0f;
                         }
-#pragma unroll 2
+                        float Mn = M;
+#pragma unroll 8
+                        for (int k = 0; k < count; k++) Mn = fmaxf(Mn, ms[k * rec]);
+                        if (r0 > 0) {
+                            const float al = M == -INFINITY ? 0.0f : ex2_approx(M - Mn);
+                            ls *= al;
+#pragma unroll
+                            for (int x = 0; x < 8; x++) o[x] *= al;
+                        }
+                        M = Mn;
+                        const float ref = M == -INFINITY ? 0.0f : M;  // nothing in any: o and l are 0
+#pragma unroll 4
                         for (int k = 0; k < count; k++) {
-                            const float m = ms[k * rec], Mn = fmaxf(M, m);
-                            if (m == -INFINITY) continue;  // nothing in it: o and l are 0
-                            const float f = ex2_approx(m - Mn), al = ex2_approx(M - Mn);
-                            M = Mn;
-                            ls = fmaf(f, ms[k * rec + pad], ls * al);
+                            const float f = ex2_approx(ms[k * rec] - ref);
+                            ls = fmaf(f, ms[k * rec + pad], ls);
 #pragma unroll
                             for (int x = 0; x < 8; x++)
-                                if (x0 + x < width) o[x] = fmaf(f, mine[k * rec + x * pad], o[x] * al);
+                                if (x0 + x < width) o[x] = fmaf(f, mine[k * rec + x * pad], o[x]);
                         }
                         const int g = q >= kTile, rr = q - g * kTile, node = div_g(a, rr);
                         const int i = c.node0 + g * a.tile_nodes + node;
