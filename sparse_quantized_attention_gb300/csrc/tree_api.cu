@@ -95,6 +95,7 @@ ffd_status make_plan(const ffd_tree_params *p, Plan *pl) {
     if (ctas > kv4::kMaxCtas) ctas = kv4::kMaxCtas;
     pl->ctas = (int)ctas;
     pl->lead = 8 * items <= ctas ? 0 : kItemPages;
+    pl->shares = p->batch <= 32 && groups <= 4 && 2 * items <= ctas;
     size_t off = kAlign;
     pl->tickets = off;
     off = align_up(off + 2 * kv4::kMaxCtas * sizeof(int));
@@ -219,6 +220,7 @@ ffd_status ffd_tree_attention(const ffd_tree_params *params, const void *q, cons
     a.window = p.window;
     a.q_stride = stride;
     a.lead = pl.lead;
+    a.shares = pl.shares;
     a.tile_nodes = kTileRows / a.G;
     a.item_nodes = a.tile_nodes * pl.tiles;
     a.wide_out = aligned(out, 32);

@@ -40,6 +40,7 @@ constexpr int kTile = 128;       // rows of a tile
 constexpr int kPageBytes = kPage * kD * 2;
 constexpr int kInfo = 8;         // steps whose pages are kept
 constexpr int kSegs = 8;         // segments that are kept: copies run at most six ahead of any reader
+constexpr int kStartPages = 4;   // pages' time that a second segment costs a CTA
 constexpr int kSlots = 2;        // records of a CTA: of the item that goes on from before, and that goes on
 constexpr uint32_t kColO = 256;  // O of tile g at kColO + 128 g
 
@@ -161,12 +162,19 @@ __device__ __forceinline__ void item_pages(const AttnArgs &a, const Seq &s, int 
     np = hi < 0 ? 0 : (hi >> 6) - fp + 1;
 }
 
-// What one item weighs: `lead` before its first page and one for each; 0 behind the last one.
+// What one item weighs, 0 behind the last one: `lead` before its first page and one for each.
 __device__ __forceinline__ int item_weight(const AttnArgs &a, const Seq &s, int rt, int groups) {
     if (rt >= groups) return 0;
     int fp, np;
     item_pages(a, s, rt, fp, np);
     return np > 0 ? np + a.lead : 0;
+}
+__device__ __forceinline__ int items_weight(const AttnArgs &a, const Seq &s) {  // of one head
+    const int groups = item_groups(a, s);
+    int w = 0;
+#pragma unroll 1
+    for (int rt = 0; rt < groups; rt++) w += item_weight(a, s, rt, groups);
+    return w;
 }
 
 __device__ __forceinline__ int lane_scan(int v, int lane) {  // sum over the lanes up to this one
@@ -208,7 +216,6 @@ __device__ __forceinline__ int record_rows(const AttnArgs &a, int left) {
 // The weights cut into ncta ranges, the first `more` of them longer by one.
 struct Ranges {
     int each, more;
-    __device__ __forceinline__ Ranges(int total, int ncta) : each(total / ncta), more(total % ncta) {}
     __device__ __forceinline__ int begin(int cta) const { return cta * each + (cta < more ? cta : more); }
     __device__ __forceinline__ int owner(int x) const {  // the CTA whose range holds x
         const int split = more * (each + 1);
@@ -279,9 +286,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         if (warp == H::kCopy) {
             if (lane < a.B) {
                 s = seq_of(a, lane, blockIdx.x == 0);
-                const int groups = item_groups(a, s);
-                for (int rt = 0; rt < groups; rt++) own += item_weight(a, s, rt, groups);
-                own *= a.Hkv;
+                own = items_weight(a, s) * a.Hkv;
             }
         } else if (warp == H::kClean) {
             Seq e = {1, 0, 0};
@@ -296,10 +301,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
 #pragma unroll 1
         for (int b = tid * chunk; b < (tid + 1) * chunk && b < a.B; b++) {
             const Seq e = seq_of(a, b, blockIdx.x == 0);
-            int w = 0;
-            const int groups = item_groups(a, e);
-            for (int rt = 0; rt < groups; rt++) w += item_weight(a, e, rt, groups);
-            own += w * a.Hkv;
+            own += items_weight(a, e) * a.Hkv;
             empty |= e.n == 0 && e.nq > 0;
         }
         empty = __syncthreads_or(empty);
@@ -726,10 +728,35 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             prefetch_tensormap(&prm.tm_k);
             prefetch_tensormap(&prm.tm_v);
         }
-        const int inc = lane_scan(own, lane);
+        int inc = lane_scan(own, lane), per = 0;
         if (few) total = __shfl_sync(0xffffffffu, inc, 31);
-        const int ncta = min(total, (int)gridDim.x);
-        const Ranges ranges(total, max(ncta, 1));
+        int ncta = min(total, (int)gridDim.x);
+        int whole = 0;  // an item's weight where all have the same
+        if (few && a.shares && total > 0) {
+            // Few items of about one length: each in equal shares, so that no CTA has the end of one and the
+            // start of another, unless that leaves too many CTAs without work. Measured, us by shares and cut
+            // regardless: 8 heads of 32768 tokens, 16 nodes 35 37; of 131072 90 94; of 4096, 60 nodes 22 24
+            // (152 CTAs); one head of 32768, 60 nodes 29 33.
+            const int groups = own > 0 ? item_groups(a, s) : 0;
+            int fp, np = 0;
+            if (groups > 0) item_pages(a, s, groups - 1, fp, np);
+            np = __reduce_max_sync(0xffffffffu, np);
+            const int items = __reduce_add_sync(0xffffffffu, groups) * a.Hkv, grid = gridDim.x;
+            const int shares = grid / items;
+            if (shares > 0) {
+                per = (np + shares - 1) / shares;
+                if (per > total / grid + kStartPages) per = 0;
+            }
+            if (per) {
+                whole = shares * per;
+                own = groups * a.Hkv * whole;
+                inc = lane_scan(own, lane);
+                total = items * whole;
+                ncta = items * shares;
+            }
+        }
+        const int lead = per ? 0 : a.lead;
+        const Ranges ranges = per ? Ranges{per, 0} : Ranges{total / max(ncta, 1), total % max(ncta, 1)};
         int x = ranges.begin(cta), b = 0, h = 0, rt = 0, into = 0;
         const int c1 = cta < ncta ? ranges.begin(cta + 1) : x;
         if (cta < ncta) {  // where the range begins: sequence b, head h, group rt, `into` the item's weight
@@ -763,7 +790,8 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             if (groups > 1) {
 #pragma unroll 1
                 for (;; rt += 32) {  // 32 items at a time
-                    const int wt = item_weight(a, s, rt + lane, groups), sum = lane_scan(wt, lane);
+                    const int wt = !whole ? item_weight(a, s, rt + lane, groups) : rt + lane < groups ? whole : 0;
+                    const int sum = lane_scan(wt, lane);
                     const uint32_t past = __ballot_sync(0xffffffffu, sum > rem);
                     if (past) {
                         const int k = __ffs(past) - 1;
@@ -781,8 +809,8 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             int fp = 0, np = 0, item = 0, at = 0, cnt = 0;  // item: its first page in the cut's scale
             if (x < c1) {
                 item_pages(a, s, rt, fp, np);
-                item = x - into + a.lead;
-                at = into > a.lead ? into - a.lead : 0;
+                item = x - into + lead;
+                at = into > lead ? into - lead : 0;
                 cnt = min(np, c1 - item) - at;  // not above 0: the item's pages are the next CTA's
             }
             const int begin = fp + at, end = begin + cnt, node0 = rt * a.item_nodes;
@@ -907,7 +935,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 if (jb >= end) break;
             }
             // ---- the next item that has pages
-            x = item + at + cnt;
+            x = per ? c1 : item + at + cnt;
             into = 0;
             if (x >= c1) continue;
             do {
