@@ -37,7 +37,7 @@ struct CommitArgs {
 // Arguments of an attention call.
 struct AttnArgs {
     int B, Hq, Hkv, G, P, max_blocks, max_q, total_q, window;
-    int lead, shares; // as in Plan
+    int lead, shares, by_mask;  // as in Plan
     int tile_nodes, item_nodes;  // of a tile of 128 rows, of an item
     int wide_out;     // out is aligned to 32 bytes
     uint32_t over_g;  // ceil(2^32 / G), too large by less than G / 2^32 of it (G > 1)
@@ -58,6 +58,7 @@ struct Plan {
     int ctas;
     int lead;   // pages' time that an item counts for besides its pages
     int shares; // whether items may be dealt out in equal shares
+    int by_mask;  // whether a mask's kept blocks are counted, and shared out evenly
     size_t tickets, records, total;
 };
 

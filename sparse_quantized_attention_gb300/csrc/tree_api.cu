@@ -68,6 +68,8 @@ ffd_status check_params(const ffd_tree_params *p) {
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
+// A mask that every CTA reads through before it begins, to share the kept blocks out evenly.
+constexpr int64_t kMaskUnits = 256, kMaskBytes = 1 << 16;
 constexpr int64_t kMinPages = 4;  // of a CTA, at least (upper bound from the table's width)
 
 // Workspace: [error word | two counters per CTA | records per CTA]. The counters, the only part that
@@ -96,6 +98,8 @@ ffd_status make_plan(const ffd_tree_params *p, Plan *pl) {
     pl->ctas = (int)ctas;
     pl->lead = 8 * items <= ctas ? 0 : kItemPages;
     pl->shares = p->batch <= 32 && groups <= 4 && 2 * items <= ctas;
+    pl->by_mask = p->batch <= 32 && groups == 1 && (int64_t)p->batch * p->num_kv_heads <= kMaskUnits &&
+                  (int64_t)p->batch * p->num_kv_heads * p->max_blocks_per_seq <= kMaskBytes;
     size_t off = kAlign;
     pl->tickets = off;
     off = align_up(off + 2 * kv4::kMaxCtas * sizeof(int));
@@ -221,6 +225,7 @@ ffd_status ffd_tree_attention(const ffd_tree_params *params, const void *q, cons
     a.q_stride = stride;
     a.lead = pl.lead;
     a.shares = pl.shares;
+    a.by_mask = keep_in && pl.by_mask;
     a.tile_nodes = kTileRows / a.G;
     a.item_nodes = a.tile_nodes * pl.tiles;
     a.wide_out = aligned(out, 32);

@@ -40,6 +40,7 @@ constexpr int kTile = 128;       // rows of a tile
 constexpr int kPageBytes = kPage * kD * 2;
 constexpr int kInfo = 8;         // steps whose pages are kept
 constexpr int kSegs = 8;         // segments that are kept: copies run at most six ahead of any reader
+constexpr int kMaxUnits = 256;   // (sequence, KV head) pairs whose kept blocks are counted
 constexpr int kStartPages = 4;   // pages' time that a second segment costs a CTA
 constexpr int kSlots = 2;        // records of a CTA: of the item that goes on from before, and that goes on
 constexpr uint32_t kColO = 256;  // O of tile g at kColO + 128 g
@@ -103,6 +104,7 @@ struct Shared {
     uint32_t tmem, aborted;
     int scan[H::kThreads / 32];
     int pre[H::kThreads];                       // weight of all items before each chunk of sequences
+    int kept[kMaxUnits];                        // blocks that a unit's item has, at least one (0: no item)
     Segment shared_item;                        // the item that began before this CTA's range (pages 0: none)
 };
 
@@ -194,6 +196,56 @@ __device__ __forceinline__ int head_weight(const AttnArgs &a, const Seq &s, int 
     return __reduce_add_sync(0xffffffffu, sum);
 }
 
+// The mask's bytes at .. at + 15 behind `base` (aligned to 16), 0 outside [lo, hi): as a word's bytes, those
+// that are not 0 with their top bit set and nothing else.
+__device__ __forceinline__ uint4 mask_chunk(const uint8_t *base, int at, int lo, int hi) {
+    uint32_t w[4] = {0, 0, 0, 0};
+    if (at >= lo && at + 16 <= hi) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(base + at));
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else {
+#pragma unroll 1
+        for (int k = at > lo ? at : lo; k < at + 16 && k < hi; k++) {
+            const uint32_t v = __ldg(base + k) ? 1u << (8 * (k & 3)) : 0u;
+#pragma unroll
+            for (int i = 0; i < 4; i++) w[i] |= (k - at) >> 2 == i ? v : 0u;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) w[i] = (w[i] | ((w[i] & 0x7f7f7f7fu) + 0x7f7f7f7fu)) & 0x80808080u;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ int chunk_count(const uint4 &x) {
+    return __popc(x.x) + __popc(x.y) + __popc(x.z) + __popc(x.w);
+}
+// How many of n blocks from `mask` on are kept, by a warp.
+__device__ __forceinline__ int count_kept(const uint8_t *mask, int n, int lane) {
+    const int lo = (int)(reinterpret_cast<uintptr_t>(mask) & 15);
+    int count = 0;
+#pragma unroll 4
+    for (int at = 16 * lane; at < lo + n; at += 512) count += chunk_count(mask_chunk(mask - lo, at, lo, lo + n));
+    return __reduce_add_sync(0xffffffffu, count);
+}
+// The block of the kept one that k others come before (n: there is none), by a warp.
+__device__ __forceinline__ int find_kept(const uint8_t *mask, int n, int k, int lane) {
+    const int lo = (int)(reinterpret_cast<uintptr_t>(mask) & 15);
+    for (int from = 0; from < lo + n; from += 512) {
+        const uint4 x = mask_chunk(mask - lo, from + 16 * lane, lo, lo + n);
+        const int count = chunk_count(x), sum = lane_scan(count, lane);
+        const uint32_t past = __ballot_sync(0xffffffffu, sum > k);
+        if (past) {
+            const int who = __ffs(past) - 1;
+            int left = k - (sum - count), at = 0;
+            for (uint32_t w[4] = {x.x, x.y, x.z, x.w}; at < 16; at++)
+                if (((at < 8 ? at < 4 ? w[0] : w[1] : at < 12 ? w[2] : w[3]) >> (8 * (at & 3) + 7) & 1u) && left-- == 0)
+                    break;
+            return from + 16 * who + __shfl_sync(0xffffffffu, at, who) - lo;
+        }
+        k -= __shfl_sync(0xffffffffu, sum, 31);
+    }
+    return n;
+}
+
 // Output of a sequence's rows that see nothing, a share of them for each CTA.
 __device__ __noinline__ void write_empty(const AttnArgs &a, int t0, int nq, int thread, int threads) {
     const int64_t rows = (int64_t)nq * a.Hq, first = (int64_t)t0 * a.Hq;
@@ -283,6 +335,16 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     int total = 0, own = 0;
     Seq s = {0, 0, 0};
     if (few) {
+        if (a.by_mask) {  // by all warps
+#pragma unroll 1
+            for (int u = warp; u < a.B * a.Hkv; u += kCtaWarps) {
+                const Seq e = seq_of(a, u / a.Hkv, false);
+                int fp = 0, np = 0;
+                if (e.nq > 0) item_pages(a, e, 0, fp, np);
+                const int kept = count_kept(a.keep_in + (int64_t)u * a.max_blocks + fp, np, lane);
+                if (lane == 0) sh.kept[u] = np > 0 ? max(kept, 1) : 0;
+            }
+        }
         if (warp == H::kCopy) {
             if (lane < a.B) {
                 s = seq_of(a, lane, blockIdx.x == 0);
@@ -477,7 +539,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                     page(x, 0);
                     largest();
                     top *= fs;
-                    const bool raise = top > limit;
+                    const bool raise = have && top > limit;  // (a tile's spare rows hold anything)
                     if (__any_sync(0xffffffffu, raise)) {
                         const float mn = raise ? top : m;
                         const float al = m == -INFINITY ? 0.0f : ex2_approx(m - mn);
@@ -728,11 +790,17 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             prefetch_tensormap(&prm.tm_k);
             prefetch_tensormap(&prm.tm_v);
         }
+        const int several = a.by_mask ? (a.B * a.Hkv + 31) / 32 : 0;  // units of a lane, where blocks are counted
+        if (several) {
+            own = 0;
+            for (int u = several * lane; u < several * (lane + 1) && u < a.B * a.Hkv; u++)
+                own += sh.kept[u] ? sh.kept[u] + a.lead : 0;
+        }
         int inc = lane_scan(own, lane), per = 0;
         if (few) total = __shfl_sync(0xffffffffu, inc, 31);
         int ncta = min(total, (int)gridDim.x);
         int whole = 0;  // an item's weight where all have the same
-        if (few && a.shares && total > 0) {
+        if (few && !several && a.shares && total > 0) {
             // Few items of about one length: each in equal shares, so that no CTA has the end of one and the
             // start of another, unless that leaves too many CTAs without work. Measured, us by shares and cut
             // regardless: 8 heads of 32768 tokens, 16 nodes 35 37; of 131072 90 94; of 4096, 60 nodes 22 24
@@ -764,7 +832,19 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             if (few) {
                 b = __ffs(__ballot_sync(0xffffffffu, inc > x)) - 1;
                 rem -= __shfl_sync(0xffffffffu, inc - own, b);
-                hp = __shfl_sync(0xffffffffu, own, b) / a.Hkv;
+                if (several) {
+                    int u = several * b;
+                    for (;; u++) {
+                        hp = sh.kept[u] ? sh.kept[u] + a.lead : 0;
+                        if (rem < hp) break;
+                        rem -= hp;
+                    }
+                    b = u / a.Hkv;
+                    h = u - b * a.Hkv;
+                    hp = 1 << 30;
+                } else {
+                    hp = __shfl_sync(0xffffffffu, own, b) / a.Hkv;
+                }
                 s.n = __shfl_sync(0xffffffffu, s.n, b);
                 s.t0 = __shfl_sync(0xffffffffu, s.t0, b);
                 s.nq = __shfl_sync(0xffffffffu, s.nq, b);
@@ -784,8 +864,10 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                     rem -= hp * a.Hkv;
                 }
             }
-            h = rem / hp;
-            rem -= h * hp;
+            if (rem >= hp) {
+                h = rem / hp;
+                rem -= h * hp;
+            }
             const int groups = item_groups(a, s);
             if (groups > 1) {
 #pragma unroll 1
@@ -806,22 +888,30 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         }
         bool fine = true;
         while (fine) {
-            int fp = 0, np = 0, item = 0, at = 0, cnt = 0;  // item: its first page in the cut's scale
+            int fp = 0, np = 0, len = 0, item = 0, at = 0, cnt = 0;  // item: its first page in the cut's scale
+            const uint8_t *keep = a.keep_in ? a.keep_in + ((int64_t)b * a.Hkv + h) * a.max_blocks : nullptr;
             if (x < c1) {
                 item_pages(a, s, rt, fp, np);
+                len = several ? sh.kept[b * a.Hkv + h] : np;  // pages that are counted
                 item = x - into + lead;
                 at = into > lead ? into - lead : 0;
-                cnt = min(np, c1 - item) - at;  // not above 0: the item's pages are the next CTA's
+                cnt = min(len, c1 - item) - at;  // not above 0: the item's pages are the next CTA's
             }
-            const int begin = fp + at, end = begin + cnt, node0 = rt * a.item_nodes;
+            int begin = fp + at, end = begin + cnt;
+            if (several && cnt > 0) {
+                begin = at > 0 ? fp + find_kept(keep + fp, np, at, lane) : fp;
+                end = fp + np;
+            }
+            const int node0 = rt * a.item_nodes;
             if (lane == 0) {
                 Segment &d = sh.seg[segs % kSegs];
                 d.pages = cnt > 0 ? cnt : 0;
                 if (cnt > 0) {
-                    d.end = end * kPage;
+                    // (five kept blocks behind the segment's: none of its own holds a node)
+                    d.end = several && len - (at + cnt) >= (kMaxNodes - 1) / kPage + 2 ? 0 : end * kPage;
                     d.h = h, d.t0 = s.t0, d.nq = s.nq, d.first = s.first(), d.node0 = node0;
                     d.begins = at == 0;
-                    d.complete = at == 0 && cnt == np;
+                    d.complete = at == 0 && cnt == len;
                 }
                 mbar_arrive(&sh.seg_full[segs % kSegs]);
             }
@@ -838,21 +928,16 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             }
             segs++;
             const int32_t *bt = a.block_table + (int64_t)b * a.max_blocks;
-            const uint8_t *keep = a.keep_in ? a.keep_in + ((int64_t)b * a.Hkv + h) * a.max_blocks : nullptr;
             int lo, hi;
             item_span(a, s, rt, lo, hi);
             const int seen = a.parents ? lo - 1 : lo;  // tokens up to here are seen by all, but for a window
             const int from = a.window > 0 ? hi - a.window : -1;  // and those behind here
-            auto look = [&](int j) {
+            auto look = [&](int j) {  // -1: dropped, -2: kept, but out of range
                 int p = -1;
                 if (j < end) {
                     p = __ldg(bt + j);  // beside the mask: it has the same way to go
-                    if (keep && !__ldg(keep + j)) {
-                        p = -1;
-                    } else if (p < 0 || p >= a.P) {
-                        raise_error(a.err, FFD_ERRBIT_BOUNDS);
-                        p = -1;
-                    }
+                    if (keep && !__ldg(keep + j)) p = -1;
+                    else if (p < 0 || p >= a.P) p = -2;
                 }
                 return p;
             };
@@ -902,38 +987,33 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 }
                 return true;
             };
-            // The listed pages one by one, the last followed by what is held back and the end (j -1, twice).
             int ahead = look(begin + lane), held = -1, held_page = 0;  // a page that waits for a second one
-            for (int jb = begin; fine; jb += 32) {
+            int left = several ? cnt : INT32_MAX;
+            for (int jb = begin; jb < end && fine && left > 0; jb += 32) {
                 const int page = ahead;
-                uint32_t todo = 0;
-                if (jb < end) {
-                    ahead = look(jb + 32 + lane);
-                    todo = __ballot_sync(0xffffffffu, page >= 0);
-                    if (todo == 0) continue;
-                }
-                do {
-                    const int k = __ffs(todo) - 1;  // -1: there are no more pages
-                    const int p = __shfl_sync(0xffffffffu, page, k & 31), j = todo ? jb + k : -1;
-                    if (j < 0 && lane == 0) {  // before the end is told of
-                        Segment &d = sh.seg[(segs - 1) % kSegs];
-                        d.p0 = ranges.owner(item), d.p1 = ranges.owner(item + np - 1);
-                    }
-                    if (kStep == 2 && held < 0 && j >= 0) {
-                        held = j;
+                ahead = look(jb + 32 + lane);
+                for (uint32_t todo = __ballot_sync(0xffffffffu, page != -1); todo && fine && left > 0;
+                     todo &= todo - 1, left--) {
+                    const int k = __ffs(todo) - 1, p = __shfl_sync(0xffffffffu, page, k);
+                    if (p < 0) {
+                        if (lane == 0) raise_error(a.err, FFD_ERRBIT_BOUNDS);
+                    } else if (kStep == 1) {
+                        fine = push(jb + k, p, -1, -1);
+                    } else if (held < 0) {
+                        held = jb + k;
                         held_page = p;
-                    } else if (kStep == 2 && held >= 0) {
-                        fine = push(held, held_page, j, p);
-                        held = -1;
-                        if (j < 0) continue;  // then the end
                     } else {
-                        fine = push(j, p, -1, -1);
+                        fine = push(held, held_page, jb + k, p);
+                        held = -1;
                     }
-                    todo &= todo - 1;
-                    if (j < 0) break;
-                } while (fine && (todo || jb >= end));
-                if (jb >= end) break;
+                }
             }
+            if (lane == 0) {  // before the end is told of
+                Segment &d = sh.seg[(segs - 1) % kSegs];
+                d.p0 = ranges.owner(item), d.p1 = ranges.owner(item + len - 1);
+            }
+            for (int tail = held < 0; fine && tail < 2; tail++)  // what is held, and the end
+                fine = push(tail ? -1 : held, held_page, -1, -1);
             // ---- the next item that has pages
             x = per ? c1 : item + at + cnt;
             into = 0;
@@ -948,7 +1028,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                     }
                 }
                 item_pages(a, s, rt, fp, np);
-            } while (np == 0);
+            } while (np == 0);  // (an item with pages counts for one block at least)
         }
         if (stopped(sh) && lane == 0) {  // leave nothing in flight
             bool done = segs == 0 || mbar_drain(&sh.q_full, (segs - 1) & 1, drain_bound_ns(a.wait_ns));

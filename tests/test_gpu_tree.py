@@ -442,3 +442,46 @@ def test_many_items_without_a_page(splits, nq):
     keep[5, 1] = 1
     keep[11, 0, 1] = 1
     x.check(keep=keep, num_splits=splits)
+
+
+@pytest.mark.parametrize("splits", [0, 7, 152])
+def test_sparse_masks_over_long_sequences(splits):
+    """Few blocks kept of many, crowded and scattered, rows of the mask on any byte."""
+    gen = torch.Generator().manual_seed(23)
+    x = Problem(7, 1, [90001, 140000, 500], [25, 18, 5], BF16, seed=24, width=2201)
+    keep = torch.zeros((3, 1, 2201), dtype=torch.uint8)
+    keep[0, 0, 1380:1407] = 255                       # the newest, the tree's among them
+    keep[0, 0, 0] = 1
+    keep[1, 0, torch.randperm(2188, generator=gen)[:60]] = 128
+    keep[2, 0, 7] = 2
+    x.check(keep=keep, num_splits=splits)
+    shifted = torch.zeros(3 * 2201 + 5, dtype=torch.uint8, device="cuda")
+    shifted[5:] = keep.flatten().cuda()
+
+    class At:                                          # a mask that begins on an odd byte
+        def cuda(self):
+            return shifted[5:].view(3, 1, 2201)
+    got, z = x.run(keep=At(), num_splits=splits)
+    want, wz = x.run(keep=keep, num_splits=splits)
+    assert torch.equal(got, want) and torch.equal(z, wz)
+    x.bt[1, :1000] = -7                                # kept or not, some of them are out of range
+    x.check(keep=keep, num_splits=splits, want=5)
+
+
+@pytest.mark.parametrize("B,Hkv", [(33, 2), (32, 8), (40, 1), (600, 1)])
+def test_many_sequences(B, Hkv):
+    gen = torch.Generator().manual_seed(B)
+    lens = torch.randint(9, 300, (B,), generator=gen).tolist()
+    nqs = torch.randint(0, 10, (B,), generator=gen).tolist()
+    lens[3], nqs[3] = 5, 5
+    x = Problem(2 * Hkv, Hkv, lens, nqs, F16, seed=B, lead=1)
+    x.check()
+    x.check(num_splits=5, window=40)
+    keep = (torch.rand((B, Hkv, x.bt.shape[1]), generator=gen) < 0.5).to(torch.uint8)
+    x.check(keep=keep)
+    x.check(keep=keep, num_splits=3)
+    # lengths that are shorter than the nodes: those rows see nothing
+    lens = list(x.lens)
+    for b in (1, B // 2, B - 1):
+        lens[b] = max(0, nqs[b] - 1)
+    x.check(lens=lens, want=5)
