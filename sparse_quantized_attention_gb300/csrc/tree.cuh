@@ -37,7 +37,9 @@ struct CommitArgs {
 // Arguments of an attention call.
 struct AttnArgs {
     int B, Hq, Hkv, G, P, max_blocks, max_q, total_q, window;
-    int lead, shares, by_mask;  // as in Plan
+    int lead, shares, groups, by_mask;  // as in Plan
+    // ceil(2^32 / d) of small divisors d, 0 for 1
+    uint32_t over_shares, over_groups, over_heads;
     int tile_nodes, item_nodes;  // of a tile of 128 rows, of an item
     int wide_out;     // out is aligned to 32 bytes
     uint32_t over_g;  // ceil(2^32 / G), too large by less than G / 2^32 of it (G > 1)
@@ -57,7 +59,8 @@ struct Plan {
     int tiles;  // of 128 rows that walk the cache together: 1 or 2
     int ctas;
     int lead;   // pages' time that an item counts for besides its pages
-    int shares; // whether items may be dealt out in equal shares
+    int shares; // equal shares that items may be dealt out in, 0: they may not
+    int groups; // of a sequence's rows, at most
     int by_mask;  // whether a mask's kept blocks are counted, and shared out evenly
     size_t tickets, records, total;
 };

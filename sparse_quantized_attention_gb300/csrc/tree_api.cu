@@ -97,7 +97,8 @@ ffd_status make_plan(const ffd_tree_params *p, Plan *pl) {
     if (ctas > kv4::kMaxCtas) ctas = kv4::kMaxCtas;
     pl->ctas = (int)ctas;
     pl->lead = 8 * items <= ctas ? 0 : kItemPages;
-    pl->shares = p->batch <= 32 && groups <= 4 && 2 * items <= ctas;
+    pl->shares = p->batch <= 32 && groups <= 4 && 2 * items <= ctas ? (int)(ctas / items) : 0;
+    pl->groups = (int)groups;
     pl->by_mask = p->batch <= 32 && groups == 1 && (int64_t)p->batch * p->num_kv_heads <= kMaskUnits &&
                   (int64_t)p->batch * p->num_kv_heads * p->max_blocks_per_seq <= kMaskBytes;
     size_t off = kAlign;
@@ -225,6 +226,11 @@ ffd_status ffd_tree_attention(const ffd_tree_params *params, const void *q, cons
     a.q_stride = stride;
     a.lead = pl.lead;
     a.shares = pl.shares;
+    a.groups = pl.groups;
+    auto over = [](uint32_t d) { return d < 2 ? 0u : (uint32_t)((((uint64_t)1 << 32) + d - 1) / d); };
+    a.over_shares = over(a.shares);
+    a.over_groups = over(a.groups);
+    a.over_heads = over(a.Hkv);
     a.by_mask = keep_in && pl.by_mask;
     a.tile_nodes = kTileRows / a.G;
     a.item_nodes = a.tile_nodes * pl.tiles;

@@ -145,7 +145,7 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, bool report) {
 }
 
 __device__ __forceinline__ int item_groups(const AttnArgs &a, const Seq &s) {
-    return (s.nq + a.item_nodes - 1) / a.item_nodes;
+    return s.nq <= a.item_nodes ? s.nq > 0 : (s.nq + a.item_nodes - 1) / a.item_nodes;
 }
 
 // Positions of an item's rows: at least lo, at most hi. A node's position is not known here; its
@@ -796,37 +796,40 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             for (int u = several * lane; u < several * (lane + 1) && u < a.B * a.Hkv; u++)
                 own += sh.kept[u] ? sh.kept[u] + a.lead : 0;
         }
-        int inc = lane_scan(own, lane), per = 0;
+        const int inc = lane_scan(own, lane);
         if (few) total = __shfl_sync(0xffffffffu, inc, 31);
-        int ncta = min(total, (int)gridDim.x);
-        int whole = 0;  // an item's weight where all have the same
-        if (few && !several && a.shares && total > 0) {
-            // Few items of about one length: each in equal shares, so that no CTA has the end of one and the
-            // start of another, unless that leaves too many CTAs without work. Measured, us by shares and cut
-            // regardless: 8 heads of 32768 tokens, 16 nodes 35 37; of 131072 90 94; of 4096, 60 nodes 22 24
-            // (152 CTAs); one head of 32768, 60 nodes 29 33.
-            const int groups = own > 0 ? item_groups(a, s) : 0;
+        int ncta = min(total, (int)gridDim.x), x, c1, b = 0, h = 0, rt = 0, into = 0, per = 0;
+        if (a.shares > 0 && !several && total > 0) {
+            // Few items, of about one length: each in a.shares equal shares of `per` pages, so that no CTA has the
+            // end of one and the start of another, unless that leaves too many CTAs without work. Measured, us
+            // by shares and cut regardless (152 CTAs): 8 heads of 32768 tokens, 16 nodes 34 37; of 131072
+            // 90 94; of 4096, 60 nodes 22 24; one head of 32768, 60 nodes 28 33.
+            const bool full = lane >= a.B || s.nq > (a.groups - 1) * a.item_nodes;  // all its groups are there
             int fp, np = 0;
-            if (groups > 0) item_pages(a, s, groups - 1, fp, np);
+            if (lane < a.B) item_pages(a, s, a.groups - 1, fp, np);
             np = __reduce_max_sync(0xffffffffu, np);
-            const int items = __reduce_add_sync(0xffffffffu, groups) * a.Hkv, grid = gridDim.x;
-            const int shares = grid / items;
-            if (shares > 0) {
-                per = (np + shares - 1) / shares;
-                if (per > total / grid + kStartPages) per = 0;
-            }
-            if (per) {
-                whole = shares * per;
-                own = groups * a.Hkv * whole;
-                inc = lane_scan(own, lane);
-                total = items * whole;
-                ncta = items * shares;
-            }
+            per = a.over_shares ? (int)__umulhi(np + a.shares - 1, a.over_shares) : np;
+            if (!__all_sync(0xffffffffu, full) || (int64_t)(per - kStartPages) * gridDim.x > total) per = 0;
         }
         const int lead = per ? 0 : a.lead;
         const Ranges ranges = per ? Ranges{per, 0} : Ranges{total / max(ncta, 1), total % max(ncta, 1)};
-        int x = ranges.begin(cta), b = 0, h = 0, rt = 0, into = 0;
-        const int c1 = cta < ncta ? ranges.begin(cta + 1) : x;
+        if (per) {  // item by item: groups of a head, heads, sequences
+            const int item = a.over_shares ? (int)__umulhi(cta, a.over_shares) : cta;
+            const int unit = a.over_groups ? (int)__umulhi(item, a.over_groups) : item;
+            b = a.over_heads ? (int)__umulhi(unit, a.over_heads) : unit;
+            h = unit - b * a.Hkv;
+            rt = item - unit * a.groups;
+            into = (cta - item * a.shares) * per;
+            x = cta * per;
+            c1 = b < a.B ? x + per : x;
+            s.n = __shfl_sync(0xffffffffu, s.n, b);
+            s.t0 = __shfl_sync(0xffffffffu, s.t0, b);
+            s.nq = __shfl_sync(0xffffffffu, s.nq, b);
+            ncta = 0;  // found
+        } else {
+            x = ranges.begin(cta);
+            c1 = cta < ncta ? ranges.begin(cta + 1) : x;
+        }
         if (cta < ncta) {  // where the range begins: sequence b, head h, group rt, `into` the item's weight
             int rem = x, hp = 1;
             if (few) {
@@ -872,7 +875,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             if (groups > 1) {
 #pragma unroll 1
                 for (;; rt += 32) {  // 32 items at a time
-                    const int wt = !whole ? item_weight(a, s, rt + lane, groups) : rt + lane < groups ? whole : 0;
+                    const int wt = item_weight(a, s, rt + lane, groups);
                     const int sum = lane_scan(wt, lane);
                     const uint32_t past = __ballot_sync(0xffffffffu, sum > rem);
                     if (past) {
@@ -903,6 +906,17 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 end = fp + np;
             }
             const int node0 = rt * a.item_nodes;
+            const int32_t *bt = a.block_table + (int64_t)b * a.max_blocks;
+            auto look = [&](int j) {  // -1: dropped, -2: kept, but out of range
+                int p = -1;
+                if (j < end) {
+                    p = __ldg(bt + j);  // beside the mask: it has the same way to go
+                    if (keep && !__ldg(keep + j)) p = -1;
+                    else if (p < 0 || p >= a.P) p = -2;
+                }
+                return p;
+            };
+            int ahead = cnt > 0 ? look(begin + lane) : -1;  // under way while the segment is described
             if (lane == 0) {
                 Segment &d = sh.seg[segs % kSegs];
                 d.pages = cnt > 0 ? cnt : 0;
@@ -927,20 +941,10 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                                     s.t0 + node0 + g * a.tile_nodes, &sh.q_full);
             }
             segs++;
-            const int32_t *bt = a.block_table + (int64_t)b * a.max_blocks;
             int lo, hi;
             item_span(a, s, rt, lo, hi);
             const int seen = a.parents ? lo - 1 : lo;  // tokens up to here are seen by all, but for a window
             const int from = a.window > 0 ? hi - a.window : -1;  // and those behind here
-            auto look = [&](int j) {  // -1: dropped, -2: kept, but out of range
-                int p = -1;
-                if (j < end) {
-                    p = __ldg(bt + j);  // beside the mask: it has the same way to go
-                    if (keep && !__ldg(keep + j)) p = -1;
-                    else if (p < 0 || p >= a.P) p = -2;
-                }
-                return p;
-            };
             auto edge = [&](int j) { return 64 * j + 63 > seen || 64 * j <= from; };
             // A step of one or two pages (j0 < 0: the segment's end).
             auto push = [&](int j0, int p0, int j1, int p1) {
@@ -987,7 +991,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 }
                 return true;
             };
-            int ahead = look(begin + lane), held = -1, held_page = 0;  // a page that waits for a second one
+            int held = -1, held_page = 0;  // a page that waits for a second one
             int left = several ? cnt : INT32_MAX;
             for (int jb = begin; jb < end && fine && left > 0; jb += 32) {
                 const int page = ahead;
