@@ -583,9 +583,8 @@ typedef struct {
  * values to the paged cache: a decode step's one token per sequence, drafted tokens, or whole prompts,
  * in one launch. Pair i < rot_dim / 2 of a row at position p turns by the angle p * inv_freq[i]:
  *   (x, y) -> rot_scale (x cos - y sin, x sin + y cos),
- * the angle being the product of the integer and the fp32 number without a rounding, taken to within
- * 1e-6 turns' accuracy or better at any position (2e-7 below 2^20); the turn is computed in fp32 and
- * rounded to dtype once. Channels from rot_dim on pass as they are. Quantised keys are those that
+ * the angle being the product of the integer and the fp32 number without a rounding, good to 1e-7 of a
+ * whole turn (2^24 radians and less); the turn is computed in fp32 and rounded to dtype once. Channels from rot_dim on pass as they are. Quantised keys are those that
  * ffd_quantize_keys writes for the rotated, rounded key.
  *   q, q_out     device [T][Hq][128], or both NULL; q_out may be q itself (same stride), and may not
  *                overlap it, k_new or v_new otherwise
@@ -643,7 +642,8 @@ typedef struct {
 } ffd_tree_params;
 
 /* Bytes of device workspace that ffd_tree_attention needs for these parameters on the current
- * device (0 for parameters that it would reject). */
+ * device (0 for parameters that it would reject): for each CTA 133 KB where max_q_len * G is at most 128
+ * (floor(128 / G) nodes), 266 KB above (40 MB on 152 SMs). */
 size_t ffd_tree_workspace_size(const ffd_tree_params *params);
 
 /*
@@ -658,8 +658,8 @@ size_t ffd_tree_workspace_size(const ffd_tree_params *params);
  * Without parents the nodes are a chain (node i hangs on i - 1): causal attention of drafts in a row or
  * of a chunk of a prompt. A row that sees no token gets out = 0 and lse = -inf. Scores and sums are
  * fp32; a probability enters the product with V as one number of dtype (off by up to 2^-8 of itself in
- * bf16, 2^-11 in fp16), so that relative L2 errors of out against 64 bits over normal data are 2.0e-3
- * (its own rounding: 1.65e-3) and 2.9e-4 (2.1e-4). A query with an infinity or a NaN in it
+ * bf16, 2^-11 in fp16), so that relative L2 errors of out against 64 bits over normal data are 2.3e-3
+ * (its own rounding: 1.7e-3) and 2.9e-4 (2.1e-4). A query with an infinity or a NaN in it
  * leaves its own (row, head) unspecified and no other; so does one whose scores times log2(e) pass
  * fp32's range. A key with one makes the rows that see it unspecified and no other, and so does a value,
  * which makes what they hold infinite or NaN.
