@@ -401,6 +401,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
 
     uint32_t steps = 0, vsteps = 0, turns = 0;  // so far: steps and V pages (ends among them), P V products
     uint32_t segs = 0;
+    bool issuer = false;  // the lane that issues a warp's matrix instructions
     // The next segment's description; null at the range's end or when the CTA has stopped.
     auto next_segment = [&]() -> const Segment * {
         const uint32_t at = segs % kSegs, parity = (segs / kSegs) & 1;
@@ -1045,23 +1046,11 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 item_pages(a, s, rt, fp, np);
             } while (np == 0);  // (an item with pages counts for one block at least)
         }
-        if (stopped(sh) && lane == 0) {  // leave nothing in flight
-            bool done = segs == 0 || mbar_drain(&sh.q_full, (segs - 1) & 1, drain_bound_ns(a.wait_ns));
-            for (uint32_t i = 0; i < H::kNK && i < steps; i++) {
-                const uint32_t last = steps - 1 - i;
-                done &= mbar_drain(&sh.k_full[last % H::kNK], (last / H::kNK) & 1, drain_bound_ns(a.wait_ns));
-            }
-            for (uint32_t i = 0; i < H::kNV && i < vsteps; i++) {
-                const uint32_t last = vsteps - 1 - i;
-                done &= mbar_drain(&sh.v_full[last % H::kNV], (last / H::kNV) & 1, drain_bound_ns(a.wait_ns));
-            }
-            if (!done) raise_error(a.err, FFD_ERRBIT_TIMEOUT);
-        }
     } else if (warp < H::kClean) {
         // ================= matrix instructions of one tile =================
         // The whole warp goes through the steps, so that operand addresses stay warp-uniform; one lane
         // issues.
-        const bool issuer = elect_one();
+        issuer = elect_one();
         const bool scores = warp < H::kValues;
         const int g = warp - (scores ? H::kScores : H::kValues);
         if (scores) {
@@ -1148,11 +1137,6 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 }
             }
         }
-        if (stopped(sh) && issuer) {
-            uint64_t *bar = &sh.drain[warp - H::kScores];
-            tc_commit(bar);
-            if (!mbar_drain(bar, 0, drain_bound_ns(a.wait_ns))) raise_error(a.err, FFD_ERRBIT_TIMEOUT);
-        }
     } else {
         // ================= values that are not finite =================
         bool fine = true;
@@ -1204,6 +1188,27 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (stopped(sh)) {  // leave nothing in flight (a warp may have been through before another's wait ran out)
+        const uint64_t bound = drain_bound_ns(a.wait_ns);
+        bool done = true;
+        if (warp == H::kCopy && lane == 0) {
+            if (segs > 0) done = mbar_drain(&sh.q_full, (segs - 1) & 1, bound);
+            for (uint32_t i = 0; i < H::kNK && i < steps; i++) {
+                const uint32_t last = steps - 1 - i;
+                done &= mbar_drain(&sh.k_full[last % H::kNK], (last / H::kNK) & 1, bound);
+            }
+            for (uint32_t i = 0; i < H::kNV && i < vsteps; i++) {
+                const uint32_t last = vsteps - 1 - i;
+                done &= mbar_drain(&sh.v_full[last % H::kNV], (last / H::kNV) & 1, bound);
+            }
+        } else if (issuer) {
+            uint64_t *bar = &sh.drain[warp - H::kScores];
+            tc_commit(bar);
+            done = mbar_drain(bar, 0, bound);
+        }
+        if (!done) raise_error(a.err, FFD_ERRBIT_TIMEOUT);
+        __syncthreads();
+    }
     __syncwarp();
     if (warp == 0) tmem_free(tmem, 512);
 }

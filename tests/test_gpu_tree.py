@@ -485,3 +485,31 @@ def test_many_sequences(B, Hkv):
     for b in (1, B // 2, B - 1):
         lens[b] = max(0, nqs[b] - 1)
     x.check(lens=lens, want=5)
+
+
+@pytest.mark.parametrize("splits", [0, 1, 3])
+@pytest.mark.parametrize("nq,lens", [(1, [100, 300]), (20, [9000, 100, 2500]), (100, [9000, 100, 2500]),
+                                     (200, [200, 260])])
+def test_a_wait_that_runs_out(nq, lens, splits):
+    """The shortest limit, below the time of a copy: the call ends, waits for its copies before it leaves, and
+    reports it or is right; on a workspace filled with zeros again the next call gives what it gave before."""
+    x = Problem(8, 2, lens, [nq] * len(lens), BF16, seed=nq)
+    want = x.run(num_splits=splits)
+    p = x.params(num_splits=splits, wait_limit_us=1)
+    args = (x.q, x.k, x.v, i32(x.lens), x.bt.cuda())
+    par, cu = i32(x.parents), i32(x.cu)
+    e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    for _ in range(20):
+        out, z = torch.empty_like(want[0]), torch.empty_like(want[1])
+        e0.record()
+        ffd.ffd_tree_attention(p, *args, out, x.ws, parents=par, cu_q=cu, lse=z)
+        e1.record()
+        status = ffd.ffd_get_error(x.ws)
+        assert e0.elapsed_time(e1) < 1500.0  # ms: no wait for what never comes (2 s)
+        assert status in (0, 7)
+        if status == 0:
+            assert torch.equal(out, want[0]) and torch.equal(z, want[1])
+        else:
+            x.ws.zero_()
+        again = x.run(num_splits=splits)
+        assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
