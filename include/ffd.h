@@ -717,7 +717,9 @@ ffd_status ffd_tree_attention(const ffd_tree_params *params, const void *q, cons
  *                 others; rows that belong to nobody are left as they were
  *   accepted      device int32 [B]: the path's length (0 for a sequence without nodes)
  *   next_token    device int64 [B]: the model's token behind the path (-1 for no nodes)
- *   new_lens      device int32 [B]: n - nq + accepted; it must not overlap seq_lens
+ *   new_lens      device int32 [B]: n - nq + accepted
+ * path, accepted, next_token and new_lens must not overlap what is read (draft, target, parents, cu_nodes,
+ * seq_lens, block_table).
  *   error_word    device int32, or NULL: FFD_ERRBIT_BOUNDS for a length, an offset or a number of nodes
  *                 out of range (nothing is moved: accepted 0, next_token -1, new_lens the length
  *                 as given, path -1 where the offsets allow it), a parent as in ffd_tree_attention, or a

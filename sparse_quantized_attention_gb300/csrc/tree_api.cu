@@ -32,7 +32,7 @@ bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(
 // Whether n bytes at p and m bytes at q share any.
 bool overlap(const void *p, int64_t n, const void *q, int64_t m) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q);
-    return x < y + (uintptr_t)m && y < x + (uintptr_t)n;
+    return n > 0 && m > 0 && x < y + (uintptr_t)m && y < x + (uintptr_t)n;
 }
 
 // Bytes from the first to the last of T rows of 16-bit elements.
@@ -280,6 +280,18 @@ ffd_status ffd_tree_commit(const ffd_cache_desc *cache, int32_t batch, int32_t m
     if ((int64_t)max_blocks_per_seq * kPage > INT32_MAX) return FFD_ERR_UNSUPPORTED;
     if ((int64_t)batch * cache->num_kv_heads > INT32_MAX) return FFD_ERR_UNSUPPORTED;  // grid.x
     if (!cu_nodes && total_nodes / batch > kMaxNodes) return FFD_ERR_UNSUPPORTED;
+    // every KV head's block reads the inputs, at its own time, and the first head's writes the results
+    const int64_t B = batch, T = total_nodes;
+    const struct {
+        const void *p;
+        int64_t n;
+    } reads[] = {{draft, 8 * T}, {target, 8 * T}, {parents, parents ? 4 * T : 0},
+                 {cu_nodes, cu_nodes ? 4 * (B + 1) : 0}, {seq_lens, 4 * B},
+                 {block_table, 4 * B * max_blocks_per_seq}},
+      writes[] = {{path, 4 * T}, {accepted, 4 * B}, {next_token, 8 * B}, {new_lens, 4 * B}};
+    for (const auto &r : reads)
+        for (const auto &w : writes)
+            if (overlap(r.p, r.n, w.p, w.n)) return FFD_ERR_INVALID_ARG;
     CommitArgs a{};
     a.B = batch;
     a.Hkv = cache->num_kv_heads;

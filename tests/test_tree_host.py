@@ -146,6 +146,19 @@ def test_commit_refusals(lib, kw, status):
     assert commit(lib, **kw) == status
 
 
+@pytest.mark.parametrize("out", ["path", "acc", "nxt", "lens"])
+@pytest.mark.parametrize("src", ["draft", "target", "par", "cu", "sl", "bt"])
+def test_commit_refuses_outputs_over_inputs(lib, out, src):
+    """One byte in common is enough: the inputs are read by blocks that start at any time."""
+    names = ["draft", "target", "par", "cu", "sl", "bt", "k", "v", "path", "acc", "nxt", "lens"]
+    apart = {n: FAKE + (i << 20) for i, n in enumerate(names)}
+    size = dict(draft=48, target=48, par=24, cu=12, sl=8, bt=24, path=24, acc=8, nxt=16, lens=8)
+    step = 8 if out == "nxt" else 4
+    low = size[src] - 1 - (size[src] - 1) % step     # the output begins in the input's last element
+    assert commit(lib, **{**apart, out: apart[src] + low}) == 1
+    assert commit(lib, **{**apart, src: apart[out] + size[out] - (8 if src in ("draft", "target") else 4)}) == 1
+
+
 # ---- the binding --------------------------------------------------------------------------------
 def rows(T=4, Hq=4, Hkv=2, B=2, P=3, dtype=torch.bfloat16):
     return dict(q=torch.zeros((T, Hq, 128), dtype=dtype), k_new=torch.zeros((T, Hkv, 128), dtype=dtype),
