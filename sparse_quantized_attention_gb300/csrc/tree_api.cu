@@ -25,7 +25,6 @@ constexpr size_t kAlign = 256;
 constexpr int64_t kMaxRows = 1 << 28;  // nodes of a sequence x G
 constexpr int64_t kMaxUnits = 65535;   // (sequence, KV head) pairs of an attention call
 constexpr int kTileRows = 128;         // smallest group of rows that walks the cache together
-constexpr int kItemPages = 9;          // pages' time that a group of rows may count for besides its pages
 
 bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
@@ -96,7 +95,6 @@ ffd_status make_plan(const ffd_tree_params *p, Plan *pl) {
     if (sms > 0 && ctas > sms) ctas = sms;
     if (ctas > kv4::kMaxCtas) ctas = kv4::kMaxCtas;
     pl->ctas = (int)ctas;
-    pl->lead = 8 * items <= ctas ? 0 : kItemPages;
     pl->shares = p->batch <= 32 && groups <= 4 && 2 * items <= ctas ? (int)(ctas / items) : 0;
     pl->groups = (int)groups;
     pl->by_mask = p->batch <= 32 && groups == 1 && (int64_t)p->batch * p->num_kv_heads <= kMaskUnits &&
@@ -224,7 +222,6 @@ ffd_status ffd_tree_attention(const ffd_tree_params *params, const void *q, cons
     a.total_q = p.total_q;
     a.window = p.window;
     a.q_stride = stride;
-    a.lead = pl.lead;
     a.shares = pl.shares;
     a.groups = pl.groups;
     auto over = [](uint32_t d) { return d < 2 ? 0u : (uint32_t)((((uint64_t)1 << 32) + d - 1) / d); };

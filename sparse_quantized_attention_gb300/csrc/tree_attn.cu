@@ -5,9 +5,8 @@
 // such tiles, at a time: an item is one such group of rows over the pages that any of them sees. The pages
 // of all items, concatenated with what each item costs besides, are cut into equal contiguous ranges, one
 // per CTA (one per SM). CTAs that share an item write their parts as records, and those in whose range it
-// does not begin join some of its channels each. In steps of one page (two tiles) or two pages (one tile) a
-// CTA computes for each tile of 128 rows
-//   S = Q K^T   (M 128, N 64 or 128, K 128; both operands in shared memory, S in tensor memory),
+// does not begin join some of its channels each. Page by page a CTA computes for each tile of 128 rows
+//   S = Q K^T   (M 128, N 64, K 128; both operands in shared memory, S in tensor memory),
 //   P = 2^(S - m) in the inputs' type against a reference m that follows the row's maximum lazily: it is
 //       raised, and O rescaled, only when a score passes it by 2^8,
 //   O += P V    (M 128, N 128, K 64 a page; P in tensor memory over S, V in shared memory, O in tensor memory).
@@ -16,7 +15,7 @@
 //
 // Roles: a copy warp goes through the CTA's range, describes each segment (a run of an item's pages) to the
 // others and fetches queries and pages (TMA), running on into the next segment while this one ends; for each
-// tile one warp issues the products for S, up to two steps ahead, and one those with V; four warps a tile do
+// tile one warp issues the products for S, as far ahead as S has places, and one those with V; four warps a tile do
 // its softmax, a row a thread; one warp looks through V where rows see different tokens: a token that some
 // row does not see may hold an infinity or a NaN, which a probability of 0 would not silence, so it is
 // zeroed and the rows that do see it are marked.
@@ -49,8 +48,8 @@ using kv4::lse_of;
 
 constexpr int kTile = 128;       // rows of a tile
 constexpr int kPageBytes = kPage * kD * 2;
-constexpr int kInfo = 8;         // steps whose pages are kept
-constexpr int kSegs = 8;         // segments that are kept: copies run at most six ahead of any reader
+constexpr int kInfo = 8;         // steps whose pages are kept: copies run at most seven ahead of any reader
+constexpr int kSegs = 8;         // segments that are kept; each is a step or more
 constexpr int kMaxUnits = 256;   // (sequence, KV head) pairs whose kept blocks are counted
 constexpr int kStartPages = 4;   // pages' time that a second segment costs a CTA
 constexpr int kSlots = 2;        // records of a CTA: of the item that goes on from before, and that goes on
@@ -73,18 +72,18 @@ struct Shape {
     static constexpr int kValues = kScores + kTiles;         // an issuer of P V a tile,
     static constexpr int kClean = kValues + kTiles;          // V's infinities
     static constexpr int kThreads = 32 * (kClean + 1);
-    static constexpr int kStep = kTiles == 1 ? 2 : 1;        // pages of a step
-    static constexpr int kNK = kTiles == 1 ? 3 : 4;          // steps' K in shared memory
-    static constexpr int kNV = 5;                            // pages' V
+    static constexpr int kNK = kTiles == 1 ? 5 : 4;          // pages' K in shared memory
+    static constexpr int kNV = kTiles == 1 ? 6 : 5;          // pages' V
+    static constexpr int kPlaces = 2;                        // places of S in tensor memory, in turn
     static constexpr int kRecord = 130 * kRows;              // floats of a record: o[128][row], m[row], l[row]
-    // tensor memory columns of S (P over its first half): a tile has two places in turn
+    // tensor memory columns of S (P over its first half)
     static __device__ __forceinline__ uint32_t col_s(int g, uint32_t step) {
-        return 64 * kStep * (2 * g + (step & 1));
+        return 64 * (kPlaces * g + step % kPlaces);
     }
 };
 
-struct Step {  // a step's pages: block indexes (first -1: the segment's end, second -1: one page)
-    int j0, j1;
+struct Step {
+    int j;     // the page's block index, -1: the segment's end
     int edge;  // some row does not see all of it
 };
 
@@ -100,15 +99,15 @@ template <int kTiles>
 struct Shared {
     using H = Shape<kTiles>;
     uint8_t q[kTiles][2 * 16384];               // tile: channels 0-63, then 64-127
-    uint8_t k[H::kNK][H::kStep * kPageBytes];   // the same for a step's tokens
-    uint8_t v[H::kNV][kPageBytes];              // the same for 64 tokens
+    uint8_t k[H::kNK][kPageBytes];              // the same for a page's tokens
+    uint8_t v[H::kNV][kPageBytes];
     uint32_t bits[kMaxNodes / 32][H::kRows];    // nodes that a row sees
     int parent[kTiles][kMaxNodes];
     // barriers, by the number of arrivals: one, kTiles, four
     uint64_t seg_full[kSegs], k_full[H::kNK], v_full[H::kNV], v_ready[H::kNV], q_full, joined;
-    uint64_t s_full[kTiles][2], o_done[kTiles][2], drain[2 * kTiles];
+    uint64_t s_full[kTiles][H::kPlaces], o_done[kTiles][H::kPlaces], drain[2 * kTiles];
     uint64_t k_free[H::kNK], v_free[H::kNV], q_free;
-    uint64_t p_full[kTiles][2], end_of_barriers;
+    uint64_t p_full[kTiles][H::kPlaces], end_of_barriers;
     uint64_t bad[H::kNV];                       // tokens of a page whose V is not finite
     Step info[kInfo];
     Segment seg[kSegs];
@@ -175,12 +174,12 @@ __device__ __forceinline__ void item_pages(const AttnArgs &a, const Seq &s, int 
     np = hi < 0 ? 0 : (hi >> 6) - fp + 1;
 }
 
-// What one item weighs, 0 behind the last one: `lead` before its first page and one for each.
+// What one item weighs, 0 behind the last one: kItemPages before its first page and one for each.
 __device__ __forceinline__ int item_weight(const AttnArgs &a, const Seq &s, int rt, int groups) {
     if (rt >= groups) return 0;
     int fp, np;
     item_pages(a, s, rt, fp, np);
-    return np > 0 ? np + a.lead : 0;
+    return np > 0 ? np + kItemPages : 0;
 }
 __device__ __forceinline__ int items_weight(const AttnArgs &a, const Seq &s) {  // of one head
     const int groups = item_groups(a, s);
@@ -207,8 +206,10 @@ __device__ __forceinline__ int head_weight(const AttnArgs &a, const Seq &s, int 
     return __reduce_add_sync(0xffffffffu, sum);
 }
 
-// The mask's bytes at .. at + 15 behind `base` (aligned to 16), 0 outside [lo, hi): as a word's bytes, those
-// that are not 0 with their top bit set and nothing else.
+// A word's bytes that are not 0 as their top bits.
+__device__ __forceinline__ uint32_t kept_bytes(uint32_t w) { return (w | ((w & 0x7f7f7f7fu) + 0x7f7f7f7fu)) & 0x80808080u; }
+__device__ __forceinline__ int chunk_count(const uint4 &x) { return __popc(x.x) + __popc(x.y) + __popc(x.z) + __popc(x.w); }
+// The mask's bytes at .. at + 15 behind `base` (aligned to 16), 0 outside [lo, hi), by their top bits.
 __device__ __forceinline__ uint4 mask_chunk(const uint8_t *base, int at, int lo, int hi) {
     uint32_t w[4] = {0, 0, 0, 0};
     if (at >= lo && at + 16 <= hi) {
@@ -222,20 +223,20 @@ __device__ __forceinline__ uint4 mask_chunk(const uint8_t *base, int at, int lo,
             for (int i = 0; i < 4; i++) w[i] |= (k - at) >> 2 == i ? v : 0u;
         }
     }
-#pragma unroll
-    for (int i = 0; i < 4; i++) w[i] = (w[i] | ((w[i] & 0x7f7f7f7fu) + 0x7f7f7f7fu)) & 0x80808080u;
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    return make_uint4(kept_bytes(w[0]), kept_bytes(w[1]), kept_bytes(w[2]), kept_bytes(w[3]));
 }
-__device__ __forceinline__ int chunk_count(const uint4 &x) {
-    return __popc(x.x) + __popc(x.y) + __popc(x.z) + __popc(x.w);
-}
-// How many of n blocks from `mask` on are kept, by a warp.
-__device__ __forceinline__ int count_kept(const uint8_t *mask, int n, int lane) {
-    const int lo = (int)(reinterpret_cast<uintptr_t>(mask) & 15);
+// How many of n blocks from `mask` on are kept: the share of one of `lanes` threads.
+__device__ __forceinline__ int count_kept(const uint8_t *mask, int n, int lane, int lanes) {
+    const int before = (int)(-reinterpret_cast<uintptr_t>(mask) & 15);  // bytes before the first 16 aligned ones
+    const int head = before < n ? before : n, chunks = (n - head) >> 4, ends = n - 16 * chunks;
     int count = 0;
 #pragma unroll 4
-    for (int at = 16 * lane; at < lo + n; at += 512) count += chunk_count(mask_chunk(mask - lo, at, lo, lo + n));
-    return __reduce_add_sync(0xffffffffu, count);
+    for (int k = lane; k < chunks; k += lanes) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(mask + head) + k);
+        count += chunk_count(make_uint4(kept_bytes(x.x), kept_bytes(x.y), kept_bytes(x.z), kept_bytes(x.w)));
+    }
+    for (int k = lane; k < ends; k += lanes) count += __ldg(mask + (k < head ? k : k + 16 * chunks)) != 0;
+    return count;
 }
 // The block of the kept one that k others come before (n: there is none), by a warp.
 __device__ __forceinline__ int find_kept(const uint8_t *mask, int n, int k, int lane) {
@@ -322,7 +323,8 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     tree_kernel(const __grid_constant__ Params prm) {
     using H = Shape<kTiles>;
     constexpr int kRows = H::kRows, kThreads = H::kThreads, kCtaWarps = kThreads / 32;
-    constexpr int kStep = H::kStep;
+    constexpr int kPlaces = H::kPlaces;
+    static_assert(H::kNV + 1 < kInfo && H::kNV + 1 < kSegs, "what copies run ahead");
     extern __shared__ uint8_t raw[];
     using Sh = Shared<kTiles>;
     Sh &sh = *reinterpret_cast<Sh *>(align_shared<1024>(raw));
@@ -346,14 +348,21 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     int total = 0, own = 0;
     Seq s = {0, 0, 0};
     if (few) {
-        if (a.by_mask) {  // by all warps
+        if (a.by_mask) {  // by all threads, 4 to 32 a unit
+            const int units = a.B * a.Hkv;
+            int log = 5;
+            while (log > 2 && units << log > kThreads) log--;
 #pragma unroll 1
-            for (int u = warp; u < a.B * a.Hkv; u += kCtaWarps) {
-                const Seq e = seq_of(a, u / a.Hkv, false);
-                int fp = 0, np = 0;
-                if (e.nq > 0) item_pages(a, e, 0, fp, np);
-                const int kept = count_kept(a.keep_in + (int64_t)u * a.max_blocks + fp, np, lane);
-                if (lane == 0) sh.kept[u] = np > 0 ? max(kept, 1) : 0;
+            for (int u0 = 0; u0 < units; u0 += kThreads >> log) {
+                const int u = u0 + (tid >> log), part = tid & ((1 << log) - 1);
+                int fp = 0, np = 0, kept = 0;
+                if (u < units) {
+                    const Seq e = seq_of(a, u / a.Hkv, false);
+                    if (e.nq > 0) item_pages(a, e, 0, fp, np);
+                    kept = count_kept(a.keep_in + (int64_t)u * a.max_blocks + fp, np, part, 1 << log);
+                }
+                for (int o = 1 << log >> 1; o; o >>= 1) kept += __shfl_xor_sync(0xffffffffu, kept, o);
+                if (u < units && part == 0) sh.kept[u] = np > 0 ? max(kept, 1) : 0;
             }
         }
         if (warp == H::kCopy) {
@@ -399,9 +408,9 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
 
-    uint32_t steps = 0, vsteps = 0, turns = 0;  // so far: steps and V pages (ends among them), P V products
-    uint32_t segs = 0;
+    uint32_t steps = 0, segs = 0;  // so far; a segment's end is a step too
     bool issuer = false;  // the lane that issues a warp's matrix instructions
+    uint32_t keys = 0;    // 1 when the copy warp stopped between a page's K and V
     // The next segment's description; null at the range's end or when the CTA has stopped.
     auto next_segment = [&]() -> const Segment * {
         const uint32_t at = segs % kSegs, parity = (segs / kSegs) & 1;
@@ -476,81 +485,35 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             float m = -INFINITY, limit = -INFINITY, l = 0.0f;  // limit: a larger score raises m
             bool any = false, far = false, tainted = false;
             while (true) {
-                const uint32_t buf = steps & 1;
-                if (!waited(a, sh, &sh.s_full[grp][buf], (steps >> 1) & 1)) break;
+                const uint32_t buf = steps % kPlaces, vs = steps % H::kNV;
+                if (!waited(a, sh, &sh.s_full[grp][buf], (steps / kPlaces) & 1)) break;
                 tc_fence_after();
                 const volatile Step &info = sh.info[steps % kInfo];
-                const int j0 = info.j0, j1 = info.j1, edge = info.edge;
+                const int j = info.j, edge = info.edge;
                 const uint32_t ts = tmem + lanes + H::col_s(grp, steps);
-                steps++;
-                if (j0 < 0) {  // arrived at like any other step, so that the phases go by steps
-                    vsteps++;
-                    if (lane == 0) mbar_arrive(&sh.p_full[grp][buf]);
-                    break;
-                }
-                const bool both = kStep == 2 && j1 >= 0;
-                if (active) {
-                    uint64_t see0 = ~0ull, see1 = ~0ull;
-                    if (edge) {
-                        see0 = visible(j0);
-                        if (both) see1 = visible(j1);
-                    }
-                    // One tile: rare changes of S are made in tensor memory, which keeps the ordinary way short
-                    // (32 sequences' drafts with a window: 110 us with them in line, 103 so). Two tiles wait
-                    // longer for that than they gain (eight ragged trees 93 in line, 97 so).
-                    auto rewrite = [&](auto change) {
-                        __syncwarp();
-#pragma unroll 1
-                        for (int n = 0; n < (both ? 4 : 2); n++) {
-                            uint32_t y[32];
-                            tmem_load32(y, ts + 32 * n);
-                            tc_wait_load();
-                            change(y, n);
-                            tmem_store32(ts + 32 * n, y);
-                        }
-                        tc_wait_store();
-                    };
-                    if (kTiles == 1 && edge)
-                        rewrite([&](uint32_t (&y)[32], int n) {
-                            const uint32_t see = (uint32_t)((n & 2 ? see1 : see0) >> (32 * (n & 1)));
-#pragma unroll
-                            for (int c = 0; c < 32; c++)
-                                if (!((see >> c) & 1u)) y[c] = 0xff800000u;
-                        });
-                    // S by pages, 64 columns; of two pages the second is read twice
-                    auto page = [&](uint32_t (&x)[64], int n) {
-                        __syncwarp();
-                        tmem_load32(reinterpret_cast<uint32_t(&)[32]>(x[0]), ts + 64 * n);
-                        tmem_load32(reinterpret_cast<uint32_t(&)[32]>(x[32]), ts + 64 * n + 32);
-                        tc_wait_load();
-                        if (kTiles == 2 && edge) {
-                            const uint32_t lo = (uint32_t)see0, hi = (uint32_t)(see0 >> 32);
-#pragma unroll
-                            for (int c = 0; c < 32; c++) {
-                                if (!((lo >> c) & 1u)) x[c] = 0xff800000u;
-                                if (!((hi >> c) & 1u)) x[32 + c] = 0xff800000u;
-                            }
-                        }
-                    };
+                if (j >= 0 && active) {
+                    const uint64_t see = edge ? visible(j) : ~0ull;
                     uint32_t x[64];
-                    float top = -INFINITY;
-                    auto largest = [&]() {
-                        float t[4] = {top, -INFINITY, -INFINITY, -INFINITY};
+                    __syncwarp();
+                    tmem_load32(reinterpret_cast<uint32_t(&)[32]>(x[0]), ts);
+                    tmem_load32(reinterpret_cast<uint32_t(&)[32]>(x[32]), ts + 32);
+                    tc_wait_load();
+                    if (edge) {
+                        const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
 #pragma unroll
-                        for (int c = 0; c < 64; c += 8)
-#pragma unroll
-                            for (int e = 0; e < 4; e++)
-                                t[e] = fmaxf(t[e], fmaxf(__uint_as_float(x[c + 2 * e]),
-                                                         __uint_as_float(x[c + 2 * e + 1])));
-                        top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-                    };
-                    if (both) {
-                        page(x, 1);
-                        largest();
+                        for (int c = 0; c < 32; c++) {
+                            if (!((lo >> c) & 1u)) x[c] = 0xff800000u;
+                            if (!((hi >> c) & 1u)) x[32 + c] = 0xff800000u;
+                        }
                     }
-                    page(x, 0);
-                    largest();
-                    top *= fs;
+                    float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < 64; c += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            t[e] = fmaxf(t[e], fmaxf(__uint_as_float(x[c + 2 * e]),
+                                                     __uint_as_float(x[c + 2 * e + 1])));
+                    const float top = fs * fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
                     const bool raise = have && top > limit;  // (a tile's spare rows hold anything)
                     if (__any_sync(0xffffffffu, raise)) {
                         const float mn = raise ? top : m;
@@ -561,7 +524,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                         far = __any_sync(0xffffffffu, is_far(m));
                         if (any) {
                             // the last step's P V (a stop is met at the next wait)
-                            waited(a, sh, &sh.o_done[grp][(turns - 1) & 1], ((turns - 1) >> 1) & 1);
+                            waited(a, sh, &sh.o_done[grp][(steps - 1) % kPlaces], ((steps - 1) / kPlaces) & 1);
                             __syncwarp();
                             tc_fence_after();
 #pragma unroll 1
@@ -581,59 +544,37 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                     const float fx = far ? 1.0f : fs;
                     const float2 f2 = make_float2(fx, fx), s2 = make_float2(sub, sub);
                     float2 l2 = make_float2(0.0f, 0.0f), l3 = l2;
-                    auto powers = [&](int n) {
-                        uint32_t p[32];
-#pragma unroll
-                        for (int c = 0; c < 32; c++) {
-                            float2 e = __ffma2_rn(make_float2(__uint_as_float(x[2 * c]),
-                                                              __uint_as_float(x[2 * c + 1])), f2, s2);
-                            e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-                            if (c & 1) l3 = __fadd2_rn(l3, e);
-                            else l2 = __fadd2_rn(l2, e);
-                            p[c] = T::pack(e.x, e.y);
-                        }
-                        __syncwarp();
-                        tmem_store32(ts + 32 * n, p);
-                    };
                     if (far) {
-                        if (kTiles == 1) {
-                            rewrite([&](uint32_t (&y)[32], int) {
 #pragma unroll
-                                for (int c = 0; c < 32; c++)
-                                    y[c] = __float_as_uint(__fmul_rn(__uint_as_float(y[c]), fs));
-                            });
-                            page(x, 0);
-                        } else {
+                        for (int c = 0; c < 64; c++)
+                            x[c] = __float_as_uint(__fmul_rn(__uint_as_float(x[c]), fs));
+                    }
+                    uint32_t p[32];
 #pragma unroll
-                            for (int c = 0; c < 64; c++)
-                                x[c] = __float_as_uint(__fmul_rn(__uint_as_float(x[c]), fs));
-                        }
+                    for (int c = 0; c < 32; c++) {
+                        float2 e = __ffma2_rn(make_float2(__uint_as_float(x[2 * c]),
+                                                          __uint_as_float(x[2 * c + 1])), f2, s2);
+                        e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+                        if (c & 1) l3 = __fadd2_rn(l3, e);
+                        else l2 = __fadd2_rn(l2, e);
+                        p[c] = T::pack(e.x, e.y);
                     }
-                    powers(0);  // P's first 32 columns lie over S's first half, which has been read
-                    if (both) {
-                        page(x, 1);
-                        powers(1);
-                    }
+                    __syncwarp();
+                    tmem_store32(ts, p);  // P's 32 columns lie over S's first half, which has been read
                     l += (l2.x + l2.y) + (l3.x + l3.y);
-                    if (edge) {
-                        for (int n = 0; n < (both ? 2 : 1); n++) {
-                            const uint32_t vs = (vsteps + n) % H::kNV;
-                            if (!waited(a, sh, &sh.v_ready[vs], ((vsteps + n) / H::kNV) & 1)) break;
-                            tainted |= (*reinterpret_cast<volatile uint64_t *>(&sh.bad[vs]) &
-                                        (n ? see1 : see0)) != 0;
-                        }
-                    }
+                    if (edge && waited(a, sh, &sh.v_ready[vs], (steps / H::kNV) & 1))
+                        tainted |= (*reinterpret_cast<volatile uint64_t *>(&sh.bad[vs]) & see) != 0;
                     tc_wait_store();
                     any = true;
                 }
-                vsteps += both ? 2 : 1;
-                turns++;
+                steps++;
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_full[grp][buf]);
+                if (lane == 0) mbar_arrive(&sh.p_full[grp][buf]);  // at a segment's end too
+                if (j < 0) break;
             }
-            if (any) {  // the last step's P V
-                waited(a, sh, &sh.o_done[grp][(turns - 1) & 1], ((turns - 1) >> 1) & 1);
+            if (any) {  // the last page's P V: two steps back, behind it the end
+                waited(a, sh, &sh.o_done[grp][(steps - 2) % kPlaces], ((steps - 2) / kPlaces) & 1);
                 tc_fence_after();
             }
             if (named_barrier_or(3, kRows, stopped(sh))) break;
@@ -806,7 +747,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         if (several) {
             own = 0;
             for (int u = several * lane; u < several * (lane + 1) && u < a.B * a.Hkv; u++)
-                own += sh.kept[u] ? sh.kept[u] + a.lead : 0;
+                own += sh.kept[u] ? sh.kept[u] + kItemPages : 0;
         }
         const int inc = lane_scan(own, lane);
         if (few) total = __shfl_sync(0xffffffffu, inc, 31);
@@ -823,7 +764,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             per = a.over_shares ? (int)__umulhi(np + a.shares - 1, a.over_shares) : np;
             if (!__all_sync(0xffffffffu, full) || (int64_t)(per - kStartPages) * gridDim.x > total) per = 0;
         }
-        const int lead = per ? 0 : a.lead;
+        const int lead = per ? 0 : kItemPages;
         const Ranges ranges = per ? Ranges{per, 0} : Ranges{total / max(ncta, 1), total % max(ncta, 1)};
         if (per) {  // item by item: groups of a head, heads, sequences
             const int item = a.over_shares ? (int)__umulhi(cta, a.over_shares) : cta;
@@ -850,7 +791,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 if (several) {
                     int u = several * b;
                     for (;; u++) {
-                        hp = sh.kept[u] ? sh.kept[u] + a.lead : 0;
+                        hp = sh.kept[u] ? sh.kept[u] + kItemPages : 0;
                         if (rem < hp) break;
                         rem -= hp;
                     }
@@ -958,52 +899,35 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             const int seen = a.parents ? lo - 1 : lo;  // tokens up to here are seen by all, but for a window
             const int from = a.window > 0 ? hi - a.window : -1;  // and those behind here
             auto edge = [&](int j) { return 64 * j + 63 > seen || 64 * j <= from; };
-            // A step of one or two pages (j0 < 0: the segment's end).
-            auto push = [&](int j0, int p0, int j1, int p1) {
-                const uint32_t ks = steps % H::kNK;
+            auto push = [&](int j, int p) {  // a page (j < 0: the segment's end)
+                const uint32_t ks = steps % H::kNK, vs = steps % H::kNV;
                 if (steps >= H::kNK && !waited(a, sh, &sh.k_free[ks], (steps / H::kNK - 1) & 1)) return false;
                 if (lane == 0) {
                     volatile Step &info = sh.info[steps % kInfo];
-                    info.j0 = j0;
-                    info.j1 = j1;
-                    info.edge = j0 >= 0 && (edge(j0) || (j1 >= 0 && edge(j1)));
-                    if (j0 >= 0) {
-                        mbar_arrive_expect_tx(&sh.k_full[ks], (j1 >= 0 ? 2 : 1) * kPageBytes);
-                        if (kStep == 1) {
-                            tma_load_3d(sh.k[ks], &prm.tm_k, 0, (p0 * a.Hkv + h) * kPage, 0, &sh.k_full[ks]);
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 2; c++) {  // channel halves
-                                tma_load_3d(sh.k[ks] + c * 16384, &prm.tm_k, 0, (p0 * a.Hkv + h) * kPage, c,
-                                            &sh.k_full[ks]);
-                                if (j1 >= 0)
-                                    tma_load_3d(sh.k[ks] + c * 16384 + 8192, &prm.tm_k, 0,
-                                                (p1 * a.Hkv + h) * kPage, c, &sh.k_full[ks]);
-                            }
-                        }
+                    info.j = j;
+                    info.edge = j >= 0 && edge(j);
+                    if (j >= 0) {
+                        mbar_arrive_expect_tx(&sh.k_full[ks], kPageBytes);
+                        tma_load_3d(sh.k[ks], &prm.tm_k, 0, (p * a.Hkv + h) * kPage, 0, &sh.k_full[ks]);
                     } else {
                         mbar_arrive(&sh.k_full[ks]);
                     }
                 }
-                steps++;
-                for (int n = 0; n < (j1 >= 0 ? 2 : 1); n++) {
-                    const uint32_t vs = vsteps % H::kNV;
-                    if (vsteps >= H::kNV && !waited(a, sh, &sh.v_free[vs], (vsteps / H::kNV - 1) & 1))
-                        return false;
-                    if (lane == 0) {
-                        if (j0 >= 0) {
-                            mbar_arrive_expect_tx(&sh.v_full[vs], kPageBytes);
-                            tma_load_3d(sh.v[vs], &prm.tm_v, 0, ((n ? p1 : p0) * a.Hkv + h) * kPage, 0,
-                                        &sh.v_full[vs]);
-                        } else {
-                            mbar_arrive(&sh.v_full[vs]);
-                        }
-                    }
-                    vsteps++;
+                if (steps >= H::kNV && !waited(a, sh, &sh.v_free[vs], (steps / H::kNV - 1) & 1)) {
+                    keys = 1;
+                    return false;
                 }
+                if (lane == 0) {
+                    if (j >= 0) {
+                        mbar_arrive_expect_tx(&sh.v_full[vs], kPageBytes);
+                        tma_load_3d(sh.v[vs], &prm.tm_v, 0, (p * a.Hkv + h) * kPage, 0, &sh.v_full[vs]);
+                    } else {
+                        mbar_arrive(&sh.v_full[vs]);
+                    }
+                }
+                steps++;
                 return true;
             };
-            int held = -1, held_page = 0;  // a page that waits for a second one
             int left = several ? cnt : INT32_MAX;
             for (int jb = begin; jb < end && fine && left > 0; jb += 32) {
                 const int page = ahead;
@@ -1013,14 +937,8 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                     const int k = __ffs(todo) - 1, p = __shfl_sync(0xffffffffu, page, k);
                     if (p < 0) {
                         if (lane == 0) raise_error(a.err, FFD_ERRBIT_BOUNDS);
-                    } else if (kStep == 1) {
-                        fine = push(jb + k, p, -1, -1);
-                    } else if (held < 0) {
-                        held = jb + k;
-                        held_page = p;
                     } else {
-                        fine = push(held, held_page, jb + k, p);
-                        held = -1;
+                        fine = push(jb + k, p);
                     }
                 }
             }
@@ -1028,8 +946,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 Segment &d = sh.seg[(segs - 1) % kSegs];
                 d.p0 = ranges.owner(item), d.p1 = ranges.owner(item + len - 1);
             }
-            for (int tail = held < 0; fine && tail < 2; tail++)  // what is held, and the end
-                fine = push(tail ? -1 : held, held_page, -1, -1);
+            fine = fine && push(-1, 0);
             // ---- the next item that has pages
             x = per ? c1 : item + at + cnt;
             into = 0;
@@ -1055,7 +972,6 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         const int g = warp - (scores ? H::kScores : H::kValues);
         if (scores) {
             const uint32_t k0 = smem_u32(sh.k[0]), qd = tc_desc(smem_u32(sh.q[g]));
-            int last0 = -1, last1 = -1;  // the product with V that has P at each of S's places, not waited for
             bool fine = true;
             while (fine) {
                 const Segment *sg = next_segment();
@@ -1063,34 +979,32 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 const bool live = g == 0 || sg->nq - sg->node0 > a.tile_nodes;
                 fine = waited(a, sh, &sh.q_full, (segs - 1) & 1);
                 while (fine) {
-                    const uint32_t ks = steps % H::kNK, buf = steps & 1, d = tmem + H::col_s(g, steps);
-                    const int t = buf ? last1 : last0;
-                    if (t >= 0 && !(fine = waited(a, sh, &sh.o_done[g][t & 1], (t >> 1) & 1))) break;
+                    const uint32_t ks = steps % H::kNK, buf = steps % kPlaces, d = tmem + H::col_s(g, steps);
                     if (!(fine = waited(a, sh, &sh.k_full[ks], (steps / H::kNK) & 1))) break;
-                    tc_fence_after();
                     const volatile Step &info = sh.info[steps % kInfo];
-                    const int pages = __shfl_sync(0xffffffffu, info.j0 < 0 ? 0 : info.j1 < 0 ? 1 : 2, 0);
-                    const uint32_t kd = tc_desc(k0 + ks * (kStep * kPageBytes));
-                    const uint32_t idesc =
-                        (kStep == 2 && pages == 2 ? tc_idesc_f16(128, 128) : tc_idesc_f16(128, 64)) |
-                        Idesc<T>::kType;
+                    const bool page = __shfl_sync(0xffffffffu, info.j, 0) >= 0;
+                    const uint32_t kd = tc_desc(k0 + ks * kPageBytes);
+                    // The place's last P has been taken in (an end: been seen), and its S before. What a tile
+                    // goes round by: nothing is left to do behind it (2048 tokens over 32768, 32/8 heads:
+                    // 771 us with K waited for behind it, 735 so).
+                    if (steps >= kPlaces &&
+                        !(fine = waited(a, sh, &sh.o_done[g][buf], (steps / kPlaces - 1) & 1)))
+                        break;
+                    tc_fence_after();
+                    constexpr uint32_t kIdescS = tc_idesc_f16(128, 64) | Idesc<T>::kType;
                     if (issuer) {
-                        if (pages && live) {
+                        if (page && live) {
 #pragma unroll
                             for (int i = 0; i < 8; i++)  // 16 channels each
                                 tc_mma(d, qd + (i >> 2) * 1024 + (i & 3) * 2,
-                                       kd + (i >> 2) * (512 * kStep) + (i & 3) * 2, idesc, i > 0);
+                                       kd + (i >> 2) * 512 + (i & 3) * 2, kIdescS, i > 0);
                         }
                         tc_commit(&sh.s_full[g][buf]);
                         tc_commit(&sh.k_free[ks]);
-                        if (!pages) tc_commit(&sh.q_free);
+                        if (!page) tc_commit(&sh.q_free);
                     }
                     steps++;
-                    (buf ? last1 : last0) = pages ? (int)turns++ : -1;
-                    if (!pages) {  // the softmax group has seen the end: it is at most one behind
-                        fine = waited(a, sh, &sh.p_full[g][buf], ((steps - 1) >> 1) & 1);
-                        break;
-                    }
+                    if (!page) break;
                 }
             }
         } else {
@@ -1103,37 +1017,26 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 const bool live = g == 0 || sg->nq - sg->node0 > a.tile_nodes;
                 bool add = false;
                 while (true) {
-                    const uint32_t vs0 = vsteps % H::kNV, vs1 = (vsteps + 1) % H::kNV;
-                    if (!(fine = waited(a, sh, &sh.v_ready[vs0], (vsteps / H::kNV) & 1))) break;
+                    const uint32_t vs = steps % H::kNV, buf = steps % kPlaces;
+                    if (!(fine = waited(a, sh, &sh.v_ready[vs], (steps / H::kNV) & 1))) break;
                     const volatile Step &info = sh.info[steps % kInfo];
-                    const int pages = __shfl_sync(0xffffffffu, info.j0 < 0 ? 0 : info.j1 < 0 ? 1 : 2, 0);
-                    if (pages == 2 && !(fine = waited(a, sh, &sh.v_ready[vs1], ((vsteps + 1) / H::kNV) & 1)))
-                        break;
-                    if (pages && !(fine = waited(a, sh, &sh.p_full[g][steps & 1], (steps >> 1) & 1))) break;
+                    const bool page = __shfl_sync(0xffffffffu, info.j, 0) >= 0;
+                    if (!(fine = waited(a, sh, &sh.p_full[g][buf], (steps / kPlaces) & 1))) break;
                     tc_fence_after();
                     const uint32_t p = tmem + H::col_s(g, steps);
                     if (issuer) {
-                        if (pages && live) {
-                            const uint32_t vd0 = tc_desc_mn(v0 + vs0 * kPageBytes, 8192);
-                            const uint32_t vd1 = tc_desc_mn(v0 + vs1 * kPageBytes, 8192);
+                        if (page && live) {
+                            const uint32_t vd = tc_desc_mn(v0 + vs * kPageBytes, 8192);
 #pragma unroll
                             for (int i = 0; i < 4; i++)  // 16 tokens each
-                                tc_mma_ta(d, p + 8 * i, vd0 + 128 * i, kIdescO, add || i > 0);
-                            if (kStep == 2 && pages == 2) {
-#pragma unroll
-                                for (int i = 0; i < 4; i++)
-                                    tc_mma_ta(d, p + 32 + 8 * i, vd1 + 128 * i, kIdescO, true);
-                            }
+                                tc_mma_ta(d, p + 8 * i, vd + 128 * i, kIdescO, add || i > 0);
                         }
-                        if (pages) tc_commit(&sh.o_done[g][turns & 1]);
-                        tc_commit(&sh.v_free[vs0]);
-                        if (pages == 2) tc_commit(&sh.v_free[vs1]);
+                        tc_commit(&sh.o_done[g][buf]);
+                        tc_commit(&sh.v_free[vs]);
                     }
-                    vsteps += pages == 2 ? 2 : 1;
                     steps++;
-                    if (!pages) break;
-                    turns++;
                     add = true;
+                    if (!page) break;
                 }
             }
         }
@@ -1143,11 +1046,11 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         while (fine && next_segment()) {
             bool end = false;
             while (fine && !end) {
-                const uint32_t vs = vsteps % H::kNV;
-                if (!(fine = waited(a, sh, &sh.v_full[vs], (vsteps / H::kNV) & 1))) break;
+                const uint32_t vs = steps % H::kNV;
+                if (!(fine = waited(a, sh, &sh.v_full[vs], (steps / H::kNV) & 1))) break;
                 const volatile Step &info = sh.info[steps % kInfo];
-                const bool edge = info.edge != 0, second = turns > 0;  // turns: pages of the step that are done
-                end = info.j0 < 0;
+                const bool edge = info.edge != 0;
+                end = info.j < 0;
                 if (edge) {
                     uint64_t bad = 0;
                     uint8_t *tile = sh.v[vs];
@@ -1179,9 +1082,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.v_ready[vs]);
-                vsteps++;
-                turns = !second && info.j1 >= 0 ? 1 : 0;
-                steps += turns == 0;
+                steps++;
             }
         }
     }
@@ -1193,12 +1094,12 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         bool done = true;
         if (warp == H::kCopy && lane == 0) {
             if (segs > 0) done = mbar_drain(&sh.q_full, (segs - 1) & 1, bound);
-            for (uint32_t i = 0; i < H::kNK && i < steps; i++) {
-                const uint32_t last = steps - 1 - i;
+            for (uint32_t i = 0; i < H::kNK && i < steps + keys; i++) {
+                const uint32_t last = steps + keys - 1 - i;
                 done &= mbar_drain(&sh.k_full[last % H::kNK], (last / H::kNK) & 1, bound);
             }
-            for (uint32_t i = 0; i < H::kNV && i < vsteps; i++) {
-                const uint32_t last = vsteps - 1 - i;
+            for (uint32_t i = 0; i < H::kNV && i < steps; i++) {
+                const uint32_t last = steps - 1 - i;
                 done &= mbar_drain(&sh.v_full[last % H::kNV], (last / H::kNV) & 1, bound);
             }
         } else if (issuer) {
@@ -1213,14 +1114,14 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     if (warp == 0) tmem_free(tmem, 512);
 }
 
-// The cache's rows as a 3-D tensor {64 channels, rows, 2 channel halves}; a copy takes a page's 64 rows of
-// `halves` halves and lands them as tiles of 64 x 128 B with the 128-byte swizzle.
-bool page_map(CUtensorMap *map, const void *ptr, uint64_t rows, int dtype, uint32_t halves) {
+// The cache's rows as a 3-D tensor {64 channels, rows, 2 channel halves}; a copy takes a page's 64 rows
+// and lands them as two tiles of 64 x 128 B with the 128-byte swizzle.
+bool page_map(CUtensorMap *map, const void *ptr, uint64_t rows, int dtype) {
     auto fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[3] = {64, rows, 2};
     const cuuint64_t strides[2] = {kD * 2, 128};
-    const cuuint32_t box[3] = {64, (cuuint32_t)kPage, halves};
+    const cuuint32_t box[3] = {64, (cuuint32_t)kPage, 2};
     const cuuint32_t step[3] = {1, 1, 1};
     return fn(map,
               dtype == FFD_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
@@ -1276,7 +1177,8 @@ size_t tree_record_bytes(int tiles) {
 cudaError_t launch_tree_attention(const AttnArgs &a, const Plan &pl, int dtype, cudaStream_t stream) {
     Params prm;
     const uint64_t rows = (uint64_t)a.P * a.Hkv * kPage;
-    if (!query_map(&prm.tm_q, a, dtype) || !page_map(&prm.tm_k, a.k, rows, dtype, pl.tiles == 1 ? 1 : 2) || !page_map(&prm.tm_v, a.v, rows, dtype, 2))
+    if (!query_map(&prm.tm_q, a, dtype) || !page_map(&prm.tm_k, a.k, rows, dtype) ||
+        !page_map(&prm.tm_v, a.v, rows, dtype))
         return cudaErrorInvalidValue;
     prm.a = a;
     char *ws = reinterpret_cast<char *>(a.err);
