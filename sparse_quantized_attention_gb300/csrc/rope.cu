@@ -193,7 +193,8 @@ cudaError_t launch_rope_append(RopeArgs a, int dtype, cudaStream_t stream) {
     const int heads = a.Hq + 2 * a.Hkv;
     if (a.T == 0) return cudaSuccess;
     // Rows a warp takes: all of a token's, so that its angles are computed once, unless that leaves SMs
-    // without warps.
+    // without warps. us in a graph with 8 rows a warp, all, and by this rule: one token of 28/4 heads 2.9 4.7 2.9;
+    // of 64 sequences, 32/8 heads 3.3 5.8 3.3; 32768 tokens 135 121 121.
     const int64_t want = (int64_t)a.T * heads / (152 * 32);
     int per = want < heads ? (int)((want + 4 * kBatch - 1) / (4 * kBatch)) * 4 * kBatch : heads;
     if (per < 4 * kBatch) per = 4 * kBatch;

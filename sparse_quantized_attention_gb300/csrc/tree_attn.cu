@@ -348,13 +348,16 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     int total = 0, own = 0;
     Seq s = {0, 0, 0};
     if (few) {
-        if (a.by_mask) {  // by all threads, 4 to 32 a unit
+        if (a.by_mask) {  // by all threads, 4 to 32 a unit; each CTA begins elsewhere, so that not all ask for the same bytes
             const int units = a.B * a.Hkv;
             int log = 5;
             while (log > 2 && units << log > kThreads) log--;
+            const int shift = (int)blockIdx.x * units / (int)gridDim.x;
 #pragma unroll 1
             for (int u0 = 0; u0 < units; u0 += kThreads >> log) {
-                const int u = u0 + (tid >> log), part = tid & ((1 << log) - 1);
+                int u = u0 + (tid >> log);
+                if (u < units && (u += shift) >= units) u -= units;
+                const int part = tid & ((1 << log) - 1);
                 int fp = 0, np = 0, kept = 0;
                 if (u < units) {
                     const Seq e = seq_of(a, u / a.Hkv, false);
