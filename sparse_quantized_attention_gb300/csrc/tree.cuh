@@ -8,11 +8,19 @@ namespace tree {
 
 constexpr int kMaxNodes = FFD_TREE_MAX_NODES;
 constexpr int kMaxPlace = 1 << 24;  // rotary positions are below
+constexpr int kWholePages = 9;  // as many that one CTA takes all
 // Pages' time that an item counts for besides its pages when the pages of a batch are cut into equal ranges: what
 // a CTA spends between two items. us without and with it: eight sequences of 500 to 8000 tokens, 8 heads, 25 nodes
 // 47.6 44.5; 32 sequences of 1000 to 9000, 2 heads 39.8 37.8; four of 131072, 4 heads, 112 rows 170.4 167.6, 96 blocks
 // of them 36.4 33.1.
 constexpr int kItemPages = 9;
+
+// Pages of a CTA, at least, where CTAs share an item of np pages: a page takes 0.45 us and each CTA more about 0.06 of
+// the join, whose sum is least at a third of the square root.
+__host__ __device__ inline int share_pages(int np) {
+    if (np <= kWholePages) return np > 0 ? np : 1;
+    return (int)ceilf(sqrtf((float)np) * (1.0f / 3.0f));
+}
 
 // Arguments of an append.
 struct RopeArgs {

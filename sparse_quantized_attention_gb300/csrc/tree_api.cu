@@ -73,10 +73,6 @@ size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 // Where all keep as many anyway the counting costs: 200 blocks of 16 x 65536 (128 KB) 141 147, 128 of
 // 32 x 131072 (512 KB) 195 232; one sequence of 4096 13.1 13.6.
 constexpr int64_t kMaskUnits = 256, kMaskBytes = 1 << 18;
-// Pages of a CTA, at least (upper bound from the table's width). us with 1, 2, 4, 8, 16 and 32, measured before
-// steps of one page: 4096 tokens, 2 heads, 12 nodes 15.2 15.4 14.9 16.7 21.9 33.1; 1024 tokens 12.6 14.0 15.8 20.6; 4096, 8
-// heads, 60 nodes (4 and up) 21.2 22.1 31.8 52.9.
-constexpr int64_t kMinPages = 4;
 
 // Workspace: [error word | two counters per CTA | records per CTA]. The counters, the only part that
 // has to start at zero, have the same place and size whatever the parameters and are left at zero, so that
@@ -100,12 +96,13 @@ ffd_status make_plan(const ffd_tree_params *p, Plan *pl) {
             const int64_t seen = ((int64_t)p->window + p->max_q_len) / kPage + 2;
             most = most < seen ? most : seen;
         }
-        ctas = (items * most + kMinPages - 1) / kMinPages;
+        const int64_t each = share_pages((int)most);
+        ctas = items * ((most + each - 1) / each);
     }
     if (sms > 0 && ctas > sms) ctas = sms;
     if (ctas > kv4::kMaxCtas) ctas = kv4::kMaxCtas;
     pl->ctas = (int)ctas;
-    pl->shares = p->batch <= 32 && groups <= 4 && 2 * items <= ctas ? (int)(ctas / items) : 0;
+    pl->shares = p->batch <= 32 && groups <= 4 && items <= ctas ? (int)(ctas / items) : 0;
     pl->groups = (int)groups;
     pl->by_mask = p->batch <= 32 && groups == 1 && (int64_t)p->batch * p->num_kv_heads <= kMaskUnits &&
                   (int64_t)p->batch * p->num_kv_heads * p->max_blocks_per_seq <= kMaskBytes;

@@ -4,8 +4,8 @@
 // The query rows of a (sequence, KV head), nq nodes x G heads, are taken a tile of 128 / G whole nodes, or two
 // such tiles, at a time: an item is one such group of rows over the pages that any of them sees. The pages
 // of all items, concatenated with what each item costs besides, are cut into equal contiguous ranges, one
-// per CTA (one per SM). CTAs that share an item write their parts as records, and those in whose range it
-// does not begin join some of its channels each. Page by page a CTA computes for each tile of 128 rows
+// per CTA (one per SM). CTAs that share an item write their parts as records and join some of its channels each;
+// the one in whose range it begins only where that is all it has: it may have another item to join. Page by page a CTA computes for each tile of 128 rows
 //   S = Q K^T   (M 128, N 64, K 128; both operands in shared memory, S in tensor memory),
 //   P = 2^(S - m) in the inputs' type against a reference m that follows the row's maximum lazily: it is
 //       raised, and O rescaled, only when a score passes it by 2^8,
@@ -51,7 +51,7 @@ constexpr int kPageBytes = kPage * kD * 2;
 constexpr int kInfo = 8;         // steps whose pages are kept: copies run at most seven ahead of any reader
 constexpr int kSegs = 8;         // segments that are kept; each is a step or more
 constexpr int kMaxUnits = 256;   // (sequence, KV head) pairs whose kept blocks are counted
-constexpr int kStartPages = 4;   // pages' time that a second segment costs a CTA
+constexpr int kStartPages = 4;   // pages' time that a second segment costs a CTA (0: as if cut regardless; 16: no change)
 constexpr int kSlots = 2;        // records of a CTA: of the item that goes on from before, and that goes on
 constexpr uint32_t kColO = 256;  // O of tile g at kColO + 128 g
 
@@ -92,7 +92,7 @@ struct Segment {  // pages 0: there is none any more
     int h, t0, nq, first;  // KV head, first node's row, nodes, tokens before the tree
     int node0;             // the item's first node
     int begins, complete;  // whether the segment holds the item's first page, and all of them
-    int p0, p1;            // CTAs that share the item (known at the segment's end)
+    int p0, p1, j0;        // CTAs that share the item, the first that joins it (known at the segment's end)
 };
 
 template <int kTiles>
@@ -115,7 +115,7 @@ struct Shared {
     int scan[H::kThreads / 32];
     int pre[H::kThreads];                       // weight of all items before each chunk of sequences
     int kept[kMaxUnits];                        // blocks that a unit's item has, at least one (0: no item)
-    Segment shared_item;                        // the item that began before this CTA's range (pages 0: none)
+    Segment shared_item;                        // the item that this CTA joins (pages 0: none)
 };
 
 struct Params {
@@ -630,15 +630,15 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             }
             if (!complete) {  // joined below
                 fence_proxy_async_all();  // the records are read by bulk copies
-                if (tid == 0 && !begins) sh.shared_item = *sg;
+                if (tid == 0 && cta >= sg->j0) sh.shared_item = *sg;
                 named_barrier_sync(3, kRows);
                 if (tid == 0) add_acq_rel_gpu(prm.tickets + sg->p0, 1);
             }
         }
-        // ---- the item that began before this CTA's range: joined by the CTAs that have such a part
+        // ---- the shared item: it began before this CTA's range, or each CTA has a share of one item
         if (!named_barrier_or(3, kRows, stopped(sh)) && sh.shared_item.pages > 0) {
             const Segment &c = sh.shared_item;
-            const int n = c.p1 - c.p0 + 1, place = cta - c.p0 - 1, of = n - 1;
+            const int n = c.p1 - c.p0 + 1, place = cta - c.j0, of = c.p1 - c.j0 + 1;
             // channels by eights, of many CTAs by twos: at most eight of them then
             const int unit = of <= 16 ? 8 : 2, units = kD / unit;
             const int ch0 = units * place / of * unit, chs = units * (place + 1) / of * unit - ch0;
@@ -756,16 +756,22 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         if (few) total = __shfl_sync(0xffffffffu, inc, 31);
         int ncta = min(total, (int)gridDim.x), x, c1, b = 0, h = 0, rt = 0, into = 0, per = 0;
         if (a.shares > 0 && !several && total > 0) {
-            // Few items, of about one length: each in a.shares equal shares of `per` pages, so that no CTA has the
-            // end of one and the start of another, unless that leaves too many CTAs without work. Measured, us
-            // by shares and cut regardless (152 CTAs): 8 heads of 32768 tokens, 16 nodes 34 37; of 131072
-            // 90 94; of 4096, 60 nodes 22 24; one head of 32768, 60 nodes 28 33.
+            // No more items than CTAs, of about one length: each in equal shares of `per` pages, so that no CTA has
+            // the end of one and the start of another, unless that leaves too many CTAs without work. Measured,
+            // us by shares and cut regardless (152 CTAs): 8 heads of 32768 tokens, 16 nodes 34 37; of 131072
+            // 88 94; one head of 32768, 60 nodes 28 34; ten heads of 8192 19 25.
             const bool full = lane >= a.B || s.nq > (a.groups - 1) * a.item_nodes;  // all its groups are there
-            int fp, np = 0;
-            if (lane < a.B) item_pages(a, s, a.groups - 1, fp, np);
+            int np = 0;  // of the longest item: behind a window the last group's need not be
+#pragma unroll 1
+            for (int g = 0; lane < a.B && g < a.groups; g++) {
+                int fp, own_np;
+                item_pages(a, s, g, fp, own_np);
+                np = max(np, own_np);
+            }
             np = __reduce_max_sync(0xffffffffu, np);
             per = a.over_shares ? (int)__umulhi(np + a.shares - 1, a.over_shares) : np;
             if (!__all_sync(0xffffffffu, full) || (int64_t)(per - kStartPages) * gridDim.x > total) per = 0;
+            else per = max(per, share_pages(np));
         }
         const int lead = per ? 0 : kItemPages;
         const Ranges ranges = per ? Ranges{per, 0} : Ranges{total / max(ncta, 1), total % max(ncta, 1)};
@@ -947,7 +953,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             }
             if (lane == 0) {  // before the end is told of
                 Segment &d = sh.seg[(segs - 1) % kSegs];
-                d.p0 = ranges.owner(item), d.p1 = ranges.owner(item + len - 1);
+                d.p0 = ranges.owner(item), d.p1 = ranges.owner(item + len - 1), d.j0 = d.p0 + (per == 0);
             }
             fine = fine && push(-1, 0);
             // ---- the next item that has pages

@@ -513,3 +513,12 @@ def test_a_wait_that_runs_out(nq, lens, splits):
             x.ws.zero_()
         again = x.run(num_splits=splits)
         assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
+@pytest.mark.parametrize("splits", [0, 4, 8, 20])
+def test_groups_of_a_chunk_behind_a_window(splits):
+    """A chunk's groups of rows see different numbers of pages, the last not always the most."""
+    for nq, n in ((90, 700), (200, 260), (120, 4000)):
+        x = Problem(5, 1, [n], [nq], F16, kind=None, seed=nq)
+        for window in (1, 15, 40, 64, 70, 100, 128, 150, 700):
+            x.check(window=window, num_splits=splits)
