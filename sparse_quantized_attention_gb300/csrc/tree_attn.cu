@@ -50,6 +50,7 @@ constexpr int kTile = 128;       // rows of a tile
 constexpr int kPageBytes = kPage * kD * 2;
 constexpr int kInfo = 8;         // steps whose pages are kept: copies run at most seven ahead of any reader
 constexpr int kSegs = 8;         // segments that are kept; each is a step or more
+constexpr int kMaskStep = 512;   // blocks whose mask a warp looks at together
 constexpr int kMaxUnits = 256;   // (sequence, KV head) pairs whose kept blocks are counted
 constexpr int kStartPages = 4;   // pages' time that a second segment costs a CTA (0: as if cut regardless; 16: no change)
 constexpr int kSlots = 2;        // records of a CTA: of the item that goes on from before, and that goes on
@@ -114,6 +115,7 @@ struct Shared {
     uint32_t tmem, aborted;
     int scan[H::kThreads / 32];
     int pre[H::kThreads];                       // weight of all items before each chunk of sequences
+    uint16_t list[kMaskStep];                   // kept blocks, counted from a step's first
     int kept[kMaxUnits];                        // blocks that a unit's item has, at least one (0: no item)
     Segment shared_item;                        // the item that this CTA joins (pages 0: none)
 };
@@ -238,26 +240,6 @@ __device__ __forceinline__ int count_kept(const uint8_t *mask, int n, int lane, 
     for (int k = lane; k < ends; k += lanes) count += __ldg(mask + (k < head ? k : k + 16 * chunks)) != 0;
     return count;
 }
-// The block of the kept one that k others come before (n: there is none), by a warp.
-__device__ __forceinline__ int find_kept(const uint8_t *mask, int n, int k, int lane) {
-    const int lo = (int)(reinterpret_cast<uintptr_t>(mask) & 15);
-    for (int from = 0; from < lo + n; from += 512) {
-        const uint4 x = mask_chunk(mask - lo, from + 16 * lane, lo, lo + n);
-        const int count = chunk_count(x), sum = lane_scan(count, lane);
-        const uint32_t past = __ballot_sync(0xffffffffu, sum > k);
-        if (past) {
-            const int who = __ffs(past) - 1;
-            int left = k - (sum - count), at = 0;
-            for (uint32_t w[4] = {x.x, x.y, x.z, x.w}; at < 16; at++)
-                if (((at < 8 ? at < 4 ? w[0] : w[1] : at < 12 ? w[2] : w[3]) >> (8 * (at & 3) + 7) & 1u) && left-- == 0)
-                    break;
-            return from + 16 * who + __shfl_sync(0xffffffffu, at, who) - lo;
-        }
-        k -= __shfl_sync(0xffffffffu, sum, 31);
-    }
-    return n;
-}
-
 // Output of a sequence's rows that see nothing, a share of them for each CTA.
 __device__ __noinline__ void write_empty(const AttnArgs &a, int t0, int nq, int thread, int threads) {
     const int64_t rows = (int64_t)nq * a.Hq, first = (int64_t)t0 * a.Hq;
@@ -747,28 +729,32 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             prefetch_tensormap(&prm.tm_v);
         }
         const int several = a.by_mask ? (a.B * a.Hkv + 31) / 32 : 0;  // units of a lane, where blocks are counted
+        int longest = 0;  // pages of the longest of the lane's items
         if (several) {
             own = 0;
-            for (int u = several * lane; u < several * (lane + 1) && u < a.B * a.Hkv; u++)
+            for (int u = several * lane; u < several * (lane + 1) && u < a.B * a.Hkv; u++) {
                 own += sh.kept[u] ? sh.kept[u] + kItemPages : 0;
+                longest = max(longest, sh.kept[u]);
+            }
         }
         const int inc = lane_scan(own, lane);
         if (few) total = __shfl_sync(0xffffffffu, inc, 31);
         int ncta = min(total, (int)gridDim.x), x, c1, b = 0, h = 0, rt = 0, into = 0, per = 0;
-        if (a.shares > 0 && !several && total > 0) {
+        if (a.shares > 0 && total > 0) {
             // No more items than CTAs, of about one length: each in equal shares of `per` pages, so that no CTA has
             // the end of one and the start of another, unless that leaves too many CTAs without work. Measured,
             // us by shares and cut regardless (152 CTAs): 8 heads of 32768 tokens, 16 nodes 34 37; of 131072
             // 88 94; one head of 32768, 60 nodes 28 34; ten heads of 8192 19 25.
             const bool full = lane >= a.B || s.nq > (a.groups - 1) * a.item_nodes;  // all its groups are there
-            int np = 0;  // of the longest item: behind a window the last group's need not be
+            if (!several) {  // (behind a window it need not be the last group's)
 #pragma unroll 1
-            for (int g = 0; lane < a.B && g < a.groups; g++) {
-                int fp, own_np;
-                item_pages(a, s, g, fp, own_np);
-                np = max(np, own_np);
+                for (int g = 0; lane < a.B && g < a.groups; g++) {
+                    int fp, np;
+                    item_pages(a, s, g, fp, np);
+                    longest = max(longest, np);
+                }
             }
-            np = __reduce_max_sync(0xffffffffu, np);
+            const int np = __reduce_max_sync(0xffffffffu, longest);
             per = a.over_shares ? (int)__umulhi(np + a.shares - 1, a.over_shares) : np;
             if (!__all_sync(0xffffffffu, full) || (int64_t)(per - kStartPages) * gridDim.x > total) per = 0;
             else per = max(per, share_pages(np));
@@ -862,11 +848,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 at = into > lead ? into - lead : 0;
                 cnt = min(len, c1 - item) - at;  // not above 0: the item's pages are the next CTA's
             }
-            int begin = fp + at, end = begin + cnt;
-            if (several && cnt > 0) {
-                begin = at > 0 ? fp + find_kept(keep + fp, np, at, lane) : fp;
-                end = fp + np;
-            }
+            const int begin = fp + at, end = several ? fp + np : begin + cnt;
             const int node0 = rt * a.item_nodes;
             const int32_t *bt = a.block_table + (int64_t)b * a.max_blocks;
             auto look = [&](int j) {  // -1: dropped, -2: kept, but out of range
@@ -878,7 +860,13 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 }
                 return p;
             };
-            int ahead = cnt > 0 ? look(begin + lane) : -1;  // under way while the segment is described
+            // under way while the segment is described: pages, or the mask of the item's first blocks
+            const int lo16 = (int)(reinterpret_cast<uintptr_t>(keep + fp) & 15), past = lo16 + np;
+            auto flags_at = [&](int from) { return mask_chunk(keep + fp - lo16, from + 16 * lane, lo16, past); };
+            int ahead = -1;
+            uint4 flags = make_uint4(0, 0, 0, 0);
+            if (cnt > 0 && several) flags = flags_at(0);
+            else if (cnt > 0) ahead = look(begin + lane);
             if (lane == 0) {
                 Segment &d = sh.seg[segs % kSegs];
                 d.pages = cnt > 0 ? cnt : 0;
@@ -937,18 +925,56 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 steps++;
                 return true;
             };
-            int left = several ? cnt : INT32_MAX;
-            for (int jb = begin; jb < end && fine && left > 0; jb += 32) {
-                const int page = ahead;
-                ahead = look(jb + 32 + lane);
-                for (uint32_t todo = __ballot_sync(0xffffffffu, page != -1); todo && fine && left > 0;
-                     todo &= todo - 1, left--) {
-                    const int k = __ffs(todo) - 1, p = __shfl_sync(0xffffffffu, page, k);
-                    if (p < 0) {
-                        if (lane == 0) raise_error(a.err, FFD_ERRBIT_BOUNDS);
-                    } else {
-                        fine = push(jb + k, p);
+            // Pages a batch of 32 at a time. Counted masks are listed first, so that a few kept blocks of many cost
+            // no reads one after another (96 of 2048 blocks: 31.8 us with batches of 32 blocks, LISTED so).
+            int left = cnt, jb = begin;                        // pages to go (counted masks); the next block (others)
+            int next = 0, skip = at, i = 0, all = 0, base = 0;  // counted masks: next step, kept ones to pass, list
+            while (fine) {
+                int block = 0, page = -1;
+                if (several) {
+                    while (i >= all && next < past) {
+                        const int count = chunk_count(flags), sum = lane_scan(count, lane);
+                        all = __shfl_sync(0xffffffffu, sum, 31);
+                        if (skip < all) {
+                            __syncwarp();  // the list has been read
+                            int n = sum - count;
+                            const uint32_t w[4] = {flags.x, flags.y, flags.z, flags.w};
+#pragma unroll
+                            for (int q = 0; q < 4; q++)
+                                for (uint32_t v = w[q]; v; v &= v - 1)
+                                    sh.list[n++] = 16 * lane + 4 * q + ((__ffs(v) - 1) >> 3);
+                            __syncwarp();
+                            i = skip;
+                            skip = 0;
+                            base = fp + next - lo16;
+                        } else {
+                            skip -= all;
+                            i = all = 0;
+                        }
+                        next += kMaskStep;
+                        if (next < past) flags = flags_at(next);
                     }
+                    const int n = min(32, min(all - i, left));
+                    if (n <= 0) break;
+                    if (lane < n) {
+                        block = base + sh.list[i + lane];
+                        page = __ldg(bt + block);
+                        if (page < 0 || page >= a.P) page = -2;
+                    }
+                    i += 32;
+                    left -= n;
+                } else {
+                    if (jb >= end) break;
+                    block = jb + lane;
+                    page = ahead;
+                    jb += 32;
+                    ahead = look(jb + lane);
+                }
+                for (uint32_t todo = __ballot_sync(0xffffffffu, page != -1); todo && fine; todo &= todo - 1) {
+                    const int k = __ffs(todo) - 1, p = __shfl_sync(0xffffffffu, page, k);
+                    const int j = __shfl_sync(0xffffffffu, block, k);
+                    if (p >= 0) fine = push(j, p);
+                    else if (lane == 0) raise_error(a.err, FFD_ERRBIT_BOUNDS);
                 }
             }
             if (lane == 0) {  // before the end is told of

@@ -522,3 +522,15 @@ def test_groups_of_a_chunk_behind_a_window(splits):
         x = Problem(5, 1, [n], [nq], F16, kind=None, seed=nq)
         for window in (1, 15, 40, 64, 70, 100, 128, 150, 700):
             x.check(window=window, num_splits=splits)
+
+
+@pytest.mark.parametrize("share", [0.02, 0.1, 0.5, 0.95])
+@pytest.mark.parametrize("splits", [0, 1, 5])
+def test_masks_of_any_density(share, splits):
+    """Kept blocks are listed 512 blocks at a time and read 32 at a time: few, several batches and nearly all of
+    a list, over tables whose rows begin at any byte."""
+    gen = torch.Generator().manual_seed(7)
+    x = Problem(8, 2, [40000, 33000, 70, 64 * 512], [8, 5, 3, 8], BF16, seed=31, width=641)
+    keep = (torch.rand((4, 2, x.bt.shape[1]), generator=gen) < share).to(torch.uint8) * 0x81
+    x.check(keep=keep, num_splits=splits)
+    x.check(keep=keep, num_splits=splits, window=20000)
