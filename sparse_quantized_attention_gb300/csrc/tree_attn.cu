@@ -22,14 +22,16 @@
 //
 // What bounds it. One tile: memory. A page is 32 KB and takes 0.73 us an SM at the copy rate; the softmax warps
 // are busy for 0.45 of that. Four sequences of 131072 tokens, 4 heads, 112 rows: 169 us in a graph,
-// 6.4 TB/s, of which the first page's way into the CTA (5 us: lengths, tables, copies, each waiting for the one
+// 6.4 TB/s, of which the first page's way into the CTA (4 us: lengths, tables, copies, each waiting for the one
 // before) and the join (5 to 7) are what the floor of 158 lacks. Two tiles: the way round from P to the
-// next but one S of a tile. 2048 query tokens over 32768, 32/8 heads, take 757 us, 1.41 PFLOP/s or 73 % of the measured matrix
-// rate: about 1640 cycles a page, of them 1290 in a row's softmax (the special-function unit's share for
+// next but one S of a tile. 2048 query tokens over 32768, 32/8 heads, take 738 us, 1.44 PFLOP/s or 75 % of the measured matrix
+// rate: about 1600 cycles a page, of them 1270 in a row's softmax (the special-function unit's share for
 // two warps a scheduler is 720) and 640 of matrix instructions for each tile, whose queue both tiles share. A
-// third place for S would take the way apart; O of two tiles and their four places fill tensor memory.
+// third place for S would take the way apart; O of two tiles and their four places fill tensor memory, and with P in
+// shared memory, which frees S's place sooner, P V reads both operands there: 907 us.
 // A short call's time is that of instructions that run once: about 25 cycles each, so set-up is kept short,
-// and by a few warps (4096 tokens, 2 heads: 15 us in a graph, 10 of them around 3 us of pages).
+// and by a few warps. 4096 tokens, 2 heads, three pages a CTA: 12.8 us in a graph, of them 3.4 to the first scores, 2 of
+// pages, 1 of records written, 2 until all others are seen, 2 of copying and 1.5 of joining them.
 #include "kv4_walk.cuh"
 #include "splitkv.cuh"
 #include "tree.cuh"
@@ -926,7 +928,8 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                 return true;
             };
             // Pages a batch of 32 at a time. Counted masks are listed first, so that a few kept blocks of many cost
-            // no reads one after another (96 of 2048 blocks: 31.8 us with batches of 32 blocks, LISTED so).
+            // no reads one after another (64 of up to 2048 blocks, 32 sequences, 4 heads: 95 us with batches of 32
+            // blocks, 79 so).
             int left = cnt, jb = begin;                        // pages to go (counted masks); the next block (others)
             int next = 0, skip = at, i = 0, all = 0, base = 0;  // counted masks: next step, kept ones to pass, list
             while (fine) {
