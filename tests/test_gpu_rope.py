@@ -281,3 +281,22 @@ def test_pages_past_32_bits():
     for t, (p, r) in enumerate(((P - 1, 63), (P - 2, 5))):
         assert torch.equal(k[p, :, r], x[t]) and torch.equal(v[p, :, r], x[t])
     assert int((v[-4:] != 0).any(-1).sum()) == 2 * Hkv and not bool(v[:4].any())
+
+
+def test_token_indexes_past_the_rotary_range():
+    """Without positions of their own, tokens from 2^24 on are appended and reported; with them they are fine."""
+    Hkv, width = 1, (1 << 18) + 1
+    bt = torch.zeros((1, width), dtype=torch.int32, device="cuda")
+    bt[0, -1] = 1
+    x = torch.randn((3, Hkv, 128), generator=torch.Generator().manual_seed(2)).to(BF16).cuda()
+    k = torch.zeros((2, Hkv, 64, 128), dtype=BF16, device="cuda")
+    v, err, f = torch.zeros_like(k), i32([0]), frequencies(128).cuda()
+    first = (1 << 24) - 1
+    ffd.ffd_rope_append(None, x, x, f, i32([first]), bt, None, k, v, error_word=err)
+    assert ffd.ffd_get_error(err) == 6
+    assert torch.equal(v[0, 0, 63], x[0, 0]) and torch.equal(v[1, 0, :2], x[1:, 0])
+    kept = k[0, 0, 63].clone()
+    ffd.ffd_rope_append(None, x, x, f, i32([first]), bt, None, k, v, error_word=err,
+                        rope_positions=i32([first, 0, 0]))
+    assert ffd.ffd_get_error(err) == 0
+    assert torch.equal(k[0, 0, 63], kept) and torch.equal(k[1, 0, :2], x[1:, 0])

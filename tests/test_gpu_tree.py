@@ -534,3 +534,39 @@ def test_masks_of_any_density(share, splits):
     keep = (torch.rand((4, 2, x.bt.shape[1]), generator=gen) < share).to(torch.uint8) * 0x81
     x.check(keep=keep, num_splits=splits)
     x.check(keep=keep, num_splits=splits, window=20000)
+
+
+@pytest.mark.parametrize("nq", [3, 200])
+def test_a_table_that_names_one_page_again_and_again(nq):
+    """2^24 tokens and more, of which all blocks but the last few are one page: as that page's tokens once, each
+    with the weight of its blocks. What 64 bits say of the short sequence, with the sums' rounding over up to
+    1800 pages a CTA (2^-24 of l and of o each: 2.2e-4 together) on top."""
+    G, tail = 4, 5
+    times = 1 << 18
+    n = 64 * (times + tail)
+    x = Problem(G, 1, [64 * (1 + tail)], [nq], BF16, seed=nq)
+    short = x.bt.clone()
+    x.bt = torch.cat([short[:, :1].repeat(1, times), short[:, 1:]], dim=1)
+    got, z = x.run(lens=[n])
+    # by hand: scores of the short sequence, the first page's with log(times) more
+    page = short[0].long().cuda()
+    k = x.k[page, 0].reshape(-1, 128).double()
+    v = x.v[page, 0].reshape(-1, 128).double()
+    s = torch.einsum("ihd,td->iht", x.q[:nq].double(), k) / math.sqrt(128)
+    s[:, :, :64] += math.log(times)
+    see = torch.zeros((nq, k.shape[0]), dtype=torch.bool, device="cuda")
+    see[:, :k.shape[0] - nq] = True
+    for i in range(nq):
+        j = i
+        while j >= 0:
+            see[i, k.shape[0] - nq + j] = True
+            j = x.parents[j]
+    s = s.masked_fill(~see[:, None, :], -math.inf)
+    lse = s.logsumexp(-1)
+    p = (s - lse[..., None]).exp()
+    want = torch.einsum("iht,td->ihd", p, v)
+    size = torch.einsum("iht,td->ihd", p, v.abs())
+    # a probability is off by half a step of bf16, the result by another; the sums as above
+    tol = (2.0 ** -8 + 2.2e-4) * size + 2.0 ** -8 * want.abs() + 1e-6
+    assert bool(((got.double() - want).abs() <= tol).all())
+    assert float((z.double() - lse).abs().max()) <= 2.2e-4 + 1e-5
