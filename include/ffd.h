@@ -626,8 +626,8 @@ typedef struct {
     int32_t page_size;          /* must be 64 */
     int32_t num_pages;          /* P, bound for block_table entries; 64 * P * Hkv <= INT32_MAX */
     int32_t max_blocks_per_seq; /* row stride of block_table; seq_lens[b] <= 64 * this, which
-                                   is <= INT32_MAX as well as
-                                   B * Hkv * (this + 9) * (max_q_len * G / 64 + 1) */
+                                   is <= INT32_MAX, and B * Hkv * (this + 9) *
+                                   (max_q_len * G / 64 + 1) <= INT32_MAX - 4096 */
     int32_t dtype;              /* FFD_DTYPE_BF16 or FFD_DTYPE_F16, of q, k, v and out */
     int32_t max_q_len;          /* >= 1, the most nodes of one sequence; this * G <= 2^28 */
     int32_t total_q;            /* >= 1, rows of q, out, lse and parents */

@@ -105,6 +105,11 @@ __device__ __forceinline__ bool mbar_drain(uint64_t *bar, uint32_t parity, uint6
     return true;
 }
 
+// The line of global memory at p (inside an allocation), on its way to L2.
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 // ---- TMA ------------------------------------------------------------------------------------
 // 1-D bulk copy global -> shared, completion counted on `bar` (16-byte aligned, size % 16 == 0).
 __device__ __forceinline__ void tma_load_1d(void *dst, const void *src, uint32_t bytes,

@@ -24,6 +24,8 @@ namespace {
 constexpr size_t kAlign = 256;
 constexpr int64_t kMaxRows = 1 << 28;  // nodes of a sequence x G
 constexpr int64_t kMaxUnits = 65535;   // (sequence, KV head) pairs of an attention call
+// Pages of all items and what they count for besides, in int32: equal shares may end four pages a CTA behind them.
+constexpr int64_t kMaxWalk = INT32_MAX - 4 * kv4::kMaxCtas;
 constexpr int kTileRows = 128;         // smallest group of rows that walks the cache together
 
 bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
@@ -59,8 +61,8 @@ ffd_status check_params(const ffd_tree_params *p) {
     if ((int64_t)p->num_pages * p->num_kv_heads > INT32_MAX / kPage) return FFD_ERR_UNSUPPORTED;
     const int64_t pages = (int64_t)p->batch * p->num_kv_heads * ((int64_t)p->max_blocks_per_seq + kItemPages);
     const int64_t rows = (int64_t)p->max_q_len * (p->num_q_heads / p->num_kv_heads);
-    if (rows > kMaxRows || pages > INT32_MAX ||
-        pages > INT32_MAX / (rows / 64 + 1))  // a tile has more than 64 rows
+    if (rows > kMaxRows || pages > kMaxWalk ||
+        pages > kMaxWalk / (rows / 64 + 1))  // a tile has more than 64 rows
         return FFD_ERR_UNSUPPORTED;
     return FFD_OK;
 }

@@ -99,6 +99,13 @@ def test_attention_refuses_params(lib, kw, status):
     assert ffd.ffd_tree_workspace_size(p) == 0
 
 
+def test_attention_refuses_walks_past_int32(lib):
+    """B Hkv (blocks + 9) stays below INT32_MAX - 4096: shares of items may end behind the last page."""
+    shape = dict(batch=64, num_q_heads=1, num_kv_heads=1, max_q_len=1, total_q=64)
+    assert ffd.ffd_tree_workspace_size(params(max_blocks_per_seq=33554422, **shape)) == 0
+    assert ffd.ffd_tree_workspace_size(params(max_blocks_per_seq=33554300, **shape)) > 0
+
+
 def test_attention_refuses_shapes_and_pointers(lib):
     p = params()
     need = ffd.ffd_tree_workspace_size(p)
