@@ -71,9 +71,9 @@ size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 // A mask that every CTA reads through before it begins, to share the kept blocks out evenly; a larger one is cut
 // as if all of its blocks were kept. us cut so and evenly, with 8 heads: 64 kept blocks of 16 sequences of 4000
-// to 32768 tokens (64 KB of mask) 143 62, of 32 of 8000 to 65536 (256 KB) 222 125; 96 blocks of 4 x 131072, 4 heads 33.8 29.3.
-// Where all keep as many anyway the counting costs: 200 blocks of 16 x 65536 (128 KB) 141 147, 128 of
-// 32 x 131072 (512 KB) 195 232; one sequence of 4096 13.1 13.6.
+// to 32768 tokens (64 KB of mask) 143 54, of 32 of 8000 to 65536 (256 KB) 222 113; 96 blocks of 4 x 131072, 4 heads
+// 33.8 27.4. Where all keep as many anyway the counting costs: 200 blocks of 16 x 65536 (128 KB) 141 146, 128
+// of 32 x 131072 (512 KB) 195 232; one sequence of 4096 13.1 13.8.
 constexpr int64_t kMaskUnits = 256, kMaskBytes = 1 << 18;
 
 // Workspace: [error word | two counters per CTA | records per CTA]. The counters, the only part that
@@ -83,9 +83,10 @@ ffd_status make_plan(const ffd_tree_params *p, Plan *pl) {
     const ffd_status st = check_params(p);
     if (st != FFD_OK) return st;
     const int64_t nodes = kTileRows / (p->num_q_heads / p->num_kv_heads);  // of a tile
-    // Two tiles share what is read, which pays wherever there are rows for both: us with tiles one by one and two at
-    // a time: four sequences of 32768, 8 heads, 160 rows 152 110, 240 rows 173 114; 4096 rows over 32768 488 391. With rows for one
-    // tile alone the second's warps and memory cost: 64 sequences of 4096, 4 rows 172 for 166.
+    // Two tiles share what is read, which pays wherever there are rows for both. us with tiles one by one and
+    // two at a time: four sequences of 32768, 8 heads, 160 rows 152 110, 240 rows 173 114; 4096 rows over
+    // 32768 488 391. With rows for one tile alone the second's warps and memory cost: 64 sequences of 4096, 4
+    // rows 166 and 172.
     pl->tiles = p->max_q_len <= nodes ? 1 : 2;
     const int64_t groups = (p->max_q_len + pl->tiles * nodes - 1) / (pl->tiles * nodes);
     const int64_t items = (int64_t)p->batch * p->num_kv_heads * groups;

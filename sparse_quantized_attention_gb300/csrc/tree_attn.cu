@@ -5,7 +5,8 @@
 // such tiles, at a time: an item is one such group of rows over the pages that any of them sees. The pages
 // of all items, concatenated with what each item costs besides, are cut into equal contiguous ranges, one
 // per CTA (one per SM). CTAs that share an item write their parts as records and join some of its channels each;
-// the one in whose range it begins only where that is all it has: it may have another item to join. Page by page a CTA computes for each tile of 128 rows
+// the one in whose range it begins only where that is all it has: it may have another item to join. Page by
+// page a CTA computes for each tile of 128 rows
 //   S = Q K^T   (M 128, N 64, K 128; both operands in shared memory, S in tensor memory),
 //   P = 2^(S - m) in the inputs' type against a reference m that follows the row's maximum lazily: it is
 //       raised, and O rescaled, only when a score passes it by 2^8,
@@ -24,14 +25,14 @@
 // are busy for 0.45 of that. Four sequences of 131072 tokens, 4 heads, 112 rows: 169 us in a graph,
 // 6.4 TB/s, of which the first page's way into the CTA (4 us: lengths, tables, copies, each waiting for the one
 // before) and the join (5 to 7) are what the floor of 158 lacks. Two tiles: the way round from P to the
-// next but one S of a tile. 2048 query tokens over 32768, 32/8 heads, take 738 us, 1.44 PFLOP/s or 75 % of the measured matrix
-// rate: about 1600 cycles a page, of them 1270 in a row's softmax (the special-function unit's share for
-// two warps a scheduler is 720) and 640 of matrix instructions for each tile, whose queue both tiles share. A
-// third place for S would take the way apart; O of two tiles and their four places fill tensor memory, and with P in
-// shared memory, which frees S's place sooner, P V reads both operands there: 907 us.
+// next but one S of a tile. 2048 query tokens over 32768, 32/8 heads, take 738 us, 1.44 PFLOP/s or 75 % of the
+// measured matrix rate: about 1600 cycles a page, of them 1270 in a row's softmax (the special-function unit's
+// share for two warps a scheduler is 720) and 640 of matrix instructions for each tile, whose queue both tiles
+// share. A third place for S would take the way apart; O of two tiles and their four places fill tensor memory,
+// and with P in shared memory, which frees S's place sooner, P V reads both operands there: 907 us.
 // A short call's time is that of instructions that run once: about 25 cycles each, so set-up is kept short,
-// and by a few warps. 4096 tokens, 2 heads, three pages a CTA: 12.8 us in a graph, of them 3.4 to the first scores, 2 of
-// pages, 1 of records written, 2 until all others are seen, 2 of copying and 1.5 of joining them.
+// and by a few warps. 4096 tokens, 2 heads, three pages a CTA: 12.8 us in a graph, of them 3.4 to the first
+// scores, 2 of pages, 1 of records written, 2 until all others are seen, 2 of copying and 1.5 of joining them.
 #include "kv4_walk.cuh"
 #include "splitkv.cuh"
 #include "tree.cuh"
@@ -54,7 +55,7 @@ constexpr int kInfo = 8;         // steps whose pages are kept: copies run at mo
 constexpr int kSegs = 8;         // segments that are kept; each is a step or more
 constexpr int kMaskStep = 512;   // blocks whose mask a warp looks at together
 constexpr int kMaxUnits = 256;   // (sequence, KV head) pairs whose kept blocks are counted
-constexpr int kStartPages = 4;   // pages' time that a second segment costs a CTA (0: as if cut regardless; 16: no change)
+constexpr int kStartPages = 4;   // pages' time that a second segment costs a CTA (with 0: 5 us more, as below)
 constexpr int kSlots = 2;        // records of a CTA: of the item that goes on from before, and that goes on
 constexpr uint32_t kColO = 256;  // O of tile g at kColO + 128 g
 
@@ -211,8 +212,12 @@ __device__ __forceinline__ int head_weight(const AttnArgs &a, const Seq &s, int 
 }
 
 // A word's bytes that are not 0 as their top bits.
-__device__ __forceinline__ uint32_t kept_bytes(uint32_t w) { return (w | ((w & 0x7f7f7f7fu) + 0x7f7f7f7fu)) & 0x80808080u; }
-__device__ __forceinline__ int chunk_count(const uint4 &x) { return __popc(x.x) + __popc(x.y) + __popc(x.z) + __popc(x.w); }
+__device__ __forceinline__ uint32_t kept_bytes(uint32_t w) {
+    return (w | ((w & 0x7f7f7f7fu) + 0x7f7f7f7fu)) & 0x80808080u;
+}
+__device__ __forceinline__ int chunk_count(const uint4 &x) {
+    return __popc(x.x) + __popc(x.y) + __popc(x.z) + __popc(x.w);
+}
 // The mask's bytes at .. at + 15 behind `base` (aligned to 16), 0 outside [lo, hi), by their top bits.
 __device__ __forceinline__ uint4 mask_chunk(const uint8_t *base, int at, int lo, int hi) {
     uint32_t w[4] = {0, 0, 0, 0};
@@ -339,7 +344,8 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     int total = 0, own = 0;
     Seq s = {0, 0, 0};
     if (few) {
-        if (a.by_mask) {  // by all threads, 4 to 32 a unit; each CTA begins elsewhere, so that not all ask for the same bytes
+        // by all threads, 4 to 32 a unit; each CTA begins elsewhere, so that not all ask for the same bytes
+        if (a.by_mask) {
             const int units = a.B * a.Hkv;
             int log = 5;
             while (log > 2 && units << log > kThreads) log--;
