@@ -29,7 +29,8 @@
 // measured matrix rate: about 1600 cycles a page, of them 1270 in a row's softmax (the special-function unit's
 // share for two warps a scheduler is 720) and 640 of matrix instructions for each tile, whose queue both tiles
 // share. A third place for S would take the way apart; O of two tiles and their four places fill tensor memory,
-// and with P in shared memory, which frees S's place sooner, P V reads both operands there: 907 us.
+// and with P in shared memory, which frees S's place sooner, writing it and P V take longer than that saves: 907 us,
+// with Q in tensor memory in turn 920.
 // A short call's time is that of instructions that run once: about 25 cycles each, so set-up is kept short,
 // and by a few warps. 4096 tokens, 2 heads, three pages a CTA: 12.8 us in a graph, of them 3.4 to the first
 // scores, 2 of pages, 1 of records written, 2 until all others are seen, 2 of copying and 1.5 of joining them.
