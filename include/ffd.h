@@ -657,9 +657,10 @@ size_t ffd_tree_workspace_size(const ffd_tree_params *params);
  *   s_j = sm_scale q . K_j,  lse = log sum_j e^(s_j),  out = sum_j e^(s_j - lse) V_j.
  * Without parents the nodes are a chain (node i hangs on i - 1): causal attention of drafts in a row or
  * of a chunk of a prompt. A row that sees no token gets out = 0 and lse = -inf. Scores and sums are
- * fp32; a probability enters the product with V as one number of dtype (off by up to 2^-8 of itself in
- * bf16, 2^-11 in fp16), so that relative L2 errors of out against 64 bits over normal data are 2.3e-3
- * (its own rounding: 1.7e-3) and 2.9e-4 (2.1e-4). A query with an infinity or a NaN in it
+ * fp32. A probability enters the product with V as two numbers of dtype (off by 2^-16 of itself in bf16, 2^-22
+ * in fp16) where max_q_len is at most 2 floor(128 / G): relative L2 errors of out against 64 bits over normal
+ * data are those of its own rounding, 1.7e-3 in bf16 and 2.1e-4 in fp16. With more nodes it enters as one
+ * (2^-8 and 2^-11), and the sum that out is divided by is that of these numbers: 2.4e-3 and 2.9e-4. A query with an infinity or a NaN in it
  * leaves its own (row, head) unspecified and no other; so does one whose scores times log2(e) pass
  * fp32's range. A key with one makes the rows that see it unspecified and no other, and so does a value,
  * which makes what they hold infinite or NaN.

@@ -8,9 +8,18 @@
 // the one in whose range it begins only where that is all it has: it may have another item to join. Page by
 // page a CTA computes for each tile of 128 rows
 //   S = Q K^T   (M 128, N 64, K 128; both operands in shared memory, S in tensor memory),
-//   P = 2^(S - m) in the inputs' type against a reference m that follows the row's maximum lazily: it is
-//       raised, and O rescaled, only when a score passes it by 2^8,
+//   P = 2^(S - m) against a reference m that follows the row's maximum lazily: it is raised, and O rescaled,
+//       only when a score passes it by 2^8,
 //   O += P V    (M 128, N 128, K 64 a page; P in tensor memory over S, V in shared memory, O in tensor memory).
+// P goes into its product as two numbers of the inputs' type, itself rounded and what that leaves out: one number
+// would add an error as large as the output's own rounding (relative L2 1.7e-3 -> 2.4e-3 in bf16, 2.1e-4 -> 2.9e-4 in fp16).
+// One tile has room for the second product: four of 131072 tokens, 112 rows 175 us with one part and with two, 32
+// windows of 4096 99 and 99. Two tiles pay for it: four of 32768, 8 heads, 240 rows 110 and 131 us, eight ragged trees
+// of 30 to 61 nodes 89 and 101, 96 blocks of 4 x 131072 31.2 and 33.8. Where there are more rows than two tiles take,
+// the matrix unit is what bounds the call (2048 tokens over 32768: 729 and 947) and P has one part. Its rounding
+// then counts on both sides: O is divided by the sum of the rounded numbers, so that the weights of V have the sum 1
+// whatever they were rounded to (771, where one sum serves the log-sum-exp and the division 729; 300 rows over four
+// of 32768 154 with one part and one sum, 163 so, 179 with two parts).
 // Both K and V lie in shared memory as the cache holds them, tokens by channels: K is read along its rows,
 // V across them.
 //
@@ -308,7 +317,7 @@ __device__ __forceinline__ uint64_t upto(int k) {
     return k < 0 ? 0ull : k >= 63 ? ~0ull : (2ull << k) - 1;
 }
 
-template <class T, int kTiles>
+template <class T, int kTiles, int kParts>
 __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     tree_kernel(const __grid_constant__ Params prm) {
     using H = Shape<kTiles>;
@@ -484,6 +493,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             };
 
             float m = -INFINITY, limit = -INFINITY, l = 0.0f;  // limit: a larger score raises m
+            float lr = 0.0f;  // what l is of the rounded probabilities, where they have one part
             bool any = false, far = false, tainted = false;
             while (true) {
                 const uint32_t buf = steps % kPlaces, vs = steps % H::kNV;
@@ -522,6 +532,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                         m = mn;
                         limit = m + (is_far(m) ? 0.0f : kLazy);
                         l *= al;
+                        lr *= al;
                         far = __any_sync(0xffffffffu, is_far(m));
                         if (any) {
                             // the last step's P V (a stop is met at the next wait)
@@ -550,7 +561,8 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                         for (int c = 0; c < 64; c++)
                             x[c] = __float_as_uint(__fmul_rn(__uint_as_float(x[c]), fs));
                     }
-                    uint32_t p[32];
+                    float2 r2 = l2, r3 = l2;
+                    uint32_t p[kParts][32];  // as numbers of T: rounded, and the rest
 #pragma unroll
                     for (int c = 0; c < 32; c++) {
                         float2 e = __ffma2_rn(make_float2(__uint_as_float(x[2 * c]),
@@ -558,11 +570,22 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                         e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
                         if (c & 1) l3 = __fadd2_rn(l3, e);
                         else l2 = __fadd2_rn(l2, e);
-                        p[c] = T::pack(e.x, e.y);
+                        p[0][c] = T::pack(e.x, e.y);
+                        const float2 first = T::unpack(p[0][c]);
+                        if constexpr (kParts == 2) {
+                            const float2 rest = __ffma2_rn(first, make_float2(-1.0f, -1.0f), e);
+                            p[1][c] = T::pack(rest.x, rest.y);
+                        } else {
+                            if (c & 1) r3 = __fadd2_rn(r3, first);
+                            else r2 = __fadd2_rn(r2, first);
+                        }
                     }
                     __syncwarp();
-                    tmem_store32(ts, p);  // P's 32 columns lie over S's first half, which has been read
+                    // 32 columns a part, over S's, which have been read
+#pragma unroll
+                    for (int i = 0; i < kParts; i++) tmem_store32(ts + 32 * i, p[i]);
                     l += (l2.x + l2.y) + (l3.x + l3.y);
+                    if (kParts == 1) lr += (r2.x + r2.y) + (r3.x + r3.y);
                     if (edge && waited(a, sh, &sh.v_ready[vs], (steps / H::kNV) & 1))
                         tainted |= (*reinterpret_cast<volatile uint64_t *>(&sh.bad[vs]) & see) != 0;
                     tc_wait_store();
@@ -583,7 +606,9 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
             // ---- the segment's results
             const int begins = sg->begins;
             if (active) {
-                const float inv = tainted ? NAN : l == 0.0f ? 0.0f : 1.0f / l;
+                // O by the weights that it was summed with
+                const float even = kParts == 1 && lr > 0.0f ? l / lr : 1.0f;
+                const float inv = tainted ? NAN : l == 0.0f ? 0.0f : even / l;
                 const int pad = record_rows(a, nq - node0);
                 float *row = prm.records + (int64_t)(kSlots * cta + begins) * H::kRecord + grp * kTile + r;
                 const int64_t at = (int64_t)(t0 + qi) * a.Hq + sg->h * a.G + rg;
@@ -618,7 +643,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                     } else {
 #pragma unroll
                         for (int e = 0; e < 32; e++)
-                            row[(32 * c + e) * pad] = tainted ? NAN : __uint_as_float(o[e]);
+                            row[(32 * c + e) * pad] = tainted ? NAN : __uint_as_float(o[e]) * even;
                     }
                 }
                 if (have) {
@@ -1080,8 +1105,8 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
                         if (page && live) {
                             const uint32_t vd = tc_desc_mn(v0 + vs * kPageBytes, 8192);
 #pragma unroll
-                            for (int i = 0; i < 4; i++)  // 16 tokens each
-                                tc_mma_ta(d, p + 8 * i, vd + 128 * i, kIdescO, add || i > 0);
+                            for (int i = 0; i < 4 * kParts; i++)  // 16 tokens each, part by part
+                                tc_mma_ta(d, p + 8 * i, vd + 128 * (i & 3), kIdescO, add || i > 0);
                         }
                         tc_commit(&sh.o_done[g][buf]);
                         tc_commit(&sh.v_free[vs]);
@@ -1198,11 +1223,11 @@ bool query_map(CUtensorMap *map, const AttnArgs &a, int dtype) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class T, int kTiles>
+template <class T, int kTiles, int kParts>
 cudaError_t launch(const Params &prm, const Plan &pl, cudaStream_t stream) {
     static int smem_set[kMaxDevicesTracked];
     constexpr int bytes = sizeof(Shared<kTiles>) + 1024;
-    cudaError_t e = raise_smem_limit(tree_kernel<T, kTiles>, bytes, smem_set);
+    cudaError_t e = raise_smem_limit(tree_kernel<T, kTiles, kParts>, bytes, smem_set);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = pl.ctas;
@@ -1215,7 +1240,7 @@ cudaError_t launch(const Params &prm, const Plan &pl, cudaStream_t stream) {
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, tree_kernel<T, kTiles>, prm);
+    e = cudaLaunchKernelEx(&cfg, tree_kernel<T, kTiles, kParts>, prm);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -1236,9 +1261,12 @@ cudaError_t launch_tree_attention(const AttnArgs &a, const Plan &pl, int dtype, 
     char *ws = reinterpret_cast<char *>(a.err);
     prm.records = reinterpret_cast<float *>(ws + pl.records);
     prm.tickets = reinterpret_cast<int *>(ws + pl.tickets);
-    if (dtype == FFD_DTYPE_BF16)
-        return pl.tiles == 1 ? launch<Bf16, 1>(prm, pl, stream) : launch<Bf16, 2>(prm, pl, stream);
-    return pl.tiles == 1 ? launch<F16, 1>(prm, pl, stream) : launch<F16, 2>(prm, pl, stream);
+    auto run = [&](auto type) {
+        using T = decltype(type);
+        if (pl.tiles == 1) return launch<T, 1, 2>(prm, pl, stream);
+        return pl.groups == 1 ? launch<T, 2, 2>(prm, pl, stream) : launch<T, 2, 1>(prm, pl, stream);
+    };
+    return dtype == FFD_DTYPE_BF16 ? run(Bf16{}) : run(F16{});
 }
 
 }  // namespace tree
