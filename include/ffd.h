@@ -586,8 +586,7 @@ typedef struct {
  * the angle being the product of the integer and the fp32 number without a rounding, good to 1e-7 of a
  * whole turn (2^24 radians and less); the turn is computed in fp32 and rounded to dtype once. Channels from rot_dim on pass as they are. Quantised keys are those that
  * ffd_quantize_keys writes for the rotated, rounded key.
- *   q, q_out     device [T][Hq][128], or both NULL; q_out may be q itself (same stride), and may not
- *                overlap it, k_new or v_new otherwise
+ *   q, q_out     device [T][Hq][128], or both NULL; q_out may be q itself (same stride)
  *   k_new, v_new device [T][Hkv][128]
  *   inv_freq     device fp32 [rot_dim / 2] (any scaling is in it); NULL where rot_dim is 0
  *   rope_positions  device int32 [T], 0 <= p < 2^24: the position that a row is rotated by (of a
@@ -605,7 +604,9 @@ typedef struct {
  *                max_blocks_per_seq or a page outside [0, P) (the token is not appended, its query is
  *                rotated all the same); FFD_ERRBIT_RANGE for a rotary position outside [0, 2^24) (its
  *                rotated channels are unspecified) or, with records, a key outside the fp16 range
- * Tensors are 16-byte aligned. Two rows that name the same (page, token) race.
+ * Tensors are 16-byte aligned. Two rows that name the same (page, token) race. What is written (q_out, the cache,
+ * the records, the error word) may share no byte with what is read or written otherwise, q_out = q apart, else
+ * FFD_ERR_INVALID_ARG; q's, q_out's, k_new's and v_new's rows may lie between each other's where their strides are equal.
  * Returns FFD_OK, FFD_ERR_INVALID_ARG, FFD_ERR_UNSUPPORTED or FFD_ERR_CUDA.
  */
 ffd_status ffd_rope_append(const ffd_rope_params *params, const void *q, const void *k_new,
@@ -678,7 +679,8 @@ size_t ffd_tree_workspace_size(const ffd_tree_params *params);
  *               sequence sees (past n, behind the window, dropped by keep_in) are not used
  *   keep_in     device u8 [B][Hkv][max_blocks_per_seq] or NULL: nonzero = the block may be seen
  *               (for instance ffd_select_blocks's mask, or a decode step's keep_mask)
- *   out         device [total_q][Hq][128] of dtype, 16-byte aligned; it must not overlap q
+ *   out         device [total_q][Hq][128] of dtype, 16-byte aligned. out, lse and the workspace must not
+ *               overlap each other or what is read
  *   lse         device fp32 [total_q][Hq] or NULL
  *   workspace   device, >= ffd_tree_workspace_size(params) bytes, 256-byte aligned; its first 4
  *               bytes are the device error word. Zero-fill it once before first use; each call
@@ -719,8 +721,8 @@ ffd_status ffd_tree_attention(const ffd_tree_params *params, const void *q, cons
  *   accepted      device int32 [B]: the path's length (0 for a sequence without nodes)
  *   next_token    device int64 [B]: the model's token behind the path (-1 for no nodes)
  *   new_lens      device int32 [B]: n - nq + accepted
- * path, accepted, next_token and new_lens must not overlap what is read (draft, target, parents, cu_nodes,
- * seq_lens, block_table).
+ * path, accepted, next_token, new_lens, the cache, the records and the error word must not overlap each other or
+ * what else is read (draft, target, parents, cu_nodes, seq_lens, block_table).
  *   error_word    device int32, or NULL: FFD_ERRBIT_BOUNDS for a length, an offset or a number of nodes
  *                 out of range (nothing is moved: accepted 0, next_token -1, new_lens the length
  *                 as given, path -1 where the offsets allow it), a parent as in ffd_tree_attention, or a

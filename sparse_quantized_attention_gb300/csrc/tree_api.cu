@@ -36,8 +36,49 @@ bool overlap(const void *p, int64_t n, const void *q, int64_t m) {
     return n > 0 && m > 0 && x < y + (uintptr_t)m && y < x + (uintptr_t)n;
 }
 
-// Bytes from the first to the last of T rows of 16-bit elements.
-int64_t span(int64_t T, int64_t stride, int64_t heads) { return T > 0 ? 2 * ((T - 1) * stride + heads * kD) : 0; }
+// T rows of `heads` heads of 16-bit elements, `stride` elements from one to the next.
+struct Rows {
+    const void *p;
+    int64_t T, stride, heads;
+    int64_t width() const { return 2 * heads * kD; }  // bytes
+    int64_t span() const {  // from the first row to the last (at most about 2^61)
+        if (!p || T < 1) return 0;
+        const int64_t most = ((int64_t)1 << 60) / T;
+        return 2 * (T - 1) * (stride < most ? stride : most) + width();
+    }
+};
+
+// Whether two lots of rows share any byte. Rows at one distance may lie between each other's, as those of a
+// fused projection do; at different distances they may not.
+bool overlap(const Rows &a, const Rows &b) {
+    if (!overlap(a.p, a.span(), b.p, b.span())) return false;
+    if (a.stride != b.stride || a.T != b.T) return true;
+    const int64_t step = 2 * a.stride;
+    const int64_t d = static_cast<const char *>(b.p) - static_cast<const char *>(a.p);
+    const int64_t r = (d % step + step) % step, m = (r - d) / step;  // row i of a, i + m of b: r apart
+    auto both = [&](int64_t x) { return x < a.T && -x < a.T; };
+    return (r < a.width() && both(m)) || (r + b.width() > step && both(m - 1));
+}
+
+struct Bytes {
+    const void *p;
+    int64_t n;
+};
+bool overlap(const Bytes &a, const Bytes &b) { return a.p && b.p && overlap(a.p, a.n, b.p, b.n); }
+bool overlap(const Rows &a, const Bytes &b) { return b.p && overlap(a.p, a.span(), b.p, b.n); }
+template <size_t n, class X>
+bool overlap_any(const Bytes (&a)[n], const X &x) {
+    for (const Bytes &y : a)
+        if (overlap(x, y)) return true;
+    return false;
+}
+template <size_t n>
+bool overlap_each_other(const Bytes (&a)[n]) {
+    for (size_t i = 0; i < n; i++)
+        for (size_t j = 0; j < i; j++)
+            if (overlap(a[i], a[j])) return true;
+    return false;
+}
 
 bool known(int32_t dtype) { return dtype == FFD_DTYPE_BF16 || dtype == FFD_DTYPE_F16; }
 
@@ -156,13 +197,22 @@ ffd_status ffd_rope_append(const ffd_rope_params *params, const void *q, const v
     if (thumb && p.dtype != FFD_DTYPE_BF16) return FFD_ERR_UNSUPPORTED;
     const int64_t heads = (int64_t)p.num_q_heads + 2 * (int64_t)p.num_kv_heads;
     if (heads > 65536 || T * ((heads + 7) / 8) > (int64_t)INT32_MAX * 4) return FFD_ERR_UNSUPPORTED;
-    if (queries) {
-        const int64_t out = span(T, p.q_out_stride, p.num_q_heads);
-        const bool same = q == q_out && (p.q_stride == p.q_out_stride || T <= 1);
-        if (!same && overlap(q_out, out, q, span(T, p.q_stride, p.num_q_heads))) {
-            // rows of q and q_out may lie between each other's only where they are the same ones
-            return FFD_ERR_INVALID_ARG;
-        }
+    // A token's rows are read and written by several warps, at their own times.
+    if (T > 0) {
+        const int64_t B = p.batch, tiles = (int64_t)p.num_pages * p.num_kv_heads;
+        const Rows in[] = {{queries ? q : nullptr, T, p.q_stride, p.num_q_heads},
+                           {k_new, T, p.k_stride, p.num_kv_heads}, {v_new, T, p.v_stride, p.num_kv_heads}};
+        const Rows out = {queries ? q_out : nullptr, T, p.q_out_stride, p.num_q_heads};
+        const Bytes reads[] = {{inv_freq, 2 * p.rot_dim}, {rope_positions, 4 * T}, {cu_tokens, 4 * (B + 1)},
+                               {positions, 4 * B}, {block_table, 4 * B * p.max_blocks_per_seq}};
+        const Bytes writes[] = {{k, tiles * kPage * 2 * kD}, {v, tiles * kPage * 2 * kD},
+                                {thumb, tiles * kThumbRec}, {resid, tiles * kResidRec}, {error_word, 4}};
+        const bool same = queries && q == q_out && (p.q_stride == p.q_out_stride || T == 1);
+        for (const Rows &x : in)
+            if (overlap_any(writes, x) || (!(same && x.p == q) && overlap(x, out))) return FFD_ERR_INVALID_ARG;
+        for (const Bytes &x : reads)
+            if (overlap_any(writes, x) || overlap(out, x)) return FFD_ERR_INVALID_ARG;
+        if (overlap_any(writes, out) || overlap_each_other(writes)) return FFD_ERR_INVALID_ARG;
     }
     RopeArgs a{};
     a.B = p.batch;
@@ -219,8 +269,17 @@ ffd_status ffd_tree_attention(const ffd_tree_params *params, const void *q, cons
     if (!cu_q && p.total_q != (int64_t)p.batch * p.max_q_len) return FFD_ERR_INVALID_ARG;
     if (workspace_bytes < pl.total) return FFD_ERR_WORKSPACE;
     const int64_t row = (int64_t)p.num_q_heads * kD, stride = p.q_stride ? p.q_stride : row;
-    if (overlap(q, span(p.total_q, stride, p.num_q_heads), out, span(p.total_q, row, p.num_q_heads)))
-        return FFD_ERR_INVALID_ARG;  // q is read by several CTAs, at their own times
+    {  // inputs are read, and parts of the result written, by several CTAs, at their own times
+        const int64_t B = p.batch, T = p.total_q, cache = (int64_t)p.num_pages * p.num_kv_heads * kPage * 2 * kD;
+        const Rows queries = {q, T, stride, p.num_q_heads};
+        const Bytes reads[] = {{k, cache}, {v, cache}, {seq_lens, 4 * B}, {cu_q, 4 * (B + 1)}, {parents, 4 * T},
+                               {block_table, 4 * B * p.max_blocks_per_seq},
+                               {keep_in, B * p.num_kv_heads * p.max_blocks_per_seq}};
+        const Bytes writes[] = {{out, 2 * T * row}, {lse, 4 * T * p.num_q_heads}, {workspace, (int64_t)pl.total}};
+        if (overlap_any(writes, queries) || overlap_each_other(writes)) return FFD_ERR_INVALID_ARG;
+        for (const Bytes &x : reads)
+            if (overlap_any(writes, x)) return FFD_ERR_INVALID_ARG;
+    }
     AttnArgs a{};
     a.B = p.batch;
     a.Hq = p.num_q_heads;
@@ -281,24 +340,20 @@ ffd_status ffd_tree_commit(const ffd_cache_desc *cache, int32_t batch, int32_t m
                           (const void *)block_table, (const void *)path, (const void *)accepted,
                           (const void *)new_lens, (const void *)error_word})
         if (!aligned(x, 4)) return FFD_ERR_INVALID_ARG;
-    if (overlap(seq_lens, 4 * (int64_t)batch, new_lens, 4 * (int64_t)batch))
-        return FFD_ERR_INVALID_ARG;  // every KV head's block reads the length, at its own time
     if (cache->head_dim != kD || cache->page_size != kPage) return FFD_ERR_UNSUPPORTED;
     if ((int64_t)max_blocks_per_seq * kPage > INT32_MAX) return FFD_ERR_UNSUPPORTED;
     if ((int64_t)batch * cache->num_kv_heads > INT32_MAX) return FFD_ERR_UNSUPPORTED;  // grid.x
     if (!cu_nodes && total_nodes / batch > kMaxNodes) return FFD_ERR_UNSUPPORTED;
     // every KV head's block reads the inputs, at its own time, and the first head's writes the results
-    const int64_t B = batch, T = total_nodes;
-    const struct {
-        const void *p;
-        int64_t n;
-    } reads[] = {{draft, 8 * T}, {target, 8 * T}, {parents, parents ? 4 * T : 0},
-                 {cu_nodes, cu_nodes ? 4 * (B + 1) : 0}, {seq_lens, 4 * B},
-                 {block_table, 4 * B * max_blocks_per_seq}},
-      writes[] = {{path, 4 * T}, {accepted, 4 * B}, {next_token, 8 * B}, {new_lens, 4 * B}};
-    for (const auto &r : reads)
-        for (const auto &w : writes)
-            if (overlap(r.p, r.n, w.p, w.n)) return FFD_ERR_INVALID_ARG;
+    const int64_t B = batch, T = total_nodes, tiles = (int64_t)cache->num_pages * cache->num_kv_heads;
+    const Bytes reads[] = {{draft, 8 * T}, {target, 8 * T}, {parents, 4 * T}, {cu_nodes, 4 * (B + 1)},
+                           {seq_lens, 4 * B}, {block_table, 4 * B * max_blocks_per_seq}};
+    const Bytes writes[] = {{path, 4 * T}, {accepted, 4 * B}, {next_token, 8 * B}, {new_lens, 4 * B},
+                            {k, tiles * kPage * 2 * kD}, {v, tiles * kPage * 2 * kD},
+                            {thumb, tiles * kThumbRec}, {resid, tiles * kResidRec}, {error_word, 4}};
+    for (const Bytes &x : reads)
+        if (overlap_any(writes, x)) return FFD_ERR_INVALID_ARG;
+    if (overlap_each_other(writes)) return FFD_ERR_INVALID_ARG;
     CommitArgs a{};
     a.B = batch;
     a.Hkv = cache->num_kv_heads;
