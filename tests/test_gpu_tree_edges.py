@@ -2,7 +2,10 @@
 import pytest
 import torch
 
+import sparse_quantized_attention_gb300 as ffd
+
 from tests import tree_refs as R
+from tests.test_gpu_rope import i32
 from tests.test_gpu_tree import BF16, F16, Problem
 
 pytestmark = pytest.mark.gpu
@@ -58,3 +61,30 @@ def test_one_value_comes_back(shape, dtype, gain):
     x.v.fill_(one)
     got, _ = x.run()
     assert bool((got[:x.T] == one).all()), int((got[:x.T] != one).sum())
+
+
+# ---- waits that run out -------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("splits", [0, 3, 40])
+@pytest.mark.parametrize("nq", [1, 20, 60, 100])
+def test_a_wait_for_other_parts_runs_out(nq, splits, dtype):
+    """The counts of published parts begin at large negative numbers, so that CTAs that share an item wait for
+    what never comes: each gives up at its limit, 1 ms, is drained at once (what it had under way has landed) and
+    the call reports it. On a workspace filled with zeros again the next call gives what it gave before."""
+    x = Problem(8, 2, [9000, 100, 2500], [nq] * 3, dtype, seed=nq)
+    want = x.run(num_splits=splits)
+    e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    p = x.params(num_splits=splits, wait_limit_us=1000)
+    args = (x.q, x.k, x.v, i32(x.lens), x.bt.cuda(), torch.empty_like(want[0]), x.ws)
+    more = dict(parents=i32(x.parents), cu_q=i32(x.cu))
+    for _ in range(3):
+        x.ws.fill_(0x80)
+        x.ws[:256].zero_()  # the error word
+        e0.record()
+        ffd.ffd_tree_attention(p, *args, **more)
+        e1.record()
+        assert ffd.ffd_get_error(x.ws) == 7
+        assert 1.0 <= e0.elapsed_time(e1) < 500.0  # ms: no drain ran to its own bound
+        x.ws.zero_()
+        again = x.run(num_splits=splits)
+        assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
