@@ -10,14 +10,15 @@ constexpr int kMaxNodes = FFD_TREE_MAX_NODES;
 constexpr int kMaxPlace = 1 << 24;  // rotary positions are below
 // Pages' time that an item counts for besides its pages when the pages of a batch are cut into equal ranges:
 // what a CTA spends between two items. us without and with it: eight sequences of 500 to 8000 tokens, 8 heads, 25
-// nodes 47.6 44.5; 32 sequences of 1000 to 9000, 2 heads 39.8 37.8; four of 131072, 4 heads, 112 rows 170.4 167.6,
-// 96 blocks of them 36.4 33.1.
+// nodes 50.4 45.3; 32 sequences of 1000 to 9000, 2 heads, 8 nodes 43.4 40; four of 131072, 4 heads, 112 rows 176.8 173.3.
 constexpr int kItemPages = 9;
 
 // Pages of a CTA, at least, where CTAs share an item of np pages: a page takes 0.45 us and each CTA more about 0.06
 // of the join, whose sum is least at a third of the square root. us by pages a CTA, 12 nodes of 8 heads: of 16
 // pages 1 12.6, 2 12.5, 4 14.0; of 64 1 14.0, 3 12.8, 8 15.3; of 256 2 17.4, 5 15.3, 16 20.1; of 1024 8 22.7, 10
-// 22.2, 24 26.8. Five pages take 11.7 one by one and 9.6 by a CTA alone, sixteen 12.5 and 15.5.
+// 22.2, 24 26.8. Five pages take 11.7 one by one and 9.6 by a CTA alone, sixteen 12.5 and 15.5. Two tiles' records are
+// twice as large, and their pages take twice the time too: 32 nodes of 8 heads, one KV head over 1024, 4096, 16384 and
+// 65536 tokens, with half of these pages, these, and twice: 15.1 15.8 17.1, 17.6 17.4 20.0, 24.3 23.6 25.5, 38.1 34.7 41.1.
 constexpr int kWholePages = 9;  // as many that one CTA takes all
 __host__ __device__ inline int share_pages(int np) {
     if (np <= kWholePages) return np > 0 ? np : 1;

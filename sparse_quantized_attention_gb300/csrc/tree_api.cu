@@ -111,10 +111,14 @@ ffd_status check_params(const ffd_tree_params *p) {
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 // A mask that every CTA reads through before it begins, to share the kept blocks out evenly; a larger one is cut
-// as if all of its blocks were kept. us cut so and evenly, with 8 heads: 64 kept blocks of 16 sequences of 4000
-// to 32768 tokens (64 KB of mask) 143 54, of 32 of 8000 to 65536 (256 KB) 222 113; 96 blocks of 4 x 131072, 4 heads
-// 33.8 27.4. Where all keep as many anyway the counting costs: 200 blocks of 16 x 65536 (128 KB) 141 146, 128
-// of 32 x 131072 (512 KB) 195 232; one sequence of 4096 13.1 13.8.
+// as if all of its blocks were kept. us in a graph cut so and evenly, 8 nodes of 8 heads: 64 kept blocks of 16
+// sequences of 4000 to 32768 tokens (64 KB of mask) 168 60, of 32 of 8000 to 65536 (256 KB) 273 118; 16 nodes over 96
+// blocks of 4 x 131072, 4 heads 37.8 28.5. Where all keep as many anyway the counting costs: 200 blocks of 16 x
+// 65536 (128 KB) 151 150, 128 of 32 x 131072 (512 KB) 210 215; one sequence of 4096 13.4 14.1.
+// Counting also takes a lane of one warp for each sequence and one list of blocks for each (sequence, head), so
+// batches past 32 and sequences of several groups of rows are cut by all their blocks: 64 kept of 4000 to 32768 tokens,
+// 8 nodes of 8 heads, 31 sequences 107, 32 111, 33 301, 64 481; 16 such of 28/4 heads, 36 nodes 57, 37 nodes (two groups) 131; 96
+// of 4 x 131072, 36 nodes 34.6, 37 53.4.
 constexpr int64_t kMaskUnits = 256, kMaskBytes = 1 << 18;
 
 // Workspace: [error word | two counters per CTA | records per CTA]. The counters, the only part that
@@ -125,9 +129,9 @@ ffd_status make_plan(const ffd_tree_params *p, Plan *pl) {
     if (st != FFD_OK) return st;
     const int64_t nodes = kTileRows / (p->num_q_heads / p->num_kv_heads);  // of a tile
     // Two tiles share what is read, which pays wherever there are rows for both. us with tiles one by one and
-    // two at a time: four sequences of 32768, 8 heads, 160 rows 152 110, 240 rows 173 114; 4096 rows over
-    // 32768 488 391. With rows for one tile alone the second's warps and memory cost: 64 sequences of 4096, 4
-    // rows 166 and 172.
+    // two at a time: four sequences of 32768, 8 heads, 160 rows 157 127, 240 rows 178 133; 4096 rows over
+    // 32768 637 416. With rows for one tile alone the second's warps and memory cost: 64 sequences of 4096, 4
+    // rows 177 and 183.
     pl->tiles = p->max_q_len <= nodes ? 1 : 2;
     const int64_t groups = (p->max_q_len + pl->tiles * nodes - 1) / (pl->tiles * nodes);
     const int64_t items = (int64_t)p->batch * p->num_kv_heads * groups;
@@ -146,6 +150,9 @@ ffd_status make_plan(const ffd_tree_params *p, Plan *pl) {
     if (sms > 0 && ctas > sms) ctas = sms;
     if (ctas > kv4::kMaxCtas) ctas = kv4::kMaxCtas;
     pl->ctas = (int)ctas;
+    // Equal shares are worked out by that warp too. Past its 32 sequences and past four groups they would change little.
+    // us without them and with: 8 nodes of 4 heads over 8192, 32 sequences 98 98 (33 take 102); one head of 8192, four groups
+    // 23.1 21.2, five 22.5 20.0, sixteen 28.5 28.7; 8 heads of 32768, four 118 118, five 143 143, sixteen 408 408.
     pl->shares = p->batch <= 32 && groups <= 4 && items <= ctas ? (int)(ctas / items) : 0;
     pl->groups = (int)groups;
     pl->by_mask = p->batch <= 32 && groups == 1 && (int64_t)p->batch * p->num_kv_heads <= kMaskUnits &&

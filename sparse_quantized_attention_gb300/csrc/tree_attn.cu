@@ -15,7 +15,7 @@
 // would add an error as large as the output's own rounding (relative L2 1.7e-3 -> 2.4e-3 in bf16, 2.1e-4 -> 2.9e-4 in fp16).
 // One tile has room for the second product: four of 131072 tokens, 112 rows 175 us with one part and with two, 32
 // windows of 4096 99 and 99. Two tiles pay for it: four of 32768, 8 heads, 240 rows 110 and 131 us, eight ragged trees
-// of 30 to 61 nodes 89 and 101, 96 blocks of 4 x 131072 31.2 and 33.8. Where there are more rows than two tiles take,
+// of 30 to 61 nodes 89 and 103, 96 blocks of 4 x 131072 with 25 nodes 31.2 and 33.8. Where there are more rows than two tiles take,
 // the matrix unit is what bounds the call (2048 tokens over 32768: 729 and 947) and P has one part. Its rounding
 // then counts on both sides: O is divided by the sum of the rounded numbers, so that the weights of V have the sum 1
 // whatever they were rounded to (771, where one sum serves the log-sum-exp and the division 729; 300 rows over four
@@ -31,17 +31,18 @@
 // zeroed and the rows that do see it are marked.
 //
 // What bounds it. One tile: memory. A page is 32 KB and takes 0.73 us an SM at the copy rate; the softmax warps
-// are busy for 0.45 of that. Four sequences of 131072 tokens, 4 heads, 112 rows: 169 us in a graph,
-// 6.4 TB/s, of which the first page's way into the CTA (4 us: lengths, tables, copies, each waiting for the one
-// before) and the join (5 to 7) are what the floor of 158 lacks. Two tiles: the way round from P to the
-// next but one S of a tile. 2048 query tokens over 32768, 32/8 heads, take 738 us, 1.44 PFLOP/s or 75 % of the
-// measured matrix rate: about 1600 cycles a page, of them 1270 in a row's softmax (the special-function unit's
-// share for two warps a scheduler is 720) and 640 of matrix instructions for each tile, whose queue both tiles
-// share. A third place for S would take the way apart; O of two tiles and their four places fill tensor memory,
-// and with P in shared memory, which frees S's place sooner, writing it and P V take longer than that saves: 907 us,
-// with Q in tensor memory in turn 920.
+// are busy for less than that. Four sequences of 131072 tokens, 4 heads, 112 rows: 172 to 174 us in a graph,
+// 6.2 TB/s, of which the first page's way into the CTA (4 us: lengths, tables, copies, each waiting for the one
+// before) and the join (5 to 7) are most of what the floor of 158 lacks. Two tiles: the way round from P to the
+// next but one S of a tile. 2048 query tokens over 32768, 32/8 heads, take 765 to 792 us in a graph, 1.37 PFLOP/s or
+// 71 % of the measured matrix rate. Clock counts with one sum of the probabilities, 1600 cycles a page: 1270 in a
+// row's softmax (the special-function unit's share for two warps a scheduler is 720), 640 of matrix instructions for
+// each tile, whose queue both tiles share; the second sum adds about 90, and two parts 256 to each tile's instructions.
+// A third place for S would take the way apart; O of two tiles and their four places fill tensor memory,
+// and with P in shared memory, which frees S's place sooner, writing it and P V take longer than that saves (716 ->
+// 907 us with one part and one sum, with Q in tensor memory in turn 920).
 // A short call's time is that of instructions that run once: about 25 cycles each, so set-up is kept short,
-// and by a few warps. 4096 tokens, 2 heads, three pages a CTA: 12.8 us in a graph, of them 3.4 to the first
+// and by a few warps. 4096 tokens, 2 heads, three pages a CTA: 13.2 us in a graph, of them 3.4 to the first
 // scores, 2 of pages, 1 of records written, 2 until all others are seen, 2 of copying and 1.5 of joining them.
 #include "kv4_walk.cuh"
 #include "splitkv.cuh"
@@ -65,7 +66,9 @@ constexpr int kInfo = 8;         // steps whose pages are kept: copies run at mo
 constexpr int kSegs = 8;         // segments that are kept; each is a step or more
 constexpr int kMaskStep = 512;   // blocks whose mask a warp looks at together
 constexpr int kMaxUnits = 256;   // (sequence, KV head) pairs whose kept blocks are counted
-constexpr int kStartPages = 4;   // pages' time that a second segment costs a CTA (with 0: 5 us more, as below)
+// Pages' time that a second segment costs a CTA. us with 0 and 4: 60 nodes of 8 heads over 4096 23.3 19.7, 8 nodes of 11
+// heads over 16384 28.4 27.6, others the same.
+constexpr int kStartPages = 4;
 constexpr int kSlots = 2;        // records of a CTA: of the item that goes on from before, and that goes on
 constexpr uint32_t kColO = 256;  // O of tile g at kColO + 128 g
 
@@ -331,8 +334,8 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     const AttnArgs &a = prm.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    // Tables set out for L2 while the lengths are read, by warps that are idle yet (96 kept blocks of 4 x 131072:
-    // 31.6 -> 31.0 us in a graph, 64 of 32 x 30000 to 131072 68.2 -> 66.2).
+    // Tables set out for L2 while the lengths are read, by warps that are idle yet (96 kept blocks of 4 x 131072,
+    // 25 nodes: 0.6 of 31 us, 64 of 32 x 30000 to 131072, 8 nodes of 4 heads: 2 of 68).
     if (warp < H::kSoft) {
         const int64_t at = 128 * ((int64_t)blockIdx.x * kRows + tid), entries = (int64_t)a.B * a.max_blocks;
         if (at < 4 * entries) prefetch_l2(reinterpret_cast<const uint8_t *>(a.block_table) + at);
@@ -784,7 +787,8 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         if (a.shares > 0 && total > 0) {
             // No more items than CTAs, of about one length: each in equal shares of `per` pages, so that no CTA has
             // the end of one and the start of another, unless that leaves too many CTAs without work. Measured,
-            // us by shares and cut regardless (152 CTAs): 8 heads of 32768 tokens, 16 nodes 34 37; of 131072
+            // us by shares and cut regardless (152 CTAs, before items
+            // cut regardless went in shares of share_pages): 8 heads of 32768 tokens, 16 nodes 34 37; of 131072
             // 88 94; one head of 32768, 60 nodes 28 34; ten heads of 8192 19 25.
             const bool full = lane >= a.B || s.nq > (a.groups - 1) * a.item_nodes;  // all its groups are there
             if (!several) {  // (behind a window it need not be the last group's)
