@@ -216,7 +216,7 @@ ffd_status ffd_rope_append(const ffd_rope_params *params, const void *q, const v
                                 {thumb, tiles * kThumbRec}, {resid, tiles * kResidRec}, {error_word, 4}};
         const bool same = queries && q == q_out && (p.q_stride == p.q_out_stride || T == 1);
         for (const Rows &x : in)
-            if (overlap_any(writes, x) || (!(same && x.p == q) && overlap(x, out))) return FFD_ERR_INVALID_ARG;
+            if (overlap_any(writes, x) || (!(same && &x == in) && overlap(x, out))) return FFD_ERR_INVALID_ARG;
         for (const Bytes &x : reads)
             if (overlap_any(writes, x) || overlap(out, x)) return FFD_ERR_INVALID_ARG;
         if (overlap_any(writes, out) || overlap_each_other(writes)) return FFD_ERR_INVALID_ARG;

@@ -92,6 +92,9 @@ def test_append_between_rows(lib):
                 assert append(lib, moved, s) == INVALID, (off, row)
             elif off % 4096 == 0 or row:
                 goes_on(lambda: append(lib, moved, s))
+    # q in place is q alone: not k_new's or v_new's rows as well
+    for n in ("k_new", "v_new"):
+        assert append(lib, {**at, n: at["q"]}, s) == INVALID
     # one distance for q_out, another for the rest: not told apart
     assert append(lib, beside, {**s, "q_out": wide}) == INVALID
     # one row has no distance
