@@ -7,6 +7,7 @@ import torch
 
 import sparse_quantized_attention_gb300 as ffd
 from sparse_quantized_attention_gb300 import _build
+from sparse_quantized_attention_gb300.ffd import RESID_RECORD_BYTES, THUMB_RECORD_BYTES
 
 INVALID, CUDA = 1, 4
 FAR = 1 << 24  # between tensors, larger than any here
@@ -42,7 +43,7 @@ ROWS = {"q": HQ, "q_out": HQ, "k_new": HKV, "v_new": HKV}
 A_ARGS = ("q", "k_new", "v_new", "freq", "places", "cu", "pos", "bt", "q_out", "k", "v", "thumb", "resid", "err")
 A_SIZE = dict(q=T * HQ * 256, q_out=T * HQ * 256, k_new=T * HKV * 256, v_new=T * HKV * 256, freq=2 * ROT, places=4 * T,
               cu=4 * (B + 1), pos=4 * B, bt=4 * B * MB, k=P * HKV * 16384, v=P * HKV * 16384,
-              thumb=P * HKV * 3072, resid=P * HKV * 8704, err=4)
+              thumb=P * HKV * THUMB_RECORD_BYTES, resid=P * HKV * RESID_RECORD_BYTES, err=4)
 
 
 def append(lib, at, strides=None, tokens=T):
@@ -130,8 +131,8 @@ C_ARGS = ("draft", "target", "par", "cu", "sl", "bt", "k", "v", "thumb", "resid"
 
 def test_commit_refuses(lib):
     size = dict(draft=8 * T, target=8 * T, par=4 * T, cu=4 * (B + 1), sl=4 * B, bt=4 * B * MB,
-                k=P * HKV * 16384, v=P * HKV * 16384, thumb=P * HKV * 3072, resid=P * HKV * 8704, path=4 * T,
-                acc=4 * B, nxt=8 * B, lens=4 * B, err=4)
+                k=P * HKV * 16384, v=P * HKV * 16384, thumb=P * HKV * THUMB_RECORD_BYTES,
+                resid=P * HKV * RESID_RECORD_BYTES, path=4 * T, acc=4 * B, nxt=8 * B, lens=4 * B, err=4)
     at = places(C_ARGS)
     desc = ffd.CacheDesc(P, HKV, 128, 64)
 
